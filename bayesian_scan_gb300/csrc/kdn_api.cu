@@ -19,6 +19,62 @@ int g_sm_count[64] = {};
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool head_dim_ok(int x) { return x == 16 || x == 32 || x == 64 || x == 128; }
+bool dtype_ok(kdn_dtype t) { return t == KDN_F32 || t == KDN_BF16; }
+uintptr_t size_of(kdn_dtype t) { return t == KDN_BF16 ? 2 : 4; }
+
+// What the forward and the backward gated recurrence check alike.
+kdn_status gated_check(const GatedArgs& a) {
+    if (a.B < 1 || a.H < 1 || a.T < 0 || a.C < 1 || !a.A) return KDN_ERR_INVALID_ARG;
+    if (!dtype_ok(a.in_dtype) || !dtype_ok(a.out_dtype)) return KDN_ERR_UNSUPPORTED;
+    if (a.offsets ? (a.nseq < 1 || a.B != 1) : a.nseq != 0) return KDN_ERR_INVALID_ARG;
+    const long long rows = static_cast<long long>(a.offsets ? a.nseq : a.B) * a.H;
+    if (rows > (1LL << 40) || rows > (1LL << 62) / a.C) return KDN_ERR_INVALID_ARG;
+    if (static_cast<long long>(a.B) * a.H > (1LL << 31)) return KDN_ERR_INVALID_ARG;
+    if (a.T > 0) {
+        const long long tokens = static_cast<long long>(a.B) * a.H * a.T;   // < 2^62
+        const bool x_read = a.x != nullptr;
+        if (a.d_ld < a.C || (x_read && a.x_ld < a.C)) return KDN_ERR_INVALID_ARG;
+        const long long ld = x_read && a.x_ld > a.d_ld ? a.x_ld : a.d_ld;
+        if (tokens > (1LL << 62) / ld) return KDN_ERR_INVALID_ARG;
+    }
+    const uintptr_t es = size_of(a.in_dtype), os = size_of(a.out_dtype);
+    const void* ins[] = {a.x, a.d, a.grad_x, a.grad_d};
+    for (const void* p : ins)
+        if (!aligned(p, es)) return KDN_ERR_INVALID_ARG;
+    const void* outs[] = {a.out, a.grad_out};
+    for (const void* p : outs)
+        if (!aligned(p, os)) return KDN_ERR_INVALID_ARG;
+    const void* words[] = {a.A, a.h0, a.offsets, a.final_state, a.grad_final_state, a.grad_A, a.grad_h0};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return KDN_ERR_INVALID_ARG;
+    return KDN_OK;
+}
+
+// What the forward and the backward query/key preparation check alike.
+kdn_status qk_check(const QkArgs& a) {
+    if (a.B < 1 || a.T < 0 || a.heads[0] < 0 || a.heads[1] < 0 || a.heads[0] + a.heads[1] < 1)
+        return KDN_ERR_INVALID_ARG;
+    if (!dtype_ok(a.in_dtype) || !dtype_ok(a.out_dtype) || !head_dim_ok(a.dk)) return KDN_ERR_UNSUPPORTED;
+    if (a.norm != KDN_NORM_NONE && a.norm != KDN_NORM_RMS && a.norm != KDN_NORM_L2) return KDN_ERR_UNSUPPORTED;
+    if (!(a.eps >= 0.f)) return KDN_ERR_INVALID_ARG;
+    if (a.rot < 0 || a.rot > a.dk || a.rot % 2 != 0) return KDN_ERR_INVALID_ARG;
+    if (a.rot > 0 && (!a.inv_freq || a.axes < 1 || a.axes > 4)) return KDN_ERR_INVALID_ARG;
+    const uintptr_t es = size_of(a.in_dtype);
+    const long long tokens = static_cast<long long>(a.B) * a.T;
+    for (int i = 0; i < 2; ++i) {
+        if (a.heads[i] == 0) continue;
+        const long long width = static_cast<long long>(a.heads[i]) * a.dk;
+        const long long lds[] = {a.ld[i], a.grad_x[i] ? a.grad_ld[i] : width};
+        for (long long ld : lds)
+            if (ld < width || ld * es % 16 != 0 || tokens > (1LL << 61) / ld) return KDN_ERR_INVALID_ARG;
+        const void* rows[] = {a.x[i], a.y[i], a.grad_y[i], a.grad_x[i]};
+        for (const void* p : rows)
+            if (!aligned(p, 16)) return KDN_ERR_INVALID_ARG;
+        if (!aligned(a.w[i], 16) || !aligned(a.grad_w[i], 4)) return KDN_ERR_INVALID_ARG;
+    }
+    if (!aligned(a.pos, 4) || !aligned(a.inv_freq, 4) || !aligned(a.axis, 4)) return KDN_ERR_INVALID_ARG;
+    return KDN_OK;
+}
 }  // namespace
 
 cudaError_t diag_take_device_error_bf16(int* status);
@@ -287,6 +343,117 @@ kdn_status kdn_mobius_scan_noalloc(const float* a, const float* b, const float* 
         if (!aligned(p, 4)) return KDN_ERR_INVALID_ARG;
     return mobius_launch_noalloc(a, b, c, d, lambda0, out, N, T, static_cast<cudaStream_t>(stream),
                                  g_wait_ns.load());
+}
+
+kdn_status kdn_gated_scan_fwd(const void* x, long long x_ld, const void* d, long long d_ld,
+                              const float* A, const float* h0, const int* offsets, int nseq, int leak,
+                              void* out, float* final_state, int B, int H, int T, int C,
+                              kdn_dtype in_dtype, kdn_dtype out_dtype, void* stream) {
+    if (T > 0 && (!x || !d || !out)) return KDN_ERR_INVALID_ARG;
+    GatedArgs a{};
+    a.x = x; a.x_ld = x_ld; a.d = d; a.d_ld = d_ld; a.A = A; a.h0 = h0; a.offsets = offsets; a.nseq = nseq;
+    a.leak = leak != 0; a.B = B; a.H = H; a.T = T; a.C = C; a.in_dtype = in_dtype; a.out_dtype = out_dtype;
+    a.out = out; a.final_state = final_state;
+    const kdn_status s = gated_check(a);
+    if (s != KDN_OK) return s;
+    return gated_fwd_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_gated_scan_bwd(const void* x, long long x_ld, const void* d, long long d_ld,
+                              const float* A, const float* h0, const int* offsets, int nseq, int leak,
+                              const void* out, const void* grad_out, const float* grad_final_state,
+                              void* grad_x, void* grad_d, float* grad_A, float* grad_h0, int B, int H,
+                              int T, int C, kdn_dtype in_dtype, kdn_dtype out_dtype, void* workspace,
+                              long long workspace_bytes, void* stream) {
+    if (T > 0 && ((leak && !x) || !d || !out || !grad_out || !grad_x || !grad_d)) return KDN_ERR_INVALID_ARG;
+    GatedArgs a{};
+    a.x = leak ? x : nullptr; a.x_ld = x_ld; a.d = d; a.d_ld = d_ld; a.A = A; a.h0 = h0;
+    a.offsets = offsets; a.nseq = nseq; a.leak = leak != 0; a.B = B; a.H = H; a.T = T; a.C = C;
+    a.in_dtype = in_dtype; a.out_dtype = out_dtype; a.out = const_cast<void*>(out); a.grad_out = grad_out;
+    a.grad_final_state = grad_final_state; a.grad_x = grad_x; a.grad_d = grad_d; a.grad_A = grad_A;
+    a.grad_h0 = grad_h0; a.workspace = workspace;
+    const kdn_status s = gated_check(a);
+    if (s != KDN_OK) return s;
+    if (workspace && (!aligned(workspace, 256) ||
+                      workspace_bytes < gated_bwd_workspace_bytes(B, H, T, C, nseq)))
+        return KDN_ERR_INVALID_ARG;
+    return gated_bwd_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_gated_scan_bwd_workspace(int B, int H, int T, int C, int nseq, long long* workspace_bytes) {
+    if (B < 1 || H < 1 || T < 0 || C < 1 || nseq < 0 || (nseq > 0 && B != 1) || !workspace_bytes)
+        return KDN_ERR_INVALID_ARG;
+    const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
+    if (rows > (1LL << 40) || rows > (1LL << 62) / C) return KDN_ERR_INVALID_ARG;
+    *workspace_bytes = gated_bwd_workspace_bytes(B, H, T, C, nseq);
+    return KDN_OK;
+}
+
+kdn_status kdn_gated_step(const void* x, const void* d, const float* A, int leak, const float* state,
+                          float* new_state, void* out, int B, int H, int C, kdn_dtype in_dtype,
+                          kdn_dtype out_dtype, void* stream) {
+    if (B < 1 || H < 1 || C < 1) return KDN_ERR_INVALID_ARG;
+    if (!x || !d || !A || !state || !new_state || !out) return KDN_ERR_INVALID_ARG;
+    if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return KDN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(B) * H > (1LL << 61) / C) return KDN_ERR_INVALID_ARG;
+    if (!aligned(x, size_of(in_dtype)) || !aligned(d, size_of(in_dtype)) || !aligned(out, size_of(out_dtype)) ||
+        !aligned(A, 4) || !aligned(state, 4) || !aligned(new_state, 4))
+        return KDN_ERR_INVALID_ARG;
+    return gated_step_launch(x, d, A, leak != 0, state, new_state, out, B, H, C, in_dtype, out_dtype,
+                             static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_qk_norm_rope_fwd(const void* q, long long q_ld, const void* k, long long k_ld,
+                                const float* wq, const float* wk, kdn_norm norm, float eps,
+                                const int* pos, int axes, const float* inv_freq, const int* axis,
+                                int rot, int interleaved, void* q_out, void* k_out, int B, int T,
+                                int Hq, int Hk, int dk, kdn_dtype in_dtype, kdn_dtype out_dtype,
+                                void* stream) {
+    if (T > 0 && ((Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)))) return KDN_ERR_INVALID_ARG;
+    QkArgs a{};
+    a.x[0] = q; a.x[1] = k; a.ld[0] = q_ld; a.ld[1] = k_ld; a.w[0] = wq; a.w[1] = wk;
+    a.heads[0] = Hq; a.heads[1] = Hk; a.y[0] = q_out; a.y[1] = k_out; a.norm = norm; a.eps = eps;
+    a.pos = pos; a.axes = axes; a.inv_freq = inv_freq; a.axis = axis; a.rot = rot;
+    a.interleaved = interleaved != 0; a.B = B; a.T = T; a.dk = dk; a.in_dtype = in_dtype;
+    a.out_dtype = out_dtype;
+    const kdn_status s = qk_check(a);
+    if (s != KDN_OK) return s;
+    if (T == 0) return KDN_OK;
+    return qk_fwd_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_qk_norm_rope_bwd(const void* q, long long q_ld, const void* k, long long k_ld,
+                                const float* wq, const float* wk, kdn_norm norm, float eps,
+                                const int* pos, int axes, const float* inv_freq, const int* axis,
+                                int rot, int interleaved, const void* grad_q_out,
+                                const void* grad_k_out, void* grad_q, long long gq_ld, void* grad_k,
+                                long long gk_ld, float* grad_wq, float* grad_wk, int B, int T, int Hq,
+                                int Hk, int dk, kdn_dtype in_dtype, kdn_dtype out_dtype,
+                                void* workspace, long long workspace_bytes, void* stream) {
+    if (T > 0 && ((Hq > 0 && (!q || !grad_q_out || !grad_q)) || (Hk > 0 && (!k || !grad_k_out || !grad_k))))
+        return KDN_ERR_INVALID_ARG;
+    QkArgs a{};
+    a.x[0] = q; a.x[1] = k; a.ld[0] = q_ld; a.ld[1] = k_ld; a.w[0] = wq; a.w[1] = wk;
+    a.heads[0] = Hq; a.heads[1] = Hk; a.grad_y[0] = grad_q_out; a.grad_y[1] = grad_k_out;
+    a.grad_x[0] = grad_q; a.grad_x[1] = grad_k; a.grad_ld[0] = gq_ld; a.grad_ld[1] = gk_ld;
+    a.grad_w[0] = Hq > 0 ? grad_wq : nullptr; a.grad_w[1] = Hk > 0 ? grad_wk : nullptr;
+    a.norm = norm; a.eps = eps; a.pos = pos; a.axes = axes; a.inv_freq = inv_freq; a.axis = axis;
+    a.rot = rot; a.interleaved = interleaved != 0; a.B = B; a.T = T; a.dk = dk; a.in_dtype = in_dtype;
+    a.out_dtype = out_dtype; a.workspace = workspace;
+    const kdn_status s = qk_check(a);
+    if (s != KDN_OK) return s;
+    if (workspace && (!aligned(workspace, 256) ||
+                      workspace_bytes < qk_bwd_workspace_bytes(B, T, Hq, Hk, dk)))
+        return KDN_ERR_INVALID_ARG;
+    if (T == 0 && !a.grad_w[0] && !a.grad_w[1]) return KDN_OK;
+    return qk_bwd_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, int dk, long long* workspace_bytes) {
+    if (B < 1 || T < 0 || Hq < 0 || Hk < 0 || Hq + Hk < 1 || !workspace_bytes) return KDN_ERR_INVALID_ARG;
+    if (!head_dim_ok(dk)) return KDN_ERR_UNSUPPORTED;
+    *workspace_bytes = qk_bwd_workspace_bytes(B, T, Hq, Hk, dk);
+    return KDN_OK;
 }
 
 const char* kdn_status_string(kdn_status s) {

@@ -93,6 +93,65 @@ struct DiagBwdArgs {
 kdn_status diag_bwd_launch(const DiagBwdArgs& a, cudaStream_t stream);
 long long diag_bwd_workspace_bytes(int B, int H, int T, int dk, int dv);
 
+// Arguments of one gated-recurrence call after host-side validation
+// (gated_scan.cu); the backward's pointers are null in a forward call.
+struct GatedArgs {
+    const void* x;
+    long long x_ld;
+    const void* d;
+    long long d_ld;
+    const float* A;
+    const float* h0;
+    const int* offsets;
+    int nseq;              // 0 without offsets
+    bool leak;
+    int B, H, T, C;
+    kdn_dtype in_dtype, out_dtype;
+    void* out;             // forward: written; backward: the forward's output
+    float* final_state;
+    const void* grad_out;
+    const float* grad_final_state;
+    void* grad_x;
+    void* grad_d;
+    float* grad_A;
+    float* grad_h0;
+    void* workspace;
+};
+kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream);
+kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream);
+long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq);
+kdn_status gated_step_launch(const void* x, const void* d, const float* A, bool leak,
+                             const float* state, float* new_state, void* out, int B, int H, int C,
+                             kdn_dtype in_dtype, kdn_dtype out_dtype, cudaStream_t stream);
+
+// Arguments of one query/key preparation after host-side validation
+// (qk_norm_rope.cu); the gradients' pointers are null in a forward call.
+struct QkArgs {
+    const void* x[2];      // q, k
+    long long ld[2];
+    const float* w[2];
+    int heads[2];
+    void* y[2];            // forward: written
+    const void* grad_y[2];
+    void* grad_x[2];
+    long long grad_ld[2];
+    float* grad_w[2];
+    kdn_norm norm;
+    float eps;
+    const int* pos;
+    int axes;
+    const float* inv_freq;
+    const int* axis;
+    int rot;
+    bool interleaved;
+    int B, T, dk;
+    kdn_dtype in_dtype, out_dtype;
+    void* workspace;
+};
+kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream);
+kdn_status qk_bwd_launch(const QkArgs& a, cudaStream_t stream);
+long long qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int dk);
+
 // Host-buffer pipelines (kdn_host.cu): arguments validated, every pointer a
 // host pointer; synchronous.
 kdn_status diag_host(const DiagArgs& a, cudaStream_t stream, long long wait_ns);

@@ -11,6 +11,10 @@ Functions mirror the C names:
 * :func:`diag_mobius_scan_fwd` -> ``kdn_diag_mobius_scan_fwd`` (per-head lambda in the same launch)
 * :func:`mobius_scan`    -> ``kdn_mobius_scan``
 * :func:`mobius_scan_noalloc` -> ``kdn_mobius_scan_noalloc``
+* :func:`gated_scan_fwd`, :func:`gated_scan_bwd`, :func:`gated_step` -> ``kdn_gated_*`` (the
+  recurrence with one gate per channel)
+* :func:`qk_norm_rope_fwd`, :func:`qk_norm_rope_bwd` -> ``kdn_qk_norm_rope_*`` (queries and keys for
+  the scans)
 * :func:`diag_scan_plan`, :func:`mobius_scan_plan` -> the ``*_plan`` queries
 * :func:`get_device_error`, :func:`set_wait_limit_ns`,
   :func:`debug_stall_mobius_tile`, :func:`status_string`, :func:`version`
@@ -72,6 +76,23 @@ def _load():
     lib.kdn_mobius_scan_host.argtypes = [fp, fp, fp, fp, fp, fp, ll, ll, vp]
     lib.kdn_mobius_scan_noalloc.restype = i
     lib.kdn_mobius_scan_noalloc.argtypes = [fp, fp, fp, fp, fp, fp, ll, ll, vp]
+    lib.kdn_gated_scan_fwd.restype = i
+    lib.kdn_gated_scan_fwd.argtypes = [vp, ll, vp, ll, fp, fp, vp, i, i, vp, fp, i, i, i, i, i, i, vp]
+    lib.kdn_gated_scan_bwd.restype = i
+    lib.kdn_gated_scan_bwd.argtypes = [vp, ll, vp, ll, fp, fp, vp, i, i, vp, vp, fp, vp, vp, fp, fp,
+                                       i, i, i, i, i, i, vp, ll, vp]
+    lib.kdn_gated_scan_bwd_workspace.restype = i
+    lib.kdn_gated_scan_bwd_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong)]
+    lib.kdn_gated_step.restype = i
+    lib.kdn_gated_step.argtypes = [vp, vp, fp, i, fp, fp, vp, i, i, i, i, i, vp]
+    lib.kdn_qk_norm_rope_fwd.restype = i
+    lib.kdn_qk_norm_rope_fwd.argtypes = [vp, ll, vp, ll, fp, fp, i, ctypes.c_float, vp, i, fp, vp, i, i,
+                                         vp, vp, i, i, i, i, i, i, i, vp]
+    lib.kdn_qk_norm_rope_bwd.restype = i
+    lib.kdn_qk_norm_rope_bwd.argtypes = [vp, ll, vp, ll, fp, fp, i, ctypes.c_float, vp, i, fp, vp, i, i,
+                                         vp, vp, vp, ll, vp, ll, fp, fp, i, i, i, i, i, i, i, vp, ll, vp]
+    lib.kdn_qk_norm_rope_bwd_workspace.restype = i
+    lib.kdn_qk_norm_rope_bwd_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong)]
     lib.kdn_status_string.restype = ctypes.c_char_p
     lib.kdn_status_string.argtypes = [i]
     lib.kdn_get_device_error.restype = i
@@ -390,6 +411,348 @@ def mobius_scan(a, b, c, d, lambda0, out=None, stream=None):
     if st != KDN_OK:
         raise KdnError(st, "kdn_mobius_scan")
     return out
+
+
+# ---------------------------------------------------------------------------
+# the recurrence with one gate per channel
+
+_DTYPES = {torch.bfloat16: KDN_BF16, torch.float32: KDN_F32}
+
+
+def _dtype_of(t, name):
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
+    return dt
+
+
+def _token_ld(t, name, dt, shape):
+    """Elements between consecutive tokens of a [B,T,C] or [B,H,T,C] tensor
+    whose channels are adjacent and whose rows follow one another (dense, or
+    for one head a column slice of a wider projection)."""
+    if t.dtype != dt:
+        raise ValueError(f"{name} must be {dt}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    T, C = shape[-2:]
+    if t.is_contiguous():
+        return C
+    st = t.stride()
+    ld = st[-2] if T > 1 else (st[0] if shape[0] > 1 and len(shape) == 3 else C)
+    if (C > 1 and st[-1] != 1) or ld < C:
+        raise ValueError(f"{name} must have adjacent channels and tokens apart by at least their number")
+    step = T * ld
+    for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
+        if n > 1 and s != step:
+            raise ValueError(f"{name}'s rows must follow one another (stride {step}), got stride {s}")
+        step *= n
+    return ld
+
+
+def _gated_sizes(x, A, offsets):
+    """(B, H, T, C, state rows, their shape) of a gated-recurrence call."""
+    if x.dim() == 3:
+        (B, T, C), H = x.shape, 1
+    elif x.dim() == 4:
+        B, H, T, C = x.shape
+    else:
+        raise ValueError(f"x must be [B,T,C] or [B,H,T,C], got {tuple(x.shape)}")
+    heads = (C,) if x.dim() == 3 else (H, C)
+    _check(A, "A", torch.float32, heads)
+    rows = B
+    if offsets is not None:
+        _check(offsets, "offsets", torch.int32)
+        if offsets.dim() != 1 or offsets.numel() < 2 or B != 1:
+            raise ValueError("offsets must be [nseq + 1] with B = 1")
+        rows = offsets.numel() - 1
+    return B, H, T, C, 0 if offsets is None else rows, (rows, *heads)
+
+
+def gated_scan_fwd(x, d, A, h0=None, leak=False, offsets=None, out=None, out_dtype=None,
+                   final_state=True, stream=None):
+    """Gated recurrence h_t = alpha_t h_{t-1} + w_t x_t, alpha_t = exp(-A d_t),
+    w_t = 1 or 1 - alpha_t with ``leak`` (see ``kdn_gated_scan_fwd``).
+
+    x, d [B,T,C] with A [C], or [B,H,T,C] with A [H,C] (x, d bf16 or fp32,
+    A fp32); a [B,T,C] x or d may be a column slice of a wider projection.
+    h0 [B,(H,)C] fp32 or None.  ``offsets`` [nseq + 1] int32 (device): packed
+    sequences in x [1,T,C] or [1,H,T,C]; h0 and final_state are then
+    [nseq,(H,)C].  ``out_dtype`` is out's type (x's by default);
+    ``final_state`` True (allocate), False/None (skip) or a tensor.  Returns
+    (out, final_state or None).  With offsets, rows of an ``out`` allocated
+    here that lie in no sequence are undefined."""
+    B, H, T, C, nseq, state = _gated_sizes(x, A, offsets)
+    it = _dtype_of(x, "x")
+    x_ld = _token_ld(x, "x", x.dtype, tuple(x.shape))
+    d_ld = _token_ld(d, "d", x.dtype, tuple(x.shape))
+    if h0 is not None:
+        _check(h0, "h0", torch.float32, state)
+    if out is None:
+        out = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
+    _check(out, "out", out_dtype, x.shape)
+    ot = _dtype_of(out, "out")
+    if final_state is True:
+        final_state = torch.empty(state, device=x.device, dtype=torch.float32)
+    elif final_state is False:
+        final_state = None
+    if final_state is not None:
+        _check(final_state, "final_state", torch.float32, state)
+    _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, final_state=final_state)
+    st = lib.kdn_gated_scan_fwd(_ptr(x), x_ld, _ptr(d), d_ld, _ptr(A), _ptr(h0), _ptr(offsets), nseq,
+                                int(leak), _ptr(out), _ptr(final_state), B, H, T, C, it, ot,
+                                _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_gated_scan_fwd")
+    return out, final_state
+
+
+def gated_scan_bwd_workspace(B, H, T, C, nseq=0) -> int:
+    """Bytes of device workspace ``gated_scan_bwd`` needs."""
+    n = ctypes.c_longlong(0)
+    st = lib.kdn_gated_scan_bwd_workspace(B, H, T, C, nseq, ctypes.byref(n))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_gated_scan_bwd_workspace")
+    return int(n.value)
+
+
+def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, grad_final_state=None,
+                   grad_x=None, grad_d=None, grad_A=True, grad_h0=True, workspace=None, stream=None):
+    """Backward pass of ``gated_scan_fwd`` (see ``kdn_gated_scan_bwd``): x, d,
+    A, h0, leak and offsets as given to it, ``out`` its output, ``grad_out``
+    of out's type.  ``grad_x``, ``grad_d``: dense tensors of x's type to write,
+    or None (allocate); ``grad_A``, ``grad_h0``: True (allocate), False/None
+    (skip) or fp32 tensors.  Returns a dict x, d, A, h0.  ``workspace``: a
+    uint8 device tensor of at least ``gated_scan_bwd_workspace`` bytes, or
+    None (one is taken from torch's caching allocator for the call)."""
+    B, H, T, C, nseq, state = _gated_sizes(x, A, offsets)
+    it = _dtype_of(x, "x")
+    x_ld = _token_ld(x, "x", x.dtype, tuple(x.shape))
+    d_ld = _token_ld(d, "d", x.dtype, tuple(x.shape))
+    ot = _dtype_of(out, "out")
+    _check(out, "out", None, x.shape)
+    _check(grad_out, "grad_out", out.dtype, x.shape)
+    for name, t in (("h0", h0), ("grad_final_state", grad_final_state)):
+        if t is not None:
+            _check(t, name, torch.float32, state)
+    g = {}
+    for name, t in (("x", grad_x), ("d", grad_d)):
+        g[name] = torch.empty(x.shape, device=x.device, dtype=x.dtype) if t is None else t
+        _check(g[name], "grad_" + name, x.dtype, x.shape)
+    for name, t, shape in (("A", grad_A, tuple(A.shape)), ("h0", grad_h0, state)):
+        if t is True:
+            t = torch.empty(shape, device=x.device, dtype=torch.float32)
+        elif t is False:
+            t = None
+        if t is not None:
+            _check(t, "grad_" + name, torch.float32, shape)
+        g[name] = t
+    ws_bytes = gated_scan_bwd_workspace(B, H, T, C, nseq)
+    if workspace is None:
+        workspace = torch.empty(max(ws_bytes, 1), device=x.device, dtype=torch.uint8)
+    elif workspace.numel() * workspace.element_size() < ws_bytes:
+        raise ValueError(f"workspace must hold {ws_bytes} bytes")
+    _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, grad_out=grad_out,
+                   grad_final_state=grad_final_state, grad_x=g["x"], grad_d=g["d"], grad_A=g["A"],
+                   grad_h0=g["h0"], workspace=workspace)
+    st = lib.kdn_gated_scan_bwd(_ptr(x), x_ld, _ptr(d), d_ld, _ptr(A), _ptr(h0), _ptr(offsets), nseq,
+                                int(leak), _ptr(out), _ptr(grad_out), _ptr(grad_final_state),
+                                _ptr(g["x"]), _ptr(g["d"]), _ptr(g["A"]), _ptr(g["h0"]), B, H, T, C,
+                                it, ot, _ptr(workspace), ws_bytes, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_gated_scan_bwd")
+    return g
+
+
+def gated_step(x, d, A, state, leak=False, new_state=None, out=None, out_dtype=None, stream=None):
+    """One token of ``gated_scan_fwd`` from a device-resident state (see
+    ``kdn_gated_step``): x, d [B,C] with A [C], or [B,H,C] with A [H,C]; state
+    fp32 of x's shape, updated in place, or left as it is when ``new_state``
+    is another tensor to write.  Returns out (x's type unless ``out_dtype``
+    says otherwise)."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [B,C] or [B,H,C], got {tuple(x.shape)}")
+    it = _dtype_of(x, "x")
+    shape = x.shape
+    if new_state is None:
+        new_state = state
+    if out is None:
+        out = torch.empty(shape, device=x.device, dtype=out_dtype or x.dtype)
+    _check(x, "x")
+    _check(d, "d", x.dtype, shape)
+    _check(A, "A", torch.float32, shape[1:])
+    _check(state, "state", torch.float32, shape)
+    _check(new_state, "new_state", torch.float32, shape)
+    _check(out, "out", out_dtype, shape)
+    ot = _dtype_of(out, "out")
+    _on_one_device(stream, x=x, d=d, A=A, state=state, new_state=new_state, out=out)
+    st = lib.kdn_gated_step(_ptr(x), _ptr(d), _ptr(A), int(leak), _ptr(state), _ptr(new_state), _ptr(out),
+                            shape[0], 1 if x.dim() == 2 else shape[1], shape[-1], it, ot, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_gated_step")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# queries and keys for the scans
+
+KDN_NORM_NONE, KDN_NORM_RMS, KDN_NORM_L2 = 0, 1, 2
+_NORMS = {"none": KDN_NORM_NONE, "rms": KDN_NORM_RMS, "l2": KDN_NORM_L2}
+
+
+def _head_rows(t, name, dt, B, T, dk):
+    """(heads, elements between tokens) of a [B,T,H,dk] tensor whose heads lie
+    side by side (dense, or a column slice of a fused projection)."""
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.shape[3] != dk:
+        raise ValueError(f"{name} must be [{B},{T},heads,{dk}], got {tuple(t.shape)}")
+    if t.dtype != dt:
+        raise ValueError(f"{name} must be {dt}, got {t.dtype}")
+    H = t.shape[2]
+    if t.is_contiguous():
+        return H, H * dk
+    st = t.stride()
+    ld = st[1] if T > 1 else (st[0] if B > 1 else H * dk)
+    if st[3] != 1 or (H > 1 and st[2] != dk) or ld < H * dk or (B > 1 and st[0] != T * ld):
+        raise ValueError(f"{name}'s heads must lie side by side and its tokens be evenly apart")
+    return H, ld
+
+
+def _qk_common(q, k, pos, inv_freq, wq, wk, norm, axis):
+    """Checks what the forward and the backward share; returns (B, T, dk,
+    dtype, norm, axes, rot, (Hq, q_ld), (Hk, k_ld))."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k must be given")
+    if first.dim() != 4:
+        raise ValueError(f"q and k must be [B,T,H,dk], got {tuple(first.shape)}")
+    B, T, _, dk = first.shape
+    dt = _dtype_of(first, "q" if q is not None else "k")
+    rows = [(0, 0) if t is None else _head_rows(t, name, first.dtype, B, T, dk)
+            for name, t in (("q", q), ("k", k))]
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _check(w, name, torch.float32, (dk,))
+    rot = axes = 0
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float32)
+        if inv_freq.dim() != 1 or 2 * inv_freq.numel() > dk:
+            raise ValueError(f"inv_freq must be [rot/2] with rot <= {dk}, got {tuple(inv_freq.shape)}")
+        rot, axes = 2 * inv_freq.numel(), 1
+        if pos is not None:
+            if pos.dim() == 2:
+                pos = pos.unsqueeze(0)
+            if pos.dim() != 3 or not 1 <= pos.shape[0] <= 4:
+                raise ValueError(f"pos must be [B,T] or [axes,B,T] with 1 to 4 axes, got {tuple(pos.shape)}")
+            axes = pos.shape[0]
+            _check(pos, "pos", torch.int32, (axes, B, T))
+        if axis is not None:
+            _check(axis, "axis", torch.int32, inv_freq.shape)
+    elif pos is not None or axis is not None:
+        raise ValueError("pos and axis need inv_freq")
+    return B, T, dk, dt, _NORMS[norm], axes, rot, rows[0], rows[1]
+
+
+def qk_norm_rope_fwd(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms", eps=1e-6, axis=None,
+                     interleaved=False, q_out=None, k_out=None, out_dtype=None, stream=None):
+    """Queries and keys for the scans (see ``kdn_qk_norm_rope_fwd``): the norm
+    of every head, the weight, the position rotation and the scans' layout.
+
+    q [B,T,Hq,dk], k [B,T,Hk,dk] bf16 or fp32, dense or column slices of a
+    fused projection (either may be None); ``pos`` [B,T] or [axes,B,T] int32
+    (None: the token index); ``inv_freq`` [rot/2] fp32 (None: no rotation);
+    ``wq``, ``wk`` [dk] fp32 or None; ``norm`` "rms", "l2" or "none"; ``axis``
+    [rot/2] int32, the position axis of each pair, or None (the first);
+    ``interleaved``: pairs (2p, 2p+1) instead of (p, p + rot/2).  Returns
+    (q_out [B,Hq,T,dk], k_out [B,Hk,T,dk]) of ``out_dtype`` (q's by default)."""
+    B, T, dk, it, nm, axes, rot, (Hq, q_ld), (Hk, k_ld) = _qk_common(q, k, pos, inv_freq, wq, wk, norm, axis)
+    first = q if q is not None else k
+    outs = []
+    for name, t, H, o in (("q_out", q, Hq, q_out), ("k_out", k, Hk, k_out)):
+        if t is None:
+            o = None
+        else:
+            if o is None:
+                o = torch.empty((B, H, T, dk), device=t.device, dtype=out_dtype or t.dtype)
+            _check(o, name, out_dtype, (B, H, T, dk))
+        outs.append(o)
+    out_dt = next(o for o in outs if o is not None)
+    ot = _dtype_of(out_dt, "out")
+    if outs[0] is not None and outs[1] is not None and outs[0].dtype != outs[1].dtype:
+        raise ValueError("q_out and k_out must have one type")
+    _on_one_device(stream, q=q, k=k, pos=pos, inv_freq=inv_freq, wq=wq, wk=wk, axis=axis, q_out=outs[0],
+                   k_out=outs[1])
+    st = lib.kdn_qk_norm_rope_fwd(_ptr(q), q_ld, _ptr(k), k_ld, _ptr(wq), _ptr(wk), nm, float(eps), _ptr(pos),
+                                  axes, _ptr(inv_freq), _ptr(axis), rot, int(interleaved), _ptr(outs[0]),
+                                  _ptr(outs[1]), B, T, Hq, Hk, dk, it, ot, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_qk_norm_rope_fwd")
+    return outs[0], outs[1]
+
+
+def qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk) -> int:
+    """Bytes of device workspace ``qk_norm_rope_bwd`` needs."""
+    n = ctypes.c_longlong(0)
+    st = lib.kdn_qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk, ctypes.byref(n))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_qk_norm_rope_bwd_workspace")
+    return int(n.value)
+
+
+def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=None, wk=None, norm="rms",
+                     eps=1e-6, axis=None, interleaved=False, grad_q=None, grad_k=None, grad_w=None,
+                     workspace=None, stream=None):
+    """Backward pass of ``qk_norm_rope_fwd`` (see ``kdn_qk_norm_rope_bwd``):
+    its inputs, and the gradients of its outputs ([B,H,T,dk], bf16 or fp32;
+    ``diag_scan_bwd``'s q and k as they are).  ``grad_q``, ``grad_k``: tensors
+    of q's type to write, dense or column slices of a fused gradient, or None
+    (allocate).  ``grad_w``: whether the weights' gradients are wanted (None:
+    of those given).  Returns a dict q, k [B,T,H,dk] and wq, wk [dk] fp32 or
+    None."""
+    B, T, dk, it, nm, axes, rot, (Hq, q_ld), (Hk, k_ld) = _qk_common(q, k, pos, inv_freq, wq, wk, norm, axis)
+    first = q if q is not None else k
+    g = {}
+    lds = {}
+    gts = []
+    for name, t, H, go, gx, w in (("q", q, Hq, grad_q_out, grad_q, wq), ("k", k, Hk, grad_k_out, grad_k, wk)):
+        g[name], lds[name], g["w" + name] = None, 0, None
+        if t is None:
+            continue
+        if go is None:
+            raise ValueError(f"grad_{name}_out must be given with {name}")
+        _check(go, f"grad_{name}_out", None, (B, H, T, dk))
+        gts.append(go.dtype)
+        g[name] = torch.empty((B, T, H, dk), device=t.device, dtype=t.dtype) if gx is None else gx
+        n, lds[name] = _head_rows(g[name], "grad_" + name, t.dtype, B, T, dk)
+        if n != H:
+            raise ValueError(f"grad_{name} must have {H} heads, got {n}")
+        if (w is not None) if grad_w is None else grad_w:
+            g["w" + name] = torch.empty(dk, device=t.device, dtype=torch.float32)
+    if len(set(gts)) > 1:
+        raise ValueError("grad_q_out and grad_k_out must have one type")
+    ot = _DTYPES.get(gts[0])
+    if ot is None:
+        raise ValueError(f"the outputs' gradients must be bf16 or fp32, got {gts[0]}")
+    ws_bytes = 0
+    if g["wq"] is not None or g["wk"] is not None:
+        ws_bytes = qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk)
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, device=first.device, dtype=torch.uint8)
+        elif workspace.numel() * workspace.element_size() < ws_bytes:
+            raise ValueError(f"workspace must hold {ws_bytes} bytes")
+    else:
+        workspace = None
+    _on_one_device(stream, q=q, k=k, grad_q_out=grad_q_out if q is not None else None,
+                   grad_k_out=grad_k_out if k is not None else None, pos=pos, inv_freq=inv_freq, wq=wq,
+                   wk=wk, axis=axis, grad_q=g["q"], grad_k=g["k"], workspace=workspace)
+    st = lib.kdn_qk_norm_rope_bwd(_ptr(q), q_ld, _ptr(k), k_ld, _ptr(wq), _ptr(wk), nm, float(eps), _ptr(pos),
+                                  axes, _ptr(inv_freq), _ptr(axis), rot, int(interleaved),
+                                  _ptr(grad_q_out), _ptr(grad_k_out), _ptr(g["q"]), lds["q"], _ptr(g["k"]),
+                                  lds["k"], _ptr(g["wq"]), _ptr(g["wk"]), B, T, Hq, Hk, dk, it, ot,
+                                  _ptr(workspace), ws_bytes, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_qk_norm_rope_bwd")
+    return g
 
 
 def diag_scan_plan(B, H, T, dk, dv, dtype=torch.bfloat16) -> dict:

@@ -2,7 +2,7 @@
  * kdn.h -- C ABI of the GB300 (sm_103a) uncertainty-tracked linear-attention
  * scans.  Plain pointers and sizes only; no C++ or framework types.
  *
- * Two operations:
+ * The two scans:
  *
  *  kdn_diag_scan_fwd -- the diagonal metaplastic update of
  *    "Learning to Remember, Learn, and Forget in Attention-Based Models"
@@ -21,6 +21,11 @@
  *    Moebius"):
  *        lambda_t = (a_t lambda_{t-1} + b_t) / (c_t lambda_{t-1} + d_t),
  *    computed as a parallel prefix scan of 2x2 matrix products.
+ *
+ * Beside them: the non-metaplastic limit, the backward pass and the one-token
+ * step of the diagonal scan, a gated recurrence with one gate per channel
+ * (forward, backward, step), and the norm and position rotation that make the
+ * scans' queries and keys (forward, backward).
  *
  * Conventions shared by every entry point:
  *  - All tensors are dense, row-major (C order) and contiguous.  Device
@@ -353,6 +358,176 @@ KDN_API kdn_status kdn_mobius_scan_plan(long long N, long long T, int* kernels,
 KDN_API kdn_status kdn_mobius_scan_noalloc(const float* a, const float* b, const float* c,
                                            const float* d, const float* lambda0, float* out,
                                            long long N, long long T, void* stream);
+
+/*
+ * kdn_gated_scan_fwd -- gated linear recurrence with one gate per channel:
+ *     alpha_t[c] = exp(-A[h][c] d_t[c]),
+ *     h_t[c] = alpha_t[c] h_{t-1}[c] + w_t[c] x_t[c],
+ * with w_t = 1 (leak = 0) or w_t = 1 - alpha_t (leak = 1: the state is a
+ * running mean of x).  It is the affine recursion of "Kalman Linear Attention
+ * (KLA)", Metodologia 2 (the information mean, an affine map per token after
+ * the lambda path), with the gate of the diagonal scan (alpha = exp(-A d)) on
+ * a vector state.
+ *
+ *   x, d      [B,H,T,C] in_dtype  input and gate input.  Consecutive tokens
+ *             are x_ld and d_ld elements apart (>= C; C when dense), rows
+ *             (b,h) T * ld: with H = 1 a tensor may be a column slice of a
+ *             wider [B,T,ld] projection.
+ *   A         [H,C] fp32          gate rate of each channel
+ *   h0        [B,H,C] fp32 or NULL (h_0 = 0)
+ *   out       [B,H,T,C] out_dtype, dense: h_t
+ *   final_state [B,H,C] fp32 or NULL: h_T (feeding it back as h0 of a call on
+ *             the following tokens gives one call's result)
+ *
+ * Packed sequences: with offsets (nseq + 1 int32 values in device memory,
+ * non-decreasing, within [0, T]) and B = 1, sequence n is tokens offsets[n]
+ * to offsets[n+1] - 1 of every head; h0 and final_state are then
+ * [nseq,H,C].  An empty sequence's final state is its initial one.  Tokens in
+ * no sequence are neither read nor written.  offsets = NULL (nseq = 0): B
+ * sequences of T tokens.  Offsets out of range are clamped to [0, T]; where
+ * they decrease, which tokens belong to which sequence is unspecified.
+ *
+ *   B >= 1, H >= 1, T >= 0, C >= 1; x, d and out element-aligned (16-byte
+ *   aligned rows, C and the lds multiples of 16 bytes, take the widest path).
+ *   B*H*T*max(x_ld, d_ld) < 2^62.  T = 0 writes only final_state.
+ *   out and final_state overlap no input.
+ *
+ * The state and every sum are fp32 whatever the types; out is rounded once.
+ * A d >= 0 is expected (alpha <= 1).  Results are deterministic.  Long
+ * sequences of few channels take stream-ordered scratch (KDN_ERR_ALLOC).
+ */
+KDN_API kdn_status kdn_gated_scan_fwd(const void* x, long long x_ld, const void* d, long long d_ld,
+                                      const float* A, const float* h0, const int* offsets, int nseq,
+                                      int leak, void* out, float* final_state, int B, int H, int T,
+                                      int C, kdn_dtype in_dtype, kdn_dtype out_dtype, void* stream);
+
+/*
+ * kdn_gated_scan_bwd -- backward pass of kdn_gated_scan_fwd: for
+ *     L = sum grad_out . out + sum grad_final_state . h_T
+ * writes dL/d(x, d, A, h0), given the forward's out.
+ *
+ *   x         as for the forward; read only when leak = 1 (may be NULL else)
+ *   d, A, h0, offsets, nseq, leak   as for the forward
+ *   out       [B,H,T,C] out_dtype, dense: the forward's output (the states)
+ *   grad_out  [B,H,T,C] out_dtype, dense
+ *   grad_final_state [B,H,C] ([nseq,H,C]) fp32 or NULL
+ *   grad_x, grad_d  [B,H,T,C] in_dtype, dense, written (tokens in no sequence
+ *             are not)
+ *   grad_A    [H,C] fp32 or NULL, written: summed over batch and tokens
+ *   grad_h0   [B,H,C] ([nseq,H,C]) fp32 or NULL, written
+ *   workspace as for kdn_diag_scan_bwd: at least kdn_gated_scan_bwd_workspace
+ *             bytes, 256-byte aligned, or NULL (stream-ordered scratch).
+ *
+ * The states enter dL/dd as given: with a bf16 out they carry its rounding.
+ * Sums in fp32, in a fixed order (deterministic).  T = 0 writes grad_h0 (=
+ * grad_final_state) and grad_A (= 0).
+ */
+KDN_API kdn_status kdn_gated_scan_bwd(const void* x, long long x_ld, const void* d, long long d_ld,
+                                      const float* A, const float* h0, const int* offsets, int nseq,
+                                      int leak, const void* out, const void* grad_out,
+                                      const float* grad_final_state, void* grad_x, void* grad_d,
+                                      float* grad_A, float* grad_h0, int B, int H, int T, int C,
+                                      kdn_dtype in_dtype, kdn_dtype out_dtype, void* workspace,
+                                      long long workspace_bytes, void* stream);
+
+/* Bytes of workspace kdn_gated_scan_bwd needs for these sizes on the current
+ * device (no GPU work; it reads the device's SM count). */
+KDN_API kdn_status kdn_gated_scan_bwd_workspace(int B, int H, int T, int C, int nseq,
+                                                long long* workspace_bytes);
+
+/*
+ * kdn_gated_step -- one token of kdn_gated_scan_fwd for B x H rows whose
+ * state is kept on the device (batched decoding).
+ *
+ *   x, d      [B,H,C] in_dtype, dense      A [H,C] fp32
+ *   state     [B,H,C] fp32: h before the token
+ *   new_state [B,H,C] fp32: h after it; may be state itself (in place), but
+ *             may not overlap it otherwise
+ *   out       [B,H,C] out_dtype
+ *
+ * Equal to kdn_gated_scan_fwd with T = 1, h0 = state, up to rounding.  No
+ * scratch.
+ */
+KDN_API kdn_status kdn_gated_step(const void* x, const void* d, const float* A, int leak,
+                                  const float* state, float* new_state, void* out, int B, int H,
+                                  int C, kdn_dtype in_dtype, kdn_dtype out_dtype, void* stream);
+
+typedef enum {
+    KDN_NORM_NONE = 0,
+    KDN_NORM_RMS = 1,   /* x / sqrt(mean(x^2) + eps) */
+    KDN_NORM_L2 = 2     /* x / sqrt(sum(x^2) + eps) */
+} kdn_norm;
+
+/*
+ * kdn_qk_norm_rope_fwd -- the queries and keys that the scans take, from the
+ * rows of a projection: every head's dk elements are normalised, scaled by a
+ * weight and rotated by the token's position, and written in the scans'
+ * [B,H,T,dk] layout.
+ *
+ *   q, k      token (b,t) is row b*T + t of q_ld (k_ld) elements, head h its
+ *             elements h*dk .. h*dk + dk - 1, in_dtype: a dense [B,T,H,dk]
+ *             (ld = H*dk) or a column slice of a fused projection.  Hq or Hk
+ *             may be 0 (that tensor, its weight, its output and its gradients
+ *             are then not touched and may be NULL).
+ *   wq, wk    [dk] fp32 or NULL (1)
+ *   norm, eps the norm above; eps >= 0, unused with KDN_NORM_NONE
+ *   rot       number of leading elements that rotate (even, 0 <= rot <= dk);
+ *             the rest are only normalised.  Pair p (p < rot/2) is elements
+ *             (p, p + rot/2), or (2p, 2p + 1) when interleaved != 0, and
+ *             (y1, y2) becomes (y1 cos - y2 sin, y1 sin + y2 cos) with
+ *             theta = pos * inv_freq[p].
+ *   pos       [axes,B,T] int32 or NULL (every axis is t).  1 <= axes <= 4:
+ *             one position per axis (for instance time, height, width).
+ *   axis      [rot/2] int32 or NULL (all 0): the axis whose position pair p
+ *             takes (values are clamped to [0, axes-1])
+ *   inv_freq  [rot/2] fp32, finite
+ *   q_out     [B,Hq,T,dk], k_out [B,Hk,T,dk]  out_dtype, dense
+ *
+ *   B >= 1, T >= 0, Hq, Hk >= 0 and not both 0, dk in {16, 32, 64, 128}.
+ *   Tensors 16-byte aligned, lds multiples of 16 bytes.  Outputs overlap no
+ *   input.
+ *
+ * The sum of squares is fp32 (|x| < 1e18).  Angles are taken in 64-bit
+ * fixed-point turns, so cos and sin have fp32's accuracy at every position.
+ */
+KDN_API kdn_status kdn_qk_norm_rope_fwd(const void* q, long long q_ld, const void* k, long long k_ld,
+                                        const float* wq, const float* wk, kdn_norm norm, float eps,
+                                        const int* pos, int axes, const float* inv_freq,
+                                        const int* axis, int rot, int interleaved, void* q_out,
+                                        void* k_out, int B, int T, int Hq, int Hk, int dk,
+                                        kdn_dtype in_dtype, kdn_dtype out_dtype, void* stream);
+
+/*
+ * kdn_qk_norm_rope_bwd -- backward pass of kdn_qk_norm_rope_fwd for
+ *     L = sum grad_q_out . q_out + sum grad_k_out . k_out.
+ *
+ *   q ... interleaved   as for the forward (the forward's inputs)
+ *   grad_q_out, grad_k_out  [B,H,T,dk] out_dtype, dense (the layout and type
+ *             of kdn_diag_scan_bwd's grad_q and grad_k with KDN_F32)
+ *   grad_q, grad_k  in_dtype, written in the projection's layout, rows of
+ *             gq_ld (gk_ld) elements
+ *   grad_wq, grad_wk  [dk] fp32 or NULL, written: summed over tokens and
+ *             heads (of the weight used, given or 1)
+ *   workspace as for kdn_diag_scan_bwd, at least
+ *             kdn_qk_norm_rope_bwd_workspace bytes (needed only when grad_wq
+ *             or grad_wk is written)
+ *
+ * Deterministic.  T = 0 writes only grad_wq, grad_wk (= 0).
+ */
+KDN_API kdn_status kdn_qk_norm_rope_bwd(const void* q, long long q_ld, const void* k, long long k_ld,
+                                        const float* wq, const float* wk, kdn_norm norm, float eps,
+                                        const int* pos, int axes, const float* inv_freq,
+                                        const int* axis, int rot, int interleaved,
+                                        const void* grad_q_out, const void* grad_k_out, void* grad_q,
+                                        long long gq_ld, void* grad_k, long long gk_ld,
+                                        float* grad_wq, float* grad_wk, int B, int T, int Hq, int Hk,
+                                        int dk, kdn_dtype in_dtype, kdn_dtype out_dtype,
+                                        void* workspace, long long workspace_bytes, void* stream);
+
+/* Bytes of workspace kdn_qk_norm_rope_bwd needs for these sizes on the
+ * current device (no GPU work; it reads the device's SM count). */
+KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, int dk,
+                                                  long long* workspace_bytes);
 
 /* Human-readable name of a status code (static string). */
 KDN_API const char* kdn_status_string(kdn_status s);
