@@ -1,8 +1,10 @@
 // gated_device.cuh -- device helpers of the per-channel gated recurrence
-// (gated_scan.cu): typed loads and stores and the gate.
+// (gated_scan.cu): typed loads and stores, packed fp32 pairs and the gate.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <cstdint>
 
 namespace kdn {
 namespace gated {
@@ -21,6 +23,38 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Two fp32 values per instruction (sm_100 and later).
+struct F2 {
+    float x, y;
+};
+
+__device__ __forceinline__ uint64_t pk(F2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ F2 unpk(uint64_t r) {
+    F2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+    return a;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)), "l"(pk(c)));
+    return unpk(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    return unpk(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    return unpk(r);
+}
+__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
+
 // The gate alpha = exp(z), z = -A d, as alpha = a + e: a the rounded value, e
 // what the rounding lost, and w = 1 - alpha.  A long memory has alpha next to
 // 1, where a float's step is 6e-8 whatever 1 - alpha is; a scan that used the
@@ -29,10 +63,40 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 //
 // |z| <= 0.35: expm1(z) = z p(z), p the degree-5 Chebyshev interpolant of
 // (e^z - 1)/z on [-0.35, 0.35] (1.3e-7 relative with its roundings).  Beyond,
-// memories are three tokens and 2^(z log2 e) of the hardware serves.
+// memories are three tokens and 2^(z log2 e) of the hardware serves; there
+// a - 1 and m are the same rounding, so e is zero by itself.
 struct Gate {
     float a, e, w;
 };
+struct Gate2 {
+    F2 a, e, w;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ Gate2 gate2(F2 z) {
+    F2 p = both(0.0013934532f);
+    p = fma2(p, z, both(0.008369861f));
+    p = fma2(p, z, both(0.041666456f));
+    p = fma2(p, z, both(0.16666499f));
+    p = fma2(p, z, both(0.5f));
+    p = fma2(p, z, both(1.0f));
+    const F2 s = mul2(p, z);
+    const F2 y = mul2(z, both(1.4426950408889634f));
+    const F2 big{ex2(y.x), ex2(y.y)};
+    const F2 bm = add2(big, both(-1.f)), sa = add2(s, both(1.f));
+    const bool bx = fabsf(z.x) <= 0.35f, by = fabsf(z.y) <= 0.35f;
+    const F2 m{bx ? s.x : bm.x, by ? s.y : bm.y};
+    Gate2 g;
+    g.a = F2{bx ? sa.x : big.x, by ? sa.y : big.y};
+    g.e = fma2(add2(g.a, both(-1.f)), both(-1.f), m);
+    g.w = mul2(m, both(-1.f));
+    return g;
+}
 
 __device__ __forceinline__ Gate gate(float z) {
     float p = 0.0013934532f;
@@ -41,20 +105,67 @@ __device__ __forceinline__ Gate gate(float z) {
     p = fmaf(p, z, 0.16666499f);
     p = fmaf(p, z, 0.5f);
     p = fmaf(p, z, 1.0f);
-    float big;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(big) : "f"(z * 1.4426950408889634f));
+    const float big = ex2(z * 1.4426950408889634f);
     const bool small = fabsf(z) <= 0.35f;
     const float m = small ? z * p : big - 1.f;   // expm1(z)
     Gate g;
     g.a = small ? 1.f + m : big;
-    g.e = small ? m - (g.a - 1.f) : 0.f;
+    g.e = m - (g.a - 1.f);
     g.w = -m;
     return g;
 }
 
-// a * s + b with a = the gate
+// alpha s + b
+__device__ __forceinline__ float decay_add(float a, float e, float s, float b) {
+    return fmaf(a, s, fmaf(e, s, b));
+}
 __device__ __forceinline__ float decay_add(const Gate& g, float s, float b) {
-    return fmaf(g.a, s, fmaf(g.e, s, b));
+    return decay_add(g.a, g.e, s, b);
+}
+
+// V adjacent elements of a type, as loaded and stored by one lane.
+template <typename T, int V>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16, 1> {
+    uint16_t r;
+    __device__ __forceinline__ float get(int) const { return __uint_as_float(static_cast<uint32_t>(r) << 16); }
+    __device__ __forceinline__ void set(const float* f) { r = __bfloat16_as_ushort(__float2bfloat16_rn(f[0])); }
+};
+template <>
+struct Vec<__nv_bfloat16, 2> {
+    uint32_t r;
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i == 0 ? r << 16 : r & 0xffff0000u);
+    }
+    __device__ __forceinline__ void set(const float* f) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[0], f[1]);
+        r = *reinterpret_cast<const uint32_t*>(&b);
+    }
+};
+template <>
+struct Vec<float, 1> {
+    float r;
+    __device__ __forceinline__ float get(int) const { return r; }
+    __device__ __forceinline__ void set(const float* f) { r = f[0]; }
+};
+template <>
+struct Vec<float, 2> {
+    float2 r;
+    __device__ __forceinline__ float get(int i) const { return i == 0 ? r.x : r.y; }
+    __device__ __forceinline__ void set(const float* f) { r = make_float2(f[0], f[1]); }
+};
+
+// Streaming loads and stores: every element is used once.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const T* p) {
+    Vec<T, V> v;
+    v.r = __ldcs(reinterpret_cast<const decltype(v.r)*>(p));
+    return v;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const Vec<T, V>& v) {
+    __stcs(reinterpret_cast<std::remove_const_t<decltype(v.r)>*>(p), v.r);
 }
 
 }  // namespace gated
