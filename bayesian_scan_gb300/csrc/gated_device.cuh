@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace kdn {
 namespace gated {
@@ -164,8 +165,79 @@ __device__ __forceinline__ Vec<T, V> load(const T* p) {
     return v;
 }
 template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> peek(const char* p) {
+    Vec<T, V> v;
+    v.r = *reinterpret_cast<const decltype(v.r)*>(p);
+    return v;
+}
+template <typename T, int V>
+__device__ __forceinline__ void poke(char* p, const Vec<T, V>& v) {
+    *reinterpret_cast<std::remove_const_t<decltype(v.r)>*>(p) = v.r;
+}
+template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const Vec<T, V>& v) {
     __stcs(reinterpret_cast<std::remove_const_t<decltype(v.r)>*>(p), v.r);
+}
+
+// Asynchronous copies global -> shared memory; `bytes` < SIZE fills the rest
+// with zeros (0: nothing is read).
+template <int SIZE>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes) {
+    if (SIZE == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A warp's K x ROWB block of rows `ld` bytes apart: rows first <= j < last,
+// columns below `width` bytes; the rest of the block becomes zeros (`safe`:
+// any valid address, named where nothing is read).  SIZE 16:
+// lanes take 16-byte pieces in order; SIZE 4: a lane takes the 4-byte words
+// lane, lane + 32, ... of every row.
+template <int SIZE, int ROWB, int K>
+__device__ __forceinline__ void rows_in(uint32_t dst, const void* safe, const char* src, long long ld, int first,
+                                        int last, int width, int lane) {
+    constexpr int PER = ROWB / SIZE;                       // pieces per row
+    if (PER >= 32) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int q = 0; q < PER / 32; ++q) {
+                const int col = (q * 32 + lane) * SIZE;
+                const bool ok = j >= first && j < last && col < width;
+                copy_async<SIZE>(dst + j * ROWB + col, ok ? src + j * ld + col : safe, ok ? SIZE : 0);
+            }
+    } else {
+        constexpr int RPI = 32 / (PER < 32 ? PER : 32);    // rows per instruction
+        const int j0 = lane / PER, col = lane % PER * SIZE;
+        const char* p = src + j0 * ld + col;
+#pragma unroll
+        for (int i = 0; i < K / RPI; ++i) {
+            const int j = j0 + i * RPI;
+            const bool ok = j >= first && j < last && col < width;
+            copy_async<SIZE>(dst + j * ROWB + col, ok ? p : safe, ok ? SIZE : 0);
+            p += RPI * ld;
+        }
+    }
+}
+
+// The other way, 16-byte pieces from shared memory.
+template <int ROWB, int K>
+__device__ __forceinline__ void rows_out(char* dst, long long ld, const char* src, int first, int last, int width,
+                                         int lane) {
+    constexpr int PER = ROWB / 16, RPI = 32 / PER;
+    const int j0 = lane / PER, col = lane % PER * 16;
+    char* p = dst + j0 * ld + col;
+#pragma unroll
+    for (int i = 0; i < K / RPI; ++i) {
+        const int j = j0 + i * RPI;
+        if (j >= first && j < last && col < width)
+            __stcs(reinterpret_cast<float4*>(p), *reinterpret_cast<const float4*>(src + j * ROWB + col));
+        p += RPI * ld;
+    }
 }
 
 }  // namespace gated

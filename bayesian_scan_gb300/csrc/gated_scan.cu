@@ -64,77 +64,138 @@ struct Cut {
     int slabs, S;
 };
 
-// An affine map h -> (a + e) h + s of one channel over a span of tokens.
-struct __align__(16) Map {
-    float a, e, s, z;      // z: the exponent's sum, alpha = exp(z)
+// An affine map h -> (a + e) h + s of a lane's V channels over a span of
+// tokens, z its exponent (a + e = exp(z)), as shared-memory words that one
+// 16-byte access per channel moves: {a, e, s, z}, or {a0, a1, e0, e1} and
+// {s0, s1, z0, z1}.
+template <int V>
+struct Map {
+    float a[V], e[V], s[V], z[V];
 };
+template <int V>
+using MapWords = float4[V][32];
 
-__device__ __forceinline__ Map map_of(float z, float s) {
-    const Gate g = gate(z);
-    return Map{g.a, g.e, s, z};
+template <int V>
+__device__ __forceinline__ Map<V> map_of(const float (&z)[V], const float (&s)[V]) {
+    Map<V> m;
+    if constexpr (V == 1) {
+        const Gate g = gate(z[0]);
+        m.a[0] = g.a;
+        m.e[0] = g.e;
+    } else {
+        const Gate2 g = gate2(F2{z[0], z[1]});
+        m.a[0] = g.a.x;
+        m.a[1] = g.a.y;
+        m.e[0] = g.e.x;
+        m.e[1] = g.e.y;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        m.s[v] = s[v];
+        m.z[v] = z[v];
+    }
+    return m;
 }
-__device__ __forceinline__ float apply(const Map& m, float h) { return decay_add(m.a, m.e, h, m.s); }
+
+template <int V>
+__device__ __forceinline__ void put_map(MapWords<V>& w, int lane, const Map<V>& m) {
+    if constexpr (V == 1) {
+        w[0][lane] = make_float4(m.a[0], m.e[0], m.s[0], m.z[0]);
+    } else {
+        w[0][lane] = make_float4(m.a[0], m.a[1], m.e[0], m.e[1]);
+        w[1][lane] = make_float4(m.s[0], m.s[1], m.z[0], m.z[1]);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ Map<V> get_map(const MapWords<V>& w, int lane) {
+    Map<V> m;
+    const float4 q = w[0][lane];
+    if constexpr (V == 1) {
+        m.a[0] = q.x;
+        m.e[0] = q.y;
+        m.s[0] = q.z;
+        m.z[0] = q.w;
+    } else {
+        const float4 r = w[1][lane];
+        m.a[0] = q.x;
+        m.a[1] = q.y;
+        m.e[0] = q.z;
+        m.e[1] = q.w;
+        m.s[0] = r.x;
+        m.s[1] = r.y;
+        m.z[0] = r.z;
+        m.z[1] = r.w;
+    }
+    return m;
+}
+
+template <int V>
+__device__ __forceinline__ void apply(const Map<V>& m, float (&h)[V]) {
+    if constexpr (V == 1) {
+        h[0] = decay_add(m.a[0], m.e[0], h[0], m.s[0]);
+    } else {
+        const F2 hh{h[0], h[1]};
+        const F2 n = fma2(F2{m.a[0], m.a[1]}, hh, fma2(F2{m.e[0], m.e[1]}, hh, F2{m.s[0], m.s[1]}));
+        h[0] = n.x;
+        h[1] = n.y;
+    }
+}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Folding the maps of a round.  Every warp hands in its map; on return
 // `start` is the state before the warp's tokens and `carry` the one after the
-// round's last tile, both from the carry before the round.
+// round's last tile, both from the carry before the round.  Rounds alternate
+// between two buffers, so one barrier a round is enough.
 template <int V>
 struct Fold {
-    Map warp[2][WARPS][V][32];
-    Map cta[2][MAX_CLUSTER][V][32];
+    MapWords<V> warp[2][WARPS];
+    MapWords<V> cta[2][MAX_CLUSTER];
 };
 
 template <int V>
 __device__ __forceinline__ void fold_round(Fold<V>& f, int buf, int S, int rank, int warp, int lane,
                                            const float (&z)[V], const float (&s)[V], float (&carry)[V],
                                            float (&start)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) f.warp[buf][warp][v][lane] = map_of(z[v], s[v]);
+    put_map<V>(f.warp[buf][warp], lane, map_of<V>(z, s));
     __syncthreads();
     if (S > 1) {
         // warp j sends the tile's map to CTA j
         if (warp < S) {
-            cg::cluster_group cl = cg::this_cluster();
-            Map* to = cl.map_shared_rank(&f.cta[buf][rank][0][lane], warp);
+            float h[V], zz[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float h = 0.f, zz = 0.f;
+            for (int v = 0; v < V; ++v) h[v] = zz[v] = 0.f;
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) {
-                    const Map m = f.warp[buf][w][v][lane];
-                    h = apply(m, h);
-                    zz += m.z;
-                }
-                to[v * 32] = map_of(zz, h);
+            for (int w = 0; w < WARPS; ++w) {
+                const Map<V> m = get_map<V>(f.warp[buf][w], lane);
+                apply<V>(m, h);
+#pragma unroll
+                for (int v = 0; v < V; ++v) zz[v] += m.z[v];
             }
+            cg::cluster_group cl = cg::this_cluster();
+            put_map<V>(*cl.map_shared_rank(&f.cta[buf][rank], warp), lane, map_of<V>(zz, h));
         }
         cluster_arrive();
         cluster_wait();
-        float c[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) c[v] = start[v] = carry[v];
-        for (int j = 0; j < S; ++j)
+        for (int v = 0; v < V; ++v) start[v] = carry[v];
+        for (int j = 0; j < S; ++j) {
+            if (j == rank)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (j == rank) start[v] = c[v];
-                c[v] = apply(f.cta[buf][j][v][lane], c[v]);
-            }
-#pragma unroll
-        for (int v = 0; v < V; ++v) carry[v] = c[v];
-        for (int w = 0; w < warp; ++w)
-#pragma unroll
-            for (int v = 0; v < V; ++v) start[v] = apply(f.warp[buf][w][v][lane], start[v]);
+                for (int v = 0; v < V; ++v) start[v] = carry[v];
+            apply<V>(get_map<V>(f.cta[buf][j], lane), carry);
+        }
+        for (int w = 0; w < warp; ++w) apply<V>(get_map<V>(f.warp[buf][w], lane), start);
     } else {
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w)
+        for (int w = 0; w < WARPS; ++w) {
+            if (w == warp)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (w == warp) start[v] = carry[v];
-                carry[v] = apply(f.warp[buf][w][v][lane], carry[v]);
-            }
+                for (int v = 0; v < V; ++v) start[v] = carry[v];
+            apply<V>(get_map<V>(f.warp[buf][w], lane), carry);
+        }
     }
 }
 
@@ -393,14 +454,355 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
         // the warps' shares, in order
         __syncthreads();
 #pragma unroll
-        for (int v = 0; v < V; ++v) fold.warp[0][warp][v][lane].s = dA[v];
+        for (int v = 0; v < V; ++v) fold.warp[0][warp][v][lane].x = dA[v];
         __syncthreads();
         if (warp == 0 && on)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float sum = 0.f;
-                for (int w = 0; w < WARPS; ++w) sum += fold.warp[0][w][v][lane].s;
+                for (int w = 0; w < WARPS; ++w) sum += fold.warp[0][w][v][lane].x;
                 part[(sr * S + rank) * p.C + c + v] = sum;
+            }
+    }
+}
+
+// The staged form: a warp's rows come through shared memory, STAGES rounds
+// ahead by asynchronous copies of SIZE bytes that fill what lies outside the
+// sequence or the channels with zeros, and with SIZE = 16 leave through it
+// too, in 16-byte pieces (a 4-byte SIZE takes rows that are only aligned to
+// that, and stores straight from the registers).  A warp reads only rows that
+// it copied itself, so no barrier beyond the fold's is needed.
+constexpr int STAGES = 2;
+
+template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
+struct FwdShared {
+    static constexpr int ROW = 32 * V * static_cast<int>(sizeof(TI)), OROW = 32 * V * static_cast<int>(sizeof(TO));
+    struct __align__(16) Stage {
+        char x[K * ROW], d[K * ROW];                 // out overwrites both
+    };
+    Stage st[STAGES][WARPS];
+    Fold<V> fold;
+};
+
+template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
+__global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p, const Cut cut) {
+    using Sh = FwdShared<TI, TO, V, K, LEAK, SIZE>;
+    static_assert(Sh::OROW * K <= static_cast<int>(sizeof(typename Sh::Stage)), "out takes the stage's place");
+    extern __shared__ __align__(16) char smem[];
+    Sh& sh = *reinterpret_cast<Sh*>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = cut.S, rank = blockIdx.x % S;
+    const long long unit = blockIdx.x / S;
+    const long long sr = unit / cut.slabs;
+    const int c0 = static_cast<int>(unit - sr * cut.slabs) * 32 * V, c = c0 + lane * V;
+    const Span sp = span_of(p, sr);
+    const int rounds = (sp.hi - sp.lo + S * WARPS * K - 1) / (S * WARPS * K);
+    const long long arow = (sr % p.H) * p.C;
+
+    float nA[V], carry[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        nA[v] = c + v < p.C ? -p.A[arow + c + v] : 0.f;
+        carry[v] = c + v < p.C && p.h0 ? p.h0[sr * p.C + c + v] : 0.f;
+    }
+    const int t0 = sp.lo + (rank * WARPS + warp) * K, step = S * WARPS * K;
+    const long long xld = p.x_ld * sizeof(TI), dld = p.d_ld * sizeof(TI);
+    const char* xp = static_cast<const char*>(p.x) + (sp.row * p.T + t0) * xld + c0 * sizeof(TI);
+    const char* dp = static_cast<const char*>(p.d) + (sp.row * p.T + t0) * dld + c0 * sizeof(TI);
+    TO* op = static_cast<TO*>(p.out) + (sp.row * p.T + t0) * p.C + c0;
+    const int width = (p.C - c0) * static_cast<int>(sizeof(TI)), owidth = (p.C - c0) * static_cast<int>(sizeof(TO));
+
+    auto fetch = [&](int r) {
+        const int n = sp.hi - t0 - r * step;               // tokens left
+        if (n > 0) {
+            typename Sh::Stage& st = sh.st[r % STAGES][warp];
+            const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(st.x));
+            rows_in<SIZE, Sh::ROW, K>(a, p.x, xp + static_cast<long long>(r) * step * xld, xld, 0, n, width, lane);
+            rows_in<SIZE, Sh::ROW, K>(a + K * Sh::ROW, p.d, dp + static_cast<long long>(r) * step * dld, dld, 0, n, width, lane);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+        if (i < rounds) fetch(i);
+        else copy_commit();
+    if (S > 1) {   // every CTA of the cluster runs before its shared memory is written
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int r = 0; r < rounds; ++r) {
+        const int n = sp.hi - t0 - r * step;
+        char* xs = sh.st[r % STAGES][warp].x;
+        const char* ds = sh.st[r % STAGES][warp].d;
+        copy_wait<STAGES - 1>();
+        __syncwarp();
+        Gates<V, K> g;
+        float b[K][V], z[V], s[V], h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
+        if (n > 0) {                                        // (the warp as one)
+#pragma unroll
+            for (int i = 0; i < K * V / 2; ++i) {
+                const int k0 = 2 * i / V, v0 = 2 * i % V, k1 = (2 * i + 1) / V, v1 = (2 * i + 1) % V;
+                const Vec<TI, V> d0 = peek<TI, V>(ds + k0 * Sh::ROW + lane * V * sizeof(TI)),
+                                 x0 = peek<TI, V>(xs + k0 * Sh::ROW + lane * V * sizeof(TI));
+                Vec<TI, V> d1 = d0, x1 = x0;
+                if (V == 1) {
+                    d1 = peek<TI, V>(ds + k1 * Sh::ROW + lane * V * sizeof(TI));
+                    x1 = peek<TI, V>(xs + k1 * Sh::ROW + lane * V * sizeof(TI));
+                }
+                const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{d0.get(v0), d1.get(v1)});
+                const Gate2 gg = gate2(zz);
+                g.a[k0][v0] = gg.a.x;
+                g.a[k1][v1] = gg.a.y;
+                g.put(i, gg.e);
+                F2 x{x0.get(v0), x1.get(v1)};
+                if (LEAK) x = mul2(x, gg.w);
+                b[k0][v0] = x.x;
+                b[k1][v1] = x.y;
+                if constexpr (V == 1) {
+                    z[0] += zz.x + zz.y;
+                    s[0] = decay_add(gg.a.x, gg.e.x, s[0], x.x);
+                    s[0] = decay_add(gg.a.y, gg.e.y, s[0], x.y);
+                } else {
+                    const F2 ss{s[0], s[1]};
+                    const F2 m = fma2(gg.a, ss, fma2(gg.e, ss, x)), zs = add2(F2{z[0], z[1]}, zz);
+                    s[0] = m.x;
+                    s[1] = m.y;
+                    z[0] = zs.x;
+                    z[1] = zs.y;
+                }
+            }
+        }
+        fold_round<V>(sh.fold, r & 1, S, rank, warp, lane, z, s, carry, h);
+        if (n > 0) {
+            TO* o = op + static_cast<long long>(r) * step * p.C;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if constexpr (V == 1) {
+                    h[0] = decay_add(g.a[k][0], g.err1(k, 0), h[0], b[k][0]);
+                } else {
+                    const F2 hh{h[0], h[1]};
+                    const F2 m = fma2(F2{g.a[k][0], g.a[k][1]}, hh, fma2(g.err(k), hh, F2{b[k][0], b[k][1]}));
+                    h[0] = m.x;
+                    h[1] = m.y;
+                }
+                if (SIZE == 16) {
+                    Vec<TO, V> q;
+                    q.set(h);
+                    poke<TO, V>(xs + k * Sh::OROW + lane * V * sizeof(TO), q);
+                } else if (k < n) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (c + v < p.C) __stcs(o + static_cast<long long>(k) * p.C + lane * V + v, from_f32<TO>(h[v]));
+                }
+            }
+            __syncwarp();
+            if (SIZE == 16) {
+                rows_out<Sh::OROW, K>(reinterpret_cast<char*>(o), p.C * static_cast<long long>(sizeof(TO)), xs, 0, n,
+                                      owidth, lane);
+                __syncwarp();
+            }
+        }
+        if (r + STAGES < rounds) fetch(r + STAGES);
+        else copy_commit();
+    }
+    if (p.final_state && rank == 0 && warp == 0)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (c + v < p.C) p.final_state[sr * p.C + c + v] = carry[v];
+}
+
+template <typename TI, typename TO, int V, int K>
+struct BwdShared {
+    static constexpr int ROW = 32 * V * static_cast<int>(sizeof(TI)), OROW = 32 * V * static_cast<int>(sizeof(TO));
+    struct __align__(16) Stage {
+        char d[K * ROW], x[K * ROW], g[K * OROW], h[K * OROW];   // grad d overwrites d, grad x x
+    };
+    Stage st[STAGES][WARPS];
+    Fold<V> fold;
+};
+
+template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
+__global__ void __launch_bounds__(THREADS, 2)
+gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
+    using Sh = BwdShared<TI, TO, V, K>;
+    extern __shared__ __align__(16) char smem[];
+    Sh& sh = *reinterpret_cast<Sh*>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = cut.S, rank = blockIdx.x % S;
+    const long long unit = blockIdx.x / S;
+    const long long sr = unit / cut.slabs;
+    const int c0 = static_cast<int>(unit - sr * cut.slabs) * 32 * V, c = c0 + lane * V;
+    const Span sp = span_of(p, sr);
+    const int rounds = (sp.hi - sp.lo + S * WARPS * K - 1) / (S * WARPS * K);
+    const long long arow = (sr % p.H) * p.C;
+
+    float nA[V], carry[V], dA[V], first[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const bool on = c + v < p.C;
+        nA[v] = on ? -p.A[arow + c + v] : 0.f;
+        carry[v] = on && p.grad_final_state ? p.grad_final_state[sr * p.C + c + v] : 0.f;
+        first[v] = on && p.h0 ? p.h0[sr * p.C + c + v] : 0.f;
+        dA[v] = 0.f;
+    }
+    // a warp's rows of round r are tokens base - r step .. + K - 1, walked from the last
+    const int base = sp.hi - (rank * WARPS + warp + 1) * K, step = S * WARPS * K;
+    const long long dld = p.d_ld * sizeof(TI), xld = p.x_ld * sizeof(TI), old_ = p.C * static_cast<long long>(sizeof(TO));
+    const long long row = sp.row * p.T;
+    const int width = (p.C - c0) * static_cast<int>(sizeof(TI)), owidth = (p.C - c0) * static_cast<int>(sizeof(TO));
+
+    auto fetch = [&](int r) {
+        const int t = base - r * step;
+        if (t + K > sp.lo) {
+            typename Sh::Stage& st = sh.st[r % STAGES][warp];
+            const int f = max(sp.lo - t, 0);               // rows before the sequence
+            const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(st.d));
+            constexpr int N = K * Sh::ROW, M = K * Sh::OROW;
+            rows_in<SIZE, Sh::ROW, K>(a, p.d, static_cast<const char*>(p.d) + (row + t) * dld + c0 * sizeof(TI), dld, f, K,
+                                      width, lane);
+            if (LEAK)
+                rows_in<SIZE, Sh::ROW, K>(a + N, p.x, static_cast<const char*>(p.x) + (row + t) * xld + c0 * sizeof(TI), xld,
+                                          f, K, width, lane);
+            rows_in<SIZE, Sh::OROW, K>(a + 2 * N, p.grad_out, static_cast<const char*>(p.grad_out) + (row + t) * old_ + c0 * sizeof(TO),
+                                       old_, f, K, owidth, lane);
+            // the states before: one token earlier (h0 for the first one, below)
+            rows_in<SIZE, Sh::OROW, K>(a + 2 * N + M, p.out, static_cast<const char*>(p.out) + (row + t - 1) * old_ + c0 * sizeof(TO),
+                                       old_, f + (t + f == sp.lo), K, owidth, lane);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+        if (i < rounds) fetch(i);
+        else copy_commit();
+    if (S > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int r = 0; r < rounds; ++r) {
+        const int t = base - r * step;
+        const bool any = t + K > sp.lo;
+        typename Sh::Stage& st = sh.st[r % STAGES][warp];
+        copy_wait<STAGES - 1>();
+        __syncwarp();
+        Gates<V, K> g;
+        float w[LEAK ? K : 1][V], z[V], s[V], u[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
+        if (any) {
+            // u = alpha (g + u): the map of a token is (alpha, alpha g); index k counts back from the last
+#pragma unroll
+            for (int i = 0; i < K * V / 2; ++i) {
+                const int k0 = 2 * i / V, v0 = 2 * i % V, k1 = (2 * i + 1) / V, v1 = (2 * i + 1) % V;
+                const int j0 = K - 1 - k0, j1 = K - 1 - k1;
+                const Vec<TI, V> d0 = peek<TI, V>(st.d + j0 * Sh::ROW + lane * V * sizeof(TI));
+                const Vec<TO, V> g0 = peek<TO, V>(st.g + j0 * Sh::OROW + lane * V * sizeof(TO));
+                Vec<TI, V> d1 = d0;
+                Vec<TO, V> g1 = g0;
+                if (V == 1) {
+                    d1 = peek<TI, V>(st.d + j1 * Sh::ROW + lane * V * sizeof(TI));
+                    g1 = peek<TO, V>(st.g + j1 * Sh::OROW + lane * V * sizeof(TO));
+                }
+                const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{d0.get(v0), d1.get(v1)});
+                const Gate2 gg = gate2(zz);
+                g.a[k0][v0] = gg.a.x;
+                g.a[k1][v1] = gg.a.y;
+                if (LEAK) {                                 // e follows from w
+                    w[LEAK ? k0 : 0][v0] = gg.w.x;
+                    w[LEAK ? k1 : 0][v1] = gg.w.y;
+                } else {
+                    g.put(i, gg.e);
+                }
+                if constexpr (V == 1) {
+                    z[0] += zz.x + zz.y;
+                    const float h0 = s[0] + g0.get(0);
+                    s[0] = decay_add(gg.a.x, gg.e.x, h0, 0.f);
+                    const float h1 = s[0] + g1.get(0);
+                    s[0] = decay_add(gg.a.y, gg.e.y, h1, 0.f);
+                } else {
+                    const F2 dh = add2(F2{s[0], s[1]}, F2{g0.get(0), g0.get(1)});
+                    const F2 m = fma2(gg.a, dh, mul2(gg.e, dh)), zs = add2(F2{z[0], z[1]}, zz);
+                    s[0] = m.x;
+                    s[1] = m.y;
+                    z[0] = zs.x;
+                    z[1] = zs.y;
+                }
+            }
+        }
+        fold_round<V>(sh.fold, r & 1, S, rank, warp, lane, z, s, carry, u);
+        if (any) {
+            TI* gx_out = static_cast<TI*>(p.grad_x) + (row + t) * p.C + c0;
+            TI* gd_out = static_cast<TI*>(p.grad_d) + (row + t) * p.C + c0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int j = K - 1 - k;
+                const Vec<TI, V> dv = peek<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI));
+                const Vec<TO, V> gv = peek<TO, V>(st.g + j * Sh::OROW + lane * V * sizeof(TO));
+                const Vec<TO, V> hv = peek<TO, V>(st.h + j * Sh::OROW + lane * V * sizeof(TO));
+                Vec<TI, V> xv = dv;
+                if (LEAK) xv = peek<TI, V>(st.x + j * Sh::ROW + lane * V * sizeof(TI));
+                float gx[V], gd[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float a = g.a[k][v];
+                    const float e = LEAK ? -w[LEAK ? k : 0][v] - (a - 1.f) : g.err1(k, v);
+                    const float dh = u[v] + gv.get(v);
+                    u[v] = fmaf(a, dh, e * dh);
+                    float prev = t + j == sp.lo ? first[v] : hv.get(v);
+                    gx[v] = dh;
+                    if (LEAK) {
+                        prev -= xv.get(v);
+                        gx[v] = w[LEAK ? k : 0][v] * dh;
+                    }
+                    const float m = u[v] * prev;
+                    gd[v] = nA[v] * m;
+                    dA[v] = fmaf(-dv.get(v), m, dA[v]);     // (d = 0 outside the sequence)
+                }
+                if (SIZE == 16) {
+                    Vec<TI, V> q;
+                    q.set(gx);
+                    poke<TI, V>(st.x + j * Sh::ROW + lane * V * sizeof(TI), q);
+                    q.set(gd);
+                    poke<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI), q);
+                } else if (t + j >= sp.lo) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (c + v < p.C) {
+                            __stcs(gx_out + static_cast<long long>(j) * p.C + lane * V + v, from_f32<TI>(gx[v]));
+                            __stcs(gd_out + static_cast<long long>(j) * p.C + lane * V + v, from_f32<TI>(gd[v]));
+                        }
+                }
+            }
+            __syncwarp();
+            if (SIZE == 16) {
+                const int f = max(sp.lo - t, 0);
+                const long long ld = p.C * static_cast<long long>(sizeof(TI));
+                rows_out<Sh::ROW, K>(reinterpret_cast<char*>(gx_out), ld, st.x, f, K, width, lane);
+                rows_out<Sh::ROW, K>(reinterpret_cast<char*>(gd_out), ld, st.d, f, K, width, lane);
+                __syncwarp();
+            }
+        }
+        if (r + STAGES < rounds) fetch(r + STAGES);
+        else copy_commit();
+    }
+    if (p.grad_h0 && rank == 0 && warp == 0)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (c + v < p.C) p.grad_h0[sr * p.C + c + v] = carry[v];
+    if (part) {
+        // the warps' shares, in order
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) sh.fold.warp[0][warp][v][lane].x = dA[v];
+        __syncthreads();
+        if (warp == 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float sum = 0.f;
+                for (int i = 0; i < WARPS; ++i) sum += sh.fold.warp[0][i][v][lane].x;
+                if (c + v < p.C) part[(sr * S + rank) * p.C + c + v] = sum;
             }
     }
 }
@@ -449,27 +851,32 @@ int cluster_size(long long rows, int C, int T) {
     return S;
 }
 
-// Whether every row of every tensor takes V-element accesses.
-bool vector_ok(const GatedArgs& a, int V) {
-    if (a.C % V) return false;
-    const uintptr_t is = (a.in_dtype == KDN_BF16 ? 2 : 4) * V, os = (a.out_dtype == KDN_BF16 ? 2 : 4) * V;
-    const void* ins[] = {a.x, a.d, a.grad_x, a.grad_d};
-    const void* outs[] = {a.out, a.grad_out};
-    for (const void* q : ins)
-        if (reinterpret_cast<uintptr_t>(q) % is) return false;
-    for (const void* q : outs)
-        if (reinterpret_cast<uintptr_t>(q) % os) return false;
-    return (!a.x || a.x_ld % V == 0) && a.d_ld % V == 0;
+// Whether every row of every tensor starts on a multiple of `bytes` and is a
+// multiple of it long.
+bool rows_ok(const GatedArgs& a, long long bytes) {
+    const long long is = a.in_dtype == KDN_BF16 ? 2 : 4, os = a.out_dtype == KDN_BF16 ? 2 : 4;
+    const void* ptrs[] = {a.x, a.d, a.grad_x, a.grad_d, a.out, a.grad_out};
+    for (const void* q : ptrs)
+        if (reinterpret_cast<uintptr_t>(q) % bytes) return false;
+    return a.C * is % bytes == 0 && a.C * os % bytes == 0 && a.d_ld * is % bytes == 0 &&
+           (!a.x || a.x_ld * is % bytes == 0);
 }
 
 // One launch of a walk kernel over all (state row, slab) units.
 template <typename... KArgs, typename... Args>
-kdn_status launch_walk(void (*kernel)(KArgs...), long long rows, const Cut& cut, cudaStream_t stream, Args... args) {
+kdn_status launch_walk(void (*kernel)(KArgs...), long long rows, const Cut& cut, size_t smem, cudaStream_t stream,
+                       Args... args) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return from_cuda(e);
+    }
     const long long blocks = rows * cut.slabs * cut.S;
     if (blocks > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -493,16 +900,20 @@ kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream) {
     return by_type(a, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
-        constexpr int VV = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1;
-        auto go = [&](auto kernel, int V) {
-            cut.slabs = (a.C + 32 * V - 1) / (32 * V);
-            return launch_walk(kernel, rows, cut, stream, a, cut);
+        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 16;
+        auto go = [&](auto kernel, int v, size_t smem) {
+            cut.slabs = (a.C + 32 * v - 1) / (32 * v);
+            return launch_walk(kernel, rows, cut, smem, stream, a, cut);
         };
-        if (VV > 1 && vector_ok(a, VV))
-            return a.leak ? go(gated_fwd_kernel<TI, TO, VV, 16, true>, VV)
-                          : go(gated_fwd_kernel<TI, TO, VV, 16, false>, VV);
-        return a.leak ? go(gated_fwd_kernel<TI, TO, 1, 16, true>, 1)
-                      : go(gated_fwd_kernel<TI, TO, 1, 16, false>, 1);
+        auto leak = [&](auto l) {
+            constexpr bool L = decltype(l)::value;
+            if (rows_ok(a, 16))
+                return go(gated_fwd_staged<TI, TO, V, K, L, 16>, V, sizeof(FwdShared<TI, TO, V, K, L, 16>));
+            if (rows_ok(a, 4))
+                return go(gated_fwd_staged<TI, TO, V, K, L, 4>, V, sizeof(FwdShared<TI, TO, V, K, L, 4>));
+            return go(gated_fwd_kernel<TI, TO, 1, K, L>, 1, 0);
+        };
+        return a.leak ? leak(std::true_type()) : leak(std::false_type());
     });
 }
 
@@ -518,16 +929,18 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream) {
     kdn_status s = by_type(a, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
-        constexpr int VV = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1;
-        auto go = [&](auto kernel, int V) {
-            cut.slabs = (a.C + 32 * V - 1) / (32 * V);
-            return launch_walk(kernel, rows, cut, stream, a, cut, part);
+        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 8;
+        auto go = [&](auto kernel, int v, size_t smem) {
+            cut.slabs = (a.C + 32 * v - 1) / (32 * v);
+            return launch_walk(kernel, rows, cut, smem, stream, a, cut, part);
         };
-        if (VV > 1 && vector_ok(a, VV))
-            return a.leak ? go(gated_bwd_kernel<TI, TO, VV, 8, true>, VV)
-                          : go(gated_bwd_kernel<TI, TO, VV, 8, false>, VV);
-        return a.leak ? go(gated_bwd_kernel<TI, TO, 1, 8, true>, 1)
-                      : go(gated_bwd_kernel<TI, TO, 1, 8, false>, 1);
+        auto leak = [&](auto l) {
+            constexpr bool L = decltype(l)::value;
+            if (rows_ok(a, 16)) return go(gated_bwd_staged<TI, TO, V, K, L, 16>, V, sizeof(BwdShared<TI, TO, V, K>));
+            if (rows_ok(a, 4)) return go(gated_bwd_staged<TI, TO, V, K, L, 4>, V, sizeof(BwdShared<TI, TO, V, K>));
+            return go(gated_bwd_kernel<TI, TO, 1, K, L>, 1, 0);
+        };
+        return a.leak ? leak(std::true_type()) : leak(std::false_type());
     });
     if (s == KDN_OK && a.grad_A) {
         const long long blocks = static_cast<long long>((a.C + THREADS - 1) / THREADS) * a.H;
