@@ -56,48 +56,53 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 }
 __device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
 
-// The gate alpha = exp(z), z = -A d, as alpha = a + e: a the rounded value, e
-// what the rounding lost, and w = 1 - alpha.  A long memory has alpha next to
-// 1, where a float's step is 6e-8 whatever 1 - alpha is; a scan that used the
-// rounded alpha alone would drift by that much per token of its memory
-// (7e-6 of the state at a memory of a thousand tokens; with e, 1e-7).
-//
-// |z| <= 0.35: expm1(z) = z p(z), p the degree-5 Chebyshev interpolant of
-// (e^z - 1)/z on [-0.35, 0.35] (1.3e-7 relative with its roundings).  Beyond,
-// memories are three tokens and 2^(z log2 e) of the hardware serves; there
-// a - 1 and m are the same rounding, so e is zero by itself.
-struct Gate {
-    float a, e, w;
-};
-struct Gate2 {
-    F2 a, e, w;
-};
-
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
+// The gate alpha = exp(z), z = -A d, of two elements, and w = 1 - alpha.
+//
+// |z| <= 0.25: expm1(z) = z p(z), p the degree-4 Chebyshev interpolant of
+// (e^z - 1)/z on [-0.25, 0.25] (1.9e-7 of expm1 with its roundings, alpha to
+// half a step and a little).  Beyond, memories are four tokens and 2^(z log2
+// e) of the hardware (2^-22) serves.
+struct Gate2 {
+    F2 a, w;
+};
+
+template <bool W>
 __device__ __forceinline__ Gate2 gate2(F2 z) {
-    F2 p = both(0.0013934532f);
-    p = fma2(p, z, both(0.008369861f));
-    p = fma2(p, z, both(0.041666456f));
-    p = fma2(p, z, both(0.16666499f));
-    p = fma2(p, z, both(0.5f));
-    p = fma2(p, z, both(1.0f));
-    const F2 s = mul2(p, z);
+    F2 p = both(0.00834884773939848f);
+    p = fma2(p, z, both(0.04177529364824295f));
+    p = fma2(p, z, both(0.1666664183139801f));
+    p = fma2(p, z, both(0.4999983012676239f));
+    p = fma2(p, z, both(1.f));
     const F2 y = mul2(z, both(1.4426950408889634f));
-    const F2 big{ex2(y.x), ex2(y.y)};
-    const F2 bm = add2(big, both(-1.f)), sa = add2(s, both(1.f));
-    const bool bx = fabsf(z.x) <= 0.35f, by = fabsf(z.y) <= 0.35f;
-    const F2 m{bx ? s.x : bm.x, by ? s.y : bm.y};
+    const F2 big{ex2(y.x), ex2(y.y)}, near = fma2(p, z, both(1.f));
+    const bool bx = fabsf(z.x) <= 0.25f, by = fabsf(z.y) <= 0.25f;
     Gate2 g;
-    g.a = F2{bx ? sa.x : big.x, by ? sa.y : big.y};
-    g.e = fma2(add2(g.a, both(-1.f)), both(-1.f), m);
-    g.w = mul2(m, both(-1.f));
+    g.a = F2{bx ? near.x : big.x, by ? near.y : big.y};
+    if (W) {
+        const F2 m = mul2(p, F2{-z.x, -z.y}), f = fma2(big, both(-1.f), both(1.f));
+        g.w = F2{bx ? m.x : f.x, by ? m.y : f.y};
+    }
     return g;
 }
+
+// The same as alpha = a + e: a the rounded value, e what the rounding lost.
+// A long memory has alpha next to 1, where a float's step is 6e-8 whatever
+// 1 - alpha is: a state carried through a thousand rounded decays would be
+// off by 7e-6.  So a span's decay is exp of its summed exponents, in this
+// form, and only the at most 16 tokens that a warp composes itself multiply
+// rounded alphas.
+//
+// |z| <= 0.35: degree 5, 1.3e-7 of expm1; beyond, a - 1 and m are the same
+// rounding, so e is zero by itself.
+struct Gate {
+    float a, e, w;
+};
 
 __device__ __forceinline__ Gate gate(float z) {
     float p = 0.0013934532f;
@@ -194,32 +199,40 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 
 // A warp's K x ROWB block of rows `ld` bytes apart: rows first <= j < last,
 // columns below `width` bytes; the rest of the block becomes zeros (`safe`:
-// any valid address, named where nothing is read).  SIZE 16:
-// lanes take 16-byte pieces in order; SIZE 4: a lane takes the 4-byte words
-// lane, lane + 32, ... of every row.
+// any valid address, named where nothing is read).  SIZE 16: lanes take
+// 16-byte pieces in order; SIZE 4: a lane takes 4-byte words 32 apart.
+template <int SIZE, int ROWB, int K>
+struct Rows {
+    static constexpr int PER = ROWB / SIZE;                    // pieces per row
+    static constexpr int RPI = PER >= 32 ? 1 : 32 / PER;       // rows per instruction
+    static constexpr int CPR = PER >= 32 ? PER / 32 : 1;       // instructions per row
+};
+
 template <int SIZE, int ROWB, int K>
 __device__ __forceinline__ void rows_in(uint32_t dst, const void* safe, const char* src, long long ld, int first,
                                         int last, int width, int lane) {
-    constexpr int PER = ROWB / SIZE;                       // pieces per row
-    if (PER >= 32) {
+    using R = Rows<SIZE, ROWB, K>;
+    const int j0 = R::PER >= 32 ? 0 : lane / R::PER, col = (R::PER >= 32 ? lane : lane % R::PER) * SIZE;
+    const char* p = src + j0 * ld + col;
+    dst += j0 * ROWB + col;
+    if (first <= 0 && last >= K && width >= ROWB) {            // (the warp as one)
 #pragma unroll
-        for (int j = 0; j < K; ++j)
+        for (int i = 0; i < K / R::RPI; ++i) {
 #pragma unroll
-            for (int q = 0; q < PER / 32; ++q) {
-                const int col = (q * 32 + lane) * SIZE;
-                const bool ok = j >= first && j < last && col < width;
-                copy_async<SIZE>(dst + j * ROWB + col, ok ? src + j * ld + col : safe, ok ? SIZE : 0);
-            }
+            for (int q = 0; q < R::CPR; ++q)
+                copy_async<SIZE>(dst + i * R::RPI * ROWB + q * 32 * SIZE, p + q * 32 * SIZE, SIZE);
+            p += R::RPI * ld;
+        }
     } else {
-        constexpr int RPI = 32 / (PER < 32 ? PER : 32);    // rows per instruction
-        const int j0 = lane / PER, col = lane % PER * SIZE;
-        const char* p = src + j0 * ld + col;
 #pragma unroll
-        for (int i = 0; i < K / RPI; ++i) {
-            const int j = j0 + i * RPI;
-            const bool ok = j >= first && j < last && col < width;
-            copy_async<SIZE>(dst + j * ROWB + col, ok ? p : safe, ok ? SIZE : 0);
-            p += RPI * ld;
+        for (int i = 0; i < K / R::RPI; ++i) {
+            const int j = j0 + i * R::RPI;
+#pragma unroll
+            for (int q = 0; q < R::CPR; ++q) {
+                const bool ok = j >= first && j < last && col + q * 32 * SIZE < width;
+                copy_async<SIZE>(dst + i * R::RPI * ROWB + q * 32 * SIZE, ok ? p + q * 32 * SIZE : safe, ok ? SIZE : 0);
+            }
+            p += R::RPI * ld;
         }
     }
 }
@@ -228,15 +241,17 @@ __device__ __forceinline__ void rows_in(uint32_t dst, const void* safe, const ch
 template <int ROWB, int K>
 __device__ __forceinline__ void rows_out(char* dst, long long ld, const char* src, int first, int last, int width,
                                          int lane) {
-    constexpr int PER = ROWB / 16, RPI = 32 / PER;
-    const int j0 = lane / PER, col = lane % PER * 16;
+    using R = Rows<16, ROWB, K>;
+    const int j0 = lane / R::PER, col = lane % R::PER * 16;
     char* p = dst + j0 * ld + col;
+    src += j0 * ROWB + col;
+    const bool full = first <= 0 && last >= K && width >= ROWB;
 #pragma unroll
-    for (int i = 0; i < K / RPI; ++i) {
-        const int j = j0 + i * RPI;
-        if (j >= first && j < last && col < width)
-            __stcs(reinterpret_cast<float4*>(p), *reinterpret_cast<const float4*>(src + j * ROWB + col));
-        p += RPI * ld;
+    for (int i = 0; i < K / R::RPI; ++i) {
+        const int j = j0 + i * R::RPI;
+        if (full || (j >= first && j < last && col < width))
+            __stcs(reinterpret_cast<float4*>(p), *reinterpret_cast<const float4*>(src + i * R::RPI * ROWB));
+        p += R::RPI * ld;
     }
 }
 

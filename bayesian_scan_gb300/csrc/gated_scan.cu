@@ -12,7 +12,7 @@
 //
 // Layout.  Tokens lie C elements apart, so lanes run along the channels (V
 // each, 128 bytes a warp) and every warp owns K consecutive tokens of a tile
-// of WARPS * K.  A warp composes its tokens from a zero state (the affine map
+// of NW * K.  A warp composes its tokens from a zero state (the affine map
 // h -> alpha h + s of its span), the warps' maps are folded through shared
 // memory, and a second pass over the tokens, still in registers, writes the
 // states.  So every element is read once and written once, and HBM bounds the
@@ -24,22 +24,22 @@
 // to all others' shared memory and one cluster barrier later every CTA knows
 // the state before its tile and before the next round.  The composition's
 // order is fixed, so results do not depend on the schedule.
-#include <cooperative_groups.h>
-
 #include <type_traits>
 
 #include "gated_device.cuh"
+#include "kdn_device.cuh"
 #include "kdn_internal.h"
 
 namespace kdn {
 namespace {
 
-namespace cg = cooperative_groups;
 using namespace gated;
 
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
 constexpr int MAX_CLUSTER = 8;
+constexpr int THREADS = 256;      // of the kernels without tiles
+constexpr int FWD_WARPS = 8, BWD_WARPS = 8;
+
+__device__ int g_gated_error = 0;
 
 // The tokens of state row n*H + h (a batch, or a packed sequence): [lo, hi)
 // of the T-token row `row`.
@@ -62,6 +62,7 @@ __device__ __forceinline__ Span span_of(const GatedArgs& p, long long sr) {
 // How one call is cut: slabs of 32 V channels, clusters of S CTAs.
 struct Cut {
     int slabs, S;
+    long long wait_ns;     // limit of one wait inside a cluster
 };
 
 // An affine map h -> (a + e) h + s of a lane's V channels over a span of
@@ -78,19 +79,11 @@ using MapWords = float4[V][32];
 template <int V>
 __device__ __forceinline__ Map<V> map_of(const float (&z)[V], const float (&s)[V]) {
     Map<V> m;
-    if constexpr (V == 1) {
-        const Gate g = gate(z[0]);
-        m.a[0] = g.a;
-        m.e[0] = g.e;
-    } else {
-        const Gate2 g = gate2(F2{z[0], z[1]});
-        m.a[0] = g.a.x;
-        m.a[1] = g.a.y;
-        m.e[0] = g.e.x;
-        m.e[1] = g.e.y;
-    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+        const Gate g = gate(z[v]);
+        m.a[v] = g.a;
+        m.e[v] = g.e;
         m.s[v] = s[v];
         m.z[v] = z[v];
     }
@@ -142,43 +135,118 @@ __device__ __forceinline__ void apply(const Map<V>& m, float (&h)[V]) {
     }
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Folding the maps of a round.  Every warp hands in its map; on return
 // `start` is the state before the warp's tokens and `carry` the one after the
 // round's last tile, both from the carry before the round.  Rounds alternate
 // between two buffers, so one barrier a round is enough.
-template <int V>
+//
+// In a cluster the tile's map goes to every CTA's shared memory by stores
+// that complete on the receiver's mbarrier: no fence waits for the round's
+// global stores, as the cluster barrier's release would (an eighth of the
+// time).  A CTA sends round r only after all its warps have read round r - 2,
+// and receives all of round r - 1 before it sends round r, so no store finds
+// its buffer in use.
+template <int V, int NW>
 struct Fold {
-    MapWords<V> warp[2][WARPS];
+    MapWords<V> warp[2][NW];
     MapWords<V> cta[2][MAX_CLUSTER];
+    uint64_t full[2];
+
+    // Every CTA of the cluster runs, its barriers set up, before one sends.
+    __device__ __forceinline__ void begin(int S) {
+        if (S > 1) {
+            if (threadIdx.x == 0) {
+                mbar_init(&full[0], 1);
+                mbar_init(&full[1], 1);
+                mbar_init_fence();
+            }
+            cluster_sync();
+        }
+    }
+    // No CTA leaves while another may still send to it.
+    __device__ __forceinline__ void end(int S, bool late) {
+        if (S > 1) {
+            cluster_sync();
+            if (late) {   // what was sent and not waited for arrives in the meantime
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 100000) __nanosleep(1000);
+            }
+        }
+    }
 };
 
-template <int V>
-__device__ __forceinline__ void fold_round(Fold<V>& f, int buf, int S, int rank, int warp, int lane,
-                                           const float (&z)[V], const float (&s)[V], float (&carry)[V],
-                                           float (&start)[V]) {
+__device__ __forceinline__ bool full_try(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded: after limit_ns it records an error and no later round waits.
+__device__ __forceinline__ void full_wait(uint64_t* bar, uint32_t parity, long long limit_ns, bool& late) {
+    if (late || full_try(bar, parity)) return;
+    const unsigned long long t0 = globaltimer_ns();
+    while (!full_try(bar, parity))
+        if (static_cast<long long>(globaltimer_ns() - t0) > limit_ns) {
+            record_error(&g_gated_error, KDN_ERR_TIMEOUT);
+            late = true;
+            return;
+        }
+}
+
+__device__ __forceinline__ void send(uint32_t dst, float4 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    return r;
+}
+
+template <int V, int NW>
+__device__ __forceinline__ void fold_round(Fold<V, NW>& f, int r, int S, int rank, int warp, int lane,
+                                           long long limit_ns, bool& late, const float (&z)[V], const float (&s)[V],
+                                           float (&carry)[V], float (&start)[V]) {
+    const int buf = r & 1;
     put_map<V>(f.warp[buf][warp], lane, map_of<V>(z, s));
     __syncthreads();
     if (S > 1) {
-        // warp j sends the tile's map to CTA j
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&f.full[buf], S * sizeof(MapWords<V>));
         if (warp < S) {
             float h[V], zz[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = zz[v] = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const Map<V> m = get_map<V>(f.warp[buf][w], lane);
                 apply<V>(m, h);
 #pragma unroll
                 for (int v = 0; v < V; ++v) zz[v] += m.z[v];
             }
-            cg::cluster_group cl = cg::this_cluster();
-            put_map<V>(*cl.map_shared_rank(&f.cta[buf][rank], warp), lane, map_of<V>(zz, h));
+            const Map<V> m = map_of<V>(zz, h);
+            for (int j = warp; j < S; j += NW) {
+                const uint32_t to = at_rank(&f.cta[buf][rank][0][lane], j), bar = at_rank(&f.full[buf], j);
+                if constexpr (V == 1) {
+                    send(to, make_float4(m.a[0], m.e[0], m.s[0], m.z[0]), bar);
+                } else {
+                    send(to, make_float4(m.a[0], m.a[1], m.e[0], m.e[1]), bar);
+                    send(to + 512, make_float4(m.s[0], m.s[1], m.z[0], m.z[1]), bar);
+                }
+            }
         }
-        cluster_arrive();
-        cluster_wait();
+        full_wait(&f.full[buf], (r >> 1) & 1, limit_ns, late);
 #pragma unroll
         for (int v = 0; v < V; ++v) start[v] = carry[v];
         for (int j = 0; j < S; ++j) {
@@ -190,7 +258,7 @@ __device__ __forceinline__ void fold_round(Fold<V>& f, int buf, int S, int rank,
         for (int w = 0; w < warp; ++w) apply<V>(get_map<V>(f.warp[buf][w], lane), start);
     } else {
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = 0; w < NW; ++w) {
             if (w == warp)
 #pragma unroll
                 for (int v = 0; v < V; ++v) start[v] = carry[v];
@@ -199,27 +267,9 @@ __device__ __forceinline__ void fold_round(Fold<V>& f, int buf, int S, int rank,
     }
 }
 
-// Pairs of gates: two channels of a token, or (V = 1) two tokens of a channel.
-template <int V, int K>
-struct Gates {
-    float a[K][V];
-    uint32_t e[K * V / 2];   // bf16 pairs: e is under 2^-25, three digits of it are plenty
-    __device__ __forceinline__ F2 err(int i) const {
-        return F2{__uint_as_float(e[i] << 16), __uint_as_float(e[i] & 0xffff0000u)};
-    }
-    __device__ __forceinline__ float err1(int k, int v) const {
-        const F2 f = err((k * V + v) / 2);
-        return (k * V + v) & 1 ? f.y : f.x;
-    }
-    __device__ __forceinline__ void put(int i, F2 x) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
-        e[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-};
-
-template <typename TI, typename TO, int V, int K, bool LEAK>
-__global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const GatedArgs p, const Cut cut) {
-    __shared__ Fold<V> fold;
+template <typename TI, typename TO, int V, int K, int NW, bool LEAK>
+__global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_kernel(const GatedArgs p, const Cut cut) {
+    __shared__ Fold<V, NW> fold;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = cut.S, rank = blockIdx.x % S;
     const long long unit = blockIdx.x / S;
@@ -227,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const GatedArgs p
     const int c = (static_cast<int>(unit - sr * cut.slabs) * 32 + lane) * V;
     const bool on = c < p.C;
     const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * WARPS * K - 1) / (S * WARPS * K);
+    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
     const long long arow = (sr % p.H) * p.C;
 
     float nA[V], carry[V];
@@ -242,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const GatedArgs p
 
     Vec<TI, V> xr[K], dr[K];
     auto fetch = [&](int r) {
-        const int t = sp.lo + ((r * S + rank) * WARPS + warp) * K;
+        const int t = sp.lo + ((r * S + rank) * NW + warp) * K;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             xr[k] = Vec<TI, V>{};
@@ -254,36 +304,32 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const GatedArgs p
         }
     };
     if (rounds > 0) fetch(0);
-    if (S > 1) {   // every CTA of the cluster runs before its shared memory is written
-        cluster_arrive();
-        cluster_wait();
-    }
+    fold.begin(S);
+    bool late = false;
     for (int r = 0; r < rounds; ++r) {
-        const int t = sp.lo + ((r * S + rank) * WARPS + warp) * K;
+        const int t = sp.lo + ((r * S + rank) * NW + warp) * K;
         // tokens behind the end have d = x = 0: alpha = 1, nothing added
-        Gates<V, K> g;
-        float b[K][V], z[V], s[V];
+        float a[K][V], b[K][V], z[V], s[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
 #pragma unroll
         for (int i = 0; i < K * V / 2; ++i) {
             const int k0 = 2 * i / V, v0 = 2 * i % V, k1 = (2 * i + 1) / V, v1 = (2 * i + 1) % V;
             const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{dr[k0].get(v0), dr[k1].get(v1)});
-            const Gate2 gg = gate2(zz);
-            g.a[k0][v0] = gg.a.x;
-            g.a[k1][v1] = gg.a.y;
-            g.put(i, gg.e);
+            const Gate2 gg = gate2<LEAK>(zz);
+            a[k0][v0] = gg.a.x;
+            a[k1][v1] = gg.a.y;
             F2 x{xr[k0].get(v0), xr[k1].get(v1)};
             if (LEAK) x = mul2(x, gg.w);
             b[k0][v0] = x.x;
             b[k1][v1] = x.y;
             if (V == 1) {
                 z[0] += zz.x + zz.y;
-                s[0] = decay_add(gg.a.x, gg.e.x, s[0], x.x);
-                s[0] = decay_add(gg.a.y, gg.e.y, s[0], x.y);
+                s[0] = fmaf(gg.a.x, s[0], x.x);
+                s[0] = fmaf(gg.a.y, s[0], x.y);
             } else {
                 const F2 ss{s[v0], s[v1]};
-                const F2 n = fma2(gg.a, ss, fma2(gg.e, ss, x)), zs = add2(F2{z[v0], z[v1]}, zz);
+                const F2 n = fma2(gg.a, ss, x), zs = add2(F2{z[v0], z[v1]}, zz);
                 s[v0] = n.x;
                 s[v1] = n.y;
                 z[v0] = zs.x;
@@ -292,17 +338,16 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const GatedArgs p
         }
         if (r + 1 < rounds) fetch(r + 1);
         float h[V];
-        fold_round<V>(fold, r & 1, S, rank, warp, lane, z, s, carry, h);
+        fold_round<V, NW>(fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, h);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (V == 1) {
-                h[0] = decay_add(g.a[k][0], g.err1(k, 0), h[0], b[k][0]);
+                h[0] = fmaf(a[k][0], h[0], b[k][0]);
             } else {
 #pragma unroll
                 for (int v = 0; v < V; v += 2) {
                     const F2 hh{h[v], h[v + 1]};
-                    const F2 n = fma2(F2{g.a[k][v], g.a[k][v + 1]}, hh,
-                                      fma2(g.err((k * V + v) / 2), hh, F2{b[k][v], b[k][v + 1]}));
+                    const F2 n = fma2(F2{a[k][v], a[k][v + 1]}, hh, F2{b[k][v], b[k][v + 1]});
                     h[v] = n.x;
                     h[v + 1] = n.y;
                 }
@@ -314,6 +359,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const GatedArgs p
             }
         }
     }
+    fold.end(S, late);
     if (p.final_state && rank == 0 && warp == 0 && on)
 #pragma unroll
         for (int v = 0; v < V; ++v) p.final_state[sr * p.C + c + v] = carry[v];
@@ -321,10 +367,10 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const GatedArgs p
 
 // The same walk from the last token to the first.  `part` [state row, rank, C]
 // takes each CTA's share of grad A.
-template <typename TI, typename TO, int V, int K, bool LEAK>
-__global__ void __launch_bounds__(THREADS, 2)
+template <typename TI, typename TO, int V, int K, int NW, bool LEAK>
+__global__ void __launch_bounds__(NW * 32, 16 / NW)
 gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
-    __shared__ Fold<V> fold;
+    __shared__ Fold<V, NW> fold;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = cut.S, rank = blockIdx.x % S;
     const long long unit = blockIdx.x / S;
@@ -332,7 +378,7 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
     const int c = (static_cast<int>(unit - sr * cut.slabs) * 32 + lane) * V;
     const bool on = c < p.C;
     const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * WARPS * K - 1) / (S * WARPS * K);
+    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
     const long long arow = (sr % p.H) * p.C;
 
     float nA[V], carry[V], dA[V], first[V];
@@ -354,7 +400,7 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
     Vec<TI, V> dn[K];
     Vec<TO, V> gn[K];
     auto fetch = [&](int r) {
-        const int t = sp.hi - 1 - ((r * S + rank) * WARPS + warp) * K;
+        const int t = sp.hi - 1 - ((r * S + rank) * NW + warp) * K;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             dn[k] = Vec<TI, V>{};
@@ -366,12 +412,10 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
         }
     };
     if (rounds > 0) fetch(0);
-    if (S > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
+    fold.begin(S);
+    bool late = false;
     for (int r = 0; r < rounds; ++r) {
-        const int t = sp.hi - 1 - ((r * S + rank) * WARPS + warp) * K;
+        const int t = sp.hi - 1 - ((r * S + rank) * NW + warp) * K;
         Vec<TO, V> hr[K];
         Vec<TI, V> xr[K], dr[K];
         Vec<TO, V> gr[K];
@@ -384,8 +428,7 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
             dr[k] = dn[k];
             gr[k] = gn[k];
         }
-        Gates<V, K> g;
-        float z[V], s[V], w[LEAK ? K : 1][V];
+        float a[K][V], z[V], s[V], w[LEAK ? K : 1][V];
 #pragma unroll
         for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
         // u = alpha (g + u): the map of a token is (alpha, alpha g)
@@ -393,24 +436,22 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
         for (int i = 0; i < K * V / 2; ++i) {
             const int k0 = 2 * i / V, v0 = 2 * i % V, k1 = (2 * i + 1) / V, v1 = (2 * i + 1) % V;
             const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{dr[k0].get(v0), dr[k1].get(v1)});
-            const Gate2 gg = gate2(zz);
-            g.a[k0][v0] = gg.a.x;
-            g.a[k1][v1] = gg.a.y;
-            if (LEAK) {   // e follows from w
+            const Gate2 gg = gate2<LEAK>(zz);
+            a[k0][v0] = gg.a.x;
+            a[k1][v1] = gg.a.y;
+            if (LEAK) {
                 w[LEAK ? k0 : 0][v0] = gg.w.x;
                 w[LEAK ? k1 : 0][v1] = gg.w.y;
-            } else {
-                g.put(i, gg.e);
             }
             if (V == 1) {
                 z[0] += zz.x + zz.y;
                 const float d0 = s[0] + gr[k0].get(0);
-                s[0] = decay_add(gg.a.x, gg.e.x, d0, 0.f);
+                s[0] = gg.a.x * d0;
                 const float d1 = s[0] + gr[k1].get(0);
-                s[0] = decay_add(gg.a.y, gg.e.y, d1, 0.f);
+                s[0] = gg.a.y * d1;
             } else {
                 const F2 dh = add2(F2{s[v0], s[v1]}, F2{gr[k0].get(v0), gr[k0].get(v1)});
-                const F2 n = fma2(gg.a, dh, mul2(gg.e, dh)), zs = add2(F2{z[v0], z[v1]}, zz);
+                const F2 n = mul2(gg.a, dh), zs = add2(F2{z[v0], z[v1]}, zz);
                 s[v0] = n.x;
                 s[v1] = n.y;
                 z[v0] = zs.x;
@@ -419,15 +460,14 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
         }
         if (r + 1 < rounds) fetch(r + 1);
         float u[V];
-        fold_round<V>(fold, r & 1, S, rank, warp, lane, z, s, carry, u);
+        fold_round<V, NW>(fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, u);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float gx[V], gd[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float a = g.a[k][v], e = LEAK ? -w[LEAK ? k : 0][v] - (a - 1.f) : g.err1(k, v);
                 const float dh = u[v] + gr[k].get(v);
-                u[v] = fmaf(a, dh, e * dh);
+                u[v] = a[k][v] * dh;
                 float prev = t - k > sp.lo ? hr[k].get(v) : first[v];
                 gx[v] = dh;
                 if (LEAK) {
@@ -447,6 +487,7 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
             }
         }
     }
+    fold.end(S, late);
     if (p.grad_h0 && rank == 0 && warp == 0 && on)
 #pragma unroll
         for (int v = 0; v < V; ++v) p.grad_h0[sr * p.C + c + v] = carry[v];
@@ -460,7 +501,7 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float sum = 0.f;
-                for (int w = 0; w < WARPS; ++w) sum += fold.warp[0][w][v][lane].x;
+                for (int w = 0; w < NW; ++w) sum += fold.warp[0][w][v][lane].x;
                 part[(sr * S + rank) * p.C + c + v] = sum;
             }
     }
@@ -474,19 +515,19 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
 // it copied itself, so no barrier beyond the fold's is needed.
 constexpr int STAGES = 2;
 
-template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
+template <typename TI, typename TO, int V, int K, int NW>
 struct FwdShared {
     static constexpr int ROW = 32 * V * static_cast<int>(sizeof(TI)), OROW = 32 * V * static_cast<int>(sizeof(TO));
     struct __align__(16) Stage {
         char x[K * ROW], d[K * ROW];                 // out overwrites both
     };
-    Stage st[STAGES][WARPS];
-    Fold<V> fold;
+    Stage st[STAGES][NW];
+    Fold<V, NW> fold;
 };
 
-template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
-__global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p, const Cut cut) {
-    using Sh = FwdShared<TI, TO, V, K, LEAK, SIZE>;
+template <typename TI, typename TO, int V, int K, int NW, bool LEAK, int SIZE>
+__global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_staged(const GatedArgs p, const Cut cut) {
+    using Sh = FwdShared<TI, TO, V, K, NW>;
     static_assert(Sh::OROW * K <= static_cast<int>(sizeof(typename Sh::Stage)), "out takes the stage's place");
     extern __shared__ __align__(16) char smem[];
     Sh& sh = *reinterpret_cast<Sh*>(smem);
@@ -496,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p
     const long long sr = unit / cut.slabs;
     const int c0 = static_cast<int>(unit - sr * cut.slabs) * 32 * V, c = c0 + lane * V;
     const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * WARPS * K - 1) / (S * WARPS * K);
+    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
     const long long arow = (sr % p.H) * p.C;
 
     float nA[V], carry[V];
@@ -505,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p
         nA[v] = c + v < p.C ? -p.A[arow + c + v] : 0.f;
         carry[v] = c + v < p.C && p.h0 ? p.h0[sr * p.C + c + v] : 0.f;
     }
-    const int t0 = sp.lo + (rank * WARPS + warp) * K, step = S * WARPS * K;
+    const int t0 = sp.lo + (rank * NW + warp) * K, step = S * NW * K;
     const long long xld = p.x_ld * sizeof(TI), dld = p.d_ld * sizeof(TI);
     const char* xp = static_cast<const char*>(p.x) + (sp.row * p.T + t0) * xld + c0 * sizeof(TI);
     const char* dp = static_cast<const char*>(p.d) + (sp.row * p.T + t0) * dld + c0 * sizeof(TI);
@@ -516,9 +557,9 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p
         const int n = sp.hi - t0 - r * step;               // tokens left
         if (n > 0) {
             typename Sh::Stage& st = sh.st[r % STAGES][warp];
-            const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(st.x));
-            rows_in<SIZE, Sh::ROW, K>(a, p.x, xp + static_cast<long long>(r) * step * xld, xld, 0, n, width, lane);
-            rows_in<SIZE, Sh::ROW, K>(a + K * Sh::ROW, p.d, dp + static_cast<long long>(r) * step * dld, dld, 0, n, width, lane);
+            const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(st.x));
+            rows_in<SIZE, Sh::ROW, K>(sm, p.x, xp + static_cast<long long>(r) * step * xld, xld, 0, n, width, lane);
+            rows_in<SIZE, Sh::ROW, K>(sm + K * Sh::ROW, p.d, dp + static_cast<long long>(r) * step * dld, dld, 0, n, width, lane);
         }
         copy_commit();
     };
@@ -526,18 +567,15 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p
     for (int i = 0; i < STAGES; ++i)
         if (i < rounds) fetch(i);
         else copy_commit();
-    if (S > 1) {   // every CTA of the cluster runs before its shared memory is written
-        cluster_arrive();
-        cluster_wait();
-    }
+    sh.fold.begin(S);
+    bool late = false;
     for (int r = 0; r < rounds; ++r) {
         const int n = sp.hi - t0 - r * step;
         char* xs = sh.st[r % STAGES][warp].x;
         const char* ds = sh.st[r % STAGES][warp].d;
         copy_wait<STAGES - 1>();
         __syncwarp();
-        Gates<V, K> g;
-        float b[K][V], z[V], s[V], h[V];
+        float a[K][V], b[K][V], z[V], s[V], h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
         if (n > 0) {                                        // (the warp as one)
@@ -552,21 +590,20 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p
                     x1 = peek<TI, V>(xs + k1 * Sh::ROW + lane * V * sizeof(TI));
                 }
                 const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{d0.get(v0), d1.get(v1)});
-                const Gate2 gg = gate2(zz);
-                g.a[k0][v0] = gg.a.x;
-                g.a[k1][v1] = gg.a.y;
-                g.put(i, gg.e);
+                const Gate2 gg = gate2<LEAK>(zz);
+                a[k0][v0] = gg.a.x;
+                a[k1][v1] = gg.a.y;
                 F2 x{x0.get(v0), x1.get(v1)};
                 if (LEAK) x = mul2(x, gg.w);
                 b[k0][v0] = x.x;
                 b[k1][v1] = x.y;
                 if constexpr (V == 1) {
                     z[0] += zz.x + zz.y;
-                    s[0] = decay_add(gg.a.x, gg.e.x, s[0], x.x);
-                    s[0] = decay_add(gg.a.y, gg.e.y, s[0], x.y);
+                    s[0] = fmaf(gg.a.x, s[0], x.x);
+                    s[0] = fmaf(gg.a.y, s[0], x.y);
                 } else {
                     const F2 ss{s[0], s[1]};
-                    const F2 m = fma2(gg.a, ss, fma2(gg.e, ss, x)), zs = add2(F2{z[0], z[1]}, zz);
+                    const F2 m = fma2(gg.a, ss, x), zs = add2(F2{z[0], z[1]}, zz);
                     s[0] = m.x;
                     s[1] = m.y;
                     z[0] = zs.x;
@@ -574,16 +611,16 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p
                 }
             }
         }
-        fold_round<V>(sh.fold, r & 1, S, rank, warp, lane, z, s, carry, h);
+        fold_round<V, NW>(sh.fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, h);
         if (n > 0) {
             TO* o = op + static_cast<long long>(r) * step * p.C;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if constexpr (V == 1) {
-                    h[0] = decay_add(g.a[k][0], g.err1(k, 0), h[0], b[k][0]);
+                    h[0] = fmaf(a[k][0], h[0], b[k][0]);
                 } else {
                     const F2 hh{h[0], h[1]};
-                    const F2 m = fma2(F2{g.a[k][0], g.a[k][1]}, hh, fma2(g.err(k), hh, F2{b[k][0], b[k][1]}));
+                    const F2 m = fma2(F2{a[k][0], a[k][1]}, hh, F2{b[k][0], b[k][1]});
                     h[0] = m.x;
                     h[1] = m.y;
                 }
@@ -607,26 +644,27 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_staged(const GatedArgs p
         if (r + STAGES < rounds) fetch(r + STAGES);
         else copy_commit();
     }
+    sh.fold.end(S, late);
     if (p.final_state && rank == 0 && warp == 0)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (c + v < p.C) p.final_state[sr * p.C + c + v] = carry[v];
 }
 
-template <typename TI, typename TO, int V, int K>
+template <typename TI, typename TO, int V, int K, int NW>
 struct BwdShared {
     static constexpr int ROW = 32 * V * static_cast<int>(sizeof(TI)), OROW = 32 * V * static_cast<int>(sizeof(TO));
     struct __align__(16) Stage {
         char d[K * ROW], x[K * ROW], g[K * OROW], h[K * OROW];   // grad d overwrites d, grad x x
     };
-    Stage st[STAGES][WARPS];
-    Fold<V> fold;
+    Stage st[STAGES][NW];
+    Fold<V, NW> fold;
 };
 
-template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
-__global__ void __launch_bounds__(THREADS, 2)
+template <typename TI, typename TO, int V, int K, int NW, bool LEAK, int SIZE>
+__global__ void __launch_bounds__(NW * 32, 16 / NW)
 gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
-    using Sh = BwdShared<TI, TO, V, K>;
+    using Sh = BwdShared<TI, TO, V, K, NW>;
     extern __shared__ __align__(16) char smem[];
     Sh& sh = *reinterpret_cast<Sh*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -635,7 +673,7 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
     const long long sr = unit / cut.slabs;
     const int c0 = static_cast<int>(unit - sr * cut.slabs) * 32 * V, c = c0 + lane * V;
     const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * WARPS * K - 1) / (S * WARPS * K);
+    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
     const long long arow = (sr % p.H) * p.C;
 
     float nA[V], carry[V], dA[V], first[V];
@@ -648,7 +686,7 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
         dA[v] = 0.f;
     }
     // a warp's rows of round r are tokens base - r step .. + K - 1, walked from the last
-    const int base = sp.hi - (rank * WARPS + warp + 1) * K, step = S * WARPS * K;
+    const int base = sp.hi - (rank * NW + warp + 1) * K, step = S * NW * K;
     const long long dld = p.d_ld * sizeof(TI), xld = p.x_ld * sizeof(TI), old_ = p.C * static_cast<long long>(sizeof(TO));
     const long long row = sp.row * p.T;
     const int width = (p.C - c0) * static_cast<int>(sizeof(TI)), owidth = (p.C - c0) * static_cast<int>(sizeof(TO));
@@ -658,17 +696,17 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
         if (t + K > sp.lo) {
             typename Sh::Stage& st = sh.st[r % STAGES][warp];
             const int f = max(sp.lo - t, 0);               // rows before the sequence
-            const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(st.d));
+            const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(st.d));
             constexpr int N = K * Sh::ROW, M = K * Sh::OROW;
-            rows_in<SIZE, Sh::ROW, K>(a, p.d, static_cast<const char*>(p.d) + (row + t) * dld + c0 * sizeof(TI), dld, f, K,
+            rows_in<SIZE, Sh::ROW, K>(sm, p.d, static_cast<const char*>(p.d) + (row + t) * dld + c0 * sizeof(TI), dld, f, K,
                                       width, lane);
             if (LEAK)
-                rows_in<SIZE, Sh::ROW, K>(a + N, p.x, static_cast<const char*>(p.x) + (row + t) * xld + c0 * sizeof(TI), xld,
+                rows_in<SIZE, Sh::ROW, K>(sm + N, p.x, static_cast<const char*>(p.x) + (row + t) * xld + c0 * sizeof(TI), xld,
                                           f, K, width, lane);
-            rows_in<SIZE, Sh::OROW, K>(a + 2 * N, p.grad_out, static_cast<const char*>(p.grad_out) + (row + t) * old_ + c0 * sizeof(TO),
+            rows_in<SIZE, Sh::OROW, K>(sm + 2 * N, p.grad_out, static_cast<const char*>(p.grad_out) + (row + t) * old_ + c0 * sizeof(TO),
                                        old_, f, K, owidth, lane);
             // the states before: one token earlier (h0 for the first one, below)
-            rows_in<SIZE, Sh::OROW, K>(a + 2 * N + M, p.out, static_cast<const char*>(p.out) + (row + t - 1) * old_ + c0 * sizeof(TO),
+            rows_in<SIZE, Sh::OROW, K>(sm + 2 * N + M, p.out, static_cast<const char*>(p.out) + (row + t - 1) * old_ + c0 * sizeof(TO),
                                        old_, f + (t + f == sp.lo), K, owidth, lane);
         }
         copy_commit();
@@ -677,18 +715,15 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
     for (int i = 0; i < STAGES; ++i)
         if (i < rounds) fetch(i);
         else copy_commit();
-    if (S > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
+    sh.fold.begin(S);
+    bool late = false;
     for (int r = 0; r < rounds; ++r) {
         const int t = base - r * step;
         const bool any = t + K > sp.lo;
         typename Sh::Stage& st = sh.st[r % STAGES][warp];
         copy_wait<STAGES - 1>();
         __syncwarp();
-        Gates<V, K> g;
-        float w[LEAK ? K : 1][V], z[V], s[V], u[V];
+        float a[K][V], w[LEAK ? K : 1][V], z[V], s[V], u[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
         if (any) {
@@ -706,24 +741,22 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                     g1 = peek<TO, V>(st.g + j1 * Sh::OROW + lane * V * sizeof(TO));
                 }
                 const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{d0.get(v0), d1.get(v1)});
-                const Gate2 gg = gate2(zz);
-                g.a[k0][v0] = gg.a.x;
-                g.a[k1][v1] = gg.a.y;
-                if (LEAK) {                                 // e follows from w
+                const Gate2 gg = gate2<LEAK>(zz);
+                a[k0][v0] = gg.a.x;
+                a[k1][v1] = gg.a.y;
+                if (LEAK) {
                     w[LEAK ? k0 : 0][v0] = gg.w.x;
                     w[LEAK ? k1 : 0][v1] = gg.w.y;
-                } else {
-                    g.put(i, gg.e);
                 }
                 if constexpr (V == 1) {
                     z[0] += zz.x + zz.y;
                     const float h0 = s[0] + g0.get(0);
-                    s[0] = decay_add(gg.a.x, gg.e.x, h0, 0.f);
+                    s[0] = gg.a.x * h0;
                     const float h1 = s[0] + g1.get(0);
-                    s[0] = decay_add(gg.a.y, gg.e.y, h1, 0.f);
+                    s[0] = gg.a.y * h1;
                 } else {
                     const F2 dh = add2(F2{s[0], s[1]}, F2{g0.get(0), g0.get(1)});
-                    const F2 m = fma2(gg.a, dh, mul2(gg.e, dh)), zs = add2(F2{z[0], z[1]}, zz);
+                    const F2 m = mul2(gg.a, dh), zs = add2(F2{z[0], z[1]}, zz);
                     s[0] = m.x;
                     s[1] = m.y;
                     z[0] = zs.x;
@@ -731,7 +764,7 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                 }
             }
         }
-        fold_round<V>(sh.fold, r & 1, S, rank, warp, lane, z, s, carry, u);
+        fold_round<V, NW>(sh.fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, u);
         if (any) {
             TI* gx_out = static_cast<TI*>(p.grad_x) + (row + t) * p.C + c0;
             TI* gd_out = static_cast<TI*>(p.grad_d) + (row + t) * p.C + c0;
@@ -746,10 +779,8 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                 float gx[V], gd[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float a = g.a[k][v];
-                    const float e = LEAK ? -w[LEAK ? k : 0][v] - (a - 1.f) : g.err1(k, v);
                     const float dh = u[v] + gv.get(v);
-                    u[v] = fmaf(a, dh, e * dh);
+                    u[v] = a[k][v] * dh;
                     float prev = t + j == sp.lo ? first[v] : hv.get(v);
                     gx[v] = dh;
                     if (LEAK) {
@@ -787,6 +818,7 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
         if (r + STAGES < rounds) fetch(r + STAGES);
         else copy_commit();
     }
+    sh.fold.end(S, late);
     if (p.grad_h0 && rank == 0 && warp == 0)
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -801,7 +833,7 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float sum = 0.f;
-                for (int i = 0; i < WARPS; ++i) sum += sh.fold.warp[0][i][v][lane].x;
+                for (int i = 0; i < NW; ++i) sum += sh.fold.warp[0][i][v][lane].x;
                 if (c + v < p.C) part[(sr * S + rank) * p.C + c + v] = sum;
             }
     }
@@ -864,7 +896,7 @@ bool rows_ok(const GatedArgs& a, long long bytes) {
 
 // One launch of a walk kernel over all (state row, slab) units.
 template <typename... KArgs, typename... Args>
-kdn_status launch_walk(void (*kernel)(KArgs...), long long rows, const Cut& cut, size_t smem, cudaStream_t stream,
+kdn_status launch_walk(void (*kernel)(KArgs...), int threads, long long rows, const Cut& cut, size_t smem, cudaStream_t stream,
                        Args... args) {
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -875,7 +907,7 @@ kdn_status launch_walk(void (*kernel)(KArgs...), long long rows, const Cut& cut,
     if (blocks > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at{};
@@ -894,32 +926,32 @@ long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq) {
     return rows * cluster_size(rows, C, T) * C * 4;
 }
 
-kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream) {
+kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
     const long long rows = state_rows(a);
-    Cut cut{0, cluster_size(rows, a.C, a.T)};
+    Cut cut{0, cluster_size(rows, a.C, a.T), wait_ns};
     return by_type(a, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
-        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 16;
+        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 16, NW = FWD_WARPS;
         auto go = [&](auto kernel, int v, size_t smem) {
             cut.slabs = (a.C + 32 * v - 1) / (32 * v);
-            return launch_walk(kernel, rows, cut, smem, stream, a, cut);
+            return launch_walk(kernel, NW * 32, rows, cut, smem, stream, a, cut);
         };
         auto leak = [&](auto l) {
             constexpr bool L = decltype(l)::value;
             if (rows_ok(a, 16))
-                return go(gated_fwd_staged<TI, TO, V, K, L, 16>, V, sizeof(FwdShared<TI, TO, V, K, L, 16>));
+                return go(gated_fwd_staged<TI, TO, V, K, NW, L, 16>, V, sizeof(FwdShared<TI, TO, V, K, NW>));
             if (rows_ok(a, 4))
-                return go(gated_fwd_staged<TI, TO, V, K, L, 4>, V, sizeof(FwdShared<TI, TO, V, K, L, 4>));
-            return go(gated_fwd_kernel<TI, TO, 1, K, L>, 1, 0);
+                return go(gated_fwd_staged<TI, TO, V, K, NW, L, 4>, V, sizeof(FwdShared<TI, TO, V, K, NW>));
+            return go(gated_fwd_kernel<TI, TO, 1, K, NW, L>, 1, 0);
         };
         return a.leak ? leak(std::true_type()) : leak(std::false_type());
     });
 }
 
-kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream) {
+kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
     const long long rows = state_rows(a);
-    Cut cut{0, cluster_size(rows, a.C, a.T)};
+    Cut cut{0, cluster_size(rows, a.C, a.T), wait_ns};
     float* part = a.grad_A ? static_cast<float*>(a.workspace) : nullptr;
     const bool own = a.grad_A && !part;
     if (own) {
@@ -929,16 +961,16 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream) {
     kdn_status s = by_type(a, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
-        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 8;
+        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 8, NW = BWD_WARPS;
         auto go = [&](auto kernel, int v, size_t smem) {
             cut.slabs = (a.C + 32 * v - 1) / (32 * v);
-            return launch_walk(kernel, rows, cut, smem, stream, a, cut, part);
+            return launch_walk(kernel, NW * 32, rows, cut, smem, stream, a, cut, part);
         };
         auto leak = [&](auto l) {
             constexpr bool L = decltype(l)::value;
-            if (rows_ok(a, 16)) return go(gated_bwd_staged<TI, TO, V, K, L, 16>, V, sizeof(BwdShared<TI, TO, V, K>));
-            if (rows_ok(a, 4)) return go(gated_bwd_staged<TI, TO, V, K, L, 4>, V, sizeof(BwdShared<TI, TO, V, K>));
-            return go(gated_bwd_kernel<TI, TO, 1, K, L>, 1, 0);
+            if (rows_ok(a, 16)) return go(gated_bwd_staged<TI, TO, V, K, NW, L, 16>, V, sizeof(BwdShared<TI, TO, V, K, NW>));
+            if (rows_ok(a, 4)) return go(gated_bwd_staged<TI, TO, V, K, NW, L, 4>, V, sizeof(BwdShared<TI, TO, V, K, NW>));
+            return go(gated_bwd_kernel<TI, TO, 1, K, NW, L>, 1, 0);
         };
         return a.leak ? leak(std::true_type()) : leak(std::false_type());
     });
@@ -952,6 +984,14 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream) {
         if (s == KDN_OK) s = f;
     }
     return s;
+}
+
+cudaError_t gated_take_device_error(int* status) {
+    int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_gated_error, sizeof(int));
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_gated_error, &zero, sizeof(int));
+    *status = v;
+    return e;
 }
 
 kdn_status gated_step_launch(const void* x, const void* d, const float* A, bool leak, const float* state,

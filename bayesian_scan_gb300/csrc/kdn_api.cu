@@ -356,7 +356,7 @@ kdn_status kdn_gated_scan_fwd(const void* x, long long x_ld, const void* d, long
     a.out = out; a.final_state = final_state;
     const kdn_status s = gated_check(a);
     if (s != KDN_OK) return s;
-    return gated_fwd_launch(a, static_cast<cudaStream_t>(stream));
+    return gated_fwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load());
 }
 
 kdn_status kdn_gated_scan_bwd(const void* x, long long x_ld, const void* d, long long d_ld,
@@ -377,7 +377,7 @@ kdn_status kdn_gated_scan_bwd(const void* x, long long x_ld, const void* d, long
     if (workspace && (!aligned(workspace, 256) ||
                       workspace_bytes < gated_bwd_workspace_bytes(B, H, T, C, nseq)))
         return KDN_ERR_INVALID_ARG;
-    return gated_bwd_launch(a, static_cast<cudaStream_t>(stream));
+    return gated_bwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load());
 }
 
 kdn_status kdn_gated_scan_bwd_workspace(int B, int H, int T, int C, int nseq, long long* workspace_bytes) {
@@ -471,11 +471,13 @@ const char* kdn_status_string(kdn_status s) {
 kdn_status kdn_get_device_error(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return from_cuda(e);
-    int s1 = 0, s2 = 0, s3 = 0;
+    int s1 = 0, s2 = 0, s3 = 0, s4 = 0;
     if ((e = diag_take_device_error_bf16(&s1)) != cudaSuccess) return from_cuda(e);
     if ((e = diag_take_device_error_f32(&s2)) != cudaSuccess) return from_cuda(e);
     if ((e = mobius_take_device_error(&s3)) != cudaSuccess) return from_cuda(e);
+    if ((e = gated_take_device_error(&s4)) != cudaSuccess) return from_cuda(e);
     if (s1) return static_cast<kdn_status>(s1);
+    if (s4) return static_cast<kdn_status>(s4);
     if (s2) return static_cast<kdn_status>(s2);
     return static_cast<kdn_status>(s3);
 }

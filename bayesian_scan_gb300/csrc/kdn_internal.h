@@ -117,8 +117,8 @@ struct GatedArgs {
     float* grad_h0;
     void* workspace;
 };
-kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream);
-kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream);
+kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns);
+kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns);
 long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq);
 kdn_status gated_step_launch(const void* x, const void* d, const float* A, bool leak,
                              const float* state, float* new_state, void* out, int B, int H, int C,
@@ -163,6 +163,7 @@ kdn_status mobius_host(const float* a, const float* b, const float* c, const flo
 // device error word; these read-and-clear it on the current device.
 cudaError_t diag_take_device_error(int* status);
 cudaError_t mobius_take_device_error(int* status);
+cudaError_t gated_take_device_error(int* status);
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
