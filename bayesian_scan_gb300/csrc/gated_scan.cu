@@ -874,13 +874,22 @@ kdn_status by_type(const GatedArgs& a, F f) {
 
 long long state_rows(const GatedArgs& a) { return static_cast<long long>(a.nseq > 0 ? a.nseq : a.B) * a.H; }
 
-// CTAs per cluster: enough to fill the GPU's two CTAs per SM, no more than
-// the sequence has tiles.
-int cluster_size(long long rows, int C, int T) {
-    const long long slabs = (C + 63) / 64, want = 2LL * sm_count();
-    int S = 1;
-    while (S < MAX_CLUSTER && rows * slabs * S < want && S * 128 < T) S *= 2;
-    return S;
+// CTAs per cluster: as many as keep the grid within the GPU's two CTAs per
+// SM, no more than a sequence has tiles.  The exchange of a round costs a
+// cluster more than half of the round itself (2.5 us alone on two CTAs per
+// SM, 3.3 us with four, 4.0 us with eight), so a grid that fills the SMs
+// without clusters stays without (8 x 4096 x 2048: 80 us, 91 with two), and
+// one that does not gains from every CTA (65536 x 2048: 257 us with eight).
+// Packed sequences have one length on average and may have others, so a long
+// average gets a cluster whatever the grid.
+int cluster_size(const GatedArgs& a, int V) {
+    constexpr int TILE = FWD_WARPS * 16;
+    const long long units = state_rows(a) * ((a.C + 32 * V - 1) / (32 * V));
+    const long long len = a.nseq > 0 ? (a.T + a.nseq - 1) / a.nseq : a.T, tiles = (len + TILE - 1) / TILE;
+    long long S = 2LL * sm_count() / units;
+    if (a.nseq > 0 && S < tiles / 4) S = tiles / 4;
+    if (S > tiles) S = tiles;
+    return static_cast<int>(S < 1 ? 1 : S > MAX_CLUSTER ? MAX_CLUSTER : S);
 }
 
 // Whether every row of every tensor starts on a multiple of `bytes` and is a
@@ -922,19 +931,25 @@ kdn_status launch_walk(void (*kernel)(KArgs...), int threads, long long rows, co
 }  // namespace
 
 long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq) {
-    const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
-    return rows * cluster_size(rows, C, T) * C * 4;
+    GatedArgs a{};
+    a.B = B;
+    a.H = H;
+    a.T = T;
+    a.C = C;
+    a.nseq = nseq;
+    return state_rows(a) * cluster_size(a, 2) * C * 4;   // (V = 1 makes clusters no larger)
 }
 
 kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
     const long long rows = state_rows(a);
-    Cut cut{0, cluster_size(rows, a.C, a.T), wait_ns};
+    Cut cut{0, 1, wait_ns};
     return by_type(a, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
         constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 16, NW = FWD_WARPS;
         auto go = [&](auto kernel, int v, size_t smem) {
             cut.slabs = (a.C + 32 * v - 1) / (32 * v);
+            cut.S = cluster_size(a, v);
             return launch_walk(kernel, NW * 32, rows, cut, smem, stream, a, cut);
         };
         auto leak = [&](auto l) {
@@ -951,11 +966,11 @@ kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
 
 kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
     const long long rows = state_rows(a);
-    Cut cut{0, cluster_size(rows, a.C, a.T), wait_ns};
+    Cut cut{0, 1, wait_ns};
     float* part = a.grad_A ? static_cast<float*>(a.workspace) : nullptr;
     const bool own = a.grad_A && !part;
     if (own) {
-        const kdn_status s = from_cuda(cudaMallocAsync(&part, rows * cut.S * a.C * 4, stream));
+        const kdn_status s = from_cuda(cudaMallocAsync(&part, rows * cluster_size(a, 2) * a.C * 4, stream));
         if (s != KDN_OK) return s;
     }
     kdn_status s = by_type(a, [&](auto ti, auto to) {
@@ -964,6 +979,7 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
         constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 8, NW = BWD_WARPS;
         auto go = [&](auto kernel, int v, size_t smem) {
             cut.slabs = (a.C + 32 * v - 1) / (32 * v);
+            cut.S = cluster_size(a, v);
             return launch_walk(kernel, NW * 32, rows, cut, smem, stream, a, cut, part);
         };
         auto leak = [&](auto l) {

@@ -123,12 +123,15 @@ def version() -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle of torch's current stream: a stream object costs as much
+    # host time as the rest of a small call
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(t, name, dtype=None, shape=None):
@@ -136,7 +139,7 @@ def _check(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -144,6 +147,9 @@ def _on_one_device(stream, **tensors):
     """Every given tensor must be a CUDA tensor on the current device (the
     device whose stream the call is issued on): the C ABI receives raw
     pointers and cannot tell host memory or another GPU's memory apart."""
+    seen = {t.get_device() for t in tensors.values() if t is not None}
+    if stream is None and len(seen) == 1 and min(seen) >= 0 and torch._C._cuda_getDevice() in seen:
+        return
     given = [(name, t) for name, t in tensors.items() if t is not None]
     for name, t in given:
         if not t.is_cuda:
