@@ -29,6 +29,7 @@
 #include "gated_device.cuh"
 #include "kdn_device.cuh"
 #include "kdn_internal.h"
+#include "sum_rows.cuh"
 
 namespace kdn {
 namespace {
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_kernel(const Gated
         for (int v = 0; v < V; ++v) p.final_state[sr * p.C + c + v] = carry[v];
 }
 
-// The same walk from the last token to the first.  `part` [state row, rank, C]
-// takes each CTA's share of grad A.
+// The same walk from the last token to the first.  `part` [sequence, rank,
+// H, C] takes each CTA's share of grad A.
 template <typename TI, typename TO, int V, int K, int NW, bool LEAK>
 __global__ void __launch_bounds__(NW * 32, 16 / NW)
 gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
@@ -502,7 +503,7 @@ gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
             for (int v = 0; v < V; ++v) {
                 float sum = 0.f;
                 for (int w = 0; w < NW; ++w) sum += fold.warp[0][w][v][lane].x;
-                part[(sr * S + rank) * p.C + c + v] = sum;
+                part[((sr / p.H * S + rank) * p.H + sr % p.H) * p.C + c + v] = sum;
             }
     }
 }
@@ -834,22 +835,9 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
             for (int v = 0; v < V; ++v) {
                 float sum = 0.f;
                 for (int i = 0; i < NW; ++i) sum += sh.fold.warp[0][i][v][lane].x;
-                if (c + v < p.C) part[(sr * S + rank) * p.C + c + v] = sum;
+                if (c + v < p.C) part[((sr / p.H * S + rank) * p.H + sr % p.H) * p.C + c + v] = sum;
             }
     }
-}
-
-// grad A: the shares of one head's state rows, in order.
-__global__ void __launch_bounds__(THREADS)
-gated_dA_kernel(const float* __restrict__ part, float* __restrict__ grad_A, long long rows, int H, int C, int S) {
-    const int cb = (C + THREADS - 1) / THREADS;
-    const int c = static_cast<int>(blockIdx.x % cb) * THREADS + threadIdx.x;
-    if (c >= C) return;
-    const int hd = blockIdx.x / cb;
-    float s = 0.f;
-    for (long long r = hd; r < rows; r += H)
-        for (int j = 0; j < S; ++j) s += part[(r * S + j) * C + c];
-    grad_A[static_cast<long long>(hd) * C + c] = s;
 }
 
 template <typename TI, typename TO>
@@ -991,9 +979,8 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
         return a.leak ? leak(std::true_type()) : leak(std::false_type());
     });
     if (s == KDN_OK && a.grad_A) {
-        const long long blocks = static_cast<long long>((a.C + THREADS - 1) / THREADS) * a.H;
-        gated_dA_kernel<<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(part, a.grad_A, rows, a.H, a.C, cut.S);
-        s = from_cuda(cudaGetLastError());
+        const long long HC = static_cast<long long>(a.H) * a.C;
+        s = from_cuda(sum_rows(part, rows / a.H * cut.S, HC, a.grad_A, nullptr, HC, stream));
     }
     if (own) {
         const kdn_status f = from_cuda(cudaFreeAsync(part, stream));
