@@ -13,8 +13,7 @@
 // are, so the rotation needs no other lane; dk / 8 lanes hold a head, and a
 // warp 32 / (dk / 8) heads side by side, all of one token where there are so
 // many.  It keeps the token's cos and sin in registers and walks the heads,
-// UNROLL rows' loads in flight; the angles, too dear to take per head, cost
-// a tenth of the instructions at 32 heads.
+// a few rows' loads in flight.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -26,11 +25,10 @@
 namespace kdn {
 namespace {
 
-using gated::from_f32;
-using gated::to_f32;
+using namespace gated;
 
 constexpr int WARPS = 8;
-constexpr int UNROLL = 4;
+constexpr int FWD_BLOCKS_PER_SM = 4, BWD_BLOCKS_PER_SM = 2;
 
 // The turns per position of a frequency, f / (2 pi) modulo 1, in 2^-64: the
 // double's 53 bits in a 64-bit fraction, whose product with an integer
@@ -42,12 +40,29 @@ __device__ __forceinline__ unsigned long long turns_per_position(float f) {
     return static_cast<unsigned long long>(t * 18446744073709551616.0);
 }
 
+// Reduced to an eighth of a turn either side of the nearest quarter, x in
+// [-1, 1] eighths: sin(x pi/4) = x S(x^2), cos(x pi/4) = C(x^2), S and C the
+// Chebyshev interpolants of degree 3 and 4 on [0, 1] (both within 2^-23.5).
 __device__ __forceinline__ float2 cos_sin(int pos, unsigned long long per) {
     const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos)) * per;
-    const int half = static_cast<int>(ph >> 32);   // in 2^-32 turns, [-1/2, 1/2)
-    float s, c;
-    sincospif(static_cast<float>(half) * 4.656612873077392578125e-10f, &s, &c);   // 2^-31: half turns
-    return make_float2(c, s);
+    const unsigned int turn = static_cast<unsigned int>(ph >> 32);             // 2^-32 turns
+    const unsigned int quarter = (turn + 0x20000000u) >> 30;
+    const float x = static_cast<float>(static_cast<int>(turn - (quarter << 30))) * 1.862645149230957e-09f;   // 2^-29
+    const float u = x * x;
+    float s = -3.595429006963968e-05f;
+    s = fmaf(s, u, 0.0024900068528950214f);
+    s = fmaf(s, u, -0.08074543625116348f);
+    s = fmaf(s, u, 0.7853981852531433f);
+    s *= x;
+    float c = 3.5297971407999285e-06f;
+    c = fmaf(c, u, -0.0003259385994169861f);
+    c = fmaf(c, u, 0.015854325145483017f);
+    c = fmaf(c, u, -0.3084251284599304f);
+    c = fmaf(c, u, 1.f);
+    const bool swap = quarter & 1;
+    const float co = swap ? s : c, si = swap ? c : s;
+    return make_float2(__uint_as_float(__float_as_uint(co) ^ ((quarter + 1) & 2) << 30),
+                       __uint_as_float(__float_as_uint(si) ^ (quarter & 2) << 30));
 }
 
 // What a lane holds of a row: pairs 4l .. 4l + 3 of the dk/2, pair p < rot/2
@@ -80,62 +95,112 @@ __device__ __forceinline__ Place place_of(int l, int rot) {
     return q;
 }
 
-__device__ __forceinline__ void get4(const float* p, float* v) {
-    const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
-    v[0] = q.x;
-    v[1] = q.y;
-    v[2] = q.z;
-    v[3] = q.w;
-}
-__device__ __forceinline__ void get4(const __nv_bfloat16* p, float* v) {
-    const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
-    v[0] = __uint_as_float(q.x << 16);
-    v[1] = __uint_as_float(q.x & 0xffff0000u);
-    v[2] = __uint_as_float(q.y << 16);
-    v[3] = __uint_as_float(q.y & 0xffff0000u);
-}
-__device__ __forceinline__ void put4(float* p, const float* v) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-}
-__device__ __forceinline__ void put4(__nv_bfloat16* p, const float* v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    uint2 q;
-    q.x = *reinterpret_cast<const uint32_t*>(&a);
-    q.y = *reinterpret_cast<const uint32_t*>(&b);
-    __stcs(reinterpret_cast<uint2*>(p), q);
+// A row's 8 elements: the pairs' first elements in a, their second in b.
+struct Row8 {
+    F2 a[2], b[2];
+};
+
+// The same as loaded: one or two 4-element groups.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 r;
+    __device__ __forceinline__ float get(int i) const { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
+    __device__ __forceinline__ void set(float a, float b, float c, float d) { r = make_float4(a, b, c, d); }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 r;
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w = i < 2 ? r.x : r.y;
+        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    }
+    __device__ __forceinline__ void set(float a, float b, float c, float d) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b), q = __floats2bfloat162_rn(c, d);
+        r.x = *reinterpret_cast<const uint32_t*>(&p);
+        r.y = *reinterpret_cast<const uint32_t*>(&q);
+    }
+};
+template <typename T>
+struct RawRow {
+    Raw4<T> u, v;
+};
+
+template <typename T>
+__device__ __forceinline__ RawRow<T> get_raw(const T* p, const Place& q) {
+    RawRow<T> r;
+    if (q.vec) {
+        r.u.r = __ldcs(reinterpret_cast<const decltype(r.u.r)*>(p + q.g0));
+        r.v.r = __ldcs(reinterpret_cast<const decltype(r.v.r)*>(p + q.g1));
+    } else {   // (never interleaved) pair by pair
+        r.u.set(to_f32(p[q.first(0)]), to_f32(p[q.first(1)]), to_f32(p[q.first(2)]), to_f32(p[q.first(3)]));
+        r.v.set(to_f32(p[q.second(0)]), to_f32(p[q.second(1)]), to_f32(p[q.second(2)]), to_f32(p[q.second(3)]));
+    }
+    return r;
 }
 
-// A row's 8 elements, v[i] and v[i + 4] a pair (INTER: v[2i], v[2i + 1]).
 template <bool INTER, typename T>
-__device__ __forceinline__ void get_row(const T* p, const Place& q, float* v) {
+__device__ __forceinline__ Row8 row_of(const RawRow<T>& r) {
+    Row8 o;
+    if (INTER) {
+        o.a[0] = F2{r.u.get(0), r.u.get(2)};
+        o.b[0] = F2{r.u.get(1), r.u.get(3)};
+        o.a[1] = F2{r.v.get(0), r.v.get(2)};
+        o.b[1] = F2{r.v.get(1), r.v.get(3)};
+    } else {
+        o.a[0] = F2{r.u.get(0), r.u.get(1)};
+        o.a[1] = F2{r.u.get(2), r.u.get(3)};
+        o.b[0] = F2{r.v.get(0), r.v.get(1)};
+        o.b[1] = F2{r.v.get(2), r.v.get(3)};
+    }
+    return o;
+}
+
+template <bool INTER, typename T>
+__device__ __forceinline__ void put_row(T* p, const Place& q, const Row8& o) {
+    RawRow<T> r;
+    if (INTER) {
+        r.u.set(o.a[0].x, o.b[0].x, o.a[0].y, o.b[0].y);
+        r.v.set(o.a[1].x, o.b[1].x, o.a[1].y, o.b[1].y);
+    } else {
+        r.u.set(o.a[0].x, o.a[0].y, o.a[1].x, o.a[1].y);
+        r.v.set(o.b[0].x, o.b[0].y, o.b[1].x, o.b[1].y);
+    }
     if (q.vec) {
-        get4(p + q.g0, v);
-        get4(p + q.g1, v + 4);
+        __stcs(reinterpret_cast<decltype(r.u.r)*>(p + q.g0), r.u.r);
+        __stcs(reinterpret_cast<decltype(r.v.r)*>(p + q.g1), r.v.r);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = to_f32(p[q.first(i)]);
-            v[i + 4] = to_f32(p[q.second(i)]);
+            p[q.first(i)] = from_f32<T>(r.u.get(i));
+            p[q.second(i)] = from_f32<T>(r.v.get(i));
         }
     }
 }
-template <bool INTER, typename T>
-__device__ __forceinline__ void put_row(T* p, const Place& q, const float* v) {
-    if (q.vec) {
-        put4(p + q.g0, v);
-        put4(p + q.g1, v + 4);
-    } else {
+
+__device__ __forceinline__ F2 neg2(F2 v) { return F2{-v.x, -v.y}; }
+
+// Rotation by the pairs' angles, c and s each (pair 0, pair 1), (pair 2, pair 3).
+struct Turn {
+    F2 c[2], s[2];
+};
+template <bool BACK>
+__device__ __forceinline__ void rotate(Row8& v, const Turn& t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[q.first(i)] = from_f32<T>(v[i]);
-            p[q.second(i)] = from_f32<T>(v[i + 4]);
-        }
+    for (int i = 0; i < 2; ++i) {
+        const F2 s = BACK ? neg2(t.s[i]) : t.s[i];
+        const F2 a = fma2(v.a[i], t.c[i], neg2(mul2(v.b[i], s)));
+        v.b[i] = fma2(v.a[i], s, mul2(v.b[i], t.c[i]));
+        v.a[i] = a;
     }
 }
+
 template <bool INTER>
-__device__ __forceinline__ constexpr int one(int i) { return INTER ? 2 * i : i; }
-template <bool INTER>
-__device__ __forceinline__ constexpr int two(int i) { return INTER ? 2 * i + 1 : i + 4; }
+__device__ __forceinline__ Row8 weight_of(const float* w, const Place& q) {
+    if (!w) return Row8{{both(1.f), both(1.f)}, {both(1.f), both(1.f)}};
+    return row_of<INTER>(get_raw(w, q));
+}
 
 // How one call's rows are dealt out: HS heads of a token side by side in a
 // warp (TPW = tokens side by side), the heads of a token over `chunks` warps.
@@ -144,36 +209,38 @@ struct Deal {
     int HS, chunks;
 };
 
-template <int LPR>
-struct Lane {
-    int l, head, token;    // lane in the row, head and token of the first row (token: in the group)
-};
+// The frequencies of a call in shared memory: turns per position and axis of
+// every pair; pairs behind rot have neither (cos = 1, sin = 0).
+template <int DK>
+struct Freqs {
+    unsigned long long per[DK / 2];
+    int ax[DK / 2];
 
-template <int LPR>
-__device__ __forceinline__ Lane<LPR> lane_of(int HS) {
-    const int lane = threadIdx.x & 31, sub = lane / LPR;
-    return Lane<LPR>{lane % LPR, sub % HS, sub / HS};
-}
+    __device__ __forceinline__ void fill(const QkArgs& p) {
+        for (int i = threadIdx.x; i < DK / 2; i += blockDim.x) {
+            per[i] = 0;
+            ax[i] = 0;
+            if (2 * i < p.rot) {
+                per[i] = turns_per_position(p.inv_freq[i]);
+                if (p.axis) ax[i] = min(max(p.axis[i], 0), p.axes - 1);
+            }
+        }
+        __syncthreads();
+    }
+};
 
 // cos and sin of a lane's 4 pairs at its token.  The HS rows of a token need
 // the same ones: with two of them each takes every second pair, with four or
 // more each takes one, and the lanes exchange them.
-template <int LPR, int M>
-__device__ __forceinline__ void angles_shared(const QkArgs& p, const int* pos, long long stride, int l, int sub,
-                                              int base, const unsigned long long* per, const int* ax, float2* cs) {
-    float2 mine[4 / M];
+template <int DK, int M>
+__device__ __forceinline__ Turn turn_shared(const Freqs<DK>& f, const int* pos, long long stride, int t, int l, int sub,
+                                            int base) {
+    constexpr int LPR = DK / 8;
+    float2 mine[4 / M], cs[4];
 #pragma unroll
     for (int k = 0; k < 4 / M; ++k) {
-        const int i = sub % M + M * k;
-        unsigned long long f = per[0];
-        int a = ax[0];
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-            if (i == j) {
-                f = per[j];
-                a = ax[j];
-            }
-        mine[k] = cos_sin(pos ? pos[a * stride] : static_cast<int>(stride), f);
+        const int i = 4 * l + sub % M + M * k;
+        mine[k] = cos_sin(pos ? pos[f.ax[i] * stride] : t, f.per[i]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -185,38 +252,20 @@ __device__ __forceinline__ void angles_shared(const QkArgs& p, const int* pos, l
             cs[i].y = __shfl_sync(0xffffffffu, mine[i / M].y, src);
         }
     }
+    return Turn{{F2{cs[0].x, cs[1].x}, F2{cs[2].x, cs[3].x}}, {F2{cs[0].y, cs[1].y}, F2{cs[2].y, cs[3].y}}};
 }
 
-template <int LPR>
-struct Angles {
-    unsigned long long per[4];
-    int ax[4], half, p0;
-
-    __device__ __forceinline__ void begin(const QkArgs& p, const Place& q) {
-        half = q.half;
-        p0 = q.p0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            per[i] = 0;
-            ax[i] = 0;
-            if (p0 + i < half) {
-                per[i] = turns_per_position(p.inv_freq[p0 + i]);
-                if (p.axis) ax[i] = min(max(p.axis[p0 + i], 0), p.axes - 1);
-            }
-        }
-    }
-    // (the whole warp; a lane without a token passes any valid one)
-    __device__ __forceinline__ void at(const QkArgs& p, long long token, int HS, int l, float2* cs) const {
-        const int sub = (threadIdx.x & 31) / LPR, base = sub / HS * HS;
-        const long long n = static_cast<long long>(p.B) * p.T;
-        const int* pos = p.pos ? p.pos + token : nullptr;
-        const long long stride = p.pos ? n : token % p.T;
-        if (HS >= 4) angles_shared<LPR, 4>(p, pos, stride, l, sub, base, per, ax, cs);
-        else if (HS == 2) angles_shared<LPR, 2>(p, pos, stride, l, sub, base, per, ax, cs);
-        else angles_shared<LPR, 1>(p, pos, stride, l, sub, base, per, ax, cs);
-        // pairs behind rot have no frequency: per = 0, cos = 1, sin = 0
-    }
-};
+// (the whole warp; a lane without a token passes any valid one)
+template <int DK>
+__device__ __forceinline__ Turn turn_at(const Freqs<DK>& f, const QkArgs& p, long long token, int t, int HS, int l) {
+    if (p.rot == 0) return Turn{{both(1.f), both(1.f)}, {both(0.f), both(0.f)}};
+    const int sub = (threadIdx.x & 31) / (DK / 8), base = sub / HS * HS;
+    const long long n = static_cast<long long>(p.B) * p.T;
+    const int* pos = p.pos ? p.pos + token : nullptr;
+    if (HS >= 4) return turn_shared<DK, 4>(f, pos, n, t, l, sub, base);
+    if (HS == 2) return turn_shared<DK, 2>(f, pos, n, t, l, sub, base);
+    return turn_shared<DK, 1>(f, pos, n, t, l, sub, base);
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -225,164 +274,165 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// Sum of products of two rows' elements over the row's lanes.
+template <int LPR>
+__device__ __forceinline__ float row_dot(const Row8& x, const Row8& y) {
+    const F2 s = fma2(x.a[0], y.a[0], fma2(x.a[1], y.a[1], fma2(x.b[0], y.b[0], mul2(x.b[1], y.b[1]))));
+    return row_sum<LPR>(s.x + s.y);
+}
+
 template <int DK>
 __device__ __forceinline__ float inverse_norm(const QkArgs& p, float ss) {
     if (p.norm == KDN_NORM_NONE) return 1.f;
     return rsqrtf((p.norm == KDN_NORM_RMS ? ss * (1.f / DK) : ss) + p.eps);
 }
 
-template <typename TI, typename TO, int DK, bool INTER>
-__global__ void __launch_bounds__(WARPS * 32) qk_fwd_kernel(const QkArgs p, const Deal deal) {
-    constexpr int LPR = DK / 8, RPW = 32 / LPR;
-    const long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-    if (item >= deal.items) return;
-    const int HS = deal.HS, tpw = RPW / HS;
-    const Lane<LPR> ln = lane_of<LPR>(HS);
-    const long long tokens = static_cast<long long>(p.B) * p.T;
-    const long long group = item / deal.chunks;
-    const int chunk = static_cast<int>(item - group * deal.chunks);
-    long long token = group * tpw + ln.token;
-    const bool here = token < tokens;
-    if (!here) token = tokens - 1;
-    const long long b = token / p.T;
-    const int t = static_cast<int>(token - b * p.T);
-    const Place q = place_of<INTER>(ln.l, p.rot);
-    float2 cs[4];
-    if (p.rot > 0) {
-        Angles<LPR> an;
-        an.begin(p, q);
-        an.at(p, token, HS, ln.l, cs);
+// A warp's place in a call: its lanes' head and token beside one another, and
+// which item it is at.
+template <int DK>
+struct Walk {
+    static constexpr int LPR = DK / 8, RPW = 32 / LPR;
+    int l, head, sub_token, HS, tpw, chunks, chunk, t;
+    long long tokens, token, b;
+    bool here;
+
+    __device__ __forceinline__ Walk(const QkArgs& p, const Deal& d) {
+        const int lane = threadIdx.x & 31, sub = lane / LPR;
+        HS = d.HS;
+        chunks = d.chunks;
+        tpw = RPW / HS;
+        l = lane % LPR;
+        head = sub % HS;
+        sub_token = sub / HS;
+        tokens = static_cast<long long>(p.B) * p.T;
     }
+    __device__ __forceinline__ void at(const QkArgs& p, long long item) {
+        const long long group = item / chunks;
+        chunk = static_cast<int>(item - group * chunks);
+        token = group * tpw + sub_token;
+        here = token < tokens;
+        if (!here) token = tokens - 1;
+        b = token / p.T;
+        t = static_cast<int>(token - b * p.T);
+    }
+};
+
+template <typename TI, typename TO, int DK, bool INTER>
+__global__ void __launch_bounds__(WARPS * 32, FWD_BLOCKS_PER_SM) qk_fwd_kernel(const QkArgs p, const Deal deal) {
+    constexpr int LPR = DK / 8, UNROLL = sizeof(TI) == 2 ? 4 : 2;
+    __shared__ Freqs<DK> freqs;
+    freqs.fill(p);
+    Walk<DK> at(p, deal);
+    const Place q = place_of<INTER>(at.l, p.rot);
+    const long long ystep = static_cast<long long>(p.T) * DK;
+    const int step = at.HS * at.chunks;
+    for (long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); item < deal.items;
+         item += static_cast<long long>(gridDim.x) * WARPS) {
+        at.at(p, item);
+        const Turn turn = turn_at<DK>(freqs, p, at.token, at.t, at.HS, at.l);
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const int H = p.heads[which];
-        if (H == 0) continue;
-        float w[8];
+        for (int which = 0; which < 2; ++which) {
+            const int H = p.heads[which];
+            if (H == 0) continue;
+            const Row8 w = weight_of<INTER>(p.w[which], q);
+            // this warp's heads: every chunks-th group of HS
+            const int h_ = at.chunk * at.HS;
+            const TI* x = static_cast<const TI*>(p.x[which]) + at.token * p.ld[which];
+            TO* y = static_cast<TO*>(p.y[which]) + (at.b * H * p.T + at.t) * DK;
+            for (int h0 = h_; h0 < H; h0 += UNROLL * step) {
+                RawRow<TI> raw[UNROLL];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.f;
-        if (p.w[which]) get_row<INTER>(p.w[which], q, w);
-        // this warp's heads: every chunks-th group of HS
-        const TI* x = static_cast<const TI*>(p.x[which]) + token * p.ld[which];
-        TO* y = static_cast<TO*>(p.y[which]) + (b * H * p.T + t) * DK;
-        const long long ystep = static_cast<long long>(p.T) * DK;
-        const int step = HS * deal.chunks;
-        for (int h0 = chunk * HS + ln.head; h0 - ln.head < H; h0 += UNROLL * step) {
-            float v[UNROLL][8];
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int h = h0 + u * step;
-                if (here && h < H) {
-                    get_row<INTER>(x + h * DK, q, v[u]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int h = h0 + u * step + at.head;
+                    raw[u] = RawRow<TI>{};
+                    if (at.here && h < H) raw[u] = get_raw(x + h * DK, q);
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int h = h0 + u * step;
-                float ss = 0.f;
+                for (int u = 0; u < UNROLL; ++u) {
+                    if (h0 + u * step >= H) break;             // (the warp as one)
+                    const int h = h0 + u * step + at.head;
+                    Row8 v = row_of<INTER>(raw[u]);
+                    const F2 r = both(inverse_norm<DK>(p, row_dot<LPR>(v, v)));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
-                const float r = inverse_norm<DK>(p, row_sum<LPR>(ss));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] *= r * w[i];
-                if (p.rot > 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float y1 = v[u][one<INTER>(i)], y2 = v[u][two<INTER>(i)];
-                        v[u][one<INTER>(i)] = fmaf(y1, cs[i].x, -y2 * cs[i].y);
-                        v[u][two<INTER>(i)] = fmaf(y1, cs[i].y, y2 * cs[i].x);
+                    for (int i = 0; i < 2; ++i) {
+                        v.a[i] = mul2(v.a[i], mul2(r, w.a[i]));
+                        v.b[i] = mul2(v.b[i], mul2(r, w.b[i]));
                     }
+                    rotate<false>(v, turn);
+                    if (at.here && h < H) put_row<INTER>(y + h * ystep, q, v);
                 }
-                if (here && h < H) put_row<INTER>(y + h * ystep, q, v[u]);
             }
         }
     }
 }
 
-// Backward.  A persistent grid, so that few blocks' shares of the weights'
-// gradients are left to add: part [block][2 dk], q's then k's.
+// Backward.  part [block][2 dk] takes each block's share of the weights'
+// gradients, q's then k's.
 template <typename TI, typename TO, int DK, bool INTER>
-__global__ void __launch_bounds__(WARPS * 32) qk_bwd_kernel(const QkArgs p, const Deal deal, float* part) {
-    constexpr int LPR = DK / 8, RPW = 32 / LPR, UNR = 2;
+__global__ void __launch_bounds__(WARPS * 32, BWD_BLOCKS_PER_SM)
+qk_bwd_kernel(const QkArgs p, const Deal deal, float* part) {
+    constexpr int LPR = DK / 8, UNR = 2;
+    __shared__ Freqs<DK> freqs;
     __shared__ float share[WARPS][DK];
-    const int warp = threadIdx.x >> 5;
-    const int HS = deal.HS, tpw = RPW / HS;
-    const Lane<LPR> ln = lane_of<LPR>(HS);
-    const long long tokens = static_cast<long long>(p.B) * p.T;
-    const Place q = place_of<INTER>(ln.l, p.rot);
+    freqs.fill(p);
+    Walk<DK> at(p, deal);
+    const Place q = place_of<INTER>(at.l, p.rot);
     const float inv_n = p.norm == KDN_NORM_RMS ? 1.f / DK : 1.f;
-    Angles<LPR> an;
-    if (p.rot > 0) an.begin(p, q);
-    float dw[2][8];
+    const long long ystep = static_cast<long long>(p.T) * DK;
+    const int step = at.HS * at.chunks;
+    Row8 dw[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+    for (int i = 0; i < 2; ++i) dw[0].a[i] = dw[0].b[i] = dw[1].a[i] = dw[1].b[i] = both(0.f);
 
-    for (long long item = static_cast<long long>(blockIdx.x) * WARPS + warp; item < deal.items;
+    for (long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); item < deal.items;
          item += static_cast<long long>(gridDim.x) * WARPS) {
-        const long long group = item / deal.chunks;
-        const int chunk = static_cast<int>(item - group * deal.chunks);
-        long long token = group * tpw + ln.token;
-        const bool here = token < tokens;
-        if (!here) token = tokens - 1;
-        const long long b = token / p.T;
-        const int t = static_cast<int>(token - b * p.T);
-        float2 cs[4];
-        if (p.rot > 0) an.at(p, token, HS, ln.l, cs);
+        at.at(p, item);
+        const Turn turn = turn_at<DK>(freqs, p, at.token, at.t, at.HS, at.l);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const int H = p.heads[which];
             if (H == 0) continue;
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 1.f;
-            if (p.w[which]) get_row<INTER>(p.w[which], q, w);
-            const TI* x = static_cast<const TI*>(p.x[which]) + token * p.ld[which];
-            TI* gx = static_cast<TI*>(p.grad_x[which]) + token * p.grad_ld[which];
-            const TO* gy = static_cast<const TO*>(p.grad_y[which]) + (b * H * p.T + t) * DK;
-            const long long ystep = static_cast<long long>(p.T) * DK;
-            const int step = HS * deal.chunks;
-            for (int h0 = chunk * HS + ln.head; h0 - ln.head < H; h0 += UNR * step) {
-                float v[UNR][8], g[UNR][8];
+            const Row8 w = weight_of<INTER>(p.w[which], q);
+            const TI* x = static_cast<const TI*>(p.x[which]) + at.token * p.ld[which];
+            TI* gx = static_cast<TI*>(p.grad_x[which]) + at.token * p.grad_ld[which];
+            const TO* gy = static_cast<const TO*>(p.grad_y[which]) + (at.b * H * p.T + at.t) * DK;
+            for (int h0 = at.chunk * at.HS; h0 < H; h0 += UNR * step) {
+                RawRow<TI> xr[UNR];
+                RawRow<TO> gr[UNR];
 #pragma unroll
                 for (int u = 0; u < UNR; ++u) {
-                    const int h = h0 + u * step;
-                    if (here && h < H) {
-                        get_row<INTER>(x + h * DK, q, v[u]);
-                        get_row<INTER>(gy + h * ystep, q, g[u]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[u][i] = g[u][i] = 0.f;
+                    const int h = h0 + u * step + at.head;
+                    xr[u] = RawRow<TI>{};
+                    gr[u] = RawRow<TO>{};
+                    if (at.here && h < H) {
+                        xr[u] = get_raw(x + h * DK, q);
+                        gr[u] = get_raw(gy + h * ystep, q);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < UNR; ++u) {
-                    const int h = h0 + u * step;
-                    if (p.rot > 0) {
+                    if (h0 + u * step >= H) break;             // (the warp as one)
+                    const int h = h0 + u * step + at.head;
+                    const Row8 v = row_of<INTER>(xr[u]);
+                    Row8 g = row_of<INTER>(gr[u]);
+                    rotate<true>(g, turn);
+                    const float r = inverse_norm<DK>(p, row_dot<LPR>(v, v));
+                    Row8 t;                                    // g w
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float g1 = g[u][one<INTER>(i)], g2 = g[u][two<INTER>(i)];
-                            g[u][one<INTER>(i)] = fmaf(g1, cs[i].x, g2 * cs[i].y);
-                            g[u][two<INTER>(i)] = fmaf(g2, cs[i].x, -g1 * cs[i].y);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        t.a[i] = mul2(g.a[i], w.a[i]);
+                        t.b[i] = mul2(g.b[i], w.b[i]);
                     }
-                    float ss = 0.f, tx = 0.f;
+                    const float back = p.norm == KDN_NORM_NONE ? 0.f : -(r * r * r) * (row_dot<LPR>(t, v) * inv_n);
+                    Row8 o;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        ss = fmaf(v[u][i], v[u][i], ss);
-                        tx = fmaf(v[u][i], g[u][i] * w[i], tx);
+                    for (int i = 0; i < 2; ++i) {
+                        o.a[i] = fma2(both(r), t.a[i], mul2(both(back), v.a[i]));
+                        o.b[i] = fma2(both(r), t.b[i], mul2(both(back), v.b[i]));
+                        dw[which].a[i] = fma2(mul2(both(r), v.a[i]), g.a[i], dw[which].a[i]);
+                        dw[which].b[i] = fma2(mul2(both(r), v.b[i]), g.b[i], dw[which].b[i]);
                     }
-                    const float r = inverse_norm<DK>(p, row_sum<LPR>(ss));
-                    const float back = p.norm == KDN_NORM_NONE ? 0.f : r * r * r * row_sum<LPR>(tx) * inv_n;
-                    float o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float rg = r * g[u][i];
-                        dw[which][i] = fmaf(v[u][i], rg, dw[which][i]);
-                        o[i] = fmaf(rg, w[i], -v[u][i] * back);
-                    }
-                    if (here && h < H) put_row<INTER>(gx + h * DK, q, o);
+                    if (at.here && h < H) put_row<INTER>(gx + h * DK, q, o);
                 }
             }
         }
@@ -393,14 +443,17 @@ __global__ void __launch_bounds__(WARPS * 32) qk_bwd_kernel(const QkArgs p, cons
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float s = dw[which][i];
+            const F2 f = i < 4 ? dw[which].a[i / 2] : dw[which].b[(i - 4) / 2];
+            float s = i & 1 ? f.y : f.x;
 #pragma unroll
             for (int o = LPR; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if ((threadIdx.x & 31) < LPR) {
-                const int j = INTER ? 8 * ln.l + i : i < 4 ? q.first(i) : q.second(i - 4);
-                // vectors' groups are elements in order
-                share[warp][q.vec ? (i < 4 ? q.g0 + i : q.g1 + i - 4) : j] = s;
-            }
+            // pair i & 3, its first element (i < 4) or its second; where a lane holds two
+            // groups of a half-rotated head's rest, `a` is the first group
+            int j;
+            if (INTER) j = 2 * (q.p0 + (i & 3)) + (i >= 4);
+            else if (q.vec) j = (i < 4 ? q.g0 : q.g1) + (i & 3);
+            else j = i < 4 ? q.first(i) : q.second(i - 4);
+            if ((threadIdx.x & 31) < LPR) share[threadIdx.x >> 5][j] = s;
         }
         __syncthreads();
         for (int j = threadIdx.x; j < DK; j += WARPS * 32) {
@@ -412,8 +465,6 @@ __global__ void __launch_bounds__(WARPS * 32) qk_bwd_kernel(const QkArgs p, cons
         __syncthreads();
     }
 }
-
-constexpr int BWD_BLOCKS_PER_SM = 2;
 
 // Heads side by side: a power of two, as many as a warp takes and there are.
 // Few tokens' heads are dealt to more warps, so that every SM has some.
@@ -429,10 +480,15 @@ Deal deal_of(long long tokens, int Hq, int Hk, int dk) {
     return d;
 }
 
-int bwd_blocks(int B, int T, int Hq, int Hk, int dk) {
-    const long long items = deal_of(static_cast<long long>(B) * T, Hq, Hk, dk).items;
-    const long long blocks = (items + WARPS - 1) / WARPS, cap = static_cast<long long>(sm_count()) * BWD_BLOCKS_PER_SM;
+// A persistent grid: the frequencies are taken once per block, and few
+// blocks' shares of the weights' gradients are left to add.
+int blocks_of(const Deal& d, int per_sm) {
+    const long long blocks = (d.items + WARPS - 1) / WARPS, cap = static_cast<long long>(sm_count()) * per_sm;
     return static_cast<int>(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+}
+
+int bwd_blocks(int B, int T, int Hq, int Hk, int dk) {
+    return blocks_of(deal_of(static_cast<long long>(B) * T, Hq, Hk, dk), BWD_BLOCKS_PER_SM);
 }
 
 template <typename F>
@@ -465,17 +521,16 @@ long long qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int dk) {
 
 kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream) {
     const Deal deal = deal_of(static_cast<long long>(a.B) * a.T, a.heads[0], a.heads[1], a.dk);
-    const long long blocks = (deal.items + WARPS - 1) / WARPS;
-    if (blocks > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
+    const int blocks = blocks_of(deal, FWD_BLOCKS_PER_SM);
     return by_type(a, [&](auto ti, auto to) {
         return by_dk(a.dk, [&](auto n) {
             using TI = decltype(ti);
             using TO = decltype(to);
             constexpr int DK = decltype(n)::value;
             if (a.interleaved)
-                qk_fwd_kernel<TI, TO, DK, true><<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(a, deal);
+                qk_fwd_kernel<TI, TO, DK, true><<<blocks, WARPS * 32, 0, stream>>>(a, deal);
             else
-                qk_fwd_kernel<TI, TO, DK, false><<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(a, deal);
+                qk_fwd_kernel<TI, TO, DK, false><<<blocks, WARPS * 32, 0, stream>>>(a, deal);
             return from_cuda(cudaGetLastError());
         });
     });
