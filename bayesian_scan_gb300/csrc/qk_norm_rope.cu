@@ -28,7 +28,7 @@ namespace {
 using namespace gated;
 
 constexpr int WARPS = 8;
-constexpr int FWD_BLOCKS_PER_SM = 4, BWD_BLOCKS_PER_SM = 2;
+constexpr int FWD_BLOCKS_PER_SM = 3, BWD_BLOCKS_PER_SM = 2, BWD_DEPTH = 4;
 
 // The turns per position of a frequency, f / (2 pi) modulo 1, in 2^-64: the
 // double's 53 bits in a 64-bit fraction, whose product with an integer
@@ -287,80 +287,114 @@ __device__ __forceinline__ float inverse_norm(const QkArgs& p, float ss) {
     return rsqrtf((p.norm == KDN_NORM_RMS ? ss * (1.f / DK) : ss) + p.eps);
 }
 
-// A warp's place in a call: its lanes' head and token beside one another, and
-// which item it is at.
+// A warp's place in a call: an item is a group of tokens and a share of their
+// heads, every chunks-th step of HS heads, the queries' and then the keys'.
 template <int DK>
-struct Walk {
+struct Place2 {
     static constexpr int LPR = DK / 8, RPW = 32 / LPR;
-    int l, head, sub_token, HS, tpw, chunks, chunk, t;
-    long long tokens, token, b;
+    int l, sub, t, b, n0, n, h;   // steps of the queries' heads, of both; first head of the lane
+    long long token;
     bool here;
 
-    __device__ __forceinline__ Walk(const QkArgs& p, const Deal& d) {
-        const int lane = threadIdx.x & 31, sub = lane / LPR;
-        HS = d.HS;
-        chunks = d.chunks;
-        tpw = RPW / HS;
-        l = lane % LPR;
-        head = sub % HS;
-        sub_token = sub / HS;
-        tokens = static_cast<long long>(p.B) * p.T;
-    }
-    __device__ __forceinline__ void at(const QkArgs& p, long long item) {
-        const long long group = item / chunks;
-        chunk = static_cast<int>(item - group * chunks);
-        token = group * tpw + sub_token;
+    __device__ __forceinline__ Place2() : l(threadIdx.x % 32 % LPR), sub(threadIdx.x % 32 / LPR) {}
+    __device__ __forceinline__ void at(const QkArgs& p, const Deal& d, long long item) {
+        const long long group = item / d.chunks, tokens = static_cast<long long>(p.B) * p.T;
+        const int first = static_cast<int>(item - group * d.chunks) * d.HS, step = d.HS * d.chunks;
+        token = group * (RPW / d.HS) + sub / d.HS;
         here = token < tokens;
         if (!here) token = tokens - 1;
-        b = token / p.T;
-        t = static_cast<int>(token - b * p.T);
+        b = static_cast<int>(token / p.T);
+        t = static_cast<int>(token - static_cast<long long>(b) * p.T);
+        n0 = p.heads[0] > first ? (p.heads[0] - first + step - 1) / step : 0;
+        n = n0 + (p.heads[1] > first ? (p.heads[1] - first + step - 1) / step : 0);
+        h = first + sub % d.HS;
     }
 };
 
+// A lane's rows on their way: a slot per step in shared memory that the lane
+// alone fills and reads, DEPTH steps ahead, so that neither registers nor a
+// barrier is needed for what is in flight.
+template <typename T, int DEPTH>
+struct Ring {
+    Raw4<T> slot[DEPTH][2][WARPS * 32];      // 8 or 16 adjacent bytes a lane: no bank conflicts
+
+    __device__ __forceinline__ void fetch(int i, const T* row, const Place& q) {
+        const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(&slot[i % DEPTH][0][threadIdx.x])),
+                       b = a + sizeof(Raw4<T>) * WARPS * 32;
+        if (sizeof(T) == 2) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(a), "l"(row + q.g0) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(b), "l"(row + q.g1) : "memory");
+        } else {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(row + q.g0) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(b), "l"(row + q.g1) : "memory");
+        }
+    }
+    __device__ __forceinline__ RawRow<T> take(int i) const {
+        return RawRow<T>{slot[i % DEPTH][0][threadIdx.x], slot[i % DEPTH][1][threadIdx.x]};
+    }
+};
+
+// One row from the loaded elements to the stored ones.
 template <typename TI, typename TO, int DK, bool INTER>
-__global__ void __launch_bounds__(WARPS * 32, FWD_BLOCKS_PER_SM) qk_fwd_kernel(const QkArgs p, const Deal deal) {
-    constexpr int LPR = DK / 8, UNROLL = sizeof(TI) == 2 ? 4 : 2;
+__device__ __forceinline__ void qk_row(const QkArgs& p, const RawRow<TI>& raw, const Row8& w, const Turn& turn,
+                                       const Place& q, TO* y, bool on) {
+    Row8 v = row_of<INTER>(raw);
+    const F2 r = both(inverse_norm<DK>(p, row_dot<DK / 8>(v, v)));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        v.a[k] = mul2(v.a[k], mul2(r, w.a[k]));
+        v.b[k] = mul2(v.b[k], mul2(r, w.b[k]));
+    }
+    rotate<false>(v, turn);
+    if (on) put_row<INTER>(y, q, v);
+}
+
+template <typename TI, typename TO, int DK, bool INTER>
+__global__ void __launch_bounds__(WARPS * 32, FWD_BLOCKS_PER_SM)
+qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
+    constexpr int UNROLL = sizeof(TI) == 2 ? 4 : 2;
     __shared__ Freqs<DK> freqs;
     freqs.fill(p);
-    Walk<DK> at(p, deal);
+    Place2<DK> at;
     const Place q = place_of<INTER>(at.l, p.rot);
-    const long long ystep = static_cast<long long>(p.T) * DK;
-    const int step = at.HS * at.chunks;
+    const int step = deal.HS * deal.chunks;
+    const long long xstep = static_cast<long long>(step) * DK, ystep = xstep * p.T;
     for (long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); item < deal.items;
          item += static_cast<long long>(gridDim.x) * WARPS) {
-        at.at(p, item);
-        const Turn turn = turn_at<DK>(freqs, p, at.token, at.t, at.HS, at.l);
+        at.at(p, deal, item);
+        const Turn turn = turn_at<DK>(freqs, p, at.token, at.t, deal.HS, at.l);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const int H = p.heads[which];
-            if (H == 0) continue;
+            const int H = p.heads[which], steps = which ? at.n - at.n0 : at.n0;
+            if (steps == 0) continue;
             const Row8 w = weight_of<INTER>(p.w[which], q);
-            // this warp's heads: every chunks-th group of HS
-            const int h_ = at.chunk * at.HS;
-            const TI* x = static_cast<const TI*>(p.x[which]) + at.token * p.ld[which];
-            TO* y = static_cast<TO*>(p.y[which]) + (at.b * H * p.T + at.t) * DK;
-            for (int h0 = h_; h0 < H; h0 += UNROLL * step) {
-                RawRow<TI> raw[UNROLL];
+            const TI* x = static_cast<const TI*>(p.x[which]) + at.token * p.ld[which] + at.h * DK;
+            TO* y = static_cast<TO*>(p.y[which]) +
+                    ((static_cast<long long>(at.b) * H + at.h) * p.T + at.t) * DK;
+            // steps whose rows are all there, UNROLL rows' loads in flight
+            const int whole = __all_sync(0xffffffffu, at.here && at.h + (steps - 1) * step < H) ? steps : steps - 1;
+            int i = 0;
+            if (__all_sync(0xffffffffu, at.here))
+                for (; i + UNROLL <= whole; i += UNROLL) {
+                    RawRow<TI> raw[UNROLL];
 #pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    const int h = h0 + u * step + at.head;
-                    raw[u] = RawRow<TI>{};
-                    if (at.here && h < H) raw[u] = get_raw(x + h * DK, q);
-                }
-#pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    if (h0 + u * step >= H) break;             // (the warp as one)
-                    const int h = h0 + u * step + at.head;
-                    Row8 v = row_of<INTER>(raw[u]);
-                    const F2 r = both(inverse_norm<DK>(p, row_dot<LPR>(v, v)));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        v.a[i] = mul2(v.a[i], mul2(r, w.a[i]));
-                        v.b[i] = mul2(v.b[i], mul2(r, w.b[i]));
+                    for (int u = 0; u < UNROLL; ++u) {
+                        raw[u] = get_raw(x, q);
+                        x += xstep;
                     }
-                    rotate<false>(v, turn);
-                    if (at.here && h < H) put_row<INTER>(y + h * ystep, q, v);
+#pragma unroll
+                    for (int u = 0; u < UNROLL; ++u) {
+                        qk_row<TI, TO, DK, INTER>(p, raw[u], w, turn, q, y, true);
+                        y += ystep;
+                    }
                 }
+            for (; i < steps; ++i) {
+                const bool on = at.here && at.h + i * step < H;
+                RawRow<TI> raw{};
+                if (on) raw = get_raw(x, q);
+                qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, on);
+                x += xstep;
+                y += ystep;
             }
         }
     }
@@ -368,72 +402,92 @@ __global__ void __launch_bounds__(WARPS * 32, FWD_BLOCKS_PER_SM) qk_fwd_kernel(c
 
 // Backward.  part [block][2 dk] takes each block's share of the weights'
 // gradients, q's then k's.
+template <typename TI, typename TO, int DEPTH>
+struct BwdRing {
+    Ring<TI, DEPTH> x;
+    Ring<TO, DEPTH> g;
+};
+
 template <typename TI, typename TO, int DK, bool INTER>
 __global__ void __launch_bounds__(WARPS * 32, BWD_BLOCKS_PER_SM)
-qk_bwd_kernel(const QkArgs p, const Deal deal, float* part) {
-    constexpr int LPR = DK / 8, UNR = 2;
+qk_bwd_kernel(const __grid_constant__ QkArgs p, const Deal deal, float* part) {
+    constexpr int LPR = DK / 8, DEPTH = BWD_DEPTH;
     __shared__ Freqs<DK> freqs;
     __shared__ float share[WARPS][DK];
+    extern __shared__ __align__(16) char smem[];
+    BwdRing<TI, TO, DEPTH>& ring = *reinterpret_cast<BwdRing<TI, TO, DEPTH>*>(smem);
     freqs.fill(p);
-    Walk<DK> at(p, deal);
+    Place2<DK> at;
     const Place q = place_of<INTER>(at.l, p.rot);
     const float inv_n = p.norm == KDN_NORM_RMS ? 1.f / DK : 1.f;
+    const int step = deal.HS * deal.chunks;
     const long long ystep = static_cast<long long>(p.T) * DK;
-    const int step = at.HS * at.chunks;
     Row8 dw[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) dw[0].a[i] = dw[0].b[i] = dw[1].a[i] = dw[1].b[i] = both(0.f);
 
     for (long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); item < deal.items;
          item += static_cast<long long>(gridDim.x) * WARPS) {
-        at.at(p, item);
-        const Turn turn = turn_at<DK>(freqs, p, at.token, at.t, at.HS, at.l);
+        at.at(p, deal, item);
+        const TI* x[2];
+        const TO* gy[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            x[w] = static_cast<const TI*>(p.x[w]) + at.token * p.ld[w];
+            gy[w] = static_cast<const TO*>(p.grad_y[w]) + (static_cast<long long>(at.b) * p.heads[w] * p.T + at.t) * DK;
+        }
+        auto fetch = [&](int i) {
+            if (i < at.n) {
+                const int which = i >= at.n0, h = at.h + (which ? i - at.n0 : i) * step;
+                if (q.vec && at.here && h < p.heads[which]) {
+                    ring.x.fetch(i, (which ? x[1] : x[0]) + h * DK, q);
+                    ring.g.fetch(i, (which ? gy[1] : gy[0]) + h * ystep, q);
+                }
+            }
+            copy_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) fetch(i);
+        const Turn turn = turn_at<DK>(freqs, p, at.token, at.t, deal.HS, at.l);
+        int i = 0;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const int H = p.heads[which];
-            if (H == 0) continue;
+            const int H = p.heads[which], end = which ? at.n : at.n0;
+            if (i >= end) continue;
             const Row8 w = weight_of<INTER>(p.w[which], q);
-            const TI* x = static_cast<const TI*>(p.x[which]) + at.token * p.ld[which];
+            int h = at.h;
             TI* gx = static_cast<TI*>(p.grad_x[which]) + at.token * p.grad_ld[which];
-            const TO* gy = static_cast<const TO*>(p.grad_y[which]) + (at.b * H * p.T + at.t) * DK;
-            for (int h0 = at.chunk * at.HS; h0 < H; h0 += UNR * step) {
-                RawRow<TI> xr[UNR];
-                RawRow<TO> gr[UNR];
-#pragma unroll
-                for (int u = 0; u < UNR; ++u) {
-                    const int h = h0 + u * step + at.head;
-                    xr[u] = RawRow<TI>{};
-                    gr[u] = RawRow<TO>{};
-                    if (at.here && h < H) {
-                        xr[u] = get_raw(x + h * DK, q);
-                        gr[u] = get_raw(gy + h * ystep, q);
-                    }
+            for (; i < end; ++i, h += step) {
+                const bool on = at.here && h < H;
+                copy_wait<DEPTH - 1>();
+                RawRow<TI> xr{};
+                RawRow<TO> gr{};
+                if (on) {
+                    xr = q.vec ? ring.x.take(i) : get_raw(x[which] + h * DK, q);
+                    gr = q.vec ? ring.g.take(i) : get_raw(gy[which] + h * ystep, q);
                 }
+                const Row8 v = row_of<INTER>(xr);
+                Row8 g = row_of<INTER>(gr);
+                rotate<true>(g, turn);
+                // a row that is not there adds nothing, whatever 1 / sqrt(eps) is
+                const float ss = row_dot<LPR>(v, v), r = on ? inverse_norm<DK>(p, ss) : 0.f;
+                fetch(i + DEPTH);
+                Row8 t;                                        // g w
 #pragma unroll
-                for (int u = 0; u < UNR; ++u) {
-                    if (h0 + u * step >= H) break;             // (the warp as one)
-                    const int h = h0 + u * step + at.head;
-                    const Row8 v = row_of<INTER>(xr[u]);
-                    Row8 g = row_of<INTER>(gr[u]);
-                    rotate<true>(g, turn);
-                    const float r = inverse_norm<DK>(p, row_dot<LPR>(v, v));
-                    Row8 t;                                    // g w
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        t.a[i] = mul2(g.a[i], w.a[i]);
-                        t.b[i] = mul2(g.b[i], w.b[i]);
-                    }
-                    const float back = p.norm == KDN_NORM_NONE ? 0.f : -(r * r * r) * (row_dot<LPR>(t, v) * inv_n);
-                    Row8 o;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        o.a[i] = fma2(both(r), t.a[i], mul2(both(back), v.a[i]));
-                        o.b[i] = fma2(both(r), t.b[i], mul2(both(back), v.b[i]));
-                        dw[which].a[i] = fma2(mul2(both(r), v.a[i]), g.a[i], dw[which].a[i]);
-                        dw[which].b[i] = fma2(mul2(both(r), v.b[i]), g.b[i], dw[which].b[i]);
-                    }
-                    if (at.here && h < H) put_row<INTER>(gx + h * DK, q, o);
+                for (int k = 0; k < 2; ++k) {
+                    t.a[k] = mul2(g.a[k], w.a[k]);
+                    t.b[k] = mul2(g.b[k], w.b[k]);
                 }
+                const float back = p.norm == KDN_NORM_NONE ? 0.f : -(r * r * r) * (row_dot<LPR>(t, v) * inv_n);
+                Row8 o;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    o.a[k] = fma2(both(r), t.a[k], mul2(both(back), v.a[k]));
+                    o.b[k] = fma2(both(r), t.b[k], mul2(both(back), v.b[k]));
+                    dw[which].a[k] = fma2(mul2(both(r), v.a[k]), g.a[k], dw[which].a[k]);
+                    dw[which].b[k] = fma2(mul2(both(r), v.b[k]), g.b[k], dw[which].b[k]);
+                }
+                if (on) put_row<INTER>(gx + h * DK, q, o);
             }
         }
     }
@@ -551,8 +605,11 @@ kdn_status qk_bwd_launch(const QkArgs& a, cudaStream_t stream) {
             using TI = decltype(ti);
             using TO = decltype(to);
             constexpr int DK = decltype(n)::value;
-            if (a.interleaved) qk_bwd_kernel<TI, TO, DK, true><<<blocks, WARPS * 32, 0, stream>>>(a, deal, part);
-            else qk_bwd_kernel<TI, TO, DK, false><<<blocks, WARPS * 32, 0, stream>>>(a, deal, part);
+            auto kernel = a.interleaved ? qk_bwd_kernel<TI, TO, DK, true> : qk_bwd_kernel<TI, TO, DK, false>;
+            const int smem = sizeof(BwdRing<TI, TO, BWD_DEPTH>);
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return from_cuda(e);
+            kernel<<<blocks, WARPS * 32, smem, stream>>>(a, deal, part);
             return from_cuda(cudaGetLastError());
         });
     });

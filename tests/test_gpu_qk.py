@@ -124,6 +124,16 @@ def test_axis_out_of_range_is_clamped_and_zero_rows():
         check(s, 2, 2, 64, F32, norm)
 
 
+def test_no_eps():
+    # without eps 1 / sqrt(0) is infinite; it stays with rows of zeros, of which there are none here,
+    # and not with the places of a warp that have no row
+    for B, T, Hq, Hk in ((1, 3, 3, 1), (1, 1, 1, 1), (1, 5, 7, 2)):
+        s = draw(B, T, Hq, Hk, 16, F32, seed=T)
+        check(s, Hq, Hk, 16, F32, "rms", eps=0.0)
+        s = draw(B, T, Hq, Hk, 128, BF16, seed=T)
+        check(s, Hq, Hk, 128, F32, "l2", eps=0.0)
+
+
 def test_one_tensor_alone_and_slices_written():
     from bayesian_scan_gb300 import kdn
     s = draw(2, 11, 3, 2, 32, BF16, seed=4)
