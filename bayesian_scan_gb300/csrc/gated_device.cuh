@@ -62,30 +62,32 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// The gate alpha = exp(z), z = -A d, of two elements, and w = 1 - alpha.
+constexpr float LOG2E = 1.4426950408889634f;
+
+// The gate alpha = exp(-A d) = 2^y, y = -A log2(e) d, of two elements, and
+// w = 1 - alpha.
 //
-// |z| <= 0.25: expm1(z) = z p(z), p the degree-4 Chebyshev interpolant of
-// (e^z - 1)/z on [-0.25, 0.25] (1.9e-7 of expm1 with its roundings, alpha to
-// half a step and a little).  Beyond, memories are four tokens and 2^(z log2
-// e) of the hardware (2^-22) serves.
+// |y| <= 0.36: 2^y - 1 = y p(y), p the degree-4 Chebyshev interpolant of
+// (2^y - 1)/y on [-0.36, 0.36] (1.9e-7 of it with its roundings; alpha to
+// half a step and a little).  Beyond, memories are four tokens and the
+// hardware's 2^y (2^-22) serves.
 struct Gate2 {
     F2 a, w;
 };
 
 template <bool W>
-__device__ __forceinline__ Gate2 gate2(F2 z) {
-    F2 p = both(0.00834884773939848f);
-    p = fma2(p, z, both(0.04177529364824295f));
-    p = fma2(p, z, both(0.1666664183139801f));
-    p = fma2(p, z, both(0.4999983012676239f));
-    p = fma2(p, z, both(1.f));
-    const F2 y = mul2(z, both(1.4426950408889634f));
-    const F2 big{ex2(y.x), ex2(y.y)}, near = fma2(p, z, both(1.f));
-    const bool bx = fabsf(z.x) <= 0.25f, by = fabsf(z.y) <= 0.25f;
+__device__ __forceinline__ Gate2 gate2(F2 y) {
+    F2 p = both(0.0013358289143070579f);
+    p = fma2(p, y, both(0.009643110446631908f));
+    p = fma2(p, y, both(0.055504027754068375f));
+    p = fma2(p, y, both(0.24022570252418518f));
+    p = fma2(p, y, both(0.6931471824645996f));
+    const F2 big{ex2(y.x), ex2(y.y)}, near = fma2(p, y, both(1.f));
+    const bool bx = fabsf(y.x) <= 0.36f, by = fabsf(y.y) <= 0.36f;
     Gate2 g;
     g.a = F2{bx ? near.x : big.x, by ? near.y : big.y};
     if (W) {
-        const F2 m = mul2(p, F2{-z.x, -z.y}), f = fma2(big, both(-1.f), both(1.f));
+        const F2 m = mul2(p, F2{-y.x, -y.y}), f = fma2(big, both(-1.f), both(1.f));
         g.w = F2{bx ? m.x : f.x, by ? m.y : f.y};
     }
     return g;
@@ -94,26 +96,26 @@ __device__ __forceinline__ Gate2 gate2(F2 z) {
 // The same as alpha = a + e: a the rounded value, e what the rounding lost.
 // A long memory has alpha next to 1, where a float's step is 6e-8 whatever
 // 1 - alpha is: a state carried through a thousand rounded decays would be
-// off by 7e-6.  So a span's decay is exp of its summed exponents, in this
+// off by 7e-6.  So a span's decay is 2^y of its summed exponents, in this
 // form, and only the at most 16 tokens that a warp composes itself multiply
 // rounded alphas.
 //
-// |z| <= 0.35: degree 5, 1.3e-7 of expm1; beyond, a - 1 and m are the same
+// |y| <= 0.5: degree 5, 1.2e-7 of 2^y - 1; beyond, a - 1 and m are the same
 // rounding, so e is zero by itself.
 struct Gate {
     float a, e, w;
 };
 
-__device__ __forceinline__ Gate gate(float z) {
-    float p = 0.0013934532f;
-    p = fmaf(p, z, 0.008369861f);
-    p = fmaf(p, z, 0.041666456f);
-    p = fmaf(p, z, 0.16666499f);
-    p = fmaf(p, z, 0.5f);
-    p = fmaf(p, z, 1.0f);
-    const float big = ex2(z * 1.4426950408889634f);
-    const bool small = fabsf(z) <= 0.35f;
-    const float m = small ? z * p : big - 1.f;   // expm1(z)
+__device__ __forceinline__ Gate gate(float y) {
+    float p = 0.00015453163359779865f;
+    p = fmaf(p, y, 0.0013390863314270973f);
+    p = fmaf(p, y, 0.009618083015084267f);
+    p = fmaf(p, y, 0.055503569543361664f);
+    p = fmaf(p, y, 0.24022650718688965f);
+    p = fmaf(p, y, 0.6931471824645996f);
+    const float big = ex2(y);
+    const bool small = fabsf(y) <= 0.5f;
+    const float m = small ? y * p : big - 1.f;   // 2^y - 1
     Gate g;
     g.a = small ? 1.f + m : big;
     g.e = m - (g.a - 1.f);
@@ -162,13 +164,6 @@ struct Vec<float, 2> {
     __device__ __forceinline__ void set(const float* f) { r = make_float2(f[0], f[1]); }
 };
 
-// Streaming loads and stores: every element is used once.
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load(const T* p) {
-    Vec<T, V> v;
-    v.r = __ldcs(reinterpret_cast<const decltype(v.r)*>(p));
-    return v;
-}
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> peek(const char* p) {
     Vec<T, V> v;
@@ -179,9 +174,38 @@ template <typename T, int V>
 __device__ __forceinline__ void poke(char* p, const Vec<T, V>& v) {
     *reinterpret_cast<std::remove_const_t<decltype(v.r)>*>(p) = v.r;
 }
-template <typename T, int V>
-__device__ __forceinline__ void store(T* p, const Vec<T, V>& v) {
-    __stcs(reinterpret_cast<std::remove_const_t<decltype(v.r)>*>(p), v.r);
+// N adjacent elements as fp32; N = 4 takes aligned addresses.
+template <int N, typename T>
+__device__ __forceinline__ void load_n(const T* p, float* v) {
+    if constexpr (N == 1) {
+        v[0] = to_f32(*p);
+    } else if constexpr (sizeof(T) == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        v[0] = q.x;
+        v[1] = q.y;
+        v[2] = q.z;
+        v[3] = q.w;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        v[0] = __uint_as_float(q.x << 16);
+        v[1] = __uint_as_float(q.x & 0xffff0000u);
+        v[2] = __uint_as_float(q.y << 16);
+        v[3] = __uint_as_float(q.y & 0xffff0000u);
+    }
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_n(T* p, const float* v) {
+    if constexpr (N == 1) {
+        *p = from_f32<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        uint2 q;
+        q.x = *reinterpret_cast<const uint32_t*>(&a);
+        q.y = *reinterpret_cast<const uint32_t*>(&b);
+        *reinterpret_cast<uint2*>(p) = q;
+    }
 }
 
 // Asynchronous copies global -> shared memory; `bytes` < SIZE fills the rest
@@ -200,19 +224,43 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // A warp's K x ROWB block of rows `ld` bytes apart: rows first <= j < last,
 // columns below `width` bytes; the rest of the block becomes zeros (`safe`:
 // any valid address, named where nothing is read).  SIZE 16: lanes take
-// 16-byte pieces in order; SIZE 4: a lane takes 4-byte words 32 apart.
+// 16-byte pieces in order; SIZE 4: a lane takes 4-byte words 32 apart; SIZE 2:
+// 2-byte elements 32 apart, by plain loads.
 template <int SIZE, int ROWB, int K>
 struct Rows {
-    static constexpr int PER = ROWB / SIZE;                    // pieces per row
+    static constexpr int SIZE_ = SIZE;
+    static constexpr int PER = ROWB  / SIZE;                    // pieces per row
     static constexpr int RPI = PER >= 32 ? 1 : 32 / PER;       // rows per instruction
     static constexpr int CPR = PER >= 32 ? PER / 32 : 1;       // instructions per row
 };
 
 template <int SIZE, int ROWB, int K>
-__device__ __forceinline__ void rows_in(uint32_t dst, const void* safe, const char* src, long long ld, int first,
+__device__ __forceinline__ void rows_in(char* to, const void* safe, const char* src, long long ld, int first,
                                         int last, int width, int lane) {
-    using R = Rows<SIZE, ROWB, K>;
-    const int j0 = R::PER >= 32 ? 0 : lane / R::PER, col = (R::PER >= 32 ? lane : lane % R::PER) * SIZE;
+    using R = Rows<SIZE < 4 ? 4 : SIZE, ROWB, K>;
+    if constexpr (SIZE == 2) {
+        // by element, in two batches of loads
+#pragma unroll
+        for (int h = 0; h < K; h += K / 2) {
+            uint16_t v[K / 2][ROWB / 64];
+#pragma unroll
+            for (int i = 0; i < K / 2; ++i)
+#pragma unroll
+                for (int q = 0; q < ROWB / 64; ++q) {
+                    const int j = h + i, col = (q * 32 + lane) * 2;
+                    const bool ok = j >= first && j < last && col < width;
+                    v[i][q] = ok ? *reinterpret_cast<const uint16_t*>(src + j * ld + col) : uint16_t(0);
+                }
+#pragma unroll
+            for (int i = 0; i < K / 2; ++i)
+#pragma unroll
+                for (int q = 0; q < ROWB / 64; ++q)
+                    *reinterpret_cast<uint16_t*>(to + (h + i) * ROWB + (q * 32 + lane) * 2) = v[i][q];
+        }
+        return;
+    }
+    uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    const int j0 = R::PER >= 32 ? 0 : lane / R::PER, col = (R::PER >= 32 ? lane : lane % R::PER) * R::SIZE_;
     const char* p = src + j0 * ld + col;
     dst += j0 * ROWB + col;
     if (first <= 0 && last >= K && width >= ROWB) {            // (the warp as one)
@@ -220,7 +268,7 @@ __device__ __forceinline__ void rows_in(uint32_t dst, const void* safe, const ch
         for (int i = 0; i < K / R::RPI; ++i) {
 #pragma unroll
             for (int q = 0; q < R::CPR; ++q)
-                copy_async<SIZE>(dst + i * R::RPI * ROWB + q * 32 * SIZE, p + q * 32 * SIZE, SIZE);
+                copy_async<SIZE < 4 ? 4 : SIZE>(dst + i * R::RPI * ROWB + q * 32 * R::SIZE_, p + q * 32 * R::SIZE_, R::SIZE_);
             p += R::RPI * ld;
         }
     } else {
@@ -229,8 +277,8 @@ __device__ __forceinline__ void rows_in(uint32_t dst, const void* safe, const ch
             const int j = j0 + i * R::RPI;
 #pragma unroll
             for (int q = 0; q < R::CPR; ++q) {
-                const bool ok = j >= first && j < last && col + q * 32 * SIZE < width;
-                copy_async<SIZE>(dst + i * R::RPI * ROWB + q * 32 * SIZE, ok ? p + q * 32 * SIZE : safe, ok ? SIZE : 0);
+                const bool ok = j >= first && j < last && col + q * 32 * R::SIZE_ < width;
+                copy_async<SIZE < 4 ? 4 : SIZE>(dst + i * R::RPI * ROWB + q * 32 * R::SIZE_, ok ? p + q * 32 * R::SIZE_ : safe, ok ? R::SIZE_ : 0);
             }
             p += R::RPI * ld;
         }

@@ -14,17 +14,24 @@
 // each, 128 bytes a warp) and every warp owns K consecutive tokens of a tile
 // of NW * K.  A warp composes its tokens from a zero state (the affine map
 // h -> alpha h + s of its span), the warps' maps are folded through shared
-// memory, and a second pass over the tokens, still in registers, writes the
-// states.  So every element is read once and written once, and HBM bounds the
-// kernel: 6 bytes per element forward (bf16), 10 backward.
+// memory, and a second pass over the tokens writes the states.  So every
+// element is read once and written once, and HBM bounds the kernel: 6 bytes
+// per element forward (bf16), 10 backward.
 //
 // One CTA walks one sequence of one slab of channels, tile after tile, the
-// next tile's loads in flight.  Where that makes too few CTAs a cluster of S
-// of them takes S consecutive tiles per round: each CTA sends its tile's map
-// to all others' shared memory and one cluster barrier later every CTA knows
-// the state before its tile and before the next round.  The composition's
-// order is fixed, so results do not depend on the schedule.
+// rows of the next tiles on their way.  Where that makes too few CTAs a
+// cluster of S of them takes S consecutive tiles per round: each CTA sends
+// its tile's map to all others' shared memory, and every CTA then knows the
+// state before its tile and before the next round.  Where even clusters leave
+// SMs free (a long sequence of few channels) the tokens are cut into parts;
+// a first kernel takes maps of 512 tokens, a second read of two tensors.
+// The order of composition is fixed, so results do not depend on the
+// schedule.
+#include <cfloat>
+#include <map>
+#include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "gated_device.cuh"
 #include "kdn_device.cuh"
@@ -36,38 +43,59 @@ namespace {
 
 using namespace gated;
 
-constexpr int MAX_CLUSTER = 8;
-constexpr int THREADS = 256;      // of the kernels without tiles
-constexpr int FWD_WARPS = 8, BWD_WARPS = 8;
+constexpr int MAX_CLUSTER = 8, MAX_PARTS = 16;
+constexpr int NW = 8;             // warps per CTA
+constexpr int FWD_K = 16, BWD_K = 8;
+constexpr int STAGES = 2;
+constexpr int MAP_TOKENS = 512;   // of one map where a sequence is cut into parts
 
 __device__ int g_gated_error = 0;
 
-// The tokens of state row n*H + h (a batch, or a packed sequence): [lo, hi)
-// of the T-token row `row`.
-struct Span {
-    long long row;
-    int lo, hi;
-};
-
-__device__ __forceinline__ Span span_of(const GatedArgs& p, long long sr) {
-    Span s{sr, 0, p.T};
-    if (p.offsets) {
-        const long long n = sr / p.H;
-        s.row = sr - n * p.H;
-        s.lo = min(max(p.offsets[n], 0), p.T);
-        s.hi = min(max(p.offsets[n + 1], s.lo), p.T);
-    }
-    return s;
-}
-
-// How one call is cut: slabs of 32 V channels, clusters of S CTAs.
+// How one call is cut: slabs of 32 V channels, clusters of S CTAs, parts of
+// `len` tokens (one part: the sequence).
 struct Cut {
-    int slabs, S;
+    int slabs, S, parts, len;
+    const float4* maps;    // [state row, T / MAP_TOKENS, C]: {a, e, s, z}
     long long wait_ns;     // limit of one wait inside a cluster
 };
 
+// A warp's place: its channels, its part's tokens [lo, hi) of the T-token row
+// `row`, the sequence's first token, and the rounds of its CTA.
+template <int V, int K>
+struct Place {
+    int warp, lane, S, rank, part, c0, c, lo, hi, begin, rounds;
+    long long sr, row;     // state row n*H + h, row of the tensors
+
+    __device__ __forceinline__ Place(const GatedArgs& p, const Cut& cut) {
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
+        S = cut.S;
+        rank = static_cast<int>(blockIdx.x % S);
+        const long long unit = blockIdx.x / S, u = unit / cut.slabs;
+        c0 = static_cast<int>(unit - u * cut.slabs) * 32 * V;
+        c = c0 + lane * V;
+        sr = u / cut.parts;
+        part = static_cast<int>(u - sr * cut.parts);
+        row = sr;
+        lo = 0;
+        hi = p.T;
+        if (p.offsets) {
+            const long long n = sr / p.H;
+            row = sr - n * p.H;
+            lo = min(max(p.offsets[n], 0), p.T);
+            hi = min(max(p.offsets[n + 1], lo), p.T);
+        }
+        begin = lo;
+        if (cut.parts > 1) {
+            lo = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(part) * cut.len));
+            hi = static_cast<int>(min(static_cast<long long>(hi), static_cast<long long>(lo) + cut.len));
+        }
+        rounds = (hi - lo + S * NW * K - 1) / (S * NW * K);
+    }
+};
+
 // An affine map h -> (a + e) h + s of a lane's V channels over a span of
-// tokens, z its exponent (a + e = exp(z)), as shared-memory words that one
+// tokens, z its exponent (a + e = 2^z), as shared-memory words that one
 // 16-byte access per channel moves: {a, e, s, z}, or {a0, a1, e0, e1} and
 // {s0, s1, z0, z1}.
 template <int V>
@@ -152,7 +180,7 @@ __device__ __forceinline__ void cluster_sync() {
 // time).  A CTA sends round r only after all its warps have read round r - 2,
 // and receives all of round r - 1 before it sends round r, so no store finds
 // its buffer in use.
-template <int V, int NW>
+template <int V>
 struct Fold {
     MapWords<V> warp[2][NW];
     MapWords<V> cta[2][MAX_CLUSTER];
@@ -216,16 +244,22 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
     return r;
 }
 
-template <int V, int NW>
-__device__ __forceinline__ void fold_round(Fold<V, NW>& f, int r, int S, int rank, int warp, int lane,
-                                           long long limit_ns, bool& late, const float (&z)[V], const float (&s)[V],
-                                           float (&carry)[V], float (&start)[V]) {
+__device__ __forceinline__ float from_rank(const float* p, int rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at_rank(p, rank)) : "memory");
+    return v;
+}
+
+template <int V>
+__device__ __forceinline__ void fold_round(Fold<V>& f, int r, int S, int rank, int warp, int lane, long long limit_ns,
+                                           bool& late, const float (&z)[V], const float (&s)[V], float (&carry)[V],
+                                           float (&start)[V]) {
     const int buf = r & 1;
     put_map<V>(f.warp[buf][warp], lane, map_of<V>(z, s));
     __syncthreads();
     if (S > 1) {
         if (threadIdx.x == 0) mbar_arrive_expect_tx(&f.full[buf], S * sizeof(MapWords<V>));
-        if (warp < S) {
+        if (warp < S) {   // warp j sends the tile's map to CTA j
             float h[V], zz[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = zz[v] = 0.f;
@@ -237,14 +271,12 @@ __device__ __forceinline__ void fold_round(Fold<V, NW>& f, int r, int S, int ran
                 for (int v = 0; v < V; ++v) zz[v] += m.z[v];
             }
             const Map<V> m = map_of<V>(zz, h);
-            for (int j = warp; j < S; j += NW) {
-                const uint32_t to = at_rank(&f.cta[buf][rank][0][lane], j), bar = at_rank(&f.full[buf], j);
-                if constexpr (V == 1) {
-                    send(to, make_float4(m.a[0], m.e[0], m.s[0], m.z[0]), bar);
-                } else {
-                    send(to, make_float4(m.a[0], m.a[1], m.e[0], m.e[1]), bar);
-                    send(to + 512, make_float4(m.s[0], m.s[1], m.z[0], m.z[1]), bar);
-                }
+            const uint32_t to = at_rank(&f.cta[buf][rank][0][lane], warp), bar = at_rank(&f.full[buf], warp);
+            if constexpr (V == 1) {
+                send(to, make_float4(m.a[0], m.e[0], m.s[0], m.z[0]), bar);
+            } else {
+                send(to, make_float4(m.a[0], m.a[1], m.e[0], m.e[1]), bar);
+                send(to + 512, make_float4(m.s[0], m.s[1], m.z[0], m.z[1]), bar);
             }
         }
         full_wait(&f.full[buf], (r >> 1) & 1, limit_ns, late);
@@ -267,313 +299,108 @@ __device__ __forceinline__ void fold_round(Fold<V, NW>& f, int r, int S, int ran
         }
     }
 }
+static_assert(MAX_CLUSTER <= NW, "a warp sends to one CTA");
+static_assert(MAX_CLUSTER * NW * BWD_K % MAP_TOKENS == 0 && MAX_CLUSTER * NW * FWD_K % MAP_TOKENS == 0, "parts are whole maps");
 
-template <typename TI, typename TO, int V, int K, int NW, bool LEAK>
-__global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_kernel(const GatedArgs p, const Cut cut) {
-    __shared__ Fold<V, NW> fold;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = cut.S, rank = blockIdx.x % S;
-    const long long unit = blockIdx.x / S;
-    const long long sr = unit / cut.slabs;
-    const int c = (static_cast<int>(unit - sr * cut.slabs) * 32 + lane) * V;
-    const bool on = c < p.C;
-    const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
-    const long long arow = (sr % p.H) * p.C;
-
-    float nA[V], carry[V];
+// The state that a part starts from: the sequence's carry through the maps of
+// the tokens before the part (those after it, backward).  Each warp composes
+// a share of the maps; all fold the shares.
+template <int V, bool BWD>
+__device__ __forceinline__ void through_parts(const GatedArgs& p, const Cut& cut, Fold<V>& f, long long sr, int part,
+                                              int warp, int lane, int c, float (&carry)[V]) {
+    if (cut.parts == 1) return;
+    const int all = (p.T + MAP_TOKENS - 1) / MAP_TOKENS, edge = (part + (BWD ? 1 : 0)) * (cut.len / MAP_TOKENS);
+    const int n = BWD ? max(all - edge, 0) : edge, share = (n + NW - 1) / NW;
+    float z[V], s[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        nA[v] = on ? -p.A[arow + c + v] : 0.f;
-        carry[v] = on && p.h0 ? p.h0[sr * p.C + c + v] : 0.f;
-    }
-    const TI* xp = static_cast<const TI*>(p.x) + sp.row * p.T * p.x_ld + c;
-    const TI* dp = static_cast<const TI*>(p.d) + sp.row * p.T * p.d_ld + c;
-    TO* op = static_cast<TO*>(p.out) + sp.row * p.T * p.C + c;
-
-    Vec<TI, V> xr[K], dr[K];
-    auto fetch = [&](int r) {
-        const int t = sp.lo + ((r * S + rank) * NW + warp) * K;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            xr[k] = Vec<TI, V>{};
-            dr[k] = Vec<TI, V>{};
-            if (on && t + k < sp.hi) {
-                xr[k] = load<TI, V>(xp + static_cast<long long>(t + k) * p.x_ld);
-                dr[k] = load<TI, V>(dp + static_cast<long long>(t + k) * p.d_ld);
-            }
-        }
-    };
-    if (rounds > 0) fetch(0);
-    fold.begin(S);
-    bool late = false;
-    for (int r = 0; r < rounds; ++r) {
-        const int t = sp.lo + ((r * S + rank) * NW + warp) * K;
-        // tokens behind the end have d = x = 0: alpha = 1, nothing added
-        float a[K][V], b[K][V], z[V], s[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
-#pragma unroll
-        for (int i = 0; i < K * V / 2; ++i) {
-            const int k0 = 2 * i / V, v0 = 2 * i % V, k1 = (2 * i + 1) / V, v1 = (2 * i + 1) % V;
-            const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{dr[k0].get(v0), dr[k1].get(v1)});
-            const Gate2 gg = gate2<LEAK>(zz);
-            a[k0][v0] = gg.a.x;
-            a[k1][v1] = gg.a.y;
-            F2 x{xr[k0].get(v0), xr[k1].get(v1)};
-            if (LEAK) x = mul2(x, gg.w);
-            b[k0][v0] = x.x;
-            b[k1][v1] = x.y;
-            if (V == 1) {
-                z[0] += zz.x + zz.y;
-                s[0] = fmaf(gg.a.x, s[0], x.x);
-                s[0] = fmaf(gg.a.y, s[0], x.y);
-            } else {
-                const F2 ss{s[v0], s[v1]};
-                const F2 n = fma2(gg.a, ss, x), zs = add2(F2{z[v0], z[v1]}, zz);
-                s[v0] = n.x;
-                s[v1] = n.y;
-                z[v0] = zs.x;
-                z[v1] = zs.y;
-            }
-        }
-        if (r + 1 < rounds) fetch(r + 1);
-        float h[V];
-        fold_round<V, NW>(fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, h);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (V == 1) {
-                h[0] = fmaf(a[k][0], h[0], b[k][0]);
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; v += 2) {
-                    const F2 hh{h[v], h[v + 1]};
-                    const F2 n = fma2(F2{a[k][v], a[k][v + 1]}, hh, F2{b[k][v], b[k][v + 1]});
-                    h[v] = n.x;
-                    h[v + 1] = n.y;
-                }
-            }
-            if (on && t + k < sp.hi) {
-                Vec<TO, V> o;
-                o.set(h);
-                store<TO, V>(op + static_cast<long long>(t + k) * p.C, o);
-            }
+        z[v] = s[v] = 0.f;
+        if (c + v >= p.C) continue;
+        const float4* m = cut.maps + sr * all * p.C + c + v;
+#pragma unroll 8
+        for (int i = warp * share; i < min(n, (warp + 1) * share); ++i) {
+            const float4 q = m[static_cast<long long>(BWD ? all - 1 - i : i) * p.C];
+            s[v] = decay_add(q.x, q.y, s[v], q.z);
+            z[v] += q.w;
         }
     }
-    fold.end(S, late);
-    if (p.final_state && rank == 0 && warp == 0 && on)
+    put_map<V>(f.warp[0][warp], lane, map_of<V>(z, s));
+    __syncthreads();
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.final_state[sr * p.C + c + v] = carry[v];
+    for (int w = 0; w < NW; ++w) apply<V>(get_map<V>(f.warp[0][w], lane), carry);
+    __syncthreads();
 }
 
-// The same walk from the last token to the first.  `part` [sequence, rank,
-// H, C] takes each CTA's share of grad A.
-template <typename TI, typename TO, int V, int K, int NW, bool LEAK>
-__global__ void __launch_bounds__(NW * 32, 16 / NW)
-gated_bwd_kernel(const GatedArgs p, const Cut cut, float* part) {
-    __shared__ Fold<V, NW> fold;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = cut.S, rank = blockIdx.x % S;
-    const long long unit = blockIdx.x / S;
-    const long long sr = unit / cut.slabs;
-    const int c = (static_cast<int>(unit - sr * cut.slabs) * 32 + lane) * V;
-    const bool on = c < p.C;
-    const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
-    const long long arow = (sr % p.H) * p.C;
-
-    float nA[V], carry[V], dA[V], first[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        nA[v] = on ? -p.A[arow + c + v] : 0.f;
-        carry[v] = on && p.grad_final_state ? p.grad_final_state[sr * p.C + c + v] : 0.f;
-        first[v] = on && p.h0 ? p.h0[sr * p.C + c + v] : 0.f;
-        dA[v] = 0.f;
-    }
-    const TI* dp = static_cast<const TI*>(p.d) + sp.row * p.T * p.d_ld + c;
-    const TI* xp = LEAK ? static_cast<const TI*>(p.x) + sp.row * p.T * p.x_ld + c : nullptr;
-    const long long row = sp.row * p.T * p.C + c;
-    const TO* hp = static_cast<const TO*>(p.out) + row;
-    const TO* gp = static_cast<const TO*>(p.grad_out) + row;
-    TI* gxp = static_cast<TI*>(p.grad_x) + row;
-    TI* gdp = static_cast<TI*>(p.grad_d) + row;
-
-    Vec<TI, V> dn[K];
-    Vec<TO, V> gn[K];
-    auto fetch = [&](int r) {
-        const int t = sp.hi - 1 - ((r * S + rank) * NW + warp) * K;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            dn[k] = Vec<TI, V>{};
-            gn[k] = Vec<TO, V>{};
-            if (on && t - k >= sp.lo) {
-                dn[k] = load<TI, V>(dp + static_cast<long long>(t - k) * p.d_ld);
-                gn[k] = load<TO, V>(gp + static_cast<long long>(t - k) * p.C);
-            }
-        }
-    };
-    if (rounds > 0) fetch(0);
-    fold.begin(S);
-    bool late = false;
-    for (int r = 0; r < rounds; ++r) {
-        const int t = sp.hi - 1 - ((r * S + rank) * NW + warp) * K;
-        Vec<TO, V> hr[K];
-        Vec<TI, V> xr[K], dr[K];
-        Vec<TO, V> gr[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            hr[k] = Vec<TO, V>{};
-            xr[k] = Vec<TI, V>{};
-            if (on && t - k > sp.lo) hr[k] = load<TO, V>(hp + static_cast<long long>(t - k - 1) * p.C);
-            if (LEAK && on && t - k >= sp.lo) xr[k] = load<TI, V>(xp + static_cast<long long>(t - k) * p.x_ld);
-            dr[k] = dn[k];
-            gr[k] = gn[k];
-        }
-        float a[K][V], z[V], s[V], w[LEAK ? K : 1][V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) z[v] = s[v] = 0.f;
-        // u = alpha (g + u): the map of a token is (alpha, alpha g)
-#pragma unroll
-        for (int i = 0; i < K * V / 2; ++i) {
-            const int k0 = 2 * i / V, v0 = 2 * i % V, k1 = (2 * i + 1) / V, v1 = (2 * i + 1) % V;
-            const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{dr[k0].get(v0), dr[k1].get(v1)});
-            const Gate2 gg = gate2<LEAK>(zz);
-            a[k0][v0] = gg.a.x;
-            a[k1][v1] = gg.a.y;
-            if (LEAK) {
-                w[LEAK ? k0 : 0][v0] = gg.w.x;
-                w[LEAK ? k1 : 0][v1] = gg.w.y;
-            }
-            if (V == 1) {
-                z[0] += zz.x + zz.y;
-                const float d0 = s[0] + gr[k0].get(0);
-                s[0] = gg.a.x * d0;
-                const float d1 = s[0] + gr[k1].get(0);
-                s[0] = gg.a.y * d1;
-            } else {
-                const F2 dh = add2(F2{s[v0], s[v1]}, F2{gr[k0].get(v0), gr[k0].get(v1)});
-                const F2 n = mul2(gg.a, dh), zs = add2(F2{z[v0], z[v1]}, zz);
-                s[v0] = n.x;
-                s[v1] = n.y;
-                z[v0] = zs.x;
-                z[v1] = zs.y;
-            }
-        }
-        if (r + 1 < rounds) fetch(r + 1);
-        float u[V];
-        fold_round<V, NW>(fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, u);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float gx[V], gd[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float dh = u[v] + gr[k].get(v);
-                u[v] = a[k][v] * dh;
-                float prev = t - k > sp.lo ? hr[k].get(v) : first[v];
-                gx[v] = dh;
-                if (LEAK) {
-                    prev -= xr[k].get(v);
-                    gx[v] = w[LEAK ? k : 0][v] * dh;
-                }
-                const float m = u[v] * prev;
-                gd[v] = nA[v] * m;
-                if (t - k >= sp.lo) dA[v] = fmaf(-dr[k].get(v), m, dA[v]);
-            }
-            if (on && t - k >= sp.lo) {
-                Vec<TI, V> o;
-                o.set(gx);
-                store<TI, V>(gxp + static_cast<long long>(t - k) * p.C, o);
-                o.set(gd);
-                store<TI, V>(gdp + static_cast<long long>(t - k) * p.C, o);
-            }
-        }
-    }
-    fold.end(S, late);
-    if (p.grad_h0 && rank == 0 && warp == 0 && on)
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.grad_h0[sr * p.C + c + v] = carry[v];
-    if (part) {
-        // the warps' shares, in order
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; ++v) fold.warp[0][warp][v][lane].x = dA[v];
-        __syncthreads();
-        if (warp == 0 && on)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float sum = 0.f;
-                for (int w = 0; w < NW; ++w) sum += fold.warp[0][w][v][lane].x;
-                part[((sr / p.H * S + rank) * p.H + sr % p.H) * p.C + c + v] = sum;
-            }
-    }
-}
-
-// The staged form: a warp's rows come through shared memory, STAGES rounds
-// ahead by asynchronous copies of SIZE bytes that fill what lies outside the
-// sequence or the channels with zeros, and with SIZE = 16 leave through it
-// too, in 16-byte pieces (a 4-byte SIZE takes rows that are only aligned to
-// that, and stores straight from the registers).  A warp reads only rows that
-// it copied itself, so no barrier beyond the fold's is needed.
-constexpr int STAGES = 2;
-
-template <typename TI, typename TO, int V, int K, int NW>
+// A warp's rows come through shared memory, STAGES rounds ahead: by
+// asynchronous copies of SIZE = 16 or 4 bytes, whichever the tensors' rows
+// allow, or, for rows of an odd number of bf16, by element (SIZE = 2, not
+// asynchronous); what lies outside the sequence or the channels becomes
+// zeros (d = x = 0: alpha = 1, nothing added).  With SIZE = 16 results leave
+// through shared memory too, in 16-byte pieces, else straight from the
+// registers.  A warp reads only rows that it copied itself, so no barrier
+// beyond the fold's is needed.
+//
+// 16-byte pieces matter: single loads and stores of a lane's channels, with
+// their addresses and predicates, were half of all instructions (8 x 4096 x
+// 2048 bf16: 212 us, against 117 us in pieces).
+template <typename TI, typename TO, int V, int K>
 struct FwdShared {
     static constexpr int ROW = 32 * V * static_cast<int>(sizeof(TI)), OROW = 32 * V * static_cast<int>(sizeof(TO));
     struct __align__(16) Stage {
         char x[K * ROW], d[K * ROW];                 // out overwrites both
     };
     Stage st[STAGES][NW];
-    Fold<V, NW> fold;
+    Fold<V> fold;
 };
 
-template <typename TI, typename TO, int V, int K, int NW, bool LEAK, int SIZE>
-__global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_staged(const GatedArgs p, const Cut cut) {
-    using Sh = FwdShared<TI, TO, V, K, NW>;
+// Measured (GB300; 16-bit in and out, 134 M elements, 805 MB, where 118 us is
+// the copy's rate): as 16 x 4096 x 2048 160 us, 4 x 16384 x 2048 (clusters of
+// 2) 167 us, 1 x 65536 x 2048 (clusters of 8) 231 us; 2 CTAs per SM (128
+// registers), 24 instructions per element.
+template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
+__global__ void __launch_bounds__(NW * 32, 2)
+gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cut cut) {
+    using Sh = FwdShared<TI, TO, V, K>;
     static_assert(Sh::OROW * K <= static_cast<int>(sizeof(typename Sh::Stage)), "out takes the stage's place");
     extern __shared__ __align__(16) char smem[];
     Sh& sh = *reinterpret_cast<Sh*>(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = cut.S, rank = blockIdx.x % S;
-    const long long unit = blockIdx.x / S;
-    const long long sr = unit / cut.slabs;
-    const int c0 = static_cast<int>(unit - sr * cut.slabs) * 32 * V, c = c0 + lane * V;
-    const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
-    const long long arow = (sr % p.H) * p.C;
+    const Place<V, K> at(p, cut);
+    const int lane = at.lane, c = at.c;
+    const long long arow = (at.sr % p.H) * p.C;
 
-    float nA[V], carry[V];
+    float rate[V], carry[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        nA[v] = c + v < p.C ? -p.A[arow + c + v] : 0.f;
-        carry[v] = c + v < p.C && p.h0 ? p.h0[sr * p.C + c + v] : 0.f;
+        rate[v] = c + v < p.C ? -LOG2E * p.A[arow + c + v] : 0.f;
+        carry[v] = c + v < p.C && p.h0 ? p.h0[at.sr * p.C + c + v] : 0.f;
     }
-    const int t0 = sp.lo + (rank * NW + warp) * K, step = S * NW * K;
+    const int t0 = at.lo + (at.rank * NW + at.warp) * K, step = at.S * NW * K;
     const long long xld = p.x_ld * sizeof(TI), dld = p.d_ld * sizeof(TI);
-    const char* xp = static_cast<const char*>(p.x) + (sp.row * p.T + t0) * xld + c0 * sizeof(TI);
-    const char* dp = static_cast<const char*>(p.d) + (sp.row * p.T + t0) * dld + c0 * sizeof(TI);
-    TO* op = static_cast<TO*>(p.out) + (sp.row * p.T + t0) * p.C + c0;
-    const int width = (p.C - c0) * static_cast<int>(sizeof(TI)), owidth = (p.C - c0) * static_cast<int>(sizeof(TO));
+    const char* xp = static_cast<const char*>(p.x) + (at.row * p.T + t0) * xld + at.c0 * sizeof(TI);
+    const char* dp = static_cast<const char*>(p.d) + (at.row * p.T + t0) * dld + at.c0 * sizeof(TI);
+    TO* op = static_cast<TO*>(p.out) + (at.row * p.T + t0) * p.C + at.c0;
+    const int width = (p.C - at.c0) * static_cast<int>(sizeof(TI)), owidth = (p.C - at.c0) * static_cast<int>(sizeof(TO));
 
     auto fetch = [&](int r) {
-        const int n = sp.hi - t0 - r * step;               // tokens left
+        const int n = at.hi - t0 - r * step;               // tokens left
         if (n > 0) {
-            typename Sh::Stage& st = sh.st[r % STAGES][warp];
-            const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(st.x));
-            rows_in<SIZE, Sh::ROW, K>(sm, p.x, xp + static_cast<long long>(r) * step * xld, xld, 0, n, width, lane);
-            rows_in<SIZE, Sh::ROW, K>(sm + K * Sh::ROW, p.d, dp + static_cast<long long>(r) * step * dld, dld, 0, n, width, lane);
+            typename Sh::Stage& st = sh.st[r % STAGES][at.warp];
+            rows_in<SIZE, Sh::ROW, K>(st.x, p.x, xp + static_cast<long long>(r) * step * xld, xld, 0, n, width, lane);
+            rows_in<SIZE, Sh::ROW, K>(st.d, p.d, dp + static_cast<long long>(r) * step * dld, dld, 0, n, width, lane);
         }
         copy_commit();
     };
 #pragma unroll
     for (int i = 0; i < STAGES; ++i)
-        if (i < rounds) fetch(i);
+        if (i < at.rounds) fetch(i);
         else copy_commit();
-    sh.fold.begin(S);
+    through_parts<V, false>(p, cut, sh.fold, at.sr, at.part, at.warp, lane, c, carry);
+    sh.fold.begin(at.S);
     bool late = false;
-    for (int r = 0; r < rounds; ++r) {
-        const int n = sp.hi - t0 - r * step;
-        char* xs = sh.st[r % STAGES][warp].x;
-        const char* ds = sh.st[r % STAGES][warp].d;
+    for (int r = 0; r < at.rounds; ++r) {
+        const int n = at.hi - t0 - r * step;
+        char* xs = sh.st[r % STAGES][at.warp].x;
+        const char* ds = sh.st[r % STAGES][at.warp].d;
         copy_wait<STAGES - 1>();
         __syncwarp();
         float a[K][V], b[K][V], z[V], s[V], h[V];
@@ -582,6 +409,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_staged(const Gated
         if (n > 0) {                                        // (the warp as one)
 #pragma unroll
             for (int i = 0; i < K * V / 2; ++i) {
+                // two channels of a token, or (V = 1) two tokens of a channel
                 const int k0 = 2 * i / V, v0 = 2 * i % V, k1 = (2 * i + 1) / V, v1 = (2 * i + 1) % V;
                 const Vec<TI, V> d0 = peek<TI, V>(ds + k0 * Sh::ROW + lane * V * sizeof(TI)),
                                  x0 = peek<TI, V>(xs + k0 * Sh::ROW + lane * V * sizeof(TI));
@@ -590,21 +418,19 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_staged(const Gated
                     d1 = peek<TI, V>(ds + k1 * Sh::ROW + lane * V * sizeof(TI));
                     x1 = peek<TI, V>(xs + k1 * Sh::ROW + lane * V * sizeof(TI));
                 }
-                const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{d0.get(v0), d1.get(v1)});
+                const F2 zz = mul2(F2{rate[v0], rate[v1]}, F2{d0.get(v0), d1.get(v1)});
                 const Gate2 gg = gate2<LEAK>(zz);
-                a[k0][v0] = gg.a.x;
-                a[k1][v1] = gg.a.y;
                 F2 x{x0.get(v0), x1.get(v1)};
                 if (LEAK) x = mul2(x, gg.w);
+                a[k0][v0] = gg.a.x;
+                a[k1][v1] = gg.a.y;
                 b[k0][v0] = x.x;
                 b[k1][v1] = x.y;
                 if constexpr (V == 1) {
                     z[0] += zz.x + zz.y;
-                    s[0] = fmaf(gg.a.x, s[0], x.x);
-                    s[0] = fmaf(gg.a.y, s[0], x.y);
+                    s[0] = fmaf(gg.a.y, fmaf(gg.a.x, s[0], x.x), x.y);
                 } else {
-                    const F2 ss{s[0], s[1]};
-                    const F2 m = fma2(gg.a, ss, x), zs = add2(F2{z[0], z[1]}, zz);
+                    const F2 m = fma2(gg.a, F2{s[0], s[1]}, x), zs = add2(F2{z[0], z[1]}, zz);
                     s[0] = m.x;
                     s[1] = m.y;
                     z[0] = zs.x;
@@ -612,7 +438,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_staged(const Gated
                 }
             }
         }
-        fold_round<V, NW>(sh.fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, h);
+        fold_round<V>(sh.fold, r, at.S, at.rank, at.warp, lane, cut.wait_ns, late, z, s, carry, h);
         if (n > 0) {
             TO* o = op + static_cast<long long>(r) * step * p.C;
 #pragma unroll
@@ -620,8 +446,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_staged(const Gated
                 if constexpr (V == 1) {
                     h[0] = fmaf(a[k][0], h[0], b[k][0]);
                 } else {
-                    const F2 hh{h[0], h[1]};
-                    const F2 m = fma2(F2{a[k][0], a[k][1]}, hh, F2{b[k][0], b[k][1]});
+                    const F2 m = fma2(F2{a[k][0], a[k][1]}, F2{h[0], h[1]}, F2{b[k][0], b[k][1]});
                     h[0] = m.x;
                     h[1] = m.y;
                 }
@@ -642,86 +467,86 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) gated_fwd_staged(const Gated
                 __syncwarp();
             }
         }
-        if (r + STAGES < rounds) fetch(r + STAGES);
+        if (r + STAGES < at.rounds) fetch(r + STAGES);
         else copy_commit();
     }
-    sh.fold.end(S, late);
-    if (p.final_state && rank == 0 && warp == 0)
+    sh.fold.end(at.S, late);
+    if (p.final_state && at.rank == 0 && at.warp == 0 && at.part == cut.parts - 1)
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (c + v < p.C) p.final_state[sr * p.C + c + v] = carry[v];
+            if (c + v < p.C) p.final_state[at.sr * p.C + c + v] = carry[v];
 }
 
-template <typename TI, typename TO, int V, int K, int NW>
+template <typename TI, typename TO, int V, int K>
 struct BwdShared {
     static constexpr int ROW = 32 * V * static_cast<int>(sizeof(TI)), OROW = 32 * V * static_cast<int>(sizeof(TO));
     struct __align__(16) Stage {
         char d[K * ROW], x[K * ROW], g[K * OROW], h[K * OROW];   // grad d overwrites d, grad x x
     };
     Stage st[STAGES][NW];
-    Fold<V, NW> fold;
+    Fold<V> fold;
+    float dA[V][32];
 };
 
-template <typename TI, typename TO, int V, int K, int NW, bool LEAK, int SIZE>
-__global__ void __launch_bounds__(NW * 32, 16 / NW)
-gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
-    using Sh = BwdShared<TI, TO, V, K, NW>;
+// The same walk from the last token to the first.  `sums` [sequence, part, H,
+// C] takes the shares of grad A (the sums themselves where there is one).
+template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
+__global__ void __launch_bounds__(NW * 32, 2)
+gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cut cut, float* sums) {
+    using Sh = BwdShared<TI, TO, V, K>;
     extern __shared__ __align__(16) char smem[];
     Sh& sh = *reinterpret_cast<Sh*>(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = cut.S, rank = blockIdx.x % S;
-    const long long unit = blockIdx.x / S;
-    const long long sr = unit / cut.slabs;
-    const int c0 = static_cast<int>(unit - sr * cut.slabs) * 32 * V, c = c0 + lane * V;
-    const Span sp = span_of(p, sr);
-    const int rounds = (sp.hi - sp.lo + S * NW * K - 1) / (S * NW * K);
-    const long long arow = (sr % p.H) * p.C;
+    const Place<V, K> at(p, cut);
+    const int lane = at.lane, c = at.c;
+    const long long arow = (at.sr % p.H) * p.C;
 
-    float nA[V], carry[V], dA[V], first[V];
+    float nA[V], rate[V], carry[V], dA[V], first[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const bool on = c + v < p.C;
         nA[v] = on ? -p.A[arow + c + v] : 0.f;
-        carry[v] = on && p.grad_final_state ? p.grad_final_state[sr * p.C + c + v] : 0.f;
-        first[v] = on && p.h0 ? p.h0[sr * p.C + c + v] : 0.f;
+        rate[v] = LOG2E * nA[v];
+        carry[v] = on && p.grad_final_state ? p.grad_final_state[at.sr * p.C + c + v] : 0.f;
+        first[v] = on && p.h0 ? p.h0[at.sr * p.C + c + v] : 0.f;
         dA[v] = 0.f;
     }
     // a warp's rows of round r are tokens base - r step .. + K - 1, walked from the last
-    const int base = sp.hi - (rank * NW + warp + 1) * K, step = S * NW * K;
-    const long long dld = p.d_ld * sizeof(TI), xld = p.x_ld * sizeof(TI), old_ = p.C * static_cast<long long>(sizeof(TO));
-    const long long row = sp.row * p.T;
-    const int width = (p.C - c0) * static_cast<int>(sizeof(TI)), owidth = (p.C - c0) * static_cast<int>(sizeof(TO));
+    const int base = at.hi - (at.rank * NW + at.warp + 1) * K, step = at.S * NW * K;
+    const long long dld = p.d_ld * sizeof(TI), xld = p.x_ld * sizeof(TI), tld = p.C * static_cast<long long>(sizeof(TO));
+    const long long row = at.row * p.T;
+    const int width = (p.C - at.c0) * static_cast<int>(sizeof(TI)), owidth = (p.C - at.c0) * static_cast<int>(sizeof(TO));
 
     auto fetch = [&](int r) {
         const int t = base - r * step;
-        if (t + K > sp.lo) {
-            typename Sh::Stage& st = sh.st[r % STAGES][warp];
-            const int f = max(sp.lo - t, 0);               // rows before the sequence
-            const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(st.d));
-            constexpr int N = K * Sh::ROW, M = K * Sh::OROW;
-            rows_in<SIZE, Sh::ROW, K>(sm, p.d, static_cast<const char*>(p.d) + (row + t) * dld + c0 * sizeof(TI), dld, f, K,
-                                      width, lane);
+        if (t + K > at.lo) {
+            typename Sh::Stage& st = sh.st[r % STAGES][at.warp];
+            const int f = max(at.lo - t, 0);               // rows before the part
+            rows_in<SIZE, Sh::ROW, K>(st.d, p.d, static_cast<const char*>(p.d) + (row + t) * dld + at.c0 * sizeof(TI), dld,
+                                      f, K, width, lane);
             if (LEAK)
-                rows_in<SIZE, Sh::ROW, K>(sm + N, p.x, static_cast<const char*>(p.x) + (row + t) * xld + c0 * sizeof(TI), xld,
-                                          f, K, width, lane);
-            rows_in<SIZE, Sh::OROW, K>(sm + 2 * N, p.grad_out, static_cast<const char*>(p.grad_out) + (row + t) * old_ + c0 * sizeof(TO),
-                                       old_, f, K, owidth, lane);
-            // the states before: one token earlier (h0 for the first one, below)
-            rows_in<SIZE, Sh::OROW, K>(sm + 2 * N + M, p.out, static_cast<const char*>(p.out) + (row + t - 1) * old_ + c0 * sizeof(TO),
-                                       old_, f + (t + f == sp.lo), K, owidth, lane);
+                rows_in<SIZE, Sh::ROW, K>(st.x, p.x, static_cast<const char*>(p.x) + (row + t) * xld + at.c0 * sizeof(TI),
+                                          xld, f, K, width, lane);
+            rows_in<SIZE, Sh::OROW, K>(st.g, p.grad_out,
+                                       static_cast<const char*>(p.grad_out) + (row + t) * tld + at.c0 * sizeof(TO), tld, f,
+                                       K, owidth, lane);
+            // the states before: one token earlier (h0 for the sequence's first one, below)
+            rows_in<SIZE, Sh::OROW, K>(st.h, p.out,
+                                       static_cast<const char*>(p.out) + (row + t - 1) * tld + at.c0 * sizeof(TO), tld,
+                                       f + (t + f == at.begin), K, owidth, lane);
         }
         copy_commit();
     };
 #pragma unroll
     for (int i = 0; i < STAGES; ++i)
-        if (i < rounds) fetch(i);
+        if (i < at.rounds) fetch(i);
         else copy_commit();
-    sh.fold.begin(S);
+    through_parts<V, true>(p, cut, sh.fold, at.sr, at.part, at.warp, lane, c, carry);
+    sh.fold.begin(at.S);
     bool late = false;
-    for (int r = 0; r < rounds; ++r) {
+    for (int r = 0; r < at.rounds; ++r) {
         const int t = base - r * step;
-        const bool any = t + K > sp.lo;
-        typename Sh::Stage& st = sh.st[r % STAGES][warp];
+        const bool any = t + K > at.lo;                     // (the warp as one)
+        typename Sh::Stage& st = sh.st[r % STAGES][at.warp];
         copy_wait<STAGES - 1>();
         __syncwarp();
         float a[K][V], w[LEAK ? K : 1][V], z[V], s[V], u[V];
@@ -741,7 +566,7 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                     d1 = peek<TI, V>(st.d + j1 * Sh::ROW + lane * V * sizeof(TI));
                     g1 = peek<TO, V>(st.g + j1 * Sh::OROW + lane * V * sizeof(TO));
                 }
-                const F2 zz = mul2(F2{nA[v0], nA[v1]}, F2{d0.get(v0), d1.get(v1)});
+                const F2 zz = mul2(F2{rate[v0], rate[v1]}, F2{d0.get(v0), d1.get(v1)});
                 const Gate2 gg = gate2<LEAK>(zz);
                 a[k0][v0] = gg.a.x;
                 a[k1][v1] = gg.a.y;
@@ -751,13 +576,10 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                 }
                 if constexpr (V == 1) {
                     z[0] += zz.x + zz.y;
-                    const float h0 = s[0] + g0.get(0);
-                    s[0] = gg.a.x * h0;
-                    const float h1 = s[0] + g1.get(0);
-                    s[0] = gg.a.y * h1;
+                    s[0] = gg.a.y * (gg.a.x * (s[0] + g0.get(0)) + g1.get(0));
                 } else {
-                    const F2 dh = add2(F2{s[0], s[1]}, F2{g0.get(0), g0.get(1)});
-                    const F2 m = mul2(gg.a, dh), zs = add2(F2{z[0], z[1]}, zz);
+                    const F2 m = mul2(gg.a, add2(F2{s[0], s[1]}, F2{g0.get(0), g0.get(1)}));
+                    const F2 zs = add2(F2{z[0], z[1]}, zz);
                     s[0] = m.x;
                     s[1] = m.y;
                     z[0] = zs.x;
@@ -765,10 +587,10 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                 }
             }
         }
-        fold_round<V, NW>(sh.fold, r, S, rank, warp, lane, cut.wait_ns, late, z, s, carry, u);
+        fold_round<V>(sh.fold, r, at.S, at.rank, at.warp, lane, cut.wait_ns, late, z, s, carry, u);
         if (any) {
-            TI* gx_out = static_cast<TI*>(p.grad_x) + (row + t) * p.C + c0;
-            TI* gd_out = static_cast<TI*>(p.grad_d) + (row + t) * p.C + c0;
+            TI* gx_out = static_cast<TI*>(p.grad_x) + (row + t) * p.C + at.c0;
+            TI* gd_out = static_cast<TI*>(p.grad_d) + (row + t) * p.C + at.c0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int j = K - 1 - k;
@@ -777,20 +599,38 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                 const Vec<TO, V> hv = peek<TO, V>(st.h + j * Sh::OROW + lane * V * sizeof(TO));
                 Vec<TI, V> xv = dv;
                 if (LEAK) xv = peek<TI, V>(st.x + j * Sh::ROW + lane * V * sizeof(TI));
-                float gx[V], gd[V];
+                float gx[V], gd[V], prev[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float dh = u[v] + gv.get(v);
-                    u[v] = a[k][v] * dh;
-                    float prev = t + j == sp.lo ? first[v] : hv.get(v);
-                    gx[v] = dh;
+                for (int v = 0; v < V; ++v) prev[v] = t + j == at.begin ? first[v] : hv.get(v);
+                if constexpr (V == 1) {
+                    const float dh = u[0] + gv.get(0);
+                    u[0] = a[k][0] * dh;
+                    gx[0] = dh;
                     if (LEAK) {
-                        prev -= xv.get(v);
-                        gx[v] = w[LEAK ? k : 0][v] * dh;
+                        prev[0] -= xv.get(0);
+                        gx[0] = w[LEAK ? k : 0][0] * dh;
                     }
-                    const float m = u[v] * prev;
-                    gd[v] = nA[v] * m;
-                    dA[v] = fmaf(-dv.get(v), m, dA[v]);     // (d = 0 outside the sequence)
+                    const float m = u[0] * prev[0];
+                    gd[0] = nA[0] * m;
+                    dA[0] = fmaf(dv.get(0), m, dA[0]);       // (d = 0 outside the sequence)
+                } else {
+                    const F2 dh = add2(F2{u[0], u[1]}, F2{gv.get(0), gv.get(1)});
+                    const F2 n = mul2(F2{a[k][0], a[k][1]}, dh);
+                    F2 x = dh, before{prev[0], prev[1]};
+                    if (LEAK) {
+                        before = add2(before, F2{-xv.get(0), -xv.get(1)});
+                        x = mul2(F2{w[LEAK ? k : 0][0], w[LEAK ? k : 0][1]}, dh);
+                    }
+                    const F2 m = mul2(n, before), d = mul2(F2{nA[0], nA[1]}, m);
+                    const F2 sum = fma2(F2{dv.get(0), dv.get(1)}, m, F2{dA[0], dA[1]});
+                    u[0] = n.x;
+                    u[1] = n.y;
+                    gx[0] = x.x;
+                    gx[1] = x.y;
+                    gd[0] = d.x;
+                    gd[1] = d.y;
+                    dA[0] = sum.x;
+                    dA[1] = sum.y;
                 }
                 if (SIZE == 16) {
                     Vec<TI, V> q;
@@ -798,7 +638,7 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
                     poke<TI, V>(st.x + j * Sh::ROW + lane * V * sizeof(TI), q);
                     q.set(gd);
                     poke<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI), q);
-                } else if (t + j >= sp.lo) {
+                } else if (t + j >= at.lo) {
 #pragma unroll
                     for (int v = 0; v < V; ++v)
                         if (c + v < p.C) {
@@ -809,76 +649,138 @@ gated_bwd_staged(const GatedArgs p, const Cut cut, float* part) {
             }
             __syncwarp();
             if (SIZE == 16) {
-                const int f = max(sp.lo - t, 0);
+                const int f = max(at.lo - t, 0);
                 const long long ld = p.C * static_cast<long long>(sizeof(TI));
                 rows_out<Sh::ROW, K>(reinterpret_cast<char*>(gx_out), ld, st.x, f, K, width, lane);
                 rows_out<Sh::ROW, K>(reinterpret_cast<char*>(gd_out), ld, st.d, f, K, width, lane);
                 __syncwarp();
             }
         }
-        if (r + STAGES < rounds) fetch(r + STAGES);
+        if (r + STAGES < at.rounds) fetch(r + STAGES);
         else copy_commit();
     }
-    sh.fold.end(S, late);
-    if (p.grad_h0 && rank == 0 && warp == 0)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (c + v < p.C) p.grad_h0[sr * p.C + c + v] = carry[v];
-    if (part) {
-        // the warps' shares, in order
+    if (sums) {
+        // the warps' shares, in order, then the cluster's
         __syncthreads();
 #pragma unroll
-        for (int v = 0; v < V; ++v) sh.fold.warp[0][warp][v][lane].x = dA[v];
+        for (int v = 0; v < V; ++v) sh.fold.warp[0][at.warp][v][lane].x = dA[v];
         __syncthreads();
-        if (warp == 0)
+        if (at.warp == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float sum = 0.f;
                 for (int i = 0; i < NW; ++i) sum += sh.fold.warp[0][i][v][lane].x;
-                if (c + v < p.C) part[((sr / p.H * S + rank) * p.H + sr % p.H) * p.C + c + v] = sum;
+                sh.dA[v][lane] = sum;
             }
+        if (at.S == 1) __syncwarp();
     }
+    sh.fold.end(at.S, late);
+    if (at.rank == 0 && at.warp == 0)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (p.grad_h0 && at.part == 0 && c + v < p.C) p.grad_h0[at.sr * p.C + c + v] = carry[v];
+            if (sums) {
+                float sum = 0.f;
+                for (int j = 0; j < at.S; ++j)
+                    sum += at.S == 1 ? sh.dA[v][lane] : from_rank(&sh.dA[v][lane], j);
+                const long long n = at.sr / p.H, hd = at.sr % p.H;
+                if (c + v < p.C) sums[((n * cut.parts + at.part) * p.H + hd) * p.C + c + v] = -sum;
+            }
+        }
+    if (sums && at.S > 1) cluster_sync();   // rank 0 has read the others' sums
 }
 
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(THREADS)
+// The maps of every MAP_TOKENS tokens of long sequences of few channels: {a,
+// e, s, z}, [state row, T / MAP_TOKENS, C].  A warp composes an eighth of
+// them, a channel per lane, UN tokens' loads in flight.
+template <typename TI, typename TO, bool LEAK, bool BWD>
+__global__ void __launch_bounds__(NW * 32) gated_maps_kernel(const __grid_constant__ GatedArgs p, float4* maps) {
+    constexpr int UN = 16, sub = MAP_TOKENS / NW;
+    __shared__ float4 share[NW][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slabs = (p.C + 31) / 32, c = static_cast<int>(blockIdx.x % slabs) * 32 + lane;
+    const int all = (p.T + MAP_TOKENS - 1) / MAP_TOKENS;
+    const long long u = blockIdx.x / slabs, sr = u / all;
+    const int chunk = static_cast<int>(u - sr * all);
+    const bool on = c < p.C;
+    const long long from = min(static_cast<long long>(p.T), static_cast<long long>(chunk) * MAP_TOKENS + warp * sub);
+    const long long to = min(static_cast<long long>(p.T), from + sub);
+    const float rate = on ? -LOG2E * p.A[(sr % p.H) * p.C + c] : 0.f;
+    const TI* d = static_cast<const TI*>(p.d) + sr * p.T * p.d_ld + c;
+    const TI* x = static_cast<const TI*>(p.x) + sr * p.T * p.x_ld + c;
+    const TO* g = static_cast<const TO*>(p.grad_out) + sr * p.T * p.C + c;
+    float z = 0.f, s = 0.f, sz = 0.f;
+    for (long long t = from; t < to; t += UN) {
+        float dv[UN], xv[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const long long k = BWD ? to - 1 - (t - from) - i : t + i;
+            const bool ok = on && k >= from && k < to;
+            dv[i] = ok ? to_f32(d[k * p.d_ld]) : 0.f;
+            xv[i] = !ok ? 0.f : BWD ? to_f32(g[k * p.C]) : to_f32(x[k * p.x_ld]);
+        }
+        // spans of UN tokens are composed by their exponents' sum, as a warp's are in the walk
+        float zz = 0.f, ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < UN; i += 2) {
+            const F2 e = mul2(both(rate), F2{dv[i], dv[i + 1]});
+            const Gate2 q = gate2<LEAK && !BWD>(e);
+            zz += e.x + e.y;
+            if (BWD) ss = q.a.y * (q.a.x * (ss + xv[i]) + xv[i + 1]);
+            else if (LEAK) ss = fmaf(q.a.y, fmaf(q.a.x, ss, q.w.x * xv[i]), q.w.y * xv[i + 1]);
+            else ss = fmaf(q.a.y, fmaf(q.a.x, ss, xv[i]), xv[i + 1]);
+        }
+        const Gate q = gate(zz);
+        s = decay_add(q, s, ss);
+        z += zz;
+        sz = z;
+    }
+    share[warp][lane] = make_float4(0.f, 0.f, s, sz);
+    __syncthreads();
+    if (warp > 0 || !on) return;
+    z = s = 0.f;
+    for (int i = 0; i < NW; ++i) {
+        const float4 m = share[BWD ? NW - 1 - i : i][lane];
+        const Gate q = gate(m.w);
+        s = decay_add(q, s, m.z);
+        z += m.w;
+    }
+    const Gate q = gate(z);
+    maps[(sr * all + chunk) * p.C + c] = make_float4(q.a, q.e, s, z);
+}
+
+// A step moves 4 (state) + 4 + 2 + 2 + 2 bytes per element (bf16) once, so a
+// large batch is bound by HBM and a small one by its launch; N elements per
+// thread where rows and addresses allow.
+template <typename TI, typename TO, int N>
+__global__ void __launch_bounds__(NW * 32)
 gated_step_kernel(const TI* __restrict__ x, const TI* __restrict__ d, const float* __restrict__ A, bool leak,
                   const float* state, float* new_state, TO* __restrict__ out, long long n, long long HC) {
-    const long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+    const long long i = (static_cast<long long>(blockIdx.x) * (NW * 32) + threadIdx.x) * N;
     if (i >= n) return;
-    const Gate g = gate(-A[i % HC] * to_f32(d[i]));
-    const float xi = to_f32(x[i]);
-    const float h = decay_add(g, state[i], leak ? g.w * xi : xi);
-    new_state[i] = h;
-    out[i] = from_f32<TO>(h);
+    const long long j = i % HC;
+    float xv[N], dv[N], s[N], Av[N], h[N];
+    load_n<N>(x + i, xv);
+    load_n<N>(d + i, dv);
+    load_n<N>(A + j, Av);
+    load_n<N>(state + i, s);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const Gate g = gate(-LOG2E * (Av[k] * dv[k]));
+        h[k] = decay_add(g, s[k], leak ? g.w * xv[k] : xv[k]);
+    }
+    store_n<N>(new_state + i, h);
+    store_n<N>(out + i, h);
 }
 
 template <typename F>
-kdn_status by_type(const GatedArgs& a, F f) {
-    if (a.in_dtype == KDN_BF16)
-        return a.out_dtype == KDN_BF16 ? f(__nv_bfloat16(), __nv_bfloat16()) : f(__nv_bfloat16(), float());
-    return a.out_dtype == KDN_BF16 ? f(float(), __nv_bfloat16()) : f(float(), float());
+kdn_status by_type(kdn_dtype in, kdn_dtype out, F f) {
+    if (in == KDN_BF16)
+        return out == KDN_BF16 ? f(__nv_bfloat16(), __nv_bfloat16()) : f(__nv_bfloat16(), float());
+    return out == KDN_BF16 ? f(float(), __nv_bfloat16()) : f(float(), float());
 }
 
 long long state_rows(const GatedArgs& a) { return static_cast<long long>(a.nseq > 0 ? a.nseq : a.B) * a.H; }
-
-// CTAs per cluster: as many as keep the grid within the GPU's two CTAs per
-// SM, no more than a sequence has tiles.  The exchange of a round costs a
-// cluster more than half of the round itself (2.5 us alone on two CTAs per
-// SM, 3.3 us with four, 4.0 us with eight), so a grid that fills the SMs
-// without clusters stays without (8 x 4096 x 2048: 80 us, 91 with two), and
-// one that does not gains from every CTA (65536 x 2048: 257 us with eight).
-// Packed sequences have one length on average and may have others, so a long
-// average gets a cluster whatever the grid.
-int cluster_size(const GatedArgs& a, int V) {
-    constexpr int TILE = FWD_WARPS * 16;
-    const long long units = state_rows(a) * ((a.C + 32 * V - 1) / (32 * V));
-    const long long len = a.nseq > 0 ? (a.T + a.nseq - 1) / a.nseq : a.T, tiles = (len + TILE - 1) / TILE;
-    long long S = 2LL * sm_count() / units;
-    if (a.nseq > 0 && S < tiles / 4) S = tiles / 4;
-    if (S > tiles) S = tiles;
-    return static_cast<int>(S < 1 ? 1 : S > MAX_CLUSTER ? MAX_CLUSTER : S);
-}
 
 // Whether every row of every tensor starts on a multiple of `bytes` and is a
 // multiple of it long.
@@ -891,20 +793,121 @@ bool rows_ok(const GatedArgs& a, long long bytes) {
            (!a.x || a.x_ld * is % bytes == 0);
 }
 
-// One launch of a walk kernel over all (state row, slab) units.
-template <typename... KArgs, typename... Args>
-kdn_status launch_walk(void (*kernel)(KArgs...), int threads, long long rows, const Cut& cut, size_t smem, cudaStream_t stream,
-                       Args... args) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return from_cuda(e);
+// What the current device holds of a kernel at once: clusters of 1 .. 8 CTAs
+// (0: none).  Asked once per device and kernel, when the kernel's shared
+// memory is set up too.
+struct Resident {
+    int clusters[MAX_CLUSTER];
+};
+
+cudaError_t resident(const void* kernel, size_t smem, Resident* out) {
+    static std::mutex lock;
+    static std::map<std::pair<int, const void*>, Resident> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const std::lock_guard<std::mutex> hold(lock);
+    auto it = known.find({dev, kernel});
+    if (it == known.end()) {
+        Resident r{};
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NW * 32, smem);
+        if (e != cudaSuccess) return e;
+        r.clusters[0] = n * sm_count();
+        for (int S = 2; S <= MAX_CLUSTER; ++S) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(S);
+            cfg.blockDim = dim3(NW * 32);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute at{};
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = S;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&r.clusters[S - 1], kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                r.clusters[S - 1] = 0;
+            }
+        }
+        it = known.emplace(std::make_pair(dev, kernel), r).first;
     }
-    const long long blocks = rows * cut.slabs * cut.S;
+    *out = it->second;
+    return cudaSuccess;
+}
+
+// A bound of the parts that plan() takes, whatever the types and kernels.
+int most_parts(long long rows, int C, int T) {
+    const long long units = rows * ((C + 63) / 64), slots = 2LL * sm_count() / MAX_CLUSTER;
+    const long long rounds = T / (MAX_CLUSTER * NW * BWD_K), by_rounds = rounds / 4;
+    long long n = slots / units;
+    n = n < by_rounds ? n : by_rounds;
+    return static_cast<int>(n < 1 ? 1 : n > MAX_PARTS ? MAX_PARTS : n);
+}
+
+// Cluster size and parts.  A round of a cluster costs more than a CTA's alone
+// (the exchange), by what was measured on 134 M elements: 4 % with two CTAs,
+// 16 % with four, 44 % with eight; an SM with one CTA does a round in about
+// two thirds of the time that it takes for two.  So the size with the least
+// of (waves of resident clusters) x (rounds) x (cost) is taken: 8 x 4096 x
+// 2048 runs without clusters (80 us, 91 with two CTAs), 65536 x 2048 with
+// eight.  (A wave is what the device holds at once, less than its CTA slots:
+// its GPCs hold whole clusters.)  Packed sequences have one length on average
+// and may have others, so a long average gets a cluster whatever the grid.
+//
+// Parts are taken where clusters of eight leave half the device free, if they
+// save `worth` rounds of about 2 us: the maps' launch costs 8 us, scratch of
+// its own another 15 (65536 x 64: 144 -> 41 us, backward 265 -> 54 us; 4 x
+// 9001 x 64 fp32 backward 40 -> 25 us, but forward, scratch included, 21 ->
+// 33 us).
+kdn_status plan(const GatedArgs& a, const void* kernel, size_t smem, int V, int K, int worth, Cut* cut) {
+    Resident held;
+    const cudaError_t e = resident(kernel, smem, &held);
+    if (e != cudaSuccess) return from_cuda(e);
+    cut->slabs = (a.C + 32 * V - 1) / (32 * V);
+    cut->S = cut->parts = 1;
+    cut->len = a.T;
+    const int tile = NW * K;
+    const long long rows = state_rows(a), units = rows * cut->slabs;
+    const long long len = a.nseq > 0 ? (a.T + a.nseq - 1) / a.nseq : a.T, tiles = (len + tile - 1) / tile;
+    static const double cost[MAX_CLUSTER] = {1, 1.04, 1.10, 1.16, 1.23, 1.30, 1.37, 1.44};
+    double best = DBL_MAX;
+    for (int S = 1; S <= MAX_CLUSTER && (S == 1 || S <= tiles); ++S) {
+        const int n = held.clusters[S - 1];
+        if (n < 1) continue;
+        double t = static_cast<double>((units + n - 1) / n) * static_cast<double>((tiles + S - 1) / S) * cost[S - 1];
+        if (units * S <= sm_count()) t *= 0.65;
+        if (t < best * 0.98) {
+            best = t;
+            cut->S = S;
+        }
+    }
+    if (a.nseq > 0) {
+        const long long s = tiles / 4 < MAX_CLUSTER ? tiles / 4 : MAX_CLUSTER;
+        if (cut->S < s && held.clusters[s - 1] > 0) cut->S = static_cast<int>(s);
+    } else if (cut->S == MAX_CLUSTER) {
+        const int bound = most_parts(rows, a.C, a.T);
+        const long long rounds = (tiles + MAX_CLUSTER - 1) / MAX_CLUSTER;
+        long long n = held.clusters[MAX_CLUSTER - 1] / units;
+        if (n > rounds / 4) n = rounds / 4;
+        if (n > bound) n = bound;
+        if (n > 1 && rounds - rounds / n >= worth) {
+            cut->len = static_cast<int>((rounds + n - 1) / n) * MAX_CLUSTER * tile;
+            cut->parts = (a.T + cut->len - 1) / cut->len;
+        }
+    }
+    return KDN_OK;
+}
+
+template <typename... KArgs, typename... Args>
+kdn_status launch_walk(void (*kernel)(KArgs...), long long rows, const Cut& cut, size_t smem, cudaStream_t stream, Args... args) {
+    const long long blocks = rows * cut.parts * cut.slabs * cut.S;
     if (blocks > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at{};
@@ -916,77 +919,112 @@ kdn_status launch_walk(void (*kernel)(KArgs...), int threads, long long rows, co
     return from_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
+// A call's stream-ordered scratch, freed on the stream when it leaves scope.
+struct Scratch {
+    cudaStream_t stream;
+    void* p = nullptr;
+    explicit Scratch(cudaStream_t s) : stream(s) {}
+    kdn_status take(long long bytes) { return from_cuda(cudaMallocAsync(&p, static_cast<size_t>(bytes), stream)); }
+    ~Scratch() {
+        if (p) cudaFreeAsync(p, stream);
+    }
+};
+
+template <typename TI, typename TO, bool LEAK, bool BWD>
+kdn_status launch_maps(const GatedArgs& a, float4* maps, cudaStream_t stream) {
+    // (parts are for few channels: this is under 2^31)
+    const long long blocks = state_rows(a) * ((a.T + MAP_TOKENS - 1) / MAP_TOKENS) * ((a.C + 31) / 32);
+    gated_maps_kernel<TI, TO, LEAK, BWD><<<static_cast<unsigned>(blocks), NW * 32, 0, stream>>>(a, maps);
+    return from_cuda(cudaGetLastError());
+}
+
+long long maps_bytes(long long rows, int parts, int C, int T) {
+    return parts > 1 ? rows * ((T + MAP_TOKENS - 1) / MAP_TOKENS) * C * 16 : 0;
+}
+
 }  // namespace
 
 long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq) {
-    GatedArgs a{};
-    a.B = B;
-    a.H = H;
-    a.T = T;
-    a.C = C;
-    a.nseq = nseq;
-    return state_rows(a) * cluster_size(a, 2) * C * 4;   // (V = 1 makes clusters no larger)
+    const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
+    const int parts = nseq > 0 ? 1 : most_parts(rows, C, T);
+    return maps_bytes(rows, parts, C, T) + (rows / H * parts > 1 ? rows * parts * C * 4 : 0);
 }
 
 kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
-    const long long rows = state_rows(a);
-    Cut cut{0, 1, wait_ns};
-    return by_type(a, [&](auto ti, auto to) {
+    return by_type(a.in_dtype, a.out_dtype, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
-        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 16, NW = FWD_WARPS;
-        auto go = [&](auto kernel, int v, size_t smem) {
-            cut.slabs = (a.C + 32 * v - 1) / (32 * v);
-            cut.S = cluster_size(a, v);
-            return launch_walk(kernel, NW * 32, rows, cut, smem, stream, a, cut);
+        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1;
+        auto go = [&](auto leak, auto size) {
+            constexpr bool L = decltype(leak)::value;
+            auto kernel = gated_fwd_kernel<TI, TO, V, FWD_K, L, decltype(size)::value>;
+            const size_t smem = sizeof(FwdShared<TI, TO, V, FWD_K>);
+            Cut cut{};
+            cut.wait_ns = wait_ns;
+            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, FWD_K, 12, &cut);
+            if (s != KDN_OK) return s;
+            Scratch scratch(stream);
+            if (cut.parts > 1) {
+                s = scratch.take(maps_bytes(state_rows(a), cut.parts, a.C, a.T));
+                if (s != KDN_OK) return s;
+                cut.maps = static_cast<float4*>(scratch.p);
+                s = launch_maps<TI, TO, L, false>(a, static_cast<float4*>(scratch.p), stream);
+                if (s != KDN_OK) return s;
+            }
+            return launch_walk(kernel, state_rows(a), cut, smem, stream, a, cut);
         };
-        auto leak = [&](auto l) {
-            constexpr bool L = decltype(l)::value;
-            if (rows_ok(a, 16))
-                return go(gated_fwd_staged<TI, TO, V, K, NW, L, 16>, V, sizeof(FwdShared<TI, TO, V, K, NW>));
-            if (rows_ok(a, 4))
-                return go(gated_fwd_staged<TI, TO, V, K, NW, L, 4>, V, sizeof(FwdShared<TI, TO, V, K, NW>));
-            return go(gated_fwd_kernel<TI, TO, 1, K, NW, L>, 1, 0);
+        auto sized = [&](auto leak) {
+            if (rows_ok(a, 16)) return go(leak, std::integral_constant<int, 16>());
+            if (sizeof(TI) == 4 && sizeof(TO) == 4) return go(leak, std::integral_constant<int, 4>());
+            if (rows_ok(a, 4)) return go(leak, std::integral_constant<int, 4>());
+            return go(leak, std::integral_constant<int, 2>());
         };
-        return a.leak ? leak(std::true_type()) : leak(std::false_type());
+        return a.leak ? sized(std::true_type()) : sized(std::false_type());
     });
 }
 
 kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
-    const long long rows = state_rows(a);
-    Cut cut{0, 1, wait_ns};
-    float* part = a.grad_A ? static_cast<float*>(a.workspace) : nullptr;
-    const bool own = a.grad_A && !part;
-    if (own) {
-        const kdn_status s = from_cuda(cudaMallocAsync(&part, rows * cluster_size(a, 2) * a.C * 4, stream));
-        if (s != KDN_OK) return s;
-    }
-    kdn_status s = by_type(a, [&](auto ti, auto to) {
+    return by_type(a.in_dtype, a.out_dtype, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
-        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1, K = 8, NW = BWD_WARPS;
-        auto go = [&](auto kernel, int v, size_t smem) {
-            cut.slabs = (a.C + 32 * v - 1) / (32 * v);
-            cut.S = cluster_size(a, v);
-            return launch_walk(kernel, NW * 32, rows, cut, smem, stream, a, cut, part);
+        constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1;
+        auto go = [&](auto leak, auto size) {
+            constexpr bool L = decltype(leak)::value;
+            auto kernel = gated_bwd_kernel<TI, TO, V, BWD_K, L, decltype(size)::value>;
+            const size_t smem = sizeof(BwdShared<TI, TO, V, BWD_K>);
+            Cut cut{};
+            cut.wait_ns = wait_ns;
+            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, BWD_K, a.workspace ? 4 : 12, &cut);
+            if (s != KDN_OK) return s;
+            const long long rows = state_rows(a), shares = rows / a.H * cut.parts;
+            const long long maps = maps_bytes(rows, cut.parts, a.C, a.T), HC = static_cast<long long>(a.H) * a.C;
+            const long long bytes = maps + (shares > 1 && a.grad_A ? shares * HC * 4 : 0);
+            Scratch scratch(stream);
+            char* ws = static_cast<char*>(a.workspace);
+            if (bytes > 0 && !ws) {
+                s = scratch.take(bytes);
+                if (s != KDN_OK) return s;
+                ws = static_cast<char*>(scratch.p);
+            }
+            if (cut.parts > 1) {
+                cut.maps = reinterpret_cast<float4*>(ws);
+                s = launch_maps<TI, TO, L, true>(a, reinterpret_cast<float4*>(ws), stream);
+                if (s != KDN_OK) return s;
+            }
+            float* sums = !a.grad_A ? nullptr : shares > 1 ? reinterpret_cast<float*>(ws + maps) : a.grad_A;
+            s = launch_walk(kernel, rows, cut, smem, stream, a, cut, sums);
+            if (s == KDN_OK && a.grad_A && shares > 1)
+                s = from_cuda(sum_rows(sums, shares, HC, a.grad_A, nullptr, HC, stream));
+            return s;
         };
-        auto leak = [&](auto l) {
-            constexpr bool L = decltype(l)::value;
-            if (rows_ok(a, 16)) return go(gated_bwd_staged<TI, TO, V, K, NW, L, 16>, V, sizeof(BwdShared<TI, TO, V, K, NW>));
-            if (rows_ok(a, 4)) return go(gated_bwd_staged<TI, TO, V, K, NW, L, 4>, V, sizeof(BwdShared<TI, TO, V, K, NW>));
-            return go(gated_bwd_kernel<TI, TO, 1, K, NW, L>, 1, 0);
+        auto sized = [&](auto leak) {
+            if (rows_ok(a, 16)) return go(leak, std::integral_constant<int, 16>());
+            if (sizeof(TI) == 4 && sizeof(TO) == 4) return go(leak, std::integral_constant<int, 4>());
+            if (rows_ok(a, 4)) return go(leak, std::integral_constant<int, 4>());
+            return go(leak, std::integral_constant<int, 2>());
         };
-        return a.leak ? leak(std::true_type()) : leak(std::false_type());
+        return a.leak ? sized(std::true_type()) : sized(std::false_type());
     });
-    if (s == KDN_OK && a.grad_A) {
-        const long long HC = static_cast<long long>(a.H) * a.C;
-        s = from_cuda(sum_rows(part, rows / a.H * cut.S, HC, a.grad_A, nullptr, HC, stream));
-    }
-    if (own) {
-        const kdn_status f = from_cuda(cudaFreeAsync(part, stream));
-        if (s == KDN_OK) s = f;
-    }
-    return s;
 }
 
 cudaError_t gated_take_device_error(int* status) {
@@ -1001,17 +1039,17 @@ kdn_status gated_step_launch(const void* x, const void* d, const float* A, bool 
                              float* new_state, void* out, int B, int H, int C, kdn_dtype in_dtype,
                              kdn_dtype out_dtype, cudaStream_t stream) {
     const long long HC = static_cast<long long>(H) * C, n = HC * B;
-    const long long blocks = (n + THREADS - 1) / THREADS;
+    const void* ptrs[] = {x, d, A, state, new_state, out};
+    bool wide = HC % 4 == 0 && n >= 4LL * NW * 32 * sm_count();   // (a small call wants threads, not width)
+    for (const void* q : ptrs) wide = wide && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+    const long long per = wide ? 4 : 1, blocks = (n / per + NW * 32 - 1) / (NW * 32);
     if (blocks > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
-    GatedArgs t{};
-    t.in_dtype = in_dtype;
-    t.out_dtype = out_dtype;
-    return by_type(t, [&](auto ti, auto to) {
+    return by_type(in_dtype, out_dtype, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
-        gated_step_kernel<TI, TO><<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(
-            static_cast<const TI*>(x), static_cast<const TI*>(d), A, leak, state, new_state,
-            static_cast<TO*>(out), n, HC);
+        auto kernel = wide ? gated_step_kernel<TI, TO, 4> : gated_step_kernel<TI, TO, 1>;
+        kernel<<<static_cast<unsigned>(blocks), NW * 32, 0, stream>>>(
+            static_cast<const TI*>(x), static_cast<const TI*>(d), A, leak, state, new_state, static_cast<TO*>(out), n, HC);
         return from_cuda(cudaGetLastError());
     });
 }

@@ -513,7 +513,7 @@ def gated_scan_fwd(x, d, A, h0=None, leak=False, offsets=None, out=None, out_dty
 
 
 def gated_scan_bwd_workspace(B, H, T, C, nseq=0) -> int:
-    """Bytes of device workspace ``gated_scan_bwd`` needs."""
+    """Bytes of device workspace ``gated_scan_bwd`` needs (0: none)."""
     n = ctypes.c_longlong(0)
     st = lib.kdn_gated_scan_bwd_workspace(B, H, T, C, nseq, ctypes.byref(n))
     if st != KDN_OK:
@@ -554,7 +554,8 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
         g[name] = t
     ws_bytes = gated_scan_bwd_workspace(B, H, T, C, nseq)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 1), device=x.device, dtype=torch.uint8)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, device=x.device, dtype=torch.uint8)
     elif workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError(f"workspace must hold {ws_bytes} bytes")
     _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, grad_out=grad_out,

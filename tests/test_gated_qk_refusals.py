@@ -64,7 +64,7 @@ def test_bwd_rejects_more(kdn):
     for f in ("gf", "gA", "gh0"):
         assert bwd(kdn, **{f: FAKE + 2}) == -1
     assert bwd(kdn, gx=FAKE + 1) == -1 and bwd(kdn, go=FAKE + 1) == -1
-    assert bwd(kdn, ws=FAKE + 16, n=1 << 30) == -1 and bwd(kdn, ws=FAKE, n=8) == -1
+    assert bwd(kdn, ws=FAKE + 16, n=1 << 30) == -1 and bwd(kdn, B=2, ws=FAKE, n=8) == -1
 
 
 def test_workspaces(kdn):
