@@ -36,6 +36,7 @@
 #include "gated_device.cuh"
 #include "kdn_device.cuh"
 #include "kdn_internal.h"
+#include "kernel_setup.h"
 #include "sum_rows.cuh"
 
 namespace kdn {
@@ -43,7 +44,7 @@ namespace {
 
 using namespace gated;
 
-constexpr int MAX_CLUSTER = 8, MAX_PARTS = 16;
+constexpr int MAX_CLUSTER = 8;
 constexpr int NW = 8;             // warps per CTA
 constexpr int FWD_K = 16, BWD_K = 8;
 constexpr int STAGES = 2;
@@ -300,7 +301,6 @@ __device__ __forceinline__ void fold_round(Fold<V>& f, int r, int S, int rank, i
     }
 }
 static_assert(MAX_CLUSTER <= NW, "a warp sends to one CTA");
-static_assert(MAX_CLUSTER * NW * BWD_K % MAP_TOKENS == 0 && MAX_CLUSTER * NW * FWD_K % MAP_TOKENS == 0, "parts are whole maps");
 
 // The state that a part starts from: the sequence's carry through the maps of
 // the tokens before the part (those after it, backward).  Each warp composes
@@ -810,7 +810,7 @@ cudaError_t resident(const void* kernel, size_t smem, Resident* out) {
     auto it = known.find({dev, kernel});
     if (it == known.end()) {
         Resident r{};
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        e = allow_smem(kernel, smem);
         if (e != cudaSuccess) return e;
         int n = 0;
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NW * 32, smem);
@@ -838,31 +838,34 @@ cudaError_t resident(const void* kernel, size_t smem, Resident* out) {
     return cudaSuccess;
 }
 
-// A bound of the parts that plan() takes, whatever the types and kernels.
-int most_parts(long long rows, int C, int T) {
-    const long long units = rows * ((C + 63) / 64), slots = 2LL * sm_count() / MAX_CLUSTER;
-    const long long rounds = T / (MAX_CLUSTER * NW * BWD_K), by_rounds = rounds / 4;
-    long long n = slots / units;
-    n = n < by_rounds ? n : by_rounds;
-    return static_cast<int>(n < 1 ? 1 : n > MAX_PARTS ? MAX_PARTS : n);
+int maps_of(int T) { return (T + MAP_TOKENS - 1) / MAP_TOKENS; }
+
+// A bound of the parts that plan() takes, whatever the types and kernels: one
+// map each at least, and no more than fill the device.
+long long most_parts(long long rows, int C, int T) {
+    const long long n = 2LL * sm_count() / (rows * ((C + 63) / 64));
+    return n < 1 ? 1 : n < maps_of(T) ? n : maps_of(T) > 0 ? maps_of(T) : 1;
 }
 
-// Cluster size and parts.  A round of a cluster costs more than a CTA's alone
-// (the exchange), by what was measured on 134 M elements: 4 % with two CTAs,
-// 16 % with four, 44 % with eight; an SM with one CTA does a round in about
-// two thirds of the time that it takes for two.  So the size with the least
-// of (waves of resident clusters) x (rounds) x (cost) is taken: 8 x 4096 x
-// 2048 runs without clusters (80 us, 91 with two CTAs), 65536 x 2048 with
-// eight.  (A wave is what the device holds at once, less than its CTA slots:
-// its GPCs hold whole clusters.)  Packed sequences have one length on average
-// and may have others, so a long average gets a cluster whatever the grid.
+// Cluster size and parts, by a model in rounds of a full device (two CTAs per
+// SM, 2.5 us): waves x (rounds x cost + START).
 //
-// Parts are taken where clusters of eight leave half the device free, if they
-// save `worth` rounds of about 2 us: the maps' launch costs 8 us, scratch of
-// its own another 15 (65536 x 64: 144 -> 41 us, backward 265 -> 54 us; 4 x
-// 9001 x 64 fp32 backward 40 -> 25 us, but forward, scratch included, 21 ->
-// 33 us).
-kdn_status plan(const GatedArgs& a, const void* kernel, size_t smem, int V, int K, int worth, Cut* cut) {
+// A wave is what the device holds at once: its CTA slots, or fewer for
+// clusters, which a GPC holds whole.  A cluster's round costs more than a
+// CTA's alone (the exchange), by what was measured on 134 M elements: 4 %
+// with two CTAs, 16 % with four, 44 % with eight; an SM with one CTA does a
+// round in about two thirds of the time that it takes for two; starting a CTA
+// costs about 1.5 rounds.  So 8 x 4096 x 2048 runs without clusters (80 us,
+// 91 with two CTAs), 65536 x 2048 with eight.
+//
+// Parts add a pass over two tensors (the walk's own time again: its loads are
+// single elements) and a launch (`fixed` rounds; three and a half, nine with scratch of its own), and make
+// units enough that no or small clusters do: 65536 x 64 144 -> 41 us, backward
+// 265 -> 54 us.
+//
+// Packed sequences have one length on average and may have others; a long
+// average gets a cluster whatever the grid.
+kdn_status plan(const GatedArgs& a, const void* kernel, size_t smem, int V, int K, double fixed, Cut* cut) {
     Resident held;
     const cudaError_t e = resident(kernel, smem, &held);
     if (e != cudaSuccess) return from_cuda(e);
@@ -871,33 +874,42 @@ kdn_status plan(const GatedArgs& a, const void* kernel, size_t smem, int V, int 
     cut->len = a.T;
     const int tile = NW * K;
     const long long rows = state_rows(a), units = rows * cut->slabs;
-    const long long len = a.nseq > 0 ? (a.T + a.nseq - 1) / a.nseq : a.T, tiles = (len + tile - 1) / tile;
+    const long long len = a.nseq > 0 ? (a.T + a.nseq - 1) / a.nseq : a.T;
     static const double cost[MAX_CLUSTER] = {1, 1.04, 1.10, 1.16, 1.23, 1.30, 1.37, 1.44};
+    constexpr double START = 1.5, SECOND_READ = 1.0;
     double best = DBL_MAX;
-    for (int S = 1; S <= MAX_CLUSTER && (S == 1 || S <= tiles); ++S) {
-        const int n = held.clusters[S - 1];
-        if (n < 1) continue;
-        double t = static_cast<double>((units + n - 1) / n) * static_cast<double>((tiles + S - 1) / S) * cost[S - 1];
-        if (units * S <= sm_count()) t *= 0.65;
-        if (t < best * 0.98) {
-            best = t;
-            cut->S = S;
+    auto consider = [&](long long parts, long long tokens, double more) {
+        const long long tiles = (tokens + tile - 1) / tile, n = units * parts;
+        for (int S = 1; S <= MAX_CLUSTER && (S == 1 || S <= tiles); ++S) {
+            const int h = held.clusters[S - 1];
+            if (h < 1) continue;
+            double t = static_cast<double>((n + h - 1) / h) *
+                       (static_cast<double>((tiles + S - 1) / S) * cost[S - 1] + START);
+            if (n * S <= sm_count()) t *= 0.65;
+            if (t + more < best * 0.98) {
+                best = t + more;
+                cut->S = S;
+                cut->parts = static_cast<int>(parts);
+                cut->len = static_cast<int>(tokens);
+            }
         }
-    }
+    };
+    consider(1, len, 0.0);
     if (a.nseq > 0) {
-        const long long s = tiles / 4 < MAX_CLUSTER ? tiles / 4 : MAX_CLUSTER;
+        const long long s = len / tile / 4 < MAX_CLUSTER ? len / tile / 4 : MAX_CLUSTER;
         if (cut->S < s && held.clusters[s - 1] > 0) cut->S = static_cast<int>(s);
-    } else if (cut->S == MAX_CLUSTER) {
-        const int bound = most_parts(rows, a.C, a.T);
-        const long long rounds = (tiles + MAX_CLUSTER - 1) / MAX_CLUSTER;
-        long long n = held.clusters[MAX_CLUSTER - 1] / units;
-        if (n > rounds / 4) n = rounds / 4;
-        if (n > bound) n = bound;
-        if (n > 1 && rounds - rounds / n >= worth) {
-            cut->len = static_cast<int>((rounds + n - 1) / n) * MAX_CLUSTER * tile;
-            cut->parts = (a.T + cut->len - 1) / cut->len;
-        }
+        return KDN_OK;
     }
+    const long long bound = most_parts(rows, a.C, a.T), maps = maps_of(a.T);
+    long long n = held.clusters[0] / units;
+    if (n > bound) n = bound;
+    if (n > 1) {
+        const long long each = (maps + n - 1) / n;                    // maps of a part
+        const long long tokens = each * MAP_TOKENS;
+        const double again = SECOND_READ * static_cast<double>(units * ((a.T + tile - 1) / tile)) / held.clusters[0];
+        consider((maps + each - 1) / each, tokens, again + fixed);
+    }
+    if (cut->parts == 1) cut->len = a.T;
     return KDN_OK;
 }
 
@@ -933,20 +945,20 @@ struct Scratch {
 template <typename TI, typename TO, bool LEAK, bool BWD>
 kdn_status launch_maps(const GatedArgs& a, float4* maps, cudaStream_t stream) {
     // (parts are for few channels: this is under 2^31)
-    const long long blocks = state_rows(a) * ((a.T + MAP_TOKENS - 1) / MAP_TOKENS) * ((a.C + 31) / 32);
+    const long long blocks = state_rows(a) * maps_of(a.T) * ((a.C + 31) / 32);
     gated_maps_kernel<TI, TO, LEAK, BWD><<<static_cast<unsigned>(blocks), NW * 32, 0, stream>>>(a, maps);
     return from_cuda(cudaGetLastError());
 }
 
-long long maps_bytes(long long rows, int parts, int C, int T) {
-    return parts > 1 ? rows * ((T + MAP_TOKENS - 1) / MAP_TOKENS) * C * 16 : 0;
+long long maps_bytes(long long rows, long long parts, int C, int T) {
+    return parts > 1 ? rows * maps_of(T) * C * 16 : 0;
 }
 
 }  // namespace
 
 long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq) {
     const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
-    const int parts = nseq > 0 ? 1 : most_parts(rows, C, T);
+    const long long parts = nseq > 0 ? 1 : most_parts(rows, C, T);
     return maps_bytes(rows, parts, C, T) + (rows / H * parts > 1 ? rows * parts * C * 4 : 0);
 }
 
@@ -961,7 +973,7 @@ kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
             const size_t smem = sizeof(FwdShared<TI, TO, V, FWD_K>);
             Cut cut{};
             cut.wait_ns = wait_ns;
-            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, FWD_K, 12, &cut);
+            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, FWD_K, 9.0, &cut);
             if (s != KDN_OK) return s;
             Scratch scratch(stream);
             if (cut.parts > 1) {
@@ -994,7 +1006,7 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
             const size_t smem = sizeof(BwdShared<TI, TO, V, BWD_K>);
             Cut cut{};
             cut.wait_ns = wait_ns;
-            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, BWD_K, a.workspace ? 4 : 12, &cut);
+            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, BWD_K, a.workspace ? 3.5 : 9.0, &cut);
             if (s != KDN_OK) return s;
             const long long rows = state_rows(a), shares = rows / a.H * cut.parts;
             const long long maps = maps_bytes(rows, cut.parts, a.C, a.T), HC = static_cast<long long>(a.H) * a.C;

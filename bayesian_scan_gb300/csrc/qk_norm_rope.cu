@@ -20,6 +20,7 @@
 
 #include "gated_device.cuh"
 #include "kdn_internal.h"
+#include "kernel_setup.h"
 #include "sum_rows.cuh"
 
 namespace kdn {
@@ -371,12 +372,12 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
             const TI* x = static_cast<const TI*>(p.x[which]) + at.token * p.ld[which] + at.h * DK;
             TO* y = static_cast<TO*>(p.y[which]) +
                     ((static_cast<long long>(at.b) * H + at.h) * p.T + at.t) * DK;
-            // steps whose rows are all there, UNROLL rows' loads in flight
-            const int whole = __all_sync(0xffffffffu, at.here && at.h + (steps - 1) * step < H) ? steps : steps - 1;
-            int i = 0;
-            if (__all_sync(0xffffffffu, at.here))
-                for (; i + UNROLL <= whole; i += UNROLL) {
-                    RawRow<TI> raw[UNROLL];
+            // UNROLL rows' loads in flight; a batch whose rows are all there has no predicates
+            const int whole = !__all_sync(0xffffffffu, at.here) ? 0
+                              : __all_sync(0xffffffffu, at.h + (steps - 1) * step < H) ? steps : steps - 1;
+            for (int i = 0; i < steps; i += UNROLL) {
+                RawRow<TI> raw[UNROLL];
+                if (i + UNROLL <= whole) {
 #pragma unroll
                     for (int u = 0; u < UNROLL; ++u) {
                         raw[u] = get_raw(x, q);
@@ -387,14 +388,20 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
                         qk_row<TI, TO, DK, INTER>(p, raw[u], w, turn, q, y, true);
                         y += ystep;
                     }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < UNROLL; ++u) {
+                        raw[u] = RawRow<TI>{};
+                        if (at.here && at.h + (i + u) * step < H) raw[u] = get_raw(x, q);
+                        x += xstep;
+                    }
+#pragma unroll
+                    for (int u = 0; u < UNROLL; ++u) {
+                        if (i + u >= steps) break;             // (the warp as one)
+                        qk_row<TI, TO, DK, INTER>(p, raw[u], w, turn, q, y, at.here && at.h + (i + u) * step < H);
+                        y += ystep;
+                    }
                 }
-            for (; i < steps; ++i) {
-                const bool on = at.here && at.h + i * step < H;
-                RawRow<TI> raw{};
-                if (on) raw = get_raw(x, q);
-                qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, on);
-                x += xstep;
-                y += ystep;
             }
         }
     }
@@ -606,8 +613,8 @@ kdn_status qk_bwd_launch(const QkArgs& a, cudaStream_t stream) {
             using TO = decltype(to);
             constexpr int DK = decltype(n)::value;
             auto kernel = a.interleaved ? qk_bwd_kernel<TI, TO, DK, true> : qk_bwd_kernel<TI, TO, DK, false>;
-            const int smem = sizeof(BwdRing<TI, TO, BWD_DEPTH>);
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            const size_t smem = sizeof(BwdRing<TI, TO, BWD_DEPTH>);
+            const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
             if (e != cudaSuccess) return from_cuda(e);
             kernel<<<blocks, WARPS * 32, smem, stream>>>(a, deal, part);
             return from_cuda(cudaGetLastError());

@@ -423,6 +423,16 @@ def mobius_scan(a, b, c, d, lambda0, out=None, stream=None):
 # the recurrence with one gate per channel
 
 _DTYPES = {torch.bfloat16: KDN_BF16, torch.float32: KDN_F32}
+_F32 = torch.float32
+
+
+def _new(like, dtype):
+    """An uninitialised dense tensor of like's shape."""
+    if dtype is None or dtype is like.dtype:
+        if like.is_contiguous():
+            return torch.empty_like(like)
+        dtype = like.dtype
+    return torch.empty(like.shape, device=like.device, dtype=dtype)
 
 
 def _dtype_of(t, name):
@@ -438,9 +448,9 @@ def _token_ld(t, name, dt, shape):
     for one head a column slice of a wider projection)."""
     if t.dtype != dt:
         raise ValueError(f"{name} must be {dt}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    T, C = shape[-2:]
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, C = shape[-2], shape[-1]
     if t.is_contiguous():
         return C
     st = t.stride()
@@ -489,20 +499,21 @@ def gated_scan_fwd(x, d, A, h0=None, leak=False, offsets=None, out=None, out_dty
     here that lie in no sequence are undefined."""
     B, H, T, C, nseq, state = _gated_sizes(x, A, offsets)
     it = _dtype_of(x, "x")
-    x_ld = _token_ld(x, "x", x.dtype, tuple(x.shape))
-    d_ld = _token_ld(d, "d", x.dtype, tuple(x.shape))
+    x_ld = _token_ld(x, "x", x.dtype, x.shape)
+    d_ld = _token_ld(d, "d", x.dtype, x.shape)
     if h0 is not None:
         _check(h0, "h0", torch.float32, state)
     if out is None:
-        out = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
-    _check(out, "out", out_dtype, x.shape)
+        out = _new(x, out_dtype)
+    else:
+        _check(out, "out", out_dtype, x.shape)
     ot = _dtype_of(out, "out")
     if final_state is True:
-        final_state = torch.empty(state, device=x.device, dtype=torch.float32)
+        final_state = torch.empty(state, device=x.device, dtype=_F32)
     elif final_state is False:
         final_state = None
-    if final_state is not None:
-        _check(final_state, "final_state", torch.float32, state)
+    elif final_state is not None:
+        _check(final_state, "final_state", _F32, state)
     _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, final_state=final_state)
     st = lib.kdn_gated_scan_fwd(_ptr(x), x_ld, _ptr(d), d_ld, _ptr(A), _ptr(h0), _ptr(offsets), nseq,
                                 int(leak), _ptr(out), _ptr(final_state), B, H, T, C, it, ot,
@@ -532,8 +543,8 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
     None (one is taken from torch's caching allocator for the call)."""
     B, H, T, C, nseq, state = _gated_sizes(x, A, offsets)
     it = _dtype_of(x, "x")
-    x_ld = _token_ld(x, "x", x.dtype, tuple(x.shape))
-    d_ld = _token_ld(d, "d", x.dtype, tuple(x.shape))
+    x_ld = _token_ld(x, "x", x.dtype, x.shape)
+    d_ld = _token_ld(d, "d", x.dtype, x.shape)
     ot = _dtype_of(out, "out")
     _check(out, "out", None, x.shape)
     _check(grad_out, "grad_out", out.dtype, x.shape)
@@ -542,15 +553,18 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
             _check(t, name, torch.float32, state)
     g = {}
     for name, t in (("x", grad_x), ("d", grad_d)):
-        g[name] = torch.empty(x.shape, device=x.device, dtype=x.dtype) if t is None else t
-        _check(g[name], "grad_" + name, x.dtype, x.shape)
+        if t is None:
+            t = _new(x, None)
+        else:
+            _check(t, "grad_" + name, x.dtype, x.shape)
+        g[name] = t
     for name, t, shape in (("A", grad_A, tuple(A.shape)), ("h0", grad_h0, state)):
         if t is True:
-            t = torch.empty(shape, device=x.device, dtype=torch.float32)
+            t = torch.empty(shape, device=x.device, dtype=_F32)
         elif t is False:
             t = None
-        if t is not None:
-            _check(t, "grad_" + name, torch.float32, shape)
+        elif t is not None:
+            _check(t, "grad_" + name, _F32, shape)
         g[name] = t
     ws_bytes = gated_scan_bwd_workspace(B, H, T, C, nseq)
     if workspace is None:
@@ -576,24 +590,37 @@ def gated_step(x, d, A, state, leak=False, new_state=None, out=None, out_dtype=N
     fp32 of x's shape, updated in place, or left as it is when ``new_state``
     is another tensor to write.  Returns out (x's type unless ``out_dtype``
     says otherwise)."""
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x must be [B,C] or [B,H,C], got {tuple(x.shape)}")
+    shape, dt = x.shape, x.dtype
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x must be [B,C] or [B,H,C], got {tuple(shape)}")
     it = _dtype_of(x, "x")
-    shape = x.shape
     if new_state is None:
         new_state = state
     if out is None:
-        out = torch.empty(shape, device=x.device, dtype=out_dtype or x.dtype)
-    _check(x, "x")
-    _check(d, "d", x.dtype, shape)
-    _check(A, "A", torch.float32, shape[1:])
-    _check(state, "state", torch.float32, shape)
-    _check(new_state, "new_state", torch.float32, shape)
-    _check(out, "out", out_dtype, shape)
+        out = _new(x, out_dtype)
+    heads = shape[1:]
+    # a step is a few microseconds: one expression where all is well, the
+    # messages where it is not
+    if not (d.dtype is dt and A.dtype is _F32 and state.dtype is _F32 and new_state.dtype is _F32
+            and (out_dtype is None or out.dtype is out_dtype)
+            and d.shape == shape and state.shape == shape and new_state.shape == shape and out.shape == shape
+            and A.shape == heads and x.is_contiguous() and d.is_contiguous() and A.is_contiguous()
+            and state.is_contiguous() and new_state.is_contiguous() and out.is_contiguous()):
+        _check(x, "x")
+        _check(d, "d", dt, shape)
+        _check(A, "A", _F32, heads)
+        _check(state, "state", _F32, shape)
+        _check(new_state, "new_state", _F32, shape)
+        _check(out, "out", out_dtype, shape)
     ot = _dtype_of(out, "out")
-    _on_one_device(stream, x=x, d=d, A=A, state=state, new_state=new_state, out=out)
-    st = lib.kdn_gated_step(_ptr(x), _ptr(d), _ptr(A), int(leak), _ptr(state), _ptr(new_state), _ptr(out),
-                            shape[0], 1 if x.dim() == 2 else shape[1], shape[-1], it, ot, _stream(stream))
+    dev = x.get_device()
+    if not (stream is None and dev >= 0 and dev == torch._C._cuda_getDevice() and d.get_device() == dev
+            and A.get_device() == dev and state.get_device() == dev and new_state.get_device() == dev
+            and out.get_device() == dev):
+        _on_one_device(stream, x=x, d=d, A=A, state=state, new_state=new_state, out=out)
+    st = lib.kdn_gated_step(x.data_ptr(), d.data_ptr(), A.data_ptr(), int(leak), state.data_ptr(),
+                            new_state.data_ptr(), out.data_ptr(), shape[0], 1 if len(shape) == 2 else shape[1],
+                            shape[-1], it, ot, _stream(stream))
     if st != KDN_OK:
         raise KdnError(st, "kdn_gated_step")
     return out
@@ -609,11 +636,12 @@ _NORMS = {"none": KDN_NORM_NONE, "rms": KDN_NORM_RMS, "l2": KDN_NORM_L2}
 def _head_rows(t, name, dt, B, T, dk):
     """(heads, elements between tokens) of a [B,T,H,dk] tensor whose heads lie
     side by side (dense, or a column slice of a fused projection)."""
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.shape[3] != dk:
-        raise ValueError(f"{name} must be [{B},{T},heads,{dk}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != dk:
+        raise ValueError(f"{name} must be [{B},{T},heads,{dk}], got {tuple(shape)}")
     if t.dtype != dt:
         raise ValueError(f"{name} must be {dt}, got {t.dtype}")
-    H = t.shape[2]
+    H = shape[2]
     if t.is_contiguous():
         return H, H * dk
     st = t.stride()
@@ -681,7 +709,8 @@ def qk_norm_rope_fwd(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms"
         else:
             if o is None:
                 o = torch.empty((B, H, T, dk), device=t.device, dtype=out_dtype or t.dtype)
-            _check(o, name, out_dtype, (B, H, T, dk))
+            else:
+                _check(o, name, out_dtype, (B, H, T, dk))
         outs.append(o)
     out_dt = next(o for o in outs if o is not None)
     ot = _dtype_of(out_dt, "out")
@@ -729,10 +758,13 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
             raise ValueError(f"grad_{name}_out must be given with {name}")
         _check(go, f"grad_{name}_out", None, (B, H, T, dk))
         gts.append(go.dtype)
-        g[name] = torch.empty((B, T, H, dk), device=t.device, dtype=t.dtype) if gx is None else gx
-        n, lds[name] = _head_rows(g[name], "grad_" + name, t.dtype, B, T, dk)
-        if n != H:
-            raise ValueError(f"grad_{name} must have {H} heads, got {n}")
+        if gx is None:
+            g[name], lds[name] = torch.empty((B, T, H, dk), device=t.device, dtype=t.dtype), H * dk
+        else:
+            g[name] = gx
+            n, lds[name] = _head_rows(gx, "grad_" + name, t.dtype, B, T, dk)
+            if n != H:
+                raise ValueError(f"grad_{name} must have {H} heads, got {n}")
         if (w is not None) if grad_w is None else grad_w:
             g["w" + name] = torch.empty(dk, device=t.device, dtype=torch.float32)
     if len(set(gts)) > 1:
