@@ -184,8 +184,8 @@ __device__ __forceinline__ void cluster_sync() {
 template <int V>
 struct Fold {
     MapWords<V> warp[2][NW];
-    MapWords<V> cta[2][MAX_CLUSTER];
     uint64_t full[2];
+    MapWords<V> cta[2][MAX_CLUSTER];   // last: a CTA alone has no memory for it
 
     // Every CTA of the cluster runs, its barriers set up, before one sends.
     __device__ __forceinline__ void begin(int S) {
@@ -477,15 +477,20 @@ gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
             if (c + v < p.C) p.final_state[at.sr * p.C + c + v] = carry[v];
 }
 
-template <typename TI, typename TO, int V, int K>
+// grad d overwrites d; grad x overwrites x, or, where K is twice BWD_K and
+// there is no room for x, g.
+template <typename TI, typename TO, int V, int K, bool LEAK>
 struct BwdShared {
     static constexpr int ROW = 32 * V * static_cast<int>(sizeof(TI)), OROW = 32 * V * static_cast<int>(sizeof(TO));
+    static constexpr bool X = K == BWD_K;
+    static_assert(X || (!LEAK && sizeof(TI) == sizeof(TO)), "g takes grad x");
     struct __align__(16) Stage {
-        char d[K * ROW], x[K * ROW], g[K * OROW], h[K * OROW];   // grad d overwrites d, grad x x
+        char d[K * ROW], x[X ? K * ROW : 16], g[K * OROW], h[K * OROW];
+        __device__ __forceinline__ char* grad_x() { return X ? x : g; }
     };
     Stage st[STAGES][NW];
-    Fold<V> fold;
     float dA[V][32];
+    Fold<V> fold;
 };
 
 // The same walk from the last token to the first.  `sums` [sequence, part, H,
@@ -493,7 +498,7 @@ struct BwdShared {
 template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
 __global__ void __launch_bounds__(NW * 32, 2)
 gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cut cut, float* sums) {
-    using Sh = BwdShared<TI, TO, V, K>;
+    using Sh = BwdShared<TI, TO, V, K, LEAK>;
     extern __shared__ __align__(16) char smem[];
     Sh& sh = *reinterpret_cast<Sh*>(smem);
     const Place<V, K> at(p, cut);
@@ -635,7 +640,7 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
                 if (SIZE == 16) {
                     Vec<TI, V> q;
                     q.set(gx);
-                    poke<TI, V>(st.x + j * Sh::ROW + lane * V * sizeof(TI), q);
+                    poke<TI, V>(st.grad_x() + j * Sh::ROW + lane * V * sizeof(TI), q);
                     q.set(gd);
                     poke<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI), q);
                 } else if (t + j >= at.lo) {
@@ -651,7 +656,7 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
             if (SIZE == 16) {
                 const int f = max(at.lo - t, 0);
                 const long long ld = p.C * static_cast<long long>(sizeof(TI));
-                rows_out<Sh::ROW, K>(reinterpret_cast<char*>(gx_out), ld, st.x, f, K, width, lane);
+                rows_out<Sh::ROW, K>(reinterpret_cast<char*>(gx_out), ld, st.grad_x(), f, K, width, lane);
                 rows_out<Sh::ROW, K>(reinterpret_cast<char*>(gd_out), ld, st.d, f, K, width, lane);
                 __syncwarp();
             }
@@ -800,7 +805,7 @@ struct Resident {
     int clusters[MAX_CLUSTER];
 };
 
-cudaError_t resident(const void* kernel, size_t smem, Resident* out) {
+cudaError_t resident(const void* kernel, size_t alone, size_t smem, Resident* out) {
     static std::mutex lock;
     static std::map<std::pair<int, const void*>, Resident> known;
     int dev = 0;
@@ -813,7 +818,7 @@ cudaError_t resident(const void* kernel, size_t smem, Resident* out) {
         e = allow_smem(kernel, smem);
         if (e != cudaSuccess) return e;
         int n = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NW * 32, smem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NW * 32, alone);
         if (e != cudaSuccess) return e;
         r.clusters[0] = n * sm_count();
         for (int S = 2; S <= MAX_CLUSTER; ++S) {
@@ -865,9 +870,9 @@ long long most_parts(long long rows, int C, int T) {
 //
 // Packed sequences have one length on average and may have others; a long
 // average gets a cluster whatever the grid.
-kdn_status plan(const GatedArgs& a, const void* kernel, size_t smem, int V, int K, double fixed, Cut* cut) {
+kdn_status plan(const GatedArgs& a, const void* kernel, size_t alone, size_t smem, int V, int K, double fixed, Cut* cut) {
     Resident held;
-    const cudaError_t e = resident(kernel, smem, &held);
+    const cudaError_t e = resident(kernel, alone, smem, &held);
     if (e != cudaSuccess) return from_cuda(e);
     cut->slabs = (a.C + 32 * V - 1) / (32 * V);
     cut->S = cut->parts = 1;
@@ -912,6 +917,14 @@ kdn_status plan(const GatedArgs& a, const void* kernel, size_t smem, int V, int 
     if (cut->parts == 1) cut->len = a.T;
     return KDN_OK;
 }
+
+// A kernel's shared memory, and without what only clusters use.
+template <typename Sh>
+struct Sizes {
+    static constexpr size_t alone = sizeof(Sh) - sizeof(Sh::fold.cta);
+    static constexpr size_t smem() { return sizeof(Sh); }
+    static size_t of(const Cut& cut) { return cut.S > 1 ? smem() : alone; }
+};
 
 template <typename... KArgs, typename... Args>
 kdn_status launch_walk(void (*kernel)(KArgs...), long long rows, const Cut& cut, size_t smem, cudaStream_t stream, Args... args) {
@@ -970,10 +983,10 @@ kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
         auto go = [&](auto leak, auto size) {
             constexpr bool L = decltype(leak)::value;
             auto kernel = gated_fwd_kernel<TI, TO, V, FWD_K, L, decltype(size)::value>;
-            const size_t smem = sizeof(FwdShared<TI, TO, V, FWD_K>);
+            using Sh = FwdShared<TI, TO, V, FWD_K>;
             Cut cut{};
             cut.wait_ns = wait_ns;
-            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, FWD_K, 9.0, &cut);
+            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), Sizes<Sh>::alone, Sizes<Sh>::smem(), V, FWD_K, 9.0, &cut);
             if (s != KDN_OK) return s;
             Scratch scratch(stream);
             if (cut.parts > 1) {
@@ -983,7 +996,7 @@ kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
                 s = launch_maps<TI, TO, L, false>(a, static_cast<float4*>(scratch.p), stream);
                 if (s != KDN_OK) return s;
             }
-            return launch_walk(kernel, state_rows(a), cut, smem, stream, a, cut);
+            return launch_walk(kernel, state_rows(a), cut, Sizes<Sh>::of(cut), stream, a, cut);
         };
         auto sized = [&](auto leak) {
             if (rows_ok(a, 16)) return go(leak, std::integral_constant<int, 16>());
@@ -1002,12 +1015,27 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
         constexpr int V = std::is_same<TI, __nv_bfloat16>::value ? 2 : 1;
         auto go = [&](auto leak, auto size) {
             constexpr bool L = decltype(leak)::value;
-            auto kernel = gated_bwd_kernel<TI, TO, V, BWD_K, L, decltype(size)::value>;
-            const size_t smem = sizeof(BwdShared<TI, TO, V, BWD_K>);
+            constexpr int SIZE = decltype(size)::value;
+            auto kernel = gated_bwd_kernel<TI, TO, V, BWD_K, L, SIZE>;
+            using Sh = BwdShared<TI, TO, V, BWD_K, L>;
             Cut cut{};
             cut.wait_ns = wait_ns;
-            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), smem, V, BWD_K, a.workspace ? 3.5 : 9.0, &cut);
+            kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), Sizes<Sh>::alone, Sizes<Sh>::smem(), V, BWD_K,
+                                a.workspace ? 3.5 : 9.0, &cut);
             if (s != KDN_OK) return s;
+            size_t smem = Sizes<Sh>::of(cut);
+            // twice the tokens a round where that still leaves two CTAs to an SM: 16-bit rows, no x,
+            // no cluster
+            if constexpr (!L && SIZE == 16 && sizeof(TI) == 2 && sizeof(TO) == 2) {
+                using Wide = BwdShared<TI, TO, V, 2 * BWD_K, L>;
+                auto wide = gated_bwd_kernel<TI, TO, V, 2 * BWD_K, L, SIZE>;
+                if (cut.S == 1 && cut.parts == 1) {
+                    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(wide), Sizes<Wide>::alone);
+                    if (e != cudaSuccess) return from_cuda(e);
+                    kernel = wide;
+                    smem = Sizes<Wide>::alone;
+                }
+            }
             const long long rows = state_rows(a), shares = rows / a.H * cut.parts;
             const long long maps = maps_bytes(rows, cut.parts, a.C, a.T), HC = static_cast<long long>(a.H) * a.C;
             const long long bytes = maps + (shares > 1 && a.grad_A ? shares * HC * 4 : 0);
