@@ -44,6 +44,8 @@ namespace {
 
 using namespace gated;
 
+// The largest portable cluster.  (Nine CTAs, four such clusters to a GPC's 38
+// slots, took as long as eight on 65536 x 2048.)
 constexpr int MAX_CLUSTER = 8;
 constexpr int NW = 8;             // warps per CTA
 constexpr int FWD_K = 16, BWD_K = 8;
@@ -58,6 +60,7 @@ struct Cut {
     int slabs, S, parts, len;
     const float4* maps;    // [state row, T / MAP_TOKENS, C]: {a, e, s, z}
     long long wait_ns;     // limit of one wait inside a cluster
+    int stall;             // fault injection: the rank that sends nothing (-1: none)
 };
 
 // A warp's place: its channels, its part's tokens [lo, hi) of the T-token row
@@ -172,20 +175,26 @@ __device__ __forceinline__ void cluster_sync() {
 
 // Folding the maps of a round.  Every warp hands in its map; on return
 // `start` is the state before the warp's tokens and `carry` the one after the
-// round's last tile, both from the carry before the round.  Rounds alternate
-// between two buffers, so one barrier a round is enough.
+// round's last tile, both from the carry before the round.  One warp, another
+// each round, does what the CTA has in common (by all warps alike it was a
+// fifth of the kernel's instructions: 65536 x 2048 247 us, so 212 us).
 //
 // In a cluster the tile's map goes to every CTA's shared memory by stores
 // that complete on the receiver's mbarrier: no fence waits for the round's
 // global stores, as the cluster barrier's release would (an eighth of the
-// time).  A CTA sends round r only after all its warps have read round r - 2,
-// and receives all of round r - 1 before it sends round r, so no store finds
-// its buffer in use.
+// time).  A CTA sends round r after a barrier that the reader of its round r -
+// 2 has passed, and receives all of round r - 1 before it sends round r, so no
+// store finds its buffer in use.
 template <int V>
 struct Fold {
-    MapWords<V> warp[2][NW];
+    MapWords<V> warp[2][NW];           // a round's maps; alone [0], and in [1] the warps' starts
     uint64_t full[2];
-    MapWords<V> cta[2][MAX_CLUSTER];   // last: a CTA alone has no memory for it
+    // a CTA alone has no memory from here on
+    MapWords<V> cta[2][MAX_CLUSTER];
+    float start[V][32], carry[V][32];
+    int late;                          // a wait ran out: no more sends and waits
+
+    __device__ __forceinline__ float* starts(int w) { return reinterpret_cast<float*>(warp[1]) + w * V * 32; }
 
     // Every CTA of the cluster runs, its barriers set up, before one sends.
     __device__ __forceinline__ void begin(int S) {
@@ -194,12 +203,13 @@ struct Fold {
                 mbar_init(&full[0], 1);
                 mbar_init(&full[1], 1);
                 mbar_init_fence();
+                late = 0;
             }
             cluster_sync();
         }
     }
     // No CTA leaves while another may still send to it.
-    __device__ __forceinline__ void end(int S, bool late) {
+    __device__ __forceinline__ void end(int S) {
         if (S > 1) {
             cluster_sync();
             if (late) {   // what was sent and not waited for arrives in the meantime
@@ -222,16 +232,20 @@ __device__ __forceinline__ bool full_try(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded: after limit_ns it records an error and no later round waits.
-__device__ __forceinline__ void full_wait(uint64_t* bar, uint32_t parity, long long limit_ns, bool& late) {
-    if (late || full_try(bar, parity)) return;
-    const unsigned long long t0 = globaltimer_ns();
-    while (!full_try(bar, parity))
-        if (static_cast<long long>(globaltimer_ns() - t0) > limit_ns) {
+// Bounded: after limit_ns it records an error and returns false.  (The timer
+// is read once per 64 tries: a read costs more than a try.)
+__device__ __forceinline__ bool full_wait(uint64_t* bar, uint32_t parity, long long limit_ns) {
+    unsigned long long t0 = 0;
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (full_try(bar, parity)) return true;
+        const unsigned long long t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (static_cast<long long>(t - t0) > limit_ns) {
             record_error(&g_gated_error, KDN_ERR_TIMEOUT);
-            late = true;
-            return;
+            return false;
         }
+    }
 }
 
 __device__ __forceinline__ void send(uint32_t dst, float4 v, uint32_t bar) {
@@ -252,27 +266,56 @@ __device__ __forceinline__ float from_rank(const float* p, int rank) {
 }
 
 template <int V>
-__device__ __forceinline__ void fold_round(Fold<V>& f, int r, int S, int rank, int warp, int lane, long long limit_ns,
-                                           bool& late, const float (&z)[V], const float (&s)[V], float (&carry)[V],
+__device__ __forceinline__ void fold_round(Fold<V>& f, const Cut& cut, int r, int rank, int warp, int lane,
+                                           const float (&z)[V], const float (&s)[V], float (&carry)[V],
                                            float (&start)[V]) {
+    const int S = cut.S;
+    if (S == 1) {
+        // the folding warp works out every warp's start; the next round's first barrier comes after
+        // all have read theirs
+        put_map<V>(f.warp[0][warp], lane, map_of<V>(z, s));
+        __syncthreads();
+        if (warp == r % NW) {
+            float h[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = carry[v];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) f.starts(w)[v * 32 + lane] = h[v];
+                apply<V>(get_map<V>(f.warp[0][w], lane), h);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) f.starts(NW)[v * 32 + lane] = h[v];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            start[v] = f.starts(warp)[v * 32 + lane];
+            carry[v] = f.starts(NW)[v * 32 + lane];
+        }
+        return;
+    }
     const int buf = r & 1;
     put_map<V>(f.warp[buf][warp], lane, map_of<V>(z, s));
     __syncthreads();
-    if (S > 1) {
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(&f.full[buf], S * sizeof(MapWords<V>));
-        if (warp < S) {   // warp j sends the tile's map to CTA j
-            float h[V], zz[V];
+    if (warp == r % NW) {
+        // it composes the tile's map, sends it to every CTA and takes the round's maps in
+        const bool late = f.late;
+        if (lane == 0 && !late) mbar_arrive_expect_tx(&f.full[buf], S * sizeof(MapWords<V>));
+        float h[V], zz[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = zz[v] = 0.f;
+        for (int v = 0; v < V; ++v) h[v] = zz[v] = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const Map<V> m = get_map<V>(f.warp[buf][w], lane);
-                apply<V>(m, h);
+        for (int w = 0; w < NW; ++w) {
+            const Map<V> m = get_map<V>(f.warp[buf][w], lane);
+            apply<V>(m, h);
 #pragma unroll
-                for (int v = 0; v < V; ++v) zz[v] += m.z[v];
-            }
-            const Map<V> m = map_of<V>(zz, h);
-            const uint32_t to = at_rank(&f.cta[buf][rank][0][lane], warp), bar = at_rank(&f.full[buf], warp);
+            for (int v = 0; v < V; ++v) zz[v] += m.z[v];
+        }
+        const Map<V> m = map_of<V>(zz, h);
+        for (int j = 0; j < S && !late && rank != cut.stall; ++j) {
+            const uint32_t to = at_rank(&f.cta[buf][rank][0][lane], j), bar = at_rank(&f.full[buf], j);
             if constexpr (V == 1) {
                 send(to, make_float4(m.a[0], m.e[0], m.s[0], m.z[0]), bar);
             } else {
@@ -280,27 +323,26 @@ __device__ __forceinline__ void fold_round(Fold<V>& f, int r, int S, int rank, i
                 send(to + 512, make_float4(m.s[0], m.s[1], m.z[0], m.z[1]), bar);
             }
         }
-        full_wait(&f.full[buf], (r >> 1) & 1, limit_ns, late);
+        if (!late && !full_wait(&f.full[buf], (r >> 1) & 1, cut.wait_ns)) f.late = 1;
 #pragma unroll
-        for (int v = 0; v < V; ++v) start[v] = carry[v];
+        for (int v = 0; v < V; ++v) h[v] = carry[v];
         for (int j = 0; j < S; ++j) {
             if (j == rank)
 #pragma unroll
-                for (int v = 0; v < V; ++v) start[v] = carry[v];
-            apply<V>(get_map<V>(f.cta[buf][j], lane), carry);
+                for (int v = 0; v < V; ++v) f.start[v][lane] = h[v];
+            apply<V>(get_map<V>(f.cta[buf][j], lane), h);
         }
-        for (int w = 0; w < warp; ++w) apply<V>(get_map<V>(f.warp[buf][w], lane), start);
-    } else {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w == warp)
-#pragma unroll
-                for (int v = 0; v < V; ++v) start[v] = carry[v];
-            apply<V>(get_map<V>(f.warp[buf][w], lane), carry);
-        }
+        for (int v = 0; v < V; ++v) f.carry[v][lane] = h[v];
     }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        start[v] = f.start[v][lane];
+        carry[v] = f.carry[v][lane];
+    }
+    for (int w = 0; w < warp; ++w) apply<V>(get_map<V>(f.warp[buf][w], lane), start);
 }
-static_assert(MAX_CLUSTER <= NW, "a warp sends to one CTA");
 
 // The state that a part starts from: the sequence's carry through the maps of
 // the tokens before the part (those after it, backward).  Each warp composes
@@ -396,7 +438,6 @@ gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
         else copy_commit();
     through_parts<V, false>(p, cut, sh.fold, at.sr, at.part, at.warp, lane, c, carry);
     sh.fold.begin(at.S);
-    bool late = false;
     for (int r = 0; r < at.rounds; ++r) {
         const int n = at.hi - t0 - r * step;
         char* xs = sh.st[r % STAGES][at.warp].x;
@@ -438,7 +479,7 @@ gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
                 }
             }
         }
-        fold_round<V>(sh.fold, r, at.S, at.rank, at.warp, lane, cut.wait_ns, late, z, s, carry, h);
+        fold_round<V>(sh.fold, cut, r, at.rank, at.warp, lane, z, s, carry, h);
         if (n > 0) {
             TO* o = op + static_cast<long long>(r) * step * p.C;
 #pragma unroll
@@ -470,7 +511,7 @@ gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
         if (r + STAGES < at.rounds) fetch(r + STAGES);
         else copy_commit();
     }
-    sh.fold.end(at.S, late);
+    sh.fold.end(at.S);
     if (p.final_state && at.rank == 0 && at.warp == 0 && at.part == cut.parts - 1)
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -547,7 +588,6 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
         else copy_commit();
     through_parts<V, true>(p, cut, sh.fold, at.sr, at.part, at.warp, lane, c, carry);
     sh.fold.begin(at.S);
-    bool late = false;
     for (int r = 0; r < at.rounds; ++r) {
         const int t = base - r * step;
         const bool any = t + K > at.lo;                     // (the warp as one)
@@ -592,7 +632,7 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
                 }
             }
         }
-        fold_round<V>(sh.fold, r, at.S, at.rank, at.warp, lane, cut.wait_ns, late, z, s, carry, u);
+        fold_round<V>(sh.fold, cut, r, at.rank, at.warp, lane, z, s, carry, u);
         if (any) {
             TI* gx_out = static_cast<TI*>(p.grad_x) + (row + t) * p.C + at.c0;
             TI* gd_out = static_cast<TI*>(p.grad_d) + (row + t) * p.C + at.c0;
@@ -679,7 +719,7 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
             }
         if (at.S == 1) __syncwarp();
     }
-    sh.fold.end(at.S, late);
+    sh.fold.end(at.S);
     if (at.rank == 0 && at.warp == 0)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -798,8 +838,8 @@ bool rows_ok(const GatedArgs& a, long long bytes) {
            (!a.x || a.x_ld * is % bytes == 0);
 }
 
-// What the current device holds of a kernel at once: clusters of 1 .. 8 CTAs
-// (0: none).  Asked once per device and kernel, when the kernel's shared
+// What the current device holds of a kernel at once: clusters of 1 .. MAX_CLUSTER
+// CTAs (0: none).  Asked once per device and kernel, when the kernel's shared
 // memory is set up too.
 struct Resident {
     int clusters[MAX_CLUSTER];
@@ -857,11 +897,11 @@ long long most_parts(long long rows, int C, int T) {
 //
 // A wave is what the device holds at once: its CTA slots, or fewer for
 // clusters, which a GPC holds whole.  A cluster's round costs more than a
-// CTA's alone (the exchange), by what was measured on 134 M elements: 4 %
-// with two CTAs, 16 % with four, 44 % with eight; an SM with one CTA does a
+// CTA's alone (the exchange), by what was measured on 134 M elements: 8 %
+// with two CTAs, 14 % with four, 25 % with eight; an SM with one CTA does a
 // round in about two thirds of the time that it takes for two; starting a CTA
-// costs about 1.5 rounds.  So 8 x 4096 x 2048 runs without clusters (80 us,
-// 91 with two CTAs), 65536 x 2048 with eight.
+// costs about 1.5 rounds.  So 8 x 4096 x 2048 runs without clusters (with an
+// earlier fold 80 us, 91 with two CTAs each), 65536 x 2048 with eight.
 //
 // Parts add a pass over two tensors (the walk's own time again: its loads are
 // single elements) and a launch (`fixed` rounds; three and a half, nine with scratch of its own), and make
@@ -880,7 +920,7 @@ kdn_status plan(const GatedArgs& a, const void* kernel, size_t alone, size_t sme
     const int tile = NW * K;
     const long long rows = state_rows(a), units = rows * cut->slabs;
     const long long len = a.nseq > 0 ? (a.T + a.nseq - 1) / a.nseq : a.T;
-    static const double cost[MAX_CLUSTER] = {1, 1.04, 1.10, 1.16, 1.23, 1.30, 1.37, 1.44};
+    static const double cost[MAX_CLUSTER] = {1, 1.08, 1.11, 1.14, 1.17, 1.20, 1.23, 1.25};
     constexpr double START = 1.5, SECOND_READ = 1.0;
     double best = DBL_MAX;
     auto consider = [&](long long parts, long long tokens, double more) {
@@ -921,7 +961,7 @@ kdn_status plan(const GatedArgs& a, const void* kernel, size_t alone, size_t sme
 // A kernel's shared memory, and without what only clusters use.
 template <typename Sh>
 struct Sizes {
-    static constexpr size_t alone = sizeof(Sh) - sizeof(Sh::fold.cta);
+    static constexpr size_t alone = sizeof(Sh) - sizeof(Sh::fold.cta) - sizeof(Sh::fold.start) - sizeof(Sh::fold.carry) - sizeof(Sh::fold.late);
     static constexpr size_t smem() { return sizeof(Sh); }
     static size_t of(const Cut& cut) { return cut.S > 1 ? smem() : alone; }
 };
@@ -975,7 +1015,7 @@ long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq) {
     return maps_bytes(rows, parts, C, T) + (rows / H * parts > 1 ? rows * parts * C * 4 : 0);
 }
 
-kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
+kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns, int stall) {
     return by_type(a.in_dtype, a.out_dtype, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
@@ -986,6 +1026,7 @@ kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
             using Sh = FwdShared<TI, TO, V, FWD_K>;
             Cut cut{};
             cut.wait_ns = wait_ns;
+            cut.stall = stall;
             kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), Sizes<Sh>::alone, Sizes<Sh>::smem(), V, FWD_K, 9.0, &cut);
             if (s != KDN_OK) return s;
             Scratch scratch(stream);
@@ -1008,7 +1049,7 @@ kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
     });
 }
 
-kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns) {
+kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns, int stall) {
     return by_type(a.in_dtype, a.out_dtype, [&](auto ti, auto to) {
         using TI = decltype(ti);
         using TO = decltype(to);
@@ -1020,6 +1061,7 @@ kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long w
             using Sh = BwdShared<TI, TO, V, BWD_K, L>;
             Cut cut{};
             cut.wait_ns = wait_ns;
+            cut.stall = stall;
             kdn_status s = plan(a, reinterpret_cast<const void*>(kernel), Sizes<Sh>::alone, Sizes<Sh>::smem(), V, BWD_K,
                                 a.workspace ? 3.5 : 9.0, &cut);
             if (s != KDN_OK) return s;

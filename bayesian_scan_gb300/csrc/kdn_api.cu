@@ -15,6 +15,7 @@ namespace {
 constexpr long long kDefaultWaitNs = 2000000000LL;   // 2 s of GPU time
 std::atomic<long long> g_wait_ns{kDefaultWaitNs};
 std::atomic<long long> g_stall_tile{-1};
+std::atomic<int> g_stall_rank{-1};
 int g_sm_count[64] = {};
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -356,7 +357,7 @@ kdn_status kdn_gated_scan_fwd(const void* x, long long x_ld, const void* d, long
     a.out = out; a.final_state = final_state;
     const kdn_status s = gated_check(a);
     if (s != KDN_OK) return s;
-    return gated_fwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load());
+    return gated_fwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load(), g_stall_rank.load());
 }
 
 kdn_status kdn_gated_scan_bwd(const void* x, long long x_ld, const void* d, long long d_ld,
@@ -377,7 +378,7 @@ kdn_status kdn_gated_scan_bwd(const void* x, long long x_ld, const void* d, long
     if (workspace && (!aligned(workspace, 256) ||
                       workspace_bytes < gated_bwd_workspace_bytes(B, H, T, C, nseq)))
         return KDN_ERR_INVALID_ARG;
-    return gated_bwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load());
+    return gated_bwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load(), g_stall_rank.load());
 }
 
 kdn_status kdn_gated_scan_bwd_workspace(int B, int H, int T, int C, int nseq, long long* workspace_bytes) {
@@ -485,6 +486,8 @@ kdn_status kdn_get_device_error(void* stream) {
 void kdn_set_wait_limit_ns(long long ns) { g_wait_ns.store(ns > 0 ? ns : kDefaultWaitNs); }
 
 void kdn_debug_stall_mobius_tile(long long tile) { g_stall_tile.store(tile); }
+
+void kdn_debug_stall_gated_rank(int rank) { g_stall_rank.store(rank < 0 ? -1 : rank); }
 
 const char* kdn_version(void) { return "kdn 0.1.0 sm_103a"; }
 

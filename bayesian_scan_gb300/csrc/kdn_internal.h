@@ -117,8 +117,9 @@ struct GatedArgs {
     float* grad_h0;
     void* workspace;
 };
-kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns);
-kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns);
+// (stall: fault injection, -1 for none)
+kdn_status gated_fwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns, int stall);
+kdn_status gated_bwd_launch(const GatedArgs& a, cudaStream_t stream, long long wait_ns, int stall);
 long long gated_bwd_workspace_bytes(int B, int H, int T, int C, int nseq);
 kdn_status gated_step_launch(const void* x, const void* d, const float* A, bool leak,
                              const float* state, float* new_state, void* out, int B, int H, int C,

@@ -17,7 +17,8 @@ Functions mirror the C names:
   the scans)
 * :func:`diag_scan_plan`, :func:`mobius_scan_plan` -> the ``*_plan`` queries
 * :func:`get_device_error`, :func:`set_wait_limit_ns`,
-  :func:`debug_stall_mobius_tile`, :func:`status_string`, :func:`version`
+  :func:`debug_stall_mobius_tile`, :func:`debug_stall_gated_rank`, :func:`status_string`,
+  :func:`version`
 
 When the tensors passed to :func:`diag_scan_fwd` / :func:`mobius_scan` live in
 host memory, the call stages them to the current device on the current stream
@@ -101,6 +102,8 @@ def _load():
     lib.kdn_set_wait_limit_ns.argtypes = [ll]
     lib.kdn_debug_stall_mobius_tile.restype = None
     lib.kdn_debug_stall_mobius_tile.argtypes = [ll]
+    lib.kdn_debug_stall_gated_rank.restype = None
+    lib.kdn_debug_stall_gated_rank.argtypes = [i]
     ip, llp = ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_longlong)
     lib.kdn_diag_scan_plan.restype = i
     lib.kdn_diag_scan_plan.argtypes = [i, i, i, i, i, i, ip, ip, llp]
@@ -845,6 +848,10 @@ def set_wait_limit_ns(ns: int) -> None:
 
 def debug_stall_mobius_tile(tile: int) -> None:
     lib.kdn_debug_stall_mobius_tile(int(tile))
+
+
+def debug_stall_gated_rank(rank: int) -> None:
+    lib.kdn_debug_stall_gated_rank(int(rank))
 
 
 # ---------------------------------------------------------------------------

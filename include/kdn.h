@@ -557,6 +557,15 @@ KDN_API void kdn_set_wait_limit_ns(long long ns);
  */
 KDN_API void kdn_debug_stall_mobius_tile(long long tile);
 
+/*
+ * kdn_debug_stall_gated_rank -- fault injection for tests.  In later
+ * kdn_gated_scan_fwd / _bwd calls that run in clusters, the CTAs of this rank
+ * send nothing to the others of their cluster, whose waits must run out
+ * (KDN_ERR_TIMEOUT; each CTA waits once) instead of hanging.  A negative value
+ * (the default) disables the injection.
+ */
+KDN_API void kdn_debug_stall_gated_rank(int rank);
+
 /* Library version string, e.g. "kdn 0.1.0 sm_103a". */
 KDN_API const char* kdn_version(void);
 

@@ -354,3 +354,90 @@ def test_many_rows():
     # grad A is every row's: against the sum of the parts that grad d is made of (grad d = -A u (h - ..))
     want = (g["d"].double() / A.double().cuda() * d.double().cuda()).sum((0, 2)).cpu()
     assert torch.allclose(g["A"].cpu().double(), want, rtol=0, atol=float(2 ** -24 * 140000 * want.abs().max() + 1e-2))
+
+
+def test_a_cluster_whose_member_sends_nothing_times_out():
+    """Fault injection: one rank of every cluster keeps its maps to itself, so
+    every wait of the cluster runs out, the error is reported and the next
+    call is right again."""
+    from bayesian_scan_gb300 import kdn
+    x, d, A, h0, go, gf = draw(1, 1, 6000, 200, F32, seed=15)
+    cu = [t.cuda() for t in (x, d, A, h0)]
+    assert kdn.get_device_error() == kdn.KDN_OK
+    kdn.set_wait_limit_ns(20_000_000)
+    kdn.debug_stall_gated_rank(1)
+    try:
+        kdn.gated_scan_fwd(*cu[:3], h0=cu[3])
+        assert kdn.get_device_error() == kdn.KDN_ERR_TIMEOUT
+        kdn.gated_scan_bwd(*cu[:3], cu[0], cu[0], h0=cu[3])
+        assert kdn.get_device_error() == kdn.KDN_ERR_TIMEOUT
+    finally:
+        kdn.debug_stall_gated_rank(-1)
+        kdn.set_wait_limit_ns(0)
+    assert kdn.get_device_error() == kdn.KDN_OK
+    check_fwd(x, d, A, h0, False, F32)
+    check_bwd(x, d, A, h0, go, gf, False, F32)
+    assert kdn.get_device_error() == kdn.KDN_OK
+
+
+@pytest.mark.parametrize("in_dtype,out_dtype", TYPES)
+@pytest.mark.parametrize("C", [64, 66, 63])
+def test_clusters_in_every_alignment(C, in_dtype, out_dtype):
+    # several rounds of clusters, rows that allow copies of 16, 4 and 2 bytes, an edge in the last tile
+    x, d, A, h0, go, gf = draw(3, 1, 1300, C, in_dtype, seed=C)
+    for leak in (False, True):
+        check_fwd(x, d, A, h0, leak, out_dtype)
+        check_bwd(x, d, A, h0, go, gf, leak, out_dtype)
+
+
+def test_full_device_without_clusters():
+    # enough rows that the calls run without clusters (the halves below may not): sampled rows against the plain form
+    from bayesian_scan_gb300 import kdn
+    x, d, A, h0, go, gf = draw(20, 1, 400, 1024, BF16, seed=16)
+    o, f = kdn.gated_scan_fwd(x.cuda(), d.cuda(), A.cuda(), h0=h0.cuda())
+    g = kdn.gated_scan_bwd(x.cuda(), d.cuda(), A.cuda(), o, go.bfloat16().cuda(), h0=h0.cuda(), grad_final_state=gf.cuda())
+    pick = [0, 7, 19]
+    ro, rf, eo, ef = plain64.gated_fwd(x[pick], d[pick], A, h0[pick])
+    plain64.assert_within(o[pick], ro, eo, "out")
+    plain64.assert_within(f[pick], rf, ef, "final_state")
+    val, err = plain64.gated_bwd(x[pick], d[pick], A, o.cpu()[pick], go[pick].bfloat16(), h0[pick], g_final=gf[pick])
+    for n in ("x", "d", "h0"):
+        plain64.assert_within(g[n][pick], val[n], err[n], "grad_" + n)
+    # grad A is linear in the rows' gradients: those of two halves of the batch add up to it, each sum
+    # within its own rounding (tokens x half a step) of the magnitudes, here under 3e-4 of the largest
+    half = [kdn.gated_scan_bwd(*(t[s].contiguous().cuda() for t in (x, d)), A.cuda(), o[s].contiguous(),
+                               go[s].bfloat16().cuda(), h0=h0[s].cuda(), grad_final_state=gf[s].cuda())["A"]
+            for s in (slice(0, 10), slice(10, 20))]
+    assert (half[0] + half[1] - g["A"]).abs().max() <= 3e-4 * g["A"].abs().max()
+
+
+def test_two_streams_at_once():
+    from bayesian_scan_gb300 import kdn
+    sets = [[t.cuda() for t in draw(1, 2, 5000, 96, F32, seed=s)] for s in (20, 21)]
+    alone = []
+    for x, d, A, h0, go, gf in sets:
+        o, f = kdn.gated_scan_fwd(x, d, A, h0=h0)
+        alone.append([o, f, *kdn.gated_scan_bwd(x, d, A, o, go, h0=h0, grad_final_state=gf).values()])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for s, (x, d, A, h0, go, gf) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                o, f = kdn.gated_scan_fwd(x, d, A, h0=h0)
+                got.append([o, f, *kdn.gated_scan_bwd(x, d, A, o, go, h0=h0, grad_final_state=gf).values()])
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_a_stream_given_by_hand():
+    from bayesian_scan_gb300 import kdn
+    x, d, A, h0, go, gf = (t.cuda() for t in draw(2, 1, 90, 64, F32, seed=22))
+    ref = kdn.gated_scan_fwd(x, d, A, h0=h0)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    o, f = kdn.gated_scan_fwd(x, d, A, h0=h0, stream=s)
+    y = kdn.gated_step(x[:, :, 0].contiguous(), d[:, :, 0].contiguous(), A, h0.clone(), stream=s)
+    s.synchronize()
+    assert torch.equal(o, ref[0]) and torch.equal(f, ref[1]) and y.shape == h0.shape
