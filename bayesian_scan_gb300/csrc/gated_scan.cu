@@ -50,7 +50,7 @@ constexpr int MAX_CLUSTER = 8;
 constexpr int NW = 8;             // warps per CTA
 constexpr int FWD_K = 16, BWD_K = 8;
 constexpr int STAGES = 2;
-constexpr int MAP_TOKENS = 512;   // of one map where a sequence is cut into parts
+constexpr int MAP_TOKENS = 512, MAP_WARPS = 16;   // of one map where a sequence is cut into parts
 
 __device__ int g_gated_error = 0;
 
@@ -736,12 +736,12 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
 }
 
 // The maps of every MAP_TOKENS tokens of long sequences of few channels: {a,
-// e, s, z}, [state row, T / MAP_TOKENS, C].  A warp composes an eighth of
-// them, a channel per lane, UN tokens' loads in flight.
+// e, s, z}, [state row, T / MAP_TOKENS, C].  A warp composes a
+// sixteenth of them, a channel per lane, UN tokens' loads in flight.
 template <typename TI, typename TO, bool LEAK, bool BWD>
-__global__ void __launch_bounds__(NW * 32) gated_maps_kernel(const __grid_constant__ GatedArgs p, float4* maps) {
-    constexpr int UN = 16, sub = MAP_TOKENS / NW;
-    __shared__ float4 share[NW][32];
+__global__ void __launch_bounds__(MAP_WARPS * 32) gated_maps_kernel(const __grid_constant__ GatedArgs p, float4* maps) {
+    constexpr int UN = 16, sub = MAP_TOKENS / MAP_WARPS;
+    __shared__ float4 share[MAP_WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (p.C + 31) / 32, c = static_cast<int>(blockIdx.x % slabs) * 32 + lane;
     const int all = (p.T + MAP_TOKENS - 1) / MAP_TOKENS;
@@ -784,8 +784,8 @@ __global__ void __launch_bounds__(NW * 32) gated_maps_kernel(const __grid_consta
     __syncthreads();
     if (warp > 0 || !on) return;
     z = s = 0.f;
-    for (int i = 0; i < NW; ++i) {
-        const float4 m = share[BWD ? NW - 1 - i : i][lane];
+    for (int i = 0; i < MAP_WARPS; ++i) {
+        const float4 m = share[BWD ? MAP_WARPS - 1 - i : i][lane];
         const Gate q = gate(m.w);
         s = decay_add(q, s, m.z);
         z += m.w;
@@ -999,7 +999,7 @@ template <typename TI, typename TO, bool LEAK, bool BWD>
 kdn_status launch_maps(const GatedArgs& a, float4* maps, cudaStream_t stream) {
     // (parts are for few channels: this is under 2^31)
     const long long blocks = state_rows(a) * maps_of(a.T) * ((a.C + 31) / 32);
-    gated_maps_kernel<TI, TO, LEAK, BWD><<<static_cast<unsigned>(blocks), NW * 32, 0, stream>>>(a, maps);
+    gated_maps_kernel<TI, TO, LEAK, BWD><<<static_cast<unsigned>(blocks), MAP_WARPS * 32, 0, stream>>>(a, maps);
     return from_cuda(cudaGetLastError());
 }
 
