@@ -28,6 +28,7 @@ copies the results back; it returns host tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -535,6 +536,11 @@ def gated_scan_bwd_workspace(B, H, T, C, nseq=0) -> int:
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=256)
+def _gated_ws(device, B, H, T, C, nseq):
+    return gated_scan_bwd_workspace(B, H, T, C, nseq)
+
+
 def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, grad_final_state=None,
                    grad_x=None, grad_d=None, grad_A=True, grad_h0=True, workspace=None, stream=None):
     """Backward pass of ``gated_scan_fwd`` (see ``kdn_gated_scan_bwd``): x, d,
@@ -563,13 +569,14 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
         g[name] = t
     for name, t, shape in (("A", grad_A, tuple(A.shape)), ("h0", grad_h0, state)):
         if t is True:
-            t = torch.empty(shape, device=x.device, dtype=_F32)
+            like = A if name == "A" else h0
+            t = torch.empty(shape, device=x.device, dtype=_F32) if like is None else torch.empty_like(like)
         elif t is False:
             t = None
         elif t is not None:
             _check(t, "grad_" + name, _F32, shape)
         g[name] = t
-    ws_bytes = gated_scan_bwd_workspace(B, H, T, C, nseq)
+    ws_bytes = _gated_ws(x.get_device(), B, H, T, C, nseq)
     if workspace is None:
         if ws_bytes:
             workspace = torch.empty(ws_bytes, device=x.device, dtype=torch.uint8)
@@ -738,6 +745,11 @@ def qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk) -> int:
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=256)
+def _qk_ws(device, B, T, Hq, Hk, dk):
+    return qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk)
+
+
 def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=None, wk=None, norm="rms",
                      eps=1e-6, axis=None, interleaved=False, grad_q=None, grad_k=None, grad_w=None,
                      workspace=None, stream=None):
@@ -762,14 +774,15 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
         _check(go, f"grad_{name}_out", None, (B, H, T, dk))
         gts.append(go.dtype)
         if gx is None:
-            g[name], lds[name] = torch.empty((B, T, H, dk), device=t.device, dtype=t.dtype), H * dk
+            # (dense: t's heads lie side by side, so what empty_like makes of its order is the plain one)
+            g[name], lds[name] = torch.empty_like(t, memory_format=torch.contiguous_format), H * dk
         else:
             g[name] = gx
             n, lds[name] = _head_rows(gx, "grad_" + name, t.dtype, B, T, dk)
             if n != H:
                 raise ValueError(f"grad_{name} must have {H} heads, got {n}")
         if (w is not None) if grad_w is None else grad_w:
-            g["w" + name] = torch.empty(dk, device=t.device, dtype=torch.float32)
+            g["w" + name] = torch.empty(dk, device=t.device, dtype=_F32) if w is None else torch.empty_like(w)
     if len(set(gts)) > 1:
         raise ValueError("grad_q_out and grad_k_out must have one type")
     ot = _DTYPES.get(gts[0])
@@ -777,7 +790,7 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
         raise ValueError(f"the outputs' gradients must be bf16 or fp32, got {gts[0]}")
     ws_bytes = 0
     if g["wq"] is not None or g["wk"] is not None:
-        ws_bytes = qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk)
+        ws_bytes = _qk_ws(first.get_device(), B, T, Hq, Hk, dk)
         if workspace is None:
             workspace = torch.empty(ws_bytes, device=first.device, dtype=torch.uint8)
         elif workspace.numel() * workspace.element_size() < ws_bytes:
