@@ -845,7 +845,7 @@ struct Resident {
     int clusters[MAX_CLUSTER];
 };
 
-cudaError_t resident(const void* kernel, size_t alone, size_t smem, Resident* out) {
+cudaError_t resident(const void* kernel, size_t alone, size_t smem, Resident* out) try {
     static std::mutex lock;
     static std::map<std::pair<int, const void*>, Resident> known;
     int dev = 0;
@@ -881,6 +881,8 @@ cudaError_t resident(const void* kernel, size_t alone, size_t smem, Resident* ou
     }
     *out = it->second;
     return cudaSuccess;
+} catch (...) {   // no exception leaves a C entry point
+    return cudaErrorMemoryAllocation;
 }
 
 int maps_of(int T) { return (T + MAP_TOKENS - 1) / MAP_TOKENS; }

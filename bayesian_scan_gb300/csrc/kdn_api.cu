@@ -23,9 +23,13 @@ bool head_dim_ok(int x) { return x == 16 || x == 32 || x == 64 || x == 128; }
 bool dtype_ok(kdn_dtype t) { return t == KDN_F32 || t == KDN_BF16; }
 uintptr_t size_of(kdn_dtype t) { return t == KDN_BF16 ? 2 : 4; }
 
+// A tile's tokens beyond the last one, and a row's bytes, stay within an int.
+constexpr int kGatedMaxT = 0x7fffffff - (1 << 16), kGatedMaxC = 1 << 28;
+
 // What the forward and the backward gated recurrence check alike.
 kdn_status gated_check(const GatedArgs& a) {
     if (a.B < 1 || a.H < 1 || a.T < 0 || a.C < 1 || !a.A) return KDN_ERR_INVALID_ARG;
+    if (a.T > kGatedMaxT || a.C > kGatedMaxC) return KDN_ERR_INVALID_ARG;
     if (!dtype_ok(a.in_dtype) || !dtype_ok(a.out_dtype)) return KDN_ERR_UNSUPPORTED;
     if (a.offsets ? (a.nseq < 1 || a.B != 1) : a.nseq != 0) return KDN_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(a.offsets ? a.nseq : a.B) * a.H;
@@ -65,6 +69,7 @@ kdn_status qk_check(const QkArgs& a) {
     for (int i = 0; i < 2; ++i) {
         if (a.heads[i] == 0) continue;
         const long long width = static_cast<long long>(a.heads[i]) * a.dk;
+        if (width > (1 << 30)) return KDN_ERR_INVALID_ARG;   // a row's elements stay within an int
         const long long lds[] = {a.ld[i], a.grad_x[i] ? a.grad_ld[i] : width};
         for (long long ld : lds)
             if (ld < width || ld * es % 16 != 0 || tokens > (1LL << 61) / ld) return KDN_ERR_INVALID_ARG;
@@ -382,7 +387,8 @@ kdn_status kdn_gated_scan_bwd(const void* x, long long x_ld, const void* d, long
 }
 
 kdn_status kdn_gated_scan_bwd_workspace(int B, int H, int T, int C, int nseq, long long* workspace_bytes) {
-    if (B < 1 || H < 1 || T < 0 || C < 1 || nseq < 0 || (nseq > 0 && B != 1) || !workspace_bytes)
+    if (B < 1 || H < 1 || T < 0 || C < 1 || nseq < 0 || (nseq > 0 && B != 1) || !workspace_bytes ||
+        T > kGatedMaxT || C > kGatedMaxC)
         return KDN_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
     if (rows > (1LL << 40) || rows > (1LL << 62) / C) return KDN_ERR_INVALID_ARG;
@@ -453,6 +459,8 @@ kdn_status kdn_qk_norm_rope_bwd(const void* q, long long q_ld, const void* k, lo
 kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, int dk, long long* workspace_bytes) {
     if (B < 1 || T < 0 || Hq < 0 || Hk < 0 || Hq + Hk < 1 || !workspace_bytes) return KDN_ERR_INVALID_ARG;
     if (!head_dim_ok(dk)) return KDN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(Hq) * dk > (1 << 30) || static_cast<long long>(Hk) * dk > (1 << 30))
+        return KDN_ERR_INVALID_ARG;
     *workspace_bytes = qk_bwd_workspace_bytes(B, T, Hq, Hk, dk);
     return KDN_OK;
 }

@@ -16,10 +16,14 @@ inline cudaError_t allow_smem(const void* kernel, size_t bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const std::lock_guard<std::mutex> hold(lock);
-    if (done.count({dev, kernel})) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess) done.insert({dev, kernel});
+    try {   // no exception leaves a C entry point
+        const std::lock_guard<std::mutex> hold(lock);
+        if (done.count({dev, kernel})) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (e == cudaSuccess) done.insert({dev, kernel});
+    } catch (...) {
+        return cudaErrorMemoryAllocation;
+    }
     return e;
 }
 

@@ -446,6 +446,15 @@ def _dtype_of(t, name):
     return dt
 
 
+def _scratch(nbytes, like, stream):
+    """A call's own workspace: it is let go when the call returns, so a stream
+    that is not torch's current one has to be told of it."""
+    t = torch.empty(nbytes, device=like.device, dtype=torch.uint8)
+    if stream is not None and t.is_cuda:
+        t.record_stream(stream)
+    return t
+
+
 def _token_ld(t, name, dt, shape):
     """Elements between consecutive tokens of a [B,T,C] or [B,H,T,C] tensor
     whose channels are adjacent and whose rows follow one another (dense, or
@@ -579,7 +588,7 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
     ws_bytes = _gated_ws(x.get_device(), B, H, T, C, nseq)
     if workspace is None:
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, device=x.device, dtype=torch.uint8)
+            workspace = _scratch(ws_bytes, x, stream)
     elif workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError(f"workspace must hold {ws_bytes} bytes")
     _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, grad_out=grad_out,
@@ -792,7 +801,7 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
     if g["wq"] is not None or g["wk"] is not None:
         ws_bytes = _qk_ws(first.get_device(), B, T, Hq, Hk, dk)
         if workspace is None:
-            workspace = torch.empty(ws_bytes, device=first.device, dtype=torch.uint8)
+            workspace = _scratch(ws_bytes, first, stream)
         elif workspace.numel() * workspace.element_size() < ws_bytes:
             raise ValueError(f"workspace must hold {ws_bytes} bytes")
     else:

@@ -387,9 +387,9 @@ KDN_API kdn_status kdn_mobius_scan_noalloc(const float* a, const float* b, const
  * sequences of T tokens.  Offsets out of range are clamped to [0, T]; where
  * they decrease, which tokens belong to which sequence is unspecified.
  *
- *   B >= 1, H >= 1, T >= 0, C >= 1; x, d and out element-aligned (16-byte
- *   aligned rows, C and the lds multiples of 16 bytes, take the widest path).
- *   B*H*T*max(x_ld, d_ld) < 2^62.  T = 0 writes only final_state.
+ *   B >= 1, H >= 1, 0 <= T <= 2^31 - 1 - 2^16, 1 <= C <= 2^28; x, d and out
+ *   element-aligned (16-byte aligned rows, C and the lds multiples of 16
+ *   bytes, take the widest path).  B*H*T*max(x_ld, d_ld) < 2^62.  T = 0 writes only final_state.
  *   out and final_state overlap no input.
  *
  * The state and every sum are fp32 whatever the types; out is rounded once.
@@ -483,7 +483,8 @@ typedef enum {
  *   inv_freq  [rot/2] fp32, finite
  *   q_out     [B,Hq,T,dk], k_out [B,Hk,T,dk]  out_dtype, dense
  *
- *   B >= 1, T >= 0, Hq, Hk >= 0 and not both 0, dk in {16, 32, 64, 128}.
+ *   B >= 1, T >= 0, Hq, Hk >= 0 and not both 0, H*dk <= 2^30, dk in {16, 32,
+ *   64, 128}.
  *   Tensors 16-byte aligned, lds multiples of 16 bytes.  Outputs overlap no
  *   input.
  *

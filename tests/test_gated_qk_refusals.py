@@ -40,6 +40,7 @@ SIZES = [
     (dict(off=FAKE), -1), (dict(off=FAKE, nseq=-1), -1), (dict(nseq=3), -1), (dict(off=FAKE, nseq=3, B=2), -1),
     (dict(off=FAKE + 2, nseq=3), -1), (dict(x=FAKE + 1), -1), (dict(d=FAKE + 2, it=0), -1), (dict(A=FAKE + 2), -1),
     (dict(h0=FAKE + 1), -1), (dict(out=FAKE + 2, ot=0), -1),
+    (dict(T=0x7fffffff), -1), (dict(C=(1 << 28) + 1, x_ld=1 << 29, d_ld=1 << 29), -1),
     (dict(B=1 << 30, H=1 << 30), -1), (dict(x_ld=1 << 60, T=1 << 20), -1), (dict(B=1 << 15, H=1 << 15, T=1 << 30, C=64), -1),
 ]
 
@@ -72,13 +73,13 @@ def test_workspaces(kdn):
     f = kdn.lib.kdn_gated_scan_bwd_workspace
     assert f(2, 3, 100, 64, 0, ctypes.byref(n)) == 0 and n.value >= 2 * 3 * 64 * 4
     assert f(1, 3, 100, 64, 5, ctypes.byref(n)) == 0 and n.value >= 5 * 3 * 64 * 4
-    for bad in ((0, 1, 1, 1, 0), (1, 0, 1, 1, 0), (1, 1, -1, 1, 0), (1, 1, 1, 0, 0), (2, 1, 1, 1, 3), (1, 1, 1, 1, -1)):
+    for bad in ((1, 1, 0x7fffffff, 1, 0), (1, 1, 1, 1 << 29, 0), (0, 1, 1, 1, 0), (1, 0, 1, 1, 0), (1, 1, -1, 1, 0), (1, 1, 1, 0, 0), (2, 1, 1, 1, 3), (1, 1, 1, 1, -1)):
         assert f(*bad, ctypes.byref(n)) == -1
     assert f(1, 1, 1, 1, 0, None) == -1
     f = kdn.lib.kdn_qk_norm_rope_bwd_workspace
     assert f(2, 100, 4, 4, 64, ctypes.byref(n)) == 0 and n.value >= 2 * 64 * 4
     assert f(2, 100, 4, 4, 65, ctypes.byref(n)) == -2
-    for bad in ((0, 1, 1, 1, 64), (1, -1, 1, 1, 64), (1, 1, 0, 0, 64), (1, 1, -1, 2, 64)):
+    for bad in ((1, 1, 1 << 25, 1, 64), (0, 1, 1, 1, 64), (1, -1, 1, 1, 64), (1, 1, 0, 0, 64), (1, 1, -1, 2, 64)):
         assert f(*bad, ctypes.byref(n)) == -1
     with pytest.raises(kdn.KdnError):
         kdn.gated_scan_bwd_workspace(0, 1, 1, 1)
@@ -121,7 +122,7 @@ def qk_back(kdn, q=FAKE, q_ld=128, k=FAKE, k_ld=64, wq=None, wk=None, norm=1, ep
     (dict(rot=66), -1), (dict(rot=-2), -1), (dict(inv=None), -1), (dict(axes=0), -1), (dict(axes=5), -1),
     (dict(q_ld=127), -1), (dict(q_ld=132), -1), (dict(k_ld=56), -1), (dict(q=FAKE + 8), -1), (dict(ko=FAKE + 4), -1),
     (dict(wq=FAKE + 4), -1), (dict(pos=FAKE + 2), -1), (dict(axis=FAKE + 1), -1), (dict(inv=FAKE + 2), -1),
-    (dict(q_ld=1 << 59, T=1 << 20), -1),
+    (dict(q_ld=1 << 59, T=1 << 20), -1), (dict(Hq=1 << 25, q_ld=1 << 31), -1),
 ])
 def test_qk_rejects(kdn, kw, status):
     assert qk(kdn, **kw) == status

@@ -312,6 +312,41 @@ def test_repeats_are_equal_and_streams_and_graphs_work():
                 assert torch.equal(a, b)
 
 
+def test_parts_in_captured_graphs():
+    """A long sequence of few channels takes scratch of its own inside the
+    call; captured, the graph holds it, and two graphs do not share it."""
+    from bayesian_scan_gb300 import kdn
+    x, d, A, h0, go, gf = (t.cuda() for t in draw(1, 1, 60000, 16, F32, seed=30))
+
+    def both():
+        o, f = kdn.gated_scan_fwd(x, d, A, h0=h0)
+        return [o, f, *kdn.gated_scan_bwd(x, d, A, o, go, h0=h0, grad_final_state=gf).values()]
+
+    first = both()
+    ro, rf, eo, ef = plain64.gated_fwd(x[:, :, :9000].cpu(), d[:, :, :9000].cpu(), A.cpu(), h0.cpu())
+    plain64.assert_within(first[0][:, :, :9000], ro, eo)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = both()
+        graphs.append((graph, held))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for (graph, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, held in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(first, held))
+
+
+def test_no_tokens_but_sequences():
+    x, d, A, h0, go, gf = draw(1, 2, 0, 24, F32, seed=31, rows=3)
+    check_fwd(x, d, A, h0, True, F32, [0, 0, 0, 0])
+    check_bwd(x, d, A, h0, go, gf, True, F32, [0, 0, 0, 0])
+
+
 def test_caller_workspace_and_skipped_gradients():
     from bayesian_scan_gb300 import kdn
     x, d, A, h0, go, gf = (t.cuda() for t in draw(2, 3, 500, 56, F32, seed=13))
@@ -439,5 +474,10 @@ def test_a_stream_given_by_hand():
     s = torch.cuda.Stream()
     o, f = kdn.gated_scan_fwd(x, d, A, h0=h0, stream=s)
     y = kdn.gated_step(x[:, :, 0].contiguous(), d[:, :, 0].contiguous(), A, h0.clone(), stream=s)
+    go, gf = torch.ones_like(x), torch.ones_like(h0)
+    want = kdn.gated_scan_bwd(x, d, A, ref[0], go, h0=h0, grad_final_state=gf)
+    torch.cuda.synchronize()
+    got = kdn.gated_scan_bwd(x, d, A, ref[0], go, h0=h0, grad_final_state=gf, stream=s)
     s.synchronize()
+    assert all(torch.equal(want[n], got[n]) for n in want)
     assert torch.equal(o, ref[0]) and torch.equal(f, ref[1]) and y.shape == h0.shape
