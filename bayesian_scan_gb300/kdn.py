@@ -426,6 +426,23 @@ def mobius_scan(a, b, c, d, lambda0, out=None, stream=None):
 # ---------------------------------------------------------------------------
 # the recurrence with one gate per channel
 
+def _here(stream, *tensors):
+    """Whether the given tensors (None: not given) are all on the current
+    device and the call goes to its current stream; where not,
+    ``_on_one_device`` has the message."""
+    if stream is not None:
+        return False
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if dev >= 0 or d < 0:
+                    return False
+                dev = d
+    return dev >= 0 and dev == torch._C._cuda_getDevice()
+
+
 _DTYPES = {torch.bfloat16: KDN_BF16, torch.float32: KDN_F32}
 _F32 = torch.float32
 
@@ -527,9 +544,10 @@ def gated_scan_fwd(x, d, A, h0=None, leak=False, offsets=None, out=None, out_dty
         final_state = None
     elif final_state is not None:
         _check(final_state, "final_state", _F32, state)
-    _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, final_state=final_state)
-    st = lib.kdn_gated_scan_fwd(_ptr(x), x_ld, _ptr(d), d_ld, _ptr(A), _ptr(h0), _ptr(offsets), nseq,
-                                int(leak), _ptr(out), _ptr(final_state), B, H, T, C, it, ot,
+    if not _here(stream, x, d, A, h0, offsets, out, final_state):
+        _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, final_state=final_state)
+    st = lib.kdn_gated_scan_fwd(x.data_ptr(), x_ld, d.data_ptr(), d_ld, A.data_ptr(), _ptr(h0), _ptr(offsets), nseq,
+                                int(leak), out.data_ptr(), _ptr(final_state), B, H, T, C, it, ot,
                                 _stream(stream))
     if st != KDN_OK:
         raise KdnError(st, "kdn_gated_scan_fwd")
@@ -591,12 +609,14 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
             workspace = _scratch(ws_bytes, x, stream)
     elif workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError(f"workspace must hold {ws_bytes} bytes")
-    _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, grad_out=grad_out,
-                   grad_final_state=grad_final_state, grad_x=g["x"], grad_d=g["d"], grad_A=g["A"],
-                   grad_h0=g["h0"], workspace=workspace)
-    st = lib.kdn_gated_scan_bwd(_ptr(x), x_ld, _ptr(d), d_ld, _ptr(A), _ptr(h0), _ptr(offsets), nseq,
-                                int(leak), _ptr(out), _ptr(grad_out), _ptr(grad_final_state),
-                                _ptr(g["x"]), _ptr(g["d"]), _ptr(g["A"]), _ptr(g["h0"]), B, H, T, C,
+    gx, gd, gA, gh0 = g["x"], g["d"], g["A"], g["h0"]
+    if not _here(stream, x, d, A, h0, offsets, out, grad_out, grad_final_state, gx, gd, gA, gh0, workspace):
+        _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, grad_out=grad_out,
+                       grad_final_state=grad_final_state, grad_x=gx, grad_d=gd, grad_A=gA, grad_h0=gh0,
+                       workspace=workspace)
+    st = lib.kdn_gated_scan_bwd(x.data_ptr(), x_ld, d.data_ptr(), d_ld, A.data_ptr(), _ptr(h0), _ptr(offsets), nseq,
+                                int(leak), out.data_ptr(), grad_out.data_ptr(), _ptr(grad_final_state),
+                                gx.data_ptr(), gd.data_ptr(), _ptr(gA), _ptr(gh0), B, H, T, C,
                                 it, ot, _ptr(workspace), ws_bytes, _stream(stream))
     if st != KDN_OK:
         raise KdnError(st, "kdn_gated_scan_bwd")
@@ -632,10 +652,7 @@ def gated_step(x, d, A, state, leak=False, new_state=None, out=None, out_dtype=N
         _check(new_state, "new_state", _F32, shape)
         _check(out, "out", out_dtype, shape)
     ot = _dtype_of(out, "out")
-    dev = x.get_device()
-    if not (stream is None and dev >= 0 and dev == torch._C._cuda_getDevice() and d.get_device() == dev
-            and A.get_device() == dev and state.get_device() == dev and new_state.get_device() == dev
-            and out.get_device() == dev):
+    if not _here(stream, x, d, A, state, new_state, out):
         _on_one_device(stream, x=x, d=d, A=A, state=state, new_state=new_state, out=out)
     st = lib.kdn_gated_step(x.data_ptr(), d.data_ptr(), A.data_ptr(), int(leak), state.data_ptr(),
                             new_state.data_ptr(), out.data_ptr(), shape[0], 1 if len(shape) == 2 else shape[1],
@@ -679,32 +696,38 @@ def _qk_common(q, k, pos, inv_freq, wq, wk, norm, axis):
     if first.dim() != 4:
         raise ValueError(f"q and k must be [B,T,H,dk], got {tuple(first.shape)}")
     B, T, _, dk = first.shape
-    dt = _dtype_of(first, "q" if q is not None else "k")
-    rows = [(0, 0) if t is None else _head_rows(t, name, first.dtype, B, T, dk)
-            for name, t in (("q", q), ("k", k))]
-    if norm not in _NORMS:
+    dtype = first.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _dtype_of(first, "q" if q is not None else "k")
+    q_rows = (0, 0) if q is None else _head_rows(q, "q", dtype, B, T, dk)
+    k_rows = (0, 0) if k is None else _head_rows(k, "k", dtype, B, T, dk)
+    nm = _NORMS.get(norm)
+    if nm is None:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            _check(w, name, torch.float32, (dk,))
+    if wq is not None:
+        _check(wq, "wq", _F32, (dk,))
+    if wk is not None:
+        _check(wk, "wk", _F32, (dk,))
     rot = axes = 0
     if inv_freq is not None:
-        _check(inv_freq, "inv_freq", torch.float32)
-        if inv_freq.dim() != 1 or 2 * inv_freq.numel() > dk:
+        _check(inv_freq, "inv_freq", _F32)
+        pairs = inv_freq.numel()
+        if inv_freq.dim() != 1 or 2 * pairs > dk:
             raise ValueError(f"inv_freq must be [rot/2] with rot <= {dk}, got {tuple(inv_freq.shape)}")
-        rot, axes = 2 * inv_freq.numel(), 1
+        rot, axes = 2 * pairs, 1
         if pos is not None:
-            if pos.dim() == 2:
-                pos = pos.unsqueeze(0)
-            if pos.dim() != 3 or not 1 <= pos.shape[0] <= 4:
+            n = pos.dim()
+            if n == 3:
+                axes = pos.shape[0]
+            if n not in (2, 3) or not 1 <= axes <= 4:
                 raise ValueError(f"pos must be [B,T] or [axes,B,T] with 1 to 4 axes, got {tuple(pos.shape)}")
-            axes = pos.shape[0]
-            _check(pos, "pos", torch.int32, (axes, B, T))
+            _check(pos, "pos", torch.int32, (B, T) if n == 2 else (axes, B, T))
         if axis is not None:
             _check(axis, "axis", torch.int32, inv_freq.shape)
     elif pos is not None or axis is not None:
         raise ValueError("pos and axis need inv_freq")
-    return B, T, dk, dt, _NORMS[norm], axes, rot, rows[0], rows[1]
+    return B, T, dk, dt, nm, axes, rot, q_rows, k_rows
 
 
 def qk_norm_rope_fwd(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms", eps=1e-6, axis=None,
@@ -721,28 +744,33 @@ def qk_norm_rope_fwd(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms"
     (q_out [B,Hq,T,dk], k_out [B,Hk,T,dk]) of ``out_dtype`` (q's by default)."""
     B, T, dk, it, nm, axes, rot, (Hq, q_ld), (Hk, k_ld) = _qk_common(q, k, pos, inv_freq, wq, wk, norm, axis)
     first = q if q is not None else k
-    outs = []
-    for name, t, H, o in (("q_out", q, Hq, q_out), ("k_out", k, Hk, k_out)):
-        if t is None:
-            o = None
-        else:
-            if o is None:
-                o = torch.empty((B, H, T, dk), device=t.device, dtype=out_dtype or t.dtype)
-            else:
-                _check(o, name, out_dtype, (B, H, T, dk))
-        outs.append(o)
-    out_dt = next(o for o in outs if o is not None)
-    ot = _dtype_of(out_dt, "out")
-    if outs[0] is not None and outs[1] is not None and outs[0].dtype != outs[1].dtype:
+    if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
         raise ValueError("q_out and k_out must have one type")
-    _on_one_device(stream, q=q, k=k, pos=pos, inv_freq=inv_freq, wq=wq, wk=wk, axis=axis, q_out=outs[0],
-                   k_out=outs[1])
-    st = lib.kdn_qk_norm_rope_fwd(_ptr(q), q_ld, _ptr(k), k_ld, _ptr(wq), _ptr(wk), nm, float(eps), _ptr(pos),
-                                  axes, _ptr(inv_freq), _ptr(axis), rot, int(interleaved), _ptr(outs[0]),
-                                  _ptr(outs[1]), B, T, Hq, Hk, dk, it, ot, _stream(stream))
+    od = out_dtype or (q_out if q_out is not None else k_out if k_out is not None else first).dtype
+    ot = _DTYPES.get(od)
+    if ot is None:
+        raise ValueError(f"the outputs must be bf16 or fp32, got {od}")
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty((B, Hq, T, dk), device=first.device, dtype=od)
+    else:
+        _check(q_out, "q_out", od, (B, Hq, T, dk))
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty((B, Hk, T, dk), device=first.device, dtype=od)
+    else:
+        _check(k_out, "k_out", od, (B, Hk, T, dk))
+    if not _here(stream, q, k, pos, inv_freq, wq, wk, axis, q_out, k_out):
+        _on_one_device(stream, q=q, k=k, pos=pos, inv_freq=inv_freq, wq=wq, wk=wk, axis=axis, q_out=q_out,
+                       k_out=k_out)
+    st = lib.kdn_qk_norm_rope_fwd(_ptr(q), q_ld, _ptr(k), k_ld, _ptr(wq), _ptr(wk), nm, eps, _ptr(pos),
+                                  axes, _ptr(inv_freq), _ptr(axis), rot, int(interleaved), _ptr(q_out),
+                                  _ptr(k_out), B, T, Hq, Hk, dk, it, ot, _stream(stream))
     if st != KDN_OK:
         raise KdnError(st, "kdn_qk_norm_rope_fwd")
-    return outs[0], outs[1]
+    return q_out, k_out
 
 
 def qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk) -> int:
@@ -806,9 +834,10 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
             raise ValueError(f"workspace must hold {ws_bytes} bytes")
     else:
         workspace = None
-    _on_one_device(stream, q=q, k=k, grad_q_out=grad_q_out if q is not None else None,
-                   grad_k_out=grad_k_out if k is not None else None, pos=pos, inv_freq=inv_freq, wq=wq,
-                   wk=wk, axis=axis, grad_q=g["q"], grad_k=g["k"], workspace=workspace)
+    grad_q_out, grad_k_out = None if q is None else grad_q_out, None if k is None else grad_k_out
+    if not _here(stream, q, k, grad_q_out, grad_k_out, pos, inv_freq, wq, wk, axis, g["q"], g["k"], workspace):
+        _on_one_device(stream, q=q, k=k, grad_q_out=grad_q_out, grad_k_out=grad_k_out, pos=pos, inv_freq=inv_freq,
+                       wq=wq, wk=wk, axis=axis, grad_q=g["q"], grad_k=g["k"], workspace=workspace)
     st = lib.kdn_qk_norm_rope_bwd(_ptr(q), q_ld, _ptr(k), k_ld, _ptr(wq), _ptr(wk), nm, float(eps), _ptr(pos),
                                   axes, _ptr(inv_freq), _ptr(axis), rot, int(interleaved),
                                   _ptr(grad_q_out), _ptr(grad_k_out), _ptr(g["q"]), lds["q"], _ptr(g["k"]),
