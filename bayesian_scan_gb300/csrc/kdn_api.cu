@@ -426,7 +426,7 @@ kdn_status kdn_qk_norm_rope_fwd(const void* q, long long q_ld, const void* k, lo
     const kdn_status s = qk_check(a);
     if (s != KDN_OK) return s;
     if (T == 0) return KDN_OK;
-    return qk_fwd_launch(a, static_cast<cudaStream_t>(stream));
+    return qk_fwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load());
 }
 
 kdn_status kdn_qk_norm_rope_bwd(const void* q, long long q_ld, const void* k, long long k_ld,
@@ -480,12 +480,14 @@ const char* kdn_status_string(kdn_status s) {
 kdn_status kdn_get_device_error(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return from_cuda(e);
-    int s1 = 0, s2 = 0, s3 = 0, s4 = 0;
+    int s1 = 0, s2 = 0, s3 = 0, s4 = 0, s5 = 0;
     if ((e = diag_take_device_error_bf16(&s1)) != cudaSuccess) return from_cuda(e);
     if ((e = diag_take_device_error_f32(&s2)) != cudaSuccess) return from_cuda(e);
     if ((e = mobius_take_device_error(&s3)) != cudaSuccess) return from_cuda(e);
     if ((e = gated_take_device_error(&s4)) != cudaSuccess) return from_cuda(e);
+    if ((e = qk_take_device_error(&s5)) != cudaSuccess) return from_cuda(e);
     if (s1) return static_cast<kdn_status>(s1);
+    if (s5) return static_cast<kdn_status>(s5);
     if (s4) return static_cast<kdn_status>(s4);
     if (s2) return static_cast<kdn_status>(s2);
     return static_cast<kdn_status>(s3);

@@ -149,7 +149,7 @@ struct QkArgs {
     kdn_dtype in_dtype, out_dtype;
     void* workspace;
 };
-kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream);
+kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream, long long wait_ns);
 kdn_status qk_bwd_launch(const QkArgs& a, cudaStream_t stream);
 long long qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int dk);
 
@@ -165,6 +165,7 @@ kdn_status mobius_host(const float* a, const float* b, const float* c, const flo
 cudaError_t diag_take_device_error(int* status);
 cudaError_t mobius_take_device_error(int* status);
 cudaError_t gated_take_device_error(int* status);
+cudaError_t qk_take_device_error(int* status);
 
 // Number of SMs of the current device (cached per device).
 int sm_count();

@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "gated_device.cuh"
+#include "kdn_device.cuh"
 #include "kdn_internal.h"
 #include "kernel_setup.h"
 #include "sum_rows.cuh"
@@ -29,6 +30,9 @@ namespace {
 using namespace gated;
 
 constexpr int WARPS = 8;
+constexpr int SEG = 4096, SEG_DEPTH = 2;   // bytes of a bulk copy, copies in flight per warp
+
+__device__ int g_qk_error = 0;
 constexpr int FWD_BLOCKS_PER_SM = 3, BWD_BLOCKS_PER_SM = 2, BWD_DEPTH = 4;
 
 // The turns per position of a frequency, f / (2 pi) modulo 1, in 2^-64: the
@@ -407,6 +411,103 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
     }
 }
 
+// The forward of many tokens with a warp's worth of heads: a token's heads lie
+// side by side in its row, so they come as bulk copies of up to SEG bytes into
+// the warp's ring, SEG_DEPTH of them ahead, without a load instruction or a
+// register.  The kernel above waits for its loads (half of all stalls), and
+// rows ahead in registers cost more than they hide: 8 x 4096 tokens, 16 + 16
+// heads of 128, bf16: 102 us there, 90 us here (88 % of the copy's rate;
+// three copies ahead 92 us, six of half the size 101 us).
+template <int DK>
+struct BulkShared {
+    char ring[WARPS][SEG_DEPTH][SEG];
+    uint64_t full[WARPS][SEG_DEPTH];
+    Freqs<DK> freqs;
+};
+
+template <typename TI, typename TO, int DK, bool INTER>
+__global__ void __launch_bounds__(WARPS * 32, 2)
+qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
+    constexpr int LPR = DK / 8, RPW = 32 / LPR, ROW = DK * static_cast<int>(sizeof(TI)), HEADS = SEG / ROW;
+    extern __shared__ __align__(16) char smem[];
+    BulkShared<DK>& sh = *reinterpret_cast<BulkShared<DK>*>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < WARPS * SEG_DEPTH; ++i) mbar_init(&sh.full[0][0] + i, 1);
+        mbar_init_fence();
+    }
+    sh.freqs.fill(p);                                          // (and a barrier)
+    const Place q = place_of<INTER>(l, p.rot);
+    const long long tokens = static_cast<long long>(p.B) * p.T, stride = static_cast<long long>(gridDim.x) * WARPS;
+    const int segs[2] = {(p.heads[0] + HEADS - 1) / HEADS, (p.heads[1] + HEADS - 1) / HEADS}, per = segs[0] + segs[1];
+    const long long first = static_cast<long long>(blockIdx.x) * WARPS + warp;
+    const long long ystep = static_cast<long long>(p.T) * DK;
+
+    // the copies run ahead: their token, segment and slot
+    long long ct = first;
+    int cs = 0, cslot = 0;
+    auto copy = [&]() {
+        if (ct >= tokens) return;
+        const int which = cs >= segs[0], h = (cs - (which ? segs[0] : 0)) * HEADS;
+        const int n = min(HEADS, p.heads[which] - h);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.full[warp][cslot], n * ROW);
+            bulk_g2s(sh.ring[warp][cslot], static_cast<const TI*>(p.x[which]) + ct * p.ld[which] + h * DK, n * ROW,
+                     &sh.full[warp][cslot]);
+        }
+        if (++cs == per) {
+            cs = 0;
+            ct += stride;
+        }
+        if (++cslot == SEG_DEPTH) cslot = 0;
+    };
+    for (int i = 0; i < SEG_DEPTH; ++i) copy();
+
+    int slot = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    Row8 w{};
+    for (long long token = first; token < tokens; token += stride) {
+        const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<long long>(b) * p.T);
+        const Turn turn = turn_at<DK>(sh.freqs, p, token, t, RPW, l);
+        for (int seg = 0; seg < per; ++seg) {
+            const int which = seg >= segs[0], h0 = (seg - (which ? segs[0] : 0)) * HEADS;
+            const int H = p.heads[which], n = min(HEADS, H - h0);
+            if (seg == 0 || seg == segs[0]) w = weight_of<INTER>(p.w[which], q);
+            if (ok && !mbar_wait(&sh.full[warp][slot], parity, wait_ns)) {
+                record_error(&g_qk_error, KDN_ERR_TIMEOUT);
+                ok = false;
+            }
+            const TI* x = reinterpret_cast<const TI*>(sh.ring[warp][slot]) + sub * DK;
+            TO* y = static_cast<TO*>(p.y[which]) + ((static_cast<long long>(b) * H + h0 + sub) * p.T + t) * DK;
+            int i = 0;
+#pragma unroll 4
+            for (; i + RPW <= n; i += RPW) {
+                RawRow<TI> raw;
+                raw.u = *reinterpret_cast<const Raw4<TI>*>(x + q.g0);
+                raw.v = *reinterpret_cast<const Raw4<TI>*>(x + q.g1);
+                qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, true);
+                x += RPW * DK;
+                y += RPW * ystep;
+            }
+            if (i < n) {
+                RawRow<TI> raw{};
+                if (i + sub < n) {
+                    raw.u = *reinterpret_cast<const Raw4<TI>*>(x + q.g0);
+                    raw.v = *reinterpret_cast<const Raw4<TI>*>(x + q.g1);
+                }
+                qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, i + sub < n);
+            }
+            __syncwarp();                                      // the slot has been read
+            copy();
+            if (++slot == SEG_DEPTH) {
+                slot = 0;
+                parity ^= 1;
+            }
+        }
+    }
+}
+
 // Backward.  part [block][2 dk] takes each block's share of the weights'
 // gradients, q's then k's.
 template <typename TI, typename TO, int DEPTH>
@@ -582,7 +683,19 @@ long long qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int dk) {
     return static_cast<long long>(bwd_blocks(B, T, Hq, Hk, dk)) * 2 * dk * 4;
 }
 
-kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream) {
+// Whether a forward call is one for bulk copies: vector places, heads for a
+// whole warp in either tensor, and a token for half of the warps or more (3 x
+// 1271 tokens of 32 + 8 heads 13.9 us, 15.4 by loads; 128 tokens are faster
+// dealt out by heads).
+bool bulk_ok(const QkArgs& a, int blocks) {
+    const int rpw = 32 / (a.dk / 8);
+    for (int H : a.heads)
+        if (H != 0 && H < rpw) return false;
+    return (a.interleaved || a.rot % 8 == 0) &&
+           static_cast<long long>(a.B) * a.T >= WARPS * blocks / 2;
+}
+
+kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream, long long wait_ns) {
     const Deal deal = deal_of(static_cast<long long>(a.B) * a.T, a.heads[0], a.heads[1], a.dk);
     const int blocks = blocks_of(deal, FWD_BLOCKS_PER_SM);
     return by_type(a, [&](auto ti, auto to) {
@@ -590,6 +703,13 @@ kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream) {
             using TI = decltype(ti);
             using TO = decltype(to);
             constexpr int DK = decltype(n)::value;
+            if (bulk_ok(a, 2 * sm_count())) {
+                auto kernel = a.interleaved ? qk_fwd_bulk_kernel<TI, TO, DK, true> : qk_fwd_bulk_kernel<TI, TO, DK, false>;
+                const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), sizeof(BulkShared<DK>));
+                if (e != cudaSuccess) return from_cuda(e);
+                kernel<<<2 * sm_count(), WARPS * 32, sizeof(BulkShared<DK>), stream>>>(a, wait_ns);
+                return from_cuda(cudaGetLastError());
+            }
             if (a.interleaved)
                 qk_fwd_kernel<TI, TO, DK, true><<<blocks, WARPS * 32, 0, stream>>>(a, deal);
             else
@@ -597,6 +717,14 @@ kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream) {
             return from_cuda(cudaGetLastError());
         });
     });
+}
+
+cudaError_t qk_take_device_error(int* status) {
+    int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_qk_error, sizeof(int));
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_qk_error, &zero, sizeof(int));
+    *status = v;
+    return e;
 }
 
 kdn_status qk_bwd_launch(const QkArgs& a, cudaStream_t stream) {

@@ -87,6 +87,26 @@ def test_sizes(B, T, Hq, Hk, dk):
     check(s, Hq, Hk, dk, F32, "rms")
 
 
+@pytest.mark.parametrize("dk,Hq,Hk", [(128, 19, 2), (128, 2, 33), (64, 5, 4), (32, 8, 9), (16, 33, 17), (64, 4, 0)])
+@pytest.mark.parametrize("in_dtype,out_dtype", [(BF16, F32), (F32, BF16)])
+def test_many_tokens(dk, Hq, Hk, in_dtype, out_dtype):
+    # tokens enough for the bulk copies; heads that end inside a warp's step and inside a copy
+    from bayesian_scan_gb300 import kdn
+    B, T = 2, 701
+    for interleaved, rot in ((False, dk), (True, dk - 2), (False, dk // 2)):
+        s = draw(B, T, Hq, max(Hk, 1), dk, in_dtype, seed=dk + Hq, rot=rot, axes=2)
+        q, k = split(s["rows"], Hq, max(Hk, 1), dk)
+        dq, dk_ = split(s["rows"].cuda(), Hq, max(Hk, 1), dk)
+        theta = plain64.rotation_angles(s["pos"], s["inv_freq"], s["axis"])
+        oq, ok = kdn.qk_norm_rope_fwd(dq, dk_ if Hk else None, s["pos"].cuda(), s["inv_freq"].cuda(), s["wq"].cuda(),
+                                      s["wk"].cuda(), axis=s["axis"].cuda(), interleaved=interleaved,
+                                      out_dtype=out_dtype)
+        for x, o, w in ((q, oq, s["wq"]), (k, ok, s["wk"])) if Hk else ((q, oq, s["wq"]),):
+            ref, err = plain64.qk_fwd(x, w, theta, rot, interleaved, "rms", 1e-6)
+            plain64.assert_within(o, ref, err)
+    assert kdn.get_device_error() == kdn.KDN_OK
+
+
 def test_far_positions():
     # the angle of a far position keeps its accuracy: up to 2^31 - 1, and behind zero
     s = draw(2, 64, 2, 1, 128, F32, seed=1, axes=2)
