@@ -177,7 +177,7 @@ __device__ __forceinline__ void cluster_sync() {
 // `start` is the state before the warp's tokens and `carry` the one after the
 // round's last tile, both from the carry before the round.  One warp, another
 // each round, does what the CTA has in common (by all warps alike it was a
-// fifth of the kernel's instructions: 65536 x 2048 247 us, so 212 us).
+// fifth of the kernel's instructions: 65536 x 2048 247 us, so 210 us).
 //
 // In a cluster the tile's map goes to every CTA's shared memory by stores
 // that complete on the receiver's mbarrier: no fence waits for the round's
@@ -396,9 +396,10 @@ struct FwdShared {
 };
 
 // Measured (GB300; 16-bit in and out, 134 M elements, 805 MB, where 118 us is
-// the copy's rate): as 16 x 4096 x 2048 160 us, 4 x 16384 x 2048 (clusters of
-// 2) 167 us, 1 x 65536 x 2048 (clusters of 8) 231 us; 2 CTAs per SM (128
-// registers), 24 instructions per element.
+// the copy's rate): as 16 x 4096 x 2048 151 us, 4 x 16384 x 2048 (clusters of
+// 2) 164 us, 1 x 65536 x 2048 (clusters of 8) 189 us, 210 us of the convex
+// form; 2 CTAs per SM (128 registers), 18 instructions per element, 24 with
+// clusters of 8.
 template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
 __global__ void __launch_bounds__(NW * 32, 2)
 gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cut cut) {
