@@ -443,9 +443,9 @@ qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
     const long long first = static_cast<long long>(blockIdx.x) * WARPS + warp;
     const long long ystep = static_cast<long long>(p.T) * DK;
 
-    // the copies run ahead: their token, segment and slot, and how many
+    // the copies run ahead: their token, segment and slot
     long long ct = first;
-    int cs = 0, cslot = 0, ahead = 0;
+    int cs = 0, cslot = 0;
     auto copy = [&]() {
         if (ct >= tokens) return;
         const int which = cs >= segs[0], h = (cs - (which ? segs[0] : 0)) * HEADS;
@@ -460,12 +460,12 @@ qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
             ct += stride;
         }
         if (++cslot == SEG_DEPTH) cslot = 0;
-        ++ahead;
     };
     for (int i = 0; i < SEG_DEPTH; ++i) copy();
 
     int slot = 0;
     uint32_t parity = 0;
+    bool ok = true;
     Row8 w{};
     for (long long token = first; token < tokens; token += stride) {
         const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<long long>(b) * p.T);
@@ -474,18 +474,20 @@ qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
             const int which = seg >= segs[0], h0 = (seg - (which ? segs[0] : 0)) * HEADS;
             const int H = p.heads[which], n = min(HEADS, H - h0);
             if (seg == 0 || seg == segs[0]) w = weight_of<INTER>(p.w[which], q);
-            if (!mbar_wait(&sh.full[warp][slot], parity, wait_ns)) {
+            if (ok && !mbar_wait(&sh.full[warp][slot], parity, wait_ns)) {
                 record_error(&g_qk_error, KDN_ERR_TIMEOUT);
-                while (ahead--) {                              // its copies in flight: one more wait for each
-                    mbar_wait(&sh.full[warp][slot], parity, wait_ns);
-                    if (++slot == SEG_DEPTH) {
-                        slot = 0;
-                        parity ^= 1;
+                ok = false;
+                ct = tokens;                                   // no more copies; those in flight get one more wait each
+                int s = slot;
+                uint32_t ph = parity;
+                do {
+                    mbar_wait(&sh.full[warp][s], ph, wait_ns);
+                    if (++s == SEG_DEPTH) {
+                        s = 0;
+                        ph ^= 1;
                     }
-                }
-                return;
+                } while (s != cslot);
             }
-            --ahead;
             const TI* x = reinterpret_cast<const TI*>(sh.ring[warp][slot]) + sub * DK;
             TO* y = static_cast<TO*>(p.y[which]) + ((static_cast<long long>(b) * H + h0 + sub) * p.T + t) * DK;
             int i = 0;

@@ -463,6 +463,12 @@ def _dtype_of(t, name):
     return dt
 
 
+def _ws_device(t):
+    """The device a workspace size is asked for, the current one: the size is
+    a matter of its SMs, and a call on another device's tensors is refused."""
+    return torch._C._cuda_getDevice() if t.is_cuda else -1
+
+
 def _scratch(nbytes, like, stream):
     """A call's own workspace: it is let go when the call returns, so a stream
     that is not torch's current one has to be told of it."""
@@ -603,7 +609,7 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
         elif t is not None:
             _check(t, "grad_" + name, _F32, shape)
         g[name] = t
-    ws_bytes = _gated_ws(x.get_device(), B, H, T, C, nseq)
+    ws_bytes = _gated_ws(_ws_device(x), B, H, T, C, nseq)
     if workspace is None:
         if ws_bytes:
             workspace = _scratch(ws_bytes, x, stream)
@@ -827,7 +833,7 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
         raise ValueError(f"the outputs' gradients must be bf16 or fp32, got {gts[0]}")
     ws_bytes = 0
     if g["wq"] is not None or g["wk"] is not None:
-        ws_bytes = _qk_ws(first.get_device(), B, T, Hq, Hk, dk)
+        ws_bytes = _qk_ws(_ws_device(first), B, T, Hq, Hk, dk)
         if workspace is None:
             workspace = _scratch(ws_bytes, first, stream)
         elif workspace.numel() * workspace.element_size() < ws_bytes:

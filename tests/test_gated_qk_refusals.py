@@ -223,3 +223,16 @@ def test_binding_rejects_qk(kdn):
     ]:
         with pytest.raises(ValueError, match=match):
             kdn.qk_norm_rope_bwd(*args, **kw)
+
+
+def test_workspace_sizes_are_the_current_device_s(kdn, monkeypatch):
+    # a call on another device's tensors is refused, and leaves no size of the current device under the other's name
+    class On:
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    assert kdn._ws_device(On()) == 0
+    assert kdn._ws_device(torch.zeros(1)) == -1
