@@ -912,7 +912,14 @@ long long most_parts(long long rows, int C, int T) {
 // 265 -> 54 us.
 //
 // Packed sequences have one length on average and may have others; a long
-// average gets a cluster whatever the grid.
+// average gets a cluster whatever the grid, for the longest walks that are
+// left alone at the end: of two CTAs where the grid fills the device three
+// times, of four where it fills it, of eight else.  65536 bf16 tokens, us:
+//   32 sequences of 4096 channels, random lengths / one of half the tokens:
+//     two 324 / 323 (backward 546 / 544), four 397 / 404 (664 / 669);
+//   16 of 2048: two 215 / 256, four 176 / 180 (300 / 304), eight 228 / 234
+//     (382 / 388);
+//   8 of 1024: four 140 / 138 (250 / 247), eight 123 / 104 (213 / 184).
 kdn_status plan(const GatedArgs& a, const void* kernel, size_t alone, size_t smem, int V, int K, double fixed, Cut* cut) {
     Resident held;
     const cudaError_t e = resident(kernel, alone, smem, &held);
@@ -944,7 +951,8 @@ kdn_status plan(const GatedArgs& a, const void* kernel, size_t alone, size_t sme
     };
     consider(1, len, 0.0);
     if (a.nseq > 0) {
-        const long long s = len / tile / 4 < MAX_CLUSTER ? len / tile / 4 : MAX_CLUSTER;
+        const long long most = units > 3LL * held.clusters[0] ? 2 : units > held.clusters[0] ? 4 : MAX_CLUSTER;
+        const long long s = len / tile / 4 < most ? len / tile / 4 : most;
         if (cut->S < s && held.clusters[s - 1] > 0) cut->S = static_cast<int>(s);
         return KDN_OK;
     }

@@ -135,6 +135,28 @@ def test_packed_long_and_short_together():
     check_bwd(x, d, A, h0, go, gf, False, F32, offsets)
 
 
+@pytest.mark.parametrize("nseq,T,C", [(40, 41000, 768), (10, 20600, 1024)])
+def test_packed_long_ones_that_fill_the_device(nseq, T, C):
+    # clusters of two and of four over a full device: channels sampled at both ends
+    from bayesian_scan_gb300 import kdn
+    x, d, A, h0, go, gf = draw(1, 1, T, C, F32, seed=nseq, rows=nseq)
+    g = torch.Generator().manual_seed(nseq)
+    offsets = torch.tensor([5] + sorted(torch.randint(5, T - 50, (nseq - 1,), generator=g).tolist()) + [T - 50])
+    off = offsets.to(torch.int32).cuda()
+    dev = [t.cuda() for t in (x, d, A)]
+    o, f = kdn.gated_scan_fwd(*dev, h0=h0.cuda(), offsets=off)
+    got = kdn.gated_scan_bwd(*dev, o, go.cuda(), h0=h0.cuda(), offsets=off, grad_final_state=gf.cuda())
+    o, f, got = o.cpu(), f.cpu(), {n: t.cpu() for n, t in got.items()}
+    at = lambda t: t[..., [0, 1, 2, C - 3, C - 2, C - 1]].contiguous()
+    ro, rf, eo, ef = plain64.gated_fwd(at(x), at(d), at(A), at(h0), False, offsets)
+    plain64.assert_within(at(o), ro, eo, "out")
+    plain64.assert_within(at(f), rf, ef, "final_state")
+    val, err = plain64.gated_bwd(at(x), at(d), at(A), at(o), at(go), at(h0), False, offsets, at(gf))
+    for n in ("x", "d", "A", "h0"):
+        plain64.assert_within(at(got[n]), val[n], err[n], "grad_" + n)
+    assert kdn.get_device_error() == kdn.KDN_OK
+
+
 def test_offsets_out_of_range_are_clamped():
     from bayesian_scan_gb300 import kdn
     x, d, A, h0, go, gf = draw(1, 1, 100, 40, F32, seed=4, rows=3)
