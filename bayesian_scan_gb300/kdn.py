@@ -432,15 +432,15 @@ def _here(stream, *tensors):
     ``_on_one_device`` has the message."""
     if stream is not None:
         return False
-    dev = -1
+    dev = None
     for t in tensors:
         if t is not None:
             d = t.get_device()
             if d != dev:
-                if dev >= 0 or d < 0:
+                if dev is not None:
                     return False
                 dev = d
-    return dev >= 0 and dev == torch._C._cuda_getDevice()
+    return dev is not None and dev >= 0 and dev == torch._C._cuda_getDevice()
 
 
 _DTYPES = {torch.bfloat16: KDN_BF16, torch.float32: KDN_F32}

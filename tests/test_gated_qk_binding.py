@@ -1,0 +1,32 @@
+"""What the binding does around the gated recurrence's and the query/key
+preparation's calls: devices, sizes, streams and buffers.  Nothing here
+launches a kernel; device tensors are stood in for by objects."""
+import itertools
+
+import pytest
+import torch
+
+from bayesian_scan_gb300 import kdn
+
+
+class On:
+    """A tensor as far as the device checks look at one."""
+
+    def __init__(self, device):
+        self.device_index, self.is_cuda = device, device >= 0
+        self.device = torch.device("cuda", device) if device >= 0 else torch.device("cpu")
+
+    def get_device(self):
+        return self.device_index
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4])
+def test_every_operand_is_on_the_current_device(n, monkeypatch):
+    # host tensors (-1), the current device's (0) and another's (1), None among them, in every order
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    for devices in itertools.product((-1, 0, 1, None), repeat=n):
+        given = [d for d in devices if d is not None]
+        want = bool(given) and all(d == 0 for d in given)
+        tensors = [None if d is None else On(d) for d in devices]
+        assert kdn._here(None, *tensors) == want, devices
+        assert not kdn._here("a stream", *tensors)
