@@ -478,6 +478,13 @@ def _scratch(nbytes, like, stream):
     return t
 
 
+def _ints(*sizes):
+    """The C calls take sizes of 32 bits, to which ctypes cuts larger ones
+    without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes must be below 2**31, got {sizes}")
+
+
 def _token_ld(t, name, dt, shape):
     """Elements between consecutive tokens of a [B,T,C] or [B,H,T,C] tensor
     whose channels are adjacent and whose rows follow one another (dense, or
@@ -517,6 +524,7 @@ def _gated_sizes(x, A, offsets):
         if offsets.dim() != 1 or offsets.numel() < 2 or B != 1:
             raise ValueError("offsets must be [nseq + 1] with B = 1")
         rows = offsets.numel() - 1
+    _ints(B, H, T, C, rows)
     return B, H, T, C, 0 if offsets is None else rows, (rows, *heads)
 
 
@@ -562,6 +570,7 @@ def gated_scan_fwd(x, d, A, h0=None, leak=False, offsets=None, out=None, out_dty
 
 def gated_scan_bwd_workspace(B, H, T, C, nseq=0) -> int:
     """Bytes of device workspace ``gated_scan_bwd`` needs (0: none)."""
+    _ints(B, H, T, C, nseq)
     n = ctypes.c_longlong(0)
     st = lib.kdn_gated_scan_bwd_workspace(B, H, T, C, nseq, ctypes.byref(n))
     if st != KDN_OK:
@@ -638,6 +647,7 @@ def gated_step(x, d, A, state, leak=False, new_state=None, out=None, out_dtype=N
     shape, dt = x.shape, x.dtype
     if len(shape) not in (2, 3):
         raise ValueError(f"x must be [B,C] or [B,H,C], got {tuple(shape)}")
+    _ints(*shape)
     it = _dtype_of(x, "x")
     if new_state is None:
         new_state = state
@@ -683,6 +693,7 @@ def _head_rows(t, name, dt, B, T, dk):
         raise ValueError(f"{name} must be [{B},{T},heads,{dk}], got {tuple(shape)}")
     if t.dtype != dt:
         raise ValueError(f"{name} must be {dt}, got {t.dtype}")
+    _ints(*shape)
     H = shape[2]
     if t.is_contiguous():
         return H, H * dk
@@ -781,6 +792,7 @@ def qk_norm_rope_fwd(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms"
 
 def qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk) -> int:
     """Bytes of device workspace ``qk_norm_rope_bwd`` needs."""
+    _ints(B, T, Hq, Hk, dk)
     n = ctypes.c_longlong(0)
     st = lib.kdn_qk_norm_rope_bwd_workspace(B, T, Hq, Hk, dk, ctypes.byref(n))
     if st != KDN_OK:

@@ -30,3 +30,32 @@ def test_every_operand_is_on_the_current_device(n, monkeypatch):
         tensors = [None if d is None else On(d) for d in devices]
         assert kdn._here(None, *tensors) == want, devices
         assert not kdn._here("a stream", *tensors)
+
+
+def meta(*shape, dtype=torch.float32):
+    return torch.empty(shape, device="meta", dtype=dtype)
+
+
+BIG = 2 ** 32 + 5      # cut to 32 bits: 5
+
+
+@pytest.mark.parametrize("call", [
+    lambda: kdn.gated_scan_fwd(meta(1, BIG, 1), meta(1, BIG, 1), meta(1)),
+    lambda: kdn.gated_scan_fwd(meta(BIG, 1, 1), meta(BIG, 1, 1), meta(1)),
+    lambda: kdn.gated_scan_fwd(meta(1, BIG, 1, 1), meta(1, BIG, 1, 1), meta(BIG, 1)),
+    lambda: kdn.gated_scan_fwd(meta(1, 2, BIG), meta(1, 2, BIG), meta(BIG)),
+    lambda: kdn.gated_scan_fwd(meta(1, 2, 1), meta(1, 2, 1), meta(1), offsets=meta(BIG + 1, dtype=torch.int32)),
+    lambda: kdn.gated_scan_bwd(meta(1, BIG, 1), meta(1, BIG, 1), meta(1), meta(1, BIG, 1), meta(1, BIG, 1)),
+    lambda: kdn.gated_step(meta(BIG, 1), meta(BIG, 1), meta(1), meta(BIG, 1)),
+    lambda: kdn.gated_step(meta(2, BIG, 1), meta(2, BIG, 1), meta(BIG, 1), meta(2, BIG, 1)),
+    lambda: kdn.qk_norm_rope_fwd(meta(1, BIG, 1, 16), meta(1, BIG, 1, 16)),
+    lambda: kdn.qk_norm_rope_fwd(meta(BIG, 1, 1, 16), None),
+    lambda: kdn.qk_norm_rope_fwd(None, meta(1, 1, BIG, 16)),
+    lambda: kdn.qk_norm_rope_bwd(meta(1, BIG, 1, 16), None, meta(1, 1, BIG, 16), None),
+    lambda: kdn.gated_scan_bwd_workspace(BIG, 1, 1, 1),
+    lambda: kdn.gated_scan_bwd_workspace(1, 1, 1, 1, nseq=BIG),
+    lambda: kdn.qk_norm_rope_bwd_workspace(1, 1, BIG, 1, 16),
+])
+def test_sizes_that_32_bits_do_not_hold_are_refused(call):
+    with pytest.raises(ValueError, match=r"below 2\*\*31"):
+        call()
