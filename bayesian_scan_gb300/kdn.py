@@ -478,6 +478,12 @@ def _scratch(nbytes, like, stream):
     return t
 
 
+def _check_workspace(t, nbytes):
+    _check(t, "workspace")
+    if t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"workspace must hold {nbytes} bytes")
+
+
 def _ints(*sizes):
     """The C calls take sizes of 32 bits, to which ctypes cuts larger ones
     without a word."""
@@ -622,8 +628,8 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
     if workspace is None:
         if ws_bytes:
             workspace = _scratch(ws_bytes, x, stream)
-    elif workspace.numel() * workspace.element_size() < ws_bytes:
-        raise ValueError(f"workspace must hold {ws_bytes} bytes")
+    else:
+        _check_workspace(workspace, ws_bytes)
     gx, gd, gA, gh0 = g["x"], g["d"], g["A"], g["h0"]
     if not _here(stream, x, d, A, h0, offsets, out, grad_out, grad_final_state, gx, gd, gA, gh0, workspace):
         _on_one_device(stream, x=x, d=d, A=A, h0=h0, offsets=offsets, out=out, grad_out=grad_out,
@@ -848,8 +854,8 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
         ws_bytes = _qk_ws(_ws_device(first), B, T, Hq, Hk, dk)
         if workspace is None:
             workspace = _scratch(ws_bytes, first, stream)
-        elif workspace.numel() * workspace.element_size() < ws_bytes:
-            raise ValueError(f"workspace must hold {ws_bytes} bytes")
+        else:
+            _check_workspace(workspace, ws_bytes)
     else:
         workspace = None
     grad_q_out, grad_k_out = None if q is None else grad_q_out, None if k is None else grad_k_out

@@ -59,3 +59,14 @@ BIG = 2 ** 32 + 5      # cut to 32 bits: 5
 def test_sizes_that_32_bits_do_not_hold_are_refused(call):
     with pytest.raises(ValueError, match=r"below 2\*\*31"):
         call()
+
+
+def test_a_workspace_is_as_long_as_it_says():
+    # one byte seen a million times is not a workspace; nor is every second byte
+    x, A, q = torch.zeros(2, 5, 8), torch.zeros(8), torch.zeros(2, 5, 3, 32)
+    g = torch.zeros(2, 3, 5, 32)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 21, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            kdn.gated_scan_bwd(x, x, A, x, x, workspace=ws)
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            kdn.qk_norm_rope_bwd(q, q, g, g, grad_w=True, workspace=ws)
