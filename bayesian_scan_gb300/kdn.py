@@ -24,9 +24,14 @@ When the tensors passed to :func:`diag_scan_fwd` / :func:`mobius_scan` live in
 host memory, the call stages them to the current device on the current stream
 (pinned memory makes the copies asynchronous), runs the kernels there and
 copies the results back; it returns host tensors.
+
+Every call is issued on torch's current stream, or on ``stream``.  Given one,
+the call's inputs have to be ready there, and what it allocates (outputs and
+workspaces) is that stream's memory, as under ``torch.cuda.stream(stream)``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -138,6 +143,18 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _alloc(stream):
+    """Where a call makes the tensors that its caller did not give: in the
+    memory of the stream that will write them.  (A block that another stream
+    has let go may still be read by work queued there.)"""
+    if stream is None:
+        return _CURRENT
+    return torch.cuda.stream(stream if hasattr(stream, "device") else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+_CURRENT = contextlib.nullcontext()
+
+
 def _check(t, name, dtype=None, shape=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -194,10 +211,12 @@ def diag_scan_fwd(q, k, v, beta, d, A, I_prior=1.0, I0=None, mu0=None, out=None,
         if t is not None:
             _check(t, name, torch.float32, (B, H, dv, dk))
     if out is None:
-        out = torch.empty(B, H, T, dv, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            out = torch.empty(B, H, T, dv, device=q.device, dtype=torch.float32)
     _check(out, "out", torch.float32, (B, H, T, dv))
     if final_state is True:
-        final_state = torch.empty(2, B, H, dv, dk, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            final_state = torch.empty(2, B, H, dv, dk, device=q.device, dtype=torch.float32)
     elif final_state is False:
         final_state = None
     if final_state is not None:
@@ -239,16 +258,19 @@ def diag_mobius_scan_fwd(q, k, v, beta, d, A, ma, mb, mc, md, lambda0, I_prior=1
     _check(lambda0, "lambda0", torch.float32, (B * H,))
     _on_one_device(stream, q=q)
     if out is None:
-        out = torch.empty(B, H, T, dv, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            out = torch.empty(B, H, T, dv, device=q.device, dtype=torch.float32)
     _check(out, "out", torch.float32, (B, H, T, dv))
     if final_state is True:
-        final_state = torch.empty(2, B, H, dv, dk, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            final_state = torch.empty(2, B, H, dv, dk, device=q.device, dtype=torch.float32)
     elif final_state is False:
         final_state = None
     if final_state is not None:
         _check(final_state, "final_state", torch.float32, (2, B, H, dv, dk))
     if lambda_out is None:
-        lambda_out = torch.empty(B * H, T, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            lambda_out = torch.empty(B * H, T, device=q.device, dtype=torch.float32)
     _check(lambda_out, "lambda_out", torch.float32, (B * H, T))
     _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, I0=I0, mu0=mu0, out=out,
                    final_state=final_state, ma=ma, mb=mb, mc=mc, md=md, lambda0=lambda0,
@@ -285,10 +307,12 @@ def lin_scan_fwd(q, k, v, beta, d, A, I_prior=1.0, mu0=None, out=None, final_mu=
     if mu0 is not None:
         _check(mu0, "mu0", torch.float32, (B, H, dv, dk))
     if out is None:
-        out = torch.empty(B, H, T, dv, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            out = torch.empty(B, H, T, dv, device=q.device, dtype=torch.float32)
     _check(out, "out", torch.float32, (B, H, T, dv))
     if final_mu is True:
-        final_mu = torch.empty(B, H, dv, dk, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            final_mu = torch.empty(B, H, dv, dk, device=q.device, dtype=torch.float32)
     elif final_mu is False:
         final_mu = None
     if final_mu is not None:
@@ -344,11 +368,13 @@ def diag_scan_bwd(q, k, v, beta, d, A, grad_out, I_prior=1.0, I0=None, mu0=None,
     if grad_final_state is not None:
         _check(grad_final_state, "grad_final_state", torch.float32, (2, B, H, dv, dk))
     f32 = dict(device=q.device, dtype=torch.float32)
-    g = dict(q=torch.empty(B, H, T, dk, **f32), k=torch.empty(B, H, T, dk, **f32),
-             v=torch.empty(B, H, T, dv, **f32), beta=torch.empty(B, H, T, dv, **f32),
-             d=torch.empty(B, H, T, **f32), A=torch.empty(H, **f32))
+    with _alloc(stream):
+        g = dict(q=torch.empty(B, H, T, dk, **f32), k=torch.empty(B, H, T, dk, **f32),
+                 v=torch.empty(B, H, T, dv, **f32), beta=torch.empty(B, H, T, dv, **f32),
+                 d=torch.empty(B, H, T, **f32), A=torch.empty(H, **f32))
     if grad_init_state is True:
-        grad_init_state = torch.empty(2, B, H, dv, dk, **f32)
+        with _alloc(stream):
+            grad_init_state = torch.empty(2, B, H, dv, dk, **f32)
     elif grad_init_state is False:
         grad_init_state = None
     if grad_init_state is not None:
@@ -356,7 +382,8 @@ def diag_scan_bwd(q, k, v, beta, d, A, grad_out, I_prior=1.0, I0=None, mu0=None,
     g["init_state"] = grad_init_state
     ws_bytes = diag_scan_bwd_workspace(B, H, T, dk, dv)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 1), device=q.device, dtype=torch.uint8)
+        with _alloc(stream):
+            workspace = torch.empty(max(ws_bytes, 1), device=q.device, dtype=torch.uint8)
     elif workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError(f"workspace must hold {ws_bytes} bytes")
     _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, I0=I0, mu0=mu0, grad_out=grad_out,
@@ -391,7 +418,8 @@ def diag_step(q, k, v, beta, d, A, state, I_prior=1.0, out=None, stream=None):
             raise ValueError(f"{name} must be a CUDA tensor")
         _check(t, name, dtype, shape)
     if out is None:
-        out = torch.empty(B, H, dv, device=q.device, dtype=torch.float32)
+        with _alloc(stream):
+            out = torch.empty(B, H, dv, device=q.device, dtype=torch.float32)
     _check(out, "out", torch.float32, (B, H, dv))
     _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, state=state, out=out)
     st = lib.kdn_diag_step(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(d), _ptr(A), float(I_prior),
@@ -413,7 +441,8 @@ def mobius_scan(a, b, c, d, lambda0, out=None, stream=None):
         _check(t, name, torch.float32, (N, T))
     _check(lambda0, "lambda0", torch.float32, (N,))
     if out is None:
-        out = torch.empty(N, T, device=a.device, dtype=torch.float32)
+        with _alloc(stream):
+            out = torch.empty(N, T, device=a.device, dtype=torch.float32)
     _check(out, "out", torch.float32, (N, T))
     _on_one_device(stream, a=a, b=b, c=c, d=d, lambda0=lambda0, out=out)
     st = lib.kdn_mobius_scan(_ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(lambda0), _ptr(out),
@@ -447,8 +476,11 @@ _DTYPES = {torch.bfloat16: KDN_BF16, torch.float32: KDN_F32}
 _F32 = torch.float32
 
 
-def _new(like, dtype):
+def _new(like, dtype, stream):
     """An uninitialised dense tensor of like's shape."""
+    if stream is not None:
+        with _alloc(stream):
+            return _new(like, dtype, None)
     if dtype is None or dtype is like.dtype:
         if like.is_contiguous():
             return torch.empty_like(like)
@@ -470,12 +502,10 @@ def _ws_device(t):
 
 
 def _scratch(nbytes, like, stream):
-    """A call's own workspace: it is let go when the call returns, so a stream
-    that is not torch's current one has to be told of it."""
-    t = torch.empty(nbytes, device=like.device, dtype=torch.uint8)
-    if stream is not None and t.is_cuda:
-        t.record_stream(stream)
-    return t
+    """A call's own workspace, let go when the call returns: the stream's next
+    allocations may have it, in the stream's order."""
+    with _alloc(stream):
+        return torch.empty(nbytes, device=like.device, dtype=torch.uint8)
 
 
 def _check_workspace(t, nbytes):
@@ -554,12 +584,13 @@ def gated_scan_fwd(x, d, A, h0=None, leak=False, offsets=None, out=None, out_dty
     if h0 is not None:
         _check(h0, "h0", torch.float32, state)
     if out is None:
-        out = _new(x, out_dtype)
+        out = _new(x, out_dtype, stream)
     else:
         _check(out, "out", out_dtype, x.shape)
     ot = _dtype_of(out, "out")
     if final_state is True:
-        final_state = torch.empty(state, device=x.device, dtype=_F32)
+        with _alloc(stream):
+            final_state = torch.empty(state, device=x.device, dtype=_F32)
     elif final_state is False:
         final_state = None
     elif final_state is not None:
@@ -611,14 +642,15 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
     g = {}
     for name, t in (("x", grad_x), ("d", grad_d)):
         if t is None:
-            t = _new(x, None)
+            t = _new(x, None, stream)
         else:
             _check(t, "grad_" + name, x.dtype, x.shape)
         g[name] = t
     for name, t, shape in (("A", grad_A, tuple(A.shape)), ("h0", grad_h0, state)):
         if t is True:
             like = A if name == "A" else h0
-            t = torch.empty(shape, device=x.device, dtype=_F32) if like is None else torch.empty_like(like)
+            with _alloc(stream):
+                t = torch.empty(shape, device=x.device, dtype=_F32) if like is None else torch.empty_like(like)
         elif t is False:
             t = None
         elif t is not None:
@@ -658,7 +690,7 @@ def gated_step(x, d, A, state, leak=False, new_state=None, out=None, out_dtype=N
     if new_state is None:
         new_state = state
     if out is None:
-        out = _new(x, out_dtype)
+        out = _new(x, out_dtype, stream)
     heads = shape[1:]
     # a step is a few microseconds: one expression where all is well, the
     # messages where it is not
@@ -776,13 +808,15 @@ def qk_norm_rope_fwd(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms"
     if q is None:
         q_out = None
     elif q_out is None:
-        q_out = torch.empty((B, Hq, T, dk), device=first.device, dtype=od)
+        with _alloc(stream):
+            q_out = torch.empty((B, Hq, T, dk), device=first.device, dtype=od)
     else:
         _check(q_out, "q_out", od, (B, Hq, T, dk))
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty((B, Hk, T, dk), device=first.device, dtype=od)
+        with _alloc(stream):
+            k_out = torch.empty((B, Hk, T, dk), device=first.device, dtype=od)
     else:
         _check(k_out, "k_out", od, (B, Hk, T, dk))
     if not _here(stream, q, k, pos, inv_freq, wq, wk, axis, q_out, k_out):
@@ -836,14 +870,16 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
         gts.append(go.dtype)
         if gx is None:
             # (dense: t's heads lie side by side, so what empty_like makes of its order is the plain one)
-            g[name], lds[name] = torch.empty_like(t, memory_format=torch.contiguous_format), H * dk
+            with _alloc(stream):
+                g[name], lds[name] = torch.empty_like(t, memory_format=torch.contiguous_format), H * dk
         else:
             g[name] = gx
             n, lds[name] = _head_rows(gx, "grad_" + name, t.dtype, B, T, dk)
             if n != H:
                 raise ValueError(f"grad_{name} must have {H} heads, got {n}")
         if (w is not None) if grad_w is None else grad_w:
-            g["w" + name] = torch.empty(dk, device=t.device, dtype=_F32) if w is None else torch.empty_like(w)
+            with _alloc(stream):
+                g["w" + name] = torch.empty(dk, device=t.device, dtype=_F32) if w is None else torch.empty_like(w)
     if len(set(gts)) > 1:
         raise ValueError("grad_q_out and grad_k_out must have one type")
     ot = _DTYPES.get(gts[0])
