@@ -164,6 +164,12 @@ def _check(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _check_workspace(t, nbytes):
+    _check(t, "workspace")
+    if t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"workspace must hold {nbytes} bytes")
+
+
 def _on_one_device(stream, **tensors):
     """Every given tensor must be a CUDA tensor on the current device (the
     device whose stream the call is issued on): the C ABI receives raw
@@ -384,8 +390,8 @@ def diag_scan_bwd(q, k, v, beta, d, A, grad_out, I_prior=1.0, I0=None, mu0=None,
     if workspace is None:
         with _alloc(stream):
             workspace = torch.empty(max(ws_bytes, 1), device=q.device, dtype=torch.uint8)
-    elif workspace.numel() * workspace.element_size() < ws_bytes:
-        raise ValueError(f"workspace must hold {ws_bytes} bytes")
+    else:
+        _check_workspace(workspace, ws_bytes)
     _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, I0=I0, mu0=mu0, grad_out=grad_out,
                    grad_final_state=grad_final_state, grad_init_state=grad_init_state,
                    workspace=workspace)
@@ -506,12 +512,6 @@ def _scratch(nbytes, like, stream):
     allocations may have it, in the stream's order."""
     with _alloc(stream):
         return torch.empty(nbytes, device=like.device, dtype=torch.uint8)
-
-
-def _check_workspace(t, nbytes):
-    _check(t, "workspace")
-    if t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"workspace must hold {nbytes} bytes")
 
 
 def _ints(*sizes):

@@ -70,3 +70,14 @@ def test_a_workspace_is_as_long_as_it_says():
             kdn.gated_scan_bwd(x, x, A, x, x, workspace=ws)
         with pytest.raises(ValueError, match="workspace must be contiguous"):
             kdn.qk_norm_rope_bwd(q, q, g, g, grad_w=True, workspace=ws)
+
+
+def test_the_diagonal_backward_s_workspace_too():
+    class Dev(torch.Tensor):
+        is_cuda = True
+
+    q, v, d = (torch.zeros(1, 2, 5, 16).as_subclass(Dev) for _ in range(3))
+    d = d[..., 0].contiguous()
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 24)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        kdn.diag_scan_bwd(q, q, v, v, d, torch.zeros(2), v, workspace=ws)
