@@ -93,7 +93,7 @@ __device__ __forceinline__ Gate2 gate2(F2 y) {
     return g;
 }
 
-// The same as alpha = a + e: a the rounded value, e what the rounding lost.
+// The same as alpha = a + e: a the value rounded down, e what the rounding lost.
 // A long memory has alpha next to 1, where a float's step is 6e-8 whatever
 // 1 - alpha is: a state carried through a thousand rounded decays would be
 // off by 7e-6.  So a span's decay is 2^y of its summed exponents, in this
@@ -101,7 +101,20 @@ __device__ __forceinline__ Gate2 gate2(F2 y) {
 // rounded alphas.
 //
 // |y| <= 0.5: degree 5, 1.2e-7 of 2^y - 1; beyond, a - 1 and m are the same
-// rounding, so e is zero by itself.
+// rounding, and e is what TINY makes of zero.
+//
+// An infinite state goes through a s + (e s + b) as it is: a and e have one
+// sign and neither is 0 (a alone where y = -infinity, a decay of nothing: 0
+// times infinity is NaN) -- also of a span whose decay underflows where no
+// token's does.
+constexpr float TINY = 1.4e-45f;   // 2^-149
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 struct Gate {
     float a, e, w;
 };
@@ -117,8 +130,8 @@ __device__ __forceinline__ Gate gate(float y) {
     const bool small = fabsf(y) <= 0.5f;
     const float m = small ? y * p : big - 1.f;   // 2^y - 1
     Gate g;
-    g.a = small ? 1.f + m : big;
-    g.e = m - (g.a - 1.f);
+    g.a = max_nan(small ? __fadd_rd(1.f, m) : big, y > -INFINITY ? TINY : 0.f);
+    g.e = max_nan(m - (g.a - 1.f), TINY);
     g.w = -m;
     return g;
 }

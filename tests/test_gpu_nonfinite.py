@@ -1,0 +1,87 @@
+"""Infinities and NaN in the gated recurrence and in queries and keys: they
+propagate as the definition in IEEE arithmetic has it, and nowhere else."""
+import math
+
+import pytest
+import torch
+
+import plain64
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+INF, NAN = math.inf, math.nan
+
+
+def assert_same(got, ref, err, name):
+    """Equal where ref is not finite (NaN for NaN, the infinity's sign), else
+    within the bound and half a step of got's type."""
+    got = got.detach().cpu().double()
+    assert torch.equal(got.isnan(), ref.isnan()), f"{name}: NaN in other places"
+    odd = ref.isinf()
+    assert torch.equal(got.isinf(), odd) and torch.equal(got[odd], ref[odd]), f"{name}: infinities in other places"
+    ok = ref.isfinite()
+    return got[ok], ref[ok], err[ok]
+
+
+def assert_within(got, ref, err, name):
+    g, r, e = assert_same(got, ref, err, name)
+    plain64.assert_within(g.to(got.dtype), r, e, name)
+
+
+def draw(B, T, C, dtype, rows, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(B, 1, T, C, generator=g).to(dtype)
+    d = torch.nn.functional.softplus(torch.randn(B, 1, T, C, generator=g)).to(dtype)
+    # no token's decay underflows (A d < 6), the decay of a warp's, tile's or part's tokens does
+    A = torch.exp(torch.empty(1, C).uniform_(math.log(1e-3), 0.0, generator=g))
+    h0 = torch.randn(rows, 1, C, generator=g)
+    go = torch.randn(B, 1, T, C, generator=g).to(dtype)
+    gf = torch.randn(rows, 1, C, generator=g)
+    return x, d, A, h0, go, gf
+
+
+# tiles alone, clusters, parts, packed sequences; every alignment
+CASES = [(2, 77, 64, F32, None), (1, 1300, 200, BF16, None), (1, 1300, 201, BF16, None), (1, 9001, 64, F32, None),
+         (2, 300, 66, BF16, None), (1, 1500, 40, F32, [0, 1, 1, 40, 700, 1500]), (160, 130, 64, F32, None)]
+
+
+@pytest.mark.parametrize("B,T,C,dtype,offsets", CASES)
+@pytest.mark.parametrize("leak", [False, True])
+def test_infinite_states_and_inputs(B, T, C, dtype, offsets, leak):
+    from bayesian_scan_gb300 import kdn
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32)
+    rows = B if offsets is None else len(offsets) - 1
+    x, d, A, h0, _, _ = draw(B, T, C, dtype, rows, T + C)
+    h0[:, 0, 3], h0[:, 0, 4], h0[:, 0, 5], h0[0, 0, 6] = INF, -INF, NAN, INF
+    x[:, 0, T // 3, 7], x[:, 0, 0, 8] = INF, -INF
+    x[:, 0, T // 3, 9], x[:, 0, T // 2, 9] = INF, -INF       # their sum is NaN
+    x[:, 0, T // 2, 10] = NAN
+    d[:, 0, T // 3, 11] = NAN
+    # an infinite gate forgets the state, and makes NaN of an infinite one (to the reference a gate of
+    # 2000, whose decay is 0 in 64 bits too)
+    A[0, 12:14], h0[:, 0, 13] = 1.0, INF
+    gate = d.clone()
+    d[:, 0, T // 2, 12:14], gate[:, 0, T // 2, 12:14] = 2000.0, INF
+    o, f = kdn.gated_scan_fwd(x.cuda(), gate.cuda(), A.cuda(), h0=h0.cuda(), leak=leak,
+                              offsets=None if off is None else off.cuda())
+    ro, rf, eo, ef = plain64.gated_fwd(x, d, A, h0, leak, off)
+    assert_within(o, ro, eo, "out")
+    assert_within(f, rf, ef, "final_state")
+
+
+@pytest.mark.parametrize("leak", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_step_on_infinite_states(leak, dtype):
+    from bayesian_scan_gb300 import kdn
+    g = torch.Generator().manual_seed(5)
+    B, C = 3, 70
+    x, A, state = torch.randn(B, C, generator=g).to(dtype), torch.rand(C, generator=g), torch.randn(B, C, generator=g)
+    d = (torch.rand(B, C, generator=g) * 3).to(dtype)        # gates on both sides of 1/2
+    state[0, ::2], state[1, ::3], state[2, ::5] = INF, -INF, NAN
+    x[0, :8], x[1, :9], d[:, 20] = -INF, -INF, NAN
+    ro, rf, eo, ef = plain64.gated_fwd(x[:, None, None], d[:, None, None], A[None], state[:, None], leak)
+    s = state.cuda()
+    o = kdn.gated_step(x.cuda(), d.cuda(), A.cuda(), s, leak=leak)
+    assert_within(o, ro[:, 0, 0], eo[:, 0, 0], "out")
+    assert_within(s, rf[:, 0], ef[:, 0], "state")
