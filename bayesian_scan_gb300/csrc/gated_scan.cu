@@ -658,7 +658,7 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
                     }
                     const float m = u[0] * prev[0];
                     gd[0] = nA[0] * m;
-                    dA[0] = fmaf(dv.get(0), m, dA[0]);       // (d = 0 outside the sequence)
+                    if (t + j >= at.lo) dA[0] = fmaf(dv.get(0), m, dA[0]);   // (before it d = 0, but m may be NaN)
                 } else {
                     const F2 dh = add2(F2{u[0], u[1]}, F2{gv.get(0), gv.get(1)});
                     const F2 n = mul2(F2{a[k][0], a[k][1]}, dh);
@@ -675,8 +675,10 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
                     gx[1] = x.y;
                     gd[0] = d.x;
                     gd[1] = d.y;
-                    dA[0] = sum.x;
-                    dA[1] = sum.y;
+                    if (t + j >= at.lo) {
+                        dA[0] = sum.x;
+                        dA[1] = sum.y;
+                    }
                 }
                 if (SIZE == 16) {
                     Vec<TI, V> q;

@@ -85,3 +85,25 @@ def test_step_on_infinite_states(leak, dtype):
     o = kdn.gated_step(x.cuda(), d.cuda(), A.cuda(), s, leak=leak)
     assert_within(o, ro[:, 0, 0], eo[:, 0, 0], "out")
     assert_within(s, rf[:, 0], ef[:, 0], "state")
+
+
+@pytest.mark.parametrize("B,T,C,dtype,offsets", CASES)
+@pytest.mark.parametrize("leak", [False, True])
+def test_infinite_gradients(B, T, C, dtype, offsets, leak):
+    from bayesian_scan_gb300 import kdn
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32)
+    rows = B if offsets is None else len(offsets) - 1
+    x, d, A, h0, go, gf = draw(B, T, C, dtype, rows, T + C)
+    x, h0 = x.abs() + 0.5, h0.abs() + 0.5                    # without leak, the terms of grad A have one sign
+    out = plain64.gated_fwd(x, d, A, h0, leak, off)[0].to(dtype)
+    gf[:, 0, 3], gf[:, 0, 4], gf[:, 0, 5] = INF, -INF, NAN
+    go[:, 0, T // 3, 7], go[:, 0, T - 1, 8] = INF, -INF
+    go[:, 0, T // 3, 9], go[:, 0, T // 2, 9] = INF, -INF
+    go[:, 0, T // 2, 10] = NAN
+    d[:, 0, T // 3, 11] = NAN
+    cu = lambda t: None if t is None else t.cuda()
+    got = kdn.gated_scan_bwd(*(t.cuda() for t in (x, d, A, out, go)), h0=h0.cuda(), leak=leak, offsets=cu(off),
+                             grad_final_state=gf.cuda())
+    val, err = plain64.gated_bwd(x, d, A, out, go, h0, leak, off, gf)
+    for n in ("x", "d", "h0", "A"):
+        assert_within(got[n], val[n], err[n], "grad_" + n)
