@@ -373,7 +373,8 @@ KDN_API kdn_status kdn_mobius_scan_noalloc(const float* a, const float* b, const
  *             are x_ld and d_ld elements apart (>= C; C when dense), rows
  *             (b,h) T * ld: with H = 1 a tensor may be a column slice of a
  *             wider [B,T,ld] projection.
- *   A         [H,C] fp32          gate rate of each channel
+ *   A         [H,C] fp32          gate rate of each channel, at most 2^127 (A
+ *             log2(e) has to be a float)
  *   h0        [B,H,C] fp32 or NULL (h_0 = 0)
  *   out       [B,H,T,C] out_dtype, dense: h_t
  *   final_state [B,H,C] fp32 or NULL: h_T (feeding it back as h0 of a call on

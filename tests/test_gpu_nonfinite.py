@@ -107,3 +107,27 @@ def test_infinite_gradients(B, T, C, dtype, offsets, leak):
     val, err = plain64.gated_bwd(x, d, A, out, go, h0, leak, off, gf)
     for n in ("x", "d", "h0", "A"):
         assert_within(got[n], val[n], err[n], "grad_" + n)
+
+
+@pytest.mark.parametrize("T", [1, 77, 1300, 9001])
+@pytest.mark.parametrize("leak", [False, True])
+def test_rates_at_the_end_of_the_range(T, leak):
+    # such a channel forgets at once, also in its final state and in the gradient of its initial one,
+    # whatever lies behind the sequence's end in a tile
+    from bayesian_scan_gb300 import kdn
+    C = 40
+    x, d, A, h0, go, gf = draw(1, T, C, F32, 1, T)
+    d = d + 0.01
+    A[0, :3] = torch.tensor([2.0 ** 127, 1e38, 3e37])
+    o, f = kdn.gated_scan_fwd(x.cuda(), d.cuda(), A.cuda(), h0=h0.cuda(), leak=leak)
+    ro, rf, eo, ef = plain64.gated_fwd(x, d, A, h0, leak)
+    plain64.assert_within(o, ro, eo, "out")
+    plain64.assert_within(f, rf, ef, "final_state")
+    got = kdn.gated_scan_bwd(x.cuda(), d.cuda(), A.cuda(), ro.float().cuda(), go.cuda(), h0=h0.cuda(), leak=leak,
+                             grad_final_state=gf.cuda())
+    val, err = plain64.gated_bwd(x, d, A, ro.float(), go, h0, leak, None, gf)
+    for n in ("x", "d", "h0", "A"):
+        plain64.assert_within(got[n], val[n], err[n], "grad_" + n)
+    s = h0[:, 0].cuda()
+    y = kdn.gated_step(x[:, 0, 0].cuda(), d[:, 0, 0].cuda(), A[0].cuda(), s, leak=leak)
+    plain64.assert_within(y, ro[:, 0, 0], eo[:, 0, 0], "step")
