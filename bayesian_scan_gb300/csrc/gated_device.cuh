@@ -62,6 +62,12 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 constexpr float LOG2E = 1.4426950408889634f;
 
 // The gate alpha = exp(-A d) = 2^y, y = -A log2(e) d, of two elements, and
@@ -108,12 +114,6 @@ __device__ __forceinline__ Gate2 gate2(F2 y) {
 // times infinity is NaN) -- also of a span whose decay underflows where no
 // token's does.
 constexpr float TINY = 1.4e-45f;   // 2^-149
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 
 struct Gate {
     float a, e, w;

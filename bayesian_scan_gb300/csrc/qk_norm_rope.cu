@@ -16,6 +16,7 @@
 // a few rows' loads in flight.
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "gated_device.cuh"
@@ -184,20 +185,32 @@ __device__ __forceinline__ void put_row(T* p, const Place& q, const Row8& o) {
     }
 }
 
+__device__ __forceinline__ Row8 times(const Row8& x, const Row8& y) {
+    return Row8{{mul2(x.a[0], y.a[0]), mul2(x.a[1], y.a[1])}, {mul2(x.b[0], y.b[0]), mul2(x.b[1], y.b[1])}};
+}
+
 __device__ __forceinline__ F2 neg2(F2 v) { return F2{-v.x, -v.y}; }
 
 // Rotation by the pairs' angles, c and s each (pair 0, pair 1), (pair 2, pair 3).
 struct Turn {
     F2 c[2], s[2];
 };
-template <bool BACK>
-__device__ __forceinline__ void rotate(Row8& v, const Turn& t) {
+// Pairs behind rot have cos = 1 and sin = 0, whose product with an infinite or
+// NaN element is NaN for its partner.  EXACT leaves those pairs as they are.
+//
+// Calls that rotate part of a head have kernels of their own (PART) that go
+// over rows again, exactly, that turn out to hold other than numbers: in one
+// kernel for all calls this cost the layer 90 -> 91 us and its backward 176 ->
+// 183, selects in every row 94 and 182.
+template <bool BACK, bool EXACT>
+__device__ __forceinline__ void rotate(Row8& v, const Turn& t, const Place& q) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const F2 s = BACK ? neg2(t.s[i]) : t.s[i];
-        const F2 a = fma2(v.a[i], t.c[i], neg2(mul2(v.b[i], s)));
-        v.b[i] = fma2(v.a[i], s, mul2(v.b[i], t.c[i]));
-        v.a[i] = a;
+        const F2 a = fma2(v.a[i], t.c[i], neg2(mul2(v.b[i], s))), b = fma2(v.a[i], s, mul2(v.b[i], t.c[i]));
+        const bool x = !EXACT || q.p0 + 2 * i < q.half, y = !EXACT || q.p0 + 2 * i + 1 < q.half;
+        v.a[i] = F2{x ? a.x : v.a[i].x, y ? a.y : v.a[i].y};
+        v.b[i] = F2{x ? b.x : v.b[i].x, y ? b.y : v.b[i].y};
     }
 }
 
@@ -205,6 +218,23 @@ template <bool INTER>
 __device__ __forceinline__ Row8 weight_of(const float* w, const Place& q) {
     if (!w) return Row8{{both(1.f), both(1.f)}, {both(1.f), both(1.f)}};
     return row_of<INTER>(get_raw(w, q));
+}
+
+// The sum of squares up to which a row's elements, each times its weight, are
+// numbers: any (of less than 2^64, then) unless a weight is 2^63 or more.
+template <bool INTER>
+__device__ __forceinline__ float most_squares(const QkArgs& p, const Place& q) {
+    float most = FLT_MAX;
+    for (const float* w : p.w) {
+        if (!w) continue;
+        const Row8 r = weight_of<INTER>(w, q);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (!(fabsf(r.a[i].x) < 0x1p63f && fabsf(r.a[i].y) < 0x1p63f && fabsf(r.b[i].x) < 0x1p63f &&
+                  fabsf(r.b[i].y) < 0x1p63f))
+                most = -1.f;
+    }
+    return most;
 }
 
 // How one call's rows are dealt out: HS heads of a token side by side in a
@@ -339,22 +369,25 @@ struct Ring {
     }
 };
 
-// One row from the loaded elements to the stored ones.
-template <typename TI, typename TO, int DK, bool INTER>
-__device__ __forceinline__ void qk_row(const QkArgs& p, const RawRow<TI>& raw, const Row8& w, const Turn& turn,
-                                       const Place& q, TO* y, bool on) {
+// One row from the loaded elements to the stored ones; returns its sum of
+// squares.
+template <typename TI, typename TO, int DK, bool INTER, bool EXACT = false>
+__device__ __forceinline__ float qk_row(const QkArgs& p, const RawRow<TI>& raw, const Row8& w, const Turn& turn,
+                                        const Place& q, TO* y, bool on) {
     Row8 v = row_of<INTER>(raw);
-    const F2 r = both(inverse_norm<DK>(p, row_dot<DK / 8>(v, v)));
+    const float ss = row_dot<DK / 8>(v, v);
+    const F2 r = both(inverse_norm<DK>(p, ss));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         v.a[k] = mul2(v.a[k], mul2(r, w.a[k]));
         v.b[k] = mul2(v.b[k], mul2(r, w.b[k]));
     }
-    rotate<false>(v, turn);
+    rotate<false, EXACT>(v, turn, q);
     if (on) put_row<INTER>(y, q, v);
+    return ss;
 }
 
-template <typename TI, typename TO, int DK, bool INTER>
+template <typename TI, typename TO, int DK, bool INTER, bool PART>
 __global__ void __launch_bounds__(WARPS * 32, FWD_BLOCKS_PER_SM)
 qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
     constexpr int UNROLL = sizeof(TI) == 2 ? 4 : 2;
@@ -362,6 +395,7 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
     freqs.fill(p);
     Place2<DK> at;
     const Place q = place_of<INTER>(at.l, p.rot);
+    const float most = PART ? most_squares<INTER>(p, q) : 0.f;
     const int step = deal.HS * deal.chunks;
     const long long xstep = static_cast<long long>(step) * DK, ystep = xstep * p.T;
     for (long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); item < deal.items;
@@ -377,6 +411,7 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
             TO* y = static_cast<TO*>(p.y[which]) +
                     ((static_cast<long long>(at.b) * H + at.h) * p.T + at.t) * DK;
             // UNROLL rows' loads in flight; a batch whose rows are all there has no predicates
+            float worst = 0.f;
             const int whole = !__all_sync(0xffffffffu, at.here) ? 0
                               : __all_sync(0xffffffffu, at.h + (steps - 1) * step < H) ? steps : steps - 1;
             for (int i = 0; i < steps; i += UNROLL) {
@@ -389,7 +424,7 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
                     }
 #pragma unroll
                     for (int u = 0; u < UNROLL; ++u) {
-                        qk_row<TI, TO, DK, INTER>(p, raw[u], w, turn, q, y, true);
+                        worst = max_nan(worst, qk_row<TI, TO, DK, INTER>(p, raw[u], w, turn, q, y, true));
                         y += ystep;
                     }
                 } else {
@@ -402,9 +437,23 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
 #pragma unroll
                     for (int u = 0; u < UNROLL; ++u) {
                         if (i + u >= steps) break;             // (the warp as one)
-                        qk_row<TI, TO, DK, INTER>(p, raw[u], w, turn, q, y, at.here && at.h + (i + u) * step < H);
+                        worst = max_nan(worst, qk_row<TI, TO, DK, INTER>(p, raw[u], w, turn, q, y,
+                                                                         at.here && at.h + (i + u) * step < H));
                         y += ystep;
                     }
+                }
+            }
+            if (PART && __any_sync(0xffffffffu, !(worst <= most))) {
+                x = static_cast<const TI*>(p.x[which]) + at.token * p.ld[which] + at.h * DK;
+                y = static_cast<TO*>(p.y[which]) + ((static_cast<long long>(at.b) * H + at.h) * p.T + at.t) * DK;
+#pragma unroll 1
+                for (int i = 0; i < steps; ++i) {
+                    const bool on = at.here && at.h + i * step < H;
+                    RawRow<TI> raw{};
+                    if (on) raw = get_raw(x, q);
+                    qk_row<TI, TO, DK, INTER, true>(p, raw, w, turn, q, y, on);
+                    x += xstep;
+                    y += ystep;
                 }
             }
         }
@@ -425,7 +474,7 @@ struct BulkShared {
     Freqs<DK> freqs;
 };
 
-template <typename TI, typename TO, int DK, bool INTER>
+template <typename TI, typename TO, int DK, bool INTER, bool PART>
 __global__ void __launch_bounds__(WARPS * 32, 2)
 qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
     constexpr int LPR = DK / 8, RPW = 32 / LPR, ROW = DK * static_cast<int>(sizeof(TI)), HEADS = SEG / ROW;
@@ -438,6 +487,7 @@ qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
     }
     sh.freqs.fill(p);                                          // (and a barrier)
     const Place q = place_of<INTER>(l, p.rot);
+    const float most = PART ? most_squares<INTER>(p, q) : 0.f;
     const long long tokens = static_cast<long long>(p.B) * p.T, stride = static_cast<long long>(gridDim.x) * WARPS;
     const int segs[2] = {(p.heads[0] + HEADS - 1) / HEADS, (p.heads[1] + HEADS - 1) / HEADS}, per = segs[0] + segs[1];
     const long long first = static_cast<long long>(blockIdx.x) * WARPS + warp;
@@ -488,15 +538,18 @@ qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
                     }
                 } while (s != cslot);
             }
-            const TI* x = reinterpret_cast<const TI*>(sh.ring[warp][slot]) + sub * DK;
-            TO* y = static_cast<TO*>(p.y[which]) + ((static_cast<long long>(b) * H + h0 + sub) * p.T + t) * DK;
+            const TI* x0 = reinterpret_cast<const TI*>(sh.ring[warp][slot]) + sub * DK;
+            TO* y0 = static_cast<TO*>(p.y[which]) + ((static_cast<long long>(b) * H + h0 + sub) * p.T + t) * DK;
+            const TI* x = x0;
+            TO* y = y0;
+            float worst = 0.f;
             int i = 0;
 #pragma unroll 4
             for (; i + RPW <= n; i += RPW) {
                 RawRow<TI> raw;
                 raw.u = *reinterpret_cast<const Raw4<TI>*>(x + q.g0);
                 raw.v = *reinterpret_cast<const Raw4<TI>*>(x + q.g1);
-                qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, true);
+                worst = max_nan(worst, qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, true));
                 x += RPW * DK;
                 y += RPW * ystep;
             }
@@ -506,7 +559,22 @@ qk_fwd_bulk_kernel(const __grid_constant__ QkArgs p, long long wait_ns) {
                     raw.u = *reinterpret_cast<const Raw4<TI>*>(x + q.g0);
                     raw.v = *reinterpret_cast<const Raw4<TI>*>(x + q.g1);
                 }
-                qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, i + sub < n);
+                worst = max_nan(worst, qk_row<TI, TO, DK, INTER>(p, raw, w, turn, q, y, i + sub < n));
+            }
+            if (PART && __any_sync(0xffffffffu, !(worst <= most))) {
+                x = x0;
+                y = y0;
+#pragma unroll 1
+                for (i = 0; i < n; i += RPW) {
+                    RawRow<TI> raw{};
+                    if (i + sub < n) {
+                        raw.u = *reinterpret_cast<const Raw4<TI>*>(x + q.g0);
+                        raw.v = *reinterpret_cast<const Raw4<TI>*>(x + q.g1);
+                    }
+                    qk_row<TI, TO, DK, INTER, true>(p, raw, w, turn, q, y, i + sub < n);
+                    x += RPW * DK;
+                    y += RPW * ystep;
+                }
             }
             __syncwarp();                                      // the slot has been read
             copy();
@@ -526,7 +594,8 @@ struct BwdRing {
     Ring<TO, DEPTH> g;
 };
 
-template <typename TI, typename TO, int DK, bool INTER>
+// (PART here also without a norm: its gradient has no term of x, not even 0 x.)
+template <typename TI, typename TO, int DK, bool INTER, bool PART>
 __global__ void __launch_bounds__(WARPS * 32, BWD_BLOCKS_PER_SM)
 qk_bwd_kernel(const __grid_constant__ QkArgs p, const Deal deal, float* part) {
     constexpr int LPR = DK / 8, DEPTH = BWD_DEPTH;
@@ -586,17 +655,20 @@ qk_bwd_kernel(const __grid_constant__ QkArgs p, const Deal deal, float* part) {
                 }
                 const Row8 v = row_of<INTER>(xr);
                 Row8 g = row_of<INTER>(gr);
-                rotate<true>(g, turn);
+                rotate<true, false>(g, turn, q);
                 // a row that is not there adds nothing, whatever 1 / sqrt(eps) is
                 const float ss = row_dot<LPR>(v, v), r = on ? inverse_norm<DK>(p, ss) : 0.f;
                 fetch(i + DEPTH);
-                Row8 t;                                        // g w
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    t.a[k] = mul2(g.a[k], w.a[k]);
-                    t.b[k] = mul2(g.b[k], w.b[k]);
+                Row8 t = times(g, w);
+                float dot = row_dot<LPR>(t, v);
+                const bool odd = PART && __any_sync(0xffffffffu, !(fabsf(dot) <= FLT_MAX));
+                if (odd) {                                     // x or g is not finite, or their product
+                    g = row_of<INTER>(gr);
+                    rotate<true, true>(g, turn, q);
+                    t = times(g, w);
+                    dot = row_dot<LPR>(t, v);
                 }
-                const float back = p.norm == KDN_NORM_NONE ? 0.f : -(r * r * r) * (row_dot<LPR>(t, v) * inv_n);
+                const float back = p.norm == KDN_NORM_NONE ? 0.f : -(r * r * r) * (dot * inv_n);
                 Row8 o;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -605,6 +677,7 @@ qk_bwd_kernel(const __grid_constant__ QkArgs p, const Deal deal, float* part) {
                     dw[which].a[k] = fma2(mul2(both(r), v.a[k]), g.a[k], dw[which].a[k]);
                     dw[which].b[k] = fma2(mul2(both(r), v.b[k]), g.b[k], dw[which].b[k]);
                 }
+                if (odd && p.norm == KDN_NORM_NONE) o = t;
                 if (on) put_row<INTER>(gx + h * DK, q, o);
             }
         }
@@ -713,17 +786,21 @@ kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream, long long wait_ns
             using TI = decltype(ti);
             using TO = decltype(to);
             constexpr int DK = decltype(n)::value;
+            const int form = 2 * a.interleaved + (a.rot < DK);
             if (bulk_ok(a, 2 * sm_count())) {
-                auto kernel = a.interleaved ? qk_fwd_bulk_kernel<TI, TO, DK, true> : qk_fwd_bulk_kernel<TI, TO, DK, false>;
+                const decltype(&qk_fwd_bulk_kernel<TI, TO, DK, false, false>) forms[] = {
+                    qk_fwd_bulk_kernel<TI, TO, DK, false, false>, qk_fwd_bulk_kernel<TI, TO, DK, false, true>,
+                    qk_fwd_bulk_kernel<TI, TO, DK, true, false>, qk_fwd_bulk_kernel<TI, TO, DK, true, true>};
+                const auto kernel = forms[form];
                 const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), sizeof(BulkShared<DK>));
                 if (e != cudaSuccess) return from_cuda(e);
                 kernel<<<2 * sm_count(), WARPS * 32, sizeof(BulkShared<DK>), stream>>>(a, wait_ns);
                 return from_cuda(cudaGetLastError());
             }
-            if (a.interleaved)
-                qk_fwd_kernel<TI, TO, DK, true><<<blocks, WARPS * 32, 0, stream>>>(a, deal);
-            else
-                qk_fwd_kernel<TI, TO, DK, false><<<blocks, WARPS * 32, 0, stream>>>(a, deal);
+            const decltype(&qk_fwd_kernel<TI, TO, DK, false, false>) forms[] = {
+                qk_fwd_kernel<TI, TO, DK, false, false>, qk_fwd_kernel<TI, TO, DK, false, true>,
+                qk_fwd_kernel<TI, TO, DK, true, false>, qk_fwd_kernel<TI, TO, DK, true, true>};
+            forms[form]<<<blocks, WARPS * 32, 0, stream>>>(a, deal);
             return from_cuda(cudaGetLastError());
         });
     });
@@ -752,7 +829,10 @@ kdn_status qk_bwd_launch(const QkArgs& a, cudaStream_t stream) {
             using TI = decltype(ti);
             using TO = decltype(to);
             constexpr int DK = decltype(n)::value;
-            auto kernel = a.interleaved ? qk_bwd_kernel<TI, TO, DK, true> : qk_bwd_kernel<TI, TO, DK, false>;
+            const decltype(&qk_bwd_kernel<TI, TO, DK, false, false>) forms[] = {
+                qk_bwd_kernel<TI, TO, DK, false, false>, qk_bwd_kernel<TI, TO, DK, false, true>,
+                qk_bwd_kernel<TI, TO, DK, true, false>, qk_bwd_kernel<TI, TO, DK, true, true>};
+            const auto kernel = forms[2 * a.interleaved + (a.rot < DK || a.norm == KDN_NORM_NONE)];
             const size_t smem = sizeof(BwdRing<TI, TO, BWD_DEPTH>);
             const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
             if (e != cudaSuccess) return from_cuda(e);

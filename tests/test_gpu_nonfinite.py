@@ -131,3 +131,33 @@ def test_rates_at_the_end_of_the_range(T, leak):
     s = h0[:, 0].cuda()
     y = kdn.gated_step(x[:, 0, 0].cuda(), d[:, 0, 0].cuda(), A[0].cuda(), s, leak=leak)
     plain64.assert_within(y, ro[:, 0, 0], eo[:, 0, 0], "step")
+
+
+@pytest.mark.parametrize("dk,rot", [(128, 64), (128, 0), (64, 6), (16, 8), (128, 126), (32, 16)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,T,H", [(1, 5, 3), (2, 701, 32)])
+def test_elements_that_do_not_rotate_are_copied(dk, rot, interleaved, B, T, H):
+    from bayesian_scan_gb300 import kdn
+    g = torch.Generator().manual_seed(dk + rot)
+    x, go = torch.randn(B, T, H, dk, generator=g), torch.randn(B, H, T, dk, generator=g)
+    w = 1 + torch.rand(dk, generator=g)
+    for t in (x, go):
+        for i, v in enumerate((INF, NAN, -INF)):
+            t.view(-1, dk)[i::7, rot + i % (dk - rot)] = v
+    inv = (1e4 ** (-torch.arange(rot // 2) / max(1, rot // 2))).float()
+    more = dict(inv_freq=inv.cuda() if rot else None, wq=w.cuda(), norm="none", interleaved=interleaved)
+    theta = plain64.rotation_angles(torch.arange(T).expand(1, B, T), inv, None)
+    o = kdn.qk_norm_rope_fwd(x.cuda(), None, **more)[0].cpu()
+    want = (x * w).transpose(1, 2)                           # one fp32 product: exact
+    assert torch.equal(o[..., rot:].isnan(), want[..., rot:].isnan())
+    assert torch.equal(o[..., rot:].nan_to_num(0.25, 1e38, -1e38), want[..., rot:].nan_to_num(0.25, 1e38, -1e38))
+    ref, err = plain64.qk_fwd(x[..., :rot], w[:rot], theta, rot, interleaved, "none", 0.0)
+    plain64.assert_within(o[..., :rot], ref, err)
+    got = kdn.qk_norm_rope_bwd(x.cuda(), None, go.cuda(), None, grad_w=True, **more)
+    gx, want = got["q"].cpu(), go.transpose(1, 2) * w
+    assert torch.equal(gx[..., rot:].isnan(), want[..., rot:].isnan())
+    assert torch.equal(gx[..., rot:].nan_to_num(0.25, 1e38, -1e38), want[..., rot:].nan_to_num(0.25, 1e38, -1e38))
+    if rot:
+        gx64, ex, gw, ew = plain64.qk_bwd(x[..., :rot], w[:rot], go[..., :rot], theta, rot, interleaved, "none", 0.0)
+        plain64.assert_within(gx[..., :rot], gx64, ex)
+        plain64.assert_within(got["wq"][:rot], gw, ew)
