@@ -6,7 +6,8 @@
 //     y = r x w;   (o1, o2) = (y1 cos - y2 sin, y1 sin + y2 cos)
 // with theta = pos inv_freq of the pair's axis.  Backward, g the transposed
 // rotation of the incoming gradient and t = g w:
-//     grad x = r t - r^3 x (sum t x) / n,   grad w = sum over rows of r x g.
+//     grad x = r (t - r x (r sum t x) / n),   grad w = sum over rows of r x g
+// (r x is of order one; an r^3 would leave fp32 where rows are of 1e13 or 1e-13).
 //
 // HBM bounds both (4 bytes per element forward, 8 backward, bf16 in and
 // fp32 gradients).  A lane holds 4 pairs of a head, whichever elements those
@@ -668,14 +669,15 @@ qk_bwd_kernel(const __grid_constant__ QkArgs p, const Deal deal, float* part) {
                     t = times(g, w);
                     dot = row_dot<LPR>(t, v);
                 }
-                const float back = p.norm == KDN_NORM_NONE ? 0.f : -(r * r * r) * (dot * inv_n);
+                const float along = p.norm == KDN_NORM_NONE ? 0.f : -(r * dot) * inv_n;
                 Row8 o;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    o.a[k] = fma2(both(r), t.a[k], mul2(both(back), v.a[k]));
-                    o.b[k] = fma2(both(r), t.b[k], mul2(both(back), v.b[k]));
-                    dw[which].a[k] = fma2(mul2(both(r), v.a[k]), g.a[k], dw[which].a[k]);
-                    dw[which].b[k] = fma2(mul2(both(r), v.b[k]), g.b[k], dw[which].b[k]);
+                    const F2 na = mul2(both(r), v.a[k]), nb = mul2(both(r), v.b[k]);
+                    o.a[k] = mul2(both(r), fma2(na, both(along), t.a[k]));
+                    o.b[k] = mul2(both(r), fma2(nb, both(along), t.b[k]));
+                    dw[which].a[k] = fma2(na, g.a[k], dw[which].a[k]);
+                    dw[which].b[k] = fma2(nb, g.b[k], dw[which].b[k]);
                 }
                 if (odd && p.norm == KDN_NORM_NONE) o = t;
                 if (on) put_row<INTER>(gx + h * DK, q, o);

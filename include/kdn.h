@@ -489,8 +489,9 @@ typedef enum {
  *   Tensors 16-byte aligned, lds multiples of 16 bytes.  Outputs overlap no
  *   input.
  *
- * The sum of squares is fp32 (|x| < 1e18).  Angles are taken in 64-bit
- * fixed-point turns, so cos and sin have fp32's accuracy at every position.
+ * The sum of squares is fp32 (|x| < 1e18; without eps, rows of 1e-18 and less
+ * are lost in it).  Angles are taken in 64-bit fixed-point turns, so cos and
+ * sin have fp32's accuracy at every position.
  */
 KDN_API kdn_status kdn_qk_norm_rope_fwd(const void* q, long long q_ld, const void* k, long long k_ld,
                                         const float* wq, const float* wk, kdn_norm norm, float eps,
