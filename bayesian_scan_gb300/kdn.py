@@ -879,7 +879,10 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
                 raise ValueError(f"grad_{name} must have {H} heads, got {n}")
         if (w is not None) if grad_w is None else grad_w:
             with _alloc(stream):
-                g["w" + name] = torch.empty(dk, device=t.device, dtype=_F32) if w is None else torch.empty_like(w)
+                if H == 0:                                     # (nothing writes it)
+                    g["w" + name] = torch.zeros(dk, device=t.device, dtype=_F32)
+                else:
+                    g["w" + name] = torch.empty(dk, device=t.device, dtype=_F32) if w is None else torch.empty_like(w)
     if len(set(gts)) > 1:
         raise ValueError("grad_q_out and grad_k_out must have one type")
     ot = _DTYPES.get(gts[0])

@@ -81,3 +81,26 @@ def test_the_diagonal_backward_s_workspace_too():
     ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 24)
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         kdn.diag_scan_bwd(q, q, v, v, d, torch.zeros(2), v, workspace=ws)
+
+
+@pytest.mark.parametrize("Hq,Hk", [(0, 2), (2, 0)])
+@pytest.mark.parametrize("weight", [False, True])
+def test_no_heads_have_zero_weight_gradients(Hq, Hk, weight, monkeypatch):
+    # a tensor of no heads adds nothing to its weight's gradient, which no kernel writes
+    empty = torch.empty
+
+    def poisoned(*args, **kw):
+        t = empty(*args, **kw)
+        return t.fill_(float("nan")) if t.is_floating_point() else t
+
+    monkeypatch.setattr(torch, "empty", poisoned)
+    monkeypatch.setattr(torch, "empty_like", lambda t, **kw: poisoned(t.shape, dtype=t.dtype))
+    monkeypatch.setattr(kdn.lib, "kdn_qk_norm_rope_bwd", lambda *args: 0)
+    monkeypatch.setattr(kdn, "_on_one_device", lambda *args, **kw: None)
+    monkeypatch.setattr(kdn, "_stream", lambda s: 0)
+    q, k = torch.zeros(2, 5, Hq, 32), torch.zeros(2, 5, Hk, 32)
+    w = torch.ones(32) if weight else None
+    got = kdn.qk_norm_rope_bwd(q, k, torch.zeros(2, Hq, 5, 32), torch.zeros(2, Hk, 5, 32), wq=w, wk=w, grad_w=True)
+    none, some = ("wq", "wk") if Hq == 0 else ("wk", "wq")
+    assert got[none].shape == (32,) and (got[none] == 0).all()
+    assert got[some].isnan().all()                           # (the library's to write)
