@@ -47,14 +47,15 @@ __device__ __forceinline__ unsigned long long turns_per_position(float f) {
     return static_cast<unsigned long long>(t * 18446744073709551616.0);
 }
 
-// Reduced to an eighth of a turn either side of the nearest quarter, x in
-// [-1, 1] eighths: sin(x pi/4) = x S(x^2), cos(x pi/4) = C(x^2), S and C the
-// Chebyshev interpolants of degree 3 and 4 on [0, 1] (both within 2^-23.5).
+// Reduced to an eighth of a turn either side of the nearest quarter, all 64
+// bits of it (a slow frequency's sine is its angle), x in [-1, 1] eighths:
+// sin(x pi/4) = x S(x^2), cos(x pi/4) = C(x^2), S and C the Chebyshev
+// interpolants of degree 3 and 4 on [0, 1] (both within 2^-23.5).  Both are
+// within 6 half steps of themselves for the angle that they are given.
 __device__ __forceinline__ float2 cos_sin(int pos, unsigned long long per) {
     const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos)) * per;
-    const unsigned int turn = static_cast<unsigned int>(ph >> 32);             // 2^-32 turns
-    const unsigned int quarter = (turn + 0x20000000u) >> 30;
-    const float x = static_cast<float>(static_cast<int>(turn - (quarter << 30))) * 1.862645149230957e-09f;   // 2^-29
+    const unsigned int quarter = (static_cast<unsigned int>(ph >> 32) + 0x20000000u) >> 30;
+    const float x = static_cast<float>(static_cast<long long>(ph - (static_cast<unsigned long long>(quarter) << 62))) * 0x1p-61f;
     const float u = x * x;
     float s = -3.595429006963968e-05f;
     s = fmaf(s, u, 0.0024900068528950214f);

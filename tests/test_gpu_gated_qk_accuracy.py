@@ -1,6 +1,9 @@
 """Accuracy where the other tests' bounds are wide: angles near zero and far
 away, rows of extreme size, convex weights, and sums over many rows.  Units
 are half steps of fp32, 2^-24."""
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -10,6 +13,47 @@ pytestmark = pytest.mark.gpu
 
 F32 = torch.float32
 UNIT = plain64.UNIT
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534")
+
+
+def turned(pos, inv):
+    """cos and sin of pos x inv as the kernels have them: pairs (1, 0) turned."""
+    from bayesian_scan_gb300 import kdn
+    T, dk = len(pos), 128
+    x = torch.zeros(1, T, 1, dk, device="cuda")
+    x[..., :dk // 2] = 1
+    o = kdn.qk_norm_rope_fwd(x, None, torch.tensor(pos, dtype=torch.int32, device="cuda")[None], inv.cuda(),
+                             norm="none")[0][0, 0].cpu().double()
+    return o[:, :dk // 2], o[:, dk // 2:]
+
+
+def exact(pos, inv):
+    """(cos, sin) from the angle modulo a turn in rational arithmetic."""
+    c, s = (torch.zeros(len(pos), len(inv), dtype=torch.float64) for _ in range(2))
+    for j, f in enumerate(inv.tolist()):
+        for i, p in enumerate(pos):
+            a = Fraction(f) * p
+            a = float(a - round(a / TWO_PI) * TWO_PI)
+            c[i, j], s[i, j] = math.cos(a), math.sin(a)
+    return c, s
+
+
+# An angle in turns is a 64-bit fraction: a frequency's is within 2^-63 turns, so that of position pos
+# within |pos| 2^-63 turns, |pos| 2^-60 radians.  Beyond that cos and sin are within 6 units of
+# themselves: the conversion and the product by x one each, its square's effect less than one, the
+# polynomials 1.5 and their roundings 1.5.
+VALUE = 6 * UNIT
+
+
+def test_small_angles_keep_their_sine():
+    # frequencies down to those of long-context bases
+    inv = torch.logspace(-9, 0, 64, base=10.0)
+    pos = [0, 1, 2, 3, 7, 100, 1001, 65535, -1, -2, -5, -333, 1 << 20]
+    c, s = turned(pos, inv)
+    rc, rs = exact(pos, inv)
+    for got, ref in ((c, rc), (s, rs)):
+        lim = VALUE * ref.abs() + torch.tensor(pos).abs().double()[:, None] * 2.0 ** -60
+        assert ((got - ref).abs() <= lim).all(), float(((got - ref).abs() / lim).nan_to_num(0).max())
 
 
 @pytest.mark.parametrize("size", [1e14, 1e-14, 1e17, 1e-17])
