@@ -37,14 +37,16 @@ constexpr int SEG = 4096, SEG_DEPTH = 2;   // bytes of a bulk copy, copies in fl
 __device__ int g_qk_error = 0;
 constexpr int FWD_BLOCKS_PER_SM = 3, BWD_BLOCKS_PER_SM = 2, BWD_DEPTH = 4;
 
-// The turns per position of a frequency, f / (2 pi) modulo 1, in 2^-64: the
-// double's 53 bits in a 64-bit fraction, whose product with an integer
-// position is exact modulo a turn.  The angle is right to 2^-24 turns at the
-// farthest position.
+// The turns per position of a frequency, f / (2 pi) modulo 1, in 2^-64, and
+// within two of them up to |f| = 2^40: f times 1 / (2 pi) as a double and what
+// that leaves out, the first product's whole turns dropped before its rounding
+// error is added.  The product with an integer position is exact modulo a
+// turn, so the angle of the farthest position is within 2^-32 turns.
 __device__ __forceinline__ unsigned long long turns_per_position(float f) {
-    double t = static_cast<double>(f) * 0.15915494309189533577;
-    t -= floor(t);
-    return static_cast<unsigned long long>(t * 18446744073709551616.0);
+    constexpr double HI = 0.15915494309189535, LO = -9.839338337591243e-18;
+    const double t = __dmul_rn(f, HI), rest = __fma_rn(f, LO, __fma_rn(f, HI, -t));
+    return static_cast<unsigned long long>((t - floor(t)) * 0x1p64) +
+           static_cast<unsigned long long>(__double2ll_rn(rest * 0x1p64));
 }
 
 // Reduced to an eighth of a turn either side of the nearest quarter, all 64

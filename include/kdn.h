@@ -490,8 +490,10 @@ typedef enum {
  *   input.
  *
  * The sum of squares is fp32 (|x| < 1e18; without eps, rows of 1e-18 and less
- * are lost in it).  Angles are taken in 64-bit fixed-point turns, so cos and
- * sin have fp32's accuracy at every position.
+ * are lost in it).  Angles are taken in 64-bit fixed-point turns: for
+ * |inv_freq| <= 2^40 an angle is within |pos| 2^-60 (2^-29 at the farthest
+ * position), and cos and sin within 6 half steps of their values there, also
+ * where they are small.
  */
 KDN_API kdn_status kdn_qk_norm_rope_fwd(const void* q, long long q_ld, const void* k, long long k_ld,
                                         const float* wq, const float* wk, kdn_norm norm, float eps,

@@ -56,6 +56,18 @@ def test_small_angles_keep_their_sine():
         assert ((got - ref).abs() <= lim).all(), float(((got - ref).abs() / lim).nan_to_num(0).max())
 
 
+def test_fast_frequencies_at_far_positions():
+    # frequencies above one: a turn or many per token
+    g = torch.Generator().manual_seed(1)
+    inv = torch.cat([torch.logspace(0, 6, 60, base=10.0), torch.tensor([1.0, 402.12387, 2.0 ** 20, 2.0 ** 40])])
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 30 + 1, 12345, 1] + torch.randint(-2 ** 31, 2 ** 31, (20,), generator=g).tolist()
+    c, s = turned(pos, inv)
+    rc, rs = exact(pos, inv)
+    for got, ref in ((c, rc), (s, rs)):
+        lim = VALUE * ref.abs() + torch.tensor(pos).abs().double()[:, None] * 2.0 ** -60
+        assert ((got - ref).abs() <= lim).all(), float(((got - ref).abs() / lim).max())
+
+
 @pytest.mark.parametrize("size", [1e14, 1e-14, 1e17, 1e-17])
 @pytest.mark.parametrize("norm", ["rms", "l2"])
 @pytest.mark.parametrize("dk,Hq", [(128, 3), (16, 5)])
