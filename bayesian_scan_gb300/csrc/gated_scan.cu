@@ -461,7 +461,7 @@ gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
                     x1 = peek<TI, V>(xs + k1 * Sh::ROW + lane * V * sizeof(TI));
                 }
                 const F2 zz = mul2(F2{rate[v0], rate[v1]}, F2{d0.get(v0), d1.get(v1)});
-                const Gate2 gg = gate2<LEAK>(zz);
+                const Gate2 gg = gate2<LEAK, sizeof(TO) == 4>(zz);
                 F2 x{x0.get(v0), x1.get(v1)};
                 if (LEAK) x = mul2(x, gg.w);
                 a[k0][v0] = gg.a.x;
@@ -613,7 +613,7 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
                     g1 = peek<TO, V>(st.g + j1 * Sh::OROW + lane * V * sizeof(TO));
                 }
                 const F2 zz = mul2(F2{rate[v0], rate[v1]}, F2{d0.get(v0), d1.get(v1)});
-                const Gate2 gg = gate2<LEAK>(zz);
+                const Gate2 gg = gate2<LEAK, sizeof(TI) == 4>(zz);
                 a[k0][v0] = gg.a.x;
                 a[k1][v1] = gg.a.y;
                 if (LEAK) {
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(MAP_WARPS * 32) gated_maps_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < UN; i += 2) {
             const F2 e = mul2(both(rate), F2{dv[i], dv[i + 1]});
-            const Gate2 q = gate2<LEAK && !BWD>(e);
+            const Gate2 q = gate2<LEAK && !BWD, sizeof(TO) == 4>(e);
             zz += e.x + e.y;
             if (BWD) ss = q.a.y * (q.a.x * (ss + xv[i]) + xv[i + 1]);
             else if (LEAK) ss = fmaf(q.a.y, fmaf(q.a.x, ss, q.w.x * xv[i]), q.w.y * xv[i + 1]);

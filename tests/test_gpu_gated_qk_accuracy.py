@@ -85,3 +85,22 @@ def test_rows_of_any_size_have_their_gradient(dk, Hq, norm, size):
     assert scaled.isfinite().all()
     assert ((scaled - gx * size).abs() <= (ex + UNIT * (gx.abs() + ex)) * size).all()
     plain64.assert_within(got["wq"], gw, ew)
+
+
+def test_convex_weights():
+    # w = 1 - exp(-d) alone (A = 1, x = 1, no state), fp32 in and out.  The exponent is within 1.5 units
+    # of itself, which moves w by at most as much of itself; the polynomial branch adds 2, the hardware's
+    # 2^x (2^-22, below a half) 4, a product one: 4.5 units, and 6.5 beyond a half
+    from bayesian_scan_gb300 import kdn
+    d = torch.cat([torch.logspace(-30, 0, 2000, base=2.0), torch.linspace(0.2, 1.2, 6000), torch.linspace(1.2, 20, 192)])
+    ref = -torch.expm1(-d.double())
+    C = len(d)
+    ones, A = torch.ones(1, C, device="cuda"), torch.ones(C, device="cuda")
+    got = {"step": kdn.gated_step(ones, d.cuda()[None], A, torch.zeros_like(ones), leak=True)[0]}
+    o, f = kdn.gated_scan_fwd(ones[:, None], d.cuda()[None, None], A, leak=True)
+    got["out"], got["final"] = o[0, 0], f[0]
+    b = kdn.gated_scan_bwd(ones[:, None], d.cuda()[None, None], A, o, ones[:, None], leak=True)
+    got["grad_x"] = b["x"][0, 0]
+    for n, v in got.items():
+        off = (v.cpu().double() - ref).abs() / (UNIT * ref)
+        assert off[ref < 0.5].max() <= 4.5 and off.max() <= 6.5, (n, float(off[ref < 0.5].max()), float(off.max()))
