@@ -637,64 +637,70 @@ gated_bwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cu
         if (any) {
             TI* gx_out = static_cast<TI*>(p.grad_x) + (row + t) * p.C + at.c0;
             TI* gd_out = static_cast<TI*>(p.grad_d) + (row + t) * p.C + at.c0;
+            // (a tile with tokens before the part: d = 0 there, but their m may be NaN.  Code of its own:
+            // a predicate in every tile costs the convex layer 153 -> 156 us)
+            auto walk = [&](auto edge) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int j = K - 1 - k;
-                const Vec<TI, V> dv = peek<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI));
-                const Vec<TO, V> gv = peek<TO, V>(st.g + j * Sh::OROW + lane * V * sizeof(TO));
-                const Vec<TO, V> hv = peek<TO, V>(st.h + j * Sh::OROW + lane * V * sizeof(TO));
-                Vec<TI, V> xv = dv;
-                if (LEAK) xv = peek<TI, V>(st.x + j * Sh::ROW + lane * V * sizeof(TI));
-                float gx[V], gd[V], prev[V];
+                for (int k = 0; k < K; ++k) {
+                    const int j = K - 1 - k;
+                    const Vec<TI, V> dv = peek<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI));
+                    const Vec<TO, V> gv = peek<TO, V>(st.g + j * Sh::OROW + lane * V * sizeof(TO));
+                    const Vec<TO, V> hv = peek<TO, V>(st.h + j * Sh::OROW + lane * V * sizeof(TO));
+                    Vec<TI, V> xv = dv;
+                    if (LEAK) xv = peek<TI, V>(st.x + j * Sh::ROW + lane * V * sizeof(TI));
+                    float gx[V], gd[V], prev[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) prev[v] = t + j == at.begin ? first[v] : hv.get(v);
-                if constexpr (V == 1) {
-                    const float dh = u[0] + gv.get(0);
-                    u[0] = a[k][0] * dh;
-                    gx[0] = dh;
-                    if (LEAK) {
-                        prev[0] -= xv.get(0);
-                        gx[0] = w[LEAK ? k : 0][0] * dh;
-                    }
-                    const float m = u[0] * prev[0];
-                    gd[0] = nA[0] * m;
-                    if (t + j >= at.lo) dA[0] = fmaf(dv.get(0), m, dA[0]);   // (before it d = 0, but m may be NaN)
-                } else {
-                    const F2 dh = add2(F2{u[0], u[1]}, F2{gv.get(0), gv.get(1)});
-                    const F2 n = mul2(F2{a[k][0], a[k][1]}, dh);
-                    F2 x = dh, before{prev[0], prev[1]};
-                    if (LEAK) {
-                        before = add2(before, F2{-xv.get(0), -xv.get(1)});
-                        x = mul2(F2{w[LEAK ? k : 0][0], w[LEAK ? k : 0][1]}, dh);
-                    }
-                    const F2 m = mul2(n, before), d = mul2(F2{nA[0], nA[1]}, m);
-                    const F2 sum = fma2(F2{dv.get(0), dv.get(1)}, m, F2{dA[0], dA[1]});
-                    u[0] = n.x;
-                    u[1] = n.y;
-                    gx[0] = x.x;
-                    gx[1] = x.y;
-                    gd[0] = d.x;
-                    gd[1] = d.y;
-                    if (t + j >= at.lo) {
-                        dA[0] = sum.x;
-                        dA[1] = sum.y;
-                    }
-                }
-                if (SIZE == 16) {
-                    Vec<TI, V> q;
-                    q.set(gx);
-                    poke<TI, V>(st.grad_x() + j * Sh::ROW + lane * V * sizeof(TI), q);
-                    q.set(gd);
-                    poke<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI), q);
-                } else if (t + j >= at.lo) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (c + v < p.C) {
-                            __stcs(gx_out + static_cast<long long>(j) * p.C + lane * V + v, from_f32<TI>(gx[v]));
-                            __stcs(gd_out + static_cast<long long>(j) * p.C + lane * V + v, from_f32<TI>(gd[v]));
+                    for (int v = 0; v < V; ++v) prev[v] = t + j == at.begin ? first[v] : hv.get(v);
+                    if constexpr (V == 1) {
+                        const float dh = u[0] + gv.get(0);
+                        u[0] = a[k][0] * dh;
+                        gx[0] = dh;
+                        if (LEAK) {
+                            prev[0] -= xv.get(0);
+                            gx[0] = w[LEAK ? k : 0][0] * dh;
                         }
+                        const float m = u[0] * prev[0];
+                        gd[0] = nA[0] * m;
+                        if (!decltype(edge)::value || t + j >= at.lo) dA[0] = fmaf(dv.get(0), m, dA[0]);
+                    } else {
+                        const F2 dh = add2(F2{u[0], u[1]}, F2{gv.get(0), gv.get(1)});
+                        const F2 n = mul2(F2{a[k][0], a[k][1]}, dh);
+                        F2 x = dh, before{prev[0], prev[1]};
+                        if (LEAK) {
+                            before = add2(before, F2{-xv.get(0), -xv.get(1)});
+                            x = mul2(F2{w[LEAK ? k : 0][0], w[LEAK ? k : 0][1]}, dh);
+                        }
+                        const F2 m = mul2(n, before), d = mul2(F2{nA[0], nA[1]}, m);
+                        const F2 sum = fma2(F2{dv.get(0), dv.get(1)}, m, F2{dA[0], dA[1]});
+                        u[0] = n.x;
+                        u[1] = n.y;
+                        gx[0] = x.x;
+                        gx[1] = x.y;
+                        gd[0] = d.x;
+                        gd[1] = d.y;
+                        if (!decltype(edge)::value || t + j >= at.lo) {
+                            dA[0] = sum.x;
+                            dA[1] = sum.y;
+                        }
+                    }
+                    if (SIZE == 16) {
+                        Vec<TI, V> q;
+                        q.set(gx);
+                        poke<TI, V>(st.grad_x() + j * Sh::ROW + lane * V * sizeof(TI), q);
+                        q.set(gd);
+                        poke<TI, V>(st.d + j * Sh::ROW + lane * V * sizeof(TI), q);
+                    } else if (t + j >= at.lo) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            if (c + v < p.C) {
+                                __stcs(gx_out + static_cast<long long>(j) * p.C + lane * V + v, from_f32<TI>(gx[v]));
+                                __stcs(gd_out + static_cast<long long>(j) * p.C + lane * V + v, from_f32<TI>(gd[v]));
+                            }
+                    }
                 }
-            }
+            };
+            if (t >= at.lo) walk(std::false_type());
+            else walk(std::true_type());
             __syncwarp();
             if (SIZE == 16) {
                 const int f = max(at.lo - t, 0);
