@@ -104,3 +104,39 @@ def test_convex_weights():
     for n, v in got.items():
         off = (v.cpu().double() - ref).abs() / (UNIT * ref)
         assert off[ref < 0.5].max() <= 4.5 and off.max() <= 6.5, (n, float(off[ref < 0.5].max()), float(off.max()))
+
+
+@pytest.mark.parametrize("B,C", [(70000, 3), (4096 + 1, 33), (129, 70), (128, 5), (97, 64), (33, 1), (2, 130)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_sums_over_rows_are_complete(B, C, packed):
+    # alpha = 1 and small whole numbers: every product and sum is exact in fp32, so that a row left out
+    # or taken twice shows; every row has a share of its own
+    from bayesian_scan_gb300 import kdn
+    g = torch.Generator().manual_seed(B)
+    draw = lambda lo, hi, *shape: torch.randint(lo, hi + 1, shape, generator=g).float()
+    T = 2
+    d, go, out, h0 = draw(1, 2, B, T, C), draw(1, 2, B, T, C), draw(1, 3, B, T, C), draw(1, 3, B, C)
+    A = torch.zeros(C)
+    u = torch.stack([go[:, 0] + go[:, 1], go[:, 1]], 1)
+    share = d * u * torch.stack([h0, out[:, 0]], 1)
+    assert share.min() >= 1 and share.double().sum((0, 1)).max() < 2 ** 24
+    off = torch.arange(0, B * T + 1, T, dtype=torch.int32)
+    shaped = (lambda t: t.reshape(1, B * T, C).cuda()) if packed else (lambda t: t.cuda())
+    got = kdn.gated_scan_bwd(shaped(d), shaped(d), A.cuda(), shaped(out), shaped(go), h0=h0.cuda(),
+                             offsets=off.cuda() if packed else None)
+    assert torch.equal(got["A"].cpu(), -share.sum((0, 1)))
+    assert torch.equal(got["h0"].cpu(), u[:, 0])
+
+
+@pytest.mark.parametrize("B,T,Hq,Hk", [(1, 1, 1, 1), (3, 7, 3, 1), (2, 997, 5, 2), (8, 700, 16, 16), (1, 5000, 1, 1)])
+def test_sums_of_weights_gradients_are_complete(B, T, Hq, Hk):
+    # no norm and no rotation: grad w = sum of x g, whole numbers again
+    from bayesian_scan_gb300 import kdn
+    g = torch.Generator().manual_seed(T)
+    draw = lambda *shape: torch.randint(1, 4, shape, generator=g).float()
+    q, k, gq, gk = draw(B, T, Hq, 64), draw(B, T, Hk, 64), draw(B, Hq, T, 64), draw(B, Hk, T, 64)
+    got = kdn.qk_norm_rope_bwd(*(t.cuda() for t in (q, k, gq, gk)), norm="none", grad_w=True)
+    for n, x, go in (("wq", q, gq), ("wk", k, gk)):
+        want = (x * go.transpose(1, 2)).sum((0, 1, 2), dtype=torch.float64)
+        assert want.max() < 2 ** 24
+        assert torch.equal(got[n].cpu().double(), want)
