@@ -765,12 +765,6 @@ kdn_status by_dk(int dk, F f) {
     }
 }
 
-}  // namespace
-
-long long qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int dk) {
-    return static_cast<long long>(bwd_blocks(B, T, Hq, Hk, dk)) * 2 * dk * 4;
-}
-
 // Whether a forward call is one for bulk copies: vector places, heads for a
 // whole warp in either tensor, and a token for half of the warps or more (3 x
 // 1271 tokens of 32 + 8 heads 13.9 us, 15.4 by loads; 128 tokens are faster
@@ -781,6 +775,12 @@ bool bulk_ok(const QkArgs& a, int blocks) {
         if (H != 0 && H < rpw) return false;
     return (a.interleaved || a.rot % 8 == 0) &&
            static_cast<long long>(a.B) * a.T >= WARPS * blocks / 2;
+}
+
+}  // namespace
+
+long long qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int dk) {
+    return static_cast<long long>(bwd_blocks(B, T, Hq, Hk, dk)) * 2 * dk * 4;
 }
 
 kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream, long long wait_ns) {
