@@ -510,15 +510,32 @@ def _ws_device(t):
 def _scratch(nbytes, like, stream):
     """A call's own workspace, let go when the call returns: the stream's next
     allocations may have it, in the stream's order."""
-    with _alloc(stream):
-        return torch.empty(nbytes, device=like.device, dtype=torch.uint8)
+    return _empty(nbytes, like, torch.uint8, stream)
+
+
+_MOST = 0x7fffffff
 
 
 def _ints(*sizes):
     """The C calls take sizes of 32 bits, to which ctypes cuts larger ones
     without a word."""
-    if max(sizes) > 0x7fffffff:
+    if max(sizes) > _MOST:
         raise ValueError(f"sizes must be below 2**31, got {sizes}")
+
+
+def _empty(shape, like, dtype, stream):
+    """An uninitialised tensor on like's device, the stream's memory."""
+    if stream is not None:
+        with _alloc(stream):
+            return torch.empty(shape, device=like.device, dtype=dtype)
+    return torch.empty(shape, device=like.device, dtype=dtype)
+
+
+def _dense_like(t, stream):
+    """The same of t's shape and type; ``torch.empty_like`` where there is no
+    stream and t is dense."""
+    with _alloc(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _token_ld(t, name, dt, shape):
@@ -560,7 +577,8 @@ def _gated_sizes(x, A, offsets):
         if offsets.dim() != 1 or offsets.numel() < 2 or B != 1:
             raise ValueError("offsets must be [nseq + 1] with B = 1")
         rows = offsets.numel() - 1
-    _ints(B, H, T, C, rows)
+    if (B | H | T | C | rows) > _MOST:
+        _ints(B, H, T, C, rows)
     return B, H, T, C, 0 if offsets is None else rows, (rows, *heads)
 
 
@@ -589,8 +607,7 @@ def gated_scan_fwd(x, d, A, h0=None, leak=False, offsets=None, out=None, out_dty
         _check(out, "out", out_dtype, x.shape)
     ot = _dtype_of(out, "out")
     if final_state is True:
-        with _alloc(stream):
-            final_state = torch.empty(state, device=x.device, dtype=_F32)
+        final_state = _empty(state, x, _F32, stream)
     elif final_state is False:
         final_state = None
     elif final_state is not None:
@@ -649,8 +666,8 @@ def gated_scan_bwd(x, d, A, out, grad_out, h0=None, leak=False, offsets=None, gr
     for name, t, shape in (("A", grad_A, tuple(A.shape)), ("h0", grad_h0, state)):
         if t is True:
             like = A if name == "A" else h0
-            with _alloc(stream):
-                t = torch.empty(shape, device=x.device, dtype=_F32) if like is None else torch.empty_like(like)
+            t = (_empty(shape, x, _F32, stream) if like is None else
+                 torch.empty_like(like) if stream is None else _dense_like(like, stream))
         elif t is False:
             t = None
         elif t is not None:
@@ -685,7 +702,8 @@ def gated_step(x, d, A, state, leak=False, new_state=None, out=None, out_dtype=N
     shape, dt = x.shape, x.dtype
     if len(shape) not in (2, 3):
         raise ValueError(f"x must be [B,C] or [B,H,C], got {tuple(shape)}")
-    _ints(*shape)
+    if not 0 < x.numel() <= _MOST:                             # (else every size is below)
+        _ints(*shape)
     it = _dtype_of(x, "x")
     if new_state is None:
         new_state = state
@@ -731,8 +749,9 @@ def _head_rows(t, name, dt, B, T, dk):
         raise ValueError(f"{name} must be [{B},{T},heads,{dk}], got {tuple(shape)}")
     if t.dtype != dt:
         raise ValueError(f"{name} must be {dt}, got {t.dtype}")
-    _ints(*shape)
     H = shape[2]
+    if (B | T | H) > _MOST:
+        _ints(B, T, H)
     if t.is_contiguous():
         return H, H * dk
     st = t.stride()
@@ -808,15 +827,13 @@ def qk_norm_rope_fwd(q, k, pos=None, inv_freq=None, wq=None, wk=None, norm="rms"
     if q is None:
         q_out = None
     elif q_out is None:
-        with _alloc(stream):
-            q_out = torch.empty((B, Hq, T, dk), device=first.device, dtype=od)
+        q_out = _empty((B, Hq, T, dk), first, od, stream)
     else:
         _check(q_out, "q_out", od, (B, Hq, T, dk))
     if k is None:
         k_out = None
     elif k_out is None:
-        with _alloc(stream):
-            k_out = torch.empty((B, Hk, T, dk), device=first.device, dtype=od)
+        k_out = _empty((B, Hk, T, dk), first, od, stream)
     else:
         _check(k_out, "k_out", od, (B, Hk, T, dk))
     if not _here(stream, q, k, pos, inv_freq, wq, wk, axis, q_out, k_out):
@@ -870,19 +887,21 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
         gts.append(go.dtype)
         if gx is None:
             # (dense: t's heads lie side by side, so what empty_like makes of its order is the plain one)
-            with _alloc(stream):
-                g[name], lds[name] = torch.empty_like(t, memory_format=torch.contiguous_format), H * dk
+            g[name] = (torch.empty_like(t, memory_format=torch.contiguous_format) if stream is None
+                       else _dense_like(t, stream))
+            lds[name] = H * dk
         else:
             g[name] = gx
             n, lds[name] = _head_rows(gx, "grad_" + name, t.dtype, B, T, dk)
             if n != H:
                 raise ValueError(f"grad_{name} must have {H} heads, got {n}")
         if (w is not None) if grad_w is None else grad_w:
-            with _alloc(stream):
-                if H == 0:                                     # (nothing writes it)
+            if H == 0:                                         # (nothing writes it)
+                with _alloc(stream):
                     g["w" + name] = torch.zeros(dk, device=t.device, dtype=_F32)
-                else:
-                    g["w" + name] = torch.empty(dk, device=t.device, dtype=_F32) if w is None else torch.empty_like(w)
+            else:
+                g["w" + name] = (_empty(dk, t, _F32, stream) if w is None else
+                                 torch.empty_like(w) if stream is None else _dense_like(w, stream))
     if len(set(gts)) > 1:
         raise ValueError("grad_q_out and grad_k_out must have one type")
     ot = _DTYPES.get(gts[0])
