@@ -394,8 +394,10 @@ KDN_API kdn_status kdn_mobius_scan_noalloc(const float* a, const float* b, const
  *   out and final_state overlap no input.
  *
  * The state and every sum are fp32 whatever the types; out is rounded once.
- * A d >= 0 is expected (alpha <= 1).  Results are deterministic.  Long
- * sequences of few channels take stream-ordered scratch (KDN_ERR_ALLOC).
+ * A d >= 0 is expected (alpha <= 1).  An infinite state stays infinite; a
+ * token whose own decay underflows fp32 (A d > 87) may make NaN of it.
+ * Results are deterministic.  Long sequences of few channels take
+ * stream-ordered scratch (KDN_ERR_ALLOC).
  */
 KDN_API kdn_status kdn_gated_scan_fwd(const void* x, long long x_ld, const void* d, long long d_ld,
                                       const float* A, const float* h0, const int* offsets, int nseq,
@@ -419,7 +421,8 @@ KDN_API kdn_status kdn_gated_scan_fwd(const void* x, long long x_ld, const void*
  *   workspace as for kdn_diag_scan_bwd: at least kdn_gated_scan_bwd_workspace
  *             bytes, 256-byte aligned, or NULL (stream-ordered scratch).
  *
- * The states enter dL/dd as given: with a bf16 out they carry its rounding.
+ * The outputs overlap no input.  The states enter dL/dd as given: with a bf16
+ * out they carry its rounding, |A u_t| times up to 2^-8 |h_{t-1}| of dL/dd.
  * Sums in fp32, in a fixed order (deterministic).  T = 0 writes grad_h0 (=
  * grad_final_state) and grad_A (= 0).
  */
@@ -517,7 +520,8 @@ KDN_API kdn_status kdn_qk_norm_rope_fwd(const void* q, long long q_ld, const voi
  *             kdn_qk_norm_rope_bwd_workspace bytes (needed only when grad_wq
  *             or grad_wk is written)
  *
- * Deterministic.  T = 0 writes only grad_wq, grad_wk (= 0).
+ * The outputs overlap no input.  Deterministic.  T = 0 writes only grad_wq,
+ * grad_wk (= 0).
  */
 KDN_API kdn_status kdn_qk_norm_rope_bwd(const void* q, long long q_ld, const void* k, long long k_ld,
                                         const float* wq, const float* wk, kdn_norm norm, float eps,

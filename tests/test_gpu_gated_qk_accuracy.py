@@ -140,3 +140,32 @@ def test_sums_of_weights_gradients_are_complete(B, T, Hq, Hk):
         want = (x * go.transpose(1, 2)).sum((0, 1, 2), dtype=torch.float64)
         assert want.max() < 2 ** 24
         assert torch.equal(got[n].cpu().double(), want)
+
+
+@pytest.mark.parametrize("leak", [False, True])
+@pytest.mark.parametrize("in_dtype", [F32, torch.bfloat16])
+def test_what_bf16_states_cost(in_dtype, leak):
+    # the gradients from a bf16 forward's own output against those of the states before their rounding:
+    # grad d = -A u (h - leak x) moves by A u times the rounding of h, half a step of bf16, and by that of
+    # the states that the kernel made (GATE's units); the others do not see it, but grad A does through d
+    from bayesian_scan_gb300 import kdn
+    g = torch.Generator().manual_seed(9)
+    B, T, C = 2, 300, 64
+    x = torch.randn(B, 1, T, C, generator=g).to(in_dtype)
+    d = torch.nn.functional.softplus(torch.randn(B, 1, T, C, generator=g)).to(in_dtype)
+    A = torch.exp(torch.empty(1, C).uniform_(math.log(1e-3), 0.0, generator=g))
+    go = torch.randn(B, 1, T, C, generator=g).bfloat16()
+    out, _ = kdn.gated_scan_fwd(x.cuda(), d.cuda(), A.cuda(), leak=leak, out_dtype=torch.bfloat16)
+    got = kdn.gated_scan_bwd(x.cuda(), d.cuda(), A.cuda(), out, go.cuda(), leak=leak)
+    states, _, off, _ = plain64.gated_fwd(x, d, A, None, leak)
+    val, err = plain64.gated_bwd(x, d, A, states, go, None, leak)
+    u, rounding = torch.zeros(B, 1, C, dtype=torch.float64), torch.zeros_like(states)
+    for t in range(T - 1, -1, -1):
+        u = torch.exp(-A.double() * d[:, :, t].double()) * (go[:, :, t].double() + u)
+        if t:
+            off_t = off[:, :, t - 1] + plain64.half_step(torch.bfloat16) * (states[:, :, t - 1].abs() + off[:, :, t - 1])
+            rounding[:, :, t] = A.double() * u.abs() * off_t
+    plain64.assert_within(got["x"], val["x"], err["x"], "grad_x")
+    plain64.assert_within(got["d"], val["d"], err["d"] + rounding, "grad_d")
+    plain64.assert_within(got["A"], val["A"], err["A"] + (rounding * d.double() / A.double().unsqueeze(1)).sum((0, 2)),
+                          "grad_A")
