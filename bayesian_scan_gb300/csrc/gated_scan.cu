@@ -396,10 +396,10 @@ struct FwdShared {
 };
 
 // Measured (GB300; 16-bit in and out, 134 M elements, 805 MB, where 118 us is
-// the copy's rate): as 16 x 4096 x 2048 151 us, 4 x 16384 x 2048 (clusters of
-// 2) 164 us, 1 x 65536 x 2048 (clusters of 8) 189 us, 210 us of the convex
-// form; 2 CTAs per SM (128 registers), 18 instructions per element, 24 with
-// clusters of 8.
+// the copy's rate): as 16 x 4096 x 2048 142 us, 4 x 16384 x 2048 (clusters of
+// 2) 167 us, 1 x 65536 x 2048 (clusters of 8) 190 us, 213 us of the convex
+// form; 2 CTAs per SM (128 registers), 18.7 instructions per element, 24.5
+// with clusters of 8.
 template <typename TI, typename TO, int V, int K, bool LEAK, int SIZE>
 __global__ void __launch_bounds__(NW * 32, 2)
 gated_fwd_kernel(const __grid_constant__ GatedArgs p, const __grid_constant__ Cut cut) {

@@ -469,7 +469,7 @@ qk_fwd_kernel(const __grid_constant__ QkArgs p, const Deal deal) {
 // the warp's ring, SEG_DEPTH of them ahead, without a load instruction or a
 // register.  The kernel above waits for its loads (half of all stalls), and
 // rows ahead in registers cost more than they hide: 8 x 4096 tokens, 16 + 16
-// heads of 128, bf16: 102 us there, 90 us here (88 % of the copy's rate;
+// heads of 128, bf16: 102 us there, 90 us here (87 % of the copy's rate;
 // three copies ahead 92 us, six of half the size 101 us).
 template <int DK>
 struct BulkShared {
