@@ -418,7 +418,8 @@ kdn_status kdn_qk_norm_rope_fwd(const void* q, long long q_ld, const void* k, lo
                                 void* stream) {
     if (T > 0 && ((Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)))) return KDN_ERR_INVALID_ARG;
     QkArgs a{};
-    a.x[0] = q; a.x[1] = k; a.ld[0] = q_ld; a.ld[1] = k_ld; a.w[0] = wq; a.w[1] = wk;
+    a.x[0] = q; a.x[1] = k; a.ld[0] = q_ld; a.ld[1] = k_ld;
+    a.w[0] = Hq > 0 ? wq : nullptr; a.w[1] = Hk > 0 ? wk : nullptr;
     a.heads[0] = Hq; a.heads[1] = Hk; a.y[0] = q_out; a.y[1] = k_out; a.norm = norm; a.eps = eps;
     a.pos = pos; a.axes = axes; a.inv_freq = inv_freq; a.axis = axis; a.rot = rot;
     a.interleaved = interleaved != 0; a.B = B; a.T = T; a.dk = dk; a.in_dtype = in_dtype;
@@ -440,7 +441,8 @@ kdn_status kdn_qk_norm_rope_bwd(const void* q, long long q_ld, const void* k, lo
     if (T > 0 && ((Hq > 0 && (!q || !grad_q_out || !grad_q)) || (Hk > 0 && (!k || !grad_k_out || !grad_k))))
         return KDN_ERR_INVALID_ARG;
     QkArgs a{};
-    a.x[0] = q; a.x[1] = k; a.ld[0] = q_ld; a.ld[1] = k_ld; a.w[0] = wq; a.w[1] = wk;
+    a.x[0] = q; a.x[1] = k; a.ld[0] = q_ld; a.ld[1] = k_ld;
+    a.w[0] = Hq > 0 ? wq : nullptr; a.w[1] = Hk > 0 ? wk : nullptr;
     a.heads[0] = Hq; a.heads[1] = Hk; a.grad_y[0] = grad_q_out; a.grad_y[1] = grad_k_out;
     a.grad_x[0] = grad_q; a.grad_x[1] = grad_k; a.grad_ld[0] = gq_ld; a.grad_ld[1] = gk_ld;
     a.grad_w[0] = Hq > 0 ? grad_wq : nullptr; a.grad_w[1] = Hk > 0 ? grad_wk : nullptr;
