@@ -750,8 +750,8 @@ def _head_rows(t, name, dt, B, T, dk):
     if t.dtype != dt:
         raise ValueError(f"{name} must be {dt}, got {t.dtype}")
     H = shape[2]
-    if (B | T | H) > _MOST:
-        _ints(B, T, H)
+    if (B | T | H | dk) > _MOST:
+        _ints(B, T, H, dk)
     if t.is_contiguous():
         return H, H * dk
     st = t.stride()

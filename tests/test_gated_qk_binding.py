@@ -104,3 +104,12 @@ def test_no_heads_have_zero_weight_gradients(Hq, Hk, weight, monkeypatch):
     none, some = ("wq", "wk") if Hq == 0 else ("wk", "wq")
     assert got[none].shape == (32,) and (got[none] == 0).all()
     assert got[some].isnan().all()                           # (the library's to write)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: kdn.qk_norm_rope_fwd(meta(1, 1, 1, 2 ** 32 + 16), None),
+    lambda: kdn.qk_norm_rope_bwd(meta(1, 1, 1, 2 ** 32 + 16), None, meta(1, 1, 1, 2 ** 32 + 16), None),
+])
+def test_a_head_that_32_bits_do_not_hold_is_refused(call):
+    with pytest.raises(ValueError, match=r"below 2\*\*31"):
+        call()
