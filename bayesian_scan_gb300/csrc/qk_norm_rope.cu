@@ -44,9 +44,10 @@ constexpr int FWD_BLOCKS_PER_SM = 3, BWD_BLOCKS_PER_SM = 2, BWD_DEPTH = 4;
 // turn, so the angle of the farthest position is within 2^-32 turns.
 __device__ __forceinline__ unsigned long long turns_per_position(float f) {
     constexpr double HI = 0.15915494309189535, LO = -9.839338337591243e-18;
-    const double t = __dmul_rn(f, HI), rest = __fma_rn(f, LO, __fma_rn(f, HI, -t));
-    return static_cast<unsigned long long>((t - floor(t)) * 0x1p64) +
-           static_cast<unsigned long long>(__double2ll_rn(rest * 0x1p64));
+    const double g = fabsf(f), t = __dmul_rn(g, HI), rest = __fma_rn(g, LO, __fma_rn(g, HI, -t));
+    const unsigned long long turns = static_cast<unsigned long long>((t - floor(t)) * 0x1p64) +   // (exact for t >= 0)
+                                     static_cast<unsigned long long>(__double2ll_rn(rest * 0x1p64));
+    return f < 0.f ? 0ull - turns : turns;
 }
 
 // Reduced to an eighth of a turn either side of the nearest quarter, all 64

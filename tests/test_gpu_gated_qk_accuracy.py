@@ -169,3 +169,14 @@ def test_what_bf16_states_cost(in_dtype, leak):
     plain64.assert_within(got["d"], val["d"], err["d"] + rounding, "grad_d")
     plain64.assert_within(got["A"], val["A"], err["A"] + (rounding * d.double() / A.double().unsqueeze(1)).sum((0, 2)),
                           "grad_A")
+
+
+def test_negative_frequencies_turn_the_other_way():
+    # as exact as positive ones: slow and fast, near and far
+    inv = -torch.cat([torch.logspace(-9, 0, 40, base=10.0), torch.logspace(0.1, 6, 24, base=10.0)])
+    pos = [0, 1, 2, 7, 1001, 65535, -1, -333, 2 ** 31 - 1, -2 ** 31]
+    c, s = turned(pos, inv)
+    rc, rs = exact(pos, inv)
+    for got, ref in ((c, rc), (s, rs)):
+        lim = VALUE * ref.abs() + torch.tensor(pos).abs().double()[:, None] * 2.0 ** -60
+        assert ((got - ref).abs() <= lim).all(), float(((got - ref).abs() / lim).nan_to_num(0).max())
