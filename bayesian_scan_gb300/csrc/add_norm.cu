@@ -1,0 +1,448 @@
+// add_norm.cu -- the residual's addition and its root-mean-square norm, what
+// stands before a mixer's projection: per row of C channels
+//     s = x + residual (rounded to the residual's type),
+//     y = w . s / sqrt(mean(s^2) + eps),
+// y in bf16, fp32 or e4m3 with a scale for each group of 128 channels, and the
+// gradients of both.  One pass: a row's elements stay in registers between its
+// sum of squares and its outputs, so x and the residual are read and s and y
+// written once (8 bytes an element in bf16, bound by HBM).
+//
+// Forward: a warp to a row of up to 2048 channels, whole CTAs of G warps to
+// longer rows and to few rows (a decode batch: latency); no exchange between
+// warps in the first form.  A warp's elements are WHOLE groups of 128, so a
+// group's largest value is a matter of shuffles.
+//
+// Backward: n = s rstd, t = w . grad_y;
+//     grad = rstd (t - n mean(t . n)) + grad_sum,   grad_w = sum_rows grad_y . n.
+// A thread keeps its columns for all rows that its CTA takes, and with them
+// their share of grad_w; ROWS rows are in flight at a time, and their 2 ROWS sums
+// are one exchange.  The CTAs' shares are added in a fixed order (sum_rows.cuh).
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "kdn.h"
+#include "kdn_internal.h"
+#include "sum_rows.cuh"
+
+namespace kdn {
+namespace {
+
+constexpr int GROUP = 128;               // channels to a scale
+constexpr float TOP = 448.f;             // the largest e4m3 value
+constexpr int WARPS = 8;                 // of a CTA whose warps have rows of their own
+
+struct E4m3 {
+    unsigned char bits;
+};
+
+// VEC consecutive elements as fp32.
+template <int VEC, typename T>
+__device__ __forceinline__ void load(const T* p, float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        f[0] = static_cast<float>(*p);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void store(T* p, const float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        if constexpr (std::is_same<T, E4m3>::value) p->bits = __nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
+        else if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(f[0]);
+        else *p = f[0];
+    } else if constexpr (std::is_same<T, E4m3>::value) {
+        uint32_t u[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i], f[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2], f[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+            u[i] = lo | hi << 16;
+        }
+        *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+// What fp32 becomes in T and back.
+template <typename T>
+__device__ __forceinline__ float as(float x) {
+    if constexpr (sizeof(T) == 2) return __bfloat162float(__float2bfloat16_rn(x));
+    else return x;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// A warp's NV vectors a lane of the row (from element `first`): rounded sums
+// into s (written to memory too where there is a residual) and their squares.
+template <int VEC, int NV, typename TX, typename TR>
+__device__ __forceinline__ float sum_part(const TX* x, const TR* res, TR* sum, int first, int C, float (&s)[NV][VEC]) {
+    const int lane = threadIdx.x & 31;
+    float r[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = first + (j * 32 + lane) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s[j][e] = r[j][e] = 0.f;
+        if (c < C) {
+            load<VEC>(x + c, s[j]);
+            if (res) load<VEC>(res + c, r[j]);
+        }
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = first + (j * 32 + lane) * VEC;
+        if (res) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[j][e] = as<TR>(s[j][e] + r[j][e]);
+            if (c < C) store<VEC>(sum + c, s[j]);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) q = fmaf(s[j][e], s[j][e], q);
+    }
+    return q;
+}
+
+template <int VEC, int NV, typename TY>
+__device__ __forceinline__ void norm_part(float (&s)[NV][VEC], float rstd, const float* w, TY* y, float* scale, int first,
+                                          int C) {
+    const int lane = threadIdx.x & 31;
+    float top[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = first + (j * 32 + lane) * VEC;
+        float f[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = 1.f;
+        if (w && c < C) load<VEC>(w + c, f);
+        top[j] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            s[j][e] = s[j][e] * rstd * f[e];
+            top[j] = fmaxf(top[j], fabsf(s[j][e]));
+        }
+        if constexpr (!std::is_same<TY, E4m3>::value)
+            if (c < C) store<VEC>(y + c, s[j]);
+    }
+    if constexpr (std::is_same<TY, E4m3>::value) {
+        // a group is 16 lanes of one vector of 8, or the whole warp in 4 strips of single elements
+        if constexpr (VEC == 1) {
+#pragma unroll
+            for (int j = 0; j < NV; j += 4) {
+                const float t = fmaxf(fmaxf(top[j], top[j + 1]), fmaxf(top[j + 2], top[j + 3]));
+                top[j] = top[j + 1] = top[j + 2] = top[j + 3] = t;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = first + (j * 32 + lane) * VEC;
+#pragma unroll
+            for (int o = VEC == 1 ? 16 : 8; o > 0; o >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+            // a group of zeros has scale 1
+            const float sc = top[j] > 0.f ? top[j] / TOP : 1.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[j][e] = s[j][e] / sc;
+            if (c < C) {
+                store<VEC>(y + c, s[j]);
+                if (c % GROUP == 0) scale[c / GROUP] = sc;
+            }
+        }
+    }
+}
+
+// G = 1: a warp to a row, no exchange.  G > 1: a CTA of G warps to a row.
+template <int VEC, int NV, typename TX, typename TR, typename TY, bool ALONE>
+__global__ void __launch_bounds__(ALONE ? WARPS * 32 : 1024) add_norm_kernel(const NormArgs a) {
+    __shared__ float share[32];
+    constexpr int PER = 32 * NV * VEC;       // elements of a warp
+    const int warp = threadIdx.x >> 5, G = ALONE ? 1 : blockDim.x >> 5;
+    const long long row = ALONE ? static_cast<long long>(blockIdx.x) * WARPS + warp : blockIdx.x;
+    if (ALONE && row >= a.rows) return;
+    const int C = a.C, first = ALONE ? 0 : warp * PER;
+    const TX* x = static_cast<const TX*>(a.x) + row * a.x_ld;
+    const TR* res = a.residual ? static_cast<const TR*>(a.residual) + row * C : nullptr;
+    TR* sum = static_cast<TR*>(a.sum) + row * C;
+    TY* y = static_cast<TY*>(a.y) + row * C;
+    float* scale = a.scale + row * ((C + GROUP - 1) / GROUP);
+    float s[NV][VEC];
+    float q = sum_part<VEC, NV>(x, res, sum, first, C, s);
+    for (int c = first + G * PER; c < C; c += G * PER) {     // rows that the registers do not hold
+        float more[NV][VEC];
+        q += sum_part<VEC, NV>(x, res, sum, c, C, more);
+    }
+    q = warp_sum(q);
+    if constexpr (!ALONE) {
+        if ((threadIdx.x & 31) == 0) share[warp] = q;
+        __syncthreads();
+        q = warp_sum((threadIdx.x & 31) < G ? share[threadIdx.x & 31] : 0.f);
+    }
+    const float rstd = rsqrtf(q / static_cast<float>(C) + a.eps);
+    norm_part<VEC, NV, TY>(s, rstd, a.weight, y, scale, first, C);
+    for (int c = first + G * PER; c < C; c += G * PER) {
+        // each thread reads back what it has written itself (or x)
+        float more[NV][VEC];
+        if (res) sum_part<VEC, NV>(sum, static_cast<const TR*>(nullptr), static_cast<TR*>(nullptr), c, C, more);
+        else sum_part<VEC, NV>(x, static_cast<const TR*>(nullptr), static_cast<TR*>(nullptr), c, C, more);
+        norm_part<VEC, NV, TY>(more, rstd, a.weight, y, scale, c, C);
+    }
+}
+
+// ---- backward ----------------------------------------------------------------
+
+constexpr int BACK_ROWS = 4;                 // rows in flight
+constexpr int BACK_CTAS = 8;                 // CTAs to an SM at most (their shares of grad_w are read once more)
+
+// blockDim.x threads have VEC columns each of one slice of blockDim.x * VEC
+// columns at a time; a row of one slice stays in registers, a longer one is
+// read twice.
+template <int VEC, typename TX, typename TR, typename TY>
+__global__ void __launch_bounds__(1024) add_norm_back_kernel(const NormArgs a, float* shares, int slices) {
+    __shared__ float part[32][2 * BACK_ROWS];
+    const int C = a.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int step = blockDim.x * VEC, mine = threadIdx.x * VEC;
+    const TR* sum = static_cast<const TR*>(a.residual);
+    const TY* gy = static_cast<const TY*>(a.grad_y);
+    const TR* gs = static_cast<const TR*>(a.grad_sum);
+    float acc[VEC], w[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        acc[e] = 0.f;
+        w[e] = 1.f;
+    }
+    if (a.weight && mine < C) load<VEC>(a.weight + mine, w);
+    for (long long r0 = static_cast<long long>(blockIdx.x) * BACK_ROWS; r0 < a.rows;
+         r0 += static_cast<long long>(gridDim.x) * BACK_ROWS) {
+        float s[BACK_ROWS][VEC], g[BACK_ROWS][VEC], o[BACK_ROWS][VEC], sums[2 * BACK_ROWS];
+#pragma unroll
+        for (int i = 0; i < BACK_ROWS; ++i) {
+            const bool on = r0 + i < a.rows && mine < C;
+            const long long at = (r0 + i) * C + mine;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[i][e] = g[i][e] = o[i][e] = 0.f;
+            if (on) {
+                load<VEC>(sum + at, s[i]);
+                load<VEC>(gy + at, g[i]);
+                if (gs) load<VEC>(gs + at, o[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BACK_ROWS; ++i) {
+            float q = 0.f, d = 0.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                q = fmaf(s[i][e], s[i][e], q);
+                d = fmaf(g[i][e] * w[e], s[i][e], d);
+            }
+            for (int k = 1; k < slices; ++k) {               // columns that the registers do not hold
+                const int c = k * step + mine;
+                if (r0 + i < a.rows && c < C) {
+                    float sv[VEC], gv[VEC], wv[VEC];
+                    load<VEC>(sum + (r0 + i) * C + c, sv);
+                    load<VEC>(gy + (r0 + i) * C + c, gv);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) wv[e] = 1.f;
+                    if (a.weight) load<VEC>(a.weight + c, wv);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        q = fmaf(sv[e], sv[e], q);
+                        d = fmaf(gv[e] * wv[e], sv[e], d);
+                    }
+                }
+            }
+            sums[2 * i] = warp_sum(q);
+            sums[2 * i + 1] = warp_sum(d);
+        }
+        if (warps > 1) {
+            __syncthreads();   // the last rows' sums are read
+            if (lane == 0)
+#pragma unroll
+                for (int i = 0; i < 2 * BACK_ROWS; ++i) part[warp][i] = sums[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2 * BACK_ROWS; ++i) sums[i] = warp_sum(lane < warps ? part[lane][i] : 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < BACK_ROWS; ++i) {
+            if (r0 + i >= a.rows) break;
+            const float rstd = rsqrtf(sums[2 * i] / static_cast<float>(C) + a.eps);
+            const float mean = sums[2 * i + 1] * rstd / static_cast<float>(C);       // of t . n
+            const long long at = (r0 + i) * C + mine;
+            if (mine < C) {
+                float out[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float n = s[i][e] * rstd;
+                    acc[e] = fmaf(g[i][e], n, acc[e]);
+                    out[e] = fmaf(rstd, g[i][e] * w[e] - n * mean, o[i][e]);
+                }
+                if (a.grad_residual) store<VEC>(static_cast<TR*>(a.grad_residual) + at, out);
+                if (a.grad_x) store<VEC>(static_cast<TX*>(a.grad_x) + at, out);
+            }
+            for (int k = 1; k < slices; ++k) {
+                const int c = k * step + mine;
+                if (c >= C) break;
+                const long long more = (r0 + i) * C + c;
+                float sv[VEC], gv[VEC], wv[VEC], ov[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    wv[e] = 1.f;
+                    ov[e] = 0.f;
+                }
+                load<VEC>(sum + more, sv);
+                load<VEC>(gy + more, gv);
+                if (a.weight) load<VEC>(a.weight + c, wv);
+                if (gs) load<VEC>(gs + more, ov);
+                float* share = shares ? shares + static_cast<long long>(blockIdx.x) * C + c : nullptr;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float n = sv[e] * rstd;
+                    // (the CTA's first row sets the share, its later ones add to it)
+                    if (share) share[e] = r0 == static_cast<long long>(blockIdx.x) * BACK_ROWS && i == 0
+                                              ? gv[e] * n : fmaf(gv[e], n, share[e]);
+                    ov[e] = fmaf(rstd, gv[e] * wv[e] - n * mean, ov[e]);
+                }
+                if (a.grad_residual) store<VEC>(static_cast<TR*>(a.grad_residual) + more, ov);
+                if (a.grad_x) store<VEC>(static_cast<TX*>(a.grad_x) + more, ov);
+            }
+        }
+    }
+    if (shares && mine < C) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) shares[static_cast<long long>(blockIdx.x) * C + mine + e] = acc[e];
+    }
+}
+
+// ---- host --------------------------------------------------------------------
+
+template <typename F>
+kdn_status by_dtype(kdn_dtype t, F f) {
+    return t == KDN_BF16 ? f(__nv_bfloat16()) : f(float());
+}
+
+bool vectors(const NormArgs& a) {
+    const void* p[] = {a.x, a.residual, a.weight, a.sum, a.y, a.grad_y, a.grad_sum, a.grad_residual, a.grad_x};
+    for (const void* q : p)
+        if (reinterpret_cast<uintptr_t>(q) % 16 != 0) return false;
+    return a.C % 8 == 0 && a.x_ld % 8 == 0;
+}
+
+constexpr long long kMostBlocks = 0x7fffffffLL;
+
+template <int VEC, int NV, typename TX, typename TR, typename TY>
+kdn_status launch_fwd(const NormArgs& a, bool alone, int warps, cudaStream_t stream) {
+    if (alone) {
+        const long long blocks = (a.rows + WARPS - 1) / WARPS;
+        if (blocks > kMostBlocks) return KDN_ERR_INVALID_ARG;
+        add_norm_kernel<VEC, NV, TX, TR, TY, true><<<static_cast<unsigned>(blocks), WARPS * 32, 0, stream>>>(a);
+    } else {
+        if (a.rows > kMostBlocks) return KDN_ERR_INVALID_ARG;
+        add_norm_kernel<VEC, NV, TX, TR, TY, false><<<static_cast<unsigned>(a.rows), warps * 32, 0, stream>>>(a);
+    }
+    return from_cuda(cudaGetLastError());
+}
+
+// CTAs of the backward: enough to fill the device, each with rows enough.
+long long back_blocks(long long rows) {
+    const long long want = (rows + BACK_ROWS - 1) / BACK_ROWS, most = static_cast<long long>(sm_count()) * BACK_CTAS;
+    return want < most ? want : most;
+}
+
+}  // namespace
+
+kdn_status norm_fwd_launch(const NormArgs& a, cudaStream_t stream) {
+    if (a.rows == 0) return KDN_OK;
+    return by_dtype(a.x_dtype, [&](auto tx) {
+        return by_dtype(a.res_dtype, [&](auto tr) {
+            using TX = decltype(tx);
+            using TR = decltype(tr);
+            auto go = [&](auto ty) {
+                using TY = decltype(ty);
+                if (!vectors(a)) {
+                    constexpr int PER = 32 * 16;
+                    const int warps = (a.C + PER - 1) / PER;
+                    return launch_fwd<1, 16, TX, TR, TY>(a, warps == 1, warps < 32 ? warps : 32, stream);
+                }
+                // a warp to a row of 2048 where the rows fill the device, else CTAs with one vector a lane
+                constexpr int PER = 32 * 8;
+                if (a.C <= 8 * PER && a.rows >= static_cast<long long>(sm_count()) * WARPS) {
+                    if (a.C <= 2 * PER) return launch_fwd<8, 2, TX, TR, TY>(a, true, 1, stream);
+                    if (a.C <= 4 * PER) return launch_fwd<8, 4, TX, TR, TY>(a, true, 1, stream);
+                    return launch_fwd<8, 8, TX, TR, TY>(a, true, 1, stream);
+                }
+                const int one = (a.C + PER - 1) / PER, two = (a.C + 2 * PER - 1) / (2 * PER);
+                if (one <= 8) return launch_fwd<8, 1, TX, TR, TY>(a, one == 1, one, stream);
+                return launch_fwd<8, 2, TX, TR, TY>(a, false, two < 32 ? two : 32, stream);
+            };
+            if (a.y_dtype == KDN_E4M3) return go(E4m3());
+            return a.y_dtype == KDN_BF16 ? go(__nv_bfloat16()) : go(float());
+        });
+    });
+}
+
+long long norm_bwd_workspace_bytes(long long rows, int C) { return back_blocks(rows) * C * 4; }
+
+kdn_status norm_bwd_launch(const NormArgs& a, cudaStream_t stream) {
+    if (a.rows == 0)
+        return a.grad_weight ? from_cuda(cudaMemsetAsync(a.grad_weight, 0, sizeof(float) * a.C, stream)) : KDN_OK;
+    const long long blocks = back_blocks(a.rows);
+    void* mine = nullptr;
+    float* shares = nullptr;
+    if (a.grad_weight) {
+        shares = static_cast<float*>(a.workspace);
+        if (!shares) {
+            const kdn_status s = from_cuda(cudaMallocAsync(&mine, static_cast<size_t>(norm_bwd_workspace_bytes(a.rows, a.C)), stream));
+            if (s != KDN_OK) return s;
+            shares = static_cast<float*>(mine);
+        }
+    }
+    kdn_status s = by_dtype(a.x_dtype, [&](auto tx) {
+        return by_dtype(a.res_dtype, [&](auto tr) {
+            return by_dtype(a.y_dtype, [&](auto ty) {
+                using TX = decltype(tx);
+                using TR = decltype(tr);
+                using TY = decltype(ty);
+                auto go = [&](auto vec) {
+                    constexpr int VEC = decltype(vec)::value;
+                    const int want = (a.C + VEC - 1) / VEC, threads = want < 1024 ? (want + 31) / 32 * 32 : 1024;
+                    const int slices = (want + threads - 1) / threads;
+                    add_norm_back_kernel<VEC, TX, TR, TY><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(a, shares, slices);
+                    return from_cuda(cudaGetLastError());
+                };
+                return vectors(a) ? go(std::integral_constant<int, 8>()) : go(std::integral_constant<int, 1>());
+            });
+        });
+    });
+    if (s == KDN_OK && shares) s = from_cuda(sum_rows(shares, blocks, a.C, a.grad_weight, nullptr, a.C, stream));
+    if (mine) cudaFreeAsync(mine, stream);
+    return s;
+}
+
+}  // namespace kdn

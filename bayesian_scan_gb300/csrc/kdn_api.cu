@@ -81,6 +81,53 @@ kdn_status qk_check(const QkArgs& a) {
     if (!aligned(a.pos, 4) || !aligned(a.inv_freq, 4) || !aligned(a.axis, 4)) return KDN_ERR_INVALID_ARG;
     return KDN_OK;
 }
+
+// What the forward, the backward and the step of the delta rule check alike.
+kdn_status delta_check(const DeltaArgs& a) {
+    if (a.B < 1 || a.H < 1 || a.T < 0) return KDN_ERR_INVALID_ARG;
+    if (!dtype_ok(a.in_dtype) || !dtype_ok(a.out_dtype)) return KDN_ERR_UNSUPPORTED;
+    if (!head_dim_ok(a.dk) || !head_dim_ok(a.dv)) return KDN_ERR_UNSUPPORTED;
+    if (a.offsets ? (a.nseq < 1 || a.B != 1) : a.nseq != 0) return KDN_ERR_INVALID_ARG;
+    if (a.T > kGatedMaxT) return KDN_ERR_INVALID_ARG;
+    const long long rows = static_cast<long long>(a.offsets ? a.nseq : a.B) * a.H;
+    const long long BH = static_cast<long long>(a.B) * a.H, dmax = a.dk > a.dv ? a.dk : a.dv;
+    if (rows > (1LL << 40) || BH > (1LL << 40) || BH > (1LL << 62) / dmax / (a.T > 0 ? a.T : 1)) return KDN_ERR_INVALID_ARG;
+    const void* rows16[] = {a.q, a.k, a.v, a.out, a.grad_out, a.grad_q, a.grad_k, a.grad_v,
+                            a.S0, a.final_state, a.grad_final_state, a.grad_S0};
+    for (const void* p : rows16)
+        if (!aligned(p, 16)) return KDN_ERR_INVALID_ARG;
+    const void* gates[] = {a.beta, a.d, a.grad_beta, a.grad_d};
+    for (const void* p : gates)
+        if (!aligned(p, size_of(a.in_dtype))) return KDN_ERR_INVALID_ARG;
+    if (!aligned(a.A, 4) || !aligned(a.offsets, 4) || !aligned(a.grad_A, 4)) return KDN_ERR_INVALID_ARG;
+    return KDN_OK;
+}
+
+kdn_status delta_sizes_check(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype t) {
+    DeltaArgs a{};
+    a.B = B; a.H = H; a.T = T; a.dk = dk; a.dv = dv; a.in_dtype = a.out_dtype = t;
+    a.nseq = nseq;
+    static const int some = 0;
+    a.offsets = nseq != 0 ? &some : nullptr;
+    return delta_check(a);
+}
+
+// What the forward and the backward residual addition check alike.
+kdn_status norm_check(const NormArgs& a) {
+    if (a.rows < 0 || a.C < 1 || a.C > kGatedMaxC || a.x_ld < a.C) return KDN_ERR_INVALID_ARG;
+    if (a.rows > (1LL << 60) / a.x_ld) return KDN_ERR_INVALID_ARG;
+    if (!dtype_ok(a.x_dtype) || !dtype_ok(a.res_dtype)) return KDN_ERR_UNSUPPORTED;
+    if (!(a.eps >= 0.f)) return KDN_ERR_INVALID_ARG;
+    const uintptr_t xs = size_of(a.x_dtype), rs = size_of(a.res_dtype);
+    if (!aligned(a.x, xs) || !aligned(a.grad_x, xs)) return KDN_ERR_INVALID_ARG;
+    const void* res[] = {a.residual, a.sum, a.grad_sum, a.grad_residual};
+    for (const void* p : res)
+        if (!aligned(p, rs)) return KDN_ERR_INVALID_ARG;
+    const uintptr_t ys = a.y_dtype == KDN_E4M3 ? 1 : size_of(a.y_dtype);
+    if (!aligned(a.y, ys) || !aligned(a.grad_y, ys)) return KDN_ERR_INVALID_ARG;
+    if (!aligned(a.weight, 4) || !aligned(a.scale, 4) || !aligned(a.grad_weight, 4)) return KDN_ERR_INVALID_ARG;
+    return KDN_OK;
+}
 }  // namespace
 
 cudaError_t diag_take_device_error_bf16(int* status);
@@ -464,6 +511,119 @@ kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, int dk, 
     if (static_cast<long long>(Hq) * dk > (1 << 30) || static_cast<long long>(Hk) * dk > (1 << 30))
         return KDN_ERR_INVALID_ARG;
     *workspace_bytes = qk_bwd_workspace_bytes(B, T, Hq, Hk, dk);
+    return KDN_OK;
+}
+
+kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const void* beta, const void* d,
+                              const float* A, const float* S0, const int* offsets, int nseq, void* out,
+                              float* final_state, int B, int H, int T, int dk, int dv, kdn_dtype in_dtype,
+                              kdn_dtype out_dtype, void* workspace, long long workspace_bytes, void* stream) {
+    if (T > 0 && (!q || !k || !v || !beta || !d || !A || !out)) return KDN_ERR_INVALID_ARG;
+    DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.beta = beta; a.d = d; a.A = A; a.S0 = S0; a.offsets = offsets; a.nseq = nseq;
+    a.B = B; a.H = H; a.T = T; a.dk = dk; a.dv = dv; a.in_dtype = in_dtype; a.out_dtype = out_dtype;
+    a.out = out; a.final_state = final_state; a.workspace = workspace;
+    const kdn_status s = delta_check(a);
+    if (s != KDN_OK) return s;
+    if (workspace && (!aligned(workspace, 256) ||
+                      workspace_bytes < delta_fwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype)))
+        return KDN_ERR_INVALID_ARG;
+    if (T == 0 && !final_state) return KDN_OK;
+    return delta_fwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load());
+}
+
+kdn_status kdn_delta_scan_fwd_workspace(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype,
+                                        long long* workspace_bytes) {
+    if (!workspace_bytes) return KDN_ERR_INVALID_ARG;
+    const kdn_status s = delta_sizes_check(B, H, T, dk, dv, nseq, in_dtype);
+    if (s == KDN_OK) *workspace_bytes = delta_fwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype);
+    return s;
+}
+
+kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const void* beta, const void* d,
+                              const float* A, const float* S0, const int* offsets, int nseq,
+                              const void* grad_out, const float* grad_final_state, void* grad_q, void* grad_k,
+                              void* grad_v, void* grad_beta, void* grad_d, float* grad_A, float* grad_S0, int B,
+                              int H, int T, int dk, int dv, kdn_dtype in_dtype, kdn_dtype out_dtype,
+                              void* workspace, long long workspace_bytes, void* stream) {
+    if (T > 0 && (!q || !k || !v || !beta || !d || !A || !grad_out || !grad_q || !grad_k || !grad_v || !grad_beta ||
+                  !grad_d))
+        return KDN_ERR_INVALID_ARG;
+    DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.beta = beta; a.d = d; a.A = A; a.S0 = S0; a.offsets = offsets; a.nseq = nseq;
+    a.B = B; a.H = H; a.T = T; a.dk = dk; a.dv = dv; a.in_dtype = in_dtype; a.out_dtype = out_dtype;
+    a.grad_out = grad_out; a.grad_final_state = grad_final_state; a.grad_q = grad_q; a.grad_k = grad_k;
+    a.grad_v = grad_v; a.grad_beta = grad_beta; a.grad_d = grad_d; a.grad_A = grad_A; a.grad_S0 = grad_S0;
+    a.workspace = workspace;
+    const kdn_status s = delta_check(a);
+    if (s != KDN_OK) return s;
+    if (workspace && (!aligned(workspace, 256) ||
+                      workspace_bytes < delta_bwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype)))
+        return KDN_ERR_INVALID_ARG;
+    return delta_bwd_launch(a, static_cast<cudaStream_t>(stream), g_wait_ns.load());
+}
+
+kdn_status kdn_delta_scan_bwd_workspace(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype,
+                                        long long* workspace_bytes) {
+    if (!workspace_bytes) return KDN_ERR_INVALID_ARG;
+    const kdn_status s = delta_sizes_check(B, H, T, dk, dv, nseq, in_dtype);
+    if (s == KDN_OK) *workspace_bytes = delta_bwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype);
+    return s;
+}
+
+kdn_status kdn_delta_step(const void* q, const void* k, const void* v, const void* beta, const void* d,
+                          const float* A, const float* state, float* new_state, void* out, int B, int H, int dk,
+                          int dv, kdn_dtype in_dtype, kdn_dtype out_dtype, void* stream) {
+    if (!q || !k || !v || !beta || !d || !A || !state || !new_state || !out) return KDN_ERR_INVALID_ARG;
+    DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.beta = beta; a.d = d; a.A = A; a.out = out;
+    a.B = B; a.H = H; a.T = 1; a.dk = dk; a.dv = dv; a.in_dtype = in_dtype; a.out_dtype = out_dtype;
+    DeltaArgs c = a;
+    c.v = c.out = nullptr;                    // (single elements of these)
+    c.S0 = state;
+    c.final_state = new_state;
+    const kdn_status s = delta_check(c);
+    if (s != KDN_OK) return s;
+    if (!aligned(v, dtype_ok(in_dtype) ? size_of(in_dtype) : 1) || !aligned(out, size_of(out_dtype)))
+        return KDN_ERR_INVALID_ARG;
+    return delta_step_launch(a, state, new_state, static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_add_rms_norm_fwd(const void* x, long long x_ld, const void* residual, const float* weight, float eps,
+                                void* sum, void* y, float* scale, long long rows, int C, kdn_dtype x_dtype,
+                                kdn_dtype res_dtype, kdn_dtype y_dtype, void* stream) {
+    if (rows > 0 && (!x || !y || (residual ? !sum : sum != nullptr))) return KDN_ERR_INVALID_ARG;
+    if (!dtype_ok(y_dtype) && y_dtype != KDN_E4M3) return KDN_ERR_UNSUPPORTED;
+    if (rows > 0 && (y_dtype == KDN_E4M3) != (scale != nullptr)) return KDN_ERR_INVALID_ARG;
+    if (!residual && res_dtype != x_dtype) return KDN_ERR_INVALID_ARG;
+    NormArgs a{};
+    a.x = x; a.x_ld = x_ld; a.residual = residual; a.weight = weight; a.eps = eps; a.sum = sum; a.y = y;
+    a.scale = scale; a.rows = rows; a.C = C; a.x_dtype = x_dtype; a.res_dtype = res_dtype; a.y_dtype = y_dtype;
+    const kdn_status s = norm_check(a);
+    if (s != KDN_OK) return s;
+    return norm_fwd_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_add_rms_norm_bwd(const void* sum, const float* weight, float eps, const void* grad_y,
+                                const void* grad_sum, void* grad_residual, void* grad_x, float* grad_weight,
+                                long long rows, int C, kdn_dtype x_dtype, kdn_dtype res_dtype, kdn_dtype y_dtype,
+                                void* workspace, long long workspace_bytes, void* stream) {
+    if (rows > 0 && (!sum || !grad_y || (!grad_residual && !grad_x && !grad_weight))) return KDN_ERR_INVALID_ARG;
+    if (!dtype_ok(y_dtype)) return KDN_ERR_UNSUPPORTED;
+    NormArgs a{};
+    a.residual = sum; a.x_ld = C; a.weight = weight; a.eps = eps; a.grad_y = grad_y; a.grad_sum = grad_sum;
+    a.grad_residual = grad_residual; a.grad_x = grad_x; a.grad_weight = grad_weight; a.rows = rows; a.C = C;
+    a.x_dtype = x_dtype; a.res_dtype = res_dtype; a.y_dtype = y_dtype; a.workspace = workspace;
+    const kdn_status s = norm_check(a);
+    if (s != KDN_OK) return s;
+    if (workspace && (!aligned(workspace, 256) || workspace_bytes < norm_bwd_workspace_bytes(rows, C)))
+        return KDN_ERR_INVALID_ARG;
+    return norm_bwd_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+kdn_status kdn_add_rms_norm_bwd_workspace(long long rows, int C, long long* workspace_bytes) {
+    if (rows < 0 || C < 1 || C > kGatedMaxC || rows > (1LL << 60) / C || !workspace_bytes) return KDN_ERR_INVALID_ARG;
+    *workspace_bytes = norm_bwd_workspace_bytes(rows, C);
     return KDN_OK;
 }
 

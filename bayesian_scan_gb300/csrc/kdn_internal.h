@@ -153,6 +153,64 @@ kdn_status qk_fwd_launch(const QkArgs& a, cudaStream_t stream, long long wait_ns
 kdn_status qk_bwd_launch(const QkArgs& a, cudaStream_t stream);
 long long qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int dk);
 
+// Arguments of one gated-delta-rule call after host-side validation
+// (delta_scan.cu); the backward's pointers are null in a forward call.
+struct DeltaArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const void* beta;
+    const void* d;
+    const float* A;
+    const float* S0;
+    const int* offsets;
+    int nseq;              // 0 without offsets
+    int B, H, T, dk, dv;
+    kdn_dtype in_dtype, out_dtype;
+    void* out;
+    float* final_state;
+    const void* grad_out;
+    const float* grad_final_state;
+    void* grad_q;
+    void* grad_k;
+    void* grad_v;
+    void* grad_beta;
+    void* grad_d;
+    float* grad_A;
+    float* grad_S0;
+    void* workspace;
+};
+kdn_status delta_fwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns);
+kdn_status delta_bwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns);
+long long delta_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype);
+long long delta_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype);
+kdn_status delta_step_launch(const DeltaArgs& a, const float* state, float* new_state, cudaStream_t stream);
+
+// Arguments of one residual addition with its norm after host-side validation
+// (add_norm.cu).
+struct NormArgs {
+    const void* x;
+    long long x_ld;
+    const void* residual;   // forward: or null; backward: the sum
+    const float* weight;
+    float eps;
+    void* sum;              // forward: written, or null without a residual
+    void* y;
+    float* scale;
+    const void* grad_y;
+    const void* grad_sum;
+    void* grad_residual;
+    void* grad_x;
+    float* grad_weight;
+    long long rows;
+    int C;
+    kdn_dtype x_dtype, res_dtype, y_dtype;
+    void* workspace;
+};
+kdn_status norm_fwd_launch(const NormArgs& a, cudaStream_t stream);
+kdn_status norm_bwd_launch(const NormArgs& a, cudaStream_t stream);
+long long norm_bwd_workspace_bytes(long long rows, int C);
+
 // Host-buffer pipelines (kdn_host.cu): arguments validated, every pointer a
 // host pointer; synchronous.
 kdn_status diag_host(const DiagArgs& a, cudaStream_t stream, long long wait_ns);

@@ -15,6 +15,10 @@ Functions mirror the C names:
   recurrence with one gate per channel)
 * :func:`qk_norm_rope_fwd`, :func:`qk_norm_rope_bwd` -> ``kdn_qk_norm_rope_*`` (queries and keys for
   the scans)
+* :func:`delta_scan_fwd`, :func:`delta_scan_bwd`, :func:`delta_step` -> ``kdn_delta_*`` (the gated
+  delta rule)
+* :func:`add_rms_norm_fwd`, :func:`add_rms_norm_bwd` -> ``kdn_add_rms_norm_*`` (the residual's addition
+  and its norm)
 * :func:`diag_scan_plan`, :func:`mobius_scan_plan` -> the ``*_plan`` queries
 * :func:`get_device_error`, :func:`set_wait_limit_ns`,
   :func:`debug_stall_mobius_tile`, :func:`debug_stall_gated_rank`, :func:`status_string`,
@@ -42,7 +46,7 @@ from . import build as _build
 
 KDN_OK, KDN_ERR_INVALID_ARG, KDN_ERR_UNSUPPORTED = 0, -1, -2
 KDN_ERR_CUDA, KDN_ERR_TIMEOUT, KDN_ERR_ALLOC = -3, -4, -5
-KDN_F32, KDN_BF16 = 0, 1
+KDN_F32, KDN_BF16, KDN_E4M3 = 0, 1, 2
 
 LIB_PATH = _build.LIB
 
@@ -100,6 +104,22 @@ def _load():
                                          vp, vp, vp, ll, vp, ll, fp, fp, i, i, i, i, i, i, i, vp, ll, vp]
     lib.kdn_qk_norm_rope_bwd_workspace.restype = i
     lib.kdn_qk_norm_rope_bwd_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong)]
+    lib.kdn_delta_scan_fwd.restype = i
+    lib.kdn_delta_scan_fwd.argtypes = [vp, vp, vp, vp, vp, fp, fp, vp, i, vp, fp, i, i, i, i, i, i, i, vp, ll, vp]
+    lib.kdn_delta_scan_bwd.restype = i
+    lib.kdn_delta_scan_bwd.argtypes = [vp, vp, vp, vp, vp, fp, fp, vp, i, vp, fp, vp, vp, vp, vp, vp, fp, fp,
+                                       i, i, i, i, i, i, i, vp, ll, vp]
+    for f in (lib.kdn_delta_scan_fwd_workspace, lib.kdn_delta_scan_bwd_workspace):
+        f.restype = i
+        f.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong)]
+    lib.kdn_delta_step.restype = i
+    lib.kdn_delta_step.argtypes = [vp, vp, vp, vp, vp, fp, fp, fp, vp, i, i, i, i, i, i, vp]
+    lib.kdn_add_rms_norm_fwd.restype = i
+    lib.kdn_add_rms_norm_fwd.argtypes = [vp, ll, vp, fp, ctypes.c_float, vp, vp, fp, ll, i, i, i, i, vp]
+    lib.kdn_add_rms_norm_bwd.restype = i
+    lib.kdn_add_rms_norm_bwd.argtypes = [vp, fp, ctypes.c_float, vp, vp, vp, vp, fp, ll, i, i, i, i, vp, ll, vp]
+    lib.kdn_add_rms_norm_bwd_workspace.restype = i
+    lib.kdn_add_rms_norm_bwd_workspace.argtypes = [ll, i, ctypes.POINTER(ctypes.c_longlong)]
     lib.kdn_status_string.restype = ctypes.c_char_p
     lib.kdn_status_string.argtypes = [i]
     lib.kdn_get_device_error.restype = i
@@ -928,6 +948,351 @@ def qk_norm_rope_bwd(q, k, grad_q_out, grad_k_out, pos=None, inv_freq=None, wq=N
     if st != KDN_OK:
         raise KdnError(st, "kdn_qk_norm_rope_bwd")
     return g
+
+
+# ---------------------------------------------------------------------------
+# the gated delta rule
+
+def _delta_sizes(q, v, offsets):
+    """(B, H, T, dk, dv, nseq, shape of the states) of a delta-rule call."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q must be [B,H,T,dk] and v [B,H,T,dv], got {tuple(q.shape)} and {tuple(v.shape)}")
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    rows, nseq = B, 0
+    if offsets is not None:
+        _check(offsets, "offsets", torch.int32)
+        if offsets.dim() != 1 or offsets.numel() < 2 or B != 1:
+            raise ValueError("offsets must be [nseq + 1] with B = 1")
+        rows = nseq = offsets.numel() - 1
+    if (B | H | T | dk | dv | rows) > _MOST:
+        _ints(B, H, T, dk, dv, rows)
+    return B, H, T, dk, dv, nseq, (rows, H, dv, dk)
+
+
+def _delta_inputs(q, k, v, beta, d, A, S0, shape, state):
+    """Checks what the forward and the backward share; returns in_dtype."""
+    B, H, T, dk, dv = shape
+    it, dt = _dtype_of(q, "q"), q.dtype
+    _check(q, "q", dt)
+    _check(k, "k", dt, q.shape)
+    _check(v, "v", dt, (B, H, T, dv))
+    _check(beta, "beta", dt, (B, H, T))
+    _check(d, "d", dt, (B, H, T))
+    _check(A, "A", _F32, (H,))
+    if S0 is not None:
+        _check(S0, "S0", _F32, state)
+    return it
+
+
+def _delta_workspace(f, what, B, H, T, dk, dv, nseq, dtype):
+    _ints(B, H, T, dk, dv, nseq)
+    n = ctypes.c_longlong(0)
+    st = f(B, H, T, dk, dv, nseq, KDN_BF16 if dtype == torch.bfloat16 else KDN_F32, ctypes.byref(n))
+    if st != KDN_OK:
+        raise KdnError(st, what)
+    return int(n.value)
+
+
+def delta_scan_fwd_workspace(B, H, T, dk, dv, nseq=0, dtype=torch.bfloat16) -> int:
+    """Bytes of device workspace ``delta_scan_fwd`` needs (0: none)."""
+    return _delta_workspace(lib.kdn_delta_scan_fwd_workspace, "kdn_delta_scan_fwd_workspace", B, H, T, dk, dv, nseq,
+                            dtype)
+
+
+def delta_scan_bwd_workspace(B, H, T, dk, dv, nseq=0, dtype=torch.bfloat16) -> int:
+    """Bytes of device workspace ``delta_scan_bwd`` needs."""
+    return _delta_workspace(lib.kdn_delta_scan_bwd_workspace, "kdn_delta_scan_bwd_workspace", B, H, T, dk, dv, nseq,
+                            dtype)
+
+
+@functools.lru_cache(maxsize=512)
+def _delta_ws(device, back, *sizes):
+    return (delta_scan_bwd_workspace if back else delta_scan_fwd_workspace)(*sizes)
+
+
+def delta_scan_fwd(q, k, v, beta, d, A, S0=None, offsets=None, out=None, out_dtype=None, final_state=True,
+                   workspace=None, stream=None):
+    """The gated delta rule S_t = alpha_t S_{t-1} + beta_t (v_t - alpha_t
+    S_{t-1} k_t) k_t^T, o_t = S_t q_t, alpha_t = exp(-A d_t) (see
+    ``kdn_delta_scan_fwd``).
+
+    q, k [B,H,T,dk], v [B,H,T,dv], beta, d [B,H,T] (bf16 or fp32, all the
+    same); A [H] fp32; S0 [B,H,dv,dk] fp32 or None.  ``offsets`` [nseq + 1]
+    int32 (device): packed sequences with B = 1; S0 and final_state are then
+    [nseq,H,dv,dk].  ``out_dtype`` is out's type (q's by default);
+    ``final_state`` True (allocate), False/None (skip) or a tensor.
+    ``workspace``: a uint8 device tensor of at least
+    ``delta_scan_fwd_workspace`` bytes, or None (one is taken from torch's
+    caching allocator for the call).  Returns (out [B,H,T,dv], final_state or
+    None).  With offsets, tokens of an ``out`` allocated here that lie in no
+    sequence are undefined."""
+    B, H, T, dk, dv, nseq, state = _delta_sizes(q, v, offsets)
+    it = _delta_inputs(q, k, v, beta, d, A, S0, (B, H, T, dk, dv), state)
+    if out is None:
+        out = _new(v, out_dtype, stream)
+    else:
+        _check(out, "out", out_dtype, v.shape)
+    ot = _dtype_of(out, "out")
+    if final_state is True:
+        final_state = _empty(state, q, _F32, stream)
+    elif final_state is False:
+        final_state = None
+    elif final_state is not None:
+        _check(final_state, "final_state", _F32, state)
+    ws_bytes = _delta_ws(_ws_device(q), False, B, H, T, dk, dv, nseq, q.dtype)
+    if workspace is not None:
+        _check_workspace(workspace, ws_bytes)
+    elif ws_bytes:
+        workspace = _scratch(ws_bytes, q, stream)
+    if not _here(stream, q, k, v, beta, d, A, S0, offsets, out, final_state, workspace):
+        _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, S0=S0, offsets=offsets, out=out,
+                       final_state=final_state, workspace=workspace)
+    st = lib.kdn_delta_scan_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(d), _ptr(A), _ptr(S0), _ptr(offsets),
+                                nseq, _ptr(out), _ptr(final_state), B, H, T, dk, dv, it, ot, _ptr(workspace),
+                                ws_bytes, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_delta_scan_fwd")
+    return out, final_state
+
+
+def delta_scan_bwd(q, k, v, beta, d, A, grad_out, S0=None, offsets=None, grad_final_state=None, grad_q=None,
+                   grad_k=None, grad_v=None, grad_beta=None, grad_d=None, grad_A=True, grad_S0=True,
+                   workspace=None, stream=None):
+    """Backward pass of ``delta_scan_fwd`` (see ``kdn_delta_scan_bwd``): its
+    inputs, and ``grad_out`` [B,H,T,dv] of out's type.  ``grad_q`` ...
+    ``grad_d``: tensors of the inputs' type and shape to write, or None
+    (allocate); ``grad_A``, ``grad_S0``: True (allocate), False/None (skip) or
+    fp32 tensors.  Returns a dict q, k, v, beta, d, A, S0.  ``workspace``: a
+    uint8 device tensor of at least ``delta_scan_bwd_workspace`` bytes, or
+    None (one is taken from torch's caching allocator for the call)."""
+    B, H, T, dk, dv, nseq, state = _delta_sizes(q, v, offsets)
+    it = _delta_inputs(q, k, v, beta, d, A, S0, (B, H, T, dk, dv), state)
+    ot = _dtype_of(grad_out, "grad_out")
+    _check(grad_out, "grad_out", None, v.shape)
+    if grad_final_state is not None:
+        _check(grad_final_state, "grad_final_state", _F32, state)
+    g = {}
+    for name, like, t in (("q", q, grad_q), ("k", k, grad_k), ("v", v, grad_v), ("beta", beta, grad_beta),
+                          ("d", d, grad_d)):
+        if t is None:
+            t = _new(like, None, stream)
+        else:
+            _check(t, "grad_" + name, q.dtype, like.shape)
+        g[name] = t
+    for name, t, shape in (("A", grad_A, (H,)), ("S0", grad_S0, state)):
+        if t is True:
+            t = _empty(shape, q, _F32, stream)
+        elif t is False:
+            t = None
+        elif t is not None:
+            _check(t, "grad_" + name, _F32, shape)
+        g[name] = t
+    ws_bytes = _delta_ws(_ws_device(q), True, B, H, T, dk, dv, nseq, q.dtype)
+    if workspace is not None:
+        _check_workspace(workspace, ws_bytes)
+    elif ws_bytes:
+        workspace = _scratch(ws_bytes, q, stream)
+    if not _here(stream, q, k, v, beta, d, A, S0, offsets, grad_out, grad_final_state, *g.values(), workspace):
+        _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, S0=S0, offsets=offsets, grad_out=grad_out,
+                       grad_final_state=grad_final_state, workspace=workspace,
+                       **{"grad_" + n: t for n, t in g.items()})
+    st = lib.kdn_delta_scan_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(d), _ptr(A), _ptr(S0), _ptr(offsets),
+                                nseq, _ptr(grad_out), _ptr(grad_final_state), _ptr(g["q"]), _ptr(g["k"]),
+                                _ptr(g["v"]), _ptr(g["beta"]), _ptr(g["d"]), _ptr(g["A"]), _ptr(g["S0"]), B, H, T,
+                                dk, dv, it, ot, _ptr(workspace), ws_bytes, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_delta_scan_bwd")
+    return g
+
+
+def delta_step(q, k, v, beta, d, A, state, new_state=None, out=None, out_dtype=None, stream=None):
+    """One token of ``delta_scan_fwd`` from a device-resident state (see
+    ``kdn_delta_step``): q, k [B,H,dk]; v [B,H,dv]; beta, d [B,H] (bf16 or
+    fp32, all the same); A [H] fp32; state [B,H,dv,dk] fp32, updated in place,
+    or left as it is when ``new_state`` is another tensor to write.  Returns
+    out [B,H,dv] (q's type unless ``out_dtype`` says otherwise)."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q must be [B,H,dk] and v [B,H,dv], got {tuple(q.shape)} and {tuple(v.shape)}")
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    if (B | H | dk | dv) > _MOST:
+        _ints(B, H, dk, dv)
+    it, dt = _dtype_of(q, "q"), q.dtype
+    if new_state is None:
+        new_state = state
+    if out is None:
+        out = _new(v, out_dtype, stream)
+    _check(q, "q", dt)
+    _check(k, "k", dt, q.shape)
+    _check(v, "v", dt, (B, H, dv))
+    _check(beta, "beta", dt, (B, H))
+    _check(d, "d", dt, (B, H))
+    _check(A, "A", _F32, (H,))
+    _check(state, "state", _F32, (B, H, dv, dk))
+    _check(new_state, "new_state", _F32, (B, H, dv, dk))
+    _check(out, "out", out_dtype, v.shape)
+    ot = _dtype_of(out, "out")
+    if not _here(stream, q, k, v, beta, d, A, state, new_state, out):
+        _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, state=state, new_state=new_state, out=out)
+    st = lib.kdn_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(d), _ptr(A), _ptr(state), _ptr(new_state),
+                            _ptr(out), B, H, dk, dv, it, ot, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_delta_step")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the residual's addition and its norm
+
+_GROUP = 128                                                 # channels to a scale of an 8-bit output
+
+
+def _rows_ld(t, name):
+    """(rows, C, elements between rows) of a [..., C] tensor whose channels
+    are adjacent and whose rows are evenly apart (dense, or a column slice of
+    a wider tensor)."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must be [..., C] with C > 0, got {tuple(t.shape)}")
+    C = t.shape[-1]
+    rows = t.numel() // C
+    if C > _MOST:
+        _ints(C)
+    if t.is_contiguous():
+        return rows, C, C
+    st, ld, step = t.stride(), None, None
+    if C > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must have adjacent channels")
+    for n, s in zip(reversed(t.shape[:-1]), reversed(st[:-1])):
+        if n > 1:
+            if ld is None:
+                ld = step = s
+            if s != step:
+                raise ValueError(f"{name}'s rows must be evenly apart (stride {step}), got stride {s}")
+            step *= n
+    ld = C if ld is None else ld
+    if ld < C:
+        raise ValueError(f"{name}'s rows must be apart by at least their channels")
+    return rows, C, ld
+
+
+def add_rms_norm_fwd(x, residual=None, weight=None, eps=1e-6, sum_out=None, out=None, out_dtype=None, scale=None,
+                     stream=None):
+    """s = x + residual and y = weight . s / sqrt(mean(s^2) + eps) over the
+    last dimension (see ``kdn_add_rms_norm_fwd``).
+
+    x [...,C] bf16 or fp32, dense or a column slice; ``residual`` of x's shape,
+    bf16 or fp32, or None; ``weight`` [C] fp32 or None.  ``sum_out``: a tensor
+    of residual's type to write s to (residual itself: in place), or None
+    (allocate).  ``out_dtype``: y's type (x's by default);
+    ``torch.float8_e4m3fn`` gives y / scale in 8 bits with a ``scale``
+    [...,ceil(C/128)] fp32, one for each 128 channels (allocated unless
+    given).  Returns (y, s, scale): s is x where there is no residual, scale
+    None where y is not in 8 bits."""
+    rows, C, ld = _rows_ld(x, "x")
+    xt = _dtype_of(x, "x")
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+        rt = xt
+    else:
+        rt = _dtype_of(residual, "residual")
+        _check(residual, "residual", None, x.shape)
+        if sum_out is None:
+            sum_out = _new(residual, None, stream)
+        else:
+            _check(sum_out, "sum_out", residual.dtype, x.shape)
+    if weight is not None:
+        _check(weight, "weight", _F32, (C,))
+    if out is None:
+        out = _empty(x.shape, x, out_dtype or x.dtype, stream)
+    else:
+        _check(out, "out", out_dtype, x.shape)
+    if out.dtype is torch.float8_e4m3fn:
+        yt, shape = KDN_E4M3, (*x.shape[:-1], -(-C // _GROUP))
+        if scale is None:
+            scale = _empty(shape, x, _F32, stream)
+        else:
+            _check(scale, "scale", _F32, shape)
+    else:
+        yt = _DTYPES.get(out.dtype)
+        if yt is None:
+            raise ValueError(f"out must be bf16, fp32 or float8_e4m3fn, got {out.dtype}")
+        if scale is not None:
+            raise ValueError("scale needs an output in 8 bits")
+    if not _here(stream, x, residual, weight, sum_out, out, scale):
+        _on_one_device(stream, x=x, residual=residual, weight=weight, sum_out=sum_out, out=out, scale=scale)
+    st = lib.kdn_add_rms_norm_fwd(x.data_ptr(), ld, _ptr(residual), _ptr(weight), eps, _ptr(sum_out), out.data_ptr(),
+                                  _ptr(scale), rows, C, xt, rt, yt, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_add_rms_norm_fwd")
+    return out, x if residual is None else sum_out, scale
+
+
+def add_rms_norm_bwd_workspace(rows, C) -> int:
+    """Bytes of device workspace ``add_rms_norm_bwd`` needs."""
+    if max(C, rows >> 32) > _MOST:                           # (rows are 64 bits in the C call)
+        _ints(C, rows >> 32)
+    n = ctypes.c_longlong(0)
+    st = lib.kdn_add_rms_norm_bwd_workspace(rows, C, ctypes.byref(n))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_add_rms_norm_bwd_workspace")
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_ws(device, rows, C):
+    return add_rms_norm_bwd_workspace(rows, C)
+
+
+def add_rms_norm_bwd(sum, grad_y, weight=None, grad_sum=None, eps=1e-6, x_dtype=None, grad_residual=None, grad_x=None,
+                     grad_weight=None, workspace=None, stream=None):
+    """Backward pass of ``add_rms_norm_fwd`` with y in bf16 or fp32 (see
+    ``kdn_add_rms_norm_bwd``): ``sum`` [...,C] is the s that it returned,
+    ``grad_y`` of y's type, ``grad_sum`` the gradient that comes to s from
+    further on (sum's type) or None.  ``grad_residual``: a tensor of sum's type
+    to write (grad_sum itself: in place) or None (allocate); ``grad_x`` the
+    same in ``x_dtype`` (sum's by default: then one tensor serves both, unless
+    grad_x is given).  ``grad_weight``: whether the weight's gradient is wanted
+    (None: of one given).  Returns a dict residual, x [...,C] and weight [C]
+    fp32 or None."""
+    rows, C, ld = _rows_ld(sum, "sum")
+    _check(sum, "sum")
+    rt = _dtype_of(sum, "sum")
+    yt = _dtype_of(grad_y, "grad_y")
+    _check(grad_y, "grad_y", None, sum.shape)
+    if weight is not None:
+        _check(weight, "weight", _F32, (C,))
+    if grad_sum is not None:
+        _check(grad_sum, "grad_sum", sum.dtype, sum.shape)
+    if grad_residual is None:
+        grad_residual = _new(sum, None, stream)
+    else:
+        _check(grad_residual, "grad_residual", sum.dtype, sum.shape)
+    if grad_x is not None:
+        _check(grad_x, "grad_x", x_dtype, sum.shape)
+    elif x_dtype is not None and x_dtype is not sum.dtype:
+        grad_x = _empty(sum.shape, sum, x_dtype, stream)
+    xt = rt if grad_x is None else _dtype_of(grad_x, "grad_x")
+    gw, ws_bytes = None, 0
+    if (weight is not None) if grad_weight is None else grad_weight:
+        gw = _empty(C, sum, _F32, stream)
+        ws_bytes = _norm_ws(_ws_device(sum), rows, C)
+        if workspace is None:
+            workspace = _scratch(ws_bytes, sum, stream)
+        else:
+            _check_workspace(workspace, ws_bytes)
+    else:
+        workspace = None
+    if not _here(stream, sum, grad_y, weight, grad_sum, grad_residual, grad_x, gw, workspace):
+        _on_one_device(stream, sum=sum, grad_y=grad_y, weight=weight, grad_sum=grad_sum,
+                       grad_residual=grad_residual, grad_x=grad_x, grad_weight=gw, workspace=workspace)
+    st = lib.kdn_add_rms_norm_bwd(sum.data_ptr(), _ptr(weight), eps, grad_y.data_ptr(), _ptr(grad_sum),
+                                  grad_residual.data_ptr(), _ptr(grad_x), _ptr(gw), rows, C, xt, rt, yt,
+                                  _ptr(workspace), ws_bytes, _stream(stream))
+    if st != KDN_OK:
+        raise KdnError(st, "kdn_add_rms_norm_bwd")
+    return dict(residual=grad_residual, x=grad_residual if grad_x is None else grad_x, weight=gw)
 
 
 def diag_scan_plan(B, H, T, dk, dv, dtype=torch.bfloat16) -> dict:

@@ -24,8 +24,10 @@
  *
  * Beside them: the non-metaplastic limit, the backward pass and the one-token
  * step of the diagonal scan, a gated recurrence with one gate per channel
- * (forward, backward, step), and the norm and position rotation that make the
- * scans' queries and keys (forward, backward).
+ * (forward, backward, step), the norm and position rotation that make the
+ * scans' queries and keys (forward, backward), the gated delta rule (forward,
+ * backward, step), and the residual's addition with its norm (forward,
+ * backward).
  *
  * Conventions shared by every entry point:
  *  - All tensors are dense, row-major (C order) and contiguous.  Device
@@ -69,7 +71,8 @@ typedef enum {
 
 typedef enum {
     KDN_F32 = 0,   /* IEEE binary32 */
-    KDN_BF16 = 1   /* bfloat16 */
+    KDN_BF16 = 1,  /* bfloat16 */
+    KDN_E4M3 = 2   /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 (outputs that say so) */
 } kdn_dtype;
 
 /*
@@ -537,6 +540,157 @@ KDN_API kdn_status kdn_qk_norm_rope_bwd(const void* q, long long q_ld, const voi
  * current device (no GPU work; it reads the device's SM count). */
 KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, int dk,
                                                   long long* workspace_bytes);
+
+/*
+ * kdn_delta_scan_fwd -- the gated delta rule: decayed linear attention that
+ * writes what the state does not yet answer for a key.  Per head a d_v x d_k
+ * state S, and per token
+ *     r_t = v_t - alpha_t S_{t-1} k_t,           alpha_t = exp(-A[h] d_t),
+ *     S_t = alpha_t S_{t-1} + beta_t r_t k_t^T,  o_t = S_t q_t,
+ * with one beta per token and head.  The gate, the layouts and the readout are
+ * kdn_lin_scan_fwd's, whose update writes beta_t v_t instead.
+ *
+ *   q, k      [B,H,T,dk] in_dtype     v [B,H,T,dv] in_dtype
+ *   beta, d   [B,H,T]    in_dtype     A [H] fp32
+ *   S0        [B,H,dv,dk] fp32 or NULL (S_0 = 0)
+ *   out       [B,H,T,dv] out_dtype
+ *   final_state [B,H,dv,dk] fp32 or NULL: S_T (feeding it back as S0 of a call
+ *             on the following tokens gives one call's result)
+ *
+ * Packed sequences: offsets, nseq, S0 and final_state [nseq,H,dv,dk] as for
+ * kdn_gated_scan_fwd (B = 1; sequence n is tokens offsets[n] to offsets[n+1] -
+ * 1 of every head; an empty sequence's final state is its initial one; tokens
+ * in no sequence are neither read nor written).
+ *
+ *   workspace at least kdn_delta_scan_fwd_workspace bytes, 256-byte aligned, or
+ *             NULL (stream-ordered scratch), as for kdn_diag_scan_bwd.  Calls
+ *             that overlap on the GPU need workspaces of their own.
+ *
+ *   B >= 1, H >= 1, T >= 0; dk, dv in {16, 32, 64, 128}; B*H*T*max(dk,dv) <
+ *   2^62.  Tensors 16-byte aligned (d, beta: element-aligned; A, offsets: 4).
+ *   T = 0 writes only final_state.  Outputs overlap no input.
+ *
+ * The state and every sum are fp32; out is rounded once.  alpha_t <= 1 and
+ * beta_t |k_t|^2 <= 2 are expected (the state grows otherwise).
+ * Deterministic.
+ */
+KDN_API kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const void* beta,
+                                      const void* d, const float* A, const float* S0,
+                                      const int* offsets, int nseq, void* out, float* final_state,
+                                      int B, int H, int T, int dk, int dv, kdn_dtype in_dtype,
+                                      kdn_dtype out_dtype, void* workspace,
+                                      long long workspace_bytes, void* stream);
+
+/* Bytes of workspace kdn_delta_scan_fwd needs for these sizes on the current
+ * device (0: none; no GPU work). */
+KDN_API kdn_status kdn_delta_scan_fwd_workspace(int B, int H, int T, int dk, int dv, int nseq,
+                                                kdn_dtype in_dtype, long long* workspace_bytes);
+
+/*
+ * kdn_delta_scan_bwd -- backward pass of kdn_delta_scan_fwd: for
+ *     L = sum grad_out . out + sum grad_final_state . S_T
+ * writes dL/d(input) for every input.  The forward is recomputed inside.
+ *
+ *   q ... nseq  as for the forward
+ *   grad_out  [B,H,T,dv] out_dtype
+ *   grad_final_state [B,H,dv,dk] ([nseq,H,dv,dk]) fp32 or NULL
+ *   grad_q, grad_k [B,H,T,dk], grad_v [B,H,T,dv], grad_beta, grad_d [B,H,T]
+ *             in_dtype, written (tokens in no sequence are not)
+ *   grad_A    [H] fp32 or NULL, written: summed over batch and tokens
+ *   grad_S0   [B,H,dv,dk] ([nseq,H,dv,dk]) fp32 or NULL, written
+ *   workspace at least kdn_delta_scan_bwd_workspace bytes (about B*H*T*dv*(dk/8
+ *             + 8): each 64th token's state and its adjoint, and two rows a
+ *             token), or NULL
+ *
+ * Sizes, alignment and rules as for the forward.  T = 0 writes grad_S0 (=
+ * grad_final_state) and grad_A (= 0).  Sums in fp32, in a fixed order
+ * (deterministic).
+ */
+KDN_API kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const void* beta,
+                                      const void* d, const float* A, const float* S0,
+                                      const int* offsets, int nseq, const void* grad_out,
+                                      const float* grad_final_state, void* grad_q, void* grad_k,
+                                      void* grad_v, void* grad_beta, void* grad_d, float* grad_A,
+                                      float* grad_S0, int B, int H, int T, int dk, int dv,
+                                      kdn_dtype in_dtype, kdn_dtype out_dtype, void* workspace,
+                                      long long workspace_bytes, void* stream);
+
+/* Bytes of workspace kdn_delta_scan_bwd needs for these sizes on the current
+ * device (no GPU work). */
+KDN_API kdn_status kdn_delta_scan_bwd_workspace(int B, int H, int T, int dk, int dv, int nseq,
+                                                kdn_dtype in_dtype, long long* workspace_bytes);
+
+/*
+ * kdn_delta_step -- one token of kdn_delta_scan_fwd for B x H heads whose state
+ * is kept on the device (batched decoding).
+ *
+ *   q, k      [B,H,dk], v [B,H,dv], beta, d [B,H]  in_dtype     A [H] fp32
+ *   state     [B,H,dv,dk] fp32: S before the token
+ *   new_state [B,H,dv,dk] fp32: S after it; may be state itself (in place),
+ *             but may not overlap it otherwise
+ *   out       [B,H,dv] out_dtype
+ *
+ * Equal to kdn_delta_scan_fwd with T = 1, S0 = state, up to rounding.  Tensors
+ * 16-byte aligned (d, beta, v, out: element-aligned; A: 4).  No scratch.
+ */
+KDN_API kdn_status kdn_delta_step(const void* q, const void* k, const void* v, const void* beta,
+                                  const void* d, const float* A, const float* state,
+                                  float* new_state, void* out, int B, int H, int dk, int dv,
+                                  kdn_dtype in_dtype, kdn_dtype out_dtype, void* stream);
+
+/*
+ * kdn_add_rms_norm_fwd -- the residual's addition and its norm, before a
+ * mixer's projection: for each row of C channels
+ *     s = x + residual (rounded to res_dtype),  y = weight . s / sqrt(mean(s^2) + eps).
+ *
+ *   x         rows of C elements, x_ld >= C apart, x_dtype
+ *   residual  [rows,C] res_dtype, or NULL (s = x; sum is then NULL too, and
+ *             res_dtype is x_dtype)
+ *   weight    [C] fp32 or NULL (1)           eps >= 0
+ *   sum       [rows,C] res_dtype: s; may be residual itself (in place)
+ *   y         [rows,C] y_dtype.  With KDN_E4M3 it is in 8 bits, y / scale
+ *             rounded to nearest (ties to even), with
+ *   scale     [rows, ceil(C/128)] fp32: for each group of 128 channels its
+ *             largest |y| / 448, or 1 where that is 0.  NULL for other types.
+ *
+ *   rows >= 0, 1 <= C <= 2^28, rows * x_ld < 2^60; element-aligned (16-byte
+ *   aligned tensors, C and x_ld multiples of 8, take the widest path).  Outputs overlap no
+ *   input otherwise.  The sum of squares is fp32 (|s| < 1e18; without eps,
+ *   rows of 1e-18 and less are lost in it).
+ */
+KDN_API kdn_status kdn_add_rms_norm_fwd(const void* x, long long x_ld, const void* residual,
+                                        const float* weight, float eps, void* sum, void* y,
+                                        float* scale, long long rows, int C, kdn_dtype x_dtype,
+                                        kdn_dtype res_dtype, kdn_dtype y_dtype, void* stream);
+
+/*
+ * kdn_add_rms_norm_bwd -- backward pass of kdn_add_rms_norm_fwd with y in bf16
+ * or fp32: for L = sum grad_y . y + sum grad_sum . s, with s the forward's sum
+ * (or x without a residual); x and residual have one gradient, dL/ds.
+ *
+ *   sum       [rows,C] res_dtype            weight, eps as for the forward
+ *   grad_y    [rows,C] y_dtype
+ *   grad_sum  [rows,C] res_dtype or NULL (0)
+ *   grad_residual [rows,C] res_dtype or NULL, written; may be grad_sum itself
+ *   grad_x    [rows,C] x_dtype or NULL, written (the same values in x's type)
+ *   grad_weight [C] fp32 or NULL, written: summed over the rows (of the weight
+ *             used, given or 1)
+ *   workspace at least kdn_add_rms_norm_bwd_workspace bytes, as for
+ *             kdn_diag_scan_bwd (needed only when grad_weight is written)
+ *
+ * Outputs overlap no input otherwise.  Deterministic.  rows = 0 writes only
+ * grad_weight (= 0).
+ */
+KDN_API kdn_status kdn_add_rms_norm_bwd(const void* sum, const float* weight, float eps,
+                                        const void* grad_y, const void* grad_sum,
+                                        void* grad_residual, void* grad_x, float* grad_weight,
+                                        long long rows, int C, kdn_dtype x_dtype,
+                                        kdn_dtype res_dtype, kdn_dtype y_dtype, void* workspace,
+                                        long long workspace_bytes, void* stream);
+
+/* Bytes of workspace kdn_add_rms_norm_bwd needs for these sizes on the current
+ * device (no GPU work; it reads the device's SM count). */
+KDN_API kdn_status kdn_add_rms_norm_bwd_workspace(long long rows, int C, long long* workspace_bytes);
 
 /* Human-readable name of a status code (static string). */
 KDN_API const char* kdn_status_string(kdn_status s);
