@@ -77,6 +77,31 @@ __device__ __forceinline__ Span span_of(const DeltaArgs& a, long long n) {
     return s;
 }
 
+// The chunk of slot `slot`: its sequence and first token; false where none is.
+__device__ __forceinline__ bool chunk_of(const DeltaArgs& a, long long slot, long long* n, int* t0, int* m, long long* row) {
+    if (!a.offsets) {
+        const int per = (a.T + CHUNK - 1) / CHUNK;
+        *n = *row = slot / per;
+        *t0 = static_cast<int>(slot % per) * CHUNK;
+        *m = min(CHUNK, a.T - *t0);
+        return true;
+    }
+    int low = 0, high = a.nseq - 1;   // the last sequence that begins at or before the slot
+    while (low < high) {
+        const int mid = (low + high + 1) / 2;
+        if (clamped(a.offsets[mid], a.T) / CHUNK + mid <= slot) low = mid;
+        else high = mid - 1;
+    }
+    const int lo = clamped(a.offsets[low], a.T), hi = clamped(a.offsets[low + 1], a.T);
+    const long long c = slot - (lo / CHUNK + low);
+    if (c < 0 || c * CHUNK >= hi - lo) return false;
+    *n = low;
+    *row = 0;
+    *t0 = lo + static_cast<int>(c) * CHUNK;
+    *m = min(CHUNK, hi - *t0);
+    return true;
+}
+
 }  // namespace
 
 // Chunks that the scratch has room for.

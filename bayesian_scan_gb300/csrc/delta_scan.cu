@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "delta_device.cuh"
+#include "delta_tc.h"
 #include "kdn.h"
 #include "kdn_internal.h"
 #include "kernel_setup.h"
@@ -453,31 +454,6 @@ constexpr int grad_smem(int dv) {
     return (2 * CHUNK * (DK + 4) + 3 * CHUNK * (dv + 4) + 2 * CHUNK * (CHUNK + 4) + 9 * CHUNK + 8) * 4;
 }
 
-// The chunk of slot `slot`: its sequence and first token; false where none is.
-__device__ __forceinline__ bool chunk_of(const DeltaArgs& a, long long slot, long long* n, int* t0, int* m, long long* row) {
-    if (!a.offsets) {
-        const int per = (a.T + CHUNK - 1) / CHUNK;
-        *n = *row = slot / per;
-        *t0 = static_cast<int>(slot % per) * CHUNK;
-        *m = min(CHUNK, a.T - *t0);
-        return true;
-    }
-    int low = 0, high = a.nseq - 1;   // the last sequence that begins at or before the slot
-    while (low < high) {
-        const int mid = (low + high + 1) / 2;
-        if (clamped(a.offsets[mid], a.T) / CHUNK + mid <= slot) low = mid;
-        else high = mid - 1;
-    }
-    const int lo = clamped(a.offsets[low], a.T), hi = clamped(a.offsets[low + 1], a.T);
-    const long long c = slot - (lo / CHUNK + low);
-    if (c < 0 || c * CHUNK >= hi - lo) return false;
-    *n = low;
-    *row = 0;
-    *t0 = lo + static_cast<int>(c) * CHUNK;
-    *m = min(CHUNK, hi - *t0);
-    return true;
-}
-
 __device__ __forceinline__ float block_sum(float x, float* share) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -880,7 +856,7 @@ struct BackLayout {
 using namespace delta;
 
 long long delta_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
-    return 0;
+    return tc_takes(T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, nseq) : 0;
 }
 
 long long delta_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
@@ -888,6 +864,16 @@ long long delta_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nse
 }
 
 kdn_status delta_fwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns) {
+    if (tc_takes(a.T, a.dk, a.dv, a.nseq, a.in_dtype)) {
+        Scratch scratch(stream);
+        char* ws = static_cast<char*>(a.workspace);
+        if (!ws) {
+            const kdn_status s = scratch.take(tc_fwd_bytes(a.B, a.H, a.T, a.nseq));
+            if (s != KDN_OK) return s;
+            ws = static_cast<char*>(scratch.p);
+        }
+        return tc_fwd(a, ws, stream, wait_ns);
+    }
     return by_type(a.in_dtype, a.out_dtype, [&](auto ti, auto to) {
         return by_size(a.dk, [&](auto dk) {
             using TI = decltype(ti);

@@ -1,0 +1,17 @@
+// delta_tc.h -- the gated delta rule in chunks on the tensor cores (delta_tc.cu).
+#pragma once
+#include <cuda_runtime.h>
+
+#include "kdn_internal.h"
+
+namespace kdn {
+namespace delta {
+
+// Whether a call takes this form.
+bool tc_takes(int T, int dk, int dv, int nseq, kdn_dtype in_dtype);
+// Scratch of a forward call.
+long long tc_fwd_bytes(int B, int H, int T, int nseq);
+kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long wait_ns);
+
+}  // namespace delta
+}  // namespace kdn

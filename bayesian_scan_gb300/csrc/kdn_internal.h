@@ -224,6 +224,7 @@ cudaError_t diag_take_device_error(int* status);
 cudaError_t mobius_take_device_error(int* status);
 cudaError_t gated_take_device_error(int* status);
 cudaError_t qk_take_device_error(int* status);
+cudaError_t delta_take_device_error(int* status);
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
