@@ -45,13 +45,14 @@ constexpr int PREP_P = 2 * TILE_T;           // P hi, lo
 constexpr int PREP_GATES = 4 * TILE_T;       // e^g, e^{g_C - g}, beta: [3][64] fp32, then e^{g_C}
 constexpr int PREP_BYTES = PREP_GATES + 1024;
 
-// x0, x1 as bf16 pairs hi + lo: hi rounded to nearest, lo what is left,
-// rounded: within 2^-17 of x, and 2^-20 in the mean.
-__device__ __forceinline__ void halves(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+// x as bf16 pairs hi + lo: hi rounded to nearest, lo what is left, rounded:
+// within 2^-17 of x, and 2^-20 in the mean.
+__device__ __forceinline__ void halves(float2 x, uint32_t& hi, uint32_t& lo) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
     hi = *reinterpret_cast<const uint32_t*>(&h);
-    const __nv_bfloat162 l =
-        __floats2bfloat162_rn(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+    const float2 up = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+    const float2 d = __ffma2_rn(up, make_float2(-1.f, -1.f), x);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(d.x, d.y);
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
@@ -82,9 +83,65 @@ __device__ __forceinline__ void load_kq(uint32_t tile, const __nv_bfloat16* k, c
 // ---- preparation -------------------------------------------------------------
 
 constexpr int PREP_THREADS = 128;
-constexpr int LG = C + 4;                    // a row of G and T in shared memory
-constexpr int P_OFF_KQ = 0, P_OFF_G = 2 * TILE_X, P_OFF_T = P_OFF_G + C * LG * 4, P_OFF_X = P_OFF_T + C * LG * 4,
-              P_OFF_GATE = P_OFF_X + 32 * 36 * 4, P_SMEM = P_OFF_GATE + 5 * C * 4 + 64;
+constexpr int LG = C + 4, LX = 36;           // a row of G, T and of X in shared memory
+constexpr int P_OFF_KQ = 0, P_OFF_G = 2 * TILE_X, P_OFF_T = P_OFF_G + C * LG * 4, P_OFF_GATE = P_OFF_T + C * LG * 4,
+              P_SMEM = P_OFF_GATE + 3 * C * 4 + 64;
+// once the product is done, where k and q lay
+constexpr int P_OFF_N = 0, P_OFF_X = P_OFF_N + C * LG * 4;
+static_assert(P_OFF_X + 32 * LX * 4 <= 2 * TILE_X, "the solve's rows fit where k and q lay");
+
+// acc[r] += sum_s A[r * RS][s] B[s] for R rows and 4 columns: A's rows in shared
+// memory LA apart, B's LB apart.
+template <int R, int RS, int N>
+__device__ __forceinline__ void small_product(const float* A, int LA, const float* B, int LB, float2 (&acc)[R][2]) {
+#pragma unroll
+    for (int s = 0; s < N; s += 4) {
+        float4 b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4*>(B + (s + e) * LB);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float4 f = *reinterpret_cast<const float4*>(A + r * RS * LA + s);
+            const float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[r][0] = __ffma2_rn(make_float2(x[e], x[e]), make_float2(b[e].x, b[e].y), acc[r][0]);
+                acc[r][1] = __ffma2_rn(make_float2(x[e], x[e]), make_float2(b[e].z, b[e].w), acc[r][1]);
+            }
+        }
+    }
+}
+
+// T21 = -(X + T2 (beta2 X)), X = G21 + N21 T1 with N = G beta, of pairs of
+// blocks of SIZE: a thread has 4 columns of R rows, 16 apart.
+template <int SIZE>
+__device__ __forceinline__ void join_blocks(const float* sG, const float* sN, float* sT, float* sXb, const float* sb) {
+    constexpr int PER = PREP_THREADS * 2 * SIZE / C, R = SIZE / 16;
+    const int p = threadIdx.x / PER, i = threadIdx.x % PER, o = 2 * SIZE * p;
+    const int c4 = (i % (SIZE / 4)) * 4, r0 = i / (SIZE / 4);
+    float* Xb = sXb + p * SIZE * LX;
+    float2 x[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float4 f = *reinterpret_cast<const float4*>(sG + (o + SIZE + r0 + 16 * r) * LG + o + c4);
+        x[r][0] = make_float2(f.x, f.y);
+        x[r][1] = make_float2(f.z, f.w);
+    }
+    small_product<R, 16, SIZE>(sN + (o + SIZE + r0) * LG + o, LG, sT + o * LG + o + c4, LG, x);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float b = sb[o + SIZE + r0 + 16 * r];
+        *reinterpret_cast<float4*>(Xb + (r0 + 16 * r) * LX + c4) =
+            make_float4(b * x[r][0].x, b * x[r][0].y, b * x[r][1].x, b * x[r][1].y);
+    }
+    __syncthreads();
+    small_product<R, 16, SIZE>(sT + (o + SIZE + r0) * LG + o + SIZE, LG, Xb + c4, LX, x);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        *reinterpret_cast<float4*>(sT + (o + SIZE + r0 + 16 * r) * LG + o + c4) =
+            make_float4(-x[r][0].x, -x[r][0].y, -x[r][1].x, -x[r][1].y);
+    __syncthreads();
+}
 
 // A CTA makes one chunk's T and P: one product [K; Q] K^T (M = 128, N = 64),
 // then T from G by blocks.  With T1, T2 the blocks' own,
@@ -95,11 +152,11 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     extern __shared__ __align__(128) unsigned char smem[];
     float* sG = reinterpret_cast<float*>(smem + P_OFF_G);        // [t][s]
     float* sT = reinterpret_cast<float*>(smem + P_OFF_T);
-    float* sX = reinterpret_cast<float*>(smem + P_OFF_X);        // [32][36]
+    float* sN = reinterpret_cast<float*>(smem + P_OFF_N);        // G beta
     float* gh = reinterpret_cast<float*>(smem + P_OFF_GATE);     // log2 decay since the chunk began, as two floats
     float* gl = gh + C;
     float* sb = gl + C;
-    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P_OFF_GATE + 5 * C * 4);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P_OFF_GATE + 3 * C * 4);
     uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = static_cast<int>(blockIdx.x % a.H);
@@ -173,27 +230,46 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     tc_fence_after_sync();
     {   // row tid: K K^T of token tid, or Q K^T of token tid - 64
         const int t = tid & (C - 1);
-        const float th = gh[t], tl = gl[t];
+        const bool reads = tid < C;          // k_t reads the state before its token, q_t the one after
+        const float2 th = make_float2(gh[t], gh[t]), tl = make_float2(gl[t], gl[t]), minus = make_float2(-1.f, -1.f);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float x[32];
             tmem_ld32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + 32 * half, x);
+            if (__any_sync(0xffffffffu, 32 * half <= t)) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int s = 32 * half + e;
-                const float w = ex2((th - gh[s]) + (tl - gl[s]));
-                x[e] = (tid < C ? s < t : s <= t) ? x[e] * w : 0.f;
+                for (int e = 0; e < 32; e += 4) {
+                    const int s = 32 * half + e;
+                    const float4 h = *reinterpret_cast<const float4*>(gh + s), l = *reinterpret_cast<const float4*>(gl + s);
+                    const float2 w0 = __fadd2_rn(__ffma2_rn(make_float2(h.x, h.y), minus, th),
+                                                 __ffma2_rn(make_float2(l.x, l.y), minus, tl));
+                    const float2 w1 = __fadd2_rn(__ffma2_rn(make_float2(h.z, h.w), minus, th),
+                                                 __ffma2_rn(make_float2(l.z, l.w), minus, tl));
+                    const int last = reads ? t - 1 : t;
+                    x[e] = s <= last ? x[e] * ex2(w0.x) : 0.f;
+                    x[e + 1] = s + 1 <= last ? x[e + 1] * ex2(w0.y) : 0.f;
+                    x[e + 2] = s + 2 <= last ? x[e + 2] * ex2(w1.x) : 0.f;
+                    x[e + 3] = s + 3 <= last ? x[e + 3] * ex2(w1.y) : 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = 0.f;
             }
-            if (tid < C) {
+            if (reads) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(sG + t * LG + 32 * half + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                for (int e = 0; e < 32; e += 4) {
+                    const int s = 32 * half + e;
+                    const float4 b = *reinterpret_cast<const float4*>(sb + s);
+                    *reinterpret_cast<float4*>(sG + t * LG + s) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    *reinterpret_cast<float4*>(sN + t * LG + s) =
+                        make_float4(x[e] * b.x, x[e + 1] * b.y, x[e + 2] * b.z, x[e + 3] * b.w);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) halves(x[e + 2 * p], x[e + 2 * p + 1], hi[p], lo[p]);
+                    for (int p = 0; p < 4; ++p) halves(make_float2(x[e + 2 * p], x[e + 2 * p + 1]), hi[p], lo[p]);
                     const int off = PREP_P + at_c(t, 4 * half + e / 8);
                     *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(out + off + TILE_T) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -204,63 +280,36 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     tc_fence_before_sync();
     __syncthreads();   // G is in shared memory; tensor memory is read
     if (warp == 0) tmem_dealloc(tmem, 64);
-    {   // 16 x 16 blocks on the diagonal: lane c has column c, rows one after another
+    {   // 16 x 16 blocks on the diagonal: lane c has column c, T_t = -(G_t + sum_{s < t} N_ts T_s) row after row
         const int o = 16 * warp, c = lane & 15;
         float col[16];
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-            float x = sG[(o + t) * LG + o + c];
+            float x = sG[(o + t) * LG + o + c], y = 0.f;
 #pragma unroll
-            for (int s = 0; s < t; ++s) x = fmaf(sG[(o + t) * LG + o + s] * sb[o + s], col[s], x);
-            col[t] = -x;                     // (0 above and on the diagonal: G is, and the rows before are)
+            for (int s4 = 0; s4 < t; s4 += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(sN + (o + t) * LG + o + s4);
+                x = fmaf(f.x, col[s4], x);
+                if (s4 + 1 < t) y = fmaf(f.y, col[s4 + 1], y);
+                if (s4 + 2 < t) x = fmaf(f.z, col[s4 + 2], x);
+                if (s4 + 3 < t) y = fmaf(f.w, col[s4 + 3], y);
+            }
+            col[t] = -(x + y);               // (0 above and on the diagonal: G is, and the rows before are)
         }
         if (lane < 16)
 #pragma unroll
             for (int t = 0; t < 16; ++t) sT[(o + t) * LG + o + c] = col[t];
     }
     __syncthreads();
-    // pairs of blocks of `size`: X = G21 + G21 beta1 T1, T21 = -(X + T2 beta2 X)
-#pragma unroll
-    for (int size = 16; size < C; size *= 2) {
-        const int pairs = C / (2 * size), per = PREP_THREADS / pairs;      // threads to a pair: 64, 128
-        const int p = tid / per, i = tid % per, o = 2 * size * p;
-        const int c4 = (i % (size / 4)) * 4, r0 = i / (size / 4);
-        const int step = per / (size / 4);                                  // 16, 16
-        float* X = sX + p * 16 * 36;
-        for (int r = r0; r < size; r += step) {
-            float4 x = *reinterpret_cast<const float4*>(sG + (o + size + r) * LG + o + c4);
-            for (int s = 0; s < size; ++s) {
-                const float g = sG[(o + size + r) * LG + o + s] * sb[o + s];
-                const float4 y = *reinterpret_cast<const float4*>(sT + (o + s) * LG + o + c4);
-                x.x = fmaf(g, y.x, x.x);
-                x.y = fmaf(g, y.y, x.y);
-                x.z = fmaf(g, y.z, x.z);
-                x.w = fmaf(g, y.w, x.w);
-            }
-            *reinterpret_cast<float4*>(X + r * 36 + c4) = x;
-        }
-        __syncthreads();
-        for (int r = r0; r < size; r += step) {
-            float4 x = *reinterpret_cast<const float4*>(X + r * 36 + c4);
-            for (int s = 0; s < r; ++s) {    // (T2 is strictly lower)
-                const float g = sT[(o + size + r) * LG + o + size + s] * sb[o + size + s];
-                const float4 y = *reinterpret_cast<const float4*>(X + s * 36 + c4);
-                x.x = fmaf(g, y.x, x.x);
-                x.y = fmaf(g, y.y, x.y);
-                x.z = fmaf(g, y.z, x.z);
-                x.w = fmaf(g, y.w, x.w);
-            }
-            *reinterpret_cast<float4*>(sT + (o + size + r) * LG + o + c4) = make_float4(-x.x, -x.y, -x.z, -x.w);
-        }
-        __syncthreads();
-    }
+    join_blocks<16>(sG, sN, sT, reinterpret_cast<float*>(smem + P_OFF_X), sb);
+    join_blocks<32>(sG, sN, sT, reinterpret_cast<float*>(smem + P_OFF_X), sb);
     for (int i = tid; i < C * (C / 8); i += PREP_THREADS) {
         const int t = i & (C - 1), c8 = i / C;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const int s = 8 * c8 + 2 * p;
-            halves(sT[t * LG + s], sT[t * LG + s + 1], hi[p], lo[p]);
+            halves(*reinterpret_cast<const float2*>(sT + t * LG + s), hi[p], lo[p]);
         }
         const int off = PREP_T + at_c(t, c8);
         *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -271,10 +320,12 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
 
 // ---- the walk ------------------------------------------------------------------
 
-// Warps 0-7 work on the state's rows (thread = row i = lane of tensor memory,
-// warp / 4 = half of the columns), warp 8 issues the products, warps 9 and 10
-// bring the tiles, one chunk ahead.
-constexpr int ROW_WARPS = 8, MMA_WARP = 8, LOAD_WARPS = 2, CH_THREADS = (ROW_WARPS + 1 + LOAD_WARPS) * 32;
+// Warps 0-15 work on the state's rows (thread = row i = lane of tensor memory,
+// warp / 4 = quarter of the columns and of the tokens), warp 16 issues the
+// products, warps 17 and 18 bring the tiles, one chunk ahead.  Sixteen row
+// warps: with eight, two to a scheduler, their dependent steps took 1.6 times
+// as long (a chunk 7900 cycles).
+constexpr int ROW_WARPS = 16, MMA_WARP = ROW_WARPS, LOAD_WARPS = 2, CH_THREADS = (ROW_WARPS + 1 + LOAD_WARPS) * 32;
 // shared memory: two stages of [k; q], v and the prepared chunk
 constexpr int ST_V = 2 * TILE_X, ST_PREP = ST_V + TILE_X, STAGE_BYTES = ST_PREP + PREP_BYTES;
 constexpr int CH_OFF_BAR = 2 * STAGE_BYTES, CH_SMEM = CH_OFF_BAR + 128;
@@ -311,25 +362,52 @@ __device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-        "%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+__device__ __forceinline__ void tmem_st8w(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
-
-// The halves of 32 tokens' values: hi in 16 columns, lo in the 16 behind them.
-__device__ __forceinline__ void put_halves(uint32_t taddr, const float (&x)[32]) {
-    uint32_t hi[16], lo[16];
+__device__ __forceinline__ void tmem_get16(uint32_t taddr, float2 (&x)[8]) {
+    float v[16];
+    tmem_ld16_async(taddr, v);
+    tmem_wait_ld16(v);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) halves(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
-    tmem_st16w(taddr, hi);
-    tmem_st16w(taddr + 16, lo);
+    for (int e = 0; e < 8; ++e) x[e] = make_float2(v[2 * e], v[2 * e + 1]);
 }
-// ... and where K step ks (16 tokens) of such halves lies.
-__device__ __forceinline__ uint32_t half_at(int ks) { return 32 * (ks >> 1) + 8 * (ks & 1); }
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const float2 (&x)[8]) {
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[2 * e] = x[e].x;
+        v[2 * e + 1] = x[e].y;
+    }
+    tmem_st16(taddr, v);
+}
+// The halves of 16 tokens' values, one K step: hi in 8 columns, lo in the 8 behind them.
+__device__ __forceinline__ void put_halves(uint32_t taddr, const float2 (&x)[8]) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
+    tmem_st8w(taddr, hi);
+    tmem_st8w(taddr + 8, lo);
+}
+// 16 consecutive floats of shared memory (16-byte aligned).
+__device__ __forceinline__ void get16(const float* p, float2 (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float4 f = reinterpret_cast<const float4*>(p)[e];
+        x[2 * e] = make_float2(f.x, f.y);
+        x[2 * e + 1] = make_float2(f.z, f.w);
+    }
+}
+// Column i of 16 rows of [t][D] bf16.
+__device__ __forceinline__ void get_column(const __nv_bfloat16* p, float2 (&x)[8]) {
+    const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = make_float2(__uint_as_float(static_cast<uint32_t>(u[2 * e * D]) << 16),
+                           __uint_as_float(static_cast<uint32_t>(u[(2 * e + 1) * D]) << 16));
+}
 
 template <typename TO>
 __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, long long wait_ns) {
@@ -399,6 +477,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 bulk_g2s(stage + ST_PREP, mine + c * static_cast<long long>(a.H) * PREP_BYTES, PREP_BYTES, full + st);
             }
             load_kq(smem_addr(stage), k + row, q + row, m, l, LOAD_WARPS * 32);
+            // no token: zeros, not what lay there before
+            for (int e = l; e < (C - m) * (D / 8); e += LOAD_WARPS * 32)
+                *reinterpret_cast<uint4*>(stage + ST_V + m * D * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
             copies_done();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(full + st);
@@ -432,10 +513,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 for (int ks = 0; ks < C / 16; ++ks) {
                     const uint64_t hi = umma_desc_kmajor(pr + PREP_T + ks * 256, 128, ROWS_C);
                     const uint64_t lo = umma_desc_kmajor(pr + PREP_T + TILE_T + ks * 256, 128, ROWS_C);
-                    const uint32_t z = tmem + COL_W + half_at(ks);
+                    const uint32_t z = tmem + COL_W + 16 * ks;
                     umma_ta(tmem + COL_Z, z, hi, ID_N64, ks > 0 ? 1u : 0u);
                     umma_ta(tmem + COL_Z, z, lo, ID_N64, 1u);
-                    umma_ta(tmem + COL_Z, z + 16, hi, ID_N64, 1u);
+                    umma_ta(tmem + COL_Z, z + 8, hi, ID_N64, 1u);
                 }
                 umma_commit(done_r);
                 wait(have_w, par);
@@ -444,8 +525,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks) {
                     const uint64_t b = umma_desc_mnmajor(kq + ks * 2 * ROWS_D, ROWS_D, 128);
-                    umma_ta(tmem + COL_S, tmem + COL_W + half_at(ks), b, ID_S, 1u);
-                    umma_ta(tmem + COL_S, tmem + COL_W + half_at(ks) + 16, b, ID_S, 1u);
+                    umma_ta(tmem + COL_S, tmem + COL_W + 16 * ks, b, ID_S, 1u);
+                    umma_ta(tmem + COL_S, tmem + COL_W + 16 * ks + 8, b, ID_S, 1u);
                 }
                 umma_commit(done_s);
                 wait(have_u, par);
@@ -455,10 +536,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 for (int ks = 0; ks < C / 16; ++ks) {
                     const uint64_t hi = umma_desc_kmajor(pr + PREP_P + ks * 256, 128, ROWS_C);
                     const uint64_t lo = umma_desc_kmajor(pr + PREP_P + TILE_T + ks * 256, 128, ROWS_C);
-                    const uint32_t u = tmem + COL_Z + half_at(ks);
+                    const uint32_t u = tmem + COL_Z + 16 * ks;
                     umma_ta(tmem + COL_O, u, hi, ID_N64, ks > 0 ? 1u : 0u);
                     umma_ta(tmem + COL_O, u, lo, ID_N64, 1u);
-                    umma_ta(tmem + COL_O, u + 16, hi, ID_N64, 1u);
+                    umma_ta(tmem + COL_O, u + 8, hi, ID_N64, 1u);
                 }
                 umma_commit(done_o);
                 umma_commit(empty + st);
@@ -468,113 +549,114 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         __syncwarp();
     } else {
         // ---- rows -------------------------------------------------------------------
-        const int q4 = warp & 3, half = warp >> 2, i = 32 * q4 + lane;
+        const int q4 = warp & 3, part = warp >> 2, i = 32 * q4 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
-        const int cb = 64 * half, tb = 32 * half;        // its columns of S, its tokens
+        const int cb = 32 * part, tb = 16 * part;        // its columns of S, its tokens
         auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
             wait(bar, parity);
             __syncwarp();
             tc_fence_after_sync();
         };
         auto arrive = [&](uint64_t* bar) {
+            tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            float x[32];
+            float2 x[8];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
+            for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (S0) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * D + cb + 32 * p + j);
-                x[j] = f.x;
-                x[j + 1] = f.y;
-                x[j + 2] = f.z;
-                x[j + 3] = f.w;
+                if (S0) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * D + cb + 16 * p + 2 * e);
+                x[e] = make_float2(f.x, f.y);
+                x[e + 1] = make_float2(f.z, f.w);
             }
-            tmem_st32(tl + COL_S + cb + 32 * p, x);
+            tmem_put16(tl + COL_S + cb + 16 * p, x);
         }
         tmem_wait_st();
         TO* out = static_cast<TO*>(a.out) + tok * D + i;
-        float qs[32];                                    // e^g Q S^T of the chunk before
+        float2 qs[8];                                    // e^g Q S^T of the chunk before
         auto finish = [&](int c) {                       // outputs of chunk c
             wait_warp(done_o, c & 1);
-            float o[32];
-            tmem_ld32(tl + COL_O + tb, o);
+            float2 o[8];
+            tmem_get16(tl + COL_O + tb, o);
             const int m = len - c * C - tb;
             TO* dst = out + (static_cast<long long>(c) * C + tb) * D;
 #pragma unroll
-            for (int t = 0; t < 32; ++t)
-                if (t < m) dst[static_cast<long long>(t) * D] = from_f32<TO>(o[t] + qs[t]);
+            for (int e = 0; e < 8; ++e) {
+                const float2 y = __fadd2_rn(o[e], qs[e]);
+                if (2 * e < m) dst[2 * e * D] = from_f32<TO>(y.x);
+                if (2 * e + 1 < m) dst[(2 * e + 1) * D] = from_f32<TO>(y.y);
+            }
         };
         auto read_qs = [&](int c) {                      // (the last use of its stage)
             wait_warp(done_s, c & 1);
-            tmem_ld32(tl + COL_QS + tb, qs);
-            const float* eg = reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + ST_PREP + PREP_GATES) + tb;
+            float2 eg[8];
+            tmem_get16(tl + COL_QS + tb, qs);
+            get16(reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + ST_PREP + PREP_GATES) + tb, eg);
 #pragma unroll
-            for (int t = 0; t < 32; ++t) qs[t] *= eg[t];
+            for (int e = 0; e < 8; ++e) qs[e] = __fmul2_rn(qs[e], eg[e]);
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + (c & 1));
         };
         for (int c = 0; c < chunks; ++c) {
-            const int st = c & 1, m = min(C, len - c * C);
+            const int st = c & 1;
             const uint32_t par = c & 1;
             unsigned char* stage = smem + st * STAGE_BYTES;
-            const float* eg = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
+            const float* eg = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES) + tb;
             const float *ew = eg + C, *be = ew + C;
             if (c > 0) read_qs(c - 1);
             wait_warp(full + st, (c >> 1) & 1);
             {   // the state's halves, and its decay over the chunk in place
-                const float end = eg[3 * C];
+                const float end = *(reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES) + 3 * C);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    float x[32];
-                    tmem_ld32(tl + COL_S + cb + 32 * p, x);
-                    uint32_t hi[16], lo[16];
+                    float2 x[8];
+                    tmem_get16(tl + COL_S + cb + 16 * p, x);
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) halves(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
-                    tmem_st16w(tl + COL_SH + (cb + 32 * p) / 2, hi);
-                    tmem_st16w(tl + COL_SL + (cb + 32 * p) / 2, lo);
+                    for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
+                    tmem_st8w(tl + COL_SH + (cb + 16 * p) / 2, hi);
+                    tmem_st8w(tl + COL_SL + (cb + 16 * p) / 2, lo);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] *= end;
-                    tmem_st32(tl + COL_S + cb + 32 * p, x);
+                    for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(x[e], make_float2(end, end));
+                    tmem_put16(tl + COL_S + cb + 16 * p, x);
                 }
-                tmem_wait_st();
             }
             arrive(have_s);
             if (c > 0) finish(c - 1);
-            // z = v - e^g S k
-            float z[32];
-            {
+            float2 z[8], b[8];
+            get_column(reinterpret_cast<const __nv_bfloat16*>(stage + ST_V) + tb * D + i, z);
+            get16(be, b);
+            {   // z = v - e^g S k
+                float2 x[8], g[8];
+                get16(eg, g);
                 wait_warp(done_z, par);
-                float x[32];
-                tmem_ld32(tl + COL_Z + tb, x);
-                const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(stage + ST_V) + tb * D + i;
+                tmem_get16(tl + COL_Z + tb, x);
 #pragma unroll
-                for (int t = 0; t < 32; ++t) {
-                    z[t] = fmaf(-eg[tb + t], x[t], to_f32(v[t * D]));
-                    if (tb + t >= m) z[t] = 0.f;         // (no token: what lies there is old)
-                    x[t] = be[tb + t] * z[t];
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = __fmul2_rn(x[e], g[e]);
+                    z[e] = __ffma2_rn(x[e], make_float2(-1.f, -1.f), z[e]);
+                    x[e] = __fmul2_rn(b[e], z[e]);
                 }
                 put_halves(tl + COL_W + tb, x);
-                tmem_wait_st();
                 arrive(have_z);
             }
             {   // r = z + T beta z, u = beta r
+                float2 x[8], w[8];
+                get16(ew, w);
                 wait_warp(done_r, par);
-                float x[32];
-                tmem_ld32(tl + COL_Z + tb, x);
+                tmem_get16(tl + COL_Z + tb, x);
 #pragma unroll
-                for (int t = 0; t < 32; ++t) {
-                    z[t] = be[tb + t] * (z[t] + x[t]);
-                    x[t] = ew[tb + t] * z[t];
+                for (int e = 0; e < 8; ++e) {
+                    z[e] = __fmul2_rn(b[e], __fadd2_rn(z[e], x[e]));
+                    x[e] = __fmul2_rn(w[e], z[e]);
                 }
                 put_halves(tl + COL_W + tb, x);
-                tmem_wait_st();
                 arrive(have_w);
                 put_halves(tl + COL_Z + tb, z);
-                tmem_wait_st();
                 arrive(have_u);
             }
         }
@@ -583,12 +665,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         if (final_state) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float x[32];
-                tmem_ld32(tl + COL_S + cb + 32 * p, x);
-                float* dst = final_state + static_cast<long long>(i) * D + cb + 32 * p;
+                float2 x[8];
+                tmem_get16(tl + COL_S + cb + 16 * p, x);
+                float* dst = final_state + static_cast<long long>(i) * D + cb + 16 * p;
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                for (int e = 0; e < 8; e += 2)
+                    *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(x[e].x, x[e].y, x[e + 1].x, x[e + 1].y);
             }
         }
     }
