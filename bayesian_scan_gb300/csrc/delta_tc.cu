@@ -84,11 +84,11 @@ __device__ __forceinline__ void load_kq(uint32_t tile, const __nv_bfloat16* k, c
 
 constexpr int PREP_THREADS = 128;
 constexpr int LG = C + 4, LX = 36;           // a row of G, T and of X in shared memory
-constexpr int P_OFF_KQ = 0, P_OFF_G = 2 * TILE_X, P_OFF_T = P_OFF_G + C * LG * 4, P_OFF_GATE = P_OFF_T + C * LG * 4,
-              P_SMEM = P_OFF_GATE + 3 * C * 4 + 64;
-// once the product is done, where k and q lay
-constexpr int P_OFF_N = 0, P_OFF_X = P_OFF_N + C * LG * 4;
-static_assert(P_OFF_X + 32 * LX * 4 <= 2 * TILE_X, "the solve's rows fit where k and q lay");
+// G (then T, block by block in its place), N = G beta and X lie where k and q
+// lay before the product: five CTAs to an SM hide one another's waits.
+constexpr int P_OFF_KQ = 0, P_OFF_G = 0, P_OFF_N = P_OFF_G + C * LG * 4, P_OFF_X = P_OFF_N + C * LG * 4,
+              P_OFF_GATE = P_OFF_X + 32 * LX * 4, P_SMEM = P_OFF_GATE + 3 * C * 4 + 64;
+static_assert(P_OFF_GATE >= 2 * TILE_X, "the gates lie behind k and q");
 
 // acc[r] += sum_s A[r * RS][s] B[s] for R rows and 4 columns: A's rows in shared
 // memory LA apart, B's LB apart.
@@ -115,7 +115,7 @@ __device__ __forceinline__ void small_product(const float* A, int LA, const floa
 // T21 = -(X + T2 (beta2 X)), X = G21 + N21 T1 with N = G beta, of pairs of
 // blocks of SIZE: a thread has 4 columns of R rows, 16 apart.
 template <int SIZE>
-__device__ __forceinline__ void join_blocks(const float* sG, const float* sN, float* sT, float* sXb, const float* sb) {
+__device__ __forceinline__ void join_blocks(float* sT, const float* sN, float* sXb, const float* sb) {
     constexpr int PER = PREP_THREADS * 2 * SIZE / C, R = SIZE / 16;
     const int p = threadIdx.x / PER, i = threadIdx.x % PER, o = 2 * SIZE * p;
     const int c4 = (i % (SIZE / 4)) * 4, r0 = i / (SIZE / 4);
@@ -123,7 +123,7 @@ __device__ __forceinline__ void join_blocks(const float* sG, const float* sN, fl
     float2 x[R][2];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float4 f = *reinterpret_cast<const float4*>(sG + (o + SIZE + r0 + 16 * r) * LG + o + c4);
+        const float4 f = *reinterpret_cast<const float4*>(sT + (o + SIZE + r0 + 16 * r) * LG + o + c4);   // G21
         x[r][0] = make_float2(f.x, f.y);
         x[r][1] = make_float2(f.z, f.w);
     }
@@ -151,7 +151,6 @@ __device__ __forceinline__ void join_blocks(const float* sG, const float* sN, fl
 __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArgs a, char* prep, long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
     float* sG = reinterpret_cast<float*>(smem + P_OFF_G);        // [t][s]
-    float* sT = reinterpret_cast<float*>(smem + P_OFF_T);
     float* sN = reinterpret_cast<float*>(smem + P_OFF_N);        // G beta
     float* gh = reinterpret_cast<float*>(smem + P_OFF_GATE);     // log2 decay since the chunk began, as two floats
     float* gl = gh + C;
@@ -169,7 +168,6 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
 
     load_kq(smem_addr(smem), static_cast<const __nv_bfloat16*>(a.k) + tok * D,
             static_cast<const __nv_bfloat16*>(a.q) + tok * D, m, tid, PREP_THREADS);
-    for (int i = tid; i < C * LG; i += PREP_THREADS) sT[i] = 0.f;
     if (warp == 0) {
         tmem_alloc(holder, 64);
     } else if (warp == 1) {
@@ -296,20 +294,21 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
             }
             col[t] = -(x + y);               // (0 above and on the diagonal: G is, and the rows before are)
         }
+        __syncwarp();
         if (lane < 16)
 #pragma unroll
-            for (int t = 0; t < 16; ++t) sT[(o + t) * LG + o + c] = col[t];
+            for (int t = 0; t < 16; ++t) sG[(o + t) * LG + o + c] = col[t];
     }
     __syncthreads();
-    join_blocks<16>(sG, sN, sT, reinterpret_cast<float*>(smem + P_OFF_X), sb);
-    join_blocks<32>(sG, sN, sT, reinterpret_cast<float*>(smem + P_OFF_X), sb);
+    join_blocks<16>(sG, sN, reinterpret_cast<float*>(smem + P_OFF_X), sb);
+    join_blocks<32>(sG, sN, reinterpret_cast<float*>(smem + P_OFF_X), sb);
     for (int i = tid; i < C * (C / 8); i += PREP_THREADS) {
         const int t = i & (C - 1), c8 = i / C;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const int s = 8 * c8 + 2 * p;
-            halves(*reinterpret_cast<const float2*>(sT + t * LG + s), hi[p], lo[p]);
+            halves(*reinterpret_cast<const float2*>(sG + t * LG + s), hi[p], lo[p]);
         }
         const int off = PREP_T + at_c(t, c8);
         *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -353,12 +352,21 @@ struct Waits {
     }
 };
 
+// Issue by a whole warp, whose values are all uniform: one thread of it is
+// elected for the instruction.  (Out of a branch of one lane each operand went
+// through vector registers, and a product took 56 cycles to issue.)
 // D (TMEM) = A (TMEM, bf16 pairs packed per column, lane = row) * B^T (smem)
 __device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_done(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_addr(bar))
         : "memory");
 }
 
@@ -414,12 +422,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);   // [2] a stage is here
     uint64_t* empty = full + 2;                                        // [2] a stage is read
-    uint64_t* done_z = empty + 2;                                      // products: Z and Q S^T, R, S, O
+    uint64_t* done_z = empty + 2;                                      // products: Z, R, S, O
     uint64_t* done_r = done_z + 1;
-    uint64_t* done_s = done_r + 1;
-    uint64_t* done_o = done_s + 1;
-    uint64_t* have_s = done_o + 1;                                     // operands: S, beta Z, wU, U
-    uint64_t* have_z = have_s + 1;
+    uint64_t* done_s = done_r + 1;                                     // [2] (columns 0-63 and 64-127)
+    uint64_t* done_o = done_s + 2;
+    uint64_t* have_s = done_o + 1;                                     // operands: S [2], beta Z, wU, U
+    uint64_t* have_z = have_s + 2;
     uint64_t* have_w = have_z + 1;
     uint64_t* have_u = have_w + 1;
     uint32_t* holder = reinterpret_cast<uint32_t*>(have_u + 1);
@@ -444,8 +452,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             mbar_init(full + s, LOAD_WARPS * 32 + 1);
             mbar_init(empty + s, 1 + ROW_WARPS);
         }
-        for (uint64_t* b : {done_z, done_r, done_s, done_o}) mbar_init(b, 1);
-        for (uint64_t* b : {have_s, have_z, have_w, have_u}) mbar_init(b, ROW_WARPS);
+        for (uint64_t* b : {done_z, done_r, done_s, done_s + 1, done_o}) mbar_init(b, 1);
+        for (uint64_t* b : {have_z, have_w, have_u}) mbar_init(b, ROW_WARPS);
+        for (uint64_t* b : {have_s, have_s + 1}) mbar_init(b, ROW_WARPS / 2);
         mbar_init_fence();
         *dead = 0;
     }
@@ -488,65 +497,78 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         if (l == 0 && sent >= 0 && !mbar_wait(full + (sent & 1), (sent >> 1) & 1, wait_ns)) *dead = 1;
     } else if (warp == MMA_WARP) {
         // ---- products ---------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t ID_N128 = umma_idesc_bf16_f32(128, 128), ID_N64 = umma_idesc_bf16_f32(128, C),
-                               ID_S = umma_idesc_bf16_f32(128, D, false, true);
+        {
+            auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+                wait(bar, parity);
+                __syncwarp();
+                tc_fence_after_sync();
+            };
+            constexpr uint32_t ID_T = umma_idesc_bf16_f32(128, C), ID_S = umma_idesc_bf16_f32(128, D / 2, false, true);
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
-                wait(full + st, (c >> 1) & 1);
-                wait(have_s, par);
-                if (c > 0) wait(done_o, par ^ 1);        // (U's halves were read out of COL_Z)
-                tc_fence_after_sync();
-                // [S K^T | S Q^T]
+                wait_warp(full + st, (c >> 1) & 1);
+                if (c > 0) wait_warp(done_o, par ^ 1);   // (U's halves were read out of COL_Z)
+                // S K^T, from the columns of S as they come
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    wait_warp(have_s + half, par);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const int ks = half * (D / 32) + e;
+                        const uint64_t b = umma_desc_kmajor(kq + ks * 256, 128, ROWS_D);
+                        umma_ta(tmem + COL_Z, tmem + COL_SH + 8 * ks, b, ID_T, ks > 0 ? 1u : 0u);
+                        umma_ta(tmem + COL_Z, tmem + COL_SL + 8 * ks, b, ID_T, 1u);
+                    }
+                }
+                umma_done(done_z);
+                // S Q^T, while the rows work on Z
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t b = umma_desc_kmajor(kq + ks * 256, 128, ROWS_D);
-                    umma_ta(tmem + COL_Z, tmem + COL_SH + 8 * ks, b, ID_N128, ks > 0 ? 1u : 0u);
-                    umma_ta(tmem + COL_Z, tmem + COL_SL + 8 * ks, b, ID_N128, 1u);
+                    const uint64_t b = umma_desc_kmajor(kq + TILE_X + ks * 256, 128, ROWS_D);
+                    umma_ta(tmem + COL_QS, tmem + COL_SH + 8 * ks, b, ID_T, ks > 0 ? 1u : 0u);
+                    umma_ta(tmem + COL_QS, tmem + COL_SL + 8 * ks, b, ID_T, 1u);
                 }
-                umma_commit(done_z);
-                wait(have_z, par);
-                tc_fence_after_sync();
+                wait_warp(have_z, par);
                 // (beta Z)^T T^T: hi hi, hi lo, lo hi
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks) {
                     const uint64_t hi = umma_desc_kmajor(pr + PREP_T + ks * 256, 128, ROWS_C);
                     const uint64_t lo = umma_desc_kmajor(pr + PREP_T + TILE_T + ks * 256, 128, ROWS_C);
                     const uint32_t z = tmem + COL_W + 16 * ks;
-                    umma_ta(tmem + COL_Z, z, hi, ID_N64, ks > 0 ? 1u : 0u);
-                    umma_ta(tmem + COL_Z, z, lo, ID_N64, 1u);
-                    umma_ta(tmem + COL_Z, z + 8, hi, ID_N64, 1u);
+                    umma_ta(tmem + COL_Z, z, hi, ID_T, ks > 0 ? 1u : 0u);
+                    umma_ta(tmem + COL_Z, z, lo, ID_T, 1u);
+                    umma_ta(tmem + COL_Z, z + 8, hi, ID_T, 1u);
                 }
-                umma_commit(done_r);
-                wait(have_w, par);
-                tc_fence_after_sync();
-                // S += (e^{g_C - g} U)^T K
+                umma_done(done_r);
+                wait_warp(have_w, par);
+                // S += (e^{g_C - g} U)^T K, in two halves of its columns
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks) {
-                    const uint64_t b = umma_desc_mnmajor(kq + ks * 2 * ROWS_D, ROWS_D, 128);
-                    umma_ta(tmem + COL_S, tmem + COL_W + 16 * ks, b, ID_S, 1u);
-                    umma_ta(tmem + COL_S, tmem + COL_W + 16 * ks + 8, b, ID_S, 1u);
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks) {
+                        const uint64_t b = umma_desc_mnmajor(kq + ks * 2 * ROWS_D + half * (D / 16) * 128, ROWS_D, 128);
+                        umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks, b, ID_S, 1u);
+                        umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks + 8, b, ID_S, 1u);
+                    }
+                    umma_done(done_s + half);
                 }
-                umma_commit(done_s);
-                wait(have_u, par);
-                tc_fence_after_sync();
+                wait_warp(have_u, par);
                 // U^T P^T
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks) {
                     const uint64_t hi = umma_desc_kmajor(pr + PREP_P + ks * 256, 128, ROWS_C);
                     const uint64_t lo = umma_desc_kmajor(pr + PREP_P + TILE_T + ks * 256, 128, ROWS_C);
                     const uint32_t u = tmem + COL_Z + 16 * ks;
-                    umma_ta(tmem + COL_O, u, hi, ID_N64, ks > 0 ? 1u : 0u);
-                    umma_ta(tmem + COL_O, u, lo, ID_N64, 1u);
-                    umma_ta(tmem + COL_O, u + 8, hi, ID_N64, 1u);
+                    umma_ta(tmem + COL_O, u, hi, ID_T, ks > 0 ? 1u : 0u);
+                    umma_ta(tmem + COL_O, u, lo, ID_T, 1u);
+                    umma_ta(tmem + COL_O, u + 8, hi, ID_T, 1u);
                 }
-                umma_commit(done_o);
-                umma_commit(empty + st);
+                umma_done(done_o);
+                umma_done(empty + st);
             }
             if (!mbar_wait(done_o, (chunks - 1) & 1, wait_ns)) *dead = 1;   // nor does a product
         }
-        __syncwarp();
     } else {
         // ---- rows -------------------------------------------------------------------
         const int q4 = warp & 3, part = warp >> 2, i = 32 * q4 + lane;
@@ -592,7 +614,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             }
         };
         auto read_qs = [&](int c) {                      // (the last use of its stage)
-            wait_warp(done_s, c & 1);
+            wait_warp(done_s + (part >> 1), c & 1);
             float2 eg[8];
             tmem_get16(tl + COL_QS + tb, qs);
             get16(reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + ST_PREP + PREP_GATES) + tb, eg);
@@ -625,7 +647,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                     tmem_put16(tl + COL_S + cb + 16 * p, x);
                 }
             }
-            arrive(have_s);
+            arrive(have_s + (part >> 1));
             if (c > 0) finish(c - 1);
             float2 z[8], b[8];
             get_column(reinterpret_cast<const __nv_bfloat16*>(stage + ST_V) + tb * D + i, z);
