@@ -12,6 +12,7 @@
 // T and P need no state: delta_prep_kernel makes them for all chunks side by
 // side, and delta_chunk_kernel walks a head's chunks with four products each.
 #include <type_traits>
+#include <utility>
 
 #include "delta_device.cuh"
 #include "delta_tc.h"
@@ -19,6 +20,7 @@
 #include "kdn_device.cuh"
 #include "kdn_internal.h"
 #include "kernel_setup.h"
+#include "sum_rows.cuh"
 
 namespace kdn {
 namespace delta {
@@ -42,8 +44,13 @@ __host__ __device__ constexpr int at_c(int r, int c8) { return (r / 8) * ROWS_C 
 // What the preparation leaves of a chunk, as the walk reads it.
 constexpr int PREP_T = 0;                    // T hi, lo
 constexpr int PREP_P = 2 * TILE_T;           // P hi, lo
-constexpr int PREP_GATES = 4 * TILE_T;       // e^g, e^{g_C - g}, beta: [3][64] fp32, then e^{g_C}
-constexpr int PREP_BYTES = PREP_GATES + 1024;
+constexpr int PREP_GATES = 4 * TILE_T;       // fp32: five rows of 64 and e^{g_C}
+constexpr int G_E = 0, G_W = C, G_BETA = 2 * C, G_HI = 3 * C, G_LO = 4 * C, G_END = 5 * C;   // e^g, e^{g_C - g}, beta, log2 e . g
+constexpr int PREP_BYTES = PREP_GATES + 1408;
+// What the backward's walks leave of a chunk beside it: a state (S before the
+// chunk, or its adjoint D behind it) as [i][j] bf16 halves, hi then lo, and the
+// rows R and Y as [i][t], hi in columns 0-63 and lo in columns 64-127.
+constexpr int STATE_BYTES = 2 * D * D * 2, ROWS_BYTES = D * 2 * C * 2;
 
 // x as bf16 pairs hi + lo: hi rounded to nearest, lo what is left, rounded:
 // within 2^-17 of x, and 2^-20 in the mean.
@@ -77,6 +84,15 @@ __device__ __forceinline__ void load_kq(uint32_t tile, const __nv_bfloat16* k, c
         const int r = (w >> 2) * 8 + a, c8 = (w & 3) * 4 + b, t = r & (C - 1);
         const __nv_bfloat16* src = (r < C ? k : q) + (t < n ? static_cast<long long>(t) * D : 0) + c8 * 8;
         copy16_or_zero(tile + at_d(r, c8), src, t < n);
+    }
+}
+
+// The same of one tensor: 64 rows.
+__device__ __forceinline__ void load_tile(uint32_t tile, const __nv_bfloat16* x, int n, int tid, int threads) {
+    const int lane = tid & 31, a = lane & 7, b = lane >> 3;
+    for (int w = tid >> 5; w < C / 8 * 4; w += threads >> 5) {
+        const int t = (w >> 2) * 8 + a, c8 = (w & 3) * 4 + b;
+        copy16_or_zero(tile + at_d(t, c8), x + (t < n ? static_cast<long long>(t) * D : 0) + c8 * 8, t < n);
     }
 }
 
@@ -203,11 +219,13 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
             gh[t] = static_cast<float>(g[e]);
             gl[t] = static_cast<float>(g[e] - gh[t]);
             sb[t] = b[e];
-            gates[t] = exp2f(static_cast<float>(g[e]));
-            gates[C + t] = exp2f(static_cast<float>(end - g[e]));
-            gates[2 * C + t] = b[e];
+            gates[G_E + t] = exp2f(static_cast<float>(g[e]));
+            gates[G_W + t] = exp2f(static_cast<float>(end - g[e]));
+            gates[G_BETA + t] = b[e];
+            gates[G_HI + t] = gh[t];
+            gates[G_LO + t] = gl[t];
         }
-        if (lane == 0) gates[3 * C] = exp2f(static_cast<float>(end));
+        if (lane == 0) gates[G_END] = exp2f(static_cast<float>(end));
     }
     copies_done();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -325,7 +343,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
 // warps: with eight, two to a scheduler, their dependent steps took 1.6 times
 // as long (a chunk 7900 cycles).
 constexpr int ROW_WARPS = 16, MMA_WARP = ROW_WARPS, LOAD_WARPS = 2, CH_THREADS = (ROW_WARPS + 1 + LOAD_WARPS) * 32;
-// shared memory: two stages of [k; q], v and the prepared chunk
+// shared memory: two stages of [k; q], v (backward: do) and the prepared chunk
 constexpr int ST_V = 2 * TILE_X, ST_PREP = ST_V + TILE_X, STAGE_BYTES = ST_PREP + PREP_BYTES;
 constexpr int CH_OFF_BAR = 2 * STAGE_BYTES, CH_SMEM = CH_OFF_BAR + 128;
 static_assert(CH_SMEM <= 227 * 1024, "shared memory");
@@ -361,6 +379,14 @@ __device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64
         "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// ... the same with A in shared memory.
+__device__ __forceinline__ void umma_sa(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void umma_done(uint64_t* bar) {
@@ -417,8 +443,59 @@ __device__ __forceinline__ void get_column(const __nv_bfloat16* p, float2 (&x)[8
                            __uint_as_float(static_cast<uint32_t>(u[(2 * e + 1) * D]) << 16));
 }
 
-template <typename TO>
-__global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, long long wait_ns) {
+// n chunks' tiles of k, q and x (v, or do), by the loading warps; `backwards`:
+// the last chunk first.
+__device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full, uint64_t* empty, const Waits& wait,
+                                            const __nv_bfloat16* k, const __nv_bfloat16* q, const __nv_bfloat16* x,
+                                            const char* prep, long long prep_step, int len, int chunks, bool backwards,
+                                            int l) {
+    int sent = -1;                                   // the last one whose copies were issued
+    for (int n = 0; n < chunks; ++n) {
+        const int c = backwards ? chunks - 1 - n : n, st = n & 1, m = min(C, len - c * C);
+        if (n >= 2) wait(empty + st, ((n >> 1) - 1) & 1);
+        if (*wait.dead) break;
+        sent = n;
+        unsigned char* stage = smem + st * STAGE_BYTES;
+        const long long row = static_cast<long long>(c) * C * D;
+        if (l == 0) {
+            mbar_arrive_expect_tx(full + st, PREP_BYTES + (backwards ? 0 : m * D * 2));
+            bulk_g2s(stage + ST_PREP, prep + c * prep_step, PREP_BYTES, full + st);
+            if (!backwards) bulk_g2s(stage + ST_V, x + row, m * D * 2, full + st);
+        }
+        load_kq(smem_addr(stage), k + row, q + row, m, l, LOAD_WARPS * 32);
+        if (backwards) {
+            load_tile(smem_addr(stage + ST_V), x + row, m, l, LOAD_WARPS * 32);   // (an operand: in core matrices)
+        } else {
+            // rows as they are; no token: zeros, not what lay there before
+            for (int e = l; e < (C - m) * (D / 8); e += LOAD_WARPS * 32)
+                *reinterpret_cast<uint4*>(stage + ST_V + m * D * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        copies_done();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(full + st);
+    }
+    // no copy outlives the CTA
+    if (l == 0 && sent >= 0 && !mbar_wait(full + (sent & 1), (sent >> 1) & 1, wait.limit)) *wait.dead = 1;
+}
+
+// Halves of 16 columns of row i, columns c8 * 8 and on, of a kept tile.
+__device__ __forceinline__ void keep_halves(char* hi_at, char* lo_at, const uint32_t (&hi)[8], const uint32_t (&lo)[8]) {
+    *reinterpret_cast<uint4*>(hi_at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(hi_at + 128) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+    *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(lo_at + 128) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+}
+
+// A walk's kept tiles; null in a forward call.
+struct KeepTiles {
+    char* states;      // STATE_BYTES a chunk
+    char* rows;        // ROWS_BYTES a chunk
+};
+
+// KEEP: no outputs, but the state before each chunk and R.
+template <typename TO, bool KEEP>
+__global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, const KeepTiles keep,
+                                                                    long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);   // [2] a stage is here
     uint64_t* empty = full + 2;                                        // [2] a stage is read
@@ -441,7 +518,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     const float* S0 = a.S0 ? a.S0 + sr * size : nullptr;
     float* final_state = a.final_state ? a.final_state + sr * size : nullptr;
     if (chunks == 0) {
-        if (final_state)
+        if (!KEEP && final_state)
             for (int i = tid; i < size / 4; i += CH_THREADS)
                 reinterpret_cast<float4*>(final_state)[i] =
                     S0 ? reinterpret_cast<const float4*>(S0)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -467,34 +544,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
 
     if (warp > MMA_WARP) {
         // ---- tiles ------------------------------------------------------------------
-        const int l = tid - (MMA_WARP + 1) * 32;
-        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + tok * D;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + tok * D;
-        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + tok * D;
-        const char* mine = prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES);
-        int sent = -1;                                   // the last chunk whose copies were issued
-        for (int c = 0; c < chunks; ++c) {
-            const int st = c & 1, m = min(C, len - c * C);
-            if (c >= 2) wait(empty + st, ((c >> 1) - 1) & 1);
-            if (*dead) break;
-            sent = c;
-            unsigned char* stage = smem + st * STAGE_BYTES;
-            const long long row = static_cast<long long>(c) * C * D;
-            if (l == 0) {
-                mbar_arrive_expect_tx(full + st, m * D * 2 + PREP_BYTES);
-                bulk_g2s(stage + ST_V, v + row, m * D * 2, full + st);
-                bulk_g2s(stage + ST_PREP, mine + c * static_cast<long long>(a.H) * PREP_BYTES, PREP_BYTES, full + st);
-            }
-            load_kq(smem_addr(stage), k + row, q + row, m, l, LOAD_WARPS * 32);
-            // no token: zeros, not what lay there before
-            for (int e = l; e < (C - m) * (D / 8); e += LOAD_WARPS * 32)
-                *reinterpret_cast<uint4*>(stage + ST_V + m * D * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-            copies_done();
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(full + st);
-        }
-        // no copy outlives the CTA
-        if (l == 0 && sent >= 0 && !mbar_wait(full + (sent & 1), (sent >> 1) & 1, wait_ns)) *dead = 1;
+        const long long step = static_cast<long long>(a.H) * PREP_BYTES;
+        load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
+                    static_cast<const __nv_bfloat16*>(a.q) + tok * D, static_cast<const __nv_bfloat16*>(a.v) + tok * D,
+                    prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, false,
+                    tid - (MMA_WARP + 1) * 32);
     } else if (warp == MMA_WARP) {
         // ---- products ---------------------------------------------------------------
         {
@@ -508,7 +562,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 const int st = c & 1;
                 const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
                 wait_warp(full + st, (c >> 1) & 1);
-                if (c > 0) wait_warp(done_o, par ^ 1);   // (U's halves were read out of COL_Z)
+                if (!KEEP && c > 0) wait_warp(done_o, par ^ 1);   // (U's halves were read out of COL_Z)
                 // S K^T, from the columns of S as they come
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -524,7 +578,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 umma_done(done_z);
                 // S Q^T, while the rows work on Z
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
+                for (int ks = 0; ks < (KEEP ? 0 : D / 16); ++ks) {
                     const uint64_t b = umma_desc_kmajor(kq + TILE_X + ks * 256, 128, ROWS_D);
                     umma_ta(tmem + COL_QS, tmem + COL_SH + 8 * ks, b, ID_T, ks > 0 ? 1u : 0u);
                     umma_ta(tmem + COL_QS, tmem + COL_SL + 8 * ks, b, ID_T, 1u);
@@ -553,6 +607,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                     }
                     umma_done(done_s + half);
                 }
+                if (KEEP) {
+                    umma_done(empty + st);
+                    continue;
+                }
                 wait_warp(have_u, par);
                 // U^T P^T
 #pragma unroll
@@ -567,7 +625,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 umma_done(done_o);
                 umma_done(empty + st);
             }
-            if (!mbar_wait(done_o, (chunks - 1) & 1, wait_ns)) *dead = 1;   // nor does a product
+            if (!mbar_wait(KEEP ? done_s + 1 : done_o, (chunks - 1) & 1, wait_ns)) *dead = 1;   // nor does a product
         }
     } else {
         // ---- rows -------------------------------------------------------------------
@@ -615,6 +673,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         };
         auto read_qs = [&](int c) {                      // (the last use of its stage)
             wait_warp(done_s + (part >> 1), c & 1);
+            if (KEEP) return;
             float2 eg[8];
             tmem_get16(tl + COL_QS + tb, qs);
             get16(reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + ST_PREP + PREP_GATES) + tb, eg);
@@ -628,11 +687,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             const uint32_t par = c & 1;
             unsigned char* stage = smem + st * STAGE_BYTES;
             const float* eg = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES) + tb;
-            const float *ew = eg + C, *be = ew + C;
+            const float *ew = eg + G_W, *be = eg + G_BETA;
             if (c > 0) read_qs(c - 1);
             wait_warp(full + st, (c >> 1) & 1);
             {   // the state's halves, and its decay over the chunk in place
-                const float end = *(reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES) + 3 * C);
+                const float end = *(reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES) + G_END);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     float2 x[8];
@@ -640,6 +699,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
+                    if (KEEP) {
+                        char* to = keep.states + ((sp.slot + c) * a.H + h) * STATE_BYTES + at_d(i, (cb + 16 * p) / 8);
+                        keep_halves(to, to + D * D * 2, hi, lo);
+                    }
                     tmem_st8w(tl + COL_SH + (cb + 16 * p) / 2, hi);
                     tmem_st8w(tl + COL_SL + (cb + 16 * p) / 2, lo);
 #pragma unroll
@@ -648,7 +711,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 }
             }
             arrive(have_s + (part >> 1));
-            if (c > 0) finish(c - 1);
+            if (!KEEP && c > 0) finish(c - 1);
             float2 z[8], b[8];
             get_column(reinterpret_cast<const __nv_bfloat16*>(stage + ST_V) + tb * D + i, z);
             get16(be, b);
@@ -673,18 +736,30 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 tmem_get16(tl + COL_Z + tb, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    z[e] = __fmul2_rn(b[e], __fadd2_rn(z[e], x[e]));
-                    x[e] = __fmul2_rn(w[e], z[e]);
+                    z[e] = __fadd2_rn(z[e], x[e]);
+                    x[e] = __fmul2_rn(w[e], __fmul2_rn(b[e], z[e]));
                 }
                 put_halves(tl + COL_W + tb, x);
                 arrive(have_w);
-                put_halves(tl + COL_Z + tb, z);
-                arrive(have_u);
+                if (KEEP) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) halves(z[e], hi[e], lo[e]);
+                    char* to = keep.rows + ((sp.slot + c) * a.H + h) * ROWS_BYTES + at_d(i, tb / 8);
+                    keep_halves(to, to + (C / 8) * 128, hi, lo);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty + st);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] = __fmul2_rn(b[e], z[e]);
+                    put_halves(tl + COL_Z + tb, z);
+                    arrive(have_u);
+                }
             }
         }
         read_qs(chunks - 1);
-        finish(chunks - 1);
-        if (final_state) {
+        if (!KEEP) finish(chunks - 1);
+        if (!KEEP && final_state) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 float2 x[8];
@@ -705,6 +780,639 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     if (tid == 0 && *dead) record_error(&g_delta_error, KDN_ERR_TIMEOUT);
 }
 
+// ---- the adjoint's walk --------------------------------------------------------
+
+// D, the adjoint of the state behind a chunk, walks to the chunk before it:
+//     dU = P^T dO + e^{g_C - g} (K D^T),   Y = dU + T^T (beta dU),   L = beta Y,
+//     D' = e^{g_C} D + dO^T (e^g Q) - L^T (e^g K),
+// with the forward's shape (D for S, dU for Z, Y for R).  P^T dO and dO^T (e^g
+// Q) do not wait for D.  dV = L; D (behind the chunk) and Y are kept.
+constexpr uint32_t COL_P = 320, COL_X = 384;   // P^T dO, and the halves of e^g dO
+
+__global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const DeltaArgs a, const char* prep, const KeepTiles keep,
+                                                                      long long wait_ns) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);
+    uint64_t* empty = full + 2;
+    uint64_t* done_z = empty + 2;                                      // products: K D^T (and P^T dO), T^T beta dU, D
+    uint64_t* done_r = done_z + 1;
+    uint64_t* done_s = done_r + 1;                                     // [2]
+    uint64_t* have_s = done_s + 2;                                     // operands: D [2], e^g dO, beta dU, L
+    uint64_t* have_x = have_s + 2;
+    uint64_t* have_z = have_x + 1;
+    uint64_t* have_w = have_z + 1;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(have_w + 1);
+    volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long sr = blockIdx.x, n = sr / a.H;
+    const int h = static_cast<int>(sr % a.H);
+    const Span sp = span_of(a, n);
+    const int len = max(sp.hi - sp.lo, 0), chunks = (len + C - 1) / C;
+    const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(D) * D;
+    const float* D1 = a.grad_final_state ? a.grad_final_state + sr * size : nullptr;
+    float* D0 = a.grad_S0 ? a.grad_S0 + sr * size : nullptr;
+    if (chunks == 0) {
+        if (D0)
+            for (int i = tid; i < size / 4; i += CH_THREADS)
+                reinterpret_cast<float4*>(D0)[i] =
+                    D1 ? reinterpret_cast<const float4*>(D1)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(full + s, LOAD_WARPS * 32 + 1);
+            mbar_init(empty + s, 1 + ROW_WARPS);
+        }
+        for (uint64_t* b : {done_z, done_r, done_s, done_s + 1}) mbar_init(b, 1);
+        for (uint64_t* b : {have_x, have_z, have_w}) mbar_init(b, ROW_WARPS);
+        for (uint64_t* b : {have_s, have_s + 1}) mbar_init(b, ROW_WARPS / 2);
+        mbar_init_fence();
+        *dead = 0;
+    }
+    if (warp == MMA_WARP) tmem_alloc(holder, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *holder, base = smem_addr(smem);
+    const Waits wait{dead, wait_ns};
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        wait(bar, parity);
+        __syncwarp();
+        tc_fence_after_sync();
+    };
+
+    if (warp > MMA_WARP) {
+        const long long step = static_cast<long long>(a.H) * PREP_BYTES;
+        load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
+                    static_cast<const __nv_bfloat16*>(a.q) + tok * D,
+                    static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D,
+                    prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, true,
+                    tid - (MMA_WARP + 1) * 32);
+    } else if (warp == MMA_WARP) {
+        constexpr uint32_t ID_T = umma_idesc_bf16_f32(128, C), ID_TN = umma_idesc_bf16_f32(128, C, false, true),
+                           ID_P = umma_idesc_bf16_f32(128, C, true, true), ID_S = umma_idesc_bf16_f32(128, D / 2, false, true),
+                           ID_Q = umma_idesc_bf16_f32(128, D, false, true);
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
+            wait_warp(full + st, (c >> 1) & 1);
+            // dO^T P
+#pragma unroll
+            for (int ks = 0; ks < C / 16; ++ks) {
+                const uint64_t g = umma_desc_mnmajor(kq + ST_V + ks * 2 * ROWS_D, ROWS_D, 128);
+                const uint64_t hi = umma_desc_mnmajor(pr + PREP_P + ks * 2 * ROWS_C, ROWS_C, 128);
+                const uint64_t lo = umma_desc_mnmajor(pr + PREP_P + TILE_T + ks * 2 * ROWS_C, ROWS_C, 128);
+                umma_sa(tmem + COL_P, g, hi, ID_P, ks > 0 ? 1u : 0u);
+                umma_sa(tmem + COL_P, g, lo, ID_P, 1u);
+            }
+            // D K^T
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                wait_warp(have_s + half, par);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) {
+                    const int ks = half * (D / 32) + e;
+                    const uint64_t b = umma_desc_kmajor(kq + ks * 256, 128, ROWS_D);
+                    umma_ta(tmem + COL_Z, tmem + COL_SH + 8 * ks, b, ID_T, ks > 0 ? 1u : 0u);
+                    umma_ta(tmem + COL_Z, tmem + COL_SL + 8 * ks, b, ID_T, 1u);
+                }
+            }
+            umma_done(done_z);
+            wait_warp(have_x, par);
+            // D += (e^g dO)^T Q, while the rows work on dU
+#pragma unroll
+            for (int ks = 0; ks < C / 16; ++ks) {
+                const uint64_t b = umma_desc_mnmajor(kq + TILE_X + ks * 2 * ROWS_D, ROWS_D, 128);
+                umma_ta(tmem + COL_S, tmem + COL_X + 16 * ks, b, ID_Q, 1u);
+                umma_ta(tmem + COL_S, tmem + COL_X + 16 * ks + 8, b, ID_Q, 1u);
+            }
+            wait_warp(have_z, par);
+            // (beta dU)^T T: hi hi, hi lo, lo hi
+#pragma unroll
+            for (int ks = 0; ks < C / 16; ++ks) {
+                const uint64_t hi = umma_desc_mnmajor(pr + PREP_T + ks * 2 * ROWS_C, ROWS_C, 128);
+                const uint64_t lo = umma_desc_mnmajor(pr + PREP_T + TILE_T + ks * 2 * ROWS_C, ROWS_C, 128);
+                const uint32_t z = tmem + COL_W + 16 * ks;
+                umma_ta(tmem + COL_Z, z, hi, ID_TN, ks > 0 ? 1u : 0u);
+                umma_ta(tmem + COL_Z, z, lo, ID_TN, 1u);
+                umma_ta(tmem + COL_Z, z + 8, hi, ID_TN, 1u);
+            }
+            umma_done(done_r);
+            wait_warp(have_w, par);
+            // D -= (e^g L)^T K, in two halves of its columns
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks) {
+                    const uint64_t b = umma_desc_mnmajor(kq + ks * 2 * ROWS_D + half * (D / 16) * 128, ROWS_D, 128);
+                    umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks, b, ID_S, 1u);
+                    umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks + 8, b, ID_S, 1u);
+                }
+                umma_done(done_s + half);
+            }
+            umma_done(empty + st);
+        }
+        if (!mbar_wait(done_s + 1, (chunks - 1) & 1, wait_ns)) *dead = 1;   // no product outlives the CTA
+    } else {
+        const int q4 = warp & 3, part = warp >> 2, i = 32 * q4 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+        const int cb = 32 * part, tb = 16 * part;
+        auto arrive = [&](uint64_t* bar) {
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float2 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (D1) f = *reinterpret_cast<const float4*>(D1 + static_cast<long long>(i) * D + cb + 16 * p + 2 * e);
+                x[e] = make_float2(f.x, f.y);
+                x[e + 1] = make_float2(f.z, f.w);
+            }
+            tmem_put16(tl + COL_S + cb + 16 * p, x);
+        }
+        tmem_wait_st();
+        __nv_bfloat16* gv = static_cast<__nv_bfloat16*>(a.grad_v) + tok * D + i;
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1, chunk = chunks - 1 - c;
+            const uint32_t par = c & 1;
+            const unsigned char* stage = smem + st * STAGE_BYTES;
+            const float* gates = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
+            const long long slot = (sp.slot + chunk) * a.H + h;
+            if (c > 0) wait_warp(done_s + (part >> 1), par ^ 1);
+            wait_warp(full + st, (c >> 1) & 1);
+            {
+                const float end = gates[G_END];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    float2 x[8];
+                    tmem_get16(tl + COL_S + cb + 16 * p, x);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
+                    tmem_st8w(tl + COL_SH + (cb + 16 * p) / 2, hi);
+                    tmem_st8w(tl + COL_SL + (cb + 16 * p) / 2, lo);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(x[e], make_float2(end, end));
+                    tmem_put16(tl + COL_S + cb + 16 * p, x);
+                    char* to = keep.states + slot * STATE_BYTES + at_d(i, (cb + 16 * p) / 8);
+                    keep_halves(to, to + D * D * 2, hi, lo);
+                }
+            }
+            arrive(have_s + (part >> 1));
+            float2 g[8], z[8], x[8];
+            {
+                const unsigned char* go = stage + ST_V + at_d(tb, i / 8) + (i % 8) * 2;
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    const float v = __uint_as_float(
+                        static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(go + (t / 8) * ROWS_D + (t % 8) * 16)) << 16);
+                    if (t & 1) z[t / 2].y = v;
+                    else z[t / 2].x = v;
+                }
+                get16(gates + G_E + tb, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = __fmul2_rn(z[e], g[e]);
+                put_halves(tl + COL_X + tb, z);
+                arrive(have_x);
+            }
+            float2 b[8];
+            get16(gates + G_BETA + tb, b);
+            {   // du = P^T dO + e^{g_C - g} K D^T
+                get16(gates + G_W + tb, g);
+                wait_warp(done_z, par);
+                tmem_get16(tl + COL_P + tb, z);
+                tmem_get16(tl + COL_Z + tb, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    z[e] = __ffma2_rn(g[e], x[e], z[e]);
+                    x[e] = __fmul2_rn(b[e], z[e]);
+                }
+                put_halves(tl + COL_W + tb, x);
+                arrive(have_z);
+            }
+            get16(gates + G_E + tb, g);
+            {   // y = du + T^T (beta du), l = beta y
+                wait_warp(done_r, par);
+                tmem_get16(tl + COL_Z + tb, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    z[e] = __fadd2_rn(z[e], x[e]);
+                    b[e] = __fmul2_rn(b[e], z[e]);
+                    x[e] = __fmul2_rn(make_float2(-g[e].x, -g[e].y), b[e]);
+                }
+                put_halves(tl + COL_W + tb, x);
+                arrive(have_w);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + st);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) halves(z[e], hi[e], lo[e]);
+                char* to = keep.rows + slot * ROWS_BYTES + at_d(i, tb / 8);
+                keep_halves(to, to + (C / 8) * 128, hi, lo);
+                const int m = len - chunk * C - tb;
+                __nv_bfloat16* dst = gv + (static_cast<long long>(chunk) * C + tb) * D;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(b[e].x);
+                    if (2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(b[e].y);
+                }
+            }
+        }
+        if (D0) {
+            wait_warp(done_s + (part >> 1), (chunks - 1) & 1);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float2 x[8];
+                tmem_get16(tl + COL_S + cb + 16 * p, x);
+                float* dst = D0 + static_cast<long long>(i) * D + cb + 16 * p;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+                    *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(x[e].x, x[e].y, x[e + 1].x, x[e + 1].y);
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && *dead) record_error(&g_delta_error, KDN_ERR_TIMEOUT);
+}
+
+// ---- the gradients of a chunk ----------------------------------------------------
+
+// A CTA makes one chunk's gradients of one head from its tiles and the walks'
+// kept ones (see delta_scan.cu for the formulas), transposed: a thread of a row
+// warp is a column j of d_k, its registers are tokens.  With u = beta R and l =
+// beta Y the products use R and Y as they are kept, and beta, E and the signs
+// come in with the sums:
+//     [s x t]  R dO^T, R Y^T -> dP^T, dG^T (E, masks) and dbeta_t = R_t . Y_t,
+//     [j x t]  S0^T dO^T, S0^T Y^T, K^T dP^T, K^T dG^T -> dq, dk as a reader,
+//     [j x s]  Q^T dP + K^T dG, D1^T R^T -> dk as a writer.
+// Every kept operand is a pair of bf16 halves (three products of two such, two
+// with an input): the gradient of A is a sum over all tokens in fp32, which one
+// half alone would leave with 10^-3.
+constexpr int GR_WARPS = 16, GR_THREADS = GR_WARPS * 32 + 32;
+constexpr int GR_KQ = 0, GR_DO = 2 * TILE_X, GR_R = GR_DO + TILE_X, GR_Y = GR_R + ROWS_BYTES, GR_S = GR_Y + ROWS_BYTES,
+              GR_P = GR_S + STATE_BYTES, GR_MISC = GR_P + 2 * C * 2 * C * 2;
+// fp32: the gates, c of each lane quarter, k.(...) of each, row warps' sums
+constexpr int GR_GATES = GR_MISC, GR_C = GR_GATES + 5 * C * 4 + 16, GR_F = GR_C + 4 * C * 4, GR_SUM = GR_F + 4 * C * 4,
+              GR_BAR = GR_SUM + GR_WARPS * 4, GR_SMEM = GR_BAR + 128;
+static_assert(GR_SMEM <= 227 * 1024, "shared memory");
+constexpr uint32_t CG_A = 0, CG_Q = 128, CG_R = 192, CG_W = 256, CG_W2 = 320, CG_Q2 = 384;   // (CG_Q2: dq, then dk)
+
+// Sums over the lanes of 16 values each: lane l holds value l % 16's (both
+// halves of a warp the same).
+__device__ __forceinline__ float lane_sums(float (&v)[16], int lane) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int e = 0; e < o; ++e) {
+            const float mine = up ? v[e + o] : v[e], other = up ? v[e] : v[e + o];
+            v[e] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
+struct GradTiles {
+    const char* prep;
+    const char* states;
+    const char* adjoints;
+    const char* r;
+    const char* y;
+    float* sum_A;           // [slots,H] or null
+};
+
+__global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const DeltaArgs a, const GradTiles in, long long wait_ns) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    float* gates = reinterpret_cast<float*>(smem + GR_GATES);
+    float* sc = reinterpret_cast<float*>(smem + GR_C);
+    float* sf = reinterpret_cast<float*>(smem + GR_F);
+    float* ssum = reinterpret_cast<float*>(smem + GR_SUM);
+    uint64_t* in_ry = reinterpret_cast<uint64_t*>(smem + GR_BAR);   // kept rows, S0, D1 are here
+    uint64_t* in_s = in_ry + 1;
+    uint64_t* in_d = in_s + 1;
+    uint64_t* done_a = in_d + 1;                                       // products
+    uint64_t* done_b = done_a + 1;
+    uint64_t* done_c = done_b + 1;
+    uint64_t* done_d = done_c + 1;
+    uint64_t* have_p = done_d + 1;                                     // dP, dG are written; S0 is read
+    uint64_t* have_dot = have_p + 1;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(have_dot + 1);
+    volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = static_cast<int>(blockIdx.x % a.H);
+    const long long slot = blockIdx.x / a.H, tile = blockIdx.x;
+    long long n, row;
+    int t0, m;
+    if (!chunk_of(a, slot, &n, &t0, &m, &row)) {
+        if (in.sum_A && tid == 0) in.sum_A[tile] = 0.f;
+        return;
+    }
+    const long long tok = (row * a.H + h) * a.T + t0;
+    const char* adjoint = in.adjoints + tile * STATE_BYTES;
+    if (tid == 0) {
+        for (uint64_t* b : {in_ry, in_s, in_d, done_a, done_b, done_c, done_d}) mbar_init(b, 1);
+        mbar_init(have_p, GR_WARPS / 2);
+        mbar_init(have_dot, GR_WARPS);
+        mbar_init_fence();
+        *dead = 0;
+        mbar_arrive_expect_tx(in_ry, 2 * ROWS_BYTES);
+        bulk_g2s(smem + GR_R, in.r + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
+        bulk_g2s(smem + GR_Y, in.y + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
+        mbar_arrive_expect_tx(in_s, STATE_BYTES);
+        bulk_g2s(smem + GR_S, in.states + tile * STATE_BYTES, STATE_BYTES, in_s);
+    }
+    if (warp == GR_WARPS) {
+        tmem_alloc(holder, 512);
+    } else {
+        const __nv_bfloat16* go = static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D;
+        load_kq(smem_addr(smem + GR_KQ), static_cast<const __nv_bfloat16*>(a.k) + tok * D,
+                static_cast<const __nv_bfloat16*>(a.q) + tok * D, m, tid, GR_WARPS * 32);
+        load_tile(smem_addr(smem + GR_DO), go, m, tid, GR_WARPS * 32);
+        const float* g = reinterpret_cast<const float*>(in.prep + tile * PREP_BYTES + PREP_GATES);
+        if (tid <= G_END) gates[tid] = g[tid];
+        copies_done();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *holder, base = smem_addr(smem);
+    const Waits wait{dead, wait_ns};
+    auto wait_warp = [&](uint64_t* bar) {
+        wait(bar, 0);
+        __syncwarp();
+        tc_fence_after_sync();
+    };
+    if (warp == GR_WARPS) {
+        constexpr uint32_t ID_AK = umma_idesc_bf16_f32(128, C, true, false), ID_AN = umma_idesc_bf16_f32(128, C, true, true),
+                           ID_A2 = umma_idesc_bf16_f32(128, 2 * C, true, true);
+        auto rows_of = [&](int off, int ks, int lo) {                  // a K step of kept rows' or K's tile, MN-major
+            return umma_desc_mnmajor(base + off + ks * 2 * ROWS_D + lo * (C / 8) * 128, ROWS_D, 128);
+        };
+        wait_warp(in_ry);
+        // [s x t]: R dO^T, R Y^T (rows 64-127 are of no use)
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t rh = rows_of(GR_R, ks, 0), rl = rows_of(GR_R, ks, 1);
+            const uint64_t g = umma_desc_kmajor(base + GR_DO + ks * 256, 128, ROWS_D);
+            const uint64_t yh = rows_of(GR_Y, ks, 0), yl = rows_of(GR_Y, ks, 1);
+            umma_sa(tmem + CG_A, rh, g, ID_AK, ks > 0 ? 1u : 0u);
+            umma_sa(tmem + CG_A, rl, g, ID_AK, 1u);
+            umma_sa(tmem + CG_A + C, rh, yh, ID_AN, ks > 0 ? 1u : 0u);
+            umma_sa(tmem + CG_A + C, rh, yl, ID_AN, 1u);
+            umma_sa(tmem + CG_A + C, rl, yh, ID_AN, 1u);
+        }
+        umma_done(done_a);
+        wait_warp(in_s);
+        // [j x t]: S0^T dO^T, S0^T Y^T
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t sh = rows_of(GR_S, ks, 0), sl = rows_of(GR_S + D * D * 2, ks, 0);
+            const uint64_t g = umma_desc_kmajor(base + GR_DO + ks * 256, 128, ROWS_D);
+            const uint64_t yh = rows_of(GR_Y, ks, 0), yl = rows_of(GR_Y, ks, 1);
+            umma_sa(tmem + CG_Q, sh, g, ID_AK, ks > 0 ? 1u : 0u);
+            umma_sa(tmem + CG_Q, sl, g, ID_AK, 1u);
+            umma_sa(tmem + CG_R, sh, yh, ID_AN, ks > 0 ? 1u : 0u);
+            umma_sa(tmem + CG_R, sh, yl, ID_AN, 1u);
+            umma_sa(tmem + CG_R, sl, yh, ID_AN, 1u);
+        }
+        umma_done(done_b);
+        wait_warp(have_p);
+        // [j x t]: K^T [dP^T | dG^T];  [j x s]: Q^T dP + K^T dG
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks) {
+            const uint64_t k = rows_of(GR_KQ, ks, 0);
+            umma_sa(tmem + CG_Q2, k, rows_of(GR_P, ks, 0), ID_A2, ks > 0 ? 1u : 0u);
+            umma_sa(tmem + CG_Q2, k, rows_of(GR_P + C * 2 * C * 2, ks, 0), ID_A2, 1u);
+        }
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks) {
+            const uint64_t k = rows_of(GR_KQ, ks, 0), q = rows_of(GR_KQ + TILE_X, ks, 0);
+#pragma unroll
+            for (int lo = 0; lo < 2; ++lo) {
+                const uint32_t p = base + GR_P + lo * C * 2 * C * 2 + ks * 256;
+                umma_sa(tmem + CG_W2, q, umma_desc_kmajor(p, 128, ROWS_D), ID_AK, ks > 0 || lo > 0 ? 1u : 0u);
+                umma_sa(tmem + CG_W2, k, umma_desc_kmajor(p + (C / 8) * 128, 128, ROWS_D), ID_AK, 1u);
+            }
+        }
+        umma_done(done_c);
+        wait_warp(done_b);
+        wait_warp(have_dot);
+        const bool more = *dead == 0;
+        if (lane == 0 && more) {
+            mbar_arrive_expect_tx(in_d, STATE_BYTES);
+            bulk_g2s(smem + GR_S, adjoint, STATE_BYTES, in_d);
+        }
+        __syncwarp();
+        wait_warp(in_d);
+        // [j x s]: D1^T R^T
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t dh = rows_of(GR_S, ks, 0), dl = rows_of(GR_S + D * D * 2, ks, 0);
+            const uint64_t rh = rows_of(GR_R, ks, 0), rl = rows_of(GR_R, ks, 1);
+            umma_sa(tmem + CG_W, dh, rh, ID_AN, ks > 0 ? 1u : 0u);
+            umma_sa(tmem + CG_W, dh, rl, ID_AN, 1u);
+            umma_sa(tmem + CG_W, dl, rh, ID_AN, 1u);
+        }
+        umma_done(done_d);
+        // neither a copy nor a product outlives the CTA
+        bool ok = mbar_wait(done_d, 0, wait_ns);
+        ok = mbar_wait(in_ry, 0, wait_ns) && mbar_wait(in_s, 0, wait_ns) && ok;
+        if (lane == 0 && more) ok = mbar_wait(in_d, 0, wait_ns) && ok;
+        if (!ok) *dead = 1;
+    } else {
+        const int q4 = warp & 3, part = warp >> 2, tb = 16 * part;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+        if (q4 < 2) {   // dP^T, dG^T: row s, 32 tokens of one of the two
+            const int s = 32 * q4 + lane, which = part >> 1, tc = 32 * (part & 1);
+            const float sh = gates[G_HI + s], sl = gates[G_LO + s], bs = gates[G_BETA + s];
+            wait_warp(done_a);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int t1 = tc + 16 * p;
+                float2 x[8], gh[8], gl[8], gb[8];
+                tmem_get16(tl + CG_A + which * C + t1, x);
+                get16(gates + G_HI + t1, gh);
+                get16(gates + G_LO + t1, gl);
+                get16(gates + G_BETA + t1, gb);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int t = t1 + 2 * e;
+                    if (which == 1) {   // R_s . Y_s
+                        if (t == s && s < m) static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[e].x);
+                        if (t + 1 == s && s < m) static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[e].y);
+                        x[e] = __fmul2_rn(x[e], make_float2(-gb[e].x, -gb[e].y));
+                    }
+                    const int first = which == 1 ? s + 1 : s;
+                    const float w0 = bs * ex2((gh[e].x - sh) + (gl[e].x - sl)), w1 = bs * ex2((gh[e].y - sh) + (gl[e].y - sl));
+                    x[e].x = t >= first ? x[e].x * w0 : 0.f;
+                    x[e].y = t + 1 >= first ? x[e].y * w1 : 0.f;
+                    halves(x[e], hi[e], lo[e]);
+                }
+                char* to = reinterpret_cast<char*>(smem) + GR_P + at_d(s, which * (C / 8) + t1 / 8);
+                keep_halves(to, to + C * 2 * C * 2, hi, lo);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(have_p);
+        }
+        // <S0, D1>: the thread's row of both, D1 from memory
+        {
+            wait_warp(in_s);
+            const int i = tid >> 2, c = (tid & 3) * 4;       // row, its 4 of 16 pieces
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int off = at_d(i, c + e);
+                const uint4 xh = *reinterpret_cast<const uint4*>(smem + GR_S + off);
+                const uint4 xl = *reinterpret_cast<const uint4*>(smem + GR_S + D * D * 2 + off);
+                const uint4 yh = *reinterpret_cast<const uint4*>(adjoint + off);
+                const uint4 yl = *reinterpret_cast<const uint4*>(adjoint + D * D * 2 + off);
+                const uint32_t X[4] = {xh.x, xh.y, xh.z, xh.w}, XL[4] = {xl.x, xl.y, xl.z, xl.w};
+                const uint32_t Y[4] = {yh.x, yh.y, yh.z, yh.w}, YL[4] = {yl.x, yl.y, yl.z, yl.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    dot = fmaf(__uint_as_float(X[w] << 16) + __uint_as_float(XL[w] << 16),
+                               __uint_as_float(Y[w] << 16) + __uint_as_float(YL[w] << 16), dot);
+                    dot = fmaf(__uint_as_float(X[w] & 0xffff0000u) + __uint_as_float(XL[w] & 0xffff0000u),
+                               __uint_as_float(Y[w] & 0xffff0000u) + __uint_as_float(YL[w] & 0xffff0000u), dot);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (lane == 0) {
+                ssum[warp] = dot;
+                mbar_arrive(have_dot);
+            }
+        }
+        const int j = 32 * q4 + lane;
+        float cc[16];
+        float2 kr[8], kj[8];
+        {
+            float2 x[8], y[8], g[8];
+            const unsigned char* at = smem + GR_KQ + at_d(tb, j / 8) + (j % 8) * 2;
+            auto column = [&](const unsigned char* p, float2 (&v)[8]) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    const float f = __uint_as_float(
+                        static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(p + (t / 8) * ROWS_D + (t % 8) * 16)) << 16);
+                    if (t & 1) v[t / 2].y = f;
+                    else v[t / 2].x = f;
+                }
+            };
+            get16(gates + G_E + tb, g);
+            wait_warp(done_b);
+            tmem_get16(tl + CG_Q + tb, x);
+            wait_warp(done_c);
+            tmem_get16(tl + CG_Q2 + tb, y);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_q) + (tok + tb) * D + j;
+            column(at + TILE_X, kj);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] = __ffma2_rn(g[e], x[e], y[e]);
+                if (tb + 2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(y[e].x);
+                if (tb + 2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(y[e].y);
+                cc[2 * e] = kj[e].x * y[e].x;
+                cc[2 * e + 1] = kj[e].y * y[e].y;
+            }
+            tmem_get16(tl + CG_R + tb, x);
+            tmem_get16(tl + CG_Q2 + C + tb, y);
+            float2 b[8];
+            get16(gates + G_BETA + tb, b);
+            column(at, kj);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                kr[e] = __ffma2_rn(__fmul2_rn(make_float2(-g[e].x, -g[e].y), b[e]), x[e], y[e]);
+                cc[2 * e] = fmaf(kj[e].x, kr[e].x, cc[2 * e]);
+                cc[2 * e + 1] = fmaf(kj[e].y, kr[e].y, cc[2 * e + 1]);
+            }
+        }
+        {
+            float2 x[8], y[8], g[8], b[8];
+            float f[16];
+            get16(gates + G_W + tb, g);
+            get16(gates + G_BETA + tb, b);
+            tmem_get16(tl + CG_W2 + tb, y);
+            wait_warp(done_d);
+            tmem_get16(tl + CG_W + tb, x);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_k) + (tok + tb) * D + j;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = __fmul2_rn(__fmul2_rn(g[e], b[e]), x[e]);
+                f[2 * e] = kj[e].x * x[e].x;
+                f[2 * e + 1] = kj[e].y * x[e].y;
+                x[e] = __fadd2_rn(x[e], y[e]);
+                cc[2 * e] = fmaf(-kj[e].x, x[e].x, cc[2 * e]);
+                cc[2 * e + 1] = fmaf(-kj[e].y, x[e].y, cc[2 * e + 1]);
+                x[e] = __fadd2_rn(x[e], kr[e]);
+                if (tb + 2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(x[e].x);
+                if (tb + 2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(x[e].y);
+            }
+            const float c1 = lane_sums(cc, lane), f1 = lane_sums(f, lane);
+            if (lane < 16) {
+                sc[q4 * C + tb + lane] = c1;
+                sf[q4 * C + tb + lane] = f1;
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == GR_WARPS) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+    if (warp == 0) {
+        // gradients of the log decays: sums from the chunk's end
+        float c[2], f = 0.f, x = lane < GR_WARPS ? ssum[lane] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            c[e] = (sc[t] + sc[C + t]) + (sc[2 * C + t] + sc[3 * C + t]);
+            f += (sf[t] + sf[C + t]) + (sf[2 * C + t] + sf[3 * C + t]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            f += __shfl_xor_sync(0xffffffffu, f, o);
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+        }
+        float s = c[0] + c[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float z = __shfl_down_sync(0xffffffffu, s, o);
+            if (lane + o < 32) s += z;
+        }
+        const float rest = fmaf(gates[G_END], x, f);
+        const float ga[2] = {s + rest, (s - c[0]) + rest};
+        const float A = a.A[h];
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            if (t < m) {
+                static_cast<__nv_bfloat16*>(a.grad_d)[tok + t] = __float2bfloat16_rn(-A * ga[e]);
+                sum = fmaf(-to_f32(static_cast<const __nv_bfloat16*>(a.d)[tok + t]), ga[e], sum);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) {
+            if (in.sum_A) in.sum_A[tile] = sum;
+            if (*dead) record_error(&g_delta_error, KDN_ERR_TIMEOUT);
+        }
+    }
+}
+
 }  // namespace
 
 bool tc_takes(int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
@@ -721,10 +1429,44 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     if (e != cudaSuccess) return from_cuda(e);
     delta_prep_kernel<<<static_cast<unsigned>(blocks), PREP_THREADS, P_SMEM, stream>>>(a, ws, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
-    auto kernel = a.out_dtype == KDN_BF16 ? delta_chunk_kernel<__nv_bfloat16> : delta_chunk_kernel<float>;
+    auto kernel = a.out_dtype == KDN_BF16 ? delta_chunk_kernel<__nv_bfloat16, false> : delta_chunk_kernel<float, false>;
     if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
-    kernel<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, ws, wait_ns);
+    kernel<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, ws, KeepTiles{}, wait_ns);
     return from_cuda(cudaGetLastError());
+}
+
+namespace {
+long long rounded(long long bytes) { return (bytes + 255) / 256 * 256; }
+}  // namespace
+
+long long tc_bwd_bytes(int B, int H, int T, int nseq) {
+    const long long tiles = slots_of(B, T, nseq) * H;
+    return tiles * (PREP_BYTES + 2 * STATE_BYTES + 2 * ROWS_BYTES) + rounded(tiles * 4);
+}
+
+kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long wait_ns) {
+    const long long slots = slots_of(a.B, a.T, a.nseq), tiles = slots * a.H;
+    const long long rows = static_cast<long long>(a.offsets ? a.nseq : a.B) * a.H;
+    if (tiles > 0x7fffffffLL || rows > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
+    char* prep = ws;
+    const KeepTiles fwd{prep + tiles * PREP_BYTES, prep + tiles * (PREP_BYTES + 2 * STATE_BYTES)};
+    const KeepTiles bwd{fwd.states + tiles * STATE_BYTES, fwd.rows + tiles * ROWS_BYTES};
+    float* shares = reinterpret_cast<float*>(bwd.rows + tiles * ROWS_BYTES);
+    auto walk = delta_chunk_kernel<float, true>;
+    const std::pair<const void*, int> kernels[] = {{reinterpret_cast<const void*>(delta_prep_kernel), P_SMEM},
+                                                   {reinterpret_cast<const void*>(walk), CH_SMEM},
+                                                   {reinterpret_cast<const void*>(delta_adjoint_kernel), CH_SMEM},
+                                                   {reinterpret_cast<const void*>(delta_tc_grad_kernel), GR_SMEM}};
+    cudaError_t e = cudaSuccess;
+    for (const auto& k : kernels)
+        if ((e = allow_smem(k.first, k.second)) != cudaSuccess) return from_cuda(e);
+    delta_prep_kernel<<<static_cast<unsigned>(tiles), PREP_THREADS, P_SMEM, stream>>>(a, prep, wait_ns);
+    walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, fwd, wait_ns);
+    delta_adjoint_kernel<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, bwd, wait_ns);
+    delta_tc_grad_kernel<<<static_cast<unsigned>(tiles), GR_THREADS, GR_SMEM, stream>>>(
+        a, GradTiles{prep, fwd.states, bwd.states, fwd.rows, bwd.rows, a.grad_A ? shares : nullptr}, wait_ns);
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.grad_A) return from_cuda(e);
+    return from_cuda(sum_rows(shares, slots, a.H, a.grad_A, nullptr, a.H, stream));
 }
 
 }  // namespace delta
