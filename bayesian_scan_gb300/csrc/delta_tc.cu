@@ -10,9 +10,22 @@
 //     O = e^g Q S^T + P U,
 //     S' = e^{g_C} S + U^T (e^{g_C - g} K).
 // T and P need no state: delta_prep_kernel makes them for all chunks side by
-// side, and delta_chunk_kernel walks a head's chunks with four products each.
+// side, and delta_chunk_kernel walks a head's chunks with five products each.
+//
+// Precision.  The inputs are bf16 and the results as exact as fp32 arithmetic
+// makes them: every other operand is a pair of fp16 numbers hi + lo (22 bits;
+// two products with an input, three of two such pairs, fp32 sums in tensor
+// memory).  Pairs of bf16 would keep 16 bits at the same cost; the state was
+// then 3e-6 off, and the gradient of A, a sum over all tokens whose chunks'
+// errors add up, up to 8e-5.  fp16 has 5 bits of exponent, so operands are
+// scaled by exact powers of two, undone where the fp32 sums are read: inputs
+// and the chunk's T and P by one for their tile, Z, U and S by one for each
+// state row, from the row's largest magnitude (rows do not touch one another,
+// whatever their sizes).  An element is exact to 2^-38 of the largest.
 #include <type_traits>
 #include <utility>
+
+#include <cuda_fp16.h>
 
 #include "delta_device.cuh"
 #include "delta_tc.h"
@@ -44,23 +57,50 @@ __host__ __device__ constexpr int at_c(int r, int c8) { return (r / 8) * ROWS_C 
 // What the preparation leaves of a chunk, as the walk reads it.
 constexpr int PREP_T = 0;                    // T hi, lo
 constexpr int PREP_P = 2 * TILE_T;           // P hi, lo
-constexpr int PREP_GATES = 4 * TILE_T;       // fp32: five rows of 64 and e^{g_C}
-constexpr int G_E = 0, G_W = C, G_BETA = 2 * C, G_HI = 3 * C, G_LO = 4 * C, G_END = 5 * C;   // e^g, e^{g_C - g}, beta, log2 e . g
+constexpr int PREP_GATES = 4 * TILE_T;       // fp32: five rows of 64, then single values
+constexpr int G_E = 0, G_W = C, G_BETA = 2 * C, G_HI = 3 * C, G_LO = 4 * C;   // e^g, e^{g_C - g}, beta, log2 e . g
+// e^{g_C}; the power of two that k, q, do are scaled with (UP) and those that undo scales (DN)
+constexpr int G_END = 5 * C, G_KUP = G_END + 1, G_KDN = G_END + 2, G_QUP = G_END + 3, G_QDN = G_END + 4, G_XUP = G_END + 5,
+              G_XDN = G_END + 6, G_TDN = G_END + 7, G_PDN = G_END + 8, G_ALL = G_END + 9;
 constexpr int PREP_BYTES = PREP_GATES + 1408;
-// What the backward's walks leave of a chunk beside it: a state (S before the
-// chunk, or its adjoint D behind it) as [i][j] bf16 halves, hi then lo, and the
-// rows R and Y as [i][t], hi in columns 0-63 and lo in columns 64-127.
-constexpr int STATE_BYTES = 2 * D * D * 2, ROWS_BYTES = D * 2 * C * 2;
+static_assert(G_ALL * 4 <= 1408, "the gates' room");
+// What the backward's walks leave of a chunk beside it, fp32: a state (S before
+// the chunk, or its adjoint D behind it) as [i][j] and the rows R and Y as
+// [i][t]; four columns of all 128 rows i, then the next four.
+constexpr int STATE_BYTES = D * D * 4, ROWS_BYTES = D * C * 4;
+__host__ __device__ constexpr int at_f(int i, int c4) { return c4 * D * 16 + i * 16; }
 
-// x as bf16 pairs hi + lo: hi rounded to nearest, lo what is left, rounded:
-// within 2^-17 of x, and 2^-20 in the mean.
+// x as fp16 pairs hi + lo: hi rounded to nearest, lo what is left, rounded:
+// within 2^-22 of x (2^-25 where lo is subnormal).
 __device__ __forceinline__ void halves(float2 x, uint32_t& hi, uint32_t& lo) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    const __half2 h = __float22half2_rn(x);
     hi = *reinterpret_cast<const uint32_t*>(&h);
-    const float2 up = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
-    const float2 d = __ffma2_rn(up, make_float2(-1.f, -1.f), x);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(d.x, d.y);
+    const float2 d = __ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), x);
+    const __half2 l = __float22half2_rn(d);
     lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// The power of two that brings the largest magnitude m to [2^13, 2^14), and its
+// inverse.  (What is below 2^-113 counts as that; infinities stay infinite.)
+__device__ __forceinline__ void scale_of(float m, float& up, float& down) {
+    const uint32_t e = max(__float_as_uint(m) >> 23, 14u);
+    up = __uint_as_float((267u - e) << 23);
+    down = __uint_as_float((e - 13u) << 23);
+}
+// ... of an input's tile: at most 2^60, so that products of two stay floats.
+__device__ __forceinline__ void input_scale(float m, float& up, float& down) {
+    scale_of(fmaxf(m, 0x1p-47f), up, down);
+    if (m != m) up = m;                      // (NaN: what its chunk gives is)
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float largest(float m, const float2 (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+    return m;
+}
+// The instruction descriptor's types: fp16 operands where the bf16 form has bf16's bits.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn = false, bool b_mn = false) {
+    return umma_idesc_bf16_f32(m, n, a_mn, b_mn) & ~((7u << 7) | (7u << 10));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -96,6 +136,38 @@ __device__ __forceinline__ void load_tile(uint32_t tile, const __nv_bfloat16* x,
     }
 }
 
+// The same 16-byte pieces from bf16 to fp16, in their place, times a power of
+// two: by the thread that copied them, when they are here.
+__device__ __forceinline__ void to_half(unsigned char* piece, float up) {
+    uint4 w = *reinterpret_cast<const uint4*>(piece);
+    uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u));
+        const __half2 h = __float22half2_rn(__fmul2_rn(f, both(up)));
+        u[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(piece) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void kq_to_half(unsigned char* tile, float k_up, float q_up, int tid, int threads) {
+    const int lane = tid & 31, a = lane & 7, b = lane >> 3;
+    for (int w = tid >> 5; w < 2 * C / 8 * 4; w += threads >> 5) {
+        const int r = (w >> 2) * 8 + a;
+        to_half(tile + at_d(r, (w & 3) * 4 + b), r < C ? k_up : q_up);
+    }
+}
+__device__ __forceinline__ void tile_to_half(unsigned char* tile, float up, int tid, int threads) {
+    const int lane = tid & 31, a = lane & 7, b = lane >> 3;
+    for (int w = tid >> 5; w < C / 8 * 4; w += threads >> 5) to_half(tile + at_d((w >> 2) * 8 + a, (w & 3) * 4 + b), up);
+}
+// The largest magnitude of 8 bf16 numbers, as bits of two.
+__device__ __forceinline__ uint32_t largest_bf16(uint32_t m, uint4 w) {
+    m = __vmaxu2(m, w.x & 0x7fff7fffu);
+    m = __vmaxu2(m, w.y & 0x7fff7fffu);
+    m = __vmaxu2(m, w.z & 0x7fff7fffu);
+    return __vmaxu2(m, w.w & 0x7fff7fffu);
+}
+
 // ---- preparation -------------------------------------------------------------
 
 constexpr int PREP_THREADS = 128;
@@ -103,7 +175,7 @@ constexpr int LG = C + 4, LX = 36;           // a row of G, T and of X in shared
 // G (then T, block by block in its place), N = G beta and X lie where k and q
 // lay before the product: five CTAs to an SM hide one another's waits.
 constexpr int P_OFF_KQ = 0, P_OFF_G = 0, P_OFF_N = P_OFF_G + C * LG * 4, P_OFF_X = P_OFF_N + C * LG * 4,
-              P_OFF_GATE = P_OFF_X + 32 * LX * 4, P_SMEM = P_OFF_GATE + 3 * C * 4 + 64;
+              P_OFF_GATE = P_OFF_X + 32 * LX * 4, P_SMEM = P_OFF_GATE + 3 * C * 4 + 128;
 static_assert(P_OFF_GATE >= 2 * TILE_X, "the gates lie behind k and q");
 
 // acc[r] += sum_s A[r * RS][s] B[s] for R rows and 4 columns: A's rows in shared
@@ -173,6 +245,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     float* sb = gl + C;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P_OFF_GATE + 3 * C * 4);
     uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 1);
+    uint32_t* tops = holder + 1;                                 // [4 warps][k, q, do], then [4] of T
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = static_cast<int>(blockIdx.x % a.H);
     const long long slot = blockIdx.x / a.H;
@@ -227,12 +300,26 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
         }
         if (lane == 0) gates[G_END] = exp2f(static_cast<float>(end));
     }
+    uint32_t top[3] = {0u, 0u, 0u};
+    if (a.grad_out) {
+        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D);
+        for (int i = tid; i < m * (D / 8); i += PREP_THREADS) top[2] = largest_bf16(top[2], g[i]);
+    }
     copies_done();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *holder, base = smem_addr(smem);
+    for (int i = tid; i < C * (D / 8); i += PREP_THREADS) {
+        top[0] = largest_bf16(top[0], *reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16));
+        top[1] = largest_bf16(top[1], *reinterpret_cast<const uint4*>(smem + P_OFF_KQ + TILE_X + i * 16));
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+        const uint32_t x = __reduce_max_sync(0xffffffffu, max(top[e] >> 16, top[e] & 0xffffu));
+        if (lane == 0) tops[3 * warp + e] = x;
+    }
     if (tid == 0) {
         constexpr uint32_t IDESC = umma_idesc_bf16_f32(128, C);
 #pragma unroll
@@ -243,7 +330,23 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
         umma_commit(bar);
     }
     const bool ok = mbar_wait(bar, 0, wait_ns);
+    __syncthreads();   // the magnitudes are here, and the product is done: k and q may be overwritten
     tc_fence_after_sync();
+    float ups[3], downs[3];
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        input_scale(__uint_as_float(max(max(tops[e], tops[3 + e]), max(tops[6 + e], tops[9 + e])) << 16), ups[e], downs[e]);
+    // |P| <= 128 max|k| max|q|: scaled by both and by 2^-21 it is below 2^14
+    const float p_up = ups[0] * ups[1] * 0x1p-21f;
+    if (tid == 0) {
+        float* gates = reinterpret_cast<float*>(out + PREP_GATES);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            gates[G_KUP + 2 * e] = ups[e];
+            gates[G_KDN + 2 * e] = downs[e];
+        }
+        gates[G_PDN] = downs[0] * downs[1] * 0x1p21f;
+    }
     {   // row tid: K K^T of token tid, or Q K^T of token tid - 64
         const int t = tid & (C - 1);
         const bool reads = tid < C;          // k_t reads the state before its token, q_t the one after
@@ -285,7 +388,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
                 for (int e = 0; e < 32; e += 8) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) halves(make_float2(x[e + 2 * p], x[e + 2 * p + 1]), hi[p], lo[p]);
+                    for (int p = 0; p < 4; ++p) halves(make_float2(p_up * x[e + 2 * p], p_up * x[e + 2 * p + 1]), hi[p], lo[p]);
                     const int off = PREP_P + at_c(t, 4 * half + e / 8);
                     *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(out + off + TILE_T) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -320,14 +423,30 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     __syncthreads();
     join_blocks<16>(sG, sN, reinterpret_cast<float*>(smem + P_OFF_X), sb);
     join_blocks<32>(sG, sN, reinterpret_cast<float*>(smem + P_OFF_X), sb);
-    for (int i = tid; i < C * (C / 8); i += PREP_THREADS) {
-        const int t = i & (C - 1), c8 = i / C;
-        uint32_t hi[4], lo[4];
+    float2 x[4][4];
+    float most = 0.f;
+#pragma unroll
+    for (int n4 = 0; n4 < 4; ++n4) {
+        const int i = tid + n4 * PREP_THREADS, t = i & (C - 1), c8 = i / C;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const int s = 8 * c8 + 2 * p;
-            halves(*reinterpret_cast<const float2*>(sG + t * LG + s), hi[p], lo[p]);
+            x[n4][p] = *reinterpret_cast<const float2*>(sG + t * LG + 8 * c8 + 2 * p);
+            most = fmaxf(most, fmaxf(fabsf(x[n4][p].x), fabsf(x[n4][p].y)));
         }
+    }
+    static_assert(C * (C / 8) == 4 * PREP_THREADS, "four pieces a thread");
+    const uint32_t warp_most = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    if (lane == 0) tops[12 + warp] = warp_most;
+    __syncthreads();
+    float up, down;
+    scale_of(__uint_as_float(max(max(tops[12], tops[13]), max(tops[14], tops[15]))), up, down);
+    if (tid == 0) reinterpret_cast<float*>(out + PREP_GATES)[G_TDN] = down;
+#pragma unroll
+    for (int n4 = 0; n4 < 4; ++n4) {
+        const int i = tid + n4 * PREP_THREADS, t = i & (C - 1), c8 = i / C;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) halves(__fmul2_rn(x[n4][p], both(up)), hi[p], lo[p]);
         const int off = PREP_T + at_c(t, c8);
         *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(out + off + TILE_T) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -338,18 +457,21 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
 // ---- the walk ------------------------------------------------------------------
 
 // Warps 0-15 work on the state's rows (thread = row i = lane of tensor memory,
-// warp / 4 = quarter of the columns and of the tokens), warp 16 issues the
-// products, warps 17 and 18 bring the tiles, one chunk ahead.  Sixteen row
-// warps: with eight, two to a scheduler, their dependent steps took 1.6 times
-// as long (a chunk 7900 cycles).
-constexpr int ROW_WARPS = 16, MMA_WARP = ROW_WARPS, LOAD_WARPS = 2, CH_THREADS = (ROW_WARPS + 1 + LOAD_WARPS) * 32;
-// shared memory: two stages of [k; q], v (backward: do) and the prepared chunk
+// warp / 4 = quarter of the columns and of the tokens); a thread's 32 columns of
+// S stay in its registers.  Warp 16 issues the products, warps 17-19 bring the
+// tiles, one chunk ahead.  Sixteen row warps: with eight, two to a scheduler,
+// their dependent steps took 1.6 times as long.
+constexpr int ROW_WARPS = 16, MMA_WARP = ROW_WARPS, LOAD_WARPS = 3, CH_THREADS = (ROW_WARPS + 1 + LOAD_WARPS) * 32;
+// shared memory: two stages of [k; q], v (backward: do) and the prepared chunk;
+// two arrays of the rows' largest magnitudes, one value of each quarter
 constexpr int ST_V = 2 * TILE_X, ST_PREP = ST_V + TILE_X, STAGE_BYTES = ST_PREP + PREP_BYTES;
-constexpr int CH_OFF_BAR = 2 * STAGE_BYTES, CH_SMEM = CH_OFF_BAR + 128;
-static_assert(CH_SMEM <= 227 * 1024, "shared memory");
-// tensor memory: S (fp32) and its bf16 halves as packed pairs (an A operand's
-// layout), the accumulators of Z (then of R, then U's halves) and of Q S^T, of
-// P U, and the halves of beta Z (then of e^{g_C - g} U)
+constexpr int CH_OFF_TOP = 2 * STAGE_BYTES, CH_OFF_BAR = CH_OFF_TOP + 2 * 4 * D * 4, CH_SMEM = CH_OFF_BAR + 192;
+// ... and the adjoint's e^g do, hi and lo
+constexpr int AD_OFF_X = (CH_SMEM + 127) / 128 * 128, AD_SMEM = AD_OFF_X + 2 * D * C * 2;
+static_assert(AD_SMEM <= 227 * 1024, "shared memory");
+// tensor memory: the chunk's share of S (fp32) and the halves of S as packed
+// pairs (an A operand's layout), the accumulators of Z (then of R, then U's
+// halves), of Q S^T and of P U, and the halves of beta Z (then of e^{g_C - g} U)
 constexpr uint32_t COL_S = 0, COL_SH = 128, COL_SL = 192, COL_Z = 256, COL_QS = 320, COL_O = 384, COL_W = 448;
 
 // Waits that end: the first that runs out marks the CTA, and the others return
@@ -370,6 +492,9 @@ struct Waits {
     }
 };
 
+// Issue by a whole warp, whose values are all uniform: one thread of it is
+// elected for the instruction.  (Out of a branch of one lane each operand went
+// through vector registers, and a product took 56 cycles to issue.)
 // Issue by a whole warp, whose values are all uniform: one thread of it is
 // elected for the instruction.  (Out of a branch of one lane each operand went
 // through vector registers, and a product took 56 cycles to issue.)
@@ -408,23 +533,6 @@ __device__ __forceinline__ void tmem_get16(uint32_t taddr, float2 (&x)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = make_float2(v[2 * e], v[2 * e + 1]);
 }
-__device__ __forceinline__ void tmem_put16(uint32_t taddr, const float2 (&x)[8]) {
-    float v[16];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        v[2 * e] = x[e].x;
-        v[2 * e + 1] = x[e].y;
-    }
-    tmem_st16(taddr, v);
-}
-// The halves of 16 tokens' values, one K step: hi in 8 columns, lo in the 8 behind them.
-__device__ __forceinline__ void put_halves(uint32_t taddr, const float2 (&x)[8]) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
-    tmem_st8w(taddr, hi);
-    tmem_st8w(taddr + 8, lo);
-}
 // 16 consecutive floats of shared memory (16-byte aligned).
 __device__ __forceinline__ void get16(const float* p, float2 (&x)[8]) {
 #pragma unroll
@@ -443,12 +551,41 @@ __device__ __forceinline__ void get_column(const __nv_bfloat16* p, float2 (&x)[8
                            __uint_as_float(static_cast<uint32_t>(u[(2 * e + 1) * D]) << 16));
 }
 
-// n chunks' tiles of k, q and x (v, or do), by the loading warps; `backwards`:
-// the last chunk first.
-__device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full, uint64_t* empty, const Waits& wait,
-                                            const __nv_bfloat16* k, const __nv_bfloat16* q, const __nv_bfloat16* x,
-                                            const char* prep, long long prep_step, int len, int chunks, bool backwards,
-                                            int l) {
+
+// The largest of a row's four quarters: each puts its own, and all four warps of
+// a lane quarter meet.  (Two arrays in turn: an array's readers are past it when
+// the next but one exchange writes it.)
+__device__ __forceinline__ float row_top(float* tops, float mine, int q4, int part, int i) {
+    tops[part * D + i] = mine;
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + q4) : "memory");
+    return fmaxf(fmaxf(tops[i], tops[D + i]), fmaxf(tops[2 * D + i], tops[3 * D + i]));
+}
+
+// The halves of 16 values times a power of two, one K step.
+__device__ __forceinline__ void put_scaled(uint32_t taddr, const float2 (&x)[8], float up) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) halves(__fmul2_rn(x[e], both(up)), hi[e], lo[e]);
+    tmem_st8w(taddr, hi);
+    tmem_st8w(taddr + 8, lo);
+}
+
+// Four consecutive values and more of a kept tile, from column c4 * 4 on.
+template <int N>
+__device__ __forceinline__ void keep_row(char* tile, int i, int c4, const float2* x) {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e)
+        *reinterpret_cast<float4*>(tile + at_f(i, c4 + e)) =
+            make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y);
+}
+
+// Chunks' tiles of k, q and x (v as it is; backwards, do as fp16) by the loading
+// warps, 96 threads; `backwards`: the last chunk first.
+__device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* landed, uint64_t* full, uint64_t* empty,
+                                            const Waits& wait, const __nv_bfloat16* k, const __nv_bfloat16* q,
+                                            const __nv_bfloat16* x, const char* prep, long long prep_step, int len,
+                                            int chunks, bool backwards, int l) {
+    constexpr int N = LOAD_WARPS * 32;
     int sent = -1;                                   // the last one whose copies were issued
     for (int n = 0; n < chunks; ++n) {
         const int c = backwards ? chunks - 1 - n : n, st = n & 1, m = min(C, len - c * C);
@@ -458,32 +595,28 @@ __device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full,
         unsigned char* stage = smem + st * STAGE_BYTES;
         const long long row = static_cast<long long>(c) * C * D;
         if (l == 0) {
-            mbar_arrive_expect_tx(full + st, PREP_BYTES + (backwards ? 0 : m * D * 2));
-            bulk_g2s(stage + ST_PREP, prep + c * prep_step, PREP_BYTES, full + st);
-            if (!backwards) bulk_g2s(stage + ST_V, x + row, m * D * 2, full + st);
+            mbar_arrive_expect_tx(landed + st, PREP_BYTES + (backwards ? 0 : m * D * 2));
+            bulk_g2s(stage + ST_PREP, prep + c * prep_step, PREP_BYTES, landed + st);
+            if (!backwards) bulk_g2s(stage + ST_V, x + row, m * D * 2, landed + st);
         }
-        load_kq(smem_addr(stage), k + row, q + row, m, l, LOAD_WARPS * 32);
+        load_kq(smem_addr(stage), k + row, q + row, m, l, N);
         if (backwards) {
-            load_tile(smem_addr(stage + ST_V), x + row, m, l, LOAD_WARPS * 32);   // (an operand: in core matrices)
+            load_tile(smem_addr(stage + ST_V), x + row, m, l, N);
         } else {
             // rows as they are; no token: zeros, not what lay there before
-            for (int e = l; e < (C - m) * (D / 8); e += LOAD_WARPS * 32)
+            for (int e = l; e < (C - m) * (D / 8); e += N)
                 *reinterpret_cast<uint4*>(stage + ST_V + m * D * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         copies_done();
+        wait(landed + st, (n >> 1) & 1);
+        const float* gates = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
+        kq_to_half(stage, gates[G_KUP], gates[G_QUP], l, N);
+        if (backwards) tile_to_half(stage + ST_V, gates[G_XUP], l, N);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(full + st);
     }
     // no copy outlives the CTA
-    if (l == 0 && sent >= 0 && !mbar_wait(full + (sent & 1), (sent >> 1) & 1, wait.limit)) *wait.dead = 1;
-}
-
-// Halves of 16 columns of row i, columns c8 * 8 and on, of a kept tile.
-__device__ __forceinline__ void keep_halves(char* hi_at, char* lo_at, const uint32_t (&hi)[8], const uint32_t (&lo)[8]) {
-    *reinterpret_cast<uint4*>(hi_at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(hi_at + 128) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-    *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(lo_at + 128) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+    if (l == 0 && sent >= 0 && !mbar_wait(landed + (sent & 1), (sent >> 1) & 1, wait.limit)) *wait.dead = 1;
 }
 
 // A walk's kept tiles; null in a forward call.
@@ -497,9 +630,11 @@ template <typename TO, bool KEEP>
 __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, const KeepTiles keep,
                                                                     long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
+    float* tops = reinterpret_cast<float*>(smem + CH_OFF_TOP);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);   // [2] a stage is here
     uint64_t* empty = full + 2;                                        // [2] a stage is read
-    uint64_t* done_z = empty + 2;                                      // products: Z, R, S, O
+    uint64_t* landed = empty + 2;                                      // [2] a stage's bulk copies are here
+    uint64_t* done_z = landed + 2;                                     // products: Z, R, S, O
     uint64_t* done_r = done_z + 1;
     uint64_t* done_s = done_r + 1;                                     // [2] (columns 0-63 and 64-127)
     uint64_t* done_o = done_s + 2;
@@ -516,9 +651,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     const int len = max(sp.hi - sp.lo, 0), chunks = (len + C - 1) / C;
     const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(D) * D;
     const float* S0 = a.S0 ? a.S0 + sr * size : nullptr;
-    float* final_state = a.final_state ? a.final_state + sr * size : nullptr;
+    float* final_state = !KEEP && a.final_state ? a.final_state + sr * size : nullptr;
     if (chunks == 0) {
-        if (!KEEP && final_state)
+        if (final_state)
             for (int i = tid; i < size / 4; i += CH_THREADS)
                 reinterpret_cast<float4*>(final_state)[i] =
                     S0 ? reinterpret_cast<const float4*>(S0)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -526,12 +661,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(full + s, LOAD_WARPS * 32 + 1);
+            mbar_init(full + s, LOAD_WARPS * 32);
             mbar_init(empty + s, 1 + ROW_WARPS);
+            mbar_init(landed + s, 1);
+            mbar_init(done_s + s, 1);
+            mbar_init(have_s + s, ROW_WARPS / 2);
         }
-        for (uint64_t* b : {done_z, done_r, done_s, done_s + 1, done_o}) mbar_init(b, 1);
+        for (uint64_t* b : {done_z, done_r, done_o}) mbar_init(b, 1);
         for (uint64_t* b : {have_z, have_w, have_u}) mbar_init(b, ROW_WARPS);
-        for (uint64_t* b : {have_s, have_s + 1}) mbar_init(b, ROW_WARPS / 2);
         mbar_init_fence();
         *dead = 0;
     }
@@ -541,23 +678,23 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     tc_fence_after_sync();
     const uint32_t tmem = *holder, base = smem_addr(smem);
     const Waits wait{dead, wait_ns};
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        wait(bar, parity);
+        __syncwarp();
+        tc_fence_after_sync();
+    };
 
-    if (warp > MMA_WARP) {
-        // ---- tiles ------------------------------------------------------------------
-        const long long step = static_cast<long long>(a.H) * PREP_BYTES;
-        load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
-                    static_cast<const __nv_bfloat16*>(a.q) + tok * D, static_cast<const __nv_bfloat16*>(a.v) + tok * D,
-                    prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, false,
-                    tid - (MMA_WARP + 1) * 32);
-    } else if (warp == MMA_WARP) {
-        // ---- products ---------------------------------------------------------------
-        {
-            auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-                wait(bar, parity);
-                __syncwarp();
-                tc_fence_after_sync();
-            };
-            constexpr uint32_t ID_T = umma_idesc_bf16_f32(128, C), ID_S = umma_idesc_bf16_f32(128, D / 2, false, true);
+    if (warp >= MMA_WARP) {
+        if (warp > MMA_WARP) {
+            // ---- tiles ------------------------------------------------------------------
+            const long long step = static_cast<long long>(a.H) * PREP_BYTES;
+            load_chunks(smem, landed, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
+                        static_cast<const __nv_bfloat16*>(a.q) + tok * D, static_cast<const __nv_bfloat16*>(a.v) + tok * D,
+                        prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, false,
+                        tid - (MMA_WARP + 1) * 32);
+        } else {
+            // ---- products ---------------------------------------------------------------
+            constexpr uint32_t ID_T = idesc_f16(128, C), ID_S = idesc_f16(128, D / 2, false, true);
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
@@ -596,68 +733,84 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 }
                 umma_done(done_r);
                 wait_warp(have_w, par);
-                // S += (e^{g_C - g} U)^T K, in two halves of its columns
+                // (e^{g_C - g} U)^T K, in two halves of its columns
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks) {
                         const uint64_t b = umma_desc_mnmajor(kq + ks * 2 * ROWS_D + half * (D / 16) * 128, ROWS_D, 128);
-                        umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks, b, ID_S, 1u);
+                        umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks, b, ID_S, ks > 0 ? 1u : 0u);
                         umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks + 8, b, ID_S, 1u);
                     }
                     umma_done(done_s + half);
                 }
-                if (KEEP) {
-                    umma_done(empty + st);
-                    continue;
-                }
-                wait_warp(have_u, par);
-                // U^T P^T
+                if (!KEEP) {
+                    wait_warp(have_u, par);
+                    // U^T P^T
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks) {
-                    const uint64_t hi = umma_desc_kmajor(pr + PREP_P + ks * 256, 128, ROWS_C);
-                    const uint64_t lo = umma_desc_kmajor(pr + PREP_P + TILE_T + ks * 256, 128, ROWS_C);
-                    const uint32_t u = tmem + COL_Z + 16 * ks;
-                    umma_ta(tmem + COL_O, u, hi, ID_T, ks > 0 ? 1u : 0u);
-                    umma_ta(tmem + COL_O, u, lo, ID_T, 1u);
-                    umma_ta(tmem + COL_O, u + 8, hi, ID_T, 1u);
+                    for (int ks = 0; ks < C / 16; ++ks) {
+                        const uint64_t hi = umma_desc_kmajor(pr + PREP_P + ks * 256, 128, ROWS_C);
+                        const uint64_t lo = umma_desc_kmajor(pr + PREP_P + TILE_T + ks * 256, 128, ROWS_C);
+                        const uint32_t u = tmem + COL_Z + 16 * ks;
+                        umma_ta(tmem + COL_O, u, hi, ID_T, ks > 0 ? 1u : 0u);
+                        umma_ta(tmem + COL_O, u, lo, ID_T, 1u);
+                        umma_ta(tmem + COL_O, u + 8, hi, ID_T, 1u);
+                    }
+                    umma_done(done_o);
                 }
-                umma_done(done_o);
                 umma_done(empty + st);
             }
-            if (!mbar_wait(KEEP ? done_s + 1 : done_o, (chunks - 1) & 1, wait_ns)) *dead = 1;   // nor does a product
+            if (!mbar_wait(KEEP ? done_s + 1 : done_o, (chunks - 1) & 1, wait_ns)) *dead = 1;   // no product outlives the CTA
         }
     } else {
         // ---- rows -------------------------------------------------------------------
         const int q4 = warp & 3, part = warp >> 2, i = 32 * q4 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
         const int cb = 32 * part, tb = 16 * part;        // its columns of S, its tokens
-        auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-            wait(bar, parity);
-            __syncwarp();
-            tc_fence_after_sync();
-        };
+        float* tops2 = tops + 4 * D;
         auto arrive = [&](uint64_t* bar) {
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        float2 S[2][8];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            float2 x[8];
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (S0) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * D + cb + 16 * p + 2 * e);
-                x[e] = make_float2(f.x, f.y);
-                x[e + 1] = make_float2(f.z, f.w);
+                S[p][e] = make_float2(f.x, f.y);
+                S[p][e + 1] = make_float2(f.z, f.w);
             }
-            tmem_put16(tl + COL_S + cb + 16 * p, x);
-        }
-        tmem_wait_st();
         TO* out = static_cast<TO*>(a.out) + tok * D + i;
         float2 qs[8];                                    // e^g Q S^T of the chunk before
+        float s_down = 1.f, w_down = 1.f, u_down = 1.f, end = 1.f;   // of the chunk before: what undoes the scales, e^{g_C}
+        // S of the chunk before, and (the last use of its stage) its Q S^T
+        auto take = [&](int c) {
+            wait_warp(done_s + (part >> 1), c & 1);
+            const float* gates = reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + ST_PREP + PREP_GATES);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float2 x[8];
+                tmem_get16(tl + COL_S + cb + 16 * p, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) S[p][e] = __ffma2_rn(x[e], both(w_down), __fmul2_rn(S[p][e], both(end)));
+            }
+            if (KEEP) return;
+            tmem_get16(tl + COL_QS + tb, qs);
+            const float f = s_down * gates[G_QDN];
+            u_down *= gates[G_PDN];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 g = reinterpret_cast<const float4*>(gates + G_E + tb)[e];
+                qs[2 * e] = __fmul2_rn(__fmul2_rn(qs[2 * e], both(f)), make_float2(g.x, g.y));
+                qs[2 * e + 1] = __fmul2_rn(__fmul2_rn(qs[2 * e + 1], both(f)), make_float2(g.z, g.w));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + (c & 1));
+        };
         auto finish = [&](int c) {                       // outputs of chunk c
             wait_warp(done_o, c & 1);
             float2 o[8];
@@ -666,108 +819,106 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             TO* dst = out + (static_cast<long long>(c) * C + tb) * D;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float2 y = __fadd2_rn(o[e], qs[e]);
+                const float2 y = __ffma2_rn(o[e], both(u_down), qs[e]);
                 if (2 * e < m) dst[2 * e * D] = from_f32<TO>(y.x);
                 if (2 * e + 1 < m) dst[(2 * e + 1) * D] = from_f32<TO>(y.y);
             }
-        };
-        auto read_qs = [&](int c) {                      // (the last use of its stage)
-            wait_warp(done_s + (part >> 1), c & 1);
-            if (KEEP) return;
-            float2 eg[8];
-            tmem_get16(tl + COL_QS + tb, qs);
-            get16(reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + ST_PREP + PREP_GATES) + tb, eg);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) qs[e] = __fmul2_rn(qs[e], eg[e]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + (c & 1));
         };
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
             const uint32_t par = c & 1;
             unsigned char* stage = smem + st * STAGE_BYTES;
-            const float* eg = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES) + tb;
-            const float *ew = eg + G_W, *be = eg + G_BETA;
-            if (c > 0) read_qs(c - 1);
-            wait_warp(full + st, (c >> 1) & 1);
-            {   // the state's halves, and its decay over the chunk in place
-                const float end = *(reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES) + G_END);
+            const float* gates = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
+            if (c > 0) take(c - 1);
+            float up;
+            {   // the state's halves
+                scale_of(row_top(tops, largest(largest(0.f, S[0]), S[1]), q4, part, i), up, s_down);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    float2 x[8];
-                    tmem_get16(tl + COL_S + cb + 16 * p, x);
                     uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
-                    if (KEEP) {
-                        char* to = keep.states + ((sp.slot + c) * a.H + h) * STATE_BYTES + at_d(i, (cb + 16 * p) / 8);
-                        keep_halves(to, to + D * D * 2, hi, lo);
-                    }
+                    for (int e = 0; e < 8; ++e) halves(__fmul2_rn(S[p][e], both(up)), hi[e], lo[e]);
                     tmem_st8w(tl + COL_SH + (cb + 16 * p) / 2, hi);
                     tmem_st8w(tl + COL_SL + (cb + 16 * p) / 2, lo);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(x[e], make_float2(end, end));
-                    tmem_put16(tl + COL_S + cb + 16 * p, x);
                 }
             }
             arrive(have_s + (part >> 1));
-            if (!KEEP && c > 0) finish(c - 1);
-            float2 z[8], b[8];
+            if (KEEP) {
+                char* to = keep.states + ((sp.slot + c) * a.H + h) * STATE_BYTES;
+                keep_row<8>(to, i, cb / 4, S[0]);
+                keep_row<8>(to, i, cb / 4 + 4, S[1]);
+            } else if (c > 0) {
+                finish(c - 1);
+            }
+            wait_warp(full + st, (c >> 1) & 1);
+            end = gates[G_END];
+            float2 z[8], x[8];
             get_column(reinterpret_cast<const __nv_bfloat16*>(stage + ST_V) + tb * D + i, z);
-            get16(be, b);
+            float z_down;
             {   // z = v - e^g S k
-                float2 x[8], g[8];
-                get16(eg, g);
+                const float f = -s_down * gates[G_KDN];
                 wait_warp(done_z, par);
                 tmem_get16(tl + COL_Z + tb, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = __fmul2_rn(x[e], g[e]);
-                    z[e] = __ffma2_rn(x[e], make_float2(-1.f, -1.f), z[e]);
-                    x[e] = __fmul2_rn(b[e], z[e]);
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 g = *reinterpret_cast<const float4*>(gates + G_E + tb + 2 * e);
+                    const float4 b = *reinterpret_cast<const float4*>(gates + G_BETA + tb + 2 * e);
+                    z[e] = __ffma2_rn(__fmul2_rn(x[e], both(f)), make_float2(g.x, g.y), z[e]);
+                    z[e + 1] = __ffma2_rn(__fmul2_rn(x[e + 1], both(f)), make_float2(g.z, g.w), z[e + 1]);
+                    x[e] = __fmul2_rn(make_float2(b.x, b.y), z[e]);
+                    x[e + 1] = __fmul2_rn(make_float2(b.z, b.w), z[e + 1]);
                 }
-                put_halves(tl + COL_W + tb, x);
+                scale_of(row_top(tops2, largest(0.f, x), q4, part, i), up, z_down);
+                put_scaled(tl + COL_W + tb, x, up);
                 arrive(have_z);
             }
             {   // r = z + T beta z, u = beta r
-                float2 x[8], w[8];
-                get16(ew, w);
+                const float f = z_down * gates[G_TDN];
                 wait_warp(done_r, par);
                 tmem_get16(tl + COL_Z + tb, x);
+                if (KEEP) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    z[e] = __fadd2_rn(z[e], x[e]);
-                    x[e] = __fmul2_rn(w[e], __fmul2_rn(b[e], z[e]));
+                    for (int e = 0; e < 8; ++e) z[e] = __ffma2_rn(x[e], both(f), z[e]);
+                    keep_row<8>(keep.rows + ((sp.slot + c) * a.H + h) * ROWS_BYTES, i, tb / 4, z);
                 }
-                put_halves(tl + COL_W + tb, x);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 b = *reinterpret_cast<const float4*>(gates + G_BETA + tb + 2 * e);
+                    const float4 w = *reinterpret_cast<const float4*>(gates + G_W + tb + 2 * e);
+                    if (!KEEP) {
+                        z[e] = __ffma2_rn(x[e], both(f), z[e]);
+                        z[e + 1] = __ffma2_rn(x[e + 1], both(f), z[e + 1]);
+                    }
+                    z[e] = __fmul2_rn(make_float2(b.x, b.y), z[e]);
+                    z[e + 1] = __fmul2_rn(make_float2(b.z, b.w), z[e + 1]);
+                    x[e] = __fmul2_rn(make_float2(w.x, w.y), z[e]);
+                    x[e + 1] = __fmul2_rn(make_float2(w.z, w.w), z[e + 1]);
+                }
+                scale_of(row_top(tops, largest(0.f, x), q4, part, i), up, w_down);
+                w_down *= gates[G_KDN];
+                put_scaled(tl + COL_W + tb, x, up);
                 arrive(have_w);
                 if (KEEP) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) halves(z[e], hi[e], lo[e]);
-                    char* to = keep.rows + ((sp.slot + c) * a.H + h) * ROWS_BYTES + at_d(i, tb / 8);
-                    keep_halves(to, to + (C / 8) * 128, hi, lo);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(empty + st);
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = __fmul2_rn(b[e], z[e]);
-                    put_halves(tl + COL_Z + tb, z);
+                    scale_of(row_top(tops2, largest(0.f, z), q4, part, i), up, u_down);
+                    put_scaled(tl + COL_Z + tb, z, up);
                     arrive(have_u);
                 }
             }
         }
-        read_qs(chunks - 1);
-        if (!KEEP) finish(chunks - 1);
-        if (!KEEP && final_state) {
+        if (!KEEP) {
+            take(chunks - 1);
+            finish(chunks - 1);
+        }
+        if (final_state) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float2 x[8];
-                tmem_get16(tl + COL_S + cb + 16 * p, x);
                 float* dst = final_state + static_cast<long long>(i) * D + cb + 16 * p;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
-                    *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(x[e].x, x[e].y, x[e + 1].x, x[e + 1].y);
+                    *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(S[p][e].x, S[p][e].y, S[p][e + 1].x, S[p][e + 1].y);
             }
         }
     }
@@ -786,15 +937,19 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
 //     dU = P^T dO + e^{g_C - g} (K D^T),   Y = dU + T^T (beta dU),   L = beta Y,
 //     D' = e^{g_C} D + dO^T (e^g Q) - L^T (e^g K),
 // with the forward's shape (D for S, dU for Z, Y for R).  P^T dO and dO^T (e^g
-// Q) do not wait for D.  dV = L; D (behind the chunk) and Y are kept.
-constexpr uint32_t COL_P = 320, COL_X = 384;   // P^T dO, and the halves of e^g dO
+// Q) do not wait for D.  dV = L; D (behind the chunk) and Y are kept.  P^T dO
+// lies in COL_W until beta dU's halves do; e^g dO is an operand in shared memory.
+constexpr uint32_t COL_X = 320;              // dO^T (e^g Q), 128 columns
 
 __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const DeltaArgs a, const char* prep, const KeepTiles keep,
                                                                       long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
+    float* tops = reinterpret_cast<float*>(smem + CH_OFF_TOP);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);
     uint64_t* empty = full + 2;
-    uint64_t* done_z = empty + 2;                                      // products: K D^T (and P^T dO), T^T beta dU, D
+    uint64_t* landed = empty + 2;
+    uint64_t* done_p = landed + 2;                                     // products: P^T dO, K D^T, T^T beta dU, D
+    uint64_t* done_z = done_p + 1;
     uint64_t* done_r = done_z + 1;
     uint64_t* done_s = done_r + 1;                                     // [2]
     uint64_t* have_s = done_s + 2;                                     // operands: D [2], e^g dO, beta dU, L
@@ -820,12 +975,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(full + s, LOAD_WARPS * 32 + 1);
+            mbar_init(full + s, LOAD_WARPS * 32);
             mbar_init(empty + s, 1 + ROW_WARPS);
+            mbar_init(landed + s, 1);
+            mbar_init(done_s + s, 1);
+            mbar_init(have_s + s, ROW_WARPS / 2);
         }
-        for (uint64_t* b : {done_z, done_r, done_s, done_s + 1}) mbar_init(b, 1);
+        for (uint64_t* b : {done_p, done_z, done_r}) mbar_init(b, 1);
         for (uint64_t* b : {have_x, have_z, have_w}) mbar_init(b, ROW_WARPS);
-        for (uint64_t* b : {have_s, have_s + 1}) mbar_init(b, ROW_WARPS / 2);
         mbar_init_fence();
         *dead = 0;
     }
@@ -841,198 +998,233 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
         tc_fence_after_sync();
     };
 
-    if (warp > MMA_WARP) {
-        const long long step = static_cast<long long>(a.H) * PREP_BYTES;
-        load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
-                    static_cast<const __nv_bfloat16*>(a.q) + tok * D,
-                    static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D,
-                    prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, true,
-                    tid - (MMA_WARP + 1) * 32);
-    } else if (warp == MMA_WARP) {
-        constexpr uint32_t ID_T = umma_idesc_bf16_f32(128, C), ID_TN = umma_idesc_bf16_f32(128, C, false, true),
-                           ID_P = umma_idesc_bf16_f32(128, C, true, true), ID_S = umma_idesc_bf16_f32(128, D / 2, false, true),
-                           ID_Q = umma_idesc_bf16_f32(128, D, false, true);
-        for (int c = 0; c < chunks; ++c) {
-            const int st = c & 1;
-            const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
-            wait_warp(full + st, (c >> 1) & 1);
-            // dO^T P
-#pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {
-                const uint64_t g = umma_desc_mnmajor(kq + ST_V + ks * 2 * ROWS_D, ROWS_D, 128);
-                const uint64_t hi = umma_desc_mnmajor(pr + PREP_P + ks * 2 * ROWS_C, ROWS_C, 128);
-                const uint64_t lo = umma_desc_mnmajor(pr + PREP_P + TILE_T + ks * 2 * ROWS_C, ROWS_C, 128);
-                umma_sa(tmem + COL_P, g, hi, ID_P, ks > 0 ? 1u : 0u);
-                umma_sa(tmem + COL_P, g, lo, ID_P, 1u);
-            }
-            // D K^T
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                wait_warp(have_s + half, par);
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) {
-                    const int ks = half * (D / 32) + e;
-                    const uint64_t b = umma_desc_kmajor(kq + ks * 256, 128, ROWS_D);
-                    umma_ta(tmem + COL_Z, tmem + COL_SH + 8 * ks, b, ID_T, ks > 0 ? 1u : 0u);
-                    umma_ta(tmem + COL_Z, tmem + COL_SL + 8 * ks, b, ID_T, 1u);
-                }
-            }
-            umma_done(done_z);
-            wait_warp(have_x, par);
-            // D += (e^g dO)^T Q, while the rows work on dU
-#pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {
-                const uint64_t b = umma_desc_mnmajor(kq + TILE_X + ks * 2 * ROWS_D, ROWS_D, 128);
-                umma_ta(tmem + COL_S, tmem + COL_X + 16 * ks, b, ID_Q, 1u);
-                umma_ta(tmem + COL_S, tmem + COL_X + 16 * ks + 8, b, ID_Q, 1u);
-            }
-            wait_warp(have_z, par);
-            // (beta dU)^T T: hi hi, hi lo, lo hi
-#pragma unroll
-            for (int ks = 0; ks < C / 16; ++ks) {
-                const uint64_t hi = umma_desc_mnmajor(pr + PREP_T + ks * 2 * ROWS_C, ROWS_C, 128);
-                const uint64_t lo = umma_desc_mnmajor(pr + PREP_T + TILE_T + ks * 2 * ROWS_C, ROWS_C, 128);
-                const uint32_t z = tmem + COL_W + 16 * ks;
-                umma_ta(tmem + COL_Z, z, hi, ID_TN, ks > 0 ? 1u : 0u);
-                umma_ta(tmem + COL_Z, z, lo, ID_TN, 1u);
-                umma_ta(tmem + COL_Z, z + 8, hi, ID_TN, 1u);
-            }
-            umma_done(done_r);
-            wait_warp(have_w, par);
-            // D -= (e^g L)^T K, in two halves of its columns
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
+    if (warp >= MMA_WARP) {
+        if (warp > MMA_WARP) {
+            const long long step = static_cast<long long>(a.H) * PREP_BYTES;
+            load_chunks(smem, landed, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
+                        static_cast<const __nv_bfloat16*>(a.q) + tok * D,
+                        static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D,
+                        prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, true,
+                        tid - (MMA_WARP + 1) * 32);
+        } else {
+            constexpr uint32_t ID_T = idesc_f16(128, C), ID_TN = idesc_f16(128, C, false, true),
+                               ID_P = idesc_f16(128, C, true, true), ID_S = idesc_f16(128, D / 2, false, true),
+                               ID_Q = idesc_f16(128, D, false, true);
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1;
+                const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
+                wait_warp(full + st, (c >> 1) & 1);
+                if (c > 0) wait_warp(done_s + 1, par ^ 1);   // (L's halves were read out of COL_W)
+                // dO^T P
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks) {
-                    const uint64_t b = umma_desc_mnmajor(kq + ks * 2 * ROWS_D + half * (D / 16) * 128, ROWS_D, 128);
-                    umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks, b, ID_S, 1u);
-                    umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks + 8, b, ID_S, 1u);
+                    const uint64_t g = umma_desc_mnmajor(kq + ST_V + ks * 2 * ROWS_D, ROWS_D, 128);
+                    const uint64_t hi = umma_desc_mnmajor(pr + PREP_P + ks * 2 * ROWS_C, ROWS_C, 128);
+                    const uint64_t lo = umma_desc_mnmajor(pr + PREP_P + TILE_T + ks * 2 * ROWS_C, ROWS_C, 128);
+                    umma_sa(tmem + COL_W, g, hi, ID_P, ks > 0 ? 1u : 0u);
+                    umma_sa(tmem + COL_W, g, lo, ID_P, 1u);
                 }
-                umma_done(done_s + half);
+                umma_done(done_p);
+                // D K^T
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    wait_warp(have_s + half, par);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const int ks = half * (D / 32) + e;
+                        const uint64_t b = umma_desc_kmajor(kq + ks * 256, 128, ROWS_D);
+                        umma_ta(tmem + COL_Z, tmem + COL_SH + 8 * ks, b, ID_T, ks > 0 ? 1u : 0u);
+                        umma_ta(tmem + COL_Z, tmem + COL_SL + 8 * ks, b, ID_T, 1u);
+                    }
+                }
+                umma_done(done_z);
+                wait_warp(have_x, par);
+                // (e^g dO)^T Q, while the rows work on dU
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks) {
+                    const uint64_t b = umma_desc_mnmajor(kq + TILE_X + ks * 2 * ROWS_D, ROWS_D, 128);
+                    const uint32_t x = base + AD_OFF_X + ks * 256;
+                    umma_sa(tmem + COL_X, umma_desc_kmajor(x, 128, ROWS_C), b, ID_Q, ks > 0 ? 1u : 0u);
+                    umma_sa(tmem + COL_X, umma_desc_kmajor(x + D * C * 2, 128, ROWS_C), b, ID_Q, 1u);
+                }
+                wait_warp(have_z, par);
+                // (beta dU)^T T: hi hi, hi lo, lo hi
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks) {
+                    const uint64_t hi = umma_desc_mnmajor(pr + PREP_T + ks * 2 * ROWS_C, ROWS_C, 128);
+                    const uint64_t lo = umma_desc_mnmajor(pr + PREP_T + TILE_T + ks * 2 * ROWS_C, ROWS_C, 128);
+                    const uint32_t z = tmem + COL_W + 16 * ks;
+                    umma_ta(tmem + COL_Z, z, hi, ID_TN, ks > 0 ? 1u : 0u);
+                    umma_ta(tmem + COL_Z, z, lo, ID_TN, 1u);
+                    umma_ta(tmem + COL_Z, z + 8, hi, ID_TN, 1u);
+                }
+                umma_done(done_r);
+                wait_warp(have_w, par);
+                // -(e^g L)^T K, in two halves of its columns
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks) {
+                        const uint64_t b = umma_desc_mnmajor(kq + ks * 2 * ROWS_D + half * (D / 16) * 128, ROWS_D, 128);
+                        umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks, b, ID_S, ks > 0 ? 1u : 0u);
+                        umma_ta(tmem + COL_S + half * (D / 2), tmem + COL_W + 16 * ks + 8, b, ID_S, 1u);
+                    }
+                    umma_done(done_s + half);
+                }
+                umma_done(empty + st);
             }
-            umma_done(empty + st);
+            if (!mbar_wait(done_s + 1, (chunks - 1) & 1, wait_ns)) *dead = 1;   // no product outlives the CTA
         }
-        if (!mbar_wait(done_s + 1, (chunks - 1) & 1, wait_ns)) *dead = 1;   // no product outlives the CTA
     } else {
         const int q4 = warp & 3, part = warp >> 2, i = 32 * q4 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
         const int cb = 32 * part, tb = 16 * part;
+        float* tops2 = tops + 4 * D;
         auto arrive = [&](uint64_t* bar) {
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        float2 S[2][8];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            float2 x[8];
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (D1) f = *reinterpret_cast<const float4*>(D1 + static_cast<long long>(i) * D + cb + 16 * p + 2 * e);
-                x[e] = make_float2(f.x, f.y);
-                x[e + 1] = make_float2(f.z, f.w);
+                S[p][e] = make_float2(f.x, f.y);
+                S[p][e + 1] = make_float2(f.z, f.w);
             }
-            tmem_put16(tl + COL_S + cb + 16 * p, x);
-        }
-        tmem_wait_st();
         __nv_bfloat16* gv = static_cast<__nv_bfloat16*>(a.grad_v) + tok * D + i;
+        float s_down = 1.f, x_down = 1.f, w_down = 1.f, end = 1.f;
+        auto take = [&](int c) {                         // D before what was chunk c of the walk
+            wait_warp(done_s + (part >> 1), c & 1);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float2 x[8];
+                tmem_get16(tl + COL_S + cb + 16 * p, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) S[p][e] = __ffma2_rn(x[e], both(w_down), __fmul2_rn(S[p][e], both(end)));
+                tmem_get16(tl + COL_X + cb + 16 * p, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) S[p][e] = __ffma2_rn(x[e], both(x_down), S[p][e]);
+            }
+        };
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1, chunk = chunks - 1 - c;
             const uint32_t par = c & 1;
             const unsigned char* stage = smem + st * STAGE_BYTES;
             const float* gates = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
             const long long slot = (sp.slot + chunk) * a.H + h;
-            if (c > 0) wait_warp(done_s + (part >> 1), par ^ 1);
-            wait_warp(full + st, (c >> 1) & 1);
+            if (c > 0) take(c - 1);
+            float up;
             {
-                const float end = gates[G_END];
+                scale_of(row_top(tops, largest(largest(0.f, S[0]), S[1]), q4, part, i), up, s_down);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    float2 x[8];
-                    tmem_get16(tl + COL_S + cb + 16 * p, x);
                     uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
+                    for (int e = 0; e < 8; ++e) halves(__fmul2_rn(S[p][e], both(up)), hi[e], lo[e]);
                     tmem_st8w(tl + COL_SH + (cb + 16 * p) / 2, hi);
                     tmem_st8w(tl + COL_SL + (cb + 16 * p) / 2, lo);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(x[e], make_float2(end, end));
-                    tmem_put16(tl + COL_S + cb + 16 * p, x);
-                    char* to = keep.states + slot * STATE_BYTES + at_d(i, (cb + 16 * p) / 8);
-                    keep_halves(to, to + D * D * 2, hi, lo);
                 }
             }
             arrive(have_s + (part >> 1));
-            float2 g[8], z[8], x[8];
-            {
+            keep_row<8>(keep.states + slot * STATE_BYTES, i, cb / 4, S[0]);
+            keep_row<8>(keep.states + slot * STATE_BYTES, i, cb / 4 + 4, S[1]);
+            wait_warp(full + st, (c >> 1) & 1);
+            end = gates[G_END];
+            float2 z[8], x[8];
+            {   // e^g dO
                 const unsigned char* go = stage + ST_V + at_d(tb, i / 8) + (i % 8) * 2;
+                const float f = gates[G_XDN];
 #pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    const float v = __uint_as_float(
-                        static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(go + (t / 8) * ROWS_D + (t % 8) * 16)) << 16);
-                    if (t & 1) z[t / 2].y = v;
-                    else z[t / 2].x = v;
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 g = *reinterpret_cast<const float4*>(gates + G_E + tb + 2 * e);
+                    float v[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int t = 2 * e + w;
+                        v[w] = __half2float(*reinterpret_cast<const __half*>(go + (t / 8) * ROWS_D + (t % 8) * 16));
+                    }
+                    x[e] = __fmul2_rn(make_float2(v[0] * f, v[1] * f), make_float2(g.x, g.y));
+                    x[e + 1] = __fmul2_rn(make_float2(v[2] * f, v[3] * f), make_float2(g.z, g.w));
                 }
-                get16(gates + G_E + tb, g);
+                scale_of(row_top(tops2, largest(0.f, x), q4, part, i), up, x_down);
+                x_down *= gates[G_QDN];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = __fmul2_rn(z[e], g[e]);
-                put_halves(tl + COL_X + tb, z);
-                arrive(have_x);
+                for (int e = 0; e < 8; e += 4) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) halves(__fmul2_rn(x[e + w], both(up)), hi[w], lo[w]);
+                    unsigned char* to = smem + AD_OFF_X + at_c(i, tb / 8 + e / 4);
+                    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(to + D * C * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(have_x);
             }
-            float2 b[8];
-            get16(gates + G_BETA + tb, b);
+            float z_down;
             {   // du = P^T dO + e^{g_C - g} K D^T
-                get16(gates + G_W + tb, g);
+                const float f = s_down * gates[G_KDN], fp = gates[G_XDN] * gates[G_PDN];
+                wait_warp(done_p, par);
+                tmem_get16(tl + COL_W + tb, z);
                 wait_warp(done_z, par);
-                tmem_get16(tl + COL_P + tb, z);
                 tmem_get16(tl + COL_Z + tb, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    z[e] = __ffma2_rn(g[e], x[e], z[e]);
-                    x[e] = __fmul2_rn(b[e], z[e]);
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 w = *reinterpret_cast<const float4*>(gates + G_W + tb + 2 * e);
+                    const float4 b = *reinterpret_cast<const float4*>(gates + G_BETA + tb + 2 * e);
+                    z[e] = __ffma2_rn(__fmul2_rn(x[e], both(f)), make_float2(w.x, w.y), __fmul2_rn(z[e], both(fp)));
+                    z[e + 1] = __ffma2_rn(__fmul2_rn(x[e + 1], both(f)), make_float2(w.z, w.w), __fmul2_rn(z[e + 1], both(fp)));
+                    x[e] = __fmul2_rn(make_float2(b.x, b.y), z[e]);
+                    x[e + 1] = __fmul2_rn(make_float2(b.z, b.w), z[e + 1]);
                 }
-                put_halves(tl + COL_W + tb, x);
+                scale_of(row_top(tops, largest(0.f, x), q4, part, i), up, z_down);
+                put_scaled(tl + COL_W + tb, x, up);
                 arrive(have_z);
             }
-            get16(gates + G_E + tb, g);
             {   // y = du + T^T (beta du), l = beta y
+                const float f = z_down * gates[G_TDN];
                 wait_warp(done_r, par);
                 tmem_get16(tl + COL_Z + tb, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    z[e] = __fadd2_rn(z[e], x[e]);
-                    b[e] = __fmul2_rn(b[e], z[e]);
-                    x[e] = __fmul2_rn(make_float2(-g[e].x, -g[e].y), b[e]);
+                for (int e = 0; e < 8; ++e) z[e] = __ffma2_rn(x[e], both(f), z[e]);
+                keep_row<8>(keep.rows + slot * ROWS_BYTES, i, tb / 4, z);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 b = *reinterpret_cast<const float4*>(gates + G_BETA + tb + 2 * e);
+                    const float4 g = *reinterpret_cast<const float4*>(gates + G_E + tb + 2 * e);
+                    z[e] = __fmul2_rn(make_float2(b.x, b.y), z[e]);
+                    z[e + 1] = __fmul2_rn(make_float2(b.z, b.w), z[e + 1]);
+                    x[e] = __fmul2_rn(make_float2(-g.x, -g.y), z[e]);
+                    x[e + 1] = __fmul2_rn(make_float2(-g.z, -g.w), z[e + 1]);
                 }
-                put_halves(tl + COL_W + tb, x);
+                scale_of(row_top(tops2, largest(0.f, x), q4, part, i), up, w_down);
+                w_down *= gates[G_KDN];
+                put_scaled(tl + COL_W + tb, x, up);
                 arrive(have_w);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + st);
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) halves(z[e], hi[e], lo[e]);
-                char* to = keep.rows + slot * ROWS_BYTES + at_d(i, tb / 8);
-                keep_halves(to, to + (C / 8) * 128, hi, lo);
                 const int m = len - chunk * C - tb;
                 __nv_bfloat16* dst = gv + (static_cast<long long>(chunk) * C + tb) * D;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(b[e].x);
-                    if (2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(b[e].y);
+                    if (2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(z[e].x);
+                    if (2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(z[e].y);
                 }
             }
         }
         if (D0) {
-            wait_warp(done_s + (part >> 1), (chunks - 1) & 1);
+            take(chunks - 1);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float2 x[8];
-                tmem_get16(tl + COL_S + cb + 16 * p, x);
                 float* dst = D0 + static_cast<long long>(i) * D + cb + 16 * p;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
-                    *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(x[e].x, x[e].y, x[e + 1].x, x[e + 1].y);
+                    *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(S[p][e].x, S[p][e].y, S[p][e + 1].x, S[p][e + 1].y);
             }
         }
     }
@@ -1054,18 +1246,20 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
 // come in with the sums:
 //     [s x t]  R dO^T, R Y^T -> dP^T, dG^T (E, masks) and dbeta_t = R_t . Y_t,
 //     [j x t]  S0^T dO^T, S0^T Y^T, K^T dP^T, K^T dG^T -> dq, dk as a reader,
-//     [j x s]  Q^T dP + K^T dG, D1^T R^T -> dk as a writer.
-// Every kept operand is a pair of bf16 halves (three products of two such, two
-// with an input): the gradient of A is a sum over all tokens in fp32, which one
-// half alone would leave with 10^-3.
+//     [j x s]  Q^T dP, K^T dG, D1^T R^T -> dk as a writer.
+// The kept fp32 tiles become pairs of fp16 in their place, each tile with one
+// power of two (its values meet in sums); D1 follows S0 there.  <S0, D1> is
+// taken in fp32: the gradient of A is a sum over all tokens to which it adds the
+// same in every token of its chunk.
 constexpr int GR_WARPS = 16, GR_THREADS = GR_WARPS * 32 + 32;
 constexpr int GR_KQ = 0, GR_DO = 2 * TILE_X, GR_R = GR_DO + TILE_X, GR_Y = GR_R + ROWS_BYTES, GR_S = GR_Y + ROWS_BYTES,
               GR_P = GR_S + STATE_BYTES, GR_MISC = GR_P + 2 * C * 2 * C * 2;
-// fp32: the gates, c of each lane quarter, k.(...) of each, row warps' sums
-constexpr int GR_GATES = GR_MISC, GR_C = GR_GATES + 5 * C * 4 + 16, GR_F = GR_C + 4 * C * 4, GR_SUM = GR_F + 4 * C * 4,
-              GR_BAR = GR_SUM + GR_WARPS * 4, GR_SMEM = GR_BAR + 128;
+// fp32: the gates, c of each lane quarter, k.(...) of each, row warps' sums and magnitudes
+constexpr int GR_GATES = GR_MISC, GR_C = GR_GATES + (G_ALL + 3) / 4 * 16, GR_F = GR_C + 4 * C * 4, GR_SUM = GR_F + 4 * C * 4,
+              GR_TOP = GR_SUM + GR_WARPS * 4, GR_BAR = GR_TOP + 5 * GR_WARPS * 4, GR_SMEM = GR_BAR + 128;
 static_assert(GR_SMEM <= 227 * 1024, "shared memory");
-constexpr uint32_t CG_A = 0, CG_Q = 128, CG_R = 192, CG_W = 256, CG_W2 = 320, CG_Q2 = 384;   // (CG_Q2: dq, then dk)
+// (CG_A: R dO^T and R Y^T, then K^T dG in its first half; CG_Q2: K^T dP^T, K^T dG^T)
+constexpr uint32_t CG_A = 0, CG_Q = 128, CG_R = 192, CG_W = 256, CG_W2 = 320, CG_Q2 = 384;
 
 // Sums over the lanes of 16 values each: lane l holds value l % 16's (both
 // halves of a warp the same).
@@ -1091,22 +1285,43 @@ struct GradTiles {
     float* sum_A;           // [slots,H] or null
 };
 
+// The largest magnitude that the row warps (or those that sync on `bar`) have:
+// one slot of `tops` each.
+__device__ __forceinline__ float block_top(float* tops, float mine, int bar, int threads, int warps, int warp) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
+    if ((threadIdx.x & 31) == 0) tops[warp] = __uint_as_float(m);
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+    const int l = threadIdx.x & 31;
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, l < warps ? __float_as_uint(tops[l]) : 0u));
+}
+
+// 8 values of a row as a 16-byte piece of halves each.
+__device__ __forceinline__ void half_pieces(unsigned char* hi_at, unsigned char* lo_at, const float2* x, float up) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) halves(__fmul2_rn(x[e], both(up)), hi[e], lo[e]);
+    *reinterpret_cast<uint4*>(hi_at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
 __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const DeltaArgs a, const GradTiles in, long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
     float* gates = reinterpret_cast<float*>(smem + GR_GATES);
     float* sc = reinterpret_cast<float*>(smem + GR_C);
     float* sf = reinterpret_cast<float*>(smem + GR_F);
     float* ssum = reinterpret_cast<float*>(smem + GR_SUM);
-    uint64_t* in_ry = reinterpret_cast<uint64_t*>(smem + GR_BAR);   // kept rows, S0, D1 are here
+    float* tops = reinterpret_cast<float*>(smem + GR_TOP);            // [5][GR_WARPS]: R, Y, S0, dP and dG, D1
+    uint64_t* in_ry = reinterpret_cast<uint64_t*>(smem + GR_BAR);   // kept rows and S0 are here
     uint64_t* in_s = in_ry + 1;
-    uint64_t* in_d = in_s + 1;
-    uint64_t* done_a = in_d + 1;                                       // products
+    uint64_t* done_a = in_s + 1;                                       // products
     uint64_t* done_b = done_a + 1;
     uint64_t* done_c = done_b + 1;
     uint64_t* done_d = done_c + 1;
-    uint64_t* have_p = done_d + 1;                                     // dP, dG are written; S0 is read
-    uint64_t* have_dot = have_p + 1;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(have_dot + 1);
+    uint64_t* have_ry = done_d + 1;                                    // operands: R and Y, S0, dP and dG, D1
+    uint64_t* have_s = have_ry + 1;
+    uint64_t* have_p = have_s + 1;
+    uint64_t* have_d = have_p + 1;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(have_d + 1);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = static_cast<int>(blockIdx.x % a.H);
@@ -1120,9 +1335,9 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
     const long long tok = (row * a.H + h) * a.T + t0;
     const char* adjoint = in.adjoints + tile * STATE_BYTES;
     if (tid == 0) {
-        for (uint64_t* b : {in_ry, in_s, in_d, done_a, done_b, done_c, done_d}) mbar_init(b, 1);
+        for (uint64_t* b : {in_ry, in_s, done_a, done_b, done_c, done_d}) mbar_init(b, 1);
+        for (uint64_t* b : {have_ry, have_s, have_d}) mbar_init(b, GR_WARPS);
         mbar_init(have_p, GR_WARPS / 2);
-        mbar_init(have_dot, GR_WARPS);
         mbar_init_fence();
         *dead = 0;
         mbar_arrive_expect_tx(in_ry, 2 * ROWS_BYTES);
@@ -1134,13 +1349,16 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
     if (warp == GR_WARPS) {
         tmem_alloc(holder, 512);
     } else {
-        const __nv_bfloat16* go = static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D;
+        constexpr int N = GR_WARPS * 32;
         load_kq(smem_addr(smem + GR_KQ), static_cast<const __nv_bfloat16*>(a.k) + tok * D,
-                static_cast<const __nv_bfloat16*>(a.q) + tok * D, m, tid, GR_WARPS * 32);
-        load_tile(smem_addr(smem + GR_DO), go, m, tid, GR_WARPS * 32);
+                static_cast<const __nv_bfloat16*>(a.q) + tok * D, m, tid, N);
+        load_tile(smem_addr(smem + GR_DO), static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D, m, tid, N);
         const float* g = reinterpret_cast<const float*>(in.prep + tile * PREP_BYTES + PREP_GATES);
-        if (tid <= G_END) gates[tid] = g[tid];
+        if (tid < G_ALL) gates[tid] = g[tid];
+        const float k_up = g[G_KUP], q_up = g[G_QUP], x_up = g[G_XUP];
         copies_done();
+        kq_to_half(smem + GR_KQ, k_up, q_up, tid, N);
+        tile_to_half(smem + GR_DO, x_up, tid, N);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     tc_fence_before_sync();
@@ -1154,12 +1372,12 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
         tc_fence_after_sync();
     };
     if (warp == GR_WARPS) {
-        constexpr uint32_t ID_AK = umma_idesc_bf16_f32(128, C, true, false), ID_AN = umma_idesc_bf16_f32(128, C, true, true),
-                           ID_A2 = umma_idesc_bf16_f32(128, 2 * C, true, true);
-        auto rows_of = [&](int off, int ks, int lo) {                  // a K step of kept rows' or K's tile, MN-major
+        constexpr uint32_t ID_AK = idesc_f16(128, C, true, false), ID_AN = idesc_f16(128, C, true, true),
+                           ID_A2 = idesc_f16(128, 2 * C, true, true);
+        auto rows_of = [&](int off, int ks, int lo) {                  // a K step of a tile of 128 columns, MN-major
             return umma_desc_mnmajor(base + off + ks * 2 * ROWS_D + lo * (C / 8) * 128, ROWS_D, 128);
         };
-        wait_warp(in_ry);
+        wait_warp(have_ry);
         // [s x t]: R dO^T, R Y^T (rows 64-127 are of no use)
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -1173,7 +1391,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             umma_sa(tmem + CG_A + C, rl, yh, ID_AN, 1u);
         }
         umma_done(done_a);
-        wait_warp(in_s);
+        wait_warp(have_s);
         // [j x t]: S0^T dO^T, S0^T Y^T
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -1188,7 +1406,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
         }
         umma_done(done_b);
         wait_warp(have_p);
-        // [j x t]: K^T [dP^T | dG^T];  [j x s]: Q^T dP + K^T dG
+        // [j x t]: K^T [dP^T | dG^T];  [j x s]: Q^T dP, K^T dG
 #pragma unroll
         for (int ks = 0; ks < C / 16; ++ks) {
             const uint64_t k = rows_of(GR_KQ, ks, 0);
@@ -1202,19 +1420,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             for (int lo = 0; lo < 2; ++lo) {
                 const uint32_t p = base + GR_P + lo * C * 2 * C * 2 + ks * 256;
                 umma_sa(tmem + CG_W2, q, umma_desc_kmajor(p, 128, ROWS_D), ID_AK, ks > 0 || lo > 0 ? 1u : 0u);
-                umma_sa(tmem + CG_W2, k, umma_desc_kmajor(p + (C / 8) * 128, 128, ROWS_D), ID_AK, 1u);
+                umma_sa(tmem + CG_A, k, umma_desc_kmajor(p + (C / 8) * 128, 128, ROWS_D), ID_AK, ks > 0 || lo > 0 ? 1u : 0u);
             }
         }
         umma_done(done_c);
-        wait_warp(done_b);
-        wait_warp(have_dot);
-        const bool more = *dead == 0;
-        if (lane == 0 && more) {
-            mbar_arrive_expect_tx(in_d, STATE_BYTES);
-            bulk_g2s(smem + GR_S, adjoint, STATE_BYTES, in_d);
-        }
-        __syncwarp();
-        wait_warp(in_d);
+        wait_warp(have_d);
         // [j x s]: D1^T R^T
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -1228,99 +1438,157 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
         // neither a copy nor a product outlives the CTA
         bool ok = mbar_wait(done_d, 0, wait_ns);
         ok = mbar_wait(in_ry, 0, wait_ns) && mbar_wait(in_s, 0, wait_ns) && ok;
-        if (lane == 0 && more) ok = mbar_wait(in_d, 0, wait_ns) && ok;
         if (!ok) *dead = 1;
     } else {
         const int q4 = warp & 3, part = warp >> 2, tb = 16 * part;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+        const int i = tid & (D - 1), quarter = tid / D;      // a row of the kept tiles, a quarter of its columns
+        auto arrive = [&](uint64_t* bar) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        float r_down, y_down, s_down, p_down, d_down, up;
+        {   // R and Y in halves
+            float2 x[8], y[8];
+            wait_warp(in_ry);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 f = *reinterpret_cast<const float4*>(smem + GR_R + at_f(i, 4 * quarter + e));
+                const float4 g = *reinterpret_cast<const float4*>(smem + GR_Y + at_f(i, 4 * quarter + e));
+                x[2 * e] = make_float2(f.x, f.y);
+                x[2 * e + 1] = make_float2(f.z, f.w);
+                y[2 * e] = make_float2(g.x, g.y);
+                y[2 * e + 1] = make_float2(g.z, g.w);
+            }
+            // (the second exchange's barrier is past every thread's loads too)
+            scale_of(block_top(tops, largest(0.f, x), 1, GR_WARPS * 32, GR_WARPS, warp), up, r_down);
+            float y_up;
+            scale_of(block_top(tops + GR_WARPS, largest(0.f, y), 1, GR_WARPS * 32, GR_WARPS, warp), y_up, y_down);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                unsigned char* to = smem + GR_R + at_d(i, 2 * quarter + e);
+                half_pieces(to, to + (C / 8) * 128, x + 4 * e, up);
+                to = smem + GR_Y + at_d(i, 2 * quarter + e);
+                half_pieces(to, to + (C / 8) * 128, y + 4 * e, y_up);
+            }
+            arrive(have_ry);
+        }
+        {   // <S0, D1>, and S0 in halves
+            float2 x[16];
+            float dot = 0.f, top = 0.f;
+            wait_warp(in_s);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float4 f = *reinterpret_cast<const float4*>(smem + GR_S + at_f(i, 8 * quarter + e));
+                const float4 g = *reinterpret_cast<const float4*>(adjoint + at_f(i, 8 * quarter + e));
+                x[2 * e] = make_float2(f.x, f.y);
+                x[2 * e + 1] = make_float2(f.z, f.w);
+                dot = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, dot))));
+                top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (lane == 0) ssum[warp] = dot;
+            scale_of(block_top(tops + 2 * GR_WARPS, top, 1, GR_WARPS * 32, GR_WARPS, warp), up, s_down);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                unsigned char* to = smem + GR_S + at_d(i, 4 * quarter + e);
+                half_pieces(to, to + D * D * 2, x + 4 * e, up);
+            }
+            arrive(have_s);
+        }
         if (q4 < 2) {   // dP^T, dG^T: row s, 32 tokens of one of the two
             const int s = 32 * q4 + lane, which = part >> 1, tc = 32 * (part & 1);
-            const float sh = gates[G_HI + s], sl = gates[G_LO + s], bs = gates[G_BETA + s];
+            const float sh = gates[G_HI + s], sl = gates[G_LO + s];
+            const float bs = gates[G_BETA + s] * r_down * (which == 1 ? -y_down : gates[G_XDN]);
+            float2 x[2][8];
             wait_warp(done_a);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const int t1 = tc + 16 * p;
-                float2 x[8], gh[8], gl[8], gb[8];
-                tmem_get16(tl + CG_A + which * C + t1, x);
-                get16(gates + G_HI + t1, gh);
-                get16(gates + G_LO + t1, gl);
-                get16(gates + G_BETA + t1, gb);
-                uint32_t hi[8], lo[8];
+                tmem_get16(tl + CG_A + which * C + t1, x[p]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int t = t1 + 2 * e;
+                    const float2 gh = *reinterpret_cast<const float2*>(gates + G_HI + t);
+                    const float2 gl = *reinterpret_cast<const float2*>(gates + G_LO + t);
                     if (which == 1) {   // R_s . Y_s
-                        if (t == s && s < m) static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[e].x);
-                        if (t + 1 == s && s < m) static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[e].y);
-                        x[e] = __fmul2_rn(x[e], make_float2(-gb[e].x, -gb[e].y));
+                        const float2 gb = *reinterpret_cast<const float2*>(gates + G_BETA + t);
+                        if (t == s && s < m)
+                            static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[p][e].x * r_down * y_down);
+                        if (t + 1 == s && s < m)
+                            static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[p][e].y * r_down * y_down);
+                        x[p][e] = __fmul2_rn(x[p][e], gb);
                     }
                     const int first = which == 1 ? s + 1 : s;
-                    const float w0 = bs * ex2((gh[e].x - sh) + (gl[e].x - sl)), w1 = bs * ex2((gh[e].y - sh) + (gl[e].y - sl));
-                    x[e].x = t >= first ? x[e].x * w0 : 0.f;
-                    x[e].y = t + 1 >= first ? x[e].y * w1 : 0.f;
-                    halves(x[e], hi[e], lo[e]);
+                    const float w0 = bs * ex2((gh.x - sh) + (gl.x - sl)), w1 = bs * ex2((gh.y - sh) + (gl.y - sl));
+                    x[p][e].x = t >= first ? x[p][e].x * w0 : 0.f;
+                    x[p][e].y = t + 1 >= first ? x[p][e].y * w1 : 0.f;
                 }
-                char* to = reinterpret_cast<char*>(smem) + GR_P + at_d(s, which * (C / 8) + t1 / 8);
-                keep_halves(to, to + C * 2 * C * 2, hi, lo);
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(have_p);
+            scale_of(block_top(tops + 3 * GR_WARPS, largest(largest(0.f, x[0]), x[1]), 2, GR_WARPS / 2 * 32, GR_WARPS / 2,
+                               2 * part + q4), up, p_down);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    unsigned char* to = smem + GR_P + at_d(s, which * (C / 8) + (tc + 16 * p) / 8 + e);
+                    half_pieces(to, to + C * 2 * C * 2, x[p] + 4 * e, up);
+                }
+            arrive(have_p);
         }
-        // <S0, D1>: the thread's row of both, D1 from memory
-        {
-            wait_warp(in_s);
-            const int i = tid >> 2, c = (tid & 3) * 4;       // row, its 4 of 16 pieces
-            float dot = 0.f;
+        wait_warp(done_b);
+        {   // D1 in halves, where S0 was
+            float2 x[16];
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float4 g = *reinterpret_cast<const float4*>(adjoint + at_f(i, 8 * quarter + e));
+                x[2 * e] = make_float2(g.x, g.y);
+                x[2 * e + 1] = make_float2(g.z, g.w);
+                top = fmaxf(fmaxf(top, fmaxf(fabsf(g.x), fabsf(g.y))), fmaxf(fabsf(g.z), fabsf(g.w)));
+            }
+            scale_of(block_top(tops + 4 * GR_WARPS, top, 1, GR_WARPS * 32, GR_WARPS, warp), up, d_down);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int off = at_d(i, c + e);
-                const uint4 xh = *reinterpret_cast<const uint4*>(smem + GR_S + off);
-                const uint4 xl = *reinterpret_cast<const uint4*>(smem + GR_S + D * D * 2 + off);
-                const uint4 yh = *reinterpret_cast<const uint4*>(adjoint + off);
-                const uint4 yl = *reinterpret_cast<const uint4*>(adjoint + D * D * 2 + off);
-                const uint32_t X[4] = {xh.x, xh.y, xh.z, xh.w}, XL[4] = {xl.x, xl.y, xl.z, xl.w};
-                const uint32_t Y[4] = {yh.x, yh.y, yh.z, yh.w}, YL[4] = {yl.x, yl.y, yl.z, yl.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    dot = fmaf(__uint_as_float(X[w] << 16) + __uint_as_float(XL[w] << 16),
-                               __uint_as_float(Y[w] << 16) + __uint_as_float(YL[w] << 16), dot);
-                    dot = fmaf(__uint_as_float(X[w] & 0xffff0000u) + __uint_as_float(XL[w] & 0xffff0000u),
-                               __uint_as_float(Y[w] & 0xffff0000u) + __uint_as_float(YL[w] & 0xffff0000u), dot);
-                }
+                unsigned char* to = smem + GR_S + at_d(i, 4 * quarter + e);
+                half_pieces(to, to + D * D * 2, x + 4 * e, up);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (lane == 0) {
-                ssum[warp] = dot;
-                mbar_arrive(have_dot);
-            }
+            arrive(have_d);
+        }
+        // dP and dG's scale again, from what the eight warps left
+        {
+            const uint32_t t = lane < GR_WARPS / 2 ? __float_as_uint(tops[3 * GR_WARPS + lane]) : 0u;
+            float unused;
+            scale_of(__uint_as_float(__reduce_max_sync(0xffffffffu, t)), unused, p_down);
         }
         const int j = 32 * q4 + lane;
+        const float kdn = gates[G_KDN], qdn = gates[G_QDN];
         float cc[16];
         float2 kr[8], kj[8];
+        auto column = [&](const unsigned char* p, float down, float2 (&v)[8]) {
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                const float f = down * __half2float(*reinterpret_cast<const __half*>(p + (t / 8) * ROWS_D + (t % 8) * 16));
+                if (t & 1) v[t / 2].y = f;
+                else v[t / 2].x = f;
+            }
+        };
+        const unsigned char* at = smem + GR_KQ + at_d(tb, j / 8) + (j % 8) * 2;
         {
             float2 x[8], y[8], g[8];
-            const unsigned char* at = smem + GR_KQ + at_d(tb, j / 8) + (j % 8) * 2;
-            auto column = [&](const unsigned char* p, float2 (&v)[8]) {
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    const float f = __uint_as_float(
-                        static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(p + (t / 8) * ROWS_D + (t % 8) * 16)) << 16);
-                    if (t & 1) v[t / 2].y = f;
-                    else v[t / 2].x = f;
-                }
-            };
             get16(gates + G_E + tb, g);
-            wait_warp(done_b);
             tmem_get16(tl + CG_Q + tb, x);
             wait_warp(done_c);
             tmem_get16(tl + CG_Q2 + tb, y);
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_q) + (tok + tb) * D + j;
-            column(at + TILE_X, kj);
+            column(at + TILE_X, qdn, kj);
+            const float f = s_down * gates[G_XDN], fp = p_down * kdn;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                y[e] = __ffma2_rn(g[e], x[e], y[e]);
+                y[e] = __ffma2_rn(__fmul2_rn(g[e], both(f)), x[e], __fmul2_rn(y[e], both(fp)));
                 if (tb + 2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(y[e].x);
                 if (tb + 2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(y[e].y);
                 cc[2 * e] = kj[e].x * y[e].x;
@@ -1330,10 +1598,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             tmem_get16(tl + CG_Q2 + C + tb, y);
             float2 b[8];
             get16(gates + G_BETA + tb, b);
-            column(at, kj);
+            column(at, kdn, kj);
+            const float fr = -s_down * y_down;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                kr[e] = __ffma2_rn(__fmul2_rn(make_float2(-g[e].x, -g[e].y), b[e]), x[e], y[e]);
+                kr[e] = __ffma2_rn(__fmul2_rn(__fmul2_rn(g[e], both(fr)), b[e]), x[e], __fmul2_rn(y[e], both(fp)));
                 cc[2 * e] = fmaf(kj[e].x, kr[e].x, cc[2 * e]);
                 cc[2 * e + 1] = fmaf(kj[e].y, kr[e].y, cc[2 * e + 1]);
             }
@@ -1341,15 +1610,20 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
         {
             float2 x[8], y[8], g[8], b[8];
             float f[16];
+            tmem_get16(tl + CG_W2 + tb, y);
+            tmem_get16(tl + CG_A + tb, x);
+            const float fq = p_down * qdn, fk = p_down * kdn;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __ffma2_rn(y[e], both(fq), __fmul2_rn(x[e], both(fk)));
             get16(gates + G_W + tb, g);
             get16(gates + G_BETA + tb, b);
-            tmem_get16(tl + CG_W2 + tb, y);
             wait_warp(done_d);
             tmem_get16(tl + CG_W + tb, x);
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_k) + (tok + tb) * D + j;
+            const float fd = d_down * r_down;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x[e] = __fmul2_rn(__fmul2_rn(g[e], b[e]), x[e]);
+                x[e] = __fmul2_rn(__fmul2_rn(__fmul2_rn(g[e], both(fd)), b[e]), x[e]);
                 f[2 * e] = kj[e].x * x[e].x;
                 f[2 * e + 1] = kj[e].y * x[e].y;
                 x[e] = __fadd2_rn(x[e], y[e]);
@@ -1455,14 +1729,14 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     auto walk = delta_chunk_kernel<float, true>;
     const std::pair<const void*, int> kernels[] = {{reinterpret_cast<const void*>(delta_prep_kernel), P_SMEM},
                                                    {reinterpret_cast<const void*>(walk), CH_SMEM},
-                                                   {reinterpret_cast<const void*>(delta_adjoint_kernel), CH_SMEM},
+                                                   {reinterpret_cast<const void*>(delta_adjoint_kernel), AD_SMEM},
                                                    {reinterpret_cast<const void*>(delta_tc_grad_kernel), GR_SMEM}};
     cudaError_t e = cudaSuccess;
     for (const auto& k : kernels)
         if ((e = allow_smem(k.first, k.second)) != cudaSuccess) return from_cuda(e);
     delta_prep_kernel<<<static_cast<unsigned>(tiles), PREP_THREADS, P_SMEM, stream>>>(a, prep, wait_ns);
     walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, fwd, wait_ns);
-    delta_adjoint_kernel<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, bwd, wait_ns);
+    delta_adjoint_kernel<<<static_cast<unsigned>(rows), CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, wait_ns);
     delta_tc_grad_kernel<<<static_cast<unsigned>(tiles), GR_THREADS, GR_SMEM, stream>>>(
         a, GradTiles{prep, fwd.states, bwd.states, fwd.rows, bwd.rows, a.grad_A ? shares : nullptr}, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.grad_A) return from_cuda(e);

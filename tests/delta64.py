@@ -23,12 +23,25 @@ from its operands), z_t = -A d_t for a log decay.
   the other's magnitude, plus e times the magnitudes.  The gradient of a log
   decay is a sum over the rest of its chunk, and so is its bound.
 
+The tensor-core form (``split`` > 0) has fp16 pairs for operands, scaled by
+powers of two to below 2^14: an element is off by 2^-22 of itself, three
+products leave out one of 2^-22 (SPLIT covers both, and those of products of
+products), or by 2^-25 / 2^13 = 2^-38 of the largest element of its tile or
+state row, which is more for what strong decays make small beside the rest of
+its chunk.  A sum of up to 128 such products is then off by 2^-31 of the largest
+product; for P, which is scaled by a bound of its largest, 2^-5 max|k| max|q| in
+place of 2^-13 of that, a sum of 64 by 2^-24 max|k| max|q| max|u|.  A token's bound
+is at least e times its own largest product, e > 2^-16, so 2^-8 of the largest
+bound among a sequence's tokens covers both (FLOOR).
+
 A result rounded to a type adds half a step of itself.
 """
 import torch
 
 UNIT = 2.0 ** -24
 CHUNK = 64
+SPLIT = 2.0 ** -20
+FLOOR = 2.0 ** -8
 
 
 def half_step(dtype):
@@ -114,6 +127,8 @@ def delta(q, k, v, beta, d, A, S0=None, offsets=None, grad_out=None, grad_final=
             kept.append((before, S, b_before, bS, r, er, M, al, z, gate))
         val["final"][n] = S
         err["final"][n] = bS.unsqueeze(-1).expand_as(S)
+        if split and hi > lo:
+            err["out"][b, :, lo:hi] += FLOOR * err["out"][b, :, lo:hi].amax((1, 2), keepdim=True)
         if grad_out is None:
             continue
         D = torch.zeros(H, dv, dk, dtype=torch.float64) if grad_final is None else grad_final[n].double()
@@ -173,6 +188,10 @@ def delta(q, k, v, beta, d, A, S0=None, offsets=None, grad_out=None, grad_final=
             N = al * N + al * lam.abs() * nk
         val["S0"][n] = D
         err["S0"][n] = bD.unsqueeze(-1).expand_as(D)
+        if split and hi > lo:
+            for name in ("q", "k", "v", "beta", "d"):
+                part = err[name][b, :, lo:hi]
+                part += FLOOR * part.flatten(1).amax(1).view(-1, *[1] * (part.dim() - 1))
     return val, err
 
 

@@ -34,7 +34,7 @@ def cuda(x):
 # how far a call may be from the 64-bit value beside its bound's fp32 part: what
 # the tensor-core form cuts from its operands (see the kernels), 0 for the rest
 def split(dk, dv, dt, T):
-    return 2.0 ** -15 if dt == BF16 else 0.0
+    return delta64.SPLIT if dt == BF16 and dk == dv == 128 and T >= 32 else 0.0
 
 
 SHAPES = [
