@@ -55,15 +55,17 @@ __host__ __device__ constexpr int at_d(int r, int c8) { return (r / 8) * ROWS_D 
 __host__ __device__ constexpr int at_c(int r, int c8) { return (r / 8) * ROWS_C + c8 * 128 + (r % 8) * 16; }
 
 // What the preparation leaves of a chunk, as the walk reads it.
-constexpr int PREP_T = 0;                    // T hi, lo
-constexpr int PREP_P = 2 * TILE_T;           // P hi, lo
-constexpr int PREP_GATES = 4 * TILE_T;       // fp32: five rows of 64, then single values
+constexpr int PREP_KQ = 0;                   // k and q, one tile of 2 x 64 rows
+constexpr int PREP_T = 2 * TILE_X;           // T hi, lo
+constexpr int PREP_P = PREP_T + 2 * TILE_T;  // P hi, lo
+constexpr int PREP_GATES = PREP_P + 2 * TILE_T;   // fp32: five rows of 64, then single values
 constexpr int G_E = 0, G_W = C, G_BETA = 2 * C, G_HI = 3 * C, G_LO = 4 * C;   // e^g, e^{g_C - g}, beta, log2 e . g
-// e^{g_C}; the power of two that k, q, do are scaled with (UP) and those that undo scales (DN)
-constexpr int G_END = 5 * C, G_KUP = G_END + 1, G_KDN = G_END + 2, G_QUP = G_END + 3, G_QDN = G_END + 4, G_XUP = G_END + 5,
-              G_XDN = G_END + 6, G_TDN = G_END + 7, G_PDN = G_END + 8, G_ALL = G_END + 9;
+// e^{g_C}, and the powers of two that undo the scales of k, q, do, T and P
+constexpr int G_END = 5 * C, G_KDN = G_END + 1, G_QDN = G_END + 2, G_XDN = G_END + 3, G_TDN = G_END + 4, G_PDN = G_END + 5,
+              G_ALL = G_END + 6;
 constexpr int PREP_BYTES = PREP_GATES + 1408;
 static_assert(G_ALL * 4 <= 1408, "the gates' room");
+constexpr int PREP_STEP = PREP_BYTES + TILE_X;   // (backward: do behind it)
 // What the backward's walks leave of a chunk beside it, fp32: a state (S before
 // the chunk, or its adjoint D behind it) as [i][j] and the rows R and Y as
 // [i][t]; four columns of all 128 rows i, then the next four.
@@ -127,19 +129,8 @@ __device__ __forceinline__ void load_kq(uint32_t tile, const __nv_bfloat16* k, c
     }
 }
 
-// The same of one tensor: 64 rows.
-__device__ __forceinline__ void load_tile(uint32_t tile, const __nv_bfloat16* x, int n, int tid, int threads) {
-    const int lane = tid & 31, a = lane & 7, b = lane >> 3;
-    for (int w = tid >> 5; w < C / 8 * 4; w += threads >> 5) {
-        const int t = (w >> 2) * 8 + a, c8 = (w & 3) * 4 + b;
-        copy16_or_zero(tile + at_d(t, c8), x + (t < n ? static_cast<long long>(t) * D : 0) + c8 * 8, t < n);
-    }
-}
-
-// The same 16-byte pieces from bf16 to fp16, in their place, times a power of
-// two: by the thread that copied them, when they are here.
-__device__ __forceinline__ void to_half(unsigned char* piece, float up) {
-    uint4 w = *reinterpret_cast<const uint4*>(piece);
+// 8 bf16 numbers as fp16, times a power of two.
+__device__ __forceinline__ uint4 to_half(uint4 w, float up) {
     uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -147,19 +138,9 @@ __device__ __forceinline__ void to_half(unsigned char* piece, float up) {
         const __half2 h = __float22half2_rn(__fmul2_rn(f, both(up)));
         u[e] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(piece) = make_uint4(u[0], u[1], u[2], u[3]);
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void kq_to_half(unsigned char* tile, float k_up, float q_up, int tid, int threads) {
-    const int lane = tid & 31, a = lane & 7, b = lane >> 3;
-    for (int w = tid >> 5; w < 2 * C / 8 * 4; w += threads >> 5) {
-        const int r = (w >> 2) * 8 + a;
-        to_half(tile + at_d(r, (w & 3) * 4 + b), r < C ? k_up : q_up);
-    }
-}
-__device__ __forceinline__ void tile_to_half(unsigned char* tile, float up, int tid, int threads) {
-    const int lane = tid & 31, a = lane & 7, b = lane >> 3;
-    for (int w = tid >> 5; w < C / 8 * 4; w += threads >> 5) to_half(tile + at_d((w >> 2) * 8 + a, (w & 3) * 4 + b), up);
-}
+
 // The largest magnitude of 8 bf16 numbers, as bits of two.
 __device__ __forceinline__ uint32_t largest_bf16(uint32_t m, uint4 w) {
     m = __vmaxu2(m, w.x & 0x7fff7fffu);
@@ -253,7 +234,8 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     int t0, m;
     if (!chunk_of(a, slot, &n, &t0, &m, &row)) return;
     const long long tok = (row * a.H + h) * a.T + t0;
-    char* out = prep + (slot * a.H + h) * static_cast<long long>(PREP_BYTES);
+    const int bytes = a.grad_out ? PREP_STEP : PREP_BYTES;
+    char* out = prep + (slot * a.H + h) * static_cast<long long>(bytes);
 
     load_kq(smem_addr(smem), static_cast<const __nv_bfloat16*>(a.k) + tok * D,
             static_cast<const __nv_bfloat16*>(a.q) + tok * D, m, tid, PREP_THREADS);
@@ -329,22 +311,30 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
         }
         umma_commit(bar);
     }
-    const bool ok = mbar_wait(bar, 0, wait_ns);
-    __syncthreads();   // the magnitudes are here, and the product is done: k and q may be overwritten
-    tc_fence_after_sync();
+    __syncthreads();   // the magnitudes are here
     float ups[3], downs[3];
 #pragma unroll
     for (int e = 0; e < 3; ++e)
         input_scale(__uint_as_float(max(max(tops[e], tops[3 + e]), max(tops[6 + e], tops[9 + e])) << 16), ups[e], downs[e]);
+    for (int i = tid; i < 2 * C * (D / 8); i += PREP_THREADS)
+        *reinterpret_cast<uint4*>(out + PREP_KQ + i * 16) =
+            to_half(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16), i < C * (D / 8) ? ups[0] : ups[1]);
+    if (a.grad_out) {
+        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D);
+        for (int i = tid; i < C * (D / 8); i += PREP_THREADS) {
+            const int t = i / (D / 8), c8 = i % (D / 8);
+            *reinterpret_cast<uint4*>(out + PREP_BYTES + at_d(t, c8)) = t < m ? to_half(g[i], ups[2]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    const bool ok = mbar_wait(bar, 0, wait_ns);
+    __syncthreads();   // the product is done and k and q are read: they may be overwritten
+    tc_fence_after_sync();
     // |P| <= 128 max|k| max|q|: scaled by both and by 2^-21 it is below 2^14
     const float p_up = ups[0] * ups[1] * 0x1p-21f;
     if (tid == 0) {
         float* gates = reinterpret_cast<float*>(out + PREP_GATES);
 #pragma unroll
-        for (int e = 0; e < 3; ++e) {
-            gates[G_KUP + 2 * e] = ups[e];
-            gates[G_KDN + 2 * e] = downs[e];
-        }
+        for (int e = 0; e < 3; ++e) gates[G_KDN + e] = downs[e];
         gates[G_PDN] = downs[0] * downs[1] * 0x1p21f;
     }
     {   // row tid: K K^T of token tid, or Q K^T of token tid - 64
@@ -458,13 +448,14 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
 
 // Warps 0-15 work on the state's rows (thread = row i = lane of tensor memory,
 // warp / 4 = quarter of the columns and of the tokens); a thread's 32 columns of
-// S stay in its registers.  Warp 16 issues the products, warps 17-19 bring the
+// S stay in its registers.  Warp 16 issues the products, warp 17 brings the
 // tiles, one chunk ahead.  Sixteen row warps: with eight, two to a scheduler,
 // their dependent steps took 1.6 times as long.
-constexpr int ROW_WARPS = 16, MMA_WARP = ROW_WARPS, LOAD_WARPS = 3, CH_THREADS = (ROW_WARPS + 1 + LOAD_WARPS) * 32;
-// shared memory: two stages of [k; q], v (backward: do) and the prepared chunk;
+constexpr int ROW_WARPS = 16, MMA_WARP = ROW_WARPS, CH_THREADS = (ROW_WARPS + 2) * 32;
+// shared memory: two stages of a prepared chunk and v (backward: do);
 // two arrays of the rows' largest magnitudes, one value of each quarter
-constexpr int ST_V = 2 * TILE_X, ST_PREP = ST_V + TILE_X, STAGE_BYTES = ST_PREP + PREP_BYTES;
+constexpr int ST_V = PREP_BYTES, STAGE_BYTES = ST_V + TILE_X;
+static_assert(ST_V % 128 == 0, "tiles on 128 bytes");
 constexpr int CH_OFF_TOP = 2 * STAGE_BYTES, CH_OFF_BAR = CH_OFF_TOP + 2 * 4 * D * 4, CH_SMEM = CH_OFF_BAR + 192;
 // ... and the adjoint's e^g do, hi and lo
 constexpr int AD_OFF_X = (CH_SMEM + 127) / 128 * 128, AD_SMEM = AD_OFF_X + 2 * D * C * 2;
@@ -579,44 +570,31 @@ __device__ __forceinline__ void keep_row(char* tile, int i, int c4, const float2
             make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y);
 }
 
-// Chunks' tiles of k, q and x (v as it is; backwards, do as fp16) by the loading
-// warps, 96 threads; `backwards`: the last chunk first.
-__device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* landed, uint64_t* full, uint64_t* empty,
-                                            const Waits& wait, const __nv_bfloat16* k, const __nv_bfloat16* q,
-                                            const __nv_bfloat16* x, const char* prep, long long prep_step, int len,
-                                            int chunks, bool backwards, int l) {
-    constexpr int N = LOAD_WARPS * 32;
+// Chunks' tiles by one thread: what the preparation left, and v where it is given
+// (with do behind the rest where not); `backwards`: the last chunk first.
+__device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full, uint64_t* empty, const Waits& wait,
+                                            const __nv_bfloat16* v, const char* prep, long long step, int len, int chunks) {
     int sent = -1;                                   // the last one whose copies were issued
     for (int n = 0; n < chunks; ++n) {
-        const int c = backwards ? chunks - 1 - n : n, st = n & 1, m = min(C, len - c * C);
+        const int c = v ? n : chunks - 1 - n, st = n & 1, m = min(C, len - c * C);
         if (n >= 2) wait(empty + st, ((n >> 1) - 1) & 1);
         if (*wait.dead) break;
         sent = n;
         unsigned char* stage = smem + st * STAGE_BYTES;
-        const long long row = static_cast<long long>(c) * C * D;
-        if (l == 0) {
-            mbar_arrive_expect_tx(landed + st, PREP_BYTES + (backwards ? 0 : m * D * 2));
-            bulk_g2s(stage + ST_PREP, prep + c * prep_step, PREP_BYTES, landed + st);
-            if (!backwards) bulk_g2s(stage + ST_V, x + row, m * D * 2, landed + st);
-        }
-        load_kq(smem_addr(stage), k + row, q + row, m, l, N);
-        if (backwards) {
-            load_tile(smem_addr(stage + ST_V), x + row, m, l, N);
-        } else {
+        if (v) {
             // rows as they are; no token: zeros, not what lay there before
-            for (int e = l; e < (C - m) * (D / 8); e += N)
-                *reinterpret_cast<uint4*>(stage + ST_V + m * D * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = m * D * 2; e < TILE_X; e += 16) *reinterpret_cast<uint4*>(stage + ST_V + e) = make_uint4(0u, 0u, 0u, 0u);
+            mbar_arrive_expect_tx(full + st, PREP_BYTES + m * D * 2);
+            bulk_g2s(stage, prep + c * step, PREP_BYTES, full + st);
+            bulk_g2s(stage + ST_V, v + static_cast<long long>(c) * C * D, m * D * 2, full + st);
+        } else {
+            mbar_arrive_expect_tx(full + st, PREP_STEP);
+            bulk_g2s(stage, prep + c * step, PREP_STEP, full + st);
         }
-        copies_done();
-        wait(landed + st, (n >> 1) & 1);
-        const float* gates = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
-        kq_to_half(stage, gates[G_KUP], gates[G_QUP], l, N);
-        if (backwards) tile_to_half(stage + ST_V, gates[G_XUP], l, N);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(full + st);
     }
     // no copy outlives the CTA
-    if (l == 0 && sent >= 0 && !mbar_wait(landed + (sent & 1), (sent >> 1) & 1, wait.limit)) *wait.dead = 1;
+    for (int n = max(sent - 1, 0); n <= sent; ++n)
+        if (!mbar_wait(full + (n & 1), (n >> 1) & 1, wait.limit)) *wait.dead = 1;
 }
 
 // A walk's kept tiles; null in a forward call.
@@ -627,14 +605,13 @@ struct KeepTiles {
 
 // KEEP: no outputs, but the state before each chunk and R.
 template <typename TO, bool KEEP>
-__global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, const KeepTiles keep,
-                                                                    long long wait_ns) {
+__global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, int prep_bytes,
+                                                                    const KeepTiles keep, long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
     float* tops = reinterpret_cast<float*>(smem + CH_OFF_TOP);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);   // [2] a stage is here
     uint64_t* empty = full + 2;                                        // [2] a stage is read
-    uint64_t* landed = empty + 2;                                      // [2] a stage's bulk copies are here
-    uint64_t* done_z = landed + 2;                                     // products: Z, R, S, O
+    uint64_t* done_z = empty + 2;                                      // products: Z, R, S, O
     uint64_t* done_r = done_z + 1;
     uint64_t* done_s = done_r + 1;                                     // [2] (columns 0-63 and 64-127)
     uint64_t* done_o = done_s + 2;
@@ -642,7 +619,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     uint64_t* have_z = have_s + 2;
     uint64_t* have_w = have_z + 1;
     uint64_t* have_u = have_w + 1;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(have_u + 1);
+    uint64_t* read_o = have_u + 1;                                     // Q S^T and P U are read
+    uint32_t* holder = reinterpret_cast<uint32_t*>(read_o + 1);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long sr = blockIdx.x, n = sr / a.H;
@@ -661,14 +639,13 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(full + s, LOAD_WARPS * 32);
+            mbar_init(full + s, 1);
             mbar_init(empty + s, 1 + ROW_WARPS);
-            mbar_init(landed + s, 1);
             mbar_init(done_s + s, 1);
             mbar_init(have_s + s, ROW_WARPS / 2);
         }
         for (uint64_t* b : {done_z, done_r, done_o}) mbar_init(b, 1);
-        for (uint64_t* b : {have_z, have_w, have_u}) mbar_init(b, ROW_WARPS);
+        for (uint64_t* b : {have_z, have_w, have_u, read_o}) mbar_init(b, ROW_WARPS);
         mbar_init_fence();
         *dead = 0;
     }
@@ -687,17 +664,16 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     if (warp >= MMA_WARP) {
         if (warp > MMA_WARP) {
             // ---- tiles ------------------------------------------------------------------
-            const long long step = static_cast<long long>(a.H) * PREP_BYTES;
-            load_chunks(smem, landed, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
-                        static_cast<const __nv_bfloat16*>(a.q) + tok * D, static_cast<const __nv_bfloat16*>(a.v) + tok * D,
-                        prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, false,
-                        tid - (MMA_WARP + 1) * 32);
+            if (lane == 0)
+                load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.v) + tok * D,
+                            prep + (sp.slot * a.H + h) * static_cast<long long>(prep_bytes),
+                            static_cast<long long>(a.H) * prep_bytes, len, chunks);
         } else {
             // ---- products ---------------------------------------------------------------
             constexpr uint32_t ID_T = idesc_f16(128, C), ID_S = idesc_f16(128, D / 2, false, true);
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
-                const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
+                const uint32_t par = c & 1, pr = base + st * STAGE_BYTES, kq = pr + PREP_KQ;
                 wait_warp(full + st, (c >> 1) & 1);
                 if (!KEEP && c > 0) wait_warp(done_o, par ^ 1);   // (U's halves were read out of COL_Z)
                 // S K^T, from the columns of S as they come
@@ -714,6 +690,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 }
                 umma_done(done_z);
                 // S Q^T, while the rows work on Z
+                if (!KEEP && c > 0) wait_warp(read_o, par ^ 1);
 #pragma unroll
                 for (int ks = 0; ks < (KEEP ? 0 : D / 16); ++ks) {
                     const uint64_t b = umma_desc_kmajor(kq + TILE_X + ks * 256, 128, ROWS_D);
@@ -785,12 +762,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 S[p][e + 1] = make_float2(f.z, f.w);
             }
         TO* out = static_cast<TO*>(a.out) + tok * D + i;
-        float2 qs[8];                                    // e^g Q S^T of the chunk before
         float s_down = 1.f, w_down = 1.f, u_down = 1.f, end = 1.f;   // of the chunk before: what undoes the scales, e^{g_C}
-        // S of the chunk before, and (the last use of its stage) its Q S^T
-        auto take = [&](int c) {
+        auto take = [&](int c) {                         // S behind chunk c
             wait_warp(done_s + (part >> 1), c & 1);
-            const float* gates = reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + ST_PREP + PREP_GATES);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 float2 x[8];
@@ -798,39 +772,42 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[p][e] = __ffma2_rn(x[e], both(w_down), __fmul2_rn(S[p][e], both(end)));
             }
-            if (KEEP) return;
-            tmem_get16(tl + COL_QS + tb, qs);
-            const float f = s_down * gates[G_QDN];
-            u_down *= gates[G_PDN];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 g = reinterpret_cast<const float4*>(gates + G_E + tb)[e];
-                qs[2 * e] = __fmul2_rn(__fmul2_rn(qs[2 * e], both(f)), make_float2(g.x, g.y));
-                qs[2 * e + 1] = __fmul2_rn(__fmul2_rn(qs[2 * e + 1], both(f)), make_float2(g.z, g.w));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + (c & 1));
         };
-        auto finish = [&](int c) {                       // outputs of chunk c
+        auto finish = [&](int c, float before) {         // outputs of chunk c, whose S had the scale `before`
+            const float* gates = reinterpret_cast<const float*>(smem + (c & 1) * STAGE_BYTES + PREP_GATES);
+            const float fq = before * gates[G_QDN], fo = u_down * gates[G_PDN];
             wait_warp(done_o, c & 1);
-            float2 o[8];
+            float2 o[8], q[8];
             tmem_get16(tl + COL_O + tb, o);
+            tmem_get16(tl + COL_QS + tb, q);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float4 g = *reinterpret_cast<const float4*>(gates + G_E + tb + 2 * e);
+                o[e] = __ffma2_rn(o[e], both(fo), __fmul2_rn(__fmul2_rn(q[e], both(fq)), make_float2(g.x, g.y)));
+                o[e + 1] = __ffma2_rn(o[e + 1], both(fo), __fmul2_rn(__fmul2_rn(q[e + 1], both(fq)), make_float2(g.z, g.w)));
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(read_o);
+                mbar_arrive(empty + (c & 1));
+            }
             const int m = len - c * C - tb;
             TO* dst = out + (static_cast<long long>(c) * C + tb) * D;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float2 y = __ffma2_rn(o[e], both(u_down), qs[e]);
-                if (2 * e < m) dst[2 * e * D] = from_f32<TO>(y.x);
-                if (2 * e + 1 < m) dst[(2 * e + 1) * D] = from_f32<TO>(y.y);
+                if (2 * e < m) dst[2 * e * D] = from_f32<TO>(o[e].x);
+                if (2 * e + 1 < m) dst[(2 * e + 1) * D] = from_f32<TO>(o[e].y);
             }
         };
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
             const uint32_t par = c & 1;
             unsigned char* stage = smem + st * STAGE_BYTES;
-            const float* gates = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
+            const float* gates = reinterpret_cast<const float*>(stage + PREP_GATES);
             if (c > 0) take(c - 1);
             float up;
+            const float before = s_down;
             {   // the state's halves
                 scale_of(row_top(tops, largest(largest(0.f, S[0]), S[1]), q4, part, i), up, s_down);
 #pragma unroll
@@ -848,7 +825,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 keep_row<8>(to, i, cb / 4, S[0]);
                 keep_row<8>(to, i, cb / 4 + 4, S[1]);
             } else if (c > 0) {
-                finish(c - 1);
+                finish(c - 1, before);
             }
             wait_warp(full + st, (c >> 1) & 1);
             end = gates[G_END];
@@ -910,7 +887,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         }
         if (!KEEP) {
             take(chunks - 1);
-            finish(chunks - 1);
+            finish(chunks - 1, s_down);
         }
         if (final_state) {
 #pragma unroll
@@ -947,8 +924,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     float* tops = reinterpret_cast<float*>(smem + CH_OFF_TOP);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);
     uint64_t* empty = full + 2;
-    uint64_t* landed = empty + 2;
-    uint64_t* done_p = landed + 2;                                     // products: P^T dO, K D^T, T^T beta dU, D
+    uint64_t* done_p = empty + 2;                                      // products: P^T dO, K D^T, T^T beta dU, D
     uint64_t* done_z = done_p + 1;
     uint64_t* done_r = done_z + 1;
     uint64_t* done_s = done_r + 1;                                     // [2]
@@ -975,9 +951,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(full + s, LOAD_WARPS * 32);
+            mbar_init(full + s, 1);
             mbar_init(empty + s, 1 + ROW_WARPS);
-            mbar_init(landed + s, 1);
             mbar_init(done_s + s, 1);
             mbar_init(have_s + s, ROW_WARPS / 2);
         }
@@ -1000,19 +975,16 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
 
     if (warp >= MMA_WARP) {
         if (warp > MMA_WARP) {
-            const long long step = static_cast<long long>(a.H) * PREP_BYTES;
-            load_chunks(smem, landed, full, empty, wait, static_cast<const __nv_bfloat16*>(a.k) + tok * D,
-                        static_cast<const __nv_bfloat16*>(a.q) + tok * D,
-                        static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D,
-                        prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_BYTES), step, len, chunks, true,
-                        tid - (MMA_WARP + 1) * 32);
+            if (lane == 0)
+                load_chunks(smem, full, empty, wait, nullptr, prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_STEP),
+                            static_cast<long long>(a.H) * PREP_STEP, len, chunks);
         } else {
             constexpr uint32_t ID_T = idesc_f16(128, C), ID_TN = idesc_f16(128, C, false, true),
                                ID_P = idesc_f16(128, C, true, true), ID_S = idesc_f16(128, D / 2, false, true),
                                ID_Q = idesc_f16(128, D, false, true);
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
-                const uint32_t par = c & 1, kq = base + st * STAGE_BYTES, pr = kq + ST_PREP;
+                const uint32_t par = c & 1, pr = base + st * STAGE_BYTES, kq = pr + PREP_KQ;
                 wait_warp(full + st, (c >> 1) & 1);
                 if (c > 0) wait_warp(done_s + 1, par ^ 1);   // (L's halves were read out of COL_W)
                 // dO^T P
@@ -1115,7 +1087,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
             const int st = c & 1, chunk = chunks - 1 - c;
             const uint32_t par = c & 1;
             const unsigned char* stage = smem + st * STAGE_BYTES;
-            const float* gates = reinterpret_cast<const float*>(stage + ST_PREP + PREP_GATES);
+            const float* gates = reinterpret_cast<const float*>(stage + PREP_GATES);
             const long long slot = (sp.slot + chunk) * a.H + h;
             if (c > 0) take(c - 1);
             float up;
@@ -1276,6 +1248,10 @@ __device__ __forceinline__ float lane_sums(float (&v)[16], int lane) {
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 struct GradTiles {
     const char* prep;
     const char* states;
@@ -1283,6 +1259,7 @@ struct GradTiles {
     const char* r;
     const char* y;
     float* sum_A;           // [slots,H] or null
+    int ahead;              // tiles between this CTA's and the one that follows it on its SM
 };
 
 // The largest magnitude that the row warps (or those that sync on `bar`) have:
@@ -1340,26 +1317,29 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
         mbar_init(have_p, GR_WARPS / 2);
         mbar_init_fence();
         *dead = 0;
-        mbar_arrive_expect_tx(in_ry, 2 * ROWS_BYTES);
+        const char* prep = in.prep + tile * PREP_STEP;
+        mbar_arrive_expect_tx(in_ry, 2 * ROWS_BYTES + 3 * TILE_X);
+        bulk_g2s(smem + GR_KQ, prep + PREP_KQ, 2 * TILE_X, in_ry);
+        bulk_g2s(smem + GR_DO, prep + PREP_BYTES, TILE_X, in_ry);
         bulk_g2s(smem + GR_R, in.r + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
         bulk_g2s(smem + GR_Y, in.y + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
         mbar_arrive_expect_tx(in_s, STATE_BYTES);
         bulk_g2s(smem + GR_S, in.states + tile * STATE_BYTES, STATE_BYTES, in_s);
+        // one CTA to an SM: what the next one reads comes to L2 while this one works
+        const long long next = tile + in.ahead;
+        if (next < gridDim.x) {
+            prefetch_l2(in.prep + next * PREP_STEP, PREP_STEP);
+            prefetch_l2(in.r + next * ROWS_BYTES, ROWS_BYTES);
+            prefetch_l2(in.y + next * ROWS_BYTES, ROWS_BYTES);
+            prefetch_l2(in.states + next * STATE_BYTES, STATE_BYTES);
+            prefetch_l2(in.adjoints + next * STATE_BYTES, STATE_BYTES);
+        }
     }
     if (warp == GR_WARPS) {
         tmem_alloc(holder, 512);
     } else {
-        constexpr int N = GR_WARPS * 32;
-        load_kq(smem_addr(smem + GR_KQ), static_cast<const __nv_bfloat16*>(a.k) + tok * D,
-                static_cast<const __nv_bfloat16*>(a.q) + tok * D, m, tid, N);
-        load_tile(smem_addr(smem + GR_DO), static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D, m, tid, N);
-        const float* g = reinterpret_cast<const float*>(in.prep + tile * PREP_BYTES + PREP_GATES);
+        const float* g = reinterpret_cast<const float*>(in.prep + tile * PREP_STEP + PREP_GATES);
         if (tid < G_ALL) gates[tid] = g[tid];
-        const float k_up = g[G_KUP], q_up = g[G_QUP], x_up = g[G_XUP];
-        copies_done();
-        kq_to_half(smem + GR_KQ, k_up, q_up, tid, N);
-        tile_to_half(smem + GR_DO, x_up, tid, N);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -1705,7 +1685,7 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
     auto kernel = a.out_dtype == KDN_BF16 ? delta_chunk_kernel<__nv_bfloat16, false> : delta_chunk_kernel<float, false>;
     if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
-    kernel<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, ws, KeepTiles{}, wait_ns);
+    kernel<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, ws, PREP_BYTES, KeepTiles{}, wait_ns);
     return from_cuda(cudaGetLastError());
 }
 
@@ -1715,7 +1695,7 @@ long long rounded(long long bytes) { return (bytes + 255) / 256 * 256; }
 
 long long tc_bwd_bytes(int B, int H, int T, int nseq) {
     const long long tiles = slots_of(B, T, nseq) * H;
-    return tiles * (PREP_BYTES + 2 * STATE_BYTES + 2 * ROWS_BYTES) + rounded(tiles * 4);
+    return tiles * (PREP_STEP + 2 * STATE_BYTES + 2 * ROWS_BYTES) + rounded(tiles * 4);
 }
 
 kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long wait_ns) {
@@ -1723,7 +1703,7 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     const long long rows = static_cast<long long>(a.offsets ? a.nseq : a.B) * a.H;
     if (tiles > 0x7fffffffLL || rows > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
     char* prep = ws;
-    const KeepTiles fwd{prep + tiles * PREP_BYTES, prep + tiles * (PREP_BYTES + 2 * STATE_BYTES)};
+    const KeepTiles fwd{prep + tiles * PREP_STEP, prep + tiles * (PREP_STEP + 2 * STATE_BYTES)};
     const KeepTiles bwd{fwd.states + tiles * STATE_BYTES, fwd.rows + tiles * ROWS_BYTES};
     float* shares = reinterpret_cast<float*>(bwd.rows + tiles * ROWS_BYTES);
     auto walk = delta_chunk_kernel<float, true>;
@@ -1735,10 +1715,10 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     for (const auto& k : kernels)
         if ((e = allow_smem(k.first, k.second)) != cudaSuccess) return from_cuda(e);
     delta_prep_kernel<<<static_cast<unsigned>(tiles), PREP_THREADS, P_SMEM, stream>>>(a, prep, wait_ns);
-    walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, fwd, wait_ns);
+    walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, PREP_STEP, fwd, wait_ns);
     delta_adjoint_kernel<<<static_cast<unsigned>(rows), CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, wait_ns);
     delta_tc_grad_kernel<<<static_cast<unsigned>(tiles), GR_THREADS, GR_SMEM, stream>>>(
-        a, GradTiles{prep, fwd.states, bwd.states, fwd.rows, bwd.rows, a.grad_A ? shares : nullptr}, wait_ns);
+        a, GradTiles{prep, fwd.states, bwd.states, fwd.rows, bwd.rows, a.grad_A ? shares : nullptr, sm_count()}, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.grad_A) return from_cuda(e);
     return from_cuda(sum_rows(shares, slots, a.H, a.grad_A, nullptr, a.H, stream));
 }
