@@ -1313,8 +1313,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
     const char* adjoint = in.adjoints + tile * STATE_BYTES;
     if (tid == 0) {
         for (uint64_t* b : {in_ry, in_s, done_a, done_b, done_c, done_d}) mbar_init(b, 1);
-        for (uint64_t* b : {have_ry, have_s, have_d}) mbar_init(b, GR_WARPS);
-        mbar_init(have_p, GR_WARPS / 2);
+        for (uint64_t* b : {have_ry, have_s, have_p, have_d}) mbar_init(b, GR_WARPS);
         mbar_init_fence();
         *dead = 0;
         const char* prep = in.prep + tile * PREP_STEP;
@@ -1455,94 +1454,101 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             }
             arrive(have_ry);
         }
+        float d_up;
         {   // <S0, D1>, and S0 in halves
-            float2 x[16];
-            float dot = 0.f, top = 0.f;
+            float4 g[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = __ldg(reinterpret_cast<const float4*>(adjoint + at_f(i, 8 * quarter + e)));
+            float dot = 0.f, top = 0.f, d_top = 0.f;
             wait_warp(in_s);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float4 f = *reinterpret_cast<const float4*>(smem + GR_S + at_f(i, 8 * quarter + e));
-                const float4 g = *reinterpret_cast<const float4*>(adjoint + at_f(i, 8 * quarter + e));
-                x[2 * e] = make_float2(f.x, f.y);
-                x[2 * e + 1] = make_float2(f.z, f.w);
-                dot = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, dot))));
+                dot = fmaf(f.x, g[e].x, fmaf(f.y, g[e].y, fmaf(f.z, g[e].z, fmaf(f.w, g[e].w, dot))));
                 top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+                d_top = fmaxf(fmaxf(d_top, fmaxf(fabsf(g[e].x), fabsf(g[e].y))), fmaxf(fabsf(g[e].z), fabsf(g[e].w)));
+                g[e] = f;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
             if (lane == 0) ssum[warp] = dot;
             scale_of(block_top(tops + 2 * GR_WARPS, top, 1, GR_WARPS * 32, GR_WARPS, warp), up, s_down);
+            scale_of(block_top(tops + 4 * GR_WARPS, d_top, 1, GR_WARPS * 32, GR_WARPS, warp), d_up, d_down);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+                const float2 x[4] = {make_float2(g[2 * e].x, g[2 * e].y), make_float2(g[2 * e].z, g[2 * e].w),
+                                     make_float2(g[2 * e + 1].x, g[2 * e + 1].y), make_float2(g[2 * e + 1].z, g[2 * e + 1].w)};
                 unsigned char* to = smem + GR_S + at_d(i, 4 * quarter + e);
-                half_pieces(to, to + D * D * 2, x + 4 * e, up);
+                half_pieces(to, to + D * D * 2, x, up);
             }
             arrive(have_s);
         }
-        if (q4 < 2) {   // dP^T, dG^T: row s, 32 tokens of one of the two
-            const int s = 32 * q4 + lane, which = part >> 1, tc = 32 * (part & 1);
+        {   // dP^T, dG^T.  Their sums lie in 64 lanes of tensor memory, half of the warps': those copy them to where
+            // dP and dG will be, as [s][t], and all warps take 16 tokens of a row s of one of the two
+            unsigned char* raw = smem + GR_P;
+            if (q4 < 2) {
+                wait_warp(done_a);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    float2 x[8];
+                    tmem_get16(tl + CG_A + 32 * part + 16 * p, x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<float4*>(raw + ((8 * part + 4 * p + e) * C + 32 * q4 + lane) * 16) =
+                            make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y);
+                }
+                tc_fence_before_sync();
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(GR_WARPS * 32) : "memory");
+            const int s = tid & (C - 1), g16 = tid / C, which = g16 >> 2, t1 = 16 * (g16 & 3);
             const float sh = gates[G_HI + s], sl = gates[G_LO + s];
             const float bs = gates[G_BETA + s] * r_down * (which == 1 ? -y_down : gates[G_XDN]);
-            float2 x[2][8];
-            wait_warp(done_a);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int t1 = tc + 16 * p;
-                tmem_get16(tl + CG_A + which * C + t1, x[p]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = t1 + 2 * e;
-                    const float2 gh = *reinterpret_cast<const float2*>(gates + G_HI + t);
-                    const float2 gl = *reinterpret_cast<const float2*>(gates + G_LO + t);
-                    if (which == 1) {   // R_s . Y_s
-                        const float2 gb = *reinterpret_cast<const float2*>(gates + G_BETA + t);
-                        if (t == s && s < m)
-                            static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[p][e].x * r_down * y_down);
-                        if (t + 1 == s && s < m)
-                            static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] = __float2bfloat16_rn(x[p][e].y * r_down * y_down);
-                        x[p][e] = __fmul2_rn(x[p][e], gb);
-                    }
-                    const int first = which == 1 ? s + 1 : s;
-                    const float w0 = bs * ex2((gh.x - sh) + (gl.x - sl)), w1 = bs * ex2((gh.y - sh) + (gl.y - sl));
-                    x[p][e].x = t >= first ? x[p][e].x * w0 : 0.f;
-                    x[p][e].y = t + 1 >= first ? x[p][e].y * w1 : 0.f;
-                }
-            }
-            scale_of(block_top(tops + 3 * GR_WARPS, largest(largest(0.f, x[0]), x[1]), 2, GR_WARPS / 2 * 32, GR_WARPS / 2,
-                               2 * part + q4), up, p_down);
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    unsigned char* to = smem + GR_P + at_d(s, which * (C / 8) + (tc + 16 * p) / 8 + e);
-                    half_pieces(to, to + C * 2 * C * 2, x[p] + 4 * e, up);
-                }
-            arrive(have_p);
-        }
-        wait_warp(done_b);
-        {   // D1 in halves, where S0 was
-            float2 x[16];
-            float top = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float4 g = *reinterpret_cast<const float4*>(adjoint + at_f(i, 8 * quarter + e));
-                x[2 * e] = make_float2(g.x, g.y);
-                x[2 * e + 1] = make_float2(g.z, g.w);
-                top = fmaxf(fmaxf(top, fmaxf(fabsf(g.x), fabsf(g.y))), fmaxf(fabsf(g.z), fabsf(g.w)));
-            }
-            scale_of(block_top(tops + 4 * GR_WARPS, top, 1, GR_WARPS * 32, GR_WARPS, warp), up, d_down);
+            float2 x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+                const float4 f = *reinterpret_cast<const float4*>(raw + ((4 * g16 + e) * C + s) * 16);
+                x[2 * e] = make_float2(f.x, f.y);
+                x[2 * e + 1] = make_float2(f.z, f.w);
+            }
+            const int first = which == 1 ? s + 1 : s;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int t = t1 + 2 * e;
+                const float2 gh = *reinterpret_cast<const float2*>(gates + G_HI + t);
+                const float2 gl = *reinterpret_cast<const float2*>(gates + G_LO + t);
+                if (which == 1) {   // R_s . Y_s
+                    const float2 gb = *reinterpret_cast<const float2*>(gates + G_BETA + t);
+                    if ((t == s || t + 1 == s) && s < m)
+                        static_cast<__nv_bfloat16*>(a.grad_beta)[tok + s] =
+                            __float2bfloat16_rn((t == s ? x[e].x : x[e].y) * r_down * y_down);
+                    x[e] = __fmul2_rn(x[e], gb);
+                }
+                const float w0 = bs * ex2((gh.x - sh) + (gl.x - sl)), w1 = bs * ex2((gh.y - sh) + (gl.y - sl));
+                x[e].x = t >= first ? x[e].x * w0 : 0.f;
+                x[e].y = t + 1 >= first ? x[e].y * w1 : 0.f;
+            }
+            // (the exchange's barrier is past every thread's loads)
+            scale_of(block_top(tops + 3 * GR_WARPS, largest(0.f, x), 1, GR_WARPS * 32, GR_WARPS, warp), up, p_down);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                unsigned char* to = smem + GR_P + at_d(s, 2 * g16 + e);
+                half_pieces(to, to + C * 2 * C * 2, x + 4 * e, up);
+            }
+            arrive(have_p);
+        }
+        {   // D1 in halves, where S0 was
+            float4 g[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = __ldg(reinterpret_cast<const float4*>(adjoint + at_f(i, 8 * quarter + e)));
+            wait_warp(done_b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x[4] = {make_float2(g[2 * e].x, g[2 * e].y), make_float2(g[2 * e].z, g[2 * e].w),
+                                     make_float2(g[2 * e + 1].x, g[2 * e + 1].y), make_float2(g[2 * e + 1].z, g[2 * e + 1].w)};
                 unsigned char* to = smem + GR_S + at_d(i, 4 * quarter + e);
-                half_pieces(to, to + D * D * 2, x + 4 * e, up);
+                half_pieces(to, to + D * D * 2, x, d_up);
             }
             arrive(have_d);
-        }
-        // dP and dG's scale again, from what the eight warps left
-        {
-            const uint32_t t = lane < GR_WARPS / 2 ? __float_as_uint(tops[3 * GR_WARPS + lane]) : 0u;
-            float unused;
-            scale_of(__uint_as_float(__reduce_max_sync(0xffffffffu, t)), unused, p_down);
         }
         const int j = 32 * q4 + lane;
         const float kdn = gates[G_KDN], qdn = gates[G_QDN];
