@@ -217,17 +217,54 @@ __global__ void __launch_bounds__(ALONE ? WARPS * 32 : 1024) add_norm_kernel(con
 
 // ---- backward ----------------------------------------------------------------
 
-constexpr int BACK_ROWS = 4;                 // rows in flight
 constexpr int BACK_CTAS = 8;                 // CTAs to an SM at most (their shares of grad_w are read once more)
 
+// VEC consecutive elements as they lie in memory.
+template <int VEC, typename T>
+struct Raw {
+    uint4 w[VEC * sizeof(T) / 16];
+    __device__ __forceinline__ void get(const T* p) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(VEC * sizeof(T) / 16); ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void to(float (&f)[VEC]) const {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t u = i == 0 ? w[0].x : i == 1 ? w[0].y : i == 2 ? w[0].z : w[0].w;
+                f[2 * i] = __uint_as_float(u << 16);
+                f[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[4 * i] = __uint_as_float(w[i].x);
+                f[4 * i + 1] = __uint_as_float(w[i].y);
+                f[4 * i + 2] = __uint_as_float(w[i].z);
+                f[4 * i + 3] = __uint_as_float(w[i].w);
+            }
+        }
+    }
+};
+template <typename T>
+struct Raw<1, T> {
+    T v;
+    __device__ __forceinline__ void get(const T* p) { v = *p; }
+    __device__ __forceinline__ void to(float (&f)[1]) const { f[0] = static_cast<float>(v); }
+};
+
 // blockDim.x threads have VEC columns each of one slice of blockDim.x * VEC
-// columns at a time; a row of one slice stays in registers, a longer one is
-// read twice.
-template <int VEC, typename TX, typename TR, typename TY>
-__global__ void __launch_bounds__(1024) add_norm_back_kernel(const NormArgs a, float* shares, int slices) {
-    __shared__ float part[32][2 * BACK_ROWS];
+// columns at a time; a row of one slice stays in registers, as it came, and the
+// next rows' loads are under way meanwhile; a longer one is read twice.
+// MOST threads: 256 with four rows of 16-bit types in flight or two of others,
+// 1024 (registers for one row of each) where a row is longer.
+template <int VEC, int MOST, typename TX, typename TR, typename TY>
+__global__ void __launch_bounds__(MOST) add_norm_back_kernel(const NormArgs a, float* shares, int slices) {
+    constexpr int ROWS = MOST > 256 ? 1 : sizeof(TR) + sizeof(TY) == 4 ? 4 : 2;
+    __shared__ float part[2][32][2 * ROWS];
     const int C = a.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int step = blockDim.x * VEC, mine = threadIdx.x * VEC;
+    const bool in = mine < C;
     const TR* sum = static_cast<const TR*>(a.residual);
     const TY* gy = static_cast<const TY*>(a.grad_y);
     const TR* gs = static_cast<const TR*>(a.grad_sum);
@@ -237,29 +274,36 @@ __global__ void __launch_bounds__(1024) add_norm_back_kernel(const NormArgs a, f
         acc[e] = 0.f;
         w[e] = 1.f;
     }
-    if (a.weight && mine < C) load<VEC>(a.weight + mine, w);
-    for (long long r0 = static_cast<long long>(blockIdx.x) * BACK_ROWS; r0 < a.rows;
-         r0 += static_cast<long long>(gridDim.x) * BACK_ROWS) {
-        float s[BACK_ROWS][VEC], g[BACK_ROWS][VEC], o[BACK_ROWS][VEC], sums[2 * BACK_ROWS];
+    if (a.weight && in) load<VEC>(a.weight + mine, w);
+    Raw<VEC, TR> rs[ROWS], ro[ROWS];
+    Raw<VEC, TY> rg[ROWS];
+    const long long first = static_cast<long long>(blockIdx.x) * ROWS, stride = static_cast<long long>(gridDim.x) * ROWS;
+    auto fetch = [&](long long r0) {
 #pragma unroll
-        for (int i = 0; i < BACK_ROWS; ++i) {
-            const bool on = r0 + i < a.rows && mine < C;
-            const long long at = (r0 + i) * C + mine;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s[i][e] = g[i][e] = o[i][e] = 0.f;
-            if (on) {
-                load<VEC>(sum + at, s[i]);
-                load<VEC>(gy + at, g[i]);
-                if (gs) load<VEC>(gs + at, o[i]);
+        for (int i = 0; i < ROWS; ++i)
+            if (in && r0 + i < a.rows) {
+                const long long at = (r0 + i) * C + mine;
+                rs[i].get(sum + at);
+                rg[i].get(gy + at);
+                if (gs) ro[i].get(gs + at);
             }
-        }
+    };
+    fetch(first);
+    int turn = 0;
+    for (long long r0 = first; r0 < a.rows; r0 += stride, turn ^= 1) {
+        float sums[2 * ROWS];
 #pragma unroll
-        for (int i = 0; i < BACK_ROWS; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             float q = 0.f, d = 0.f;
+            if (in && r0 + i < a.rows) {
+                float s[VEC], g[VEC];
+                rs[i].to(s);
+                rg[i].to(g);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                q = fmaf(s[i][e], s[i][e], q);
-                d = fmaf(g[i][e] * w[e], s[i][e], d);
+                for (int e = 0; e < VEC; ++e) {
+                    q = fmaf(s[e], s[e], q);
+                    d = fmaf(g[e] * w[e], s[e], d);
+                }
             }
             for (int k = 1; k < slices; ++k) {               // columns that the registers do not hold
                 const int c = k * step + mine;
@@ -280,31 +324,44 @@ __global__ void __launch_bounds__(1024) add_norm_back_kernel(const NormArgs a, f
             sums[2 * i] = warp_sum(q);
             sums[2 * i + 1] = warp_sum(d);
         }
-        if (warps > 1) {
-            __syncthreads();   // the last rows' sums are read
+        if (warps > 1) {   // (two arrays in turn: the last rows' readers are past it when it is written again)
             if (lane == 0)
 #pragma unroll
-                for (int i = 0; i < 2 * BACK_ROWS; ++i) part[warp][i] = sums[i];
+                for (int i = 0; i < 2 * ROWS; ++i) part[turn][warp][i] = sums[i];
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 2 * BACK_ROWS; ++i) sums[i] = warp_sum(lane < warps ? part[lane][i] : 0.f);
+            for (int i = 0; i < 2 * ROWS; ++i) sums[i] = warp_sum(lane < warps ? part[turn][lane][i] : 0.f);
         }
 #pragma unroll
-        for (int i = 0; i < BACK_ROWS; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             if (r0 + i >= a.rows) break;
             const float rstd = rsqrtf(sums[2 * i] / static_cast<float>(C) + a.eps);
             const float mean = sums[2 * i + 1] * rstd / static_cast<float>(C);       // of t . n
-            const long long at = (r0 + i) * C + mine;
-            if (mine < C) {
-                float out[VEC];
+            if (in) {
+                const long long at = (r0 + i) * C + mine;
+                float s[VEC], g[VEC], out[VEC];
+                rs[i].to(s);
+                rg[i].to(g);
+                if (gs) {
+                    ro[i].to(out);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) out[e] = 0.f;
+                }
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float n = s[i][e] * rstd;
-                    acc[e] = fmaf(g[i][e], n, acc[e]);
-                    out[e] = fmaf(rstd, g[i][e] * w[e] - n * mean, o[i][e]);
+                    const float n = s[e] * rstd;
+                    acc[e] = fmaf(g[e], n, acc[e]);
+                    out[e] = fmaf(rstd, g[e] * w[e] - n * mean, out[e]);
                 }
                 if (a.grad_residual) store<VEC>(static_cast<TR*>(a.grad_residual) + at, out);
                 if (a.grad_x) store<VEC>(static_cast<TX*>(a.grad_x) + at, out);
+                const long long next = r0 + stride + i;      // this row's registers are free
+                if (next < a.rows) {
+                    rs[i].get(sum + next * C + mine);
+                    rg[i].get(gy + next * C + mine);
+                    if (gs) ro[i].get(gs + next * C + mine);
+                }
             }
             for (int k = 1; k < slices; ++k) {
                 const int c = k * step + mine;
@@ -325,8 +382,7 @@ __global__ void __launch_bounds__(1024) add_norm_back_kernel(const NormArgs a, f
                 for (int e = 0; e < VEC; ++e) {
                     const float n = sv[e] * rstd;
                     // (the CTA's first row sets the share, its later ones add to it)
-                    if (share) share[e] = r0 == static_cast<long long>(blockIdx.x) * BACK_ROWS && i == 0
-                                              ? gv[e] * n : fmaf(gv[e], n, share[e]);
+                    if (share) share[e] = r0 == first && i == 0 ? gv[e] * n : fmaf(gv[e], n, share[e]);
                     ov[e] = fmaf(rstd, gv[e] * wv[e] - n * mean, ov[e]);
                 }
                 if (a.grad_residual) store<VEC>(static_cast<TR*>(a.grad_residual) + more, ov);
@@ -334,7 +390,7 @@ __global__ void __launch_bounds__(1024) add_norm_back_kernel(const NormArgs a, f
             }
         }
     }
-    if (shares && mine < C) {
+    if (shares && in) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) shares[static_cast<long long>(blockIdx.x) * C + mine + e] = acc[e];
     }
@@ -371,7 +427,7 @@ kdn_status launch_fwd(const NormArgs& a, bool alone, int warps, cudaStream_t str
 
 // CTAs of the backward: enough to fill the device, each with rows enough.
 long long back_blocks(long long rows) {
-    const long long want = (rows + BACK_ROWS - 1) / BACK_ROWS, most = static_cast<long long>(sm_count()) * BACK_CTAS;
+    const long long want = (rows + 3) / 4, most = static_cast<long long>(sm_count()) * BACK_CTAS;
     return want < most ? want : most;
 }
 
@@ -390,15 +446,15 @@ kdn_status norm_fwd_launch(const NormArgs& a, cudaStream_t stream) {
                     const int warps = (a.C + PER - 1) / PER;
                     return launch_fwd<1, 16, TX, TR, TY>(a, warps == 1, warps < 32 ? warps : 32, stream);
                 }
-                // a warp to a row of 2048 where the rows fill the device, else CTAs with one vector a lane
+                // a warp to a row of up to 512, CTAs with one or two vectors a thread beyond: many small
+                // CTAs keep the memory busy while others sum (a warp to 2048 channels took 205 us where
+                // eight warps take the time in the design notes)
                 constexpr int PER = 32 * 8;
-                if (a.C <= 8 * PER && a.rows >= static_cast<long long>(sm_count()) * WARPS) {
-                    if (a.C <= 2 * PER) return launch_fwd<8, 2, TX, TR, TY>(a, true, 1, stream);
-                    if (a.C <= 4 * PER) return launch_fwd<8, 4, TX, TR, TY>(a, true, 1, stream);
-                    return launch_fwd<8, 8, TX, TR, TY>(a, true, 1, stream);
-                }
-                const int one = (a.C + PER - 1) / PER, two = (a.C + 2 * PER - 1) / (2 * PER);
-                if (one <= 8) return launch_fwd<8, 1, TX, TR, TY>(a, one == 1, one, stream);
+                const int one = (a.C + PER - 1) / PER, two = (one + 1) / 2;
+                if (one == 1) return launch_fwd<8, 1, TX, TR, TY>(a, true, 1, stream);
+                if (one == 2 && a.rows >= static_cast<long long>(sm_count()) * WARPS)
+                    return launch_fwd<8, 2, TX, TR, TY>(a, true, 1, stream);
+                if (one <= 16) return launch_fwd<8, 1, TX, TR, TY>(a, false, one, stream);
                 return launch_fwd<8, 2, TX, TR, TY>(a, false, two < 32 ? two : 32, stream);
             };
             if (a.y_dtype == KDN_E4M3) return go(E4m3());
@@ -433,7 +489,8 @@ kdn_status norm_bwd_launch(const NormArgs& a, cudaStream_t stream) {
                     constexpr int VEC = decltype(vec)::value;
                     const int want = (a.C + VEC - 1) / VEC, threads = want < 1024 ? (want + 31) / 32 * 32 : 1024;
                     const int slices = (want + threads - 1) / threads;
-                    add_norm_back_kernel<VEC, TX, TR, TY><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(a, shares, slices);
+                    auto kernel = threads <= 256 ? add_norm_back_kernel<VEC, 256, TX, TR, TY> : add_norm_back_kernel<VEC, 1024, TX, TR, TY>;
+                    kernel<<<static_cast<unsigned>(blocks), threads, 0, stream>>>(a, shares, slices);
                     return from_cuda(cudaGetLastError());
                 };
                 return vectors(a) ? go(std::integral_constant<int, 8>()) : go(std::integral_constant<int, 1>());
