@@ -256,8 +256,9 @@ struct Raw<1, T> {
 // blockDim.x threads have VEC columns each of one slice of blockDim.x * VEC
 // columns at a time; a row of one slice stays in registers, as it came, and the
 // next rows' loads are under way meanwhile; a longer one is read twice.
-// MOST threads: 256 with four rows of 16-bit types in flight or two of others,
-// 1024 (registers for one row of each) where a row is longer.
+// MOST threads: 256 with four rows of 16-bit types in flight or two of others
+// (two and three CTAs to an SM gain 8 % at 2048 bf16 channels and lose a third at
+// 1000 of fp32), 1024 (registers for one row) where a row is longer.
 template <int VEC, int MOST, typename TX, typename TR, typename TY>
 __global__ void __launch_bounds__(MOST) add_norm_back_kernel(const NormArgs a, float* shares, int slices) {
     constexpr int ROWS = MOST > 256 ? 1 : sizeof(TR) + sizeof(TY) == 4 ? 4 : 2;
@@ -446,15 +447,15 @@ kdn_status norm_fwd_launch(const NormArgs& a, cudaStream_t stream) {
                     const int warps = (a.C + PER - 1) / PER;
                     return launch_fwd<1, 16, TX, TR, TY>(a, warps == 1, warps < 32 ? warps : 32, stream);
                 }
-                // a warp to a row of up to 512, CTAs with one or two vectors a thread beyond: many small
-                // CTAs keep the memory busy while others sum (a warp to 2048 channels took 205 us where
-                // eight warps take the time in the design notes)
+                // a warp to a row of up to 512, CTAs beyond with 64 bytes a thread (two vectors
+                // of 16-bit x, one of fp32): many small CTAs keep the memory busy while others sum (32768 x
+                // 2048 bf16: a warp to a row 205 us, eight warps 111 us, four with two vectors 94 us)
                 constexpr int PER = 32 * 8;
                 const int one = (a.C + PER - 1) / PER, two = (one + 1) / 2;
                 if (one == 1) return launch_fwd<8, 1, TX, TR, TY>(a, true, 1, stream);
                 if (one == 2 && a.rows >= static_cast<long long>(sm_count()) * WARPS)
                     return launch_fwd<8, 2, TX, TR, TY>(a, true, 1, stream);
-                if (one <= 16) return launch_fwd<8, 1, TX, TR, TY>(a, false, one, stream);
+                if (one <= 16 && sizeof(TX) == 4) return launch_fwd<8, 1, TX, TR, TY>(a, false, one, stream);
                 return launch_fwd<8, 2, TX, TR, TY>(a, false, two < 32 ? two : 32, stream);
             };
             if (a.y_dtype == KDN_E4M3) return go(E4m3());

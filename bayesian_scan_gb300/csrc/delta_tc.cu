@@ -571,12 +571,13 @@ __device__ __forceinline__ void keep_row(char* tile, int i, int c4, const float2
 }
 
 // Chunks' tiles by one thread: what the preparation left, and v where it is given
-// (with do behind the rest where not); `backwards`: the last chunk first.
+// (with do behind the rest and the last chunk first where not); `zeros`: no values.
 __device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full, uint64_t* empty, const Waits& wait,
-                                            const __nv_bfloat16* v, const char* prep, long long step, int len, int chunks) {
+                                            const __nv_bfloat16* v, bool zeros, const char* prep, long long step, int len,
+                                            int chunks) {
     int sent = -1;                                   // the last one whose copies were issued
     for (int n = 0; n < chunks; ++n) {
-        const int c = v ? n : chunks - 1 - n, st = n & 1, m = min(C, len - c * C);
+        const int c = v ? n : chunks - 1 - n, st = n & 1, m = zeros ? 0 : min(C, len - c * C);
         if (n >= 2) wait(empty + st, ((n >> 1) - 1) & 1);
         if (*wait.dead) break;
         sent = n;
@@ -586,7 +587,7 @@ __device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full,
             for (int e = m * D * 2; e < TILE_X; e += 16) *reinterpret_cast<uint4*>(stage + ST_V + e) = make_uint4(0u, 0u, 0u, 0u);
             mbar_arrive_expect_tx(full + st, PREP_BYTES + m * D * 2);
             bulk_g2s(stage, prep + c * step, PREP_BYTES, full + st);
-            bulk_g2s(stage + ST_V, v + static_cast<long long>(c) * C * D, m * D * 2, full + st);
+            if (m > 0) bulk_g2s(stage + ST_V, v + static_cast<long long>(c) * C * D, m * D * 2, full + st);
         } else {
             mbar_arrive_expect_tx(full + st, PREP_STEP);
             bulk_g2s(stage, prep + c * step, PREP_STEP, full + st);
@@ -603,10 +604,21 @@ struct KeepTiles {
     char* rows;        // ROWS_BYTES a chunk
 };
 
-// KEEP: no outputs, but the state before each chunk and R.
-template <typename TO, bool KEEP>
+// How a walk is cut along the tokens: `parts` parts of `len` chunks.
+struct Parts {
+    int parts, len;
+    const float* starts;   // [rows,parts,dv,dk]: a part's first state (null: one part, from S0)
+    float* ends;           // ENDS: [rows,parts - 1,2,dv,dk]
+};
+// OUTPUTS; TILES: no outputs, but the state before each chunk and R; ENDS: of a
+// part its end alone, from a zero state (N) or, without values, from the
+// identity (M): S behind the part is S M + N whatever S.
+enum Walk { OUTPUTS, TILES, ENDS };
+
+template <typename TO, Walk WALK>
 __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, int prep_bytes,
-                                                                    const KeepTiles keep, long long wait_ns) {
+                                                                    const KeepTiles keep, const Parts cut, long long wait_ns) {
+    constexpr bool KEEP = WALK != OUTPUTS;             // no outputs
     extern __shared__ __align__(128) unsigned char smem[];
     float* tops = reinterpret_cast<float*>(smem + CH_OFF_TOP);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);   // [2] a stage is here
@@ -623,13 +635,22 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     uint32_t* holder = reinterpret_cast<uint32_t*>(read_o + 1);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long sr = blockIdx.x, n = sr / a.H;
+    const int jobs = WALK == ENDS ? 2 * (cut.parts - 1) : cut.parts;   // of a state row
+    const long long sr = blockIdx.x / jobs, n = sr / a.H;
+    const int job = static_cast<int>(blockIdx.x % jobs), piece = WALK == ENDS ? job >> 1 : job;
+    const bool identity = WALK == ENDS && (job & 1);
     const int h = static_cast<int>(sr % a.H);
-    const Span sp = span_of(a, n);
+    Span sp = span_of(a, n);
+    if (cut.parts > 1) {   // this part's tokens and chunks
+        sp.lo += piece * cut.len * C;
+        sp.slot += piece * cut.len;
+        if (sp.hi - sp.lo > cut.len * C) sp.hi = sp.lo + cut.len * C;
+    }
     const int len = max(sp.hi - sp.lo, 0), chunks = (len + C - 1) / C;
     const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(D) * D;
-    const float* S0 = a.S0 ? a.S0 + sr * size : nullptr;
-    float* final_state = !KEEP && a.final_state ? a.final_state + sr * size : nullptr;
+    const float* S0 = WALK == ENDS ? nullptr : cut.starts ? cut.starts + blockIdx.x * size : a.S0 ? a.S0 + sr * size : nullptr;
+    float* final_state = WALK == ENDS ? cut.ends + blockIdx.x * size
+                         : WALK == OUTPUTS && a.final_state && piece == cut.parts - 1 ? a.final_state + sr * size : nullptr;
     if (chunks == 0) {
         if (final_state)
             for (int i = tid; i < size / 4; i += CH_THREADS)
@@ -665,7 +686,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         if (warp > MMA_WARP) {
             // ---- tiles ------------------------------------------------------------------
             if (lane == 0)
-                load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.v) + tok * D,
+                load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.v) + tok * D, identity,
                             prep + (sp.slot * a.H + h) * static_cast<long long>(prep_bytes),
                             static_cast<long long>(a.H) * prep_bytes, len, chunks);
         } else {
@@ -757,7 +778,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (S0) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * D + cb + 16 * p + 2 * e);
+                const int j = cb + 16 * p + 2 * e;
+                if (S0) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * D + j);
+                if (identity) f = make_float4(j == i, j + 1 == i, j + 2 == i, j + 3 == i);
                 S[p][e] = make_float2(f.x, f.y);
                 S[p][e + 1] = make_float2(f.z, f.w);
             }
@@ -820,11 +843,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 }
             }
             arrive(have_s + (part >> 1));
-            if (KEEP) {
+            if (WALK == TILES) {
                 char* to = keep.states + ((sp.slot + c) * a.H + h) * STATE_BYTES;
                 keep_row<8>(to, i, cb / 4, S[0]);
                 keep_row<8>(to, i, cb / 4 + 4, S[1]);
-            } else if (c > 0) {
+            } else if (WALK == OUTPUTS && c > 0) {
                 finish(c - 1, before);
             }
             wait_warp(full + st, (c >> 1) & 1);
@@ -856,7 +879,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 if (KEEP) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) z[e] = __ffma2_rn(x[e], both(f), z[e]);
-                    keep_row<8>(keep.rows + ((sp.slot + c) * a.H + h) * ROWS_BYTES, i, tb / 4, z);
+                    if (WALK == TILES) keep_row<8>(keep.rows + ((sp.slot + c) * a.H + h) * ROWS_BYTES, i, tb / 4, z);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
@@ -885,10 +908,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 }
             }
         }
-        if (!KEEP) {
-            take(chunks - 1);
-            finish(chunks - 1, s_down);
-        }
+        if (WALK != TILES) take(chunks - 1);
+        if (WALK == OUTPUTS) finish(chunks - 1, s_down);
         if (final_state) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -906,6 +927,49 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         tmem_dealloc(tmem, 512);
     }
     if (tid == 0 && *dead) record_error(&g_delta_error, KDN_ERR_TIMEOUT);
+}
+
+// The parts' first states from their ends: S_{p+1} = S_p M_p + N_p.  A CTA has
+// 16 rows of a head's state, a thread two of them by four columns.
+constexpr int FOLD_ROWS = 16, FOLD_THREADS = 256;
+__global__ void __launch_bounds__(FOLD_THREADS) delta_fold_kernel(const float* S0, const float* ends, float* starts, int parts) {
+    __shared__ float S[FOLD_ROWS][D];
+    constexpr int PER = D / FOLD_ROWS;
+    const long long row = blockIdx.x / PER, size = static_cast<long long>(D) * D;
+    const int i0 = static_cast<int>(blockIdx.x % PER) * FOLD_ROWS;
+    const int r = 2 * (threadIdx.x / 32), c = 4 * (threadIdx.x % 32);
+    float4 x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const long long at = static_cast<long long>(i0 + r + e) * D + c;
+        x[e] = S0 ? *reinterpret_cast<const float4*>(S0 + row * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int p = 0; p < parts; ++p) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            *reinterpret_cast<float4*>(&S[r + e][c]) = x[e];
+            *reinterpret_cast<float4*>(starts + (row * parts + p) * size + static_cast<long long>(i0 + r + e) * D + c) = x[e];
+        }
+        if (p == parts - 1) break;
+        __syncwarp();                                  // (a warp's two rows are its own)
+        const float* N = ends + (row * (parts - 1) + p) * 2 * size;
+        const float* M = N + size;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[e] = *reinterpret_cast<const float4*>(N + static_cast<long long>(i0 + r + e) * D + c);
+#pragma unroll 8
+        for (int j = 0; j < D; ++j) {
+            const float4 m = __ldg(reinterpret_cast<const float4*>(M + static_cast<long long>(j) * D + c));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float s = S[r + e][j];
+                x[e].x = fmaf(s, m.x, x[e].x);
+                x[e].y = fmaf(s, m.y, x[e].y);
+                x[e].z = fmaf(s, m.z, x[e].z);
+                x[e].w = fmaf(s, m.w, x[e].w);
+            }
+        }
+        __syncwarp();
+    }
 }
 
 // ---- the adjoint's walk --------------------------------------------------------
@@ -976,7 +1040,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     if (warp >= MMA_WARP) {
         if (warp > MMA_WARP) {
             if (lane == 0)
-                load_chunks(smem, full, empty, wait, nullptr, prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_STEP),
+                load_chunks(smem, full, empty, wait, nullptr, false, prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_STEP),
                             static_cast<long long>(a.H) * PREP_STEP, len, chunks);
         } else {
             constexpr uint32_t ID_T = idesc_f16(128, C), ID_TN = idesc_f16(128, C, false, true),
@@ -1679,7 +1743,42 @@ bool tc_takes(int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
     return in_dtype == KDN_BF16 && dk == D && dv == D && T / (nseq > 0 ? nseq : 1) >= 32;
 }
 
-long long tc_fwd_bytes(int B, int H, int T, int nseq) { return slots_of(B, T, nseq) * H * PREP_BYTES; }
+namespace {
+
+// Few heads and long sequences: parts walk side by side once their first states
+// are known, for which each part but the last is walked twice more (N and M) and
+// the ends are folded one after another.  In units of a chunk's walk: an end's
+// costs 0.8, a fold about one, the launches four.  No split unless it takes three
+// quarters of the time.  (Packed sequences' lengths are the device's.)
+Parts cut_of(int B, int H, int T, int nseq) {
+    Parts best{1, 0, nullptr, nullptr};
+    if (nseq > 0) return best;
+    const long long rows = static_cast<long long>(B) * H, sms = sm_count();
+    const int chunks = (T + C - 1) / C;
+    const auto rounds = [&](long long jobs) { return static_cast<double>((jobs + sms - 1) / sms); };
+    double least = 0.75 * rounds(rows) * chunks;
+    if (rows >= sms) return best;
+    for (int p = 2; p <= 64 && p <= chunks / 2; ++p) {
+        const int len = (chunks + p - 1) / p, parts = (chunks + len - 1) / len;
+        if (parts < 2) break;
+        const double cost = (rounds(rows * parts) + 0.8 * rounds(2 * rows * (parts - 1))) * len + parts + 4.0;
+        if (cost < least) {
+            least = cost;
+            best.parts = parts;
+            best.len = len;
+        }
+    }
+    return best;
+}
+long long rounded(long long bytes) { return (bytes + 255) / 256 * 256; }
+
+}  // namespace
+
+long long tc_fwd_bytes(int B, int H, int T, int nseq) {
+    const Parts cut = cut_of(B, H, T, nseq);
+    const long long rows = static_cast<long long>(B) * H, states = cut.parts > 1 ? rows * (3LL * cut.parts - 2) : 0;
+    return slots_of(B, T, nseq) * H * PREP_BYTES + states * D * D * 4;
+}
 
 kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long wait_ns) {
     const long long blocks = slots_of(a.B, a.T, a.nseq) * a.H;
@@ -1689,15 +1788,24 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     if (e != cudaSuccess) return from_cuda(e);
     delta_prep_kernel<<<static_cast<unsigned>(blocks), PREP_THREADS, P_SMEM, stream>>>(a, ws, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
-    auto kernel = a.out_dtype == KDN_BF16 ? delta_chunk_kernel<__nv_bfloat16, false> : delta_chunk_kernel<float, false>;
+    Parts cut = cut_of(a.B, a.H, a.T, a.nseq);
+    if (cut.parts > 1) {
+        auto kernel = delta_chunk_kernel<float, ENDS>;
+        if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
+        cut.ends = reinterpret_cast<float*>(ws + blocks * PREP_BYTES);
+        float* starts = cut.ends + rows * 2 * (cut.parts - 1) * D * D;
+        kernel<<<static_cast<unsigned>(rows * 2 * (cut.parts - 1)), CH_THREADS, CH_SMEM, stream>>>(a, ws, PREP_BYTES, KeepTiles{},
+                                                                                                  cut, wait_ns);
+        delta_fold_kernel<<<static_cast<unsigned>(rows * (D / FOLD_ROWS)), FOLD_THREADS, 0, stream>>>(a.S0, cut.ends, starts,
+                                                                                                     cut.parts);
+        if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
+        cut.starts = starts;
+    }
+    auto kernel = a.out_dtype == KDN_BF16 ? delta_chunk_kernel<__nv_bfloat16, OUTPUTS> : delta_chunk_kernel<float, OUTPUTS>;
     if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
-    kernel<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, ws, PREP_BYTES, KeepTiles{}, wait_ns);
+    kernel<<<static_cast<unsigned>(rows * cut.parts), CH_THREADS, CH_SMEM, stream>>>(a, ws, PREP_BYTES, KeepTiles{}, cut, wait_ns);
     return from_cuda(cudaGetLastError());
 }
-
-namespace {
-long long rounded(long long bytes) { return (bytes + 255) / 256 * 256; }
-}  // namespace
 
 long long tc_bwd_bytes(int B, int H, int T, int nseq) {
     const long long tiles = slots_of(B, T, nseq) * H;
@@ -1712,7 +1820,7 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     const KeepTiles fwd{prep + tiles * PREP_STEP, prep + tiles * (PREP_STEP + 2 * STATE_BYTES)};
     const KeepTiles bwd{fwd.states + tiles * STATE_BYTES, fwd.rows + tiles * ROWS_BYTES};
     float* shares = reinterpret_cast<float*>(bwd.rows + tiles * ROWS_BYTES);
-    auto walk = delta_chunk_kernel<float, true>;
+    auto walk = delta_chunk_kernel<float, TILES>;
     const std::pair<const void*, int> kernels[] = {{reinterpret_cast<const void*>(delta_prep_kernel), P_SMEM},
                                                    {reinterpret_cast<const void*>(walk), CH_SMEM},
                                                    {reinterpret_cast<const void*>(delta_adjoint_kernel), AD_SMEM},
@@ -1721,7 +1829,7 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     for (const auto& k : kernels)
         if ((e = allow_smem(k.first, k.second)) != cudaSuccess) return from_cuda(e);
     delta_prep_kernel<<<static_cast<unsigned>(tiles), PREP_THREADS, P_SMEM, stream>>>(a, prep, wait_ns);
-    walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, PREP_STEP, fwd, wait_ns);
+    walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, PREP_STEP, fwd, Parts{1, 0, nullptr, nullptr}, wait_ns);
     delta_adjoint_kernel<<<static_cast<unsigned>(rows), CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, wait_ns);
     delta_tc_grad_kernel<<<static_cast<unsigned>(tiles), GR_THREADS, GR_SMEM, stream>>>(
         a, GradTiles{prep, fwd.states, bwd.states, fwd.rows, bwd.rows, a.grad_A ? shares : nullptr, sm_count()}, wait_ns);

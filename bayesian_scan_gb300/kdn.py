@@ -1114,29 +1114,35 @@ def delta_step(q, k, v, beta, d, A, state, new_state=None, out=None, out_dtype=N
     out [B,H,dv] (q's type unless ``out_dtype`` says otherwise)."""
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError(f"q must be [B,H,dk] and v [B,H,dv], got {tuple(q.shape)} and {tuple(v.shape)}")
-    B, H, dk = q.shape
-    dv = v.shape[-1]
+    (B, H, dk), dv, dt = q.shape, v.shape[2], q.dtype
     if (B | H | dk | dv) > _MOST:
         _ints(B, H, dk, dv)
-    it, dt = _dtype_of(q, "q"), q.dtype
+    it = _dtype_of(q, "q")
     if new_state is None:
         new_state = state
     if out is None:
         out = _new(v, out_dtype, stream)
-    _check(q, "q", dt)
-    _check(k, "k", dt, q.shape)
-    _check(v, "v", dt, (B, H, dv))
-    _check(beta, "beta", dt, (B, H))
-    _check(d, "d", dt, (B, H))
-    _check(A, "A", _F32, (H,))
-    _check(state, "state", _F32, (B, H, dv, dk))
-    _check(new_state, "new_state", _F32, (B, H, dv, dk))
-    _check(out, "out", out_dtype, v.shape)
+    # a step is a few microseconds: one expression where all is well, the
+    # messages where it is not
+    heads, rows, states = (B, H), (B, H, dv), (B, H, dv, dk)
+    if not (k.dtype is dt and v.dtype is dt and beta.dtype is dt and d.dtype is dt and A.dtype is _F32
+            and state.dtype is _F32 and new_state.dtype is _F32 and (out_dtype is None or out.dtype is out_dtype)
+            and k.shape == q.shape and v.shape == rows and out.shape == rows and beta.shape == heads
+            and d.shape == heads and A.shape == (H,) and state.shape == states and new_state.shape == states
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and beta.is_contiguous()
+            and d.is_contiguous() and A.is_contiguous() and state.is_contiguous() and new_state.is_contiguous()
+            and out.is_contiguous()):
+        for name, t, dtype, shape in (("q", q, dt, None), ("k", k, dt, q.shape), ("v", v, dt, rows),
+                                      ("beta", beta, dt, heads), ("d", d, dt, heads), ("A", A, _F32, (H,)),
+                                      ("state", state, _F32, states), ("new_state", new_state, _F32, states),
+                                      ("out", out, out_dtype, rows)):
+            _check(t, name, dtype, shape)
     ot = _dtype_of(out, "out")
     if not _here(stream, q, k, v, beta, d, A, state, new_state, out):
         _on_one_device(stream, q=q, k=k, v=v, beta=beta, d=d, A=A, state=state, new_state=new_state, out=out)
-    st = lib.kdn_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(d), _ptr(A), _ptr(state), _ptr(new_state),
-                            _ptr(out), B, H, dk, dv, it, ot, _stream(stream))
+    st = lib.kdn_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(), d.data_ptr(), A.data_ptr(),
+                            state.data_ptr(), new_state.data_ptr(), out.data_ptr(), B, H, dk, dv, it, ot,
+                            _stream(stream))
     if st != KDN_OK:
         raise KdnError(st, "kdn_delta_step")
     return out
@@ -1152,9 +1158,10 @@ def _rows_ld(t, name):
     """(rows, C, elements between rows) of a [..., C] tensor whose channels
     are adjacent and whose rows are evenly apart (dense, or a column slice of
     a wider tensor)."""
-    if t.dim() < 1 or t.shape[-1] < 1:
-        raise ValueError(f"{name} must be [..., C] with C > 0, got {tuple(t.shape)}")
-    C = t.shape[-1]
+    shape = t.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError(f"{name} must be [..., C] with C > 0, got {tuple(shape)}")
+    C = shape[-1]
     rows = t.numel() // C
     if C > _MOST:
         _ints(C)
@@ -1205,7 +1212,7 @@ def add_rms_norm_fwd(x, residual=None, weight=None, eps=1e-6, sum_out=None, out=
     if weight is not None:
         _check(weight, "weight", _F32, (C,))
     if out is None:
-        out = _empty(x.shape, x, out_dtype or x.dtype, stream)
+        out = _new(x, out_dtype, stream)
     else:
         _check(out, "out", out_dtype, x.shape)
     if out.dtype is torch.float8_e4m3fn:

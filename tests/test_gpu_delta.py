@@ -56,6 +56,18 @@ def test_forward(kdn, B, H, T, dk, dv, dt, ot, state):
     assert delta64.far(end, val["final"], err["final"]) <= 1
 
 
+@pytest.mark.parametrize("B,H,T,state", [(1, 2, 2500, True), (1, 1, 2049, False)])
+def test_few_heads_of_long_sequences(kdn, B, H, T, state):
+    # cut along the tokens: parts' ends first, then the parts side by side
+    x, S0, _ = draw(B, H, T, 128, 128, BF16, T, state, rate=0.05)
+    assert kdn.delta_scan_fwd_workspace(B, H, T, 128, 128) > kdn.delta_scan_fwd_workspace(256 * B, H, T, 128, 128) // 256
+    val, err = delta64.delta(**x, S0=S0, split=delta64.SPLIT)
+    out, end = kdn.delta_scan_fwd(**cuda(x), S0=cuda(S0), out_dtype=F32)
+    assert delta64.far(out, val["out"], err["out"]) <= 1 and delta64.far(end, val["final"], err["final"]) <= 1
+    for got, want in ((out, val["out"]), (end, val["final"])):
+        assert float((got.cpu().double() - want).norm() / want.norm()) < 2e-5
+
+
 @pytest.mark.parametrize("B,H,T,dk,dv,dt,ot,state", SHAPES)
 def test_backward(kdn, B, H, T, dk, dv, dt, ot, state):
     x, S0, g = draw(B, H, T, dk, dv, dt, 7 * T + dv, state)
