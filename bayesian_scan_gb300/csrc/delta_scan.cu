@@ -522,8 +522,8 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
             const double x = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += x;
         }
-        const double end = __shfl_sync(0xffffffffu, s, 31);
-        g[0] = s - g[1];
+        const double end = __shfl_sync(0xffffffffu, s, 31), before = __shfl_up_sync(0xffffffffu, s, 1);
+        if (lane > 0) g[0] += before;
         g[1] = s;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

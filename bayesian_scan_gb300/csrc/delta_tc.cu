@@ -92,12 +92,12 @@ __device__ __forceinline__ void scale_of(float m, float& up, float& down) {
 // ... of an input's tile: at most 2^60, so that products of two stay floats.
 __device__ __forceinline__ void input_scale(float m, float& up, float& down) {
     scale_of(fmaxf(m, 0x1p-47f), up, down);
-    if (m != m) up = m;                      // (NaN: what its chunk gives is)
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// The largest magnitude; NaN where there is one.
 __device__ __forceinline__ float largest(float m, const float2 (&x)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+    for (int e = 0; e < 8; ++e) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x[e].x), "f"(x[e].y));
     return m;
 }
 // The instruction descriptor's types: fp16 operands where the bf16 form has bf16's bits.
@@ -141,6 +141,18 @@ __device__ __forceinline__ uint4 to_half(uint4 w, float up) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// 8 bf16 numbers without those that are not finite (0 in their place), and
+// whether there are such.
+__device__ __forceinline__ uint4 finite_bf16(uint4 w, bool& all) {
+    uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t bad = __vcmpeq2(u[e] & 0x7f807f80u, 0x7f807f80u);
+        all = all && bad == 0u;
+        u[e] &= ~bad;
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
 // The largest magnitude of 8 bf16 numbers, as bits of two.
 __device__ __forceinline__ uint32_t largest_bf16(uint32_t m, uint4 w) {
     m = __vmaxu2(m, w.x & 0x7fff7fffu);
@@ -227,6 +239,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P_OFF_GATE + 3 * C * 4);
     uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 1);
     uint32_t* tops = holder + 1;                                 // [4 warps][k, q, do], then [4] of T
+    int* gone = reinterpret_cast<int*>(tops + 16);               // the first token whose k, beta or decay is not finite
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = static_cast<int>(blockIdx.x % a.H);
     const long long slot = blockIdx.x / a.H;
@@ -264,8 +277,8 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
             const double x = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += x;
         }
-        const double end = __shfl_sync(0xffffffffu, s, 31);
-        g[0] = s - g[1];
+        const double end = __shfl_sync(0xffffffffu, s, 31), before = __shfl_up_sync(0xffffffffu, s, 1);
+        if (lane > 0) g[0] += before;            // (not s - g[1]: the second token's may be no number)
         g[1] = s;
         float* gates = reinterpret_cast<float*>(out + PREP_GATES);
 #pragma unroll
@@ -280,7 +293,12 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
             gates[G_HI + t] = gh[t];
             gates[G_LO + t] = gl[t];
         }
-        if (lane == 0) gates[G_END] = exp2f(static_cast<float>(end));
+        const bool fine0 = isfinite(g[0]) && isfinite(b[0]), fine1 = isfinite(g[1]) && isfinite(b[1]);
+        const int first = __reduce_min_sync(0xffffffffu, !fine0 ? 2 * lane : !fine1 ? 2 * lane + 1 : C);
+        if (lane == 0) {
+            gates[G_END] = exp2f(static_cast<float>(end));
+            *gone = first;
+        }
     }
     uint32_t top[3] = {0u, 0u, 0u};
     if (a.grad_out) {
@@ -312,10 +330,40 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
         umma_commit(bar);
     }
     __syncthreads();   // the magnitudes are here
+    uint32_t most3[3];
+#pragma unroll
+    for (int e = 0; e < 3; ++e) most3[e] = max(max(tops[e], tops[3 + e]), max(tops[6 + e], tops[9 + e]));
+    // What is not finite is to spoil its own token's outputs and all behind, nothing before: scales
+    // come from the rest, and the solve leaves out the tokens from the first such k on (0 times NaN
+    // is NaN).  Their own Z is not finite, which the walk looks at.
+    if (max(most3[0], max(most3[1], most3[2])) >= 0x7f80u) {
+        __syncthreads();
+        bool all[3] = {true, true, true};
+        uint32_t t3[3] = {0u, 0u, 0u};
+        for (int i = tid; i < C * (D / 8); i += PREP_THREADS) {
+            bool k_fine = true;
+            t3[0] = largest_bf16(t3[0], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16), k_fine));
+            t3[1] = largest_bf16(t3[1], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + TILE_X + i * 16), all[1]));
+            if (!k_fine) atomicMin(gone, i / (D / 8 * 8) * 8 + i % 8);   // (piece i of the tile: its row)
+            if (a.grad_out && i < m * (D / 8)) {
+                const uint4* g = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D);
+                t3[2] = largest_bf16(t3[2], finite_bf16(g[i], all[2]));
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            const uint32_t x = __reduce_max_sync(0xffffffffu, max(t3[e] >> 16, t3[e] & 0xffffu));
+            if (lane == 0) tops[3 * warp + e] = x;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 3; ++e) most3[e] = max(max(tops[e], tops[3 + e]), max(tops[6 + e], tops[9 + e]));
+    }
+    const int bad = *gone;
     float ups[3], downs[3];
 #pragma unroll
-    for (int e = 0; e < 3; ++e)
-        input_scale(__uint_as_float(max(max(tops[e], tops[3 + e]), max(tops[6 + e], tops[9 + e])) << 16), ups[e], downs[e]);
+    for (int e = 0; e < 3; ++e) input_scale(__uint_as_float(most3[e] << 16), ups[e], downs[e]);
+    if (tid >= bad && tid < C) sb[tid] = 0.f;    // (for the solve; read behind the next barrier)
     for (int i = tid; i < 2 * C * (D / 8); i += PREP_THREADS)
         *reinterpret_cast<uint4*>(out + PREP_KQ + i * 16) =
             to_half(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16), i < C * (D / 8) ? ups[0] : ups[1]);
@@ -354,7 +402,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
                                                  __ffma2_rn(make_float2(l.x, l.y), minus, tl));
                     const float2 w1 = __fadd2_rn(__ffma2_rn(make_float2(h.z, h.w), minus, th),
                                                  __ffma2_rn(make_float2(l.z, l.w), minus, tl));
-                    const int last = reads ? t - 1 : t;
+                    const int last = !reads ? t : t < bad ? t - 1 : -1;
                     x[e] = s <= last ? x[e] * ex2(w0.x) : 0.f;
                     x[e + 1] = s + 1 <= last ? x[e + 1] * ex2(w0.y) : 0.f;
                     x[e + 2] = s + 2 <= last ? x[e + 2] * ex2(w1.x) : 0.f;
@@ -545,11 +593,33 @@ __device__ __forceinline__ void get_column(const __nv_bfloat16* p, float2 (&x)[8
 
 // The largest of a row's four quarters: each puts its own, and all four warps of
 // a lane quarter meet.  (Two arrays in turn: an array's readers are past it when
-// the next but one exchange writes it.)
-__device__ __forceinline__ float row_top(float* tops, float mine, int q4, int part, int i) {
+// the next but one exchange writes it.)  A negative number says that the quarter
+// has values that are not finite; `first`: the first such quarter, or 4.
+__device__ __forceinline__ float row_top(float* tops, float mine, int q4, int part, int i, int* first = nullptr) {
     tops[part * D + i] = mine;
     asm volatile("bar.sync %0, 128;" ::"r"(1 + q4) : "memory");
-    return fmaxf(fmaxf(tops[i], tops[D + i]), fmaxf(tops[2 * D + i], tops[3 * D + i]));
+    const float t[4] = {tops[i], tops[D + i], tops[2 * D + i], tops[3 * D + i]};
+    if (first) {
+        const uint32_t sign = __float_as_uint(t[0]) | __float_as_uint(t[1]) | __float_as_uint(t[2]) | __float_as_uint(t[3]);
+        *first = 4;
+        if (sign >> 31) *first = signbit(t[0]) ? 0 : signbit(t[1]) ? 1 : signbit(t[2]) ? 2 : 3;
+    }
+    return fmaxf(fmaxf(fabsf(t[0]), fabsf(t[1])), fmaxf(fabsf(t[2]), fabsf(t[3])));
+}
+
+__device__ __forceinline__ bool finite(float top) { return top < __int_as_float(0x7f800000); }
+// Takes the values from the first that is not finite (or from `from` on) out of
+// an operand: the place of that one.  In a product its 0 weights would make NaN of
+// the tokens before it.
+__device__ __forceinline__ int cut_off(float2 (&x)[8], int from) {
+    int n = 16;
+#pragma unroll
+    for (int t = 15; t >= 0; --t)
+        if (t >= from || !isfinite(t & 1 ? x[t / 2].y : x[t / 2].x)) n = t;
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+        if (t >= n) (t & 1 ? x[t / 2].y : x[t / 2].x) = 0.f;
+    return n;
 }
 
 // The halves of 16 values times a power of two, one K step.
@@ -786,6 +856,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             }
         TO* out = static_cast<TO*>(a.out) + tok * D + i;
         float s_down = 1.f, w_down = 1.f, u_down = 1.f, end = 1.f;   // of the chunk before: what undoes the scales, e^{g_C}
+        int lost = 16;                                   // ... its tokens here whose outputs are not numbers, from this one on
+        bool row_lost = false;                           // ... and whether the row has such: its state is none either
         auto take = [&](int c) {                         // S behind chunk c
             wait_warp(done_s + (part >> 1), c & 1);
 #pragma unroll
@@ -794,6 +866,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 tmem_get16(tl + COL_S + cb + 16 * p, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[p][e] = __ffma2_rn(x[e], both(w_down), __fmul2_rn(S[p][e], both(end)));
+                if (row_lost) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) S[p][e] = both(__int_as_float(0x7fffffff));
+                }
             }
         };
         auto finish = [&](int c, float before) {         // outputs of chunk c, whose S had the scale `before`
@@ -808,6 +884,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 const float4 g = *reinterpret_cast<const float4*>(gates + G_E + tb + 2 * e);
                 o[e] = __ffma2_rn(o[e], both(fo), __fmul2_rn(__fmul2_rn(q[e], both(fq)), make_float2(g.x, g.y)));
                 o[e + 1] = __ffma2_rn(o[e + 1], both(fo), __fmul2_rn(__fmul2_rn(q[e + 1], both(fq)), make_float2(g.z, g.w)));
+            }
+            if (lost < 16) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    if (t >= lost) (t & 1 ? o[t / 2].y : o[t / 2].x) = __int_as_float(0x7fffffff);
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -868,7 +949,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                     x[e] = __fmul2_rn(make_float2(b.x, b.y), z[e]);
                     x[e + 1] = __fmul2_rn(make_float2(b.z, b.w), z[e + 1]);
                 }
-                scale_of(row_top(tops2, largest(0.f, x), q4, part, i), up, z_down);
+                int mine = 16, first;
+                float top = largest(0.f, x);
+                if (!finite(top)) {
+                    mine = cut_off(x, 16);
+                    top = largest(0.f, x);
+                }
+                scale_of(row_top(tops2, mine < 16 ? -top : top, q4, part, i, &first), up, z_down);
+                lost = first < part ? 0 : mine;
                 put_scaled(tl + COL_W + tb, x, up);
                 arrive(have_z);
             }
@@ -879,6 +967,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 if (KEEP) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) z[e] = __ffma2_rn(x[e], both(f), z[e]);
+                    if (lost < 16) {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t)
+                            if (t >= lost) (t & 1 ? z[t / 2].y : z[t / 2].x) = __int_as_float(0x7fffffff);
+                    }
                     if (WALK == TILES) keep_row<8>(keep.rows + ((sp.slot + c) * a.H + h) * ROWS_BYTES, i, tb / 4, z);
                 }
 #pragma unroll
@@ -894,7 +987,17 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                     x[e] = __fmul2_rn(make_float2(w.x, w.y), z[e]);
                     x[e + 1] = __fmul2_rn(make_float2(w.z, w.w), z[e + 1]);
                 }
-                scale_of(row_top(tops, largest(0.f, x), q4, part, i), up, w_down);
+                float top = largest(0.f, x);
+                if (lost < 16 || !finite(top)) {
+                    // w u and u are 0 from the first place on where r is none; where w alone is none, the outputs are
+                    lost = cut_off(z, lost);
+                    top = cut_off(x, lost) < lost ? __int_as_float(0x7f800000) : largest(0.f, x);
+                }
+                int first;
+                top = row_top(tops, lost < 16 ? -top : top, q4, part, i, &first);
+                scale_of(top, up, w_down);
+                row_lost = first < 4 || isinf(top);
+                if (first < part) lost = 0;
                 w_down *= gates[G_KDN];
                 put_scaled(tl + COL_W + tb, x, up);
                 arrive(have_w);

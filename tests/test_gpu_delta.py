@@ -110,7 +110,7 @@ OFFSETS = [[0, 1], [0, 5, 5, 70, 71, 200], [3, 64, 128, 130, 257], [0, 0, 0, 300
 def test_packed(kdn, offsets, dk, dv, dt):
     T, H, n = max(offsets[-1], 1) + 7, 2, len(offsets) - 1
     x, S0, g = draw(1, H, T, dk, dv, dt, T, True, n)
-    go, gf = torch.randn(1, H, T, dv, generator=g), torch.randn(n, H, dv, dk, generator=g)
+    go, gf = torch.randn(1, H, T, dv, generator=g).to(dt), torch.randn(n, H, dv, dk, generator=g)
     for name in ("q", "k", "v", "beta", "d"):                # tokens in no sequence are not read
         x[name][:, :, :offsets[0]] = x[name][:, :, offsets[-1]:] = torch.nan
     go[:, :, :offsets[0]] = go[:, :, offsets[-1]:] = torch.nan
@@ -130,13 +130,14 @@ def test_packed(kdn, offsets, dk, dv, dt):
         assert delta64.far(got[name], val[name], err[name]) <= 1, name
 
 
-def test_offsets_out_of_order_stay_in_bounds(kdn):
+@pytest.mark.parametrize("dk,dt", [(64, F32), (128, BF16)])
+def test_offsets_out_of_order_stay_in_bounds(kdn, dk, dt):
     # which tokens are whose is unspecified; nothing outside the tensors is touched, and the call returns
-    x, _, g = draw(1, 2, 150, 64, 64, F32, 5)
+    x, _, g = draw(1, 2, 150, dk, dk, dt, 5)
     for offsets in ([-9, 80, 40, 400, 20], [149, 0, 149, 0], [500, 600], [-5, -3, -1]):
         off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
         kdn.delta_scan_fwd(**cuda(x), offsets=off)
-        kdn.delta_scan_bwd(**cuda(x), grad_out=torch.ones(1, 2, 150, 64, device="cuda"), offsets=off)
+        kdn.delta_scan_bwd(**cuda(x), grad_out=torch.ones(1, 2, 150, dk, device="cuda", dtype=dt), offsets=off)
     torch.cuda.synchronize()
 
 
@@ -190,7 +191,7 @@ def test_gates_at_their_ends(kdn, dk, dt):
     x["d"] = d.to(dt)
     x["A"] = torch.tensor([1.0, 0.01])
     x["beta"][..., ::5], x["beta"][..., 1::5], x["beta"][..., 2::13] = 0.0, 1.0, 2.0
-    go = torch.randn(1, 2, 200, dk, generator=g)
+    go = torch.randn(1, 2, 200, dk, generator=g).to(dt)
     val, err = delta64.delta(**x, S0=S0, grad_out=go, split=split(dk, dk, dt, 200))
     out, end = kdn.delta_scan_fwd(**cuda(x), S0=S0.cuda(), out_dtype=F32)
     assert delta64.far(out, val["out"], err["out"]) <= 1 and delta64.far(end, val["final"], err["final"]) <= 1
@@ -203,13 +204,45 @@ def test_gates_at_their_ends(kdn, dk, dt):
     assert out.isfinite().all() and delta64.far(out[:, :, 50:], cut["out"], err["out"][:, :, 50:]) <= 1
 
 
+@pytest.mark.parametrize("at", [0, 37, 63, 64, 150])
+@pytest.mark.parametrize("name,value", [("q", torch.nan), ("k", torch.nan), ("k", torch.inf), ("v", torch.nan), ("v", -torch.inf),
+                                        ("beta", torch.nan), ("beta", torch.inf), ("d", torch.nan), ("d", -torch.inf)])
+@pytest.mark.parametrize("dk,dt", [(128, BF16), (128, F32)])
+def test_what_is_not_finite_spoils_nothing_before_it(kdn, dk, dt, name, value, at):
+    # (padding behind a sequence's tokens may hold anything)
+    x, S0, _ = draw(1, 2, 200, dk, dk, dt, 23, True)
+    val, err = delta64.delta(**x, S0=S0, split=split(dk, dk, dt, 200))
+    where = (0, 1, at, 5) if name in "qkv" else (0, 1, at)
+    x[name] = x[name].clone()
+    x[name][where] = value
+    out, end = kdn.delta_scan_fwd(**cuda(x), S0=S0.cuda(), out_dtype=F32)
+    clean = torch.ones(1, 2, 200, dk, dtype=torch.bool)
+    if name == "q":
+        clean[0, 1, at] = False                              # its own outputs
+    elif name == "v":
+        clean[0, 1, at:, 5] = False                          # its channel from there on
+    else:
+        clean[0, 1, at:] = False
+    fine = torch.where(clean, val["out"], torch.nan)
+    assert delta64.far(out, fine, err["out"]) <= 1
+    assert not out.cpu()[0, 1, at][..., 5].isfinite() and delta64.far(end[:, :1], val["final"][:, :1], err["final"][:, :1]) <= 1
+    if name == "q":
+        assert delta64.far(end, val["final"], err["final"]) <= 1
+    elif name == "v":
+        rest = torch.arange(dk) != 5
+        assert delta64.far(end[:, :, rest], val["final"][:, :, rest], err["final"][:, :, rest]) <= 1
+        assert not end[0, 1, 5].isfinite().any()
+    else:
+        assert not end[0, 1].isfinite().any()
+
+
 @pytest.mark.parametrize("dk,dt", [(128, BF16), (64, F32)])
 def test_same_keys(kdn, dk, dt):
     # one key over and over, beta 1: each write replaces the last one's answer
     x, _, g = draw(1, 1, 150, dk, dk, dt, 13)
     x["k"] = x["k"][:, :, :1].expand_as(x["k"]).contiguous()
     x["beta"] = torch.ones_like(x["beta"])
-    go = torch.randn(1, 1, 150, dk, generator=g)
+    go = torch.randn(1, 1, 150, dk, generator=g).to(dt)
     val, err = delta64.delta(**x, grad_out=go, split=split(dk, dk, dt, 150))
     out, _ = kdn.delta_scan_fwd(**cuda(x), out_dtype=F32)
     assert delta64.far(out, val["out"], err["out"]) <= 1
@@ -223,7 +256,7 @@ def test_as_exact_as_its_types(kdn, dk, dt):
     # beside the worst case: roundings of random sign.  The fp32 outputs of 700 tokens with memories of up to
     # 400: sums of roots, (272 products)^1/2 x (400 tokens)^1/2 half steps of 2^-24 -> 2e-5
     x, S0, g = draw(1, 4, 700, dk, dk, dt, 17, True)
-    go, gf = torch.randn(1, 4, 700, dk, generator=g), torch.randn(1, 4, dk, dk, generator=g)
+    go, gf = torch.randn(1, 4, 700, dk, generator=g).to(dt), torch.randn(1, 4, dk, dk, generator=g)
     val, _ = delta64.delta(**x, S0=S0, grad_out=go, grad_final=gf)
     out, end = kdn.delta_scan_fwd(**cuda(x), S0=S0.cuda(), out_dtype=F32)
     got = kdn.delta_scan_bwd(**cuda(x), grad_out=go.cuda(), S0=S0.cuda(), grad_final_state=gf.cuda())
