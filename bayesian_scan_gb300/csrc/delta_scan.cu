@@ -465,6 +465,32 @@ __device__ __forceinline__ float block_sum(float x, float* share) {
     return s;
 }
 
+// N consecutive floats (N of 1, 2, 4; aligned to N).
+template <int N>
+__device__ __forceinline__ void vec_of(const float* p, float (&x)[N]) {
+    if constexpr (N == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+    } else if constexpr (N == 2) {
+        const float2 f = *reinterpret_cast<const float2*>(p);
+        x[0] = f.x; x[1] = f.y;
+    } else {
+        x[0] = *p;
+    }
+}
+// acc[t] += sum_r A[t][at + r] B[r] of 4 rows r: A's rows in shared memory, the
+// same for the whole warp, one wide load each.
+template <int CJ>
+__device__ __forceinline__ void four_rows(float (&acc)[8][CJ], const float* A, int ld, const float (&B)[4][CJ]) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const float4 a = *reinterpret_cast<const float4*>(A + t * ld);
+#pragma unroll
+        for (int c = 0; c < CJ; ++c)
+            acc[t][c] = fmaf(a.x, B[0][c], fmaf(a.y, B[1][c], fmaf(a.z, B[2][c], fmaf(a.w, B[3][c], acc[t][c]))));
+    }
+}
+
 // A CTA makes one chunk's gradients of one head.  All operands but the states
 // lie in shared memory as fp32; a warp owns 8 tokens and all d_k columns of
 // dq, dk_read and dk_write, so that their dots with q and k stay in the warp.
@@ -611,40 +637,26 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
     {   // dq and dk_read of 8 tokens
         float dq[8][CJ] = {}, kr[8][CJ] = {};
         if (on) {
-            for (int i = 0; i < dv; ++i) {
-                float s0[CJ];
+            for (int i = 0; i < dv; i += 4) {
+                float s0[4][CJ];
 #pragma unroll
-                for (int c = 0; c < CJ; ++c) s0[c] = __ldg(S0 + static_cast<long long>(i) * DK + j + c);
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const float g = sg[(tw + t) * LDV + i], l = sl[(tw + t) * LDV + i];
-#pragma unroll
-                    for (int c = 0; c < CJ; ++c) {
-                        dq[t][c] = fmaf(g, s0[c], dq[t][c]);
-                        kr[t][c] = fmaf(-l, s0[c], kr[t][c]);
-                    }
-                }
+                for (int r = 0; r < 4; ++r) vec_of<CJ>(S0 + static_cast<long long>(i + r) * DK + j, s0[r]);
+                four_rows<CJ>(dq, sg + tw * LDV + i, LDV, s0);
+                four_rows<CJ>(kr, sl + tw * LDV + i, LDV, s0);
             }
 #pragma unroll
             for (int t = 0; t < 8; ++t)
 #pragma unroll
                 for (int c = 0; c < CJ; ++c) {
                     dq[t][c] *= eg[tw + t];
-                    kr[t][c] *= eg[tw + t];
+                    kr[t][c] *= -eg[tw + t];
                 }
-            for (int s = 0; s < tw + 8; ++s) {
-                float kc[CJ];
+            for (int s = 0; s < tw + 8; s += 4) {
+                float kc[4][CJ];
 #pragma unroll
-                for (int c = 0; c < CJ; ++c) kc[c] = sk[s * LDK + j + c];
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const float p = dP[(tw + t) * LDC + s], g = dG[(tw + t) * LDC + s];
-#pragma unroll
-                    for (int c = 0; c < CJ; ++c) {
-                        dq[t][c] = fmaf(p, kc[c], dq[t][c]);
-                        kr[t][c] = fmaf(g, kc[c], kr[t][c]);
-                    }
-                }
+                for (int r = 0; r < 4; ++r) vec_of<CJ>(sk + (s + r) * LDK + j, kc[r]);
+                four_rows<CJ>(dq, dP + tw * LDC + s, LDC, kc);
+                four_rows<CJ>(kr, dG + tw * LDC + s, LDC, kc);
             }
         }
         // dk_write, added to dk_read for dk
@@ -652,16 +664,11 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
 #pragma unroll
         for (int t = 0; t < 8; ++t) fw[t] = 0.f;
         if (on) {
-            for (int i = 0; i < dv; ++i) {
-                float d1[CJ];
+            for (int i = 0; i < dv; i += 4) {
+                float d1[4][CJ];
 #pragma unroll
-                for (int c = 0; c < CJ; ++c) d1[c] = __ldg(D1 + static_cast<long long>(i) * DK + j + c);
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const float u = su[(tw + t) * LDV + i];
-#pragma unroll
-                    for (int c = 0; c < CJ; ++c) kw[t][c] = fmaf(u, d1[c], kw[t][c]);
-                }
+                for (int r = 0; r < 4; ++r) vec_of<CJ>(D1 + static_cast<long long>(i + r) * DK + j, d1[r]);
+                four_rows<CJ>(kw, su + tw * LDV + i, LDV, d1);
             }
 #pragma unroll
             for (int t = 0; t < 8; ++t)
@@ -671,18 +678,18 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
                     fw[t] = fmaf(sk[(tw + t) * LDK + j + c], kw[t][c], fw[t]);
                 }
             for (int t = tw; t < CHUNK; ++t) {
-                float qc[CJ], kc[CJ];
+                float qc[CJ], kc[CJ], p[2][4], g[2][4];
+                vec_of<CJ>(sq + t * LDK + j, qc);
+                vec_of<CJ>(sk + t * LDK + j, kc);
 #pragma unroll
-                for (int c = 0; c < CJ; ++c) {
-                    qc[c] = sq[t * LDK + j + c];
-                    kc[c] = sk[t * LDK + j + c];
+                for (int e = 0; e < 2; ++e) {
+                    vec_of<4>(dP + t * LDC + tw + 4 * e, p[e]);
+                    vec_of<4>(dG + t * LDC + tw + 4 * e, g[e]);
                 }
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const float p = dP[t * LDC + tw + s], g = dG[t * LDC + tw + s];
+                for (int s = 0; s < 8; ++s)
 #pragma unroll
-                    for (int c = 0; c < CJ; ++c) kw[s][c] = fmaf(p, qc[c], fmaf(g, kc[c], kw[s][c]));
-                }
+                    for (int c = 0; c < CJ; ++c) kw[s][c] = fmaf(p[s / 4][s % 4], qc[c], fmaf(g[s / 4][s % 4], kc[c], kw[s][c]));
             }
         }
 #pragma unroll
