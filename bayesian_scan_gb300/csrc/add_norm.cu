@@ -15,8 +15,8 @@
 // Backward: n = s rstd, t = w . grad_y;
 //     grad = rstd (t - n mean(t . n)) + grad_sum,   grad_w = sum_rows grad_y . n.
 // A thread keeps its columns for all rows that its CTA takes, and with them
-// their share of grad_w; ROWS rows are in flight at a time, and their 2 ROWS sums
-// are one exchange.  The CTAs' shares are added in a fixed order (sum_rows.cuh).
+// their share of grad_w; several rows are in flight at a time, and the sums of
+// ROWS rows are one exchange.  The CTAs' shares are added in a fixed order (sum_rows.cuh).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -26,6 +26,7 @@
 
 #include "kdn.h"
 #include "kdn_internal.h"
+#include "kernel_setup.h"
 #include "sum_rows.cuh"
 
 namespace kdn {
@@ -397,6 +398,106 @@ __global__ void __launch_bounds__(MOST) add_norm_back_kernel(const NormArgs a, f
     }
 }
 
+// The same for rows of 16-bit types that up to 256 threads hold (C <= 2048):
+// coming rows lie in a ring in shared memory, a thread's own bytes, which only it
+// writes and reads (no barrier): GROUPS groups of ROWS rows, all but one on their
+// way.  (us in registers and through the ring: 32768 x 2048 145 and 120, 65536 x
+// 512 73 and 61.  Of wider types or rows fewer fit: 32768 x 1000 fp32 104 and 139,
+// 8192 x 8192 bf16 199 and 248.)
+constexpr int RING_ROWS = 2, RING_GROUPS = 4, RING_BYTES = RING_GROUPS * RING_ROWS * 3 * 16;   // a thread's
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+
+template <typename TX>
+__global__ void __launch_bounds__(256) add_norm_back_ring_kernel(const NormArgs a, float* shares) {
+    using T = __nv_bfloat16;
+    constexpr int ROWS = RING_ROWS, GROUPS = RING_GROUPS;
+    __shared__ float part[2][8][2 * ROWS];
+    extern __shared__ __align__(16) unsigned char ring[];
+    const int C = a.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, mine = threadIdx.x * 8;
+    const bool in = mine < C;
+    const T* from[3] = {static_cast<const T*>(a.residual), static_cast<const T*>(a.grad_y), static_cast<const T*>(a.grad_sum)};
+    float acc[8], w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        acc[e] = 0.f;
+        w[e] = 1.f;
+    }
+    if (a.weight && in) load<8>(a.weight + mine, w);
+    const long long first = static_cast<long long>(blockIdx.x) * ROWS, stride = static_cast<long long>(gridDim.x) * ROWS;
+    auto place = [&](int group, int i, int which) {
+        return ring + (((group * ROWS + i) * 3 + which) * blockDim.x + threadIdx.x) * 16;
+    };
+    auto fetch = [&](long long r0, int group) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (in && r0 + i < a.rows)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (k < 2 || from[2]) copy16(place(group, i, k), from[k] + (r0 + i) * C + mine);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int g = 0; g < GROUPS - 1; ++g) fetch(first + g * stride, g);
+    int now = 0, turn = 0;
+    for (long long r0 = first; r0 < a.rows; r0 += stride, turn ^= 1) {
+        fetch(r0 + (GROUPS - 1) * stride, (now + GROUPS - 1) % GROUPS);
+        asm volatile("cp.async.wait_group %0;" ::"n"(GROUPS - 1) : "memory");
+        float s[ROWS][8], g[ROWS][8], sums[2 * ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            float q = 0.f, d = 0.f;
+            if (in && r0 + i < a.rows) {
+                load<8>(reinterpret_cast<const T*>(place(now, i, 0)), s[i]);
+                load<8>(reinterpret_cast<const T*>(place(now, i, 1)), g[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    q = fmaf(s[i][e], s[i][e], q);
+                    d = fmaf(g[i][e] * w[e], s[i][e], d);
+                }
+            }
+            sums[2 * i] = warp_sum(q);
+            sums[2 * i + 1] = warp_sum(d);
+        }
+        if (warps > 1) {   // (two arrays in turn: the last rows' readers are past it when it is written again)
+            if (lane == 0)
+#pragma unroll
+                for (int i = 0; i < 2 * ROWS; ++i) part[turn][warp][i] = sums[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2 * ROWS; ++i) sums[i] = warp_sum(lane < warps ? part[turn][lane][i] : 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (in && r0 + i < a.rows) {
+                const float rstd = rsqrtf(sums[2 * i] / static_cast<float>(C) + a.eps);
+                const float mean = sums[2 * i + 1] * rstd / static_cast<float>(C);   // of t . n
+                const long long at = (r0 + i) * C + mine;
+                float out[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) out[e] = 0.f;
+                if (from[2]) load<8>(reinterpret_cast<const T*>(place(now, i, 2)), out);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float n = s[i][e] * rstd;
+                    acc[e] = fmaf(g[i][e], n, acc[e]);
+                    out[e] = fmaf(rstd, g[i][e] * w[e] - n * mean, out[e]);
+                }
+                if (a.grad_residual) store<8>(static_cast<T*>(a.grad_residual) + at, out);
+                if (a.grad_x) store<8>(static_cast<TX*>(a.grad_x) + at, out);
+            }
+        now = (now + 1) % GROUPS;
+    }
+    if (shares && in) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) shares[static_cast<long long>(blockIdx.x) * C + mine + e] = acc[e];
+    }
+}
+
 // ---- host --------------------------------------------------------------------
 
 template <typename F>
@@ -486,6 +587,16 @@ kdn_status norm_bwd_launch(const NormArgs& a, cudaStream_t stream) {
                 using TX = decltype(tx);
                 using TR = decltype(tr);
                 using TY = decltype(ty);
+                if constexpr (sizeof(TR) == 2 && sizeof(TY) == 2) {
+                    if (vectors(a) && a.C <= 256 * 8) {
+                        const int threads = (a.C / 8 + 31) / 32 * 32;
+                        auto kernel = add_norm_back_ring_kernel<TX>;
+                        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), 256 * RING_BYTES);
+                        if (e != cudaSuccess) return from_cuda(e);
+                        kernel<<<static_cast<unsigned>(blocks), threads, threads * RING_BYTES, stream>>>(a, shares);
+                        return from_cuda(cudaGetLastError());
+                    }
+                }
                 auto go = [&](auto vec) {
                     constexpr int VEC = decltype(vec)::value;
                     const int want = (a.C + VEC - 1) / VEC, threads = want < 1024 ? (want + 31) / 32 * 32 : 1024;
