@@ -114,7 +114,7 @@ kdn_status delta_sizes_check(int B, int H, int T, int dk, int dv, int nseq, kdn_
 
 // What the forward and the backward residual addition check alike.
 kdn_status norm_check(const NormArgs& a) {
-    if (a.rows < 0 || a.C < 1 || a.C > kGatedMaxC || a.x_ld < a.C) return KDN_ERR_INVALID_ARG;
+    if (a.rows < 0 || a.rows > 0x7fffffffLL || a.C < 1 || a.C > kGatedMaxC || a.x_ld < a.C) return KDN_ERR_INVALID_ARG;
     if (a.rows > (1LL << 60) / a.x_ld) return KDN_ERR_INVALID_ARG;
     if (!dtype_ok(a.x_dtype) || !dtype_ok(a.res_dtype)) return KDN_ERR_UNSUPPORTED;
     if (!(a.eps >= 0.f)) return KDN_ERR_INVALID_ARG;
@@ -622,7 +622,7 @@ kdn_status kdn_add_rms_norm_bwd(const void* sum, const float* weight, float eps,
 }
 
 kdn_status kdn_add_rms_norm_bwd_workspace(long long rows, int C, long long* workspace_bytes) {
-    if (rows < 0 || C < 1 || C > kGatedMaxC || rows > (1LL << 60) / C || !workspace_bytes) return KDN_ERR_INVALID_ARG;
+    if (rows < 0 || rows > 0x7fffffffLL || C < 1 || C > kGatedMaxC || !workspace_bytes) return KDN_ERR_INVALID_ARG;
     *workspace_bytes = norm_bwd_workspace_bytes(rows, C);
     return KDN_OK;
 }

@@ -1238,8 +1238,7 @@ def add_rms_norm_fwd(x, residual=None, weight=None, eps=1e-6, sum_out=None, out=
 
 def add_rms_norm_bwd_workspace(rows, C) -> int:
     """Bytes of device workspace ``add_rms_norm_bwd`` needs."""
-    if max(C, rows >> 32) > _MOST:                           # (rows are 64 bits in the C call)
-        _ints(C, rows >> 32)
+    _ints(rows, C)
     n = ctypes.c_longlong(0)
     st = lib.kdn_add_rms_norm_bwd_workspace(rows, C, ctypes.byref(n))
     if st != KDN_OK:

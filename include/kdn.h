@@ -571,8 +571,16 @@ KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, 
  *   T = 0 writes only final_state.  Outputs overlap no input.
  *
  * The state and every sum are fp32; out is rounded once.  alpha_t <= 1 and
- * beta_t |k_t|^2 <= 2 are expected (the state grows otherwise).
- * Deterministic.
+ * beta_t |k_t|^2 <= 2 are expected (the state grows otherwise).  Values that
+ * are not finite spoil the outputs of their token and of those behind it (in v:
+ * of their channel alone), and the final state; none before.  Deterministic.
+ *
+ * bf16 inputs with dk = dv = 128 and 32 tokens or more a sequence (T / nseq, of
+ * packed ones) are taken in chunks of 64 tokens on the tensor cores, with
+ * operands of 22 bits: errors are those of fp32 arithmetic, relative to the
+ * largest terms of a chunk (below 2^-24 of them; what strong decays make smaller
+ * than that beside the rest of its chunk has no bits of its own).  Few heads of
+ * long sequences (not packed ones) are cut along the tokens.
  */
 KDN_API kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const void* beta,
                                       const void* d, const float* A, const float* S0,
@@ -599,12 +607,14 @@ KDN_API kdn_status kdn_delta_scan_fwd_workspace(int B, int H, int T, int dk, int
  *   grad_A    [H] fp32 or NULL, written: summed over batch and tokens
  *   grad_S0   [B,H,dv,dk] ([nseq,H,dv,dk]) fp32 or NULL, written
  *   workspace at least kdn_delta_scan_bwd_workspace bytes (about B*H*T*dv*(dk/8
- *             + 8): each 64th token's state and its adjoint, and two rows a
- *             token), or NULL
+ *             + 8), half as much again where the tensor cores take the call: each
+ *             64th token's state and its adjoint, two rows a token, and what the
+ *             chunks' tokens say of one another), or NULL
  *
  * Sizes, alignment and rules as for the forward.  T = 0 writes grad_S0 (=
  * grad_final_state) and grad_A (= 0).  Sums in fp32, in a fixed order
- * (deterministic).
+ * (deterministic).  The tensor-core form takes the calls that the forward's
+ * does, with bf16 grad_out.
  */
 KDN_API kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const void* beta,
                                       const void* d, const float* A, const float* S0,
@@ -653,9 +663,9 @@ KDN_API kdn_status kdn_delta_step(const void* q, const void* k, const void* v, c
  *   scale     [rows, ceil(C/128)] fp32: for each group of 128 channels its
  *             largest |y| / 448, or 1 where that is 0.  NULL for other types.
  *
- *   rows >= 0, 1 <= C <= 2^28, rows * x_ld < 2^60; element-aligned (16-byte
- *   aligned tensors, C and x_ld multiples of 8, take the widest path).  Outputs overlap no
- *   input otherwise.  The sum of squares is fp32 (|s| < 1e18; without eps,
+ *   0 <= rows < 2^31, 1 <= C <= 2^28, rows * x_ld < 2^60; element-aligned
+ *   (16-byte aligned tensors, C and x_ld multiples of 8, take the widest path).
+ *   Outputs overlap no input otherwise.  What is not finite stays in its row.  The sum of squares is fp32 (|s| < 1e18; without eps,
  *   rows of 1e-18 and less are lost in it).
  */
 KDN_API kdn_status kdn_add_rms_norm_fwd(const void* x, long long x_ld, const void* residual,
