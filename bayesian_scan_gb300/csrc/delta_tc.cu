@@ -1760,35 +1760,44 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
                 cc[2 * e + 1] = fmaf(kj[e].y, kr[e].y, cc[2 * e + 1]);
             }
         }
-        {
-            float2 x[8], y[8], g[8], b[8];
-            float f[16];
+        float c1;
+        {   // what the last product adds to c is f, and comes in with its sums
+            float2 x[8], y[8];
             tmem_get16(tl + CG_W2 + tb, y);
             tmem_get16(tl + CG_A + tb, x);
             const float fq = p_down * qdn, fk = p_down * kdn;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __ffma2_rn(y[e], both(fq), __fmul2_rn(x[e], both(fk)));
+            for (int e = 0; e < 8; ++e) {
+                y[e] = __ffma2_rn(y[e], both(fq), __fmul2_rn(x[e], both(fk)));
+                cc[2 * e] = fmaf(-kj[e].x, y[e].x, cc[2 * e]);
+                cc[2 * e + 1] = fmaf(-kj[e].y, y[e].y, cc[2 * e + 1]);
+                kr[e] = __fadd2_rn(kr[e], y[e]);
+            }
+            c1 = lane_sums(cc, lane);
+        }
+        {
+            float2 x[8], g[8], b[8];
+            float f[16];
             get16(gates + G_W + tb, g);
             get16(gates + G_BETA + tb, b);
+            const float fd = d_down * r_down;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = __fmul2_rn(__fmul2_rn(g[e], both(fd)), b[e]);
             wait_warp(done_d);
             tmem_get16(tl + CG_W + tb, x);
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_k) + (tok + tb) * D + j;
-            const float fd = d_down * r_down;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x[e] = __fmul2_rn(__fmul2_rn(__fmul2_rn(g[e], both(fd)), b[e]), x[e]);
+                x[e] = __fmul2_rn(g[e], x[e]);
                 f[2 * e] = kj[e].x * x[e].x;
                 f[2 * e + 1] = kj[e].y * x[e].y;
-                x[e] = __fadd2_rn(x[e], y[e]);
-                cc[2 * e] = fmaf(-kj[e].x, x[e].x, cc[2 * e]);
-                cc[2 * e + 1] = fmaf(-kj[e].y, x[e].y, cc[2 * e + 1]);
                 x[e] = __fadd2_rn(x[e], kr[e]);
                 if (tb + 2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(x[e].x);
                 if (tb + 2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(x[e].y);
             }
-            const float c1 = lane_sums(cc, lane), f1 = lane_sums(f, lane);
+            const float f1 = lane_sums(f, lane);
             if (lane < 16) {
-                sc[q4 * C + tb + lane] = c1;
+                sc[q4 * C + tb + lane] = c1 - f1;
                 sf[q4 * C + tb + lane] = f1;
             }
         }
