@@ -7,10 +7,10 @@
 // sum of squares and its outputs, so x and the residual are read and s and y
 // written once (8 bytes an element in bf16, bound by HBM).
 //
-// Forward: a warp to a row of up to 2048 channels, whole CTAs of G warps to
-// longer rows and to few rows (a decode batch: latency); no exchange between
-// warps in the first form.  A warp's elements are WHOLE groups of 128, so a
-// group's largest value is a matter of shuffles.
+// Forward: a warp to a row of up to 512 channels, a CTA of G warps to a longer
+// one (or to few rows: a decode batch waits for latency), 64 bytes a thread.  A
+// warp's elements are whole groups of 128, so a group's largest value is a matter
+// of shuffles.
 //
 // Backward: n = s rstd, t = w . grad_y;
 //     grad = rstd (t - n mean(t . n)) + grad_sum,   grad_w = sum_rows grad_y . n.
@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(MOST) add_norm_back_kernel(const NormArgs a, f
 // The same for rows of 16-bit types that up to 256 threads hold (C <= 2048):
 // coming rows lie in a ring in shared memory, a thread's own bytes, which only it
 // writes and reads (no barrier): GROUPS groups of ROWS rows, all but one on their
-// way.  (us in registers and through the ring: 32768 x 2048 145 and 120, 65536 x
-// 512 73 and 61.  Of wider types or rows fewer fit: 32768 x 1000 fp32 104 and 139,
+// way.  (us in registers and through the ring: 32768 x 2048 145 and 112, 65536 x
+// 512 73 and 58.  Of wider types or rows fewer fit: 32768 x 1000 fp32 104 and 139,
 // 8192 x 8192 bf16 199 and 248.)
 constexpr int RING_ROWS = 2, RING_GROUPS = 4, RING_BYTES = RING_GROUPS * RING_ROWS * 3 * 16;   // a thread's
 

@@ -9,8 +9,8 @@
 // two dots S k and S q are sums over those lanes, and a CTA owns ROWS rows of
 // one head.  k, q and v come in tiles of TT tokens by asynchronous copies, one
 // tile ahead.  A token costs 6 d_k flops a row and one trip dot -> shuffles ->
-// u -> update, about 130 cycles: few heads are bound by that trip, many by
-// the FMA rate.  The dot with q reads the state after the token, off that trip.
+// u -> update, about 345 cycles (d_k = 64, few heads): few heads are bound by
+// that trip, many by the FMA rate.  The dot with q reads the state after the token, off that trip.
 //
 // Backward.  The adjoint D_t of S_t walks the other way with the same shape
 // (rows apart, one dot a token), and needs no state:
@@ -758,8 +758,9 @@ constexpr int STEP_THREADS = 256, STEP_UNR = 4;
 // DK / 4 lanes to a state row, four columns a lane; the row's three dots (S k,
 // S q, k q) are one round of shuffles, and o = a S q + u (k.q) needs no second
 // one.  A state element is read and written once: bound by HBM.  UNR rows a
-// lane keep enough loads in flight (decode of 128 x 16 heads of 128: UNR 1, 2
-// and 4 were timed, see the design notes).
+// lane keep more loads in flight where there are many (us of 2048 heads of 128 x
+// 128 with UNR 1, 2, 4: 55.1, 54.9, 53.3, 74 % of what a copy reaches; of 256:
+// 8.05, 8.27, 8.33).
 template <typename TI, typename TO, int DK, int UNR>
 __global__ void __launch_bounds__(STEP_THREADS) delta_step_kernel(const DeltaArgs a, const float* state, float* next) {
     constexpr int LPR = DK / 4, RPW = 32 / LPR;
@@ -863,19 +864,19 @@ struct BackLayout {
 using namespace delta;
 
 long long delta_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
-    return tc_takes(T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, nseq) : 0;
+    return tc_takes_fwd(B, H, T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, nseq) : 0;
 }
 
 long long delta_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
     if (T == 0) return 0;
     const long long bytes = BackLayout(B, H, T, dk, dv, nseq).bytes();
     // (the type of grad_out, which this does not know, decides the form)
-    const long long tc = tc_takes(T, dk, dv, nseq, in_dtype) ? tc_bwd_bytes(B, H, T, nseq) : 0;
+    const long long tc = tc_takes(dk, dv, in_dtype) ? tc_bwd_bytes(B, H, T, nseq) : 0;
     return tc > bytes ? tc : bytes;
 }
 
 kdn_status delta_fwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns) {
-    if (tc_takes(a.T, a.dk, a.dv, a.nseq, a.in_dtype)) {
+    if (tc_takes_fwd(a.B, a.H, a.T, a.dk, a.dv, a.nseq, a.in_dtype)) {
         Scratch scratch(stream);
         char* ws = static_cast<char*>(a.workspace);
         if (!ws) {
@@ -922,7 +923,7 @@ kdn_status delta_bwd_launch(const DeltaArgs& a, cudaStream_t stream, long long w
         if (s != KDN_OK) return s;
         ws = static_cast<char*>(scratch.p);
     }
-    if (tc_takes(a.T, a.dk, a.dv, a.nseq, a.in_dtype) && a.out_dtype == KDN_BF16) return tc_bwd(a, ws, stream, wait_ns);
+    if (tc_takes(a.dk, a.dv, a.in_dtype) && a.out_dtype == KDN_BF16) return tc_bwd(a, ws, stream, wait_ns);
     float* states = reinterpret_cast<float*>(ws);
     float* adjoints = reinterpret_cast<float*>(ws + lay.states);
     float* r = reinterpret_cast<float*>(ws + 2 * lay.states);
@@ -970,7 +971,7 @@ kdn_status delta_step_launch(const DeltaArgs& a, const float* state, float* next
                 return from_cuda(cudaGetLastError());
             };
             // few rows want every SM, many want loads in flight
-            if (rows < static_cast<long long>(NW) * RPW * STEP_UNR * sm_count() * 2) return go(std::integral_constant<int, 1>());
+            if (rows < static_cast<long long>(NW) * RPW * STEP_UNR * sm_count() * 8) return go(std::integral_constant<int, 1>());
             return go(std::integral_constant<int, STEP_UNR>());
         });
     });

@@ -1851,8 +1851,17 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
 
 }  // namespace
 
-bool tc_takes(int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
-    return in_dtype == KDN_BF16 && dk == D && dv == D && T / (nseq > 0 ? nseq : 1) >= 32;
+bool tc_takes(int dk, int dv, kdn_dtype in_dtype) { return in_dtype == KDN_BF16 && dk == D && dv == D; }
+
+// Against the walk token by token (us for heads x tokens, here / there): few heads
+// wait for two launches here, 16 x 48 19.1 / 13.7, 16 x 64 18.3 / 16.9, 16 x 96
+// 21 / 24, 64 x 48 19.3 / 18.3, 64 x 64 18.7 / 22.9; many cost a chunk's work
+// however few its tokens, 128 x 24 20.6 / 20.0, 256 x 16 34 / 25, 256 x 32 33 / 41,
+// 2048 x 16 211 / 157, 2048 x 32 204 / 264.  (Backward calls gain at any length: 16
+// x 8 44 / 65, 2048 x 8 546 / 1140, 2048 x 256 1620 / 7740.)
+bool tc_takes_fwd(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
+    const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
+    return tc_takes(dk, dv, in_dtype) && T / (nseq > 0 ? nseq : 1) >= (rows <= 64 ? 64 : 28);
 }
 
 namespace {

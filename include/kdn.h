@@ -575,8 +575,8 @@ KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, 
  * are not finite spoil the outputs of their token and of those behind it (in v:
  * of their channel alone), and the final state; none before.  Deterministic.
  *
- * bf16 inputs with dk = dv = 128 and 32 tokens or more a sequence (T / nseq, of
- * packed ones) are taken in chunks of 64 tokens on the tensor cores, with
+ * bf16 inputs with dk = dv = 128 and 64 tokens or more a sequence (T / nseq, of
+ * packed ones; 28 with more than 64 heads in all) are taken in chunks of 64 tokens on the tensor cores, with
  * operands of 22 bits: errors are those of fp32 arithmetic, relative to the
  * largest terms of a chunk (below 2^-24 of them; what strong decays make smaller
  * than that beside the rest of its chunk has no bits of its own).  Few heads of
@@ -613,8 +613,8 @@ KDN_API kdn_status kdn_delta_scan_fwd_workspace(int B, int H, int T, int dk, int
  *
  * Sizes, alignment and rules as for the forward.  T = 0 writes grad_S0 (=
  * grad_final_state) and grad_A (= 0).  Sums in fp32, in a fixed order
- * (deterministic).  The tensor-core form takes the calls that the forward's
- * does, with bf16 grad_out.
+ * (deterministic).  The tensor-core form takes bf16 inputs with dk = dv = 128
+ * and bf16 grad_out, of any length.
  */
 KDN_API kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const void* beta,
                                       const void* d, const float* A, const float* S0,
