@@ -864,7 +864,7 @@ struct BackLayout {
 using namespace delta;
 
 long long delta_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
-    return tc_takes_fwd(B, H, T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, nseq) : 0;
+    return tc_takes_fwd(B, H, T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, dk, dv, nseq) : 0;
 }
 
 long long delta_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
@@ -880,7 +880,7 @@ kdn_status delta_fwd_launch(const DeltaArgs& a, cudaStream_t stream, long long w
         Scratch scratch(stream);
         char* ws = static_cast<char*>(a.workspace);
         if (!ws) {
-            const kdn_status s = scratch.take(tc_fwd_bytes(a.B, a.H, a.T, a.nseq));
+            const kdn_status s = scratch.take(tc_fwd_bytes(a.B, a.H, a.T, a.dk, a.dv, a.nseq));
             if (s != KDN_OK) return s;
             ws = static_cast<char*>(scratch.p);
         }

@@ -117,15 +117,15 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bo
 }
 
 // n tokens of k, then of q, as one tile of 2 x 64 rows (zeros behind the last
-// token), by `threads` threads.  A warp instruction moves 8 tokens x 4 of
+// token and the last of dk columns), by `threads` threads.  A warp instruction moves 8 tokens x 4 of
 // their 16-byte pieces, so that its writes hit each bank group four times.
-__device__ __forceinline__ void load_kq(uint32_t tile, const __nv_bfloat16* k, const __nv_bfloat16* q, int n, int tid,
-                                        int threads) {
+__device__ __forceinline__ void load_kq(uint32_t tile, const __nv_bfloat16* k, const __nv_bfloat16* q, int n, int dk,
+                                        int tid, int threads) {
     const int lane = tid & 31, a = lane & 7, b = lane >> 3;
     for (int w = tid >> 5; w < 2 * C / 8 * 4; w += threads >> 5) {
         const int r = (w >> 2) * 8 + a, c8 = (w & 3) * 4 + b, t = r & (C - 1);
-        const __nv_bfloat16* src = (r < C ? k : q) + (t < n ? static_cast<long long>(t) * D : 0) + c8 * 8;
-        copy16_or_zero(tile + at_d(r, c8), src, t < n);
+        const bool there = t < n && c8 * 8 < dk;
+        copy16_or_zero(tile + at_d(r, c8), (r < C ? k : q) + (there ? static_cast<long long>(t) * dk + c8 * 8 : 0), there);
     }
 }
 
@@ -159,6 +159,14 @@ __device__ __forceinline__ uint32_t largest_bf16(uint32_t m, uint4 w) {
     m = __vmaxu2(m, w.y & 0x7fff7fffu);
     m = __vmaxu2(m, w.z & 0x7fff7fffu);
     return __vmaxu2(m, w.w & 0x7fff7fffu);
+}
+
+// Piece i (of 8 columns) of rows of D, of which there are dv in memory and zeros behind.
+template <bool FULL>
+__device__ __forceinline__ uint4 piece(const __nv_bfloat16* p, int i, int dv) {
+    if (FULL) return reinterpret_cast<const uint4*>(p)[i];
+    const int c = i % (D / 8) * 8;
+    return c < dv ? *reinterpret_cast<const uint4*>(p + static_cast<long long>(i / (D / 8)) * dv + c) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ---- preparation -------------------------------------------------------------
@@ -229,6 +237,7 @@ __device__ __forceinline__ void join_blocks(float* sT, const float* sN, float* s
 //     T21 = -(1 + T2 beta2) G21 (1 + beta1 T1),
 // from 16 x 16 blocks that a warp solves row after row.  No power of G is
 // formed: keys that are alike make those large.
+template <bool FULL>
 __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArgs a, char* prep, long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
     float* sG = reinterpret_cast<float*>(smem + P_OFF_G);        // [t][s]
@@ -250,8 +259,10 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     const int bytes = a.grad_out ? PREP_STEP : PREP_BYTES;
     char* out = prep + (slot * a.H + h) * static_cast<long long>(bytes);
 
-    load_kq(smem_addr(smem), static_cast<const __nv_bfloat16*>(a.k) + tok * D,
-            static_cast<const __nv_bfloat16*>(a.q) + tok * D, m, tid, PREP_THREADS);
+    const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+    const __nv_bfloat16* go = static_cast<const __nv_bfloat16*>(a.grad_out) + (a.grad_out ? tok * dv : 0);
+    load_kq(smem_addr(smem), static_cast<const __nv_bfloat16*>(a.k) + tok * dk,
+            static_cast<const __nv_bfloat16*>(a.q) + tok * dk, m, dk, tid, PREP_THREADS);
     if (warp == 0) {
         tmem_alloc(holder, 64);
     } else if (warp == 1) {
@@ -301,10 +312,8 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
         }
     }
     uint32_t top[3] = {0u, 0u, 0u};
-    if (a.grad_out) {
-        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D);
-        for (int i = tid; i < m * (D / 8); i += PREP_THREADS) top[2] = largest_bf16(top[2], g[i]);
-    }
+    if (a.grad_out)
+        for (int i = tid; i < m * (D / 8); i += PREP_THREADS) top[2] = largest_bf16(top[2], piece<FULL>(go, i, dv));
     copies_done();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before_sync();
@@ -345,10 +354,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
             t3[0] = largest_bf16(t3[0], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16), k_fine));
             t3[1] = largest_bf16(t3[1], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + TILE_X + i * 16), all[1]));
             if (!k_fine) atomicMin(gone, i / (D / 8 * 8) * 8 + i % 8);   // (piece i of the tile: its row)
-            if (a.grad_out && i < m * (D / 8)) {
-                const uint4* g = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D);
-                t3[2] = largest_bf16(t3[2], finite_bf16(g[i], all[2]));
-            }
+            if (a.grad_out && i < m * (D / 8)) t3[2] = largest_bf16(t3[2], finite_bf16(piece<FULL>(go, i, dv), all[2]));
         }
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
@@ -368,10 +374,9 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
         *reinterpret_cast<uint4*>(out + PREP_KQ + i * 16) =
             to_half(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16), i < C * (D / 8) ? ups[0] : ups[1]);
     if (a.grad_out) {
-        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.grad_out) + tok * D);
         for (int i = tid; i < C * (D / 8); i += PREP_THREADS) {
             const int t = i / (D / 8), c8 = i % (D / 8);
-            *reinterpret_cast<uint4*>(out + PREP_BYTES + at_d(t, c8)) = t < m ? to_half(g[i], ups[2]) : make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(out + PREP_BYTES + at_d(t, c8)) = t < m ? to_half(piece<FULL>(go, i, dv), ups[2]) : make_uint4(0u, 0u, 0u, 0u);
         }
     }
     const bool ok = mbar_wait(bar, 0, wait_ns);
@@ -643,8 +648,8 @@ __device__ __forceinline__ void keep_row(char* tile, int i, int c4, const float2
 // Chunks' tiles by one thread: what the preparation left, and v where it is given
 // (with do behind the rest and the last chunk first where not); `zeros`: no values.
 __device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full, uint64_t* empty, const Waits& wait,
-                                            const __nv_bfloat16* v, bool zeros, const char* prep, long long step, int len,
-                                            int chunks) {
+                                            const __nv_bfloat16* v, int dv, bool zeros, const char* prep, long long step,
+                                            int len, int chunks) {
     int sent = -1;                                   // the last one whose copies were issued
     for (int n = 0; n < chunks; ++n) {
         const int c = v ? n : chunks - 1 - n, st = n & 1, m = zeros ? 0 : min(C, len - c * C);
@@ -655,9 +660,14 @@ __device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full,
         if (v) {
             // rows as they are; no token: zeros, not what lay there before
             for (int e = m * D * 2; e < TILE_X; e += 16) *reinterpret_cast<uint4*>(stage + ST_V + e) = make_uint4(0u, 0u, 0u, 0u);
-            mbar_arrive_expect_tx(full + st, PREP_BYTES + m * D * 2);
+            mbar_arrive_expect_tx(full + st, PREP_BYTES + m * dv * 2);
             bulk_g2s(stage, prep + c * step, PREP_BYTES, full + st);
-            if (m > 0) bulk_g2s(stage + ST_V, v + static_cast<long long>(c) * C * D, m * D * 2, full + st);
+            const __nv_bfloat16* src = v + static_cast<long long>(c) * C * dv;
+            if (dv == D) {
+                if (m > 0) bulk_g2s(stage + ST_V, src, m * D * 2, full + st);
+            } else {   // (the columns behind are zeros from the start)
+                for (int t = 0; t < m; ++t) bulk_g2s(stage + ST_V + t * D * 2, src + t * dv, dv * 2, full + st);
+            }
         } else {
             mbar_arrive_expect_tx(full + st, PREP_STEP);
             bulk_g2s(stage, prep + c * step, PREP_STEP, full + st);
@@ -685,7 +695,7 @@ struct Parts {
 // identity (M): S behind the part is S M + N whatever S.
 enum Walk { OUTPUTS, TILES, ENDS };
 
-template <typename TO, Walk WALK>
+template <typename TO, Walk WALK, bool FULL>
 __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaArgs a, const char* prep, int prep_bytes,
                                                                     const KeepTiles keep, const Parts cut, long long wait_ns) {
     constexpr bool KEEP = WALK != OUTPUTS;             // no outputs
@@ -717,7 +727,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         if (sp.hi - sp.lo > cut.len * C) sp.hi = sp.lo + cut.len * C;
     }
     const int len = max(sp.hi - sp.lo, 0), chunks = (len + C - 1) / C;
-    const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(D) * D;
+    const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+    const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(dv) * dk;
     const float* S0 = WALK == ENDS ? nullptr : cut.starts ? cut.starts + blockIdx.x * size : a.S0 ? a.S0 + sr * size : nullptr;
     float* final_state = WALK == ENDS ? cut.ends + blockIdx.x * size
                          : WALK == OUTPUTS && a.final_state && piece == cut.parts - 1 ? a.final_state + sr * size : nullptr;
@@ -740,6 +751,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         mbar_init_fence();
         *dead = 0;
     }
+    if (!FULL && dv < D) {   // zeros behind v's columns in both stages
+        for (int e = tid; e < 2 * TILE_X / 16; e += CH_THREADS)
+            *reinterpret_cast<uint4*>(smem + e / (TILE_X / 16) * STAGE_BYTES + ST_V + e % (TILE_X / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
     if (warp == MMA_WARP) tmem_alloc(holder, 512);
     tc_fence_before_sync();
     __syncthreads();
@@ -756,7 +772,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         if (warp > MMA_WARP) {
             // ---- tiles ------------------------------------------------------------------
             if (lane == 0)
-                load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.v) + tok * D, identity,
+                load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.v) + tok * dv, dv, identity,
                             prep + (sp.slot * a.H + h) * static_cast<long long>(prep_bytes),
                             static_cast<long long>(a.H) * prep_bytes, len, chunks);
         } else {
@@ -849,12 +865,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 const int j = cb + 16 * p + 2 * e;
-                if (S0) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * D + j);
+                if (S0 && (FULL || (i < dv && j < dk))) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * dk + j);
                 if (identity) f = make_float4(j == i, j + 1 == i, j + 2 == i, j + 3 == i);
                 S[p][e] = make_float2(f.x, f.y);
                 S[p][e + 1] = make_float2(f.z, f.w);
             }
-        TO* out = static_cast<TO*>(a.out) + tok * D + i;
+        TO* out = static_cast<TO*>(a.out) + tok * dv + i;
         float s_down = 1.f, w_down = 1.f, u_down = 1.f, end = 1.f;   // of the chunk before: what undoes the scales, e^{g_C}
         int lost = 16;                                   // ... its tokens here whose outputs are not numbers, from this one on
         bool row_lost = false;                           // ... and whether the row has such: its state is none either
@@ -896,12 +912,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 mbar_arrive(read_o);
                 mbar_arrive(empty + (c & 1));
             }
-            const int m = len - c * C - tb;
-            TO* dst = out + (static_cast<long long>(c) * C + tb) * D;
+            const int m = FULL || i < dv ? len - c * C - tb : 0;
+            TO* dst = out + (static_cast<long long>(c) * C + tb) * dv;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (2 * e < m) dst[2 * e * D] = from_f32<TO>(o[e].x);
-                if (2 * e + 1 < m) dst[(2 * e + 1) * D] = from_f32<TO>(o[e].y);
+                if (2 * e < m) dst[2 * e * dv] = from_f32<TO>(o[e].x);
+                if (2 * e + 1 < m) dst[(2 * e + 1) * dv] = from_f32<TO>(o[e].y);
             }
         };
         for (int c = 0; c < chunks; ++c) {
@@ -1016,7 +1032,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         if (final_state) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float* dst = final_state + static_cast<long long>(i) * D + cb + 16 * p;
+                float* dst = final_state + static_cast<long long>(i) * dk + cb + 16 * p;
+                if (!FULL && (i >= dv || cb + 16 * p >= dk)) continue;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
                     *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(S[p][e].x, S[p][e].y, S[p][e + 1].x, S[p][e + 1].y);
@@ -1085,6 +1102,7 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_kernel(const float* S
 // lies in COL_W until beta dU's halves do; e^g dO is an operand in shared memory.
 constexpr uint32_t COL_X = 320;              // dO^T (e^g Q), 128 columns
 
+template <bool FULL>
 __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const DeltaArgs a, const char* prep, const KeepTiles keep,
                                                                       long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -1106,7 +1124,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     const int h = static_cast<int>(sr % a.H);
     const Span sp = span_of(a, n);
     const int len = max(sp.hi - sp.lo, 0), chunks = (len + C - 1) / C;
-    const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(D) * D;
+    const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+    const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(dv) * dk;
     const float* D1 = a.grad_final_state ? a.grad_final_state + sr * size : nullptr;
     float* D0 = a.grad_S0 ? a.grad_S0 + sr * size : nullptr;
     if (chunks == 0) {
@@ -1143,7 +1162,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     if (warp >= MMA_WARP) {
         if (warp > MMA_WARP) {
             if (lane == 0)
-                load_chunks(smem, full, empty, wait, nullptr, false, prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_STEP),
+                load_chunks(smem, full, empty, wait, nullptr, D, false, prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_STEP),
                             static_cast<long long>(a.H) * PREP_STEP, len, chunks);
         } else {
             constexpr uint32_t ID_T = idesc_f16(128, C), ID_TN = idesc_f16(128, C, false, true),
@@ -1231,11 +1250,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (D1) f = *reinterpret_cast<const float4*>(D1 + static_cast<long long>(i) * D + cb + 16 * p + 2 * e);
+                if (D1 && (FULL || (i < dv && cb + 16 * p < dk)))
+                    f = *reinterpret_cast<const float4*>(D1 + static_cast<long long>(i) * dk + cb + 16 * p + 2 * e);
                 S[p][e] = make_float2(f.x, f.y);
                 S[p][e + 1] = make_float2(f.z, f.w);
             }
-        __nv_bfloat16* gv = static_cast<__nv_bfloat16*>(a.grad_v) + tok * D + i;
+        __nv_bfloat16* gv = static_cast<__nv_bfloat16*>(a.grad_v) + tok * dv + i;
         float s_down = 1.f, x_down = 1.f, w_down = 1.f, end = 1.f;
         auto take = [&](int c) {                         // D before what was chunk c of the walk
             wait_warp(done_s + (part >> 1), c & 1);
@@ -1347,12 +1367,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
                 arrive(have_w);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + st);
-                const int m = len - chunk * C - tb;
-                __nv_bfloat16* dst = gv + (static_cast<long long>(chunk) * C + tb) * D;
+                const int m = FULL || i < dv ? len - chunk * C - tb : 0;
+                __nv_bfloat16* dst = gv + (static_cast<long long>(chunk) * C + tb) * dv;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(z[e].x);
-                    if (2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(z[e].y);
+                    if (2 * e < m) dst[2 * e * dv] = __float2bfloat16_rn(z[e].x);
+                    if (2 * e + 1 < m) dst[(2 * e + 1) * dv] = __float2bfloat16_rn(z[e].y);
                 }
             }
         }
@@ -1360,7 +1380,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
             take(chunks - 1);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float* dst = D0 + static_cast<long long>(i) * D + cb + 16 * p;
+                float* dst = D0 + static_cast<long long>(i) * dk + cb + 16 * p;
+                if (!FULL && (i >= dv || cb + 16 * p >= dk)) continue;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
                     *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(S[p][e].x, S[p][e].y, S[p][e + 1].x, S[p][e + 1].y);
@@ -1448,6 +1469,7 @@ __device__ __forceinline__ void half_pieces(unsigned char* hi_at, unsigned char*
     *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
+template <bool FULL>
 __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const DeltaArgs a, const GradTiles in, long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
     float* gates = reinterpret_cast<float*>(smem + GR_GATES);
@@ -1717,7 +1739,8 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             }
             arrive(have_d);
         }
-        const int j = 32 * q4 + lane;
+        const int j = 32 * q4 + lane, dk = FULL ? D : a.dk;
+        const int mine = FULL || j < dk ? m - tb : 0;          // tokens of a column that there is
         const float kdn = gates[G_KDN], qdn = gates[G_QDN];
         float cc[16];
         float2 kr[8], kj[8];
@@ -1736,14 +1759,14 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             tmem_get16(tl + CG_Q + tb, x);
             wait_warp(done_c);
             tmem_get16(tl + CG_Q2 + tb, y);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_q) + (tok + tb) * D + j;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_q) + (tok + tb) * dk + j;
             column(at + TILE_X, qdn, kj);
             const float f = s_down * gates[G_XDN], fp = p_down * kdn;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 y[e] = __ffma2_rn(__fmul2_rn(g[e], both(f)), x[e], __fmul2_rn(y[e], both(fp)));
-                if (tb + 2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(y[e].x);
-                if (tb + 2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(y[e].y);
+                if (2 * e < mine) dst[2 * e * dk] = __float2bfloat16_rn(y[e].x);
+                if (2 * e + 1 < mine) dst[(2 * e + 1) * dk] = __float2bfloat16_rn(y[e].y);
                 cc[2 * e] = kj[e].x * y[e].x;
                 cc[2 * e + 1] = kj[e].y * y[e].y;
             }
@@ -1785,15 +1808,15 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             for (int e = 0; e < 8; ++e) g[e] = __fmul2_rn(__fmul2_rn(g[e], both(fd)), b[e]);
             wait_warp(done_d);
             tmem_get16(tl + CG_W + tb, x);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_k) + (tok + tb) * D + j;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.grad_k) + (tok + tb) * dk + j;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[e] = __fmul2_rn(g[e], x[e]);
                 f[2 * e] = kj[e].x * x[e].x;
                 f[2 * e + 1] = kj[e].y * x[e].y;
                 x[e] = __fadd2_rn(x[e], kr[e]);
-                if (tb + 2 * e < m) dst[2 * e * D] = __float2bfloat16_rn(x[e].x);
-                if (tb + 2 * e + 1 < m) dst[(2 * e + 1) * D] = __float2bfloat16_rn(x[e].y);
+                if (2 * e < mine) dst[2 * e * dk] = __float2bfloat16_rn(x[e].x);
+                if (2 * e + 1 < mine) dst[(2 * e + 1) * dk] = __float2bfloat16_rn(x[e].y);
             }
             const float f1 = lane_sums(f, lane);
             if (lane < 16) {
@@ -1851,7 +1874,9 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
 
 }  // namespace
 
-bool tc_takes(int dk, int dv, kdn_dtype in_dtype) { return in_dtype == KDN_BF16 && dk == D && dv == D; }
+constexpr int NARROWEST = 64 * 64;
+
+bool tc_takes(int dk, int dv, kdn_dtype in_dtype) { return in_dtype == KDN_BF16 && dk * dv >= NARROWEST; }
 
 // Against the walk token by token (us for heads x tokens, here / there): few heads
 // wait for two launches here, 16 x 48 19.1 / 13.7, 16 x 64 18.3 / 16.9, 16 x 96
@@ -1871,9 +1896,9 @@ namespace {
 // the ends are folded one after another.  In units of a chunk's walk: an end's
 // costs 0.8, a fold about one, the launches four.  No split unless it takes three
 // quarters of the time.  (Packed sequences' lengths are the device's.)
-Parts cut_of(int B, int H, int T, int nseq) {
+Parts cut_of(int B, int H, int T, int nseq, bool full) {
     Parts best{1, 0, nullptr, nullptr};
-    if (nseq > 0) return best;
+    if (nseq > 0 || !full) return best;
     const long long rows = static_cast<long long>(B) * H, sms = sm_count();
     const int chunks = (T + C - 1) / C;
     const auto rounds = [&](long long jobs) { return static_cast<double>((jobs + sms - 1) / sms); };
@@ -1895,8 +1920,8 @@ long long rounded(long long bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
 
-long long tc_fwd_bytes(int B, int H, int T, int nseq) {
-    const Parts cut = cut_of(B, H, T, nseq);
+long long tc_fwd_bytes(int B, int H, int T, int dk, int dv, int nseq) {
+    const Parts cut = cut_of(B, H, T, nseq, dk == D && dv == D);
     const long long rows = static_cast<long long>(B) * H, states = cut.parts > 1 ? rows * (3LL * cut.parts - 2) : 0;
     return slots_of(B, T, nseq) * H * PREP_BYTES + states * D * D * 4;
 }
@@ -1905,13 +1930,15 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     const long long blocks = slots_of(a.B, a.T, a.nseq) * a.H;
     const long long rows = static_cast<long long>(a.offsets ? a.nseq : a.B) * a.H;
     if (blocks > 0x7fffffffLL || rows > 0x7fffffffLL) return KDN_ERR_INVALID_ARG;
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(delta_prep_kernel), P_SMEM);
-    if (e != cudaSuccess) return from_cuda(e);
-    delta_prep_kernel<<<static_cast<unsigned>(blocks), PREP_THREADS, P_SMEM, stream>>>(a, ws, wait_ns);
+    const bool full = a.dk == D && a.dv == D, bf16 = a.out_dtype == KDN_BF16;
+    cudaError_t e;
+    auto prepare = full ? delta_prep_kernel<true> : delta_prep_kernel<false>;
+    if ((e = allow_smem(reinterpret_cast<const void*>(prepare), P_SMEM)) != cudaSuccess) return from_cuda(e);
+    prepare<<<static_cast<unsigned>(blocks), PREP_THREADS, P_SMEM, stream>>>(a, ws, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
-    Parts cut = cut_of(a.B, a.H, a.T, a.nseq);
+    Parts cut = cut_of(a.B, a.H, a.T, a.nseq, full);
     if (cut.parts > 1) {
-        auto kernel = delta_chunk_kernel<float, ENDS>;
+        auto kernel = delta_chunk_kernel<float, ENDS, true>;
         if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
         cut.ends = reinterpret_cast<float*>(ws + blocks * PREP_BYTES);
         float* starts = cut.ends + rows * 2 * (cut.parts - 1) * D * D;
@@ -1922,7 +1949,8 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
         if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
         cut.starts = starts;
     }
-    auto kernel = a.out_dtype == KDN_BF16 ? delta_chunk_kernel<__nv_bfloat16, OUTPUTS> : delta_chunk_kernel<float, OUTPUTS>;
+    auto kernel = full ? (bf16 ? delta_chunk_kernel<__nv_bfloat16, OUTPUTS, true> : delta_chunk_kernel<float, OUTPUTS, true>)
+                       : (bf16 ? delta_chunk_kernel<__nv_bfloat16, OUTPUTS, false> : delta_chunk_kernel<float, OUTPUTS, false>);
     if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
     kernel<<<static_cast<unsigned>(rows * cut.parts), CH_THREADS, CH_SMEM, stream>>>(a, ws, PREP_BYTES, KeepTiles{}, cut, wait_ns);
     return from_cuda(cudaGetLastError());
@@ -1941,18 +1969,22 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     const KeepTiles fwd{prep + tiles * PREP_STEP, prep + tiles * (PREP_STEP + 2 * STATE_BYTES)};
     const KeepTiles bwd{fwd.states + tiles * STATE_BYTES, fwd.rows + tiles * ROWS_BYTES};
     float* shares = reinterpret_cast<float*>(bwd.rows + tiles * ROWS_BYTES);
-    auto walk = delta_chunk_kernel<float, TILES>;
-    const std::pair<const void*, int> kernels[] = {{reinterpret_cast<const void*>(delta_prep_kernel), P_SMEM},
+    const bool full = a.dk == D && a.dv == D;
+    auto prepare = full ? delta_prep_kernel<true> : delta_prep_kernel<false>;
+    auto walk = full ? delta_chunk_kernel<float, TILES, true> : delta_chunk_kernel<float, TILES, false>;
+    auto adjoint = full ? delta_adjoint_kernel<true> : delta_adjoint_kernel<false>;
+    auto gradients = full ? delta_tc_grad_kernel<true> : delta_tc_grad_kernel<false>;
+    const std::pair<const void*, int> kernels[] = {{reinterpret_cast<const void*>(prepare), P_SMEM},
                                                    {reinterpret_cast<const void*>(walk), CH_SMEM},
-                                                   {reinterpret_cast<const void*>(delta_adjoint_kernel), AD_SMEM},
-                                                   {reinterpret_cast<const void*>(delta_tc_grad_kernel), GR_SMEM}};
+                                                   {reinterpret_cast<const void*>(adjoint), AD_SMEM},
+                                                   {reinterpret_cast<const void*>(gradients), GR_SMEM}};
     cudaError_t e = cudaSuccess;
     for (const auto& k : kernels)
         if ((e = allow_smem(k.first, k.second)) != cudaSuccess) return from_cuda(e);
-    delta_prep_kernel<<<static_cast<unsigned>(tiles), PREP_THREADS, P_SMEM, stream>>>(a, prep, wait_ns);
+    prepare<<<static_cast<unsigned>(tiles), PREP_THREADS, P_SMEM, stream>>>(a, prep, wait_ns);
     walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, PREP_STEP, fwd, Parts{1, 0, nullptr, nullptr}, wait_ns);
-    delta_adjoint_kernel<<<static_cast<unsigned>(rows), CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, wait_ns);
-    delta_tc_grad_kernel<<<static_cast<unsigned>(tiles), GR_THREADS, GR_SMEM, stream>>>(
+    adjoint<<<static_cast<unsigned>(rows), CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, wait_ns);
+    gradients<<<static_cast<unsigned>(tiles), GR_THREADS, GR_SMEM, stream>>>(
         a, GradTiles{prep, fwd.states, bwd.states, fwd.rows, bwd.rows, a.grad_A ? shares : nullptr, sm_count()}, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.grad_A) return from_cuda(e);
     return from_cuda(sum_rows(shares, slots, a.H, a.grad_A, nullptr, a.H, stream));

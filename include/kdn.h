@@ -579,8 +579,9 @@ KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, 
  * packed ones; 28 with more than 64 heads in all) are taken in chunks of 64 tokens on the tensor cores, with
  * operands of 22 bits: errors are those of fp32 arithmetic, relative to the
  * largest terms of a chunk (below 2^-24 of them; what strong decays make smaller
- * than that beside the rest of its chunk has no bits of its own).  Few heads of
- * long sequences (not packed ones) are cut along the tokens.
+ * than that beside the rest of its chunk has no bits of its own, nor have keys,
+ * queries or gradients of a chunk that are all below 2^-74).  Few heads of long
+ * sequences (not packed ones) are cut along the tokens.
  */
 KDN_API kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const void* beta,
                                       const void* d, const float* A, const float* S0,

@@ -33,8 +33,8 @@ def cuda(x):
 
 # how far a call may be from the 64-bit value beside its bound's fp32 part: what
 # the tensor-core form cuts from its operands (see the kernels), 0 for the rest
-def split(dk, dv, dt, T):
-    return delta64.SPLIT if dt == BF16 and dk == dv == 128 and T >= 32 else 0.0
+def split(dk, dv, dt):
+    return delta64.SPLIT if dt == BF16 and dk * dv >= 64 * 64 else 0.0
 
 
 SHAPES = [
@@ -44,13 +44,16 @@ SHAPES = [
     (1, 1, 63, 64, 64, F32, F32, True), (2, 2, 64, 128, 128, BF16, F32, False), (1, 3, 65, 128, 128, BF16, F32, True),
     (1, 2, 130, 32, 32, F32, F32, True), (1, 2, 200, 128, 64, BF16, BF16, False), (2, 2, 257, 64, 128, F32, F32, True),
     (3, 1, 129, 128, 128, BF16, BF16, True), (1, 2, 193, 128, 128, F32, F32, False), (1, 1, 640, 128, 128, BF16, F32, True),
+    (2, 2, 130, 64, 64, BF16, BF16, True), (1, 3, 65, 64, 64, BF16, F32, True), (2, 33, 29, 64, 128, BF16, BF16, True),
+    (1, 2, 100, 32, 128, BF16, BF16, True), (1, 2, 129, 128, 32, BF16, BF16, True), (2, 3, 5, 64, 64, BF16, BF16, True),
+    (1, 65, 30, 128, 128, BF16, BF16, True), (3, 2, 1, 128, 128, BF16, BF16, True),
 ]
 
 
 @pytest.mark.parametrize("B,H,T,dk,dv,dt,ot,state", SHAPES)
 def test_forward(kdn, B, H, T, dk, dv, dt, ot, state):
     x, S0, _ = draw(B, H, T, dk, dv, dt, 7 * T + dk, state)
-    val, err = delta64.delta(**x, S0=S0, split=split(dk, dv, dt, T))
+    val, err = delta64.delta(**x, S0=S0, split=split(dk, dv, dt))
     out, end = kdn.delta_scan_fwd(**cuda(x), S0=cuda(S0), out_dtype=ot)
     assert out.dtype == ot and delta64.far(out, val["out"], err["out"], ot) <= 1
     assert delta64.far(end, val["final"], err["final"]) <= 1
@@ -73,7 +76,7 @@ def test_backward(kdn, B, H, T, dk, dv, dt, ot, state):
     x, S0, g = draw(B, H, T, dk, dv, dt, 7 * T + dv, state)
     go = torch.randn(B, H, T, dv, generator=g).to(ot)
     gf = torch.randn(B, H, dv, dk, generator=g) if state else None
-    val, err = delta64.delta(**x, S0=S0, grad_out=go, grad_final=gf, split=split(dk, dv, dt, T))
+    val, err = delta64.delta(**x, S0=S0, grad_out=go, grad_final=gf, split=split(dk, dv, dt))
     got = kdn.delta_scan_bwd(**cuda(x), grad_out=cuda(go), S0=cuda(S0), grad_final_state=cuda(gf))
     for name in ("q", "k", "v", "beta", "d"):
         assert got[name].dtype == dt and delta64.far(got[name], val[name], err[name], dt) <= 1, name
@@ -106,7 +109,8 @@ OFFSETS = [[0, 1], [0, 5, 5, 70, 71, 200], [3, 64, 128, 130, 257], [0, 0, 0, 300
 
 
 @pytest.mark.parametrize("offsets", OFFSETS)
-@pytest.mark.parametrize("dk,dv,dt", [(64, 32, F32), (128, 128, BF16), (128, 128, F32), (16, 64, BF16)])
+@pytest.mark.parametrize("dk,dv,dt", [(64, 32, F32), (128, 128, BF16), (128, 128, F32), (16, 64, BF16), (64, 64, BF16),
+                                      (128, 32, BF16)])
 def test_packed(kdn, offsets, dk, dv, dt):
     T, H, n = max(offsets[-1], 1) + 7, 2, len(offsets) - 1
     x, S0, g = draw(1, H, T, dk, dv, dt, T, True, n)
@@ -114,7 +118,7 @@ def test_packed(kdn, offsets, dk, dv, dt):
     for name in ("q", "k", "v", "beta", "d"):                # tokens in no sequence are not read
         x[name][:, :, :offsets[0]] = x[name][:, :, offsets[-1]:] = torch.nan
     go[:, :, :offsets[0]] = go[:, :, offsets[-1]:] = torch.nan
-    val, err = delta64.delta(**x, S0=S0, offsets=offsets, grad_out=go, grad_final=gf, split=split(dk, dv, dt, T))
+    val, err = delta64.delta(**x, S0=S0, offsets=offsets, grad_out=go, grad_final=gf, split=split(dk, dv, dt))
     off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
     out = torch.full((1, H, T, dv), 7.0, device="cuda")
     y, end = kdn.delta_scan_fwd(**cuda(x), S0=cuda(S0), offsets=off, out=out)
@@ -130,7 +134,7 @@ def test_packed(kdn, offsets, dk, dv, dt):
         assert delta64.far(got[name], val[name], err[name]) <= 1, name
 
 
-@pytest.mark.parametrize("dk,dt", [(64, F32), (128, BF16)])
+@pytest.mark.parametrize("dk,dt", [(64, F32), (64, BF16), (128, BF16)])
 def test_offsets_out_of_order_stay_in_bounds(kdn, dk, dt):
     # which tokens are whose is unspecified; nothing outside the tensors is touched, and the call returns
     x, _, g = draw(1, 2, 150, dk, dk, dt, 5)
@@ -151,11 +155,11 @@ def test_no_tokens(kdn):
     assert (kdn.delta_scan_bwd(**cuda(x), grad_out=cuda(x)["v"])["S0"] == 0).all()
 
 
-@pytest.mark.parametrize("dk,dv,dt", [(128, 128, BF16), (64, 32, F32)])
+@pytest.mark.parametrize("dk,dv,dt", [(128, 128, BF16), (64, 128, BF16), (64, 32, F32)])
 def test_a_state_handed_on(kdn, dk, dv, dt):
     # prefill, more prefill, single tokens: what one call gives
     x, S0, _ = draw(2, 3, 150, dk, dv, dt, 9, True)
-    val, err = delta64.delta(**x, S0=S0, split=split(dk, dv, dt, 150))
+    val, err = delta64.delta(**x, S0=S0, split=split(dk, dv, dt))
     x = cuda(x)
     part = lambda a, b: {k: t if k == "A" else t[:, :, a:b].contiguous() for k, t in x.items()}  # noqa: E731
     outs, S = [], S0.cuda()
@@ -182,7 +186,7 @@ def test_step(kdn, B, H, dk, dv, dt, ot):
     assert torch.equal(kdn.delta_step(**one, state=state, out_dtype=ot), o) and torch.equal(state, new)   # in place
 
 
-@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, F32)])
+@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, BF16), (64, F32)])
 def test_gates_at_their_ends(kdn, dk, dt):
     # decays of nothing, of everything and of infinity; betas of 0, 1 and 2
     x, S0, g = draw(1, 2, 200, dk, dk, dt, 11, True)
@@ -192,7 +196,7 @@ def test_gates_at_their_ends(kdn, dk, dt):
     x["A"] = torch.tensor([1.0, 0.01])
     x["beta"][..., ::5], x["beta"][..., 1::5], x["beta"][..., 2::13] = 0.0, 1.0, 2.0
     go = torch.randn(1, 2, 200, dk, generator=g).to(dt)
-    val, err = delta64.delta(**x, S0=S0, grad_out=go, split=split(dk, dk, dt, 200))
+    val, err = delta64.delta(**x, S0=S0, grad_out=go, split=split(dk, dk, dt))
     out, end = kdn.delta_scan_fwd(**cuda(x), S0=S0.cuda(), out_dtype=F32)
     assert delta64.far(out, val["out"], err["out"]) <= 1 and delta64.far(end, val["final"], err["final"]) <= 1
     got = kdn.delta_scan_bwd(**cuda(x), grad_out=go.cuda(), S0=S0.cuda())
@@ -207,11 +211,11 @@ def test_gates_at_their_ends(kdn, dk, dt):
 @pytest.mark.parametrize("at", [0, 37, 63, 64, 150])
 @pytest.mark.parametrize("name,value", [("q", torch.nan), ("k", torch.nan), ("k", torch.inf), ("v", torch.nan), ("v", -torch.inf),
                                         ("beta", torch.nan), ("beta", torch.inf), ("d", torch.nan), ("d", -torch.inf)])
-@pytest.mark.parametrize("dk,dt", [(128, BF16), (128, F32)])
+@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, BF16), (128, F32)])
 def test_what_is_not_finite_spoils_nothing_before_it(kdn, dk, dt, name, value, at):
     # (padding behind a sequence's tokens may hold anything)
     x, S0, _ = draw(1, 2, 200, dk, dk, dt, 23, True)
-    val, err = delta64.delta(**x, S0=S0, split=split(dk, dk, dt, 200))
+    val, err = delta64.delta(**x, S0=S0, split=split(dk, dk, dt))
     where = (0, 1, at, 5) if name in "qkv" else (0, 1, at)
     x[name] = x[name].clone()
     x[name][where] = value
@@ -236,14 +240,14 @@ def test_what_is_not_finite_spoils_nothing_before_it(kdn, dk, dt, name, value, a
         assert not end[0, 1].isfinite().any()
 
 
-@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, F32)])
+@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, BF16), (64, F32)])
 def test_same_keys(kdn, dk, dt):
     # one key over and over, beta 1: each write replaces the last one's answer
     x, _, g = draw(1, 1, 150, dk, dk, dt, 13)
     x["k"] = x["k"][:, :, :1].expand_as(x["k"]).contiguous()
     x["beta"] = torch.ones_like(x["beta"])
     go = torch.randn(1, 1, 150, dk, generator=g).to(dt)
-    val, err = delta64.delta(**x, grad_out=go, split=split(dk, dk, dt, 150))
+    val, err = delta64.delta(**x, grad_out=go, split=split(dk, dk, dt))
     out, _ = kdn.delta_scan_fwd(**cuda(x), out_dtype=F32)
     assert delta64.far(out, val["out"], err["out"]) <= 1
     got = kdn.delta_scan_bwd(**cuda(x), grad_out=go.cuda())
@@ -251,7 +255,7 @@ def test_same_keys(kdn, dk, dt):
         assert delta64.far(got[name], val[name], err[name], dt) <= 1, name
 
 
-@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, F32), (128, F32)])
+@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, BF16), (64, F32), (128, F32)])
 def test_as_exact_as_its_types(kdn, dk, dt):
     # beside the worst case: roundings of random sign.  The fp32 outputs of 700 tokens with memories of up to
     # 400: sums of roots, (272 products)^1/2 x (400 tokens)^1/2 half steps of 2^-24 -> 2e-5
@@ -266,7 +270,7 @@ def test_as_exact_as_its_types(kdn, dk, dt):
         assert off <= 2e-5 + more, (name, off)
 
 
-@pytest.mark.parametrize("dk,dv,dt", [(128, 128, BF16), (64, 32, F32)])
+@pytest.mark.parametrize("dk,dv,dt", [(128, 128, BF16), (64, 64, BF16), (64, 32, F32)])
 def test_streams_graphs_and_the_same_again(kdn, dk, dv, dt):
     x, S0, g = draw(2, 3, 150, dk, dv, dt, 19, True)
     x, S0 = cuda(x), S0.cuda()
