@@ -864,14 +864,14 @@ struct BackLayout {
 using namespace delta;
 
 long long delta_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
-    return tc_takes_fwd(B, H, T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, dk, dv, nseq) : 0;
+    return tc_takes_fwd(B, H, T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, nseq) : 0;
 }
 
 long long delta_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
     if (T == 0) return 0;
     const long long bytes = BackLayout(B, H, T, dk, dv, nseq).bytes();
     // (the type of grad_out, which this does not know, decides the form)
-    const long long tc = tc_takes(dk, dv, in_dtype) ? tc_bwd_bytes(B, H, T, nseq) : 0;
+    const long long tc = tc_takes(B, H, dk, dv, nseq, in_dtype) ? tc_bwd_bytes(B, H, T, nseq) : 0;
     return tc > bytes ? tc : bytes;
 }
 
@@ -880,7 +880,7 @@ kdn_status delta_fwd_launch(const DeltaArgs& a, cudaStream_t stream, long long w
         Scratch scratch(stream);
         char* ws = static_cast<char*>(a.workspace);
         if (!ws) {
-            const kdn_status s = scratch.take(tc_fwd_bytes(a.B, a.H, a.T, a.dk, a.dv, a.nseq));
+            const kdn_status s = scratch.take(tc_fwd_bytes(a.B, a.H, a.T, a.nseq));
             if (s != KDN_OK) return s;
             ws = static_cast<char*>(scratch.p);
         }
@@ -923,7 +923,7 @@ kdn_status delta_bwd_launch(const DeltaArgs& a, cudaStream_t stream, long long w
         if (s != KDN_OK) return s;
         ws = static_cast<char*>(scratch.p);
     }
-    if (tc_takes(a.dk, a.dv, a.in_dtype) && a.out_dtype == KDN_BF16) return tc_bwd(a, ws, stream, wait_ns);
+    if (tc_takes(a.B, a.H, a.dk, a.dv, a.nseq, a.in_dtype) && a.out_dtype == KDN_BF16) return tc_bwd(a, ws, stream, wait_ns);
     float* states = reinterpret_cast<float*>(ws);
     float* adjoints = reinterpret_cast<float*>(ws + lay.states);
     float* r = reinterpret_cast<float*>(ws + 2 * lay.states);

@@ -1,6 +1,7 @@
 // delta_tc.cu -- the gated delta rule in chunks of 64 tokens on the tensor
-// cores, for bf16 inputs and d_k = d_v = 128 (delta_device.cuh has the rule,
-// delta_scan.cu the token-by-token form for the rest).
+// cores, for bf16 inputs and heads of 128 (narrower ones have zeros behind;
+// delta_device.cuh has the rule, delta_scan.cu the token-by-token form for the
+// rest).
 //
 // With g_t the log decay since the chunk began and E_ts = e^{g_t - g_s}, and S
 // the state before the chunk,
@@ -687,8 +688,8 @@ struct KeepTiles {
 // How a walk is cut along the tokens: `parts` parts of `len` chunks.
 struct Parts {
     int parts, len;
-    const float* starts;   // [rows,parts,dv,dk]: a part's first state (null: one part, from S0)
-    float* ends;           // ENDS: [rows,parts - 1,2,dv,dk]
+    const float* starts;   // [rows,parts,D,D]: a part's first state (null: one part, from S0)
+    float* ends;           // ENDS: [rows,parts - 1,2,D,D]
 };
 // OUTPUTS; TILES: no outputs, but the state before each chunk and R; ENDS: of a
 // part its end alone, from a zero state (N) or, without values, from the
@@ -729,8 +730,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     const int len = max(sp.hi - sp.lo, 0), chunks = (len + C - 1) / C;
     const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
     const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(dv) * dk;
-    const float* S0 = WALK == ENDS ? nullptr : cut.starts ? cut.starts + blockIdx.x * size : a.S0 ? a.S0 + sr * size : nullptr;
-    float* final_state = WALK == ENDS ? cut.ends + blockIdx.x * size
+    // (the parts' states are whole, as the fold reads and writes them)
+    const float* S0 = WALK == ENDS ? nullptr : cut.starts ? cut.starts + blockIdx.x * static_cast<long long>(D * D)
+                                            : a.S0 ? a.S0 + sr * size : nullptr;
+    const int s_ld = FULL || cut.starts ? D : dk, s_rows = FULL || cut.starts ? D : dv;
+    const int f_ld = FULL || WALK == ENDS ? D : dk, f_rows = FULL || WALK == ENDS ? D : dv;
+    float* final_state = WALK == ENDS ? cut.ends + blockIdx.x * static_cast<long long>(D * D)
                          : WALK == OUTPUTS && a.final_state && piece == cut.parts - 1 ? a.final_state + sr * size : nullptr;
     if (chunks == 0) {
         if (final_state)
@@ -865,7 +870,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 const int j = cb + 16 * p + 2 * e;
-                if (S0 && (FULL || (i < dv && j < dk))) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * dk + j);
+                if (S0 && (FULL || (i < s_rows && j < s_ld))) f = *reinterpret_cast<const float4*>(S0 + static_cast<long long>(i) * s_ld + j);
                 if (identity) f = make_float4(j == i, j + 1 == i, j + 2 == i, j + 3 == i);
                 S[p][e] = make_float2(f.x, f.y);
                 S[p][e + 1] = make_float2(f.z, f.w);
@@ -1032,8 +1037,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
         if (final_state) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float* dst = final_state + static_cast<long long>(i) * dk + cb + 16 * p;
-                if (!FULL && (i >= dv || cb + 16 * p >= dk)) continue;
+                float* dst = final_state + static_cast<long long>(i) * f_ld + cb + 16 * p;
+                if (!FULL && (i >= f_rows || cb + 16 * p >= f_ld)) continue;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
                     *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(S[p][e].x, S[p][e].y, S[p][e + 1].x, S[p][e + 1].y);
@@ -1052,7 +1057,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
 // The parts' first states from their ends: S_{p+1} = S_p M_p + N_p.  A CTA has
 // 16 rows of a head's state, a thread two of them by four columns.
 constexpr int FOLD_ROWS = 16, FOLD_THREADS = 256;
-__global__ void __launch_bounds__(FOLD_THREADS) delta_fold_kernel(const float* S0, const float* ends, float* starts, int parts) {
+__global__ void __launch_bounds__(FOLD_THREADS) delta_fold_kernel(const float* S0, const float* ends, float* starts, int parts, int dk,
+                                                                  int dv) {
     __shared__ float S[FOLD_ROWS][D];
     constexpr int PER = D / FOLD_ROWS;
     const long long row = blockIdx.x / PER, size = static_cast<long long>(D) * D;
@@ -1061,8 +1067,8 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_kernel(const float* S
     float4 x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const long long at = static_cast<long long>(i0 + r + e) * D + c;
-        x[e] = S0 ? *reinterpret_cast<const float4*>(S0 + row * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const long long at = (row * dv + i0 + r + e) * dk + c;
+        x[e] = S0 && i0 + r + e < dv && c < dk ? *reinterpret_cast<const float4*>(S0 + at) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int p = 0; p < parts; ++p) {
 #pragma unroll
@@ -1874,19 +1880,29 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
 
 }  // namespace
 
-constexpr int NARROWEST = 64 * 64;
-
-bool tc_takes(int dk, int dv, kdn_dtype in_dtype) { return in_dtype == KDN_BF16 && dk * dv >= NARROWEST; }
+// Heads narrower than 128 are taken with zeros behind, at the cost of whole ones:
+// us here / token by token, forward then backward, of 16 x 32 x 4096 x 64 x 64 1739
+// / 2567, 5717 / 13385; of 128 heads x 2048 of 64 x 32 235 / 382, 775 / 1213, but of
+// 2048 x 256 471 / 308, 1503 / 1476: smaller ones where each has an SM of its own
+// (of 32 x 32 and less the gain, 234 / 360, is not worth ten times the scratch).
+bool tc_takes(int B, int H, int dk, int dv, int nseq, kdn_dtype in_dtype) {
+    const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
+    return in_dtype == KDN_BF16 && (dk * dv >= 64 * 64 || (dk * dv >= 64 * 32 && rows <= sm_count()));
+}
 
 // Against the walk token by token (us for heads x tokens, here / there): few heads
 // wait for two launches here, 16 x 48 19.1 / 13.7, 16 x 64 18.3 / 16.9, 16 x 96
 // 21 / 24, 64 x 48 19.3 / 18.3, 64 x 64 18.7 / 22.9; many cost a chunk's work
 // however few its tokens, 128 x 24 20.6 / 20.0, 256 x 16 34 / 25, 256 x 32 33 / 41,
-// 2048 x 16 211 / 157, 2048 x 32 204 / 264.  (Backward calls gain at any length: 16
-// x 8 44 / 65, 2048 x 8 546 / 1140, 2048 x 256 1620 / 7740.)
+// 2048 x 16 211 / 157, 2048 x 32 204 / 264.  Narrower heads, 128 x 64: 16 x 64 26 /
+// 21, 16 x 128 28 / 34, 2048 x 32 204 / 139, 2048 x 64 190 / 251; 64 x 64: 16 x 64
+// 25 / 20, 16 x 128 27 / 30, 2048 x 64 180 / 153, 2048 x 128 280 / 294.  (Backward
+// calls gain at any length: 16 x 8 44 / 65, 2048 x 8 546 / 1140, 2048 x 256 1620 /
+// 7740; of 64 x 64 16 x 32 53 / 55, 2048 x 32 520 / 666.)
 bool tc_takes_fwd(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
-    const long long rows = static_cast<long long>(nseq > 0 ? nseq : B) * H;
-    return tc_takes(dk, dv, in_dtype) && T / (nseq > 0 ? nseq : 1) >= (rows <= 64 ? 64 : 28);
+    const bool few = static_cast<long long>(nseq > 0 ? nseq : B) * H <= 64;
+    const int least = dk * dv == D * D ? (few ? 64 : 28) : dk * dv >= D * D / 2 ? (few ? 96 : 48) : 112;
+    return tc_takes(B, H, dk, dv, nseq, in_dtype) && T / (nseq > 0 ? nseq : 1) >= least;
 }
 
 namespace {
@@ -1896,9 +1912,9 @@ namespace {
 // the ends are folded one after another.  In units of a chunk's walk: an end's
 // costs 0.8, a fold about one, the launches four.  No split unless it takes three
 // quarters of the time.  (Packed sequences' lengths are the device's.)
-Parts cut_of(int B, int H, int T, int nseq, bool full) {
+Parts cut_of(int B, int H, int T, int nseq) {
     Parts best{1, 0, nullptr, nullptr};
-    if (nseq > 0 || !full) return best;
+    if (nseq > 0) return best;
     const long long rows = static_cast<long long>(B) * H, sms = sm_count();
     const int chunks = (T + C - 1) / C;
     const auto rounds = [&](long long jobs) { return static_cast<double>((jobs + sms - 1) / sms); };
@@ -1920,8 +1936,8 @@ long long rounded(long long bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
 
-long long tc_fwd_bytes(int B, int H, int T, int dk, int dv, int nseq) {
-    const Parts cut = cut_of(B, H, T, nseq, dk == D && dv == D);
+long long tc_fwd_bytes(int B, int H, int T, int nseq) {
+    const Parts cut = cut_of(B, H, T, nseq);
     const long long rows = static_cast<long long>(B) * H, states = cut.parts > 1 ? rows * (3LL * cut.parts - 2) : 0;
     return slots_of(B, T, nseq) * H * PREP_BYTES + states * D * D * 4;
 }
@@ -1936,16 +1952,16 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     if ((e = allow_smem(reinterpret_cast<const void*>(prepare), P_SMEM)) != cudaSuccess) return from_cuda(e);
     prepare<<<static_cast<unsigned>(blocks), PREP_THREADS, P_SMEM, stream>>>(a, ws, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
-    Parts cut = cut_of(a.B, a.H, a.T, a.nseq, full);
+    Parts cut = cut_of(a.B, a.H, a.T, a.nseq);
     if (cut.parts > 1) {
-        auto kernel = delta_chunk_kernel<float, ENDS, true>;
+        auto kernel = full ? delta_chunk_kernel<float, ENDS, true> : delta_chunk_kernel<float, ENDS, false>;
         if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
         cut.ends = reinterpret_cast<float*>(ws + blocks * PREP_BYTES);
         float* starts = cut.ends + rows * 2 * (cut.parts - 1) * D * D;
         kernel<<<static_cast<unsigned>(rows * 2 * (cut.parts - 1)), CH_THREADS, CH_SMEM, stream>>>(a, ws, PREP_BYTES, KeepTiles{},
                                                                                                   cut, wait_ns);
         delta_fold_kernel<<<static_cast<unsigned>(rows * (D / FOLD_ROWS)), FOLD_THREADS, 0, stream>>>(a.S0, cut.ends, starts,
-                                                                                                     cut.parts);
+                                                                                                     cut.parts, a.dk, a.dv);
         if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
         cut.starts = starts;
     }

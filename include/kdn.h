@@ -575,13 +575,14 @@ KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, 
  * are not finite spoil the outputs of their token and of those behind it (in v:
  * of their channel alone), and the final state; none before.  Deterministic.
  *
- * bf16 inputs with dk = dv = 128 and 64 tokens or more a sequence (T / nseq, of
- * packed ones; 28 with more than 64 heads in all) are taken in chunks of 64 tokens on the tensor cores, with
- * operands of 22 bits: errors are those of fp32 arithmetic, relative to the
- * largest terms of a chunk (below 2^-24 of them; what strong decays make smaller
- * than that beside the rest of its chunk has no bits of its own, nor have keys,
- * queries or gradients of a chunk that are all below 2^-74).  Few heads of long
- * sequences (not packed ones) are cut along the tokens.
+ * bf16 inputs with dk*dv of 64*64 or more (64*32 with few heads), and sequences
+ * (T / nseq, of packed ones) of 64 tokens or more for heads of 128 (28 with more
+ * than 64 heads in all), 48 to 112 for narrower ones, are taken in chunks of 64
+ * tokens on the tensor cores, with operands of 22 bits: errors are those of fp32
+ * arithmetic, relative to the largest terms of a chunk (below 2^-24 of them; what
+ * strong decays make smaller than that beside the rest of its chunk has no bits
+ * of its own, nor have keys, queries or gradients of a chunk that are all below
+ * 2^-74).  Few heads of long sequences (not packed ones) are cut along the tokens.
  */
 KDN_API kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const void* beta,
                                       const void* d, const float* A, const float* S0,
@@ -608,14 +609,14 @@ KDN_API kdn_status kdn_delta_scan_fwd_workspace(int B, int H, int T, int dk, int
  *   grad_A    [H] fp32 or NULL, written: summed over batch and tokens
  *   grad_S0   [B,H,dv,dk] ([nseq,H,dv,dk]) fp32 or NULL, written
  *   workspace at least kdn_delta_scan_bwd_workspace bytes (about B*H*T*dv*(dk/8
- *             + 8), half as much again where the tensor cores take the call: each
- *             64th token's state and its adjoint, two rows a token, and what the
- *             chunks' tokens say of one another), or NULL
+ *             + 8), where the tensor cores take the call 4.3 KB a token and head:
+ *             each 64th token's state and its adjoint, two rows a token, and what
+ *             the chunks' tokens say of one another), or NULL
  *
  * Sizes, alignment and rules as for the forward.  T = 0 writes grad_S0 (=
  * grad_final_state) and grad_A (= 0).  Sums in fp32, in a fixed order
- * (deterministic).  The tensor-core form takes bf16 inputs with dk = dv = 128
- * and bf16 grad_out, of any length.
+ * (deterministic).  The tensor-core form takes bf16 inputs and grad_out with
+ * dk*dv of 64*64 or more (64*32 with few heads), of any length.
  */
 KDN_API kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const void* beta,
                                       const void* d, const float* A, const float* S0,

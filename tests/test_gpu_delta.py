@@ -34,7 +34,7 @@ def cuda(x):
 # how far a call may be from the 64-bit value beside its bound's fp32 part: what
 # the tensor-core form cuts from its operands (see the kernels), 0 for the rest
 def split(dk, dv, dt):
-    return delta64.SPLIT if dt == BF16 and dk * dv >= 64 * 64 else 0.0
+    return delta64.SPLIT if dt == BF16 and dk * dv >= 64 * 32 else 0.0
 
 
 SHAPES = [
@@ -59,11 +59,12 @@ def test_forward(kdn, B, H, T, dk, dv, dt, ot, state):
     assert delta64.far(end, val["final"], err["final"]) <= 1
 
 
-@pytest.mark.parametrize("B,H,T,state", [(1, 2, 2500, True), (1, 1, 2049, False)])
-def test_few_heads_of_long_sequences(kdn, B, H, T, state):
+@pytest.mark.parametrize("B,H,T,dk,dv,state", [(1, 2, 2500, 128, 128, True), (1, 1, 2049, 128, 128, False),
+                                               (1, 2, 2500, 64, 64, True), (1, 1, 2100, 128, 32, True)])
+def test_few_heads_of_long_sequences(kdn, B, H, T, dk, dv, state):
     # cut along the tokens: parts' ends first, then the parts side by side
-    x, S0, _ = draw(B, H, T, 128, 128, BF16, T, state, rate=0.05)
-    assert kdn.delta_scan_fwd_workspace(B, H, T, 128, 128) > kdn.delta_scan_fwd_workspace(256 * B, H, T, 128, 128) // 256
+    x, S0, _ = draw(B, H, T, dk, dv, BF16, T, state, rate=0.05)
+    assert kdn.delta_scan_fwd_workspace(B, H, T, dk, dv) > kdn.delta_scan_fwd_workspace(256 * B, H, T, dk, dv) // 256
     val, err = delta64.delta(**x, S0=S0, split=delta64.SPLIT)
     out, end = kdn.delta_scan_fwd(**cuda(x), S0=cuda(S0), out_dtype=F32)
     assert delta64.far(out, val["out"], err["out"]) <= 1 and delta64.far(end, val["final"], err["final"]) <= 1
