@@ -1108,9 +1108,11 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_kernel(const float* S
 // lies in COL_W until beta dU's halves do; e^g dO is an operand in shared memory.
 constexpr uint32_t COL_X = 320;              // dO^T (e^g Q), 128 columns
 
-template <bool FULL>
+// END: of a part but the first its end alone, from zero (the last one's from the
+// final state's gradient): nothing is kept or written but that.
+template <bool FULL, bool END>
 __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const DeltaArgs a, const char* prep, const KeepTiles keep,
-                                                                      long long wait_ns) {
+                                                                      const Parts cut, long long wait_ns) {
     extern __shared__ __align__(128) unsigned char smem[];
     float* tops = reinterpret_cast<float*>(smem + CH_OFF_TOP);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + CH_OFF_BAR);
@@ -1126,14 +1128,27 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     uint32_t* holder = reinterpret_cast<uint32_t*>(have_w + 1);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long sr = blockIdx.x, n = sr / a.H;
+    const int jobs = END ? cut.parts - 1 : cut.parts;                  // of a state row
+    const long long sr = blockIdx.x / jobs, n = sr / a.H;
+    const int piece = static_cast<int>(blockIdx.x % jobs) + (END ? 1 : 0);
     const int h = static_cast<int>(sr % a.H);
-    const Span sp = span_of(a, n);
+    Span sp = span_of(a, n);
+    if (cut.parts > 1) {   // this part's tokens and chunks
+        sp.lo += piece * cut.len * C;
+        sp.slot += piece * cut.len;
+        if (sp.hi - sp.lo > cut.len * C) sp.hi = sp.lo + cut.len * C;
+    }
     const int len = max(sp.hi - sp.lo, 0), chunks = (len + C - 1) / C;
     const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
     const long long tok = (sp.row * a.H + h) * a.T + sp.lo, size = static_cast<long long>(dv) * dk;
-    const float* D1 = a.grad_final_state ? a.grad_final_state + sr * size : nullptr;
-    float* D0 = a.grad_S0 ? a.grad_S0 + sr * size : nullptr;
+    constexpr long long WHOLE = D * D;                                 // (the parts' states, as the folds have them)
+    const bool begun = !END && cut.starts;
+    const float* D1 = begun ? cut.starts + blockIdx.x * WHOLE
+                      : a.grad_final_state && piece == cut.parts - 1 ? a.grad_final_state + sr * size : nullptr;
+    float* D0 = END ? cut.ends + (sr * (cut.parts - 1) + piece - 1) * 2 * WHOLE
+                : a.grad_S0 && piece == 0 ? a.grad_S0 + sr * size : nullptr;
+    const int s_ld = FULL || begun ? D : dk, s_rows = FULL || begun ? D : dv;
+    const int f_ld = FULL || END ? D : dk, f_rows = FULL || END ? D : dv;
     if (chunks == 0) {
         if (D0)
             for (int i = tid; i < size / 4; i += CH_THREADS)
@@ -1256,8 +1271,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (D1 && (FULL || (i < dv && cb + 16 * p < dk)))
-                    f = *reinterpret_cast<const float4*>(D1 + static_cast<long long>(i) * dk + cb + 16 * p + 2 * e);
+                if (D1 && (FULL || (i < s_rows && cb + 16 * p < s_ld)))
+                    f = *reinterpret_cast<const float4*>(D1 + static_cast<long long>(i) * s_ld + cb + 16 * p + 2 * e);
                 S[p][e] = make_float2(f.x, f.y);
                 S[p][e + 1] = make_float2(f.z, f.w);
             }
@@ -1296,8 +1311,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
                 }
             }
             arrive(have_s + (part >> 1));
-            keep_row<8>(keep.states + slot * STATE_BYTES, i, cb / 4, S[0]);
-            keep_row<8>(keep.states + slot * STATE_BYTES, i, cb / 4 + 4, S[1]);
+            if (!END) {
+                keep_row<8>(keep.states + slot * STATE_BYTES, i, cb / 4, S[0]);
+                keep_row<8>(keep.states + slot * STATE_BYTES, i, cb / 4 + 4, S[1]);
+            }
             wait_warp(full + st, (c >> 1) & 1);
             end = gates[G_END];
             float2 z[8], x[8];
@@ -1357,7 +1374,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
                 tmem_get16(tl + COL_Z + tb, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[e] = __ffma2_rn(x[e], both(f), z[e]);
-                keep_row<8>(keep.rows + slot * ROWS_BYTES, i, tb / 4, z);
+                if (!END) keep_row<8>(keep.rows + slot * ROWS_BYTES, i, tb / 4, z);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     const float4 b = *reinterpret_cast<const float4*>(gates + G_BETA + tb + 2 * e);
@@ -1373,7 +1390,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
                 arrive(have_w);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + st);
-                const int m = FULL || i < dv ? len - chunk * C - tb : 0;
+                const int m = !END && (FULL || i < dv) ? len - chunk * C - tb : 0;
                 __nv_bfloat16* dst = gv + (static_cast<long long>(chunk) * C + tb) * dv;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -1386,8 +1403,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
             take(chunks - 1);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float* dst = D0 + static_cast<long long>(i) * dk + cb + 16 * p;
-                if (!FULL && (i >= dv || cb + 16 * p >= dk)) continue;
+                float* dst = D0 + static_cast<long long>(i) * f_ld + cb + 16 * p;
+                if (!FULL && (i >= f_rows || cb + 16 * p >= f_ld)) continue;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
                     *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(S[p][e].x, S[p][e].y, S[p][e + 1].x, S[p][e + 1].y);
@@ -1401,6 +1418,56 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
         tmem_dealloc(tmem, 512);
     }
     if (tid == 0 && *dead) record_error(&g_delta_error, KDN_ERR_TIMEOUT);
+}
+
+// The adjoints behind the parts from their ends: D_{p-1} = D_p M_p^T + N_p, the
+// last part's end having begun with the final state's gradient.  As the states'
+// fold otherwise; an end lies where N of the part before it was.
+__global__ void __launch_bounds__(FOLD_THREADS) delta_fold_back_kernel(const float* D1, const float* ends, float* starts, int parts,
+                                                                       int dk, int dv) {
+    __shared__ float S[FOLD_ROWS][D];
+    constexpr int PER = D / FOLD_ROWS;
+    const long long row = blockIdx.x / PER, size = static_cast<long long>(D) * D;
+    const int i0 = static_cast<int>(blockIdx.x % PER) * FOLD_ROWS;
+    const int r = 2 * (threadIdx.x / 32), lane = threadIdx.x % 32;   // two rows, columns lane + 32 e
+    float x[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int i = i0 + r + e, c = lane + 32 * w;
+            x[e][w] = D1 && i < dv && c < dk ? D1[(row * dv + i) * dk + c] : 0.f;
+        }
+    for (int p = parts - 1; p >= 0; --p) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                S[r + e][lane + 32 * w] = x[e][w];
+                starts[(row * parts + p) * size + static_cast<long long>(i0 + r + e) * D + lane + 32 * w] = x[e][w];
+            }
+        if (p == 0) break;
+        __syncwarp();                                  // (a warp's two rows are its own)
+        const float* N = ends + (row * (parts - 1) + p - 1) * 2 * size;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x[e][w] = N[static_cast<long long>(i0 + r + e) * D + lane + 32 * w];
+        if (p < parts - 1) {
+            const float* M = ends + ((row * (parts - 1) + p) * 2 + 1) * size;
+#pragma unroll 4
+            for (int j = 0; j < D; j += 4) {
+                const float4 s0 = *reinterpret_cast<const float4*>(&S[r][j]), s1 = *reinterpret_cast<const float4*>(&S[r + 1][j]);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float4 m = __ldg(reinterpret_cast<const float4*>(M + static_cast<long long>(lane + 32 * w) * D + j));
+                    x[0][w] = fmaf(s0.x, m.x, fmaf(s0.y, m.y, fmaf(s0.z, m.z, fmaf(s0.w, m.w, x[0][w]))));
+                    x[1][w] = fmaf(s1.x, m.x, fmaf(s1.y, m.y, fmaf(s1.z, m.z, fmaf(s1.w, m.w, x[1][w]))));
+                }
+            }
+        }
+        __syncwarp();
+    }
 }
 
 // ---- the gradients of a chunk ----------------------------------------------------
@@ -1934,6 +2001,18 @@ Parts cut_of(int B, int H, int T, int nseq) {
 }
 long long rounded(long long bytes) { return (bytes + 255) / 256 * 256; }
 
+// The first states of all parts.
+cudaError_t states_of_parts(const DeltaArgs& a, const char* prep, int step, const Parts& cut, float* starts, long long rows,
+                            cudaStream_t stream, long long wait_ns) {
+    auto kernel = a.dk == D && a.dv == D ? delta_chunk_kernel<float, ENDS, true> : delta_chunk_kernel<float, ENDS, false>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(rows * 2 * (cut.parts - 1)), CH_THREADS, CH_SMEM, stream>>>(a, prep, step, KeepTiles{}, cut, wait_ns);
+    delta_fold_kernel<<<static_cast<unsigned>(rows * (D / FOLD_ROWS)), FOLD_THREADS, 0, stream>>>(a.S0, cut.ends, starts, cut.parts,
+                                                                                                 a.dk, a.dv);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 long long tc_fwd_bytes(int B, int H, int T, int nseq) {
@@ -1954,15 +2033,9 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
     Parts cut = cut_of(a.B, a.H, a.T, a.nseq);
     if (cut.parts > 1) {
-        auto kernel = full ? delta_chunk_kernel<float, ENDS, true> : delta_chunk_kernel<float, ENDS, false>;
-        if ((e = allow_smem(reinterpret_cast<const void*>(kernel), CH_SMEM)) != cudaSuccess) return from_cuda(e);
         cut.ends = reinterpret_cast<float*>(ws + blocks * PREP_BYTES);
         float* starts = cut.ends + rows * 2 * (cut.parts - 1) * D * D;
-        kernel<<<static_cast<unsigned>(rows * 2 * (cut.parts - 1)), CH_THREADS, CH_SMEM, stream>>>(a, ws, PREP_BYTES, KeepTiles{},
-                                                                                                  cut, wait_ns);
-        delta_fold_kernel<<<static_cast<unsigned>(rows * (D / FOLD_ROWS)), FOLD_THREADS, 0, stream>>>(a.S0, cut.ends, starts,
-                                                                                                     cut.parts, a.dk, a.dv);
-        if ((e = cudaGetLastError()) != cudaSuccess) return from_cuda(e);
+        if ((e = states_of_parts(a, ws, PREP_BYTES, cut, starts, rows, stream, wait_ns)) != cudaSuccess) return from_cuda(e);
         cut.starts = starts;
     }
     auto kernel = full ? (bf16 ? delta_chunk_kernel<__nv_bfloat16, OUTPUTS, true> : delta_chunk_kernel<float, OUTPUTS, true>)
@@ -1974,7 +2047,9 @@ kdn_status tc_fwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
 
 long long tc_bwd_bytes(int B, int H, int T, int nseq) {
     const long long tiles = slots_of(B, T, nseq) * H;
-    return tiles * (PREP_STEP + 2 * STATE_BYTES + 2 * ROWS_BYTES) + rounded(tiles * 4);
+    const Parts cut = cut_of(B, H, T, nseq);
+    const long long states = cut.parts > 1 ? static_cast<long long>(B) * H * (3LL * cut.parts - 2) : 0;
+    return tiles * (PREP_STEP + 2 * STATE_BYTES + 2 * ROWS_BYTES) + rounded(tiles * 4) + states * STATE_BYTES;
 }
 
 kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long wait_ns) {
@@ -1988,7 +2063,7 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     const bool full = a.dk == D && a.dv == D;
     auto prepare = full ? delta_prep_kernel<true> : delta_prep_kernel<false>;
     auto walk = full ? delta_chunk_kernel<float, TILES, true> : delta_chunk_kernel<float, TILES, false>;
-    auto adjoint = full ? delta_adjoint_kernel<true> : delta_adjoint_kernel<false>;
+    auto adjoint = full ? delta_adjoint_kernel<true, false> : delta_adjoint_kernel<false, false>;
     auto gradients = full ? delta_tc_grad_kernel<true> : delta_tc_grad_kernel<false>;
     const std::pair<const void*, int> kernels[] = {{reinterpret_cast<const void*>(prepare), P_SMEM},
                                                    {reinterpret_cast<const void*>(walk), CH_SMEM},
@@ -1998,8 +2073,24 @@ kdn_status tc_bwd(const DeltaArgs& a, char* ws, cudaStream_t stream, long long w
     for (const auto& k : kernels)
         if ((e = allow_smem(k.first, k.second)) != cudaSuccess) return from_cuda(e);
     prepare<<<static_cast<unsigned>(tiles), PREP_THREADS, P_SMEM, stream>>>(a, prep, wait_ns);
-    walk<<<static_cast<unsigned>(rows), CH_THREADS, CH_SMEM, stream>>>(a, prep, PREP_STEP, fwd, Parts{1, 0, nullptr, nullptr}, wait_ns);
-    adjoint<<<static_cast<unsigned>(rows), CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, wait_ns);
+    Parts cut = cut_of(a.B, a.H, a.T, a.nseq), back = cut;
+    float* starts = nullptr;
+    if (cut.parts > 1) {
+        cut.ends = back.ends = reinterpret_cast<float*>(reinterpret_cast<char*>(shares) + rounded(tiles * 4));
+        starts = cut.ends + rows * 2 * (cut.parts - 1) * D * D;
+        if ((e = states_of_parts(a, prep, PREP_STEP, cut, starts, rows, stream, wait_ns)) != cudaSuccess) return from_cuda(e);
+        cut.starts = back.starts = starts;
+    }
+    const unsigned walks = static_cast<unsigned>(rows * cut.parts);
+    walk<<<walks, CH_THREADS, CH_SMEM, stream>>>(a, prep, PREP_STEP, fwd, cut, wait_ns);
+    if (cut.parts > 1) {   // (what the forward's ends and first states lie in is free, but M)
+        auto ends = full ? delta_adjoint_kernel<true, true> : delta_adjoint_kernel<false, true>;
+        if ((e = allow_smem(reinterpret_cast<const void*>(ends), AD_SMEM)) != cudaSuccess) return from_cuda(e);
+        ends<<<static_cast<unsigned>(rows * (cut.parts - 1)), CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, back, wait_ns);
+        delta_fold_back_kernel<<<static_cast<unsigned>(rows * (D / FOLD_ROWS)), FOLD_THREADS, 0, stream>>>(
+            a.grad_final_state, back.ends, starts, cut.parts, a.dk, a.dv);
+    }
+    adjoint<<<walks, CH_THREADS, AD_SMEM, stream>>>(a, prep, bwd, back, wait_ns);
     gradients<<<static_cast<unsigned>(tiles), GR_THREADS, GR_SMEM, stream>>>(
         a, GradTiles{prep, fwd.states, bwd.states, fwd.rows, bwd.rows, a.grad_A ? shares : nullptr, sm_count()}, wait_ns);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.grad_A) return from_cuda(e);

@@ -72,6 +72,24 @@ def test_few_heads_of_long_sequences(kdn, B, H, T, dk, dv, state):
         assert float((got.cpu().double() - want).norm() / want.norm()) < 2e-5
 
 
+@pytest.mark.parametrize("B,H,T,dk,dv,state", [(1, 2, 2500, 128, 128, True), (1, 1, 2049, 128, 128, False),
+                                               (1, 2, 2200, 64, 64, True), (1, 1, 2100, 32, 128, False)])
+def test_backward_of_few_heads_of_long_sequences(kdn, B, H, T, dk, dv, state):
+    # memories of a few hundred tokens, so that the parts' adjoints count
+    x, S0, g = draw(B, H, T, dk, dv, BF16, T, state, rate=0.05)
+    assert kdn.delta_scan_bwd_workspace(B, H, T, dk, dv) > kdn.delta_scan_bwd_workspace(256 * B, H, T, dk, dv) // 256
+    go = torch.randn(B, H, T, dv, generator=g).to(BF16)
+    gf = torch.randn(B, H, dv, dk, generator=g) if state else None
+    val, err = delta64.delta(**x, S0=S0, grad_out=go, grad_final=gf, split=delta64.SPLIT)
+    got = kdn.delta_scan_bwd(**cuda(x), grad_out=cuda(go), S0=cuda(S0), grad_final_state=cuda(gf))
+    for name in ("q", "k", "v", "beta", "d", "A", "S0"):
+        dt = BF16 if name in ("q", "k", "v", "beta", "d") else F32
+        assert delta64.far(got[name], val[name], err[name], dt) <= 1, name
+        # (beside the worst case, as below: roundings of random sign)
+        off = float((got[name].cpu().double() - val[name]).norm() / val[name].norm())
+        assert off < 2e-5 + (delta64.half_step(BF16) if dt == BF16 else 0.0), (name, off)
+
+
 @pytest.mark.parametrize("B,H,T,dk,dv,dt,ot,state", SHAPES)
 def test_backward(kdn, B, H, T, dk, dv, dt, ot, state):
     x, S0, g = draw(B, H, T, dk, dv, dt, 7 * T + dv, state)
