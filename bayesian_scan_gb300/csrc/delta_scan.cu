@@ -26,7 +26,8 @@
 //     dv = l,   dbeta_t = r_t . y_t,
 // and, dk's brackets being what k did as a reader and as a writer, the
 // gradient of a token's log decay is
-//     sum_{s >= t in the chunk} (q.dq + k.dk_read - k.dk_write)_s + <D1, S1>.
+//     sum_{s >= t in the chunk} (q.dq + k.dk_read - k.dk_write)_s + <D1, S1>,
+// taken here pair by pair (see the kernel's end).
 #include <type_traits>
 
 #include "delta_device.cuh"
@@ -451,7 +452,7 @@ constexpr int GRAD_THREADS = 256;
 
 template <int DK>
 constexpr int grad_smem(int dv) {
-    return (2 * CHUNK * (DK + 4) + 3 * CHUNK * (dv + 4) + 2 * CHUNK * (CHUNK + 4) + 9 * CHUNK + 8) * 4;
+    return (2 * CHUNK * (DK + 4) + 3 * CHUNK * (dv + 4) + 2 * CHUNK * (CHUNK + 4) + (10 + GRAD_THREADS / 32) * CHUNK + 8) * 4;
 }
 
 __device__ __forceinline__ float block_sum(float x, float* share) {
@@ -512,9 +513,11 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
     float* ew = eg + CHUNK;
     float* sb = ew + CHUNK;                  // beta, d
     float* sd = sb + CHUNK;
-    float* sc = sd + CHUNK;                  // q.dq + k.dk_read - k.dk_write of each token
-    float* si = sc + CHUNK;                  // k.(e^{g_C - g} u D1)
-    float* share = si + CHUNK;
+    float* sc = sd + CHUNK;                  // what each token reads of S0, q.(e^g dO S0) - k.(e^g l S0)
+    float* si = sc + CHUNK;                  // and writes to D1, k.(e^{g_C - g} u D1)
+    float* sr = si + CHUNK;                  // sums of W over the tokens before one, and (by warps) behind one
+    float* sw = sr + CHUNK;                  // [GRAD_THREADS / 32][CHUNK]
+    float* share = sw + GRAD_THREADS / 32 * CHUNK;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = static_cast<int>(blockIdx.x % a.H);
     const long long slot = blockIdx.x / a.H;
@@ -602,7 +605,22 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
     }
     {   // dP, dG: thread (ty, tx) has rows ty + 16 a, columns tx + 16 b
         const int tx = tid & 15, ty = tid >> 4;
-        float p[4][4] = {}, w[4][4] = {};
+        float p[4][4] = {}, w[4][4] = {}, pk[4][4] = {}, wk[4][4] = {};
+        for (int i = 0; i < DK; i += 4) {    // q_t.k_s, k_t.k_s
+            float4 u[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) u[b] = *reinterpret_cast<const float4*>(sk + (tx + 16 * b) * LDK + i);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 g = *reinterpret_cast<const float4*>(sq + (ty + 16 * r) * LDK + i);
+                const float4 l = *reinterpret_cast<const float4*>(sk + (ty + 16 * r) * LDK + i);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    pk[r][b] += g.x * u[b].x + g.y * u[b].y + g.z * u[b].z + g.w * u[b].w;
+                    wk[r][b] += l.x * u[b].x + l.y * u[b].y + l.z * u[b].z + l.w * u[b].w;
+                }
+            }
+        }
         for (int i = 0; i < dv; i += 4) {
             float4 u[4];
 #pragma unroll
@@ -624,9 +642,26 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
             for (int b = 0; b < 4; ++b) {
                 const int t = ty + 16 * r, s = tx + 16 * b;
                 const float e = s <= t ? expf((gh[t] - gh[s]) + (gl[t] - gl[s])) : 0.f;
-                dP[t * LDC + s] = s <= t ? p[r][b] * e : 0.f;
-                dG[t * LDC + s] = s < t ? -w[r][b] * e : 0.f;
+                p[r][b] = s <= t ? p[r][b] * e : 0.f;
+                w[r][b] = s < t ? -w[r][b] * e : 0.f;
+                dP[t * LDC + s] = p[r][b];
+                dG[t * LDC + s] = w[r][b];
+                // W_ts: what t reads of what s wrote
+                pk[r][b] = s < t ? fmaf(p[r][b], pk[r][b], w[r][b] * wk[r][b]) : 0.f;
             }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float x = (pk[r][0] + pk[r][1]) + (pk[r][2] + pk[r][3]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (tx == 0) sr[ty + 16 * r] = x;
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float x = (pk[0][b] + pk[1][b]) + (pk[2][b] + pk[3][b]);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (lane < 16) sw[warp * CHUNK + tx + 16 * b] = x;
+        }
     }
     __syncthreads();
     constexpr int CJ = DK >= 32 ? DK / 32 : 1;               // columns a lane
@@ -636,6 +671,8 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
     float c8[8], in8[8];
     {   // dq and dk_read of 8 tokens
         float dq[8][CJ] = {}, kr[8][CJ] = {};
+#pragma unroll
+        for (int t = 0; t < 8; ++t) c8[t] = 0.f;
         if (on) {
             for (int i = 0; i < dv; i += 4) {
                 float s0[4][CJ];
@@ -650,6 +687,8 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
                 for (int c = 0; c < CJ; ++c) {
                     dq[t][c] *= eg[tw + t];
                     kr[t][c] *= -eg[tw + t];
+                    const float q = sq[(tw + t) * LDK + j + c], k = sk[(tw + t) * LDK + j + c];
+                    c8[t] = fmaf(q, dq[t][c], fmaf(k, kr[t][c], c8[t]));
                 }
             for (int s = 0; s < tw + 8; s += 4) {
                 float kc[4][CJ];
@@ -694,13 +733,10 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            c8[t] = 0.f;
             in8[t] = fw[t];
             if (on) {
 #pragma unroll
                 for (int c = 0; c < CJ; ++c) {
-                    const float q = sq[(tw + t) * LDK + j + c], k = sk[(tw + t) * LDK + j + c];
-                    c8[t] = fmaf(q, dq[t][c], fmaf(k, kr[t][c] - kw[t][c], c8[t]));
                     if (tw + t < m) {
                         static_cast<TI*>(a.grad_q)[(tok + tw + t) * DK + j + c] = from_f32<TI>(dq[t][c]);
                         static_cast<TI*>(a.grad_k)[(tok + tw + t) * DK + j + c] = from_f32<TI>(kr[t][c] + kw[t][c]);
@@ -718,24 +754,36 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
             }
         }
     }
-    // <D1, S1> = e^{g_C} <D1, S0> + sum_t k_t.(e^{g_C - g_t} u_t D1)
     float x = 0.f;
     for (long long i = tid; i < size; i += GRAD_THREADS) x = fmaf(__ldg(S0 + i), __ldg(D1 + i), x);
     x = block_sum(x, share);                 // (and the tokens' shares are in shared memory)
     if (warp == 0) {
-        // gradients of the log decays: sums from the chunk's end
-        const float c0 = sc[2 * lane], c1 = sc[2 * lane + 1];
-        float f = si[2 * lane] + si[2 * lane + 1], s = c0 + c1;
+        // gradient of a token's log decay: all that is read behind it (itself included) of what was written
+        // before it, sums of (reads of S0) from the chunk's end, of (writes to D1) from its beginning, of W over
+        // both, which is its rows' less its columns' sums from the end, and e^{g_C} <D1, S0>.  (From q.dq + k.dk
+        // the pairs that do not stand across the token cancel but for roundings of their own, and the gradient
+        // of A was 1e-6 off.)
+        float c[2], f[2];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            float behind = 0.f;
+#pragma unroll
+            for (int w = 0; w < GRAD_THREADS / 32; ++w) behind += sw[w * CHUNK + t];
+            c[e] = sc[t] + (sr[t] - behind);
+            f[e] = si[t];
+        }
+        float s = c[0] + c[1], pre = f[0] + f[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float z = __shfl_down_sync(0xffffffffu, s, o);
+            const float z = __shfl_down_sync(0xffffffffu, s, o), y = __shfl_up_sync(0xffffffffu, pre, o);
             if (lane + o < 32) s += z;
+            if (lane >= o) pre += y;
         }
-        const float rest = fmaf(eg[CHUNK - 1], x, f);   // (tokens behind the chunk's last have no decay)
-        const float ga1 = (s - c0) + rest, ga0 = s + rest;
-        const float ga[2] = {ga0, ga1};
+        const float before = __shfl_up_sync(0xffffffffu, pre, 1);
+        const float rest = eg[CHUNK - 1] * x + (lane > 0 ? before : 0.f);   // (tokens behind the chunk's last have no decay)
+        const float above = __shfl_down_sync(0xffffffffu, s, 1);
+        const float ga[2] = {s + rest, ((lane < 31 ? above : 0.f) + c[1]) + (rest + f[0])};
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
