@@ -167,8 +167,8 @@ __device__ __forceinline__ void norm_part(float (&s)[NV][VEC], float rstd, const
             const int c = first + (j * 32 + lane) * VEC;
 #pragma unroll
             for (int o = VEC == 1 ? 16 : 8; o > 0; o >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-            // a group of zeros has scale 1
-            const float sc = top[j] > 0.f ? top[j] / TOP : 1.f;
+            // a group whose largest is 0 or rounds to it here (up to 224 x 2^-149) has scale 1
+            const float part = top[j] / TOP, sc = part > 0.f ? part : 1.f;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s[j][e] = s[j][e] / sc;
             if (c < C) {

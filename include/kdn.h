@@ -663,12 +663,15 @@ KDN_API kdn_status kdn_delta_step(const void* q, const void* k, const void* v, c
  *   y         [rows,C] y_dtype.  With KDN_E4M3 it is in 8 bits, y / scale
  *             rounded to nearest (ties to even), with
  *   scale     [rows, ceil(C/128)] fp32: for each group of 128 channels its
- *             largest |y| / 448, or 1 where that is 0.  NULL for other types.
+ *             largest |y| / 448, or 1 where that quotient is 0 in fp32.  (A
+ *             subnormal quotient has few bits; y / scale is at most 448 all the
+ *             same.)  NULL for other types.
  *
  *   0 <= rows < 2^31, 1 <= C <= 2^28, rows * x_ld < 2^60; element-aligned
  *   (16-byte aligned tensors, C and x_ld multiples of 8, take the widest path).
- *   Outputs overlap no input otherwise.  What is not finite stays in its row.  The sum of squares is fp32 (|s| < 1e18; without eps,
- *   rows of 1e-18 and less are lost in it).
+ *   Outputs overlap no input otherwise.  What is not finite stays in its row.
+ *   The sum of squares is fp32 (|s| < 1e18; without eps, rows of 1e-18 and less
+ *   are lost in it).
  */
 KDN_API kdn_status kdn_add_rms_norm_fwd(const void* x, long long x_ld, const void* residual,
                                         const float* weight, float eps, void* sum, void* y,
