@@ -1254,16 +1254,18 @@ def _norm_ws(device, rows, C):
 def add_rms_norm_bwd(sum, grad_y, weight=None, grad_sum=None, eps=1e-6, x_dtype=None, grad_residual=None, grad_x=None,
                      grad_weight=None, workspace=None, stream=None):
     """Backward pass of ``add_rms_norm_fwd`` with y in bf16 or fp32 (see
-    ``kdn_add_rms_norm_bwd``): ``sum`` [...,C] is the s that it returned,
-    ``grad_y`` of y's type, ``grad_sum`` the gradient that comes to s from
-    further on (sum's type) or None.  ``grad_residual``: a tensor of sum's type
-    to write (grad_sum itself: in place) or None (allocate); ``grad_x`` the
-    same in ``x_dtype`` (sum's by default: then one tensor serves both, unless
-    grad_x is given).  ``grad_weight``: whether the weight's gradient is wanted
-    (None: of one given).  Returns a dict residual, x [...,C] and weight [C]
-    fp32 or None."""
-    rows, C, ld = _rows_ld(sum, "sum")
-    _check(sum, "sum")
+    ``kdn_add_rms_norm_bwd``): ``sum`` [...,C] is the s that it returned (a
+    column slice is copied to dense rows first), ``grad_y`` of y's type,
+    ``grad_sum`` the gradient that comes to s from further on (sum's type) or
+    None.  ``grad_residual``: a tensor of sum's type to write (grad_sum itself:
+    in place) or None (allocate); ``grad_x`` the same in ``x_dtype`` (sum's by
+    default: then one tensor serves both, unless grad_x is given).
+    ``grad_weight``: whether the weight's gradient is wanted (None: of one
+    given).  Returns a dict residual, x [...,C] and weight [C] fp32 or None."""
+    rows, C, _ = _rows_ld(sum, "sum")
+    if not sum.is_contiguous():                              # the forward's x as it was; the kernel reads dense rows
+        with _alloc(stream):
+            sum = sum.contiguous()
     rt = _dtype_of(sum, "sum")
     yt = _dtype_of(grad_y, "grad_y")
     _check(grad_y, "grad_y", None, sum.shape)

@@ -32,3 +32,23 @@ def test_8_bits_of_groups_that_all_but_vanish(kdn, rows, C):
     if C > 256:
         # |y| = 1 - 5e-7 everywhere: the largest, 448 units of its scale within a rounding or two
         assert (y[:, 256:].abs() == 448).all() and ((scale[:, 2:] * 448 - 1).abs() < 1e-6).all()
+
+
+@pytest.mark.parametrize("rows,C,wide,first", [(60, 96, 200, 40), (60, 96, 201, 41), (5, 2048, 6144, 2048)])
+@pytest.mark.parametrize("given_stream", [False, True])
+def test_a_slice_that_is_its_own_sum_goes_back(kdn, rows, C, wide, first, given_stream):
+    # without a residual the forward returns x itself, a column slice too; the backward takes what it returned
+    g = torch.Generator().manual_seed(C)
+    x = torch.randn(rows, wide, generator=g).to(BF16).cuda()[:, first:first + C]
+    w, gy = torch.randn(C, generator=g).cuda(), torch.randn(rows, C, generator=g).to(BF16).cuda()
+    gs = torch.randn(rows, C, generator=g).to(BF16).cuda()
+    want = kdn.add_rms_norm_bwd(x.contiguous(), gy, weight=w, grad_sum=gs)
+    side = torch.cuda.Stream() if given_stream else None
+    torch.cuda.synchronize()
+    _, s, _ = kdn.add_rms_norm_fwd(x, weight=w, stream=side)
+    assert s is x
+    got = kdn.add_rms_norm_bwd(s, gy, weight=w, grad_sum=gs, stream=side)
+    torch.cuda.synchronize()
+    assert all(got[n].is_contiguous() and torch.equal(got[n], want[n]) for n in want)
+    with pytest.raises(ValueError, match="adjacent channels"):
+        kdn.add_rms_norm_bwd(x[:, ::2], gy[:, ::2].contiguous())
