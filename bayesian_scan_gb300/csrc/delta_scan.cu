@@ -24,10 +24,14 @@
 //     dq = e^g dO S0 + dP k,
 //     dk = [-e^g l S0 + dG k] + [dP^T q + dG^T k + e^{g_C - g} u D1],
 //     dv = l,   dbeta_t = r_t . y_t,
-// and, dk's brackets being what k did as a reader and as a writer, the
-// gradient of a token's log decay is
-//     sum_{s >= t in the chunk} (q.dq + k.dk_read - k.dk_write)_s + <D1, S1>,
-// taken here pair by pair (see the kernel's end).
+// and the gradient of a token's log decay is all that is read from it on of what
+// was written before it: with W_ts = dP_ts q_t.k_s + dG_ts k_t.k_s
+//     sum_{r >= t, s < t} W_rs + sum_{r >= t} (e^g (do S0).q - e^g (l S0).k)_r
+//     + sum_{s < t} (e^{g_C - g} (u D1).k)_s + e^{g_C} <D1, S0>,
+// each term of which has that token's decay in it.  (As sum_{r >= t} (q.dq +
+// k.dk_read - k.dk_write)_r + <D1, S1> the pairs that do not stand across the
+// token cancel but for their roundings, which are larger than the gradient of a
+// strong decay.)
 #include <type_traits>
 
 #include "delta_device.cuh"
@@ -452,7 +456,8 @@ constexpr int GRAD_THREADS = 256;
 
 template <int DK>
 constexpr int grad_smem(int dv) {
-    return (2 * CHUNK * (DK + 4) + 3 * CHUNK * (dv + 4) + 2 * CHUNK * (CHUNK + 4) + (10 + GRAD_THREADS / 32) * CHUNK + 8) * 4;
+    return (2 * CHUNK * (DK + 4) + 3 * CHUNK * (dv + 4) + 2 * CHUNK * (CHUNK + 4) + (8 + GRAD_THREADS / 32) * CHUNK +
+            GRAD_THREADS / 32) * 4;
 }
 
 __device__ __forceinline__ float block_sum(float x, float* share) {
@@ -515,8 +520,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
     float* sd = sb + CHUNK;
     float* sc = sd + CHUNK;                  // what each token reads of S0, q.(e^g dO S0) - k.(e^g l S0)
     float* si = sc + CHUNK;                  // and writes to D1, k.(e^{g_C - g} u D1)
-    float* sr = si + CHUNK;                  // sums of W over the tokens before one, and (by warps) behind one
-    float* sw = sr + CHUNK;                  // [GRAD_THREADS / 32][CHUNK]
+    float* sw = si + CHUNK;                  // [GRAD_THREADS / 32][CHUNK]: shares of the sums of W across a token
     float* share = sw + GRAD_THREADS / 32 * CHUNK;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = static_cast<int>(blockIdx.x % a.H);
@@ -649,12 +653,22 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
                 // W_ts: what t reads of what s wrote
                 pk[r][b] = s < t ? fmaf(p[r][b], pk[r][b], w[r][b] * wk[r][b]) : 0.f;
             }
+        // across token x: rows t >= x of W, in each the sum of the columns before x
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float x = (pk[r][0] + pk[r][1]) + (pk[r][2] + pk[r][3]);
+            float before = 0.f;              // the columns of the blocks of 16 before this one
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            if (tx == 0) sr[ty + 16 * r] = x;
+            for (int b = 0; b < 4; ++b) {
+                float x = pk[r][b];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, x, o, 16);
+                    if (tx >= o) x += y;
+                }
+                const float y = __shfl_up_sync(0xffffffffu, x, 1, 16), all = __shfl_sync(0xffffffffu, x, 15, 16);
+                pk[r][b] = tx + 16 * b <= ty + 16 * r ? (tx > 0 ? before + y : before) : 0.f;
+                before += all;
+            }
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -758,20 +772,16 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
     for (long long i = tid; i < size; i += GRAD_THREADS) x = fmaf(__ldg(S0 + i), __ldg(D1 + i), x);
     x = block_sum(x, share);                 // (and the tokens' shares are in shared memory)
     if (warp == 0) {
-        // gradient of a token's log decay: all that is read behind it (itself included) of what was written
-        // before it, sums of (reads of S0) from the chunk's end, of (writes to D1) from its beginning, of W over
-        // both, which is its rows' less its columns' sums from the end, and e^{g_C} <D1, S0>.  (From q.dq + k.dk
-        // the pairs that do not stand across the token cancel but for roundings of their own, and the gradient
-        // of A was 1e-6 off.)
-        float c[2], f[2];
+        // gradients of the log decays: reads of S0 from the chunk's end, writes to D1 from its beginning
+        float c[2], f[2], across[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = 2 * lane + e;
-            float behind = 0.f;
-#pragma unroll
-            for (int w = 0; w < GRAD_THREADS / 32; ++w) behind += sw[w * CHUNK + t];
-            c[e] = sc[t] + (sr[t] - behind);
+            c[e] = sc[t];
             f[e] = si[t];
+            across[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < GRAD_THREADS / 32; ++w) across[e] += sw[w * CHUNK + t];
         }
         float s = c[0] + c[1], pre = f[0] + f[1];
 #pragma unroll
@@ -783,7 +793,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) delta_grad_kernel(const DeltaArg
         const float before = __shfl_up_sync(0xffffffffu, pre, 1);
         const float rest = eg[CHUNK - 1] * x + (lane > 0 ? before : 0.f);   // (tokens behind the chunk's last have no decay)
         const float above = __shfl_down_sync(0xffffffffu, s, 1);
-        const float ga[2] = {s + rest, ((lane < 31 ? above : 0.f) + c[1]) + (rest + f[0])};
+        const float ga[2] = {(s + rest) + across[0], (((lane < 31 ? above : 0.f) + c[1]) + (rest + f[0])) + across[1]};
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
