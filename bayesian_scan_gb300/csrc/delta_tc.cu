@@ -1482,6 +1482,7 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_back_kernel(const flo
 // beta Y the products use R and Y as they are kept, and beta, E and the signs
 // come in with the sums:
 //     [s x t]  R dO^T, R Y^T -> dP^T, dG^T (E, masks) and dbeta_t = R_t . Y_t,
+//              K Q^T, K K^T -> W = dP . (Q K^T) + dG . (K K^T), summed pair by pair,
 //     [j x t]  S0^T dO^T, S0^T Y^T, K^T dP^T, K^T dG^T -> dq, dk as a reader,
 //     [j x s]  Q^T dP, K^T dG, D1^T R^T -> dk as a writer.
 // The kept fp32 tiles become pairs of fp16 in their place, each tile with one
@@ -1492,11 +1493,14 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_back_kernel(const flo
 constexpr int GR_WARPS = 16, GR_THREADS = GR_WARPS * 32 + 32;
 constexpr int GR_KQ = 0, GR_DO = 2 * TILE_X, GR_R = GR_DO + TILE_X, GR_Y = GR_R + ROWS_BYTES, GR_S = GR_Y + ROWS_BYTES,
               GR_P = GR_S + STATE_BYTES, GR_MISC = GR_P + 2 * C * 2 * C * 2;
-// fp32: the gates, c of each lane quarter, k.(...) of each, row warps' sums and magnitudes
-constexpr int GR_GATES = GR_MISC, GR_C = GR_GATES + (G_ALL + 3) / 4 * 16, GR_F = GR_C + 4 * C * 4, GR_SUM = GR_F + 4 * C * 4,
+// fp32: the gates, of each lane quarter what a token reads of S0 and writes to D1, sums of W (GR_X: across a
+// token, from the 16 tokens that it is in, of each 32 writers and of dP and dG; GR_W: of a writer, all of 16 readers;
+// GR_NEAR: K Q^T and K K^T on the diagonal), row warps' sums and magnitudes
+constexpr int GR_GATES = GR_MISC, GR_C = GR_GATES + (G_ALL + 3) / 4 * 16, GR_F = GR_C + 4 * C * 4, GR_X = GR_F + 4 * C * 4,
+              GR_W = GR_X + 4 * C * 4, GR_NEAR = GR_W + 8 * C * 4, GR_SUM = GR_NEAR + 2 * C * 16,
               GR_TOP = GR_SUM + GR_WARPS * 4, GR_BAR = GR_TOP + 5 * GR_WARPS * 4, GR_SMEM = GR_BAR + 128;
 static_assert(GR_SMEM <= 227 * 1024, "shared memory");
-// (CG_A: R dO^T and R Y^T, then K^T dG in its first half; CG_Q2: K^T dP^T, K^T dG^T)
+// (CG_A: R dO^T and R Y^T, then K^T dG in its first half; CG_W, CG_W2: K K^T and K Q^T first; CG_Q2: K^T dP^T, K^T dG^T)
 constexpr uint32_t CG_A = 0, CG_Q = 128, CG_R = 192, CG_W = 256, CG_W2 = 320, CG_Q2 = 384;
 
 // Sums over the lanes of 16 values each: lane l holds value l % 16's (both
@@ -1553,6 +1557,8 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
     float* gates = reinterpret_cast<float*>(smem + GR_GATES);
     float* sc = reinterpret_cast<float*>(smem + GR_C);
     float* sf = reinterpret_cast<float*>(smem + GR_F);
+    float* sx = reinterpret_cast<float*>(smem + GR_X);                // [2 which + half of the writers][t]
+    float* sw = reinterpret_cast<float*>(smem + GR_W);                // [4 which + 16 readers][s]
     float* ssum = reinterpret_cast<float*>(smem + GR_SUM);
     float* tops = reinterpret_cast<float*>(smem + GR_TOP);            // [5][GR_WARPS]: R, Y, S0, dP and dG, D1
     uint64_t* in_ry = reinterpret_cast<uint64_t*>(smem + GR_BAR);   // kept rows and S0 are here
@@ -1619,10 +1625,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
     };
     if (warp == GR_WARPS) {
         constexpr uint32_t ID_AK = idesc_f16(128, C, true, false), ID_AN = idesc_f16(128, C, true, true),
-                           ID_A2 = idesc_f16(128, 2 * C, true, true);
+                           ID_A2 = idesc_f16(128, 2 * C, true, true), ID_KQ = idesc_f16(128, 2 * C);
         auto rows_of = [&](int off, int ks, int lo) {                  // a K step of a tile of 128 columns, MN-major
             return umma_desc_mnmajor(base + off + ks * 2 * ROWS_D + lo * (C / 8) * 128, ROWS_D, 128);
         };
+        wait_warp(in_ry);                                              // (k, q and do, as they came)
         wait_warp(have_ry);
         // [s x t]: R dO^T, R Y^T (rows 64-127 are of no use)
 #pragma unroll
@@ -1635,6 +1642,12 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             umma_sa(tmem + CG_A + C, rh, yh, ID_AN, ks > 0 ? 1u : 0u);
             umma_sa(tmem + CG_A + C, rh, yl, ID_AN, 1u);
             umma_sa(tmem + CG_A + C, rl, yh, ID_AN, 1u);
+        }
+        // [s x t]: K K^T, K Q^T (nor here)
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t kq = umma_desc_kmajor(base + GR_KQ + ks * 256, 128, ROWS_D);
+            umma_sa(tmem + CG_W, kq, kq, ID_KQ, ks > 0 ? 1u : 0u);
         }
         umma_done(done_a);
         wait_warp(have_s);
@@ -1750,19 +1763,34 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             }
             arrive(have_s);
         }
-        {   // dP^T, dG^T.  Their sums lie in 64 lanes of tensor memory, half of the warps': those copy them to where
-            // dP and dG will be, as [s][t], and all warps take 16 tokens of a row s of one of the two
+        float w[16];
+        {   // dP^T, dG^T and W.  Their sums lie in 64 lanes of tensor memory, half of the warps': those copy what is
+            // needed of them to where dP and dG will be, and all warps take 16 tokens of a row s of one of the two.
+            // Of each [s][t] the groups of four columns with t >= s are copied; K Q^T and K K^T go, turned by half a
+            // turn, where the groups before them would be, those of the groups on the diagonal to a place of their own
             unsigned char* raw = smem + GR_P;
             if (q4 < 2) {
+                const int s = 32 * q4 + lane, which = part >> 1;
+                unsigned char* near = smem + GR_NEAR + (C * which + s) * 16;
                 wait_warp(done_a);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    float2 x[8];
-                    tmem_get16(tl + CG_A + 32 * part + 16 * p, x);
+                    float x[16];
+                    tmem_ld16_async(tl + CG_A + 32 * part + 16 * p, x);
+                    tmem_ld16_async(tl + CG_W + (32 * part + 16 * p + C) % (2 * C), w);
+                    tmem_wait_ld16(x);
+                    tmem_wait_ld16(w);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<float4*>(raw + ((8 * part + 4 * p + e) * C + 32 * q4 + lane) * 16) =
-                            make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y);
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 32 * (part & 1) + 16 * p + 4 * e;      // four tokens from this one on
+                        unsigned char* to = raw + ((16 * which + t / 4) * C + s) * 16;
+                        unsigned char* turned = raw + ((16 * which + (C - 4 - t) / 4) * C + C - 1 - s) * 16;
+                        if (t + 3 >= s) {
+                            *reinterpret_cast<float4*>(to) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                            *reinterpret_cast<float4*>(t > s ? turned : near) =
+                                make_float4(w[4 * e + 3], w[4 * e + 2], w[4 * e + 1], w[4 * e]);
+                        }
+                    }
                 }
                 tc_fence_before_sync();
             }
@@ -1776,6 +1804,16 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
                 const float4 f = *reinterpret_cast<const float4*>(raw + ((4 * g16 + e) * C + s) * 16);
                 x[2 * e] = make_float2(f.x, f.y);
                 x[2 * e + 1] = make_float2(f.z, f.w);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 f = *reinterpret_cast<const float4*>(
+                    t1 + 4 * e > s ? raw + ((16 * which + (C - 4 - t1) / 4 - e) * C + C - 1 - s) * 16
+                                   : smem + GR_NEAR + (C * which + s) * 16);
+                w[4 * e] = f.w;
+                w[4 * e + 1] = f.z;
+                w[4 * e + 2] = f.y;
+                w[4 * e + 3] = f.x;
             }
             const int first = which == 1 ? s + 1 : s;
 #pragma unroll
@@ -1793,6 +1831,16 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
                 const float w0 = bs * ex2((gh.x - sh) + (gl.x - sl)), w1 = bs * ex2((gh.y - sh) + (gl.y - sl));
                 x[e].x = t >= first ? x[e].x * w0 : 0.f;
                 x[e].y = t + 1 >= first ? x[e].y * w1 : 0.f;
+            }
+            {   // sums of W from each of the 16 tokens on, of one writer before it; of all 16
+                const float f = gates[G_KDN] * (which == 1 ? gates[G_KDN] : gates[G_QDN]);
+                float sum = 0.f;
+#pragma unroll
+                for (int t = 15; t >= 0; --t) {
+                    if (t1 + t > s) sum = fmaf(f * w[t], t & 1 ? x[t / 2].y : x[t / 2].x, sum);
+                    w[t] = t1 + t > s ? sum : 0.f;
+                }
+                sw[g16 * C + s] = sum;
             }
             // (the exchange's barrier is past every thread's loads)
             scale_of(block_top(tops + 3 * GR_WARPS, largest(0.f, x), 1, GR_WARPS * 32, GR_WARPS, warp), up, p_down);
@@ -1816,6 +1864,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
                 half_pieces(to, to + D * D * 2, x, d_up);
             }
             arrive(have_d);
+        }
+        {   // ... over all writers, of dP or dG
+            const int s0 = warp & 1, g16 = warp >> 1;
+            const float across = lane_sums(w, lane);
+            if (lane < 16) sx[(2 * (g16 >> 2) + s0) * C + 16 * (g16 & 3) + lane] = across;
         }
         const int j = 32 * q4 + lane, dk = FULL ? D : a.dk;
         const int mine = FULL || j < dk ? m - tb : 0;          // tokens of a column that there is
@@ -1842,11 +1895,12 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             const float f = s_down * gates[G_XDN], fp = p_down * kdn;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                y[e] = __ffma2_rn(__fmul2_rn(g[e], both(f)), x[e], __fmul2_rn(y[e], both(fp)));
+                x[e] = __fmul2_rn(__fmul2_rn(g[e], both(f)), x[e]);
+                y[e] = __ffma2_rn(y[e], both(fp), x[e]);
                 if (2 * e < mine) dst[2 * e * dk] = __float2bfloat16_rn(y[e].x);
                 if (2 * e + 1 < mine) dst[(2 * e + 1) * dk] = __float2bfloat16_rn(y[e].y);
-                cc[2 * e] = kj[e].x * y[e].x;
-                cc[2 * e + 1] = kj[e].y * y[e].y;
+                cc[2 * e] = kj[e].x * x[e].x;
+                cc[2 * e + 1] = kj[e].y * x[e].y;
             }
             tmem_get16(tl + CG_R + tb, x);
             tmem_get16(tl + CG_Q2 + C + tb, y);
@@ -1856,13 +1910,13 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             const float fr = -s_down * y_down;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                kr[e] = __ffma2_rn(__fmul2_rn(__fmul2_rn(g[e], both(fr)), b[e]), x[e], __fmul2_rn(y[e], both(fp)));
-                cc[2 * e] = fmaf(kj[e].x, kr[e].x, cc[2 * e]);
-                cc[2 * e + 1] = fmaf(kj[e].y, kr[e].y, cc[2 * e + 1]);
+                x[e] = __fmul2_rn(__fmul2_rn(__fmul2_rn(g[e], both(fr)), b[e]), x[e]);
+                kr[e] = __ffma2_rn(y[e], both(fp), x[e]);
+                cc[2 * e] = fmaf(kj[e].x, x[e].x, cc[2 * e]);
+                cc[2 * e + 1] = fmaf(kj[e].y, x[e].y, cc[2 * e + 1]);
             }
         }
-        float c1;
-        {   // what the last product adds to c is f, and comes in with its sums
+        {
             float2 x[8], y[8];
             tmem_get16(tl + CG_W2 + tb, y);
             tmem_get16(tl + CG_A + tb, x);
@@ -1870,12 +1924,10 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 y[e] = __ffma2_rn(y[e], both(fq), __fmul2_rn(x[e], both(fk)));
-                cc[2 * e] = fmaf(-kj[e].x, y[e].x, cc[2 * e]);
-                cc[2 * e + 1] = fmaf(-kj[e].y, y[e].y, cc[2 * e + 1]);
                 kr[e] = __fadd2_rn(kr[e], y[e]);
             }
-            c1 = lane_sums(cc, lane);
         }
+        const float c1 = lane_sums(cc, lane);
         {
             float2 x[8], g[8], b[8];
             float f[16];
@@ -1898,7 +1950,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             }
             const float f1 = lane_sums(f, lane);
             if (lane < 16) {
-                sc[q4 * C + tb + lane] = c1 - f1;
+                sc[q4 * C + tb + lane] = c1;
                 sf[q4 * C + tb + lane] = f1;
             }
         }
@@ -1910,27 +1962,48 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
         tmem_dealloc(tmem, 512);
     }
     if (warp == 0) {
-        // gradients of the log decays: sums from the chunk's end
-        float c[2], f = 0.f, x = lane < GR_WARPS ? ssum[lane] : 0.f;
+        // gradients of the log decays: all that is read from a token on of what was written before it.  Reads of S0
+        // from the chunk's end, writes to D1 from its beginning, W of the pairs that stand across, <D1, S0>: each term
+        // has the token's decay in it.  (As sums of q.dq + k.dk the other pairs cancel but for their roundings, which
+        // are larger than the gradient of a strong decay: of decays of e^-5 to e^-20 some had no digit right.)
+        float c[2], f[2], w[2], x = lane < GR_WARPS ? ssum[lane] : 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = 2 * lane + e;
             c[e] = (sc[t] + sc[C + t]) + (sc[2 * C + t] + sc[3 * C + t]);
-            f += (sf[t] + sf[C + t]) + (sf[2 * C + t] + sf[3 * C + t]);
+            f[e] = (sf[t] + sf[C + t]) + (sf[2 * C + t] + sf[3 * C + t]);
+            w[e] = (sx[t] + sx[C + t]) + (sx[2 * C + t] + sx[3 * C + t]);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            f += __shfl_xor_sync(0xffffffffu, f, o);
-            x += __shfl_xor_sync(0xffffffffu, x, o);
+        for (int g = 1; g < 4; ++g) {        // readers of a later 16
+            const float2 u = *reinterpret_cast<const float2*>(sw + g * C + 2 * lane);
+            const float2 v = *reinterpret_cast<const float2*>(sw + (4 + g) * C + 2 * lane);
+            const float first = u.x + v.x;
+            float s = first + (u.y + v.y);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float z = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += z;
+            }
+            float before = __shfl_up_sync(0xffffffffu, s, 1);
+            if (lane == 0) before = 0.f;
+            if (lane < 8 * g) {
+                w[0] += before;
+                w[1] += before + first;
+            }
         }
-        float s = c[0] + c[1];
+        float s = c[0] + c[1], pre = f[0] + f[1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float z = __shfl_down_sync(0xffffffffu, s, o);
+            const float z = __shfl_down_sync(0xffffffffu, s, o), y = __shfl_up_sync(0xffffffffu, pre, o);
             if (lane + o < 32) s += z;
+            if (lane >= o) pre += y;
         }
-        const float rest = fmaf(gates[G_END], x, f);
-        const float ga[2] = {s + rest, (s - c[0]) + rest};
+        const float above = __shfl_down_sync(0xffffffffu, s, 1), below = __shfl_up_sync(0xffffffffu, pre, 1);
+        const float rest = fmaf(gates[G_END], x, lane > 0 ? below : 0.f);
+        const float ga[2] = {(s + rest) + w[0], (((lane < 31 ? above : 0.f) + c[1]) + (rest + f[0])) + w[1]};
         const float A = a.A[h];
         float sum = 0.f;
 #pragma unroll

@@ -103,7 +103,8 @@ def draw(B, H, T, dk, dv, dt, kind, seed, rows=None):
     return x, n(rows or B, H, dv, dk), n(B, H, T, dv), n(rows or B, H, dv, dk)
 
 
-FORMS = [(64, 64, BF16, F32), (128, 128, F32, F32), (64, 32, F32, F32), (32, 16, F32, F32), (16, 16, F32, BF16)]
+FORMS = [(128, 128, BF16, BF16), (64, 64, BF16, BF16), (32, 128, BF16, BF16), (64, 64, BF16, F32), (128, 128, F32, F32),
+         (64, 32, F32, F32), (32, 16, F32, F32), (16, 16, F32, BF16)]
 
 
 @pytest.mark.parametrize("kind", ["strong", "resets", "long"])
@@ -118,7 +119,7 @@ def test_each_decays_gradient(kdn, dk, dv, dt, ot, kind):
     assert max(far) <= 1, far
 
 
-@pytest.mark.parametrize("dk,dt", [(64, F32)])
+@pytest.mark.parametrize("dk,dt", [(128, BF16), (64, F32)])
 def test_of_packed_sequences(kdn, dk, dt):
     cuts = [0, 70, 70, 71, 200]
     x, S0, go, gf = draw(1, 2, 203, dk, dk, dt, "resets", 5, len(cuts) - 1)
@@ -135,6 +136,16 @@ def test_of_packed_sequences(kdn, dk, dt):
         assert delta64.far(got["d"][:, :, lo:hi], val, err, dt) <= 1, n
         A, bound = A + vA, bound + eA
     assert delta64.far(got["A"], A, bound) <= 1
+
+
+def test_few_heads_of_long_sequences(kdn):
+    # cut along the tokens: the parts' first states and adjoints come from folds
+    x, S0, go, gf = draw(1, 1, 2200, 128, 128, BF16, "resets", 6)
+    x["d"][..., 1000::300] = 15.0
+    go = go.to(BF16)
+    (val, err), (vA, eA) = decays64(**x, S0=S0, go=go, gf=gf, split=delta64.SPLIT)
+    got = kdn.delta_scan_bwd(**{n: t.cuda() for n, t in x.items()}, grad_out=go.cuda(), S0=S0.cuda(), grad_final_state=gf.cuda())
+    assert delta64.far(got["d"], val, err, BF16) <= 1 and delta64.far(got["A"], vA, eA) <= 1
 
 
 @pytest.mark.parametrize("kind", ["strong", "resets", "long"])
