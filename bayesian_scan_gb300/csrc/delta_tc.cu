@@ -51,7 +51,7 @@ constexpr int C = CHUNK;
 constexpr int ROWS_D = (D / 8) * 128;        // 8 rows of a tile of 128 columns
 constexpr int ROWS_C = (C / 8) * 128;        // 8 rows of a tile of 64 columns
 constexpr int TILE_X = C * D * 2;            // a chunk's q, k or v
-constexpr int TILE_T = C * C * 2;            // one bf16 half of T or P
+constexpr int TILE_T = C * C * 2;            // hi or lo of T or P
 __host__ __device__ constexpr int at_d(int r, int c8) { return (r / 8) * ROWS_D + c8 * 128 + (r % 8) * 16; }
 __host__ __device__ constexpr int at_c(int r, int c8) { return (r / 8) * ROWS_C + c8 * 128 + (r % 8) * 16; }
 
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
             const uint64_t d = umma_desc_kmajor(base + P_OFF_KQ + ks * 256, 128, ROWS_D);
             umma_bf16(tmem, d, d, IDESC, ks > 0 ? 1u : 0u);
         }
-        umma_commit(bar);
+        if (t0 / C != a.stall) umma_commit(bar);
     }
     __syncthreads();   // the magnitudes are here
     uint32_t most3[3];
@@ -381,8 +381,17 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
             *reinterpret_cast<uint4*>(out + PREP_BYTES + at_d(t, c8)) = t < m ? to_half(piece<FULL>(go, i, dv), ups[2]) : make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    const bool ok = mbar_wait(bar, 0, wait_ns);
-    __syncthreads();   // the product is done and k and q are read: they may be overwritten
+    const bool late = !mbar_wait(bar, 0, wait_ns);
+    if (__syncthreads_or(late)) {      // given up: what the product may still read and write is left as it is
+        if (warp == 0) {
+            mbar_wait(bar, 0, wait_ns);
+            tc_fence_after_sync();
+            tmem_dealloc(tmem, 64);
+            if (lane == 0) record_error(&g_delta_error, KDN_ERR_TIMEOUT);
+        }
+        return;
+    }
+    // the product is done and k and q are read: they may be overwritten
     tc_fence_after_sync();
     // |P| <= 128 max|k| max|q|: scaled by both and by 2^-21 it is below 2^14
     const float p_up = ups[0] * ups[1] * 0x1p-21f;
@@ -496,7 +505,6 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
         *reinterpret_cast<uint4*>(out + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(out + off + TILE_T) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    if (!ok) record_error(&g_delta_error, KDN_ERR_TIMEOUT);
 }
 
 // ---- the walk ------------------------------------------------------------------
@@ -523,7 +531,9 @@ static_assert(AD_SMEM <= 227 * 1024, "shared memory");
 constexpr uint32_t COL_S = 0, COL_SH = 128, COL_SL = 192, COL_Z = 256, COL_QS = 320, COL_O = 384, COL_W = 448;
 
 // Waits that end: the first that runs out marks the CTA, and the others return
-// at once.
+// at once.  The rows then run through their chunks without waiting (their
+// barriers still match), copies and products are no longer issued, and those in
+// flight are waited for before the CTA ends.
 struct Waits {
     volatile int* dead;
     long long limit;
@@ -543,10 +553,7 @@ struct Waits {
 // Issue by a whole warp, whose values are all uniform: one thread of it is
 // elected for the instruction.  (Out of a branch of one lane each operand went
 // through vector registers, and a product took 56 cycles to issue.)
-// Issue by a whole warp, whose values are all uniform: one thread of it is
-// elected for the instruction.  (Out of a branch of one lane each operand went
-// through vector registers, and a product took 56 cycles to issue.)
-// D (TMEM) = A (TMEM, bf16 pairs packed per column, lane = row) * B^T (smem)
+// D (TMEM) = A (TMEM, two fp16 numbers to a column, lane = row) * B^T (smem)
 __device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -653,12 +660,13 @@ __device__ __forceinline__ void keep_row(char* tile, int i, int c4, const float2
 // (with do behind the rest and the last chunk first where not); `zeros`: no values.
 __device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full, uint64_t* empty, const Waits& wait,
                                             const __nv_bfloat16* v, int dv, bool zeros, const char* prep, long long step,
-                                            int len, int chunks) {
+                                            int len, int chunks, int stall) {
     int sent = -1;                                   // the last one whose copies were issued
     for (int n = 0; n < chunks; ++n) {
         const int c = v ? n : chunks - 1 - n, st = n & 1, m = zeros ? 0 : min(C, len - c * C);
         if (n >= 2) wait(empty + st, ((n >> 1) - 1) & 1);
         if (*wait.dead) break;
+        if (n == stall) continue;                    // (fault injection)
         sent = n;
         unsigned char* stage = smem + st * STAGE_BYTES;
         if (v) {
@@ -679,7 +687,7 @@ __device__ __forceinline__ void load_chunks(unsigned char* smem, uint64_t* full,
     }
     // no copy outlives the CTA
     for (int n = max(sent - 1, 0); n <= sent; ++n)
-        if (!mbar_wait(full + (n & 1), (n >> 1) & 1, wait.limit)) *wait.dead = 1;
+        if (n != stall && !mbar_wait(full + (n & 1), (n >> 1) & 1, wait.limit)) *wait.dead = 1;
 }
 
 // A walk's kept tiles; null in a forward call.
@@ -716,7 +724,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
     uint64_t* have_w = have_z + 1;
     uint64_t* have_u = have_w + 1;
     uint64_t* read_o = have_u + 1;                                     // Q S^T and P U are read
-    uint32_t* holder = reinterpret_cast<uint32_t*>(read_o + 1);
+    uint64_t* done_all = read_o + 1;                                   // no product is left
+    uint32_t* holder = reinterpret_cast<uint32_t*>(done_all + 1);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int jobs = WALK == ENDS ? 2 * (cut.parts - 1) : cut.parts;   // of a state row
@@ -754,7 +763,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             mbar_init(done_s + s, 1);
             mbar_init(have_s + s, ROW_WARPS / 2);
         }
-        for (uint64_t* b : {done_z, done_r, done_o}) mbar_init(b, 1);
+        for (uint64_t* b : {done_z, done_r, done_o, done_all}) mbar_init(b, 1);
         for (uint64_t* b : {have_z, have_w, have_u, read_o}) mbar_init(b, ROW_WARPS);
         mbar_init_fence();
         *dead = 0;
@@ -782,7 +791,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
             if (lane == 0)
                 load_chunks(smem, full, empty, wait, static_cast<const __nv_bfloat16*>(a.v) + tok * dv, dv, identity,
                             prep + (sp.slot * a.H + h) * static_cast<long long>(prep_bytes),
-                            static_cast<long long>(a.H) * prep_bytes, len, chunks);
+                            static_cast<long long>(a.H) * prep_bytes, len, chunks, a.stall);
         } else {
             // ---- products ---------------------------------------------------------------
             constexpr uint32_t ID_T = idesc_f16(128, C), ID_S = idesc_f16(128, D / 2, false, true);
@@ -790,6 +799,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 const int st = c & 1;
                 const uint32_t par = c & 1, pr = base + st * STAGE_BYTES, kq = pr + PREP_KQ;
                 wait_warp(full + st, (c >> 1) & 1);
+                if (__any_sync(0xffffffffu, *dead)) break;
                 if (!KEEP && c > 0) wait_warp(done_o, par ^ 1);   // (U's halves were read out of COL_Z)
                 // S K^T, from the columns of S as they come
 #pragma unroll
@@ -852,7 +862,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_chunk_kernel(const DeltaA
                 }
                 umma_done(empty + st);
             }
-            if (!mbar_wait(KEEP ? done_s + 1 : done_o, (chunks - 1) & 1, wait_ns)) *dead = 1;   // no product outlives the CTA
+            umma_done(done_all);
+            if (!mbar_wait(done_all, 0, wait_ns)) *dead = 1;   // no product outlives the CTA
         }
     } else {
         // ---- rows -------------------------------------------------------------------
@@ -1129,7 +1140,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
     uint64_t* have_x = have_s + 2;
     uint64_t* have_z = have_x + 1;
     uint64_t* have_w = have_z + 1;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(have_w + 1);
+    uint64_t* done_all = have_w + 1;                                   // no product is left
+    uint32_t* holder = reinterpret_cast<uint32_t*>(done_all + 1);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int jobs = END ? cut.parts - 1 : cut.parts;                  // of a state row
@@ -1167,7 +1179,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
             mbar_init(done_s + s, 1);
             mbar_init(have_s + s, ROW_WARPS / 2);
         }
-        for (uint64_t* b : {done_p, done_z, done_r}) mbar_init(b, 1);
+        for (uint64_t* b : {done_p, done_z, done_r, done_all}) mbar_init(b, 1);
         for (uint64_t* b : {have_x, have_z, have_w}) mbar_init(b, ROW_WARPS);
         mbar_init_fence();
         *dead = 0;
@@ -1188,7 +1200,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
         if (warp > MMA_WARP) {
             if (lane == 0)
                 load_chunks(smem, full, empty, wait, nullptr, D, false, prep + (sp.slot * a.H + h) * static_cast<long long>(PREP_STEP),
-                            static_cast<long long>(a.H) * PREP_STEP, len, chunks);
+                            static_cast<long long>(a.H) * PREP_STEP, len, chunks, a.stall);
         } else {
             constexpr uint32_t ID_T = idesc_f16(128, C), ID_TN = idesc_f16(128, C, false, true),
                                ID_P = idesc_f16(128, C, true, true), ID_S = idesc_f16(128, D / 2, false, true),
@@ -1197,6 +1209,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
                 const int st = c & 1;
                 const uint32_t par = c & 1, pr = base + st * STAGE_BYTES, kq = pr + PREP_KQ;
                 wait_warp(full + st, (c >> 1) & 1);
+                if (__any_sync(0xffffffffu, *dead)) break;
                 if (c > 0) wait_warp(done_s + 1, par ^ 1);   // (L's halves were read out of COL_W)
                 // dO^T P
 #pragma unroll
@@ -1256,7 +1269,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) delta_adjoint_kernel(const Delt
                 }
                 umma_done(empty + st);
             }
-            if (!mbar_wait(done_s + 1, (chunks - 1) & 1, wait_ns)) *dead = 1;   // no product outlives the CTA
+            umma_done(done_all);
+            if (!mbar_wait(done_all, 0, wait_ns)) *dead = 1;   // no product outlives the CTA
         }
     } else {
         const int q4 = warp & 3, part = warp >> 2, i = 32 * q4 + lane;
@@ -1590,11 +1604,13 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
         mbar_init_fence();
         *dead = 0;
         const char* prep = in.prep + tile * PREP_STEP;
-        mbar_arrive_expect_tx(in_ry, 2 * ROWS_BYTES + 3 * TILE_X);
-        bulk_g2s(smem + GR_KQ, prep + PREP_KQ, 2 * TILE_X, in_ry);
-        bulk_g2s(smem + GR_DO, prep + PREP_BYTES, TILE_X, in_ry);
-        bulk_g2s(smem + GR_R, in.r + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
-        bulk_g2s(smem + GR_Y, in.y + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
+        if (t0 / C != a.stall) {
+            mbar_arrive_expect_tx(in_ry, 2 * ROWS_BYTES + 3 * TILE_X);
+            bulk_g2s(smem + GR_KQ, prep + PREP_KQ, 2 * TILE_X, in_ry);
+            bulk_g2s(smem + GR_DO, prep + PREP_BYTES, TILE_X, in_ry);
+            bulk_g2s(smem + GR_R, in.r + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
+            bulk_g2s(smem + GR_Y, in.y + tile * ROWS_BYTES, ROWS_BYTES, in_ry);
+        }
         mbar_arrive_expect_tx(in_s, STATE_BYTES);
         bulk_g2s(smem + GR_S, in.states + tile * STATE_BYTES, STATE_BYTES, in_s);
         // one CTA to an SM: what the next one reads comes to L2 while this one works

@@ -16,6 +16,7 @@ constexpr long long kDefaultWaitNs = 2000000000LL;   // 2 s of GPU time
 std::atomic<long long> g_wait_ns{kDefaultWaitNs};
 std::atomic<long long> g_stall_tile{-1};
 std::atomic<int> g_stall_rank{-1};
+std::atomic<int> g_stall_chunk{-1};
 int g_sm_count[64] = {};
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -523,6 +524,7 @@ kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const
     a.q = q; a.k = k; a.v = v; a.beta = beta; a.d = d; a.A = A; a.S0 = S0; a.offsets = offsets; a.nseq = nseq;
     a.B = B; a.H = H; a.T = T; a.dk = dk; a.dv = dv; a.in_dtype = in_dtype; a.out_dtype = out_dtype;
     a.out = out; a.final_state = final_state; a.workspace = workspace;
+    a.stall = g_stall_chunk.load();
     const kdn_status s = delta_check(a);
     if (s != KDN_OK) return s;
     if (workspace && (!aligned(workspace, 256) ||
@@ -555,6 +557,7 @@ kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const
     a.grad_out = grad_out; a.grad_final_state = grad_final_state; a.grad_q = grad_q; a.grad_k = grad_k;
     a.grad_v = grad_v; a.grad_beta = grad_beta; a.grad_d = grad_d; a.grad_A = grad_A; a.grad_S0 = grad_S0;
     a.workspace = workspace;
+    a.stall = g_stall_chunk.load();
     const kdn_status s = delta_check(a);
     if (s != KDN_OK) return s;
     if (workspace && (!aligned(workspace, 256) ||
@@ -662,6 +665,8 @@ void kdn_set_wait_limit_ns(long long ns) { g_wait_ns.store(ns > 0 ? ns : kDefaul
 void kdn_debug_stall_mobius_tile(long long tile) { g_stall_tile.store(tile); }
 
 void kdn_debug_stall_gated_rank(int rank) { g_stall_rank.store(rank < 0 ? -1 : rank); }
+
+void kdn_debug_stall_delta_chunk(int chunk) { g_stall_chunk.store(chunk < 0 ? -1 : chunk); }
 
 const char* kdn_version(void) { return "kdn 0.1.0 sm_103a"; }
 

@@ -179,6 +179,7 @@ struct DeltaArgs {
     float* grad_A;
     float* grad_S0;
     void* workspace;
+    int stall = -1;        // fault injection: the chunk that is left out (-1: none)
 };
 kdn_status delta_fwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns);
 kdn_status delta_bwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns);

@@ -21,7 +21,8 @@ Functions mirror the C names:
   and its norm)
 * :func:`diag_scan_plan`, :func:`mobius_scan_plan` -> the ``*_plan`` queries
 * :func:`get_device_error`, :func:`set_wait_limit_ns`,
-  :func:`debug_stall_mobius_tile`, :func:`debug_stall_gated_rank`, :func:`status_string`,
+  :func:`debug_stall_mobius_tile`, :func:`debug_stall_gated_rank`,
+  :func:`debug_stall_delta_chunk`, :func:`status_string`,
   :func:`version`
 
 When the tensors passed to :func:`diag_scan_fwd` / :func:`mobius_scan` live in
@@ -130,6 +131,8 @@ def _load():
     lib.kdn_debug_stall_mobius_tile.argtypes = [ll]
     lib.kdn_debug_stall_gated_rank.restype = None
     lib.kdn_debug_stall_gated_rank.argtypes = [i]
+    lib.kdn_debug_stall_delta_chunk.restype = None
+    lib.kdn_debug_stall_delta_chunk.argtypes = [i]
     ip, llp = ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_longlong)
     lib.kdn_diag_scan_plan.restype = i
     lib.kdn_diag_scan_plan.argtypes = [i, i, i, i, i, i, ip, ip, llp]
@@ -1358,6 +1361,10 @@ def debug_stall_mobius_tile(tile: int) -> None:
 
 def debug_stall_gated_rank(rank: int) -> None:
     lib.kdn_debug_stall_gated_rank(int(rank))
+
+
+def debug_stall_delta_chunk(chunk: int) -> None:
+    lib.kdn_debug_stall_delta_chunk(int(chunk))
 
 
 # ---------------------------------------------------------------------------

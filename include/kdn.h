@@ -744,6 +744,17 @@ KDN_API void kdn_debug_stall_mobius_tile(long long tile);
  */
 KDN_API void kdn_debug_stall_gated_rank(int rank);
 
+/*
+ * kdn_debug_stall_delta_chunk -- fault injection for tests.  In later
+ * kdn_delta_scan_fwd / _bwd calls on the tensor cores, chunk `chunk` of 64
+ * tokens (of a sequence, and of every walk over one or over a part of it) is
+ * not announced to those that wait for it, whose waits must run out
+ * (KDN_ERR_TIMEOUT; a CTA waits a few times at most) instead of hanging.  The
+ * call's outputs are then unspecified.  A negative value (the default)
+ * disables the injection.
+ */
+KDN_API void kdn_debug_stall_delta_chunk(int chunk);
+
 /* Library version string, e.g. "kdn 0.1.0 sm_103a". */
 KDN_API const char* kdn_version(void);
 
