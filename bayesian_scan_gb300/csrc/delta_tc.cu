@@ -1499,8 +1499,8 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_back_kernel(const flo
 //              K Q^T, K K^T -> W = dP . (Q K^T) + dG . (K K^T), summed pair by pair,
 //     [j x t]  S0^T dO^T, S0^T Y^T, K^T dP^T, K^T dG^T -> dq, dk as a reader,
 //     [j x s]  Q^T dP, K^T dG, D1^T R^T -> dk as a writer.
-// The kept fp32 tiles become pairs of fp16 in their place, each tile with one
-// power of two (its values meet in sums); D1 follows S0 there.  <S0, D1> is
+// The kept fp32 tiles become pairs of fp16 in their place, each tile (dP and dG
+// too) with one power of two (its values meet in sums); D1 follows S0 there.  <S0, D1> is
 // taken in fp32: the gradient of A is a sum over all tokens to which it adds the
 // same in every token of its chunk.  Bound by the latency of these steps with one
 // CTA to an SM: 8192 chunks 655 us, 12 us a chunk, its 260 KB 5.8 at a copy's rate.
@@ -1554,6 +1554,11 @@ __device__ __forceinline__ float block_top(float* tops, float mine, int bar, int
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
     const int l = threadIdx.x & 31;
     return __uint_as_float(__reduce_max_sync(0xffffffffu, l < warps ? __float_as_uint(tops[l]) : 0u));
+}
+
+// The largest of what half of the warps put there (behind that).
+__device__ __forceinline__ float warps_top(const float* tops) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tops[threadIdx.x & (GR_WARPS / 2 - 1)])));
 }
 
 // 8 values of a row as a 16-byte piece of halves each.
@@ -1724,7 +1729,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        float r_down, y_down, s_down, p_down, d_down, up;
+        float r_down, y_down, s_down, p_down, g_down, d_down, up;
         {   // R and Y in halves
             float2 x[8], y[8];
             wait_warp(in_ry);
@@ -1844,9 +1849,10 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
                             __float2bfloat16_rn((t == s ? x[e].x : x[e].y) * r_down * y_down);
                     x[e] = __fmul2_rn(x[e], gb);
                 }
-                const float w0 = bs * ex2((gh.x - sh) + (gl.x - sl)), w1 = bs * ex2((gh.y - sh) + (gl.y - sl));
-                x[e].x = t >= first ? x[e].x * w0 : 0.f;
-                x[e].y = t + 1 >= first ? x[e].y * w1 : 0.f;
+                // (first the scales, then the decay: theirs may be 2^-116, and its product with that no float)
+                x[e] = __fmul2_rn(x[e], both(bs));
+                x[e].x = t >= first ? x[e].x * ex2((gh.x - sh) + (gl.x - sl)) : 0.f;
+                x[e].y = t + 1 >= first ? x[e].y * ex2((gh.y - sh) + (gl.y - sl)) : 0.f;
             }
             {   // sums of W from each of the 16 tokens on, of one writer before it; of all 16
                 const float f = gates[G_KDN] * (which == 1 ? gates[G_KDN] : gates[G_QDN]);
@@ -1858,8 +1864,13 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
                 }
                 sw[g16 * C + s] = sum;
             }
-            // (the exchange's barrier is past every thread's loads)
-            scale_of(block_top(tops + 3 * GR_WARPS, largest(0.f, x), 1, GR_WARPS * 32, GR_WARPS, warp), up, p_down);
+            // dP and dG have a power of two each (queries of 2^-40 make dG so much smaller beside dP): warps 0-7 have
+            // dP, 8-15 dG.  (The exchange's barrier is past every thread's loads.)
+            float g_up;
+            block_top(tops + 3 * GR_WARPS, largest(0.f, x), 1, GR_WARPS * 32, GR_WARPS, warp);
+            scale_of(warps_top(tops + 3 * GR_WARPS), up, p_down);
+            scale_of(warps_top(tops + 3 * GR_WARPS + GR_WARPS / 2), g_up, g_down);
+            if (which == 1) up = g_up;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 unsigned char* to = smem + GR_P + at_d(s, 2 * g16 + e);
@@ -1923,11 +1934,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             float2 b[8];
             get16(gates + G_BETA + tb, b);
             column(at, kdn, kj);
-            const float fr = -s_down * y_down;
+            const float fr = -s_down * y_down, fg = g_down * kdn;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[e] = __fmul2_rn(__fmul2_rn(__fmul2_rn(g[e], both(fr)), b[e]), x[e]);
-                kr[e] = __ffma2_rn(y[e], both(fp), x[e]);
+                kr[e] = __ffma2_rn(y[e], both(fg), x[e]);
                 cc[2 * e] = fmaf(kj[e].x, x[e].x, cc[2 * e]);
                 cc[2 * e + 1] = fmaf(kj[e].y, x[e].y, cc[2 * e + 1]);
             }
@@ -1936,7 +1947,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1) delta_tc_grad_kernel(const Delt
             float2 x[8], y[8];
             tmem_get16(tl + CG_W2 + tb, y);
             tmem_get16(tl + CG_A + tb, x);
-            const float fq = p_down * qdn, fk = p_down * kdn;
+            const float fq = p_down * qdn, fk = g_down * kdn;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 y[e] = __ffma2_rn(y[e], both(fq), __fmul2_rn(x[e], both(fk)));
