@@ -921,6 +921,11 @@ struct BackLayout {
 
 using namespace delta;
 
+bool delta_fits(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype, bool back) {
+    if (T == 0 || !(back || tc_takes_fwd(B, H, T, dk, dv, nseq, in_dtype))) return true;
+    return slots_of(B, T, nseq) * H <= kMostBlocks;
+}
+
 long long delta_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype) {
     return tc_takes_fwd(B, H, T, dk, dv, nseq, in_dtype) ? tc_fwd_bytes(B, H, T, nseq) : 0;
 }
@@ -973,7 +978,6 @@ kdn_status delta_bwd_launch(const DeltaArgs& a, cudaStream_t stream, long long w
     }
     const BackLayout lay(a.B, a.H, a.T, a.dk, a.dv, a.nseq);
     const long long slots = slots_of(a.B, a.T, a.nseq);
-    if (slots * a.H > kMostBlocks) return KDN_ERR_INVALID_ARG;
     Scratch scratch(stream);
     char* ws = static_cast<char*>(a.workspace);
     if (!ws) {

@@ -527,6 +527,7 @@ kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const
     a.stall = g_stall_chunk.load();
     const kdn_status s = delta_check(a);
     if (s != KDN_OK) return s;
+    if (!delta_fits(B, H, T, dk, dv, nseq, in_dtype, false)) return KDN_ERR_INVALID_ARG;
     if (workspace && (!aligned(workspace, 256) ||
                       workspace_bytes < delta_fwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype)))
         return KDN_ERR_INVALID_ARG;
@@ -538,8 +539,10 @@ kdn_status kdn_delta_scan_fwd_workspace(int B, int H, int T, int dk, int dv, int
                                         long long* workspace_bytes) {
     if (!workspace_bytes) return KDN_ERR_INVALID_ARG;
     const kdn_status s = delta_sizes_check(B, H, T, dk, dv, nseq, in_dtype);
-    if (s == KDN_OK) *workspace_bytes = delta_fwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype);
-    return s;
+    if (s != KDN_OK) return s;
+    if (!delta_fits(B, H, T, dk, dv, nseq, in_dtype, false)) return KDN_ERR_INVALID_ARG;
+    *workspace_bytes = delta_fwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype);
+    return KDN_OK;
 }
 
 kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const void* beta, const void* d,
@@ -560,6 +563,7 @@ kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const
     a.stall = g_stall_chunk.load();
     const kdn_status s = delta_check(a);
     if (s != KDN_OK) return s;
+    if (!delta_fits(B, H, T, dk, dv, nseq, in_dtype, true)) return KDN_ERR_INVALID_ARG;
     if (workspace && (!aligned(workspace, 256) ||
                       workspace_bytes < delta_bwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype)))
         return KDN_ERR_INVALID_ARG;
@@ -570,8 +574,10 @@ kdn_status kdn_delta_scan_bwd_workspace(int B, int H, int T, int dk, int dv, int
                                         long long* workspace_bytes) {
     if (!workspace_bytes) return KDN_ERR_INVALID_ARG;
     const kdn_status s = delta_sizes_check(B, H, T, dk, dv, nseq, in_dtype);
-    if (s == KDN_OK) *workspace_bytes = delta_bwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype);
-    return s;
+    if (s != KDN_OK) return s;
+    if (!delta_fits(B, H, T, dk, dv, nseq, in_dtype, true)) return KDN_ERR_INVALID_ARG;
+    *workspace_bytes = delta_bwd_workspace_bytes(B, H, T, dk, dv, nseq, in_dtype);
+    return KDN_OK;
 }
 
 kdn_status kdn_delta_step(const void* q, const void* k, const void* v, const void* beta, const void* d,

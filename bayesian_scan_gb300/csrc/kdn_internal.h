@@ -183,6 +183,9 @@ struct DeltaArgs {
 };
 kdn_status delta_fwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns);
 kdn_status delta_bwd_launch(const DeltaArgs& a, cudaStream_t stream, long long wait_ns);
+// Whether a call that goes by chunks has no more of them than a launch has blocks
+// (what it has to refuse otherwise; its workspace's size may not fit 64 bits either).
+bool delta_fits(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype, bool back);
 long long delta_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype);
 long long delta_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int nseq, kdn_dtype in_dtype);
 kdn_status delta_step_launch(const DeltaArgs& a, const float* state, float* new_state, cudaStream_t stream);

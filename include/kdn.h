@@ -566,8 +566,11 @@ KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, 
  *             NULL (stream-ordered scratch), as for kdn_diag_scan_bwd.  Calls
  *             that overlap on the GPU need workspaces of their own.
  *
- *   B >= 1, H >= 1, T >= 0; dk, dv in {16, 32, 64, 128}; B*H*T*max(dk,dv) <
- *   2^62.  Tensors 16-byte aligned (d, beta: element-aligned; A, offsets: 4).
+ *   B >= 1, H >= 1, 0 <= T <= 2^31 - 1 - 2^16; dk, dv in {16, 32, 64, 128};
+ *   B*H*T*max(dk,dv) < 2^62.  A call has at most 2^31 - 1 chunks of 64 tokens,
+ *   B*H*ceil(T/64) (packed: H*(ceil(T/64) + nseq + 1)), in the backward and on the
+ *   tensor cores, and at most that many blocks of 32 state rows (64 for dk of 32
+ *   and less).  Tensors 16-byte aligned (d, beta: element-aligned; A, offsets: 4).
  *   T = 0 writes only final_state.  Outputs overlap no input.
  *
  * The state and every sum are fp32; out is rounded once.  alpha_t <= 1 and
