@@ -142,14 +142,14 @@ __device__ __forceinline__ uint4 to_half(uint4 w, float up) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// 8 bf16 numbers without those that are not finite (0 in their place), and
-// whether there are such.
-__device__ __forceinline__ uint4 finite_bf16(uint4 w, bool& all) {
+// 8 bf16 numbers without those that are not finite (0 in their place; `all`
+// turns false where there are such).
+__device__ __forceinline__ uint4 finite_bf16(uint4 w, bool* all = nullptr) {
     uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const uint32_t bad = __vcmpeq2(u[e] & 0x7f807f80u, 0x7f807f80u);
-        all = all && bad == 0u;
+        if (all) *all = *all && bad == 0u;
         u[e] &= ~bad;
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
@@ -349,14 +349,13 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
     // is NaN).  Their own Z is not finite, which the walk looks at.
     if (max(most3[0], max(most3[1], most3[2])) >= 0x7f80u) {
         __syncthreads();
-        bool all[3] = {true, true, true};
         uint32_t t3[3] = {0u, 0u, 0u};
         for (int i = tid; i < C * (D / 8); i += PREP_THREADS) {
             bool k_fine = true;
-            t3[0] = largest_bf16(t3[0], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16), k_fine));
-            t3[1] = largest_bf16(t3[1], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + TILE_X + i * 16), all[1]));
+            t3[0] = largest_bf16(t3[0], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + i * 16), &k_fine));
+            t3[1] = largest_bf16(t3[1], finite_bf16(*reinterpret_cast<const uint4*>(smem + P_OFF_KQ + TILE_X + i * 16)));
             if (!k_fine) atomicMin(gone, i / (D / 8 * 8) * 8 + i % 8);   // (piece i of the tile: its row)
-            if (a.grad_out && i < m * (D / 8)) t3[2] = largest_bf16(t3[2], finite_bf16(piece<FULL>(go, i, dv), all[2]));
+            if (a.grad_out && i < m * (D / 8)) t3[2] = largest_bf16(t3[2], finite_bf16(piece<FULL>(go, i, dv)));
         }
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
@@ -515,7 +514,7 @@ __global__ void __launch_bounds__(PREP_THREADS) delta_prep_kernel(const DeltaArg
 // tiles, one chunk ahead.  Sixteen row warps: with eight, two to a scheduler,
 // their dependent steps took 1.6 times as long.  Bound by that chain (exchange of
 // a row's largest, halves, product, sums, four times a chunk): 128 heads of 4096
-// tokens 246 us, 7600 cycles a chunk, the tensor pipe busy in 22 % of them.
+// tokens 244 us, 7600 cycles a chunk, the tensor pipe busy in 30 % of them.
 constexpr int ROW_WARPS = 16, MMA_WARP = ROW_WARPS, CH_THREADS = (ROW_WARPS + 2) * 32;
 // shared memory: two stages of a prepared chunk and v (backward: do);
 // two arrays of the rows' largest magnitudes, one value of each quarter
@@ -1120,7 +1119,7 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_kernel(const float* S
 // with the forward's shape (D for S, dU for Z, Y for R).  P^T dO and dO^T (e^g
 // Q) do not wait for D.  dV = L; D (behind the chunk) and Y are kept.  P^T dO
 // lies in COL_W until beta dU's halves do; e^g dO is an operand in shared memory.
-// (128 heads of 4096 tokens 338 us, bound as the forward's walk is.)
+// (128 heads of 4096 tokens 334 us, bound as the forward's walk is.)
 constexpr uint32_t COL_X = 320;              // dO^T (e^g Q), 128 columns
 
 // END: of a part but the first its end alone, from zero (the last one's from the
@@ -1503,7 +1502,8 @@ __global__ void __launch_bounds__(FOLD_THREADS) delta_fold_back_kernel(const flo
 // too) with one power of two (its values meet in sums); D1 follows S0 there.  <S0, D1> is
 // taken in fp32: the gradient of A is a sum over all tokens to which it adds the
 // same in every token of its chunk.  Bound by the latency of these steps with one
-// CTA to an SM: 8192 chunks 655 us, 12 us a chunk, its 260 KB 5.8 at a copy's rate.
+// CTA to an SM: 8192 chunks 708 us (655 without W), 13 us a chunk, its 260 KB 5.8 at
+// a copy's rate.
 constexpr int GR_WARPS = 16, GR_THREADS = GR_WARPS * 32 + 32;
 constexpr int GR_KQ = 0, GR_DO = 2 * TILE_X, GR_R = GR_DO + TILE_X, GR_Y = GR_R + ROWS_BYTES, GR_S = GR_Y + ROWS_BYTES,
               GR_P = GR_S + STATE_BYTES, GR_MISC = GR_P + 2 * C * 2 * C * 2;

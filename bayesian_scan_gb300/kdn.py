@@ -1068,7 +1068,9 @@ def delta_scan_bwd(q, k, v, beta, d, A, grad_out, S0=None, offsets=None, grad_fi
     (allocate); ``grad_A``, ``grad_S0``: True (allocate), False/None (skip) or
     fp32 tensors.  Returns a dict q, k, v, beta, d, A, S0.  ``workspace``: a
     uint8 device tensor of at least ``delta_scan_bwd_workspace`` bytes, or
-    None (one is taken from torch's caching allocator for the call)."""
+    None (one is taken from torch's caching allocator for the call).  With
+    offsets, gradients allocated here are undefined for tokens that lie in no
+    sequence."""
     B, H, T, dk, dv, nseq, state = _delta_sizes(q, v, offsets)
     it = _delta_inputs(q, k, v, beta, d, A, S0, (B, H, T, dk, dv), state)
     ot = _dtype_of(grad_out, "grad_out")
