@@ -582,10 +582,12 @@ KDN_API kdn_status kdn_qk_norm_rope_bwd_workspace(int B, int T, int Hq, int Hk, 
  * (T / nseq, of packed ones) of 64 tokens or more for heads of 128 (28 with more
  * than 64 heads in all), 48 to 112 for narrower ones, are taken in chunks of 64
  * tokens on the tensor cores, with operands of 22 bits: errors are those of fp32
- * arithmetic, relative to the largest terms of a chunk (below 2^-24 of them; what
- * strong decays make smaller than that beside the rest of its chunk has no bits
- * of its own, nor have keys, queries or gradients of a chunk that are all below
- * 2^-74).  Few heads of long sequences (not packed ones) are cut along the tokens.
+ * arithmetic, relative to the largest terms of a chunk.  What is smaller than
+ * 2^-24 of those has fewer bits of its own, below 2^-38 none: what strong decays
+ * leave beside the rest of the chunk, and a token's query, key or gradient of out
+ * beside its chunk's largest (token by token they keep theirs); nor has a chunk
+ * whose keys, queries or gradients are all below 2^-74.  Few heads of long
+ * sequences (not packed ones) are cut along the tokens.
  */
 KDN_API kdn_status kdn_delta_scan_fwd(const void* q, const void* k, const void* v, const void* beta,
                                       const void* d, const float* A, const float* S0,
@@ -618,7 +620,8 @@ KDN_API kdn_status kdn_delta_scan_fwd_workspace(int B, int H, int T, int dk, int
  *
  * Sizes, alignment and rules as for the forward.  T = 0 writes grad_S0 (=
  * grad_final_state) and grad_A (= 0).  Sums in fp32, in a fixed order
- * (deterministic).  The tensor-core form takes bf16 inputs and grad_out with
+ * (deterministic).  A decay's gradient is the sum of the terms that have this
+ * decay as a factor, so a strong decay's keeps its digits, however small.  The tensor-core form takes bf16 inputs and grad_out with
  * dk*dv of 64*64 or more (64*32 with few heads), of any length.
  */
 KDN_API kdn_status kdn_delta_scan_bwd(const void* q, const void* k, const void* v, const void* beta,
